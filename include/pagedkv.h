@@ -56,7 +56,9 @@ typedef enum pa_status {
   PA_ERR_WORKSPACE = -4,     /* workspace missing or smaller than required */
   PA_ERR_DEVICE_INDEX = -5,  /* device_status reports a bad block id / slot / length */
   PA_ERR_DEVICE_TIMEOUT = -6, /* device_status reports a pipeline wait that timed out */
-  PA_ERR_OUT_OF_BLOCKS = -7   /* the block manager has too few free blocks (no change made) */
+  PA_ERR_OUT_OF_BLOCKS = -7,  /* the block manager has too few free blocks (no change made) */
+  PA_ERR_DEVICE_VALUE = -8    /* device_status reports a non-finite key or value, or a scale
+                                 that is not a positive number, and nothing worse */
 } pa_status;
 
 /* Bits a kernel ORs into *device_status. */
@@ -67,6 +69,9 @@ typedef enum pa_status {
 #define PA_DEVFLAG_TIMEOUT 0x8     /* an mbarrier wait exceeded its time limit */
 #define PA_DEVFLAG_LAYOUT 0x10     /* shared memory not aligned as the kernel requires
                                       (work skipped; reported as PA_ERR_DEVICE_INDEX) */
+
+#define PA_DEVFLAG_NONFINITE 0x20  /* a NaN or an infinity was to be stored as an 8-bit code */
+#define PA_DEVFLAG_BAD_SCALE 0x40  /* a block's scale is zero, negative, NaN or infinite */
 
 /* Geometry of one layer's pair of cache pools; validated on every call.  The attention
  * calls (pa_decode, pa_decode_append, pa_prefill_chunk, pa_attention_varlen) also need
@@ -337,6 +342,111 @@ pa_status pa_copy_blocks(void* key_cache, void* value_cache, pa_cache_desc cd,
                          const int64_t* block_mapping, int32_t num_pairs,
                          int32_t* device_status, pa_stream_t stream);
 
+/* Appends that rotate on the way.  The new tokens of every sequence (the last q_len of its
+ * context_lens[s] tokens, as in pa_compute_slot_mapping) have their query and key rows rotated
+ * by their logical positions (rotary position embedding) and their key and value rows stored
+ * to their slots, in one launch: slot mapping, rotation and pa_reshape_and_cache in one
+ * ("vLLM" (blog.rlaisqls.com), section Optimized CUDA Kernels: fused kernels skip HBM round
+ * trips; the pages describe no counterpart of the rotation itself).
+ * The token at position p turns the pair i (i = 0 .. 31) of every query and key head row,
+ *   (a, b) -> (a cos - b sin, b cos + a sin),
+ *   cos = cos_sin[p][i], sin = cos_sin[p][32 + i],
+ * in fp32, rounded once to bf16.  Pairs are dims (i, i + 32), or (2i, 2i + 1) with
+ * interleaved != 0.  Values are stored as they are.
+ *   q, q_out         bf16, token t's rows [num_q_heads][64] at q + t * q_stride; q_out may be
+ *                    q (same stride) and must not overlap it otherwise.  num_q_heads == 0 (q
+ *                    and q_out NULL): keys and values only
+ *   key, value       bf16, token t's rows [Hkv][64] at key + t * key_stride
+ *   *_stride         elements between the rows of consecutive tokens: a multiple of 8, at
+ *                    least heads * 64 (slices of one fused projection are fine)
+ *   cos_sin          float [max_positions][64]
+ *   query_start_loc  int32 [num_seqs + 1], or NULL for one token per sequence (then
+ *                    num_tokens == num_seqs, and a context of 0 marks a padding row)
+ *   num_tokens       rows of q, key and value.  Rows at or past query_start_loc[num_seqs] are
+ *                    padding: neither read nor written
+ * A token whose position is negative, past its block-table row or at or past max_positions
+ * sets PA_DEVFLAG_BAD_CONTEXT, a bad block id PA_DEVFLAG_BAD_BLOCK; such tokens are skipped.
+ * Two tokens of one call must not share a slot (the winner is undefined).
+ * num_tokens == 0 is a no-op. */
+pa_status pa_rope_append(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                         int32_t num_q_heads, const void* key, int64_t key_stride,
+                         const void* value, int64_t value_stride, const float* cos_sin,
+                         int32_t max_positions, int32_t interleaved,
+                         const int32_t* block_tables, int32_t max_blocks_per_seq,
+                         const int32_t* context_lens, const int32_t* query_start_loc,
+                         int32_t num_seqs, int32_t num_tokens, void* key_cache,
+                         void* value_cache, pa_cache_desc cd, int32_t* device_status,
+                         pa_stream_t stream);
+
+/* The 8-bit cache.  Its pools hold e4m3 codes (1 sign, 4 exponent, 3 significand bits; at most
+ * 448) in the layout of the bf16 pools, [num_blocks][Hkv][16][64] with one byte each, and one
+ * float per (block, K/V head) in key_scale / value_scale [num_blocks][Hkv]; a cached value is
+ * code * scale.  Half the bytes of the bf16 pools, for the decode's reads and for storage.
+ * The pages describe no counterpart.
+ *
+ * pa_rope_append_q8 is pa_rope_append into these pools.  cos_sin == NULL stores the keys as
+ * they are (num_q_heads must be 0 then).  Scales are powers of two: with A the largest
+ * magnitude among the call's new values of a block and head (keys after rotation, in fp32)
+ * and 2^e the smallest power of two, e >= -126, with A <= 448 * 2^e, the scale becomes 2^e
+ * where the call writes the block's first token, and max(old scale, 2^e) elsewhere.  Codes of
+ * the block's earlier tokens are rescaled when the scale grows (exactly, but for codes that
+ * turn subnormal); new ones are value / scale, rounded to nearest even once from fp32.  So a
+ * chunked append and a token-by-token one of the same tokens may round small values
+ * differently.  A NaN is stored as 0 and an infinity as the largest code of its sign; both set
+ * PA_DEVFLAG_NONFINITE.  A block with earlier tokens whose scale is not a positive finite
+ * number sets PA_DEVFLAG_BAD_SCALE and is left as it is.  Blocks that two sequences of the
+ * call append to must differ (pa_copy_blocks_q8 before writing to shared blocks).  The other
+ * arguments, checks and no-ops are pa_rope_append's; a sequence with any position out of range
+ * stores nothing. */
+pa_status pa_rope_append_q8(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                            int32_t num_q_heads, const void* key, int64_t key_stride,
+                            const void* value, int64_t value_stride, const float* cos_sin,
+                            int32_t max_positions, int32_t interleaved,
+                            const int32_t* block_tables, int32_t max_blocks_per_seq,
+                            const int32_t* context_lens, const int32_t* query_start_loc,
+                            int32_t num_seqs, int32_t num_tokens, void* key_cache,
+                            void* value_cache, float* key_scale, float* value_scale,
+                            pa_cache_desc cd, int32_t* device_status, pa_stream_t stream);
+
+/* Bytes of device workspace pa_decode_q8 needs for these sizes on the current device (0 when
+ * the sizes are invalid).  The rules of pa_decode_workspace_size hold: zero-fill it before its
+ * first use and before a call whose num_seqs or num_kv_heads differ from those of the
+ * previous call on it; calls that can overlap on the GPU (captured graphs that share it
+ * included) need buffers of their own. */
+size_t pa_decode_q8_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t num_q_heads,
+                                   int32_t max_context_len);
+
+/* pa_decode over the 8-bit pools:
+ *   out[s][h][:] = sum_j softmax_j(scale * q[s][h] . K_s[j]) V_s[j],   K = code * key_scale,
+ * with the arguments, limits, launch flags and errors of pa_decode (without partition_tokens;
+ * contexts above max_context_len are reported and undefined).  The codes 0x7f and 0xff, which
+ * pa_rope_append_q8 never stores, read as NaN.  Scales are read as any floats, not only powers
+ * of two.  key_cache, value_cache: e4m3; key_scale, value_scale: 4-byte aligned floats. */
+pa_status pa_decode_q8(void* out, const void* q, const void* key_cache, const void* value_cache,
+                       const float* key_scale, const float* value_scale, pa_cache_desc cd,
+                       const int32_t* block_tables, int32_t max_blocks_per_seq,
+                       const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads,
+                       float scale, int32_t max_context_len, void* workspace,
+                       size_t workspace_bytes, uint32_t launch_flags, int32_t* device_status,
+                       pa_stream_t stream);
+
+/* pa_prefill_chunk over the 8-bit pools: causal chunks of query rows, with that call's
+ * arguments and errors, for num_q_heads / num_kv_heads in {1, 2, 4}.  Rows of q and out at or
+ * past query_start_loc[num_seqs] are left alone. */
+pa_status pa_prefill_chunk_q8(void* out, const void* q, const int32_t* query_start_loc,
+                              int32_t num_query_tokens, int32_t max_query_len,
+                              const void* key_cache, const void* value_cache,
+                              const float* key_scale, const float* value_scale,
+                              pa_cache_desc cd, const int32_t* block_tables,
+                              int32_t max_blocks_per_seq, const int32_t* context_lens,
+                              int32_t num_seqs, int32_t num_q_heads, float scale,
+                              int32_t* device_status, pa_stream_t stream);
+
+/* pa_copy_blocks for the 8-bit pools: the blocks' codes and scales. */
+pa_status pa_copy_blocks_q8(void* key_cache, void* value_cache, float* key_scale,
+                            float* value_scale, pa_cache_desc cd, const int64_t* block_mapping,
+                            int32_t num_pairs, int32_t* device_status, pa_stream_t stream);
+
 /* Host-side block manager ("vLLM", PagedAttention and Continuous Batching): a pool of
  * num_blocks physical blocks of block_size tokens; each sequence owns a table of blocks,
  * grown one block at a time as tokens arrive; pa_bm_fork shares a sequence's blocks with a
@@ -386,7 +496,8 @@ pa_status pa_selftest_wait_timeout(int32_t* device_status, int32_t limit_ms,
 pa_status pa_stream_read(const void* buf, size_t bytes, uint32_t* xor_out, pa_stream_t stream);
 
 /* Synchronise `stream`, read *device_status and translate it: PA_OK when zero,
- * PA_ERR_DEVICE_TIMEOUT when the timeout bit is set, else PA_ERR_DEVICE_INDEX. */
+ * PA_ERR_DEVICE_TIMEOUT when the timeout bit is set, PA_ERR_DEVICE_VALUE when only
+ * PA_DEVFLAG_NONFINITE or PA_DEVFLAG_BAD_SCALE are, else PA_ERR_DEVICE_INDEX. */
 pa_status pa_check_device_status(const int32_t* device_status, pa_stream_t stream);
 
 /* Static description of a status code (never NULL). */

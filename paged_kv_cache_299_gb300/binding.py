@@ -37,7 +37,9 @@ PA_ERR_WORKSPACE = -4
 PA_ERR_DEVICE_INDEX = -5
 PA_ERR_DEVICE_TIMEOUT = -6
 PA_ERR_OUT_OF_BLOCKS = -7
+PA_ERR_DEVICE_VALUE = -8
 DEVFLAG_BAD_BLOCK, DEVFLAG_BAD_SLOT, DEVFLAG_BAD_CONTEXT, DEVFLAG_TIMEOUT = 1, 2, 4, 8
+DEVFLAG_NONFINITE, DEVFLAG_BAD_SCALE = 0x20, 0x40
 # Size of the library-owned device scratch of pa_decode_static_scratch (bytes).
 PA_DECODE_STATIC_SCRATCH_BYTES = 8 << 20
 # Launch flags of pa_decode / pa_decode_append (include/pagedkv.h states the contract).
@@ -59,7 +61,9 @@ EXPORTED = ("pa_compute_slot_mapping", "pa_reshape_and_cache", "pa_decode_worksp
             "pa_bm_fork", "pa_bm_append_tokens", "pa_bm_free_sequence", "pa_bm_num_tokens",
             "pa_bm_block_table", "pa_decode_append", "pa_selftest_wait_timeout",
             "pa_varlen_workspace_size", "pa_attention_varlen", "pa_stream_read",
-            "pa_prefill_chunk_ex", "pa_attention_varlen_ex")
+            "pa_prefill_chunk_ex", "pa_attention_varlen_ex", "pa_rope_append",
+            "pa_rope_append_q8", "pa_decode_q8_workspace_size", "pa_decode_q8",
+            "pa_prefill_chunk_q8", "pa_copy_blocks_q8")
 
 
 def library_path() -> str:
@@ -131,6 +135,22 @@ def load(path: str | None = None):
     lib.pa_bm_num_tokens.restype = i64
     lib.pa_bm_block_table.argtypes = [P, i64, P, i32]
     lib.pa_bm_block_table.restype = i32
+    lib.pa_rope_append.argtypes = [P, i64, P, i64, i32, P, i64, P, i64, P, i32, i32, P, i32, P,
+                                   P, i32, i32, P, P, CacheDesc, P, P]
+    lib.pa_rope_append.restype = st
+    lib.pa_rope_append_q8.argtypes = [P, i64, P, i64, i32, P, i64, P, i64, P, i32, i32, P, i32,
+                                      P, P, i32, i32, P, P, P, P, CacheDesc, P, P]
+    lib.pa_rope_append_q8.restype = st
+    lib.pa_decode_q8_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.pa_decode_q8_workspace_size.restype = sz
+    lib.pa_decode_q8.argtypes = [P, P, P, P, P, P, CacheDesc, P, i32, P, i32, i32, f32, i32, P,
+                                 sz, u32, P, P]
+    lib.pa_decode_q8.restype = st
+    lib.pa_prefill_chunk_q8.argtypes = [P, P, P, i32, i32, P, P, P, P, CacheDesc, P, i32, P, i32,
+                                        i32, f32, P, P]
+    lib.pa_prefill_chunk_q8.restype = st
+    lib.pa_copy_blocks_q8.argtypes = [P, P, P, P, CacheDesc, P, i32, P, P]
+    lib.pa_copy_blocks_q8.restype = st
     lib.pa_selftest_wait_timeout.argtypes = [P, i32, P]
     lib.pa_selftest_wait_timeout.restype = st
     lib.pa_stream_read.argtypes = [P, sz, P, P]
@@ -404,6 +424,187 @@ def pa_copy_blocks(key_cache, value_cache, block_mapping, device_status=None, st
                                _ptr(block_mapping), block_mapping.shape[0], _ptr(device_status),
                                _stream(stream))
     _check(st, "pa_copy_blocks")
+
+
+def _need_rows(t, name, heads=None):
+    """bf16 [T, heads, 64] whose rows are contiguous per token; returns the token stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != 64 or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, 64], "
+                         f"got {tuple(t.shape)}")
+    stride, row, one = t.stride()
+    heads = t.shape[1]
+    if one != 1 or (row != 64 and heads > 1):
+        raise ValueError(f"{name}: the head rows of a token must be contiguous")
+    return max(stride, heads * 64) if t.shape[0] <= 1 else stride
+
+
+def _need_q8(key_cache, value_cache, key_scale, value_scale):
+    for t, name in ((key_cache, "key_cache"), (value_cache, "value_cache")):
+        _need(t, name, torch.float8_e4m3fn, 4)
+    for t, name in ((key_scale, "key_scale"), (value_scale, "value_scale")):
+        _need(t, name, torch.float32, 2)
+    if key_cache.shape != value_cache.shape or key_scale.shape != value_scale.shape or \
+            key_scale.shape != key_cache.shape[:2]:
+        raise ValueError("8-bit pools are [blocks, heads, 16, 64] with scales [blocks, heads]")
+
+
+def new_q8_cache(num_blocks, num_kv_heads, device=None):
+    """(key_cache, value_cache, key_scale, value_scale) of an empty 8-bit cache: e4m3 pools
+    [num_blocks, num_kv_heads, 16, 64] and float32 scales [num_blocks, num_kv_heads]."""
+    device = device or "cuda"
+    pools = [torch.zeros(num_blocks, num_kv_heads, 16, 64, dtype=torch.uint8,
+                         device=device).view(torch.float8_e4m3fn) for _ in range(2)]
+    scales = [torch.ones(num_blocks, num_kv_heads, dtype=torch.float32, device=device)
+              for _ in range(2)]
+    return (*pools, *scales)
+
+
+def _rope_append_args(q, key, value, cos_sin, key_cache, block_tables, context_lens,
+                      query_start_loc, q_out, interleaved):
+    hkv = key_cache.shape[1]
+    ks, vs = _need_rows(key, "key", hkv), _need_rows(value, "value", hkv)
+    tokens = key.shape[0]
+    if value.shape[0] != tokens:
+        raise ValueError("key and value disagree on the token count")
+    qs = os_ = hq = 0
+    if q is not None:
+        qs = _need_rows(q, "q")
+        hq = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        os_ = _need_rows(q_out, "q_out", hq)
+        if q.shape[0] != tokens or q_out.shape[0] != tokens:
+            raise ValueError("q, q_out and key disagree on the token count")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    positions = 0
+    if cos_sin is not None:
+        _need(cos_sin, "cos_sin", torch.float32, 2)
+        if cos_sin.shape[1] != 64:
+            raise ValueError("cos_sin must be [positions, 64]: 32 cosines, then 32 sines")
+        positions = cos_sin.shape[0]
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(context_lens, "context_lens", torch.int32, 1)
+    seqs = context_lens.shape[0]
+    if block_tables.shape[0] != seqs:
+        raise ValueError("block_tables and context_lens disagree on the sequence count")
+    if query_start_loc is not None:
+        _need(query_start_loc, "query_start_loc", torch.int32, 1)
+        if query_start_loc.shape[0] != seqs + 1:
+            raise ValueError("query_start_loc must have one entry more than context_lens")
+    args = (_ptr(q), qs, _ptr(q_out), os_, hq, _ptr(key), ks, _ptr(value), vs, _ptr(cos_sin),
+            positions, int(bool(interleaved)), _ptr(block_tables), block_tables.shape[1],
+            _ptr(context_lens), _ptr(query_start_loc), seqs, tokens)
+    return q_out, args
+
+
+def pa_rope_append(q, key, value, cos_sin, key_cache, value_cache, block_tables, context_lens,
+                   query_start_loc=None, q_out=None, interleaved=False, device_status=None,
+                   stream=None):
+    """Rotate q [T, Hq, 64] and key [T, Hkv, 64] by their positions and store key and value into
+    the bf16 pools; returns the rotated queries (q_out, which may be q; None without q).  The
+    rows of a token must be contiguous, the tokens may be strided; see include/pagedkv.h."""
+    _need(key_cache, "key_cache", torch.bfloat16, 4)
+    _need(value_cache, "value_cache", torch.bfloat16, 4)
+    if key_cache.shape != value_cache.shape:
+        raise ValueError("cache shapes differ")
+    q_out, args = _rope_append_args(q, key, value, cos_sin, key_cache, block_tables,
+                                    context_lens, query_start_loc, q_out, interleaved)
+    st = load().pa_rope_append(*args, _ptr(key_cache), _ptr(value_cache), cache_desc(key_cache),
+                               _ptr(device_status), _stream(stream))
+    _check(st, "pa_rope_append")
+    return q_out
+
+
+def pa_rope_append_q8(q, key, value, cos_sin, key_cache, value_cache, key_scale, value_scale,
+                      block_tables, context_lens, query_start_loc=None, q_out=None,
+                      interleaved=False, device_status=None, stream=None):
+    """pa_rope_append into the 8-bit pools (e4m3 codes, one scale per block and head).  cos_sin
+    None stores the keys as they are (q must be None then); see include/pagedkv.h."""
+    _need_q8(key_cache, value_cache, key_scale, value_scale)
+    q_out, args = _rope_append_args(q, key, value, cos_sin, key_cache, block_tables,
+                                    context_lens, query_start_loc, q_out, interleaved)
+    st = load().pa_rope_append_q8(*args, _ptr(key_cache), _ptr(value_cache), _ptr(key_scale),
+                                  _ptr(value_scale), cache_desc(key_cache), _ptr(device_status),
+                                  _stream(stream))
+    _check(st, "pa_rope_append_q8")
+    return q_out
+
+
+def pa_decode_q8_workspace_size(num_seqs, num_kv_heads, num_q_heads, max_context_len) -> int:
+    return int(load().pa_decode_q8_workspace_size(num_seqs, num_kv_heads, num_q_heads,
+                                                  max_context_len))
+
+
+def pa_decode_q8(out, q, key_cache, value_cache, key_scale, value_scale, block_tables,
+                 context_lens, scale, max_context_len, workspace=None, device_status=None,
+                 stream=None, launch_flags=PA_LAUNCH_DEFAULT):
+    """Paged decode attention over the 8-bit pools; writes out [S, Hq, D] (bf16).  launch_flags:
+    those of pa_decode."""
+    _need(out, "out", torch.bfloat16, 3)
+    _need(q, "q", torch.bfloat16, 3)
+    _need_q8(key_cache, value_cache, key_scale, value_scale)
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(context_lens, "context_lens", torch.int32, 1)
+    num_seqs, hq, d = q.shape
+    if out.shape != q.shape or d != key_cache.shape[3] or block_tables.shape[0] != num_seqs or \
+            context_lens.shape[0] != num_seqs:
+        raise ValueError("q/out/block_tables/context_lens disagree on the sequence count")
+    if workspace is None:
+        need = pa_decode_q8_workspace_size(num_seqs, key_cache.shape[1], hq, max_context_len)
+        workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device)
+    _need(workspace, "workspace", torch.uint8, 1)
+    st = load().pa_decode_q8(_ptr(out), _ptr(q), _ptr(key_cache), _ptr(value_cache),
+                             _ptr(key_scale), _ptr(value_scale), cache_desc(key_cache),
+                             _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
+                             num_seqs, hq, float(scale), int(max_context_len), _ptr(workspace),
+                             workspace.numel(), int(launch_flags), _ptr(device_status),
+                             _stream(stream))
+    _check(st, "pa_decode_q8")
+    return out
+
+
+def pa_prefill_chunk_q8(out, q, query_start_loc, max_query_len, key_cache, value_cache,
+                        key_scale, value_scale, block_tables, context_lens, scale,
+                        device_status=None, stream=None):
+    """Causal chunked-prefill attention over the 8-bit pools; writes out [Tq, Hq, D] (bf16)."""
+    _need(out, "out", torch.bfloat16, 3)
+    _need(q, "q", torch.bfloat16, 3)
+    _need(query_start_loc, "query_start_loc", torch.int32, 1)
+    _need_q8(key_cache, value_cache, key_scale, value_scale)
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(context_lens, "context_lens", torch.int32, 1)
+    num_seqs = context_lens.shape[0]
+    if out.shape != q.shape or q.shape[2] != key_cache.shape[3] or \
+            query_start_loc.shape[0] != num_seqs + 1 or block_tables.shape[0] != num_seqs:
+        raise ValueError("prefill argument shapes disagree")
+    st = load().pa_prefill_chunk_q8(
+        _ptr(out), _ptr(q), _ptr(query_start_loc), q.shape[0], int(max_query_len),
+        _ptr(key_cache), _ptr(value_cache), _ptr(key_scale), _ptr(value_scale),
+        cache_desc(key_cache), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
+        num_seqs, q.shape[1], float(scale), _ptr(device_status), _stream(stream))
+    _check(st, "pa_prefill_chunk_q8")
+    return out
+
+
+def pa_copy_blocks_q8(key_cache, value_cache, key_scale, value_scale, block_mapping,
+                      device_status=None, stream=None):
+    """Copy whole physical blocks of the 8-bit pools with their scales: block_mapping int64
+    [n, 2] (src, dst)."""
+    _need_q8(key_cache, value_cache, key_scale, value_scale)
+    _need(block_mapping, "block_mapping", torch.int64, 2)
+    if block_mapping.shape[1] != 2:
+        raise ValueError("block_mapping is not [n, 2]")
+    st = load().pa_copy_blocks_q8(_ptr(key_cache), _ptr(value_cache), _ptr(key_scale),
+                                  _ptr(value_scale), cache_desc(key_cache), _ptr(block_mapping),
+                                  block_mapping.shape[0], _ptr(device_status), _stream(stream))
+    _check(st, "pa_copy_blocks_q8")
 
 
 class BlockManager:

@@ -37,6 +37,9 @@ pa_status from_cuda(cudaError_t e, const char* what) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+constexpr int32_t kMaxQHeads = 1024;  // query heads the rotating appends take
 
 pa_status check_desc(const pa_cache_desc& cd) {
   if (cd.num_blocks <= 0 || cd.num_kv_heads <= 0 || cd.num_kv_heads > 64)
@@ -386,6 +389,263 @@ pa_status pa_copy_blocks(void* key_cache, void* value_cache, pa_cache_desc cd,
                    "copy_blocks launch");
 }
 
+pa_status pa_copy_blocks_q8(void* key_cache, void* value_cache, float* key_scale,
+                            float* value_scale, pa_cache_desc cd, const int64_t* block_mapping,
+                            int32_t num_pairs, int32_t* device_status, pa_stream_t stream) {
+  pa_status st = check_desc(cd);
+  if (st != PA_OK) return st;
+  if (num_pairs < 0) return fail(PA_ERR_INVALID_ARG, "num_pairs %d", num_pairs);
+  if (num_pairs == 0) return ok();
+  if (!key_cache || !value_cache || !key_scale || !value_scale || !block_mapping)
+    return fail(PA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(key_cache) || !aligned16(value_cache) || !aligned4(key_scale) ||
+      !aligned4(value_scale))
+    return fail(PA_ERR_INVALID_ARG,
+                "cache pointers must be 16-byte aligned, scale pointers 4-byte aligned");
+  return from_cuda(pkv::launch_copy_blocks_q8(key_cache, value_cache, key_scale, value_scale,
+                                              block_mapping, num_pairs, cd.num_blocks,
+                                              cd.num_kv_heads, device_status,
+                                              reinterpret_cast<cudaStream_t>(stream)),
+                   "copy_blocks_q8 launch");
+}
+
+namespace {
+
+// Validation and argument packing shared by the two appends; *skip: nothing to do.
+pa_status append_args(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                      int32_t num_q_heads, const void* key, int64_t key_stride,
+                      const void* value, int64_t value_stride, const float* cos_sin,
+                      int32_t max_positions, int32_t interleaved, const int32_t* block_tables,
+                      int32_t max_blocks_per_seq, const int32_t* context_lens,
+                      const int32_t* query_start_loc, int32_t num_seqs, int32_t num_tokens,
+                      void* key_cache, void* value_cache, pa_cache_desc cd,
+                      int32_t* device_status, bool rotate, pkv::AppendArgs* a, bool* skip) {
+  *skip = false;
+  pa_status st = check_desc(cd);
+  if (st != PA_OK) return st;
+  if (num_tokens < 0 || num_seqs < 0 || max_blocks_per_seq <= 0 || num_q_heads < 0 ||
+      num_q_heads > kMaxQHeads)
+    return fail(PA_ERR_INVALID_ARG,
+                "num_tokens %d, num_seqs %d, max_blocks_per_seq %d, num_q_heads %d (0..%d)",
+                num_tokens, num_seqs, max_blocks_per_seq, num_q_heads, kMaxQHeads);
+  if (num_tokens == 0) {
+    *skip = true;
+    return PA_OK;
+  }
+  if (num_seqs == 0) return fail(PA_ERR_INVALID_ARG, "tokens without sequences");
+  if (query_start_loc == nullptr && num_tokens != num_seqs)
+    return fail(PA_ERR_INVALID_ARG, "query_start_loc NULL needs num_tokens == num_seqs");
+  if (rotate && (cos_sin == nullptr || max_positions <= 0))
+    return fail(PA_ERR_INVALID_ARG, "cos_sin %p with %d positions",
+                static_cast<const void*>(cos_sin), max_positions);
+  if (!rotate && num_q_heads != 0)
+    return fail(PA_ERR_INVALID_ARG, "query rows without cos_sin: nothing rotates them");
+  if ((num_q_heads == 0) != (q == nullptr) || (num_q_heads == 0) != (q_out == nullptr))
+    return fail(PA_ERR_INVALID_ARG, "num_q_heads %d with q %p and q_out %p", num_q_heads, q, q_out);
+  if (!key || !value || !key_cache || !value_cache || !block_tables || !context_lens)
+    return fail(PA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(q) || !aligned16(q_out) || !aligned16(key) || !aligned16(value) ||
+      !aligned16(cos_sin) || !aligned16(key_cache) || !aligned16(value_cache))
+    return fail(PA_ERR_INVALID_ARG, "q/key/value/cos_sin/cache pointers must be 16-byte aligned");
+  const int64_t q_row = static_cast<int64_t>(num_q_heads) * pkv::kHeadDim;
+  const int64_t kv_row = static_cast<int64_t>(cd.num_kv_heads) * pkv::kHeadDim;
+  if (key_stride % 8 != 0 || value_stride % 8 != 0 || key_stride < kv_row || value_stride < kv_row ||
+      (num_q_heads > 0 && (q_stride % 8 != 0 || q_out_stride % 8 != 0 || q_stride < q_row ||
+                           q_out_stride < q_row)))
+    return fail(PA_ERR_INVALID_ARG,
+                "token strides q %lld, q_out %lld, key %lld, value %lld: multiples of 8, at least "
+                "heads * 64", static_cast<long long>(q_stride),
+                static_cast<long long>(q_out_stride), static_cast<long long>(key_stride),
+                static_cast<long long>(value_stride));
+  if (q == q_out && q != nullptr && q_stride != q_out_stride)
+    return fail(PA_ERR_INVALID_ARG, "q_out is q, with another stride");
+  a->q = q;
+  a->q_out = q_out;
+  a->key = key;
+  a->value = value;
+  a->q_stride = q_stride;
+  a->q_out_stride = q_out_stride;
+  a->key_stride = key_stride;
+  a->value_stride = value_stride;
+  a->cos_sin = cos_sin;
+  a->max_positions = max_positions;
+  a->interleaved = interleaved != 0;
+  a->block_tables = block_tables;
+  a->max_blocks_per_seq = max_blocks_per_seq;
+  a->context_lens = context_lens;
+  a->query_start_loc = query_start_loc;
+  a->num_seqs = num_seqs;
+  a->num_tokens = num_tokens;
+  a->num_q_heads = num_q_heads;
+  a->num_kv_heads = cd.num_kv_heads;
+  a->num_blocks = cd.num_blocks;
+  a->key_cache = key_cache;
+  a->value_cache = value_cache;
+  a->key_scale = nullptr;
+  a->value_scale = nullptr;
+  a->status = device_status;
+  return PA_OK;
+}
+
+}  // namespace
+
+pa_status pa_rope_append(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                         int32_t num_q_heads, const void* key, int64_t key_stride,
+                         const void* value, int64_t value_stride, const float* cos_sin,
+                         int32_t max_positions, int32_t interleaved,
+                         const int32_t* block_tables, int32_t max_blocks_per_seq,
+                         const int32_t* context_lens, const int32_t* query_start_loc,
+                         int32_t num_seqs, int32_t num_tokens, void* key_cache,
+                         void* value_cache, pa_cache_desc cd, int32_t* device_status,
+                         pa_stream_t stream) {
+  pkv::AppendArgs a;
+  bool skip;
+  pa_status st = append_args(q, q_stride, q_out, q_out_stride, num_q_heads, key, key_stride, value,
+                             value_stride, cos_sin, max_positions, interleaved, block_tables,
+                             max_blocks_per_seq, context_lens, query_start_loc, num_seqs,
+                             num_tokens, key_cache, value_cache, cd, device_status, true, &a, &skip);
+  if (st != PA_OK) return st;
+  if (skip) return ok();
+  return from_cuda(pkv::launch_rope_append(a, reinterpret_cast<cudaStream_t>(stream)),
+                   "rope_append launch");
+}
+
+pa_status pa_rope_append_q8(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                            int32_t num_q_heads, const void* key, int64_t key_stride,
+                            const void* value, int64_t value_stride, const float* cos_sin,
+                            int32_t max_positions, int32_t interleaved,
+                            const int32_t* block_tables, int32_t max_blocks_per_seq,
+                            const int32_t* context_lens, const int32_t* query_start_loc,
+                            int32_t num_seqs, int32_t num_tokens, void* key_cache,
+                            void* value_cache, float* key_scale, float* value_scale,
+                            pa_cache_desc cd, int32_t* device_status, pa_stream_t stream) {
+  pkv::AppendArgs a;
+  bool skip;
+  pa_status st = append_args(q, q_stride, q_out, q_out_stride, num_q_heads, key, key_stride, value,
+                             value_stride, cos_sin, max_positions, interleaved, block_tables,
+                             max_blocks_per_seq, context_lens, query_start_loc, num_seqs,
+                             num_tokens, key_cache, value_cache, cd, device_status,
+                             cos_sin != nullptr, &a, &skip);
+  if (st != PA_OK) return st;
+  if (skip) return ok();
+  if (!key_scale || !value_scale || !aligned4(key_scale) || !aligned4(value_scale))
+    return fail(PA_ERR_INVALID_ARG, "null or misaligned scales");
+  a.key_scale = key_scale;
+  a.value_scale = value_scale;
+  return from_cuda(pkv::launch_rope_append_q8(a, reinterpret_cast<cudaStream_t>(stream)),
+                   "rope_append_q8 launch");
+}
+
+size_t pa_decode_q8_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t num_q_heads,
+                                   int32_t max_context_len) {
+  if (check_decode_sizes(num_seqs, num_kv_heads, num_q_heads, max_context_len, 0) != PA_OK) return 0;
+  return num_seqs == 0 ? 0 : 16;
+}
+
+pa_status pa_decode_q8(void* out, const void* q, const void* key_cache, const void* value_cache,
+                       const float* key_scale, const float* value_scale, pa_cache_desc cd,
+                       const int32_t* block_tables, int32_t max_blocks_per_seq,
+                       const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads,
+                       float scale, int32_t max_context_len, void* workspace,
+                       size_t workspace_bytes, uint32_t launch_flags, int32_t* device_status,
+                       pa_stream_t stream) {
+  pa_status st = check_desc(cd);
+  if (st != PA_OK) return st;
+  st = check_decode_sizes(num_seqs, cd.num_kv_heads, num_q_heads, max_context_len, 0);
+  if (st != PA_OK) return st;
+  if (num_seqs == 0) return ok();
+  if (max_blocks_per_seq <= 0)
+    return fail(PA_ERR_INVALID_ARG, "max_blocks_per_seq %d", max_blocks_per_seq);
+  if (!out || !q || !key_cache || !value_cache || !key_scale || !value_scale || !block_tables ||
+      !context_lens)
+    return fail(PA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(out) || !aligned16(q) || !aligned16(key_cache) || !aligned16(value_cache) ||
+      !aligned4(key_scale) || !aligned4(value_scale))
+    return fail(PA_ERR_INVALID_ARG,
+                "out/q/cache pointers must be 16-byte aligned, scale pointers 4-byte aligned");
+  if (!(scale > 0.f) || !isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "scale %g", scale);
+  if (launch_flags & ~kKnownLaunchFlags)
+    return fail(PA_ERR_INVALID_ARG, "unknown launch flags 0x%x", launch_flags);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < 16)
+    return fail(PA_ERR_WORKSPACE, "workspace %zu bytes at %p", workspace_bytes, workspace);
+  pkv::AttendQ8Args a;
+  a.out = out;
+  a.q = q;
+  a.query_start_loc = nullptr;
+  a.num_query_tokens = num_seqs;
+  a.max_query_len = 1;
+  a.key_cache = key_cache;
+  a.value_cache = value_cache;
+  a.key_scale = key_scale;
+  a.value_scale = value_scale;
+  a.num_blocks = cd.num_blocks;
+  a.num_kv_heads = cd.num_kv_heads;
+  a.num_q_heads = num_q_heads;
+  a.block_tables = block_tables;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.context_lens = context_lens;
+  a.num_seqs = num_seqs;
+  a.scale = scale;
+  a.status = device_status;
+  return from_cuda(pkv::launch_attend_q8_rows(a, reinterpret_cast<cudaStream_t>(stream)),
+                   "decode_q8 launch");
+}
+
+pa_status pa_prefill_chunk_q8(void* out, const void* q, const int32_t* query_start_loc,
+                              int32_t num_query_tokens, int32_t max_query_len,
+                              const void* key_cache, const void* value_cache,
+                              const float* key_scale, const float* value_scale,
+                              pa_cache_desc cd, const int32_t* block_tables,
+                              int32_t max_blocks_per_seq, const int32_t* context_lens,
+                              int32_t num_seqs, int32_t num_q_heads, float scale,
+                              int32_t* device_status, pa_stream_t stream) {
+  pa_status st = check_attention_pools(cd);
+  if (st != PA_OK) return st;
+  if (num_seqs < 0 || max_query_len < 0 || num_query_tokens < 0 || max_blocks_per_seq <= 0)
+    return fail(PA_ERR_INVALID_ARG,
+                "num_seqs %d, num_query_tokens %d, max_query_len %d, max_blocks_per_seq %d",
+                num_seqs, num_query_tokens, max_query_len, max_blocks_per_seq);
+  if (num_q_heads <= 0 || num_q_heads % cd.num_kv_heads != 0)
+    return fail(PA_ERR_INVALID_ARG, "num_q_heads %d not a multiple of num_kv_heads %d", num_q_heads,
+                cd.num_kv_heads);
+  const int group = num_q_heads / cd.num_kv_heads;
+  if (group != 1 && group != 2 && group != 4)
+    return fail(PA_ERR_UNSUPPORTED, "query heads per kv head %d (1, 2, 4 implemented)", group);
+  if (num_seqs == 0 || max_query_len == 0 || num_query_tokens == 0) return ok();
+  if (max_query_len > num_query_tokens)
+    return fail(PA_ERR_INVALID_ARG, "max_query_len %d > num_query_tokens %d", max_query_len,
+                num_query_tokens);
+  if (!out || !q || !query_start_loc || !key_cache || !value_cache || !key_scale || !value_scale ||
+      !block_tables || !context_lens)
+    return fail(PA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(out) || !aligned16(q) || !aligned16(key_cache) || !aligned16(value_cache) ||
+      !aligned4(key_scale) || !aligned4(value_scale))
+    return fail(PA_ERR_INVALID_ARG,
+                "out/q/cache pointers must be 16-byte aligned, scale pointers 4-byte aligned");
+  if (!(scale > 0.f) || !isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "scale %g", scale);
+  pkv::AttendQ8Args a;
+  a.out = out;
+  a.q = q;
+  a.query_start_loc = query_start_loc;
+  a.num_query_tokens = num_query_tokens;
+  a.max_query_len = max_query_len;
+  a.key_cache = key_cache;
+  a.value_cache = value_cache;
+  a.key_scale = key_scale;
+  a.value_scale = value_scale;
+  a.num_blocks = cd.num_blocks;
+  a.num_kv_heads = cd.num_kv_heads;
+  a.num_q_heads = num_q_heads;
+  a.block_tables = block_tables;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.context_lens = context_lens;
+  a.num_seqs = num_seqs;
+  a.scale = scale;
+  a.status = device_status;
+  return from_cuda(pkv::launch_attend_q8_rows(a, reinterpret_cast<cudaStream_t>(stream)),
+                   "prefill_chunk_q8 launch");
+}
+
 pa_status pa_selftest_wait_timeout(int32_t* device_status, int32_t limit_ms,
                                    pa_stream_t stream) {
   if (!device_status) return fail(PA_ERR_INVALID_ARG, "null status pointer");
@@ -415,10 +675,14 @@ pa_status pa_check_device_status(const int32_t* device_status, pa_stream_t strea
   if (word == 0) return ok();
   if (word & PA_DEVFLAG_TIMEOUT)
     return fail(PA_ERR_DEVICE_TIMEOUT, "device status 0x%x: a pipeline wait timed out", word);
-  return fail(PA_ERR_DEVICE_INDEX, "device status 0x%x:%s%s%s", word,
+  const bool value_only = (word & ~(PA_DEVFLAG_NONFINITE | PA_DEVFLAG_BAD_SCALE)) == 0;
+  return fail(value_only ? PA_ERR_DEVICE_VALUE : PA_ERR_DEVICE_INDEX,
+              "device status 0x%x:%s%s%s%s%s", word,
               (word & PA_DEVFLAG_BAD_BLOCK) ? " bad block id" : "",
               (word & PA_DEVFLAG_BAD_SLOT) ? " slot beyond pool" : "",
-              (word & PA_DEVFLAG_BAD_CONTEXT) ? " bad context length" : "");
+              (word & PA_DEVFLAG_BAD_CONTEXT) ? " bad context length" : "",
+              (word & PA_DEVFLAG_NONFINITE) ? " non-finite key or value" : "",
+              (word & PA_DEVFLAG_BAD_SCALE) ? " bad scale" : "");
 }
 
 const char* pa_status_string(pa_status status) {
@@ -431,6 +695,7 @@ const char* pa_status_string(pa_status status) {
     case PA_ERR_DEVICE_INDEX: return "device reported a bad index";
     case PA_ERR_DEVICE_TIMEOUT: return "device reported a wait timeout";
     case PA_ERR_OUT_OF_BLOCKS: return "not enough free blocks";
+    case PA_ERR_DEVICE_VALUE: return "device reported a non-finite value or a bad scale";
   }
   return "unknown status";
 }

@@ -7,6 +7,7 @@
 // chunks of one block are contiguous, so reads and writes are fully coalesced.
 #include "common.cuh"
 #include "internal.h"
+#include "q8.cuh"
 
 namespace pkv {
 
@@ -42,6 +43,47 @@ cudaError_t launch_copy_blocks(void* key_cache, void* value_cache, const int64_t
   copy_blocks_kernel<<<static_cast<unsigned>((total + threads - 1) / threads), threads, 0, stream>>>(
       static_cast<uint4*>(key_cache), static_cast<uint4*>(value_cache), block_mapping, num_pairs,
       num_blocks, chunks, status);
+  return cudaGetLastError();
+}
+
+// The same for the 8-bit pools: a block is Hkv KiB of codes in each pool and Hkv scales.
+__global__ void copy_blocks_q8_kernel(uint4* __restrict__ key_cache, uint4* __restrict__ value_cache,
+                                      float* __restrict__ key_scale,
+                                      float* __restrict__ value_scale,
+                                      const int64_t* __restrict__ block_mapping,
+                                      int32_t num_pairs, int32_t num_blocks,
+                                      int32_t num_kv_heads, int32_t* __restrict__ status) {
+  const int32_t chunks_per_block = num_kv_heads * (kQ8TileBytes / 16);
+  const int64_t idx = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (idx >= static_cast<int64_t>(num_pairs) * chunks_per_block) return;
+  const int32_t pair = static_cast<int32_t>(idx / chunks_per_block);
+  const int32_t c = static_cast<int32_t>(idx % chunks_per_block);
+  const int64_t src = block_mapping[2ll * pair];
+  const int64_t dst = block_mapping[2ll * pair + 1];
+  if (src < 0 || src >= num_blocks || dst < 0 || dst >= num_blocks) {
+    if (c == 0) flag_error(status, PA_DEVFLAG_BAD_BLOCK);
+    return;
+  }
+  const uint4 k = ldg_nc128(key_cache + src * chunks_per_block + c);
+  const uint4 v = ldg_nc128(value_cache + src * chunks_per_block + c);
+  key_cache[dst * chunks_per_block + c] = k;
+  value_cache[dst * chunks_per_block + c] = v;
+  if (c < num_kv_heads) {
+    key_scale[dst * num_kv_heads + c] = key_scale[src * num_kv_heads + c];
+    value_scale[dst * num_kv_heads + c] = value_scale[src * num_kv_heads + c];
+  }
+}
+
+cudaError_t launch_copy_blocks_q8(void* key_cache, void* value_cache, float* key_scale,
+                                  float* value_scale, const int64_t* block_mapping,
+                                  int32_t num_pairs, int32_t num_blocks, int32_t num_kv_heads,
+                                  int32_t* status, cudaStream_t stream) {
+  if (num_pairs == 0) return cudaSuccess;
+  const int threads = 256;
+  const int64_t total = static_cast<int64_t>(num_pairs) * num_kv_heads * (kQ8TileBytes / 16);
+  copy_blocks_q8_kernel<<<static_cast<unsigned>((total + threads - 1) / threads), threads, 0, stream>>>(
+      static_cast<uint4*>(key_cache), static_cast<uint4*>(value_cache), key_scale, value_scale,
+      block_mapping, num_pairs, num_blocks, num_kv_heads, status);
   return cudaGetLastError();
 }
 

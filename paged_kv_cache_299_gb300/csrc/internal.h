@@ -28,6 +28,60 @@ cudaError_t launch_copy_blocks(void* key_cache, void* value_cache, const int64_t
                                int32_t num_pairs, int32_t num_blocks, int32_t num_kv_heads,
                                int32_t* status, cudaStream_t stream);
 
+cudaError_t launch_copy_blocks_q8(void* key_cache, void* value_cache, float* key_scale,
+                                  float* value_scale, const int64_t* block_mapping,
+                                  int32_t num_pairs, int32_t num_blocks, int32_t num_kv_heads,
+                                  int32_t* status, cudaStream_t stream);
+
+// Rotating appends (pa_rope_append, pa_rope_append_q8).  Strides are elements from one
+// token's rows to the next one's.
+struct AppendArgs {
+  const void* q;  // null with num_q_heads == 0
+  void* q_out;
+  const void* key;
+  const void* value;
+  int64_t q_stride, q_out_stride, key_stride, value_stride;
+  const float* cos_sin;  // [max_positions][64]: 32 cosines, then 32 sines; null: no rotation
+  int32_t max_positions;
+  bool interleaved;
+  const int32_t* block_tables;
+  int32_t max_blocks_per_seq;
+  const int32_t* context_lens;
+  const int32_t* query_start_loc;  // null: one token per sequence
+  int32_t num_seqs, num_tokens, num_q_heads, num_kv_heads, num_blocks;
+  void* key_cache;
+  void* value_cache;
+  float* key_scale;  // 8-bit pools only
+  float* value_scale;
+  int32_t* status;
+};
+
+cudaError_t launch_rope_append(const AppendArgs& a, cudaStream_t stream);
+cudaError_t launch_rope_append_q8(const AppendArgs& a, cudaStream_t stream);
+
+// Attention over the 8-bit pools: rows of q are either one per sequence (query_start_loc
+// null) or causal chunks.
+struct AttendQ8Args {
+  void* out;
+  const void* q;
+  const int32_t* query_start_loc;
+  int32_t num_query_tokens;
+  int32_t max_query_len;
+  const void* key_cache;
+  const void* value_cache;
+  const float* key_scale;
+  const float* value_scale;
+  int32_t num_blocks, num_kv_heads, num_q_heads;
+  const int32_t* block_tables;
+  int32_t max_blocks_per_seq;
+  const int32_t* context_lens;
+  int32_t num_seqs;
+  float scale;
+  int32_t* status;
+};
+
+cudaError_t launch_attend_q8_rows(const AttendQ8Args& a, cudaStream_t stream);
+
 // Work decomposition of one pa_decode call (identical in the size query and the call).
 struct DecodePlan {
   int group;          // q heads per kv head

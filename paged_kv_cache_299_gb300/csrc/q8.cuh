@@ -1,0 +1,55 @@
+// The 8-bit cache's number format: a cached value is an e4m3 code times the scale of its
+// (block, K/V head), a power of two when this library chose it.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace pkv {
+
+constexpr int kQ8RowBytes = kHeadDim;                // one token of one head: 64 codes
+constexpr int kQ8TileBytes = kHeadDim * kBlockSize;  // one (block, kv head) tile: 1 KiB
+constexpr float kCodeMax = 448.f;                    // largest e4m3 magnitude
+constexpr int kMinScaleExp = -126;                   // scales stay normal floats
+
+// Two codes (low byte first) -> two halves, exact (every e4m3 value is an f16 value).
+__device__ __forceinline__ uint32_t codes2_to_half2(uint16_t c) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+  return h;
+}
+// The four codes of a word -> two half2 (bytes 0, 1 and bytes 2, 3).
+__device__ __forceinline__ void codes4_to_half2x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ float2 half2_to_float2(uint32_t h) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// Two floats -> two codes (a in the low byte), round to nearest even, saturating at +-448.
+__device__ __forceinline__ uint16_t floats_to_codes2(float a, float b) {
+  uint16_t c;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(b), "f"(a));
+  return c;
+}
+
+// 2^e of the smallest e >= kMinScaleExp with amax <= 448 * 2^e, for finite amax >= 0.
+// 448 = 1.75 * 2^8, so with amax = 1.m * 2^x the exponent is x - 8, one more where the
+// significand exceeds 1.75.  Zeros and subnormals take the smallest scale.
+__device__ __forceinline__ float scale_for(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  int e = static_cast<int>(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  if (e < kMinScaleExp) e = kMinScaleExp;
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+__device__ __forceinline__ bool scale_ok(float s) { return s > 0.f && s < INFINITY; }
+
+}  // namespace pkv
