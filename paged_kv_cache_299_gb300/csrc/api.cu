@@ -539,7 +539,11 @@ pa_status pa_rope_append_q8(const void* q, int64_t q_stride, void* q_out, int64_
 size_t pa_decode_q8_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t num_q_heads,
                                    int32_t max_context_len) {
   if (check_decode_sizes(num_seqs, num_kv_heads, num_q_heads, max_context_len, 0) != PA_OK) return 0;
-  return num_seqs == 0 ? 0 : 16;
+  if (num_seqs == 0) return 0;
+  pkv::DecodePlan plan;
+  if (pkv::plan_decode_q8(num_seqs, num_kv_heads, num_q_heads, max_context_len, &plan) != cudaSuccess)
+    return 0;
+  return plan.workspace_bytes;
 }
 
 pa_status pa_decode_q8(void* out, const void* q, const void* key_cache, const void* value_cache,
@@ -566,8 +570,13 @@ pa_status pa_decode_q8(void* out, const void* q, const void* key_cache, const vo
   if (!(scale > 0.f) || !isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "scale %g", scale);
   if (launch_flags & ~kKnownLaunchFlags)
     return fail(PA_ERR_INVALID_ARG, "unknown launch flags 0x%x", launch_flags);
-  if (!workspace || !aligned16(workspace) || workspace_bytes < 16)
-    return fail(PA_ERR_WORKSPACE, "workspace %zu bytes at %p", workspace_bytes, workspace);
+  pkv::DecodePlan plan;
+  cudaError_t e = pkv::plan_decode_q8(num_seqs, cd.num_kv_heads, num_q_heads, max_context_len, &plan,
+                                      static_cast<int32_t>(launch_flags >> 16));
+  if (e != cudaSuccess) return from_cuda(e, "decode_q8 plan");
+  if (!workspace || workspace_bytes < plan.workspace_bytes || !aligned16(workspace))
+    return fail(PA_ERR_WORKSPACE, "workspace %zu bytes at %p, need %zu (16-byte aligned)",
+                workspace_bytes, workspace, plan.workspace_bytes);
   pkv::AttendQ8Args a;
   a.out = out;
   a.q = q;
@@ -587,7 +596,9 @@ pa_status pa_decode_q8(void* out, const void* q, const void* key_cache, const vo
   a.num_seqs = num_seqs;
   a.scale = scale;
   a.status = device_status;
-  return from_cuda(pkv::launch_attend_q8_rows(a, reinterpret_cast<cudaStream_t>(stream)),
+  return from_cuda(pkv::launch_decode_q8(a, plan, workspace,
+                                         (launch_flags & PA_LAUNCH_OVERLAP_PREVIOUS) != 0,
+                                         reinterpret_cast<cudaStream_t>(stream)),
                    "decode_q8 launch");
 }
 

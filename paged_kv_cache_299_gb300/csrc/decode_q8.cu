@@ -1,0 +1,580 @@
+// Paged decode attention over the 8-bit pools.
+//
+// For every sequence s and query head h, out = softmax(scale * q K^T) V over the
+// context_lens[s] cached tokens, K = code * key_scale and V = code * value_scale with one
+// scale per (block, K/V head).  A tile, the 16 tokens of one (block, head), therefore has one
+// scale for its scores and one for its share of the output:
+//   s_j = (scale * key_scale) q . code_j        O += value_scale * sum_j p_j code_j
+// so codes enter the tensor cores as they are and the scales cost one multiplication per
+// score and one per output element and tile.
+//
+// GB300 design.  HBM-bound: a tile is 1 KiB of K and 1 KiB of V, half the bf16 cache's.  The
+// frame is the bf16 decode kernel's: the flattened (sequence, K/V head, block) tiles are cut
+// into equal contiguous runs, one per warp of a persistent grid; each warp streams its run
+// through a private ring in shared memory, and split segments merge by log-sum-exp.  What
+// differs per tile:
+//   * one plain bulk copy per pool (a tile is contiguous), 8 stages of 2 KiB per warp;
+//   * the two scales of each of the next 32 tiles sit in the lanes' registers, loaded when
+//     the first of them is issued, a ring's length before it is consumed;
+//   * codes become f16 (cvt.rn.f16x2.e4m3x2, exact: about 43 pairs per clock and SM measured,
+//     against 14 for the bit form of bf16), straight into mma.sync m16n8k16 fragments: the
+//     order of the dims along K and of the tokens along P V is free, so every lane reads 16
+//     (K) or 8 (V) consecutive bytes of a token;
+//   * q enters as f16 scaled by a power of two per row so that its largest element lies in
+//     [2^13, 2^14): a bf16 significand fits, and elements down to 2^-27 of the largest keep
+//     all their bits;
+//   * p enters as f16 times 2^7 (at most 2^15 under the lazy maximum), so weights down to
+//     2^-31 of the largest survive; half a step of f16, 2^-12, is their rounding.
+#include <math.h>
+
+#include "common.cuh"
+#include "decode_common.cuh"
+#include "internal.h"
+#include "q8.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kWarps = 12;   // streaming warps per CTA, one CTA per SM
+constexpr int kStages = 8;   // ring depth per warp: 16 KiB in flight
+constexpr int kStageBytes = 2 * kQ8TileBytes;
+constexpr int kWindow = 32;  // tiles whose block ids and scales are held in the lanes
+constexpr int kMinTilesPerRun = 2;
+constexpr int kOneSeqMaxTilesPerWarp = 4;     // one sequence up to this: one CTA per head
+constexpr int kFusedMergeMaxContext = 8192;   // longer ones merge in the parallel merge kernel
+constexpr float kPShift = 7.f;                // log2 of the factor on p
+constexpr int kQExp = 13;                     // exponent of a row's largest f16 query element
+constexpr int kPrefetchTiles = 8;
+constexpr int kPrefetchMinTilesPerWarp = 48;
+static_assert(kStages <= kWindow, "a window's scales are loaded a ring's length ahead");
+
+struct Q8Params {
+  const float* key_scale;
+  const float* value_scale;
+};
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar,
+                                          uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1], %2, [%3], %4;" ::"r"(smem_addr(dst)),
+      "l"(src), "r"(bytes), "r"(smem_addr(bar)), "l"(policy)
+      : "memory");
+}
+
+// D (+)= A B for A with rows 8-15 zero, f16 in, fp32 accumulate.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a2, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(0u), "r"(a2), "r"(0u), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a2, uint32_t b0,
+                                             uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(0u), "r"(a2), "r"(0u), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Token of column n (0..7) of score n-tile i.  Lane q of a quad owns columns 2q and 2q + 1, so
+// its tokens are t, t + 2, t + 8 and t + 10 with t = (q & 1) + 4 (q >> 1): their 64-byte rows
+// fall on both halves of the shared-memory banks, which leaves two wavefronts per 128 bytes
+// for the 8-byte V reads and the 16-byte K reads alike (the natural order leaves four and one).
+__device__ __forceinline__ int token_of(int n, int i) {
+  return ((n >> 1) & 1) + 2 * (n & 1) + 4 * (n >> 2) + 8 * i;
+}
+
+// One tile.  Lane (r = lane / 4, q = lane % 4): MMA row r is query head r of the group (rows
+// past it are zero).  Along the dims, MMA step j takes dims 16q + 4j .. + 3 of lane q, for
+// K and Q alike; output n-tile j holds dims 16q + j and 16q + 8 + j of head r.  m is the
+// running reference maximum (log2 units, raised only when a score exceeds it by more than
+// 2^8), l this lane's share of the sum of p; p, l and o all carry 2^kPShift.
+template <bool TAIL>
+__device__ __forceinline__ void attend_tile(const uint8_t* kt, const uint8_t* vt, int r, int q,
+                                            int valid_tokens, float xs, float vs,
+                                            const uint32_t (&qa0)[4], const uint32_t (&qa2)[4],
+                                            float& m, float& l, float (&o)[8][2]) {
+  const uint4 k0 = lds128(kt + token_of(r, 0) * kQ8RowBytes + 16 * q);
+  const uint4 k1 = lds128(kt + token_of(r, 1) * kQ8RowBytes + 16 * q);
+  const int t0 = token_of(2 * q, 0);
+  uint2 v[4];  // tokens t0, t0 + 2, t0 + 8, t0 + 10, codes of dims 8r .. 8r + 7
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = *reinterpret_cast<const uint2*>(vt + (t0 + 2 * (i & 1) + 8 * (i >> 1)) * kQ8RowBytes + 8 * r);
+  float s0[4], s1[4];
+  {
+    const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t a, b, c, d;
+      codes4_to_half2x2(w0[j], a, b);
+      codes4_to_half2x2(w1[j], c, d);
+      if (j == 0) {
+        mma_f16_zero(s0, qa0[j], qa2[j], a, b);
+        mma_f16_zero(s1, qa0[j], qa2[j], c, d);
+      } else {
+        mma_f16(s0, qa0[j], qa2[j], a, b);
+        mma_f16(s1, qa0[j], qa2[j], c, d);
+      }
+    }
+  }
+  float x[4] = {s0[0] * xs, s0[1] * xs, s1[0] * xs, s1[1] * xs};
+  if (TAIL) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (t0 + 2 * (i & 1) + 8 * (i >> 1) >= valid_tokens) {
+        x[i] = -INFINITY;
+        v[i] = make_uint2(0u, 0u);  // rows past the context may hold anything
+      }
+    }
+  }
+  float mt = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+  mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+  mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
+  const bool grow = mt - m > kRescaleThreshold;  // first tile: m = -inf
+  if (__any_sync(0xffffffffu, grow)) {
+    const float alpha = grow ? fast_exp2(m - mt) : 1.f;
+    if (grow) m = mt;
+    l *= alpha;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      o[j][0] *= alpha;
+      o[j][1] *= alpha;
+    }
+  }
+  const float ref = m - kPShift;
+  const float p0 = fast_exp2(x[0] - ref), p1 = fast_exp2(x[1] - ref);
+  const float p2 = fast_exp2(x[2] - ref), p3 = fast_exp2(x[3] - ref);
+  l += (p0 + p1) + (p2 + p3);
+  const uint32_t pa0 = pack_half2(p0, p1), pa2 = pack_half2(p2, p3);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t a = h ? v[0].y : v[0].x, b = h ? v[1].y : v[1].x;
+    const uint32_t c = h ? v[2].y : v[2].x, d = h ? v[3].y : v[3].x;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {  // bytes 2u, 2u + 1 of both tokens, interleaved
+      uint32_t b00, b01, b10, b11;
+      codes4_to_half2x2(__byte_perm(a, b, u ? 0x7362 : 0x5140), b00, b01);
+      codes4_to_half2x2(__byte_perm(c, d, u ? 0x7362 : 0x5140), b10, b11);
+      float acc[4];
+      const int j = 4 * h + 2 * u;
+      mma_f16_zero(acc, pa0, pa2, b00, b10);
+      o[j][0] += vs * acc[0];
+      o[j][1] += vs * acc[1];
+      mma_f16_zero(acc, pa0, pa2, b01, b11);
+      o[j + 1][0] += vs * acc[0];
+      o[j + 1][1] += vs * acc[1];
+    }
+  }
+}
+
+template <int GROUP>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+paged_decode_q8_kernel(const KParams p, const Q8Params sp8) {
+  constexpr int kThreads = kWarps * 32;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+  const int S = p.num_seqs;
+  const int KV = p.num_kv_heads;
+
+  uint8_t* ring = smem + warp * (kStages * kStageBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kWarps * kStages * kStageBytes);
+  uint64_t* full_bar = bars + warp * kStages;
+  int32_t* seq_base = reinterpret_cast<int32_t*>(bars + kWarps * kStages);
+  __shared__ int64_t warp_sums[kWarps];
+  // piece counters of split segments whose pieces all run on this CTA, by the segment's
+  // first run modulo kWarps (two such segments never share a first run)
+  __shared__ int cta_seg_count[kWarps];
+  if (tid < kWarps) cta_seg_count[tid] = 0;
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&full_bar[i], 1);
+    fence_barrier_init();
+  }
+  // query rows are read in the middle of a stream: into L2 now
+  {
+    const int64_t q_rows = static_cast<int64_t>(S) * p.num_q_heads;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + tid; i < q_rows;
+         i += static_cast<int64_t>(gridDim.x) * kThreads)
+      prefetch_l2(reinterpret_cast<const uint8_t*>(p.q) + i * kRowBytes);
+  }
+  block_prefix<kWarps, false>(p, seq_base, warp_sums);
+
+  const int64_t total = static_cast<int64_t>(seq_base[S]) * KV;
+  // From here on every warp works alone, on one run: the plan never makes more runs than
+  // the grid has warps.
+  const int64_t gw = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  if (gw >= p.grid) return;
+  const uint64_t policy = l2_evict_first_policy();
+  const int r = lane >> 2;
+  const int q = lane & 3;
+  const int64_t start = run_start(gw, total, p.grid, 0);
+  const int64_t stop = run_start(gw + 1, total, p.grid, 0);
+
+  // ---- issue side: windows of 32 tiles of the run ----
+  int64_t wc_y = start;
+  auto next_window = [&]() -> Window {
+    Window w;
+    w.tile = 0;
+    w.g = 0;
+    const int64_t left = stop - wc_y;
+    w.n = static_cast<int>(left < kWindow ? left : kWindow);
+    if (lane < w.n) {
+      const int64_t y = wc_y + lane;
+      const int s = find_seq(seq_base, S, y, KV);
+      const int nb = seq_base[s + 1] - seq_base[s];
+      const int off = static_cast<int>(y - static_cast<int64_t>(seq_base[s]) * KV);
+      const int g = off / nb;
+      const int b = off - g * nb;
+      w.tile = __ldg(p.block_tables + static_cast<int64_t>(s) * p.max_blocks_per_seq + b);
+      w.g = g;
+    }
+    wc_y += w.n;
+    return w;
+  };
+  // Scales of the window whose tiles are consumed (cur_*) and of the one being issued (nxt_*).
+  // A run's windows are 32 tiles each but its last, so tile i of the run is entry i % 32 of
+  // window i / 32 on both sides; the issue side is at most one window ahead.
+  int64_t tile64 = 0;
+  float cur_ks = 0.f, cur_vs = 0.f, nxt_ks = 0.f, nxt_vs = 0.f;
+  auto resolve_window = [&](Window& w) {
+    const bool bad = lane < w.n && (w.tile < 0 || w.tile >= p.num_blocks);
+    const bool live = lane < w.n && !bad;
+    tile64 = live ? static_cast<int64_t>(w.tile) * KV + w.g : -1;
+    nxt_ks = live ? __ldg(sp8.key_scale + tile64) : 0.f;
+    nxt_vs = live ? __ldg(sp8.value_scale + tile64) : 0.f;
+    if (__any_sync(0xffffffffu, bad) && lane == 0) flag_error(p.status, PA_DEVFLAG_BAD_BLOCK);
+  };
+  Window cur = next_window();
+  Window nxt = next_window();
+  resolve_window(cur);
+  int cur_i = 0;
+  int issued = 0;
+  auto issue_one = [&]() {
+    if (cur_i >= cur.n) {
+      cur = nxt;
+      cur_i = 0;
+      if (cur.n == 0) return;  // nothing left to issue
+      resolve_window(cur);
+      nxt = next_window();
+    }
+    const int64_t t = __shfl_sync(0xffffffffu, tile64, cur_i);
+    const int st = issued % kStages;
+    if (lane == 0) {
+      if (t >= 0) {
+        mbar_arrive_expect_tx(&full_bar[st], kStageBytes);
+        uint8_t* dst = ring + st * kStageBytes;
+        bulk_load(dst, p.key_cache + t * kQ8TileBytes, kQ8TileBytes, &full_bar[st], policy);
+        bulk_load(dst + kQ8TileBytes, p.value_cache + t * kQ8TileBytes, kQ8TileBytes, &full_bar[st],
+                  policy);
+      } else {
+        mbar_arrive(&full_bar[st]);  // invalid block: release the stage with stale data
+      }
+    }
+    ++issued;
+    ++cur_i;
+  };
+  for (int i = 0; i < kStages; ++i) issue_one();
+  // with long runs, the next tiles are asked into L2 before the wait below
+  if (p.prefetch_ok && total >= static_cast<int64_t>(kPrefetchMinTilesPerWarp) * p.grid &&
+      lane >= cur_i && lane < cur.n && lane < cur_i + kPrefetchTiles && tile64 >= 0) {
+    bulk_prefetch_l2(p.key_cache + tile64 * kQ8TileBytes, kQ8TileBytes, policy);
+    bulk_prefetch_l2(p.value_cache + tile64 * kQ8TileBytes, kQ8TileBytes, policy);
+  }
+
+  // Everything above reads only block tables, contexts, scales and codes; queries are read and
+  // anything written only after the previous kernel in the stream has finished.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (blockIdx.x == 0 && warp == 0) {
+    for (int i = lane; i <= S; i += 32) p.ws_seq_base[i] = seq_base[i];
+    if (lane == 0) {
+      *p.ws_total = total;
+      if (total > p.tile_bound) flag_error(p.status, PA_DEVFLAG_BAD_CONTEXT);
+    }
+    if (p.fused_merge) {
+      // empty contexts: zero rows (no tile writes them)
+      const int row_elems = p.num_q_heads * kHeadDim;
+      for (int s0 = 0; s0 < S; ++s0) {
+        if (seq_base[s0 + 1] != seq_base[s0]) continue;
+        __nv_bfloat16* out = p.out + static_cast<int64_t>(s0) * row_elems;
+        for (int e = lane; e < row_elems; e += 32) out[e] = __float2bfloat16_rn(0.f);
+      }
+    }
+  }
+
+  // ---- consume side: piece by piece ----
+  int waited = 0;  // tiles whose data this warp has waited for
+  bool ok = true;
+  for (int64_t y = start; y < stop && ok;) {
+    const Piece pc = piece_at(seq_base, S, KV, y, stop);
+    const int32_t L = p.context_lens[pc.s];
+    const bool whole = pc.b0 == 0 && pc.b1 == pc.nb;
+    const bool first_piece = y == start;
+    const int ntiles = pc.b1 - pc.b0;
+
+    // This lane's 16 dims of query head r, to f16 under the row's power of two.
+    uint32_t qa0[4] = {0u, 0u, 0u, 0u}, qa2[4] = {0u, 0u, 0u, 0u};
+    float row_scale = p.q_scale;
+    {
+      uint32_t w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+      if (r < GROUP) {
+        const uint4* qrow = reinterpret_cast<const uint4*>(
+            p.q + (static_cast<int64_t>(pc.s) * p.num_q_heads + pc.g * GROUP + r) * kHeadDim);
+        const uint4 a = __ldg(qrow + 2 * q), b = __ldg(qrow + 2 * q + 1);
+        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+      }
+      uint32_t big = 0u;  // largest magnitude as bits (a NaN's bits exceed infinity's)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        big = max(big, max((w[i] << 16) & 0x7fff0000u, w[i] & 0x7fff0000u));
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      int shift = 0;  // q * 2^shift
+      if (big != 0u && big < 0x7f800000u)
+        shift = min(126, kQExp + 127 - static_cast<int>(max(big >> 23, 1u)));
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+      row_scale *= __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 a = bf16x2_to_float2(w[2 * j]), b = bf16x2_to_float2(w[2 * j + 1]);
+        qa0[j] = pack_half2(a.x * up, a.y * up);
+        qa2[j] = pack_half2(b.x * up, b.y * up);
+      }
+    }
+    float m = -INFINITY, l = 0.f;
+    float o[8][2];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = 0.f;
+
+    for (int k = 0; k < ntiles && ok; ++k) {
+      const int st = waited % kStages;
+      const uint32_t phase = static_cast<uint32_t>((waited / kStages) & 1);
+      if ((waited & (kWindow - 1)) == 0) {
+        cur_ks = nxt_ks;
+        cur_vs = nxt_vs;
+      }
+      const float xs = row_scale * __shfl_sync(0xffffffffu, cur_ks, waited & (kWindow - 1));
+      const float vs = __shfl_sync(0xffffffffu, cur_vs, waited & (kWindow - 1));
+      if (!__all_sync(0xffffffffu, mbar_wait(&full_bar[st], phase))) {
+        if (lane == 0) flag_error(p.status, PA_DEVFLAG_TIMEOUT);
+        ok = false;
+        break;
+      }
+      ++waited;
+      const uint8_t* kt = ring + st * kStageBytes;
+      const uint8_t* vt = kt + kQ8TileBytes;
+      const int valid = L - (pc.b0 + k) * kBlockSize;
+      if (valid >= kBlockSize)
+        attend_tile<false>(kt, vt, r, q, kBlockSize, xs, vs, qa0, qa2, m, l, o);
+      else
+        attend_tile<true>(kt, vt, r, q, valid, xs, vs, qa0, qa2, m, l, o);
+      // Every lane's reads of this stage have completed (their values fed the arithmetic
+      // above); the warp barrier orders them before lane 0 issues the refill.
+      __syncwarp();
+      issue_one();
+    }
+    if (!ok) break;
+
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    if (r < GROUP) {
+      if (whole) {
+        const float inv = 1.f / l;
+        const int64_t row = static_cast<int64_t>(pc.s) * p.num_q_heads + pc.g * GROUP + r;
+        uint4* dst = reinterpret_cast<uint4*>(p.out + row * kHeadDim + 16 * q);
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          w[j] = pack_bf16x2(o[2 * j][0] * inv, o[2 * j + 1][0] * inv);
+          w[4 + j] = pack_bf16x2(o[2 * j][1] * inv, o[2 * j + 1][1] * inv);
+        }
+        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      } else {
+        const int slot = first_piece ? 0 : 1;
+        float* dst = p.partials + ((gw * 2 + slot) * GROUP + r) * kPartialFloats;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          *reinterpret_cast<float2*>(dst + 16 * q + 2 * j) = make_float2(o[2 * j][0], o[2 * j + 1][0]);
+          *reinterpret_cast<float2*>(dst + 16 * q + 8 + 2 * j) = make_float2(o[2 * j][1], o[2 * j + 1][1]);
+        }
+        if (q == 0) {
+          dst[kHeadDim] = m;
+          dst[kHeadDim + 1] = l;
+        }
+      }
+    }
+    if (!whole && p.fused_merge) {
+      // Publish this piece; the warp that publishes the segment's last piece merges it, with
+      // CTA-scope ordering when all the segment's pieces ran on this CTA.
+      const int64_t x0 = static_cast<int64_t>(seq_base[pc.s]) * KV + static_cast<int64_t>(pc.g) * pc.nb;
+      const SegmentPieces sp = segment_pieces(x0, x0 + pc.nb, total, p.grid, 0);
+      const bool local = sp.c_first / kWarps == sp.c_last / kWarps;
+      int last = 0;
+      if (local) {
+        __threadfence_block();
+        __syncwarp();
+        if (lane == 0) {
+          const int n = segment_piece_count(sp, x0, x0 + pc.nb, total, p.grid);
+          last = atomicAdd(&cta_seg_count[sp.c_first % kWarps], 1) == n - 1;
+        }
+        if (__shfl_sync(0xffffffffu, last, 0)) {
+          __threadfence_block();
+          merge_segment_in_warp<GROUP, true, false>(p, sp, x0, x0 + pc.nb, total, pc.s, pc.g, lane);
+          if (lane == 0) cta_seg_count[sp.c_first % kWarps] = 0;
+        }
+      } else {
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) {
+          const int n = segment_piece_count(sp, x0, x0 + pc.nb, total, p.grid);
+          last = atomicAdd(&p.seg_count[pc.s * KV + pc.g], 1) == n - 1;
+        }
+        if (__shfl_sync(0xffffffffu, last, 0)) {
+          __threadfence();
+          merge_segment_in_warp<GROUP, false, false>(p, sp, x0, x0 + pc.nb, total, pc.s, pc.g, lane);
+          if (lane == 0) p.seg_count[pc.s * KV + pc.g] = 0;
+        }
+      }
+    }
+    y += ntiles;
+  }
+  // After a timeout, leave no copy in flight into this warp's ring (bounded waits).
+  if (!ok && lane == 0) {
+    for (int t = waited; t < issued; ++t) {
+      if (!mbar_wait(&full_bar[t % kStages], static_cast<uint32_t>((t / kStages) & 1))) break;
+    }
+  }
+}
+
+size_t smem_bytes(int num_seqs) {
+  return static_cast<size_t>(kWarps) * kStages * (kStageBytes + sizeof(uint64_t)) +
+         sizeof(int32_t) * (num_seqs + 1);
+}
+
+template <int GROUP>
+cudaError_t prepare_kernel() {
+  static bool done = false;  // benign race: the attribute calls are idempotent
+  if (done) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(paged_decode_q8_kernel<GROUP>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem_bytes(kMaxSeqs)));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(paged_decode_q8_kernel<GROUP>,
+                             cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess) done = true;
+  return e;
+}
+
+template <int GROUP>
+cudaError_t launch(const AttendQ8Args& a, const DecodePlan& plan, void* workspace,
+                   bool overlap_previous, cudaStream_t stream) {
+  cudaError_t e = prepare_kernel<GROUP>();
+  if (e != cudaSuccess) return e;
+  KParams p = {};
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.key_cache = static_cast<const uint8_t*>(a.key_cache);
+  p.value_cache = static_cast<const uint8_t*>(a.value_cache);
+  p.block_tables = a.block_tables;
+  p.max_blocks_per_seq = a.max_blocks_per_seq;
+  p.context_lens = a.context_lens;
+  p.num_seqs = a.num_seqs;
+  p.num_q_heads = a.num_q_heads;
+  p.num_kv_heads = a.num_kv_heads;
+  p.num_blocks = a.num_blocks;
+  p.q_scale = a.scale * 1.4426950408889634f;
+  p.grid = plan.runs;
+  p.chunk = 0;
+  p.tile_bound = plan.tile_bound;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.ws_total = reinterpret_cast<int64_t*>(ws);
+  p.ws_seq_base = reinterpret_cast<int32_t*>(ws + 16);
+  p.seg_count = reinterpret_cast<int32_t*>(ws + plan.ws_count_offset);
+  p.partials = reinterpret_cast<float*>(ws + plan.ws_meta_bytes);
+  p.fused_merge = plan.fused_merge ? 1 : 0;
+  p.prefetch_ok = plan.prefetch_ok ? 1 : 0;
+  p.status = a.status;
+  const Q8Params s = {a.key_scale, a.value_scale};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(plan.grid);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = plan.smem_bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = overlap_previous ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, paged_decode_q8_kernel<GROUP>, p, s);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess || plan.fused_merge) return e;
+  return launch_merge<GROUP>(p, plan, false, stream);
+}
+
+}  // namespace
+
+cudaError_t plan_decode_q8(int32_t num_seqs, int32_t num_kv_heads, int32_t num_q_heads,
+                           int32_t max_context_len, DecodePlan* plan, int32_t max_sms) {
+  const int group = num_q_heads / num_kv_heads;
+  plan->group = group;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks_max = (static_cast<int64_t>(max_context_len) + kBlockSize - 1) / kBlockSize;
+  const int64_t tiles_upper = static_cast<int64_t>(num_seqs) * num_kv_heads * blocks_max;
+  // one CTA per SM (the ring takes most of its shared memory)
+  const int64_t resident = max_sms > 0 && max_sms < sms ? max_sms : sms;
+  int64_t runs = resident * kWarps;
+  const int64_t by_size = (tiles_upper + kMinTilesPerRun - 1) / kMinTilesPerRun;
+  if (by_size < runs) runs = by_size;
+  // One short sequence: one CTA per K/V head, so that every segment's pieces publish and
+  // merge with CTA-scope ordering.
+  if (num_seqs == 1 && num_kv_heads <= resident &&
+      tiles_upper <= static_cast<int64_t>(kOneSeqMaxTilesPerWarp) * num_kv_heads * kWarps)
+    runs = static_cast<int64_t>(num_kv_heads) * kWarps;
+  if (runs < 1) runs = 1;
+  plan->runs = static_cast<int>(runs);
+  plan->chunk = 0;
+  plan->tile_bound = tiles_upper;
+  plan->grid = static_cast<int>((runs + kWarps - 1) / kWarps);
+  plan->smem_bytes = smem_bytes(num_seqs);
+  plan->fused_merge = max_context_len <= kFusedMergeMaxContext;
+  const int64_t seg_pieces = runs / (static_cast<int64_t>(num_seqs) * num_kv_heads) + 2;
+  plan->merge_split_heads = !plan->fused_merge && seg_pieces >= kMergeSplitPieces;
+  plan->prefetch_ok = !(max_sms > 0 && max_sms < sms);
+  plan->ws_count_offset = (16 + sizeof(int32_t) * (num_seqs + 1) + 255) / 256 * 256;
+  plan->ws_meta_bytes = plan->ws_count_offset +
+                        (sizeof(int32_t) * num_seqs * num_kv_heads + 255) / 256 * 256;
+  // sized for the whole device, so that any SM budget fits
+  const int64_t runs_full = runs > static_cast<int64_t>(sms) * kWarps
+                                ? runs : static_cast<int64_t>(sms) * kWarps;
+  plan->workspace_bytes = plan->ws_meta_bytes +
+                          static_cast<size_t>(runs_full) * 2 * group * kPartialFloats * sizeof(float);
+  return cudaSuccess;
+}
+
+cudaError_t launch_decode_q8(const AttendQ8Args& a, const DecodePlan& plan, void* workspace,
+                             bool overlap_previous, cudaStream_t stream) {
+  switch (plan.group) {
+    case 1: return launch<1>(a, plan, workspace, overlap_previous, stream);
+    case 2: return launch<2>(a, plan, workspace, overlap_previous, stream);
+    case 4: return launch<4>(a, plan, workspace, overlap_previous, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace pkv

@@ -105,6 +105,12 @@ cudaError_t plan_decode(int32_t num_seqs, int32_t num_kv_heads, int32_t num_q_he
                         int32_t max_context_len, int32_t partition_tokens, DecodePlan* plan,
                         int32_t max_sms = 0);
 
+// The same for pa_decode_q8.
+cudaError_t plan_decode_q8(int32_t num_seqs, int32_t num_kv_heads, int32_t num_q_heads,
+                           int32_t max_context_len, DecodePlan* plan, int32_t max_sms = 0);
+cudaError_t launch_decode_q8(const AttendQ8Args& a, const DecodePlan& plan, void* workspace,
+                             bool overlap_previous, cudaStream_t stream);
+
 struct DecodeArgs {
   void* out;
   const void* q;
