@@ -52,6 +52,17 @@ pa_status check_desc(const pa_cache_desc& cd) {
   return PA_OK;
 }
 
+// The 8-bit decode numbers the (block, head) tiles of a pool in 31 bits.
+pa_status check_q8_desc(const pa_cache_desc& cd) {
+  pa_status st = check_desc(cd);
+  if (st != PA_OK) return st;
+  const int64_t tiles = static_cast<int64_t>(cd.num_blocks) * cd.num_kv_heads;
+  if (tiles >= (int64_t{1} << 31))
+    return fail(PA_ERR_UNSUPPORTED, "cache desc: %d blocks x %d kv heads = %lld tiles (fewer than "
+                "2^31 supported)", cd.num_blocks, cd.num_kv_heads, static_cast<long long>(tiles));
+  return PA_OK;
+}
+
 // The attention kernels read the pools through tensor maps over [blocks x heads x 16][64]
 // rows with 32-bit row coordinates: fewer than 2^31 rows (each pool under 256 GiB).
 pa_status check_attention_pools(const pa_cache_desc& cd) {
@@ -553,7 +564,7 @@ pa_status pa_decode_q8(void* out, const void* q, const void* key_cache, const vo
                        float scale, int32_t max_context_len, void* workspace,
                        size_t workspace_bytes, uint32_t launch_flags, int32_t* device_status,
                        pa_stream_t stream) {
-  pa_status st = check_desc(cd);
+  pa_status st = check_q8_desc(cd);
   if (st != PA_OK) return st;
   st = check_decode_sizes(num_seqs, cd.num_kv_heads, num_q_heads, max_context_len, 0);
   if (st != PA_OK) return st;

@@ -92,26 +92,32 @@ __device__ __forceinline__ int token_of(int n, int i) {
   return ((n >> 1) & 1) + 2 * (n & 1) + 4 * (n >> 2) + 8 * i;
 }
 
-// One tile.  Lane (r = lane / 4, q = lane % 4): MMA row r is query head r of the group (rows
-// past it are zero).  Along the dims, MMA step j takes dims 16q + 4j .. + 3 of lane q, for
-// K and Q alike; output n-tile j holds dims 16q + j and 16q + 8 + j of head r.  m is the
-// running reference maximum (log2 units, raised only when a score exceeds it by more than
-// 2^8), l this lane's share of the sum of p; p, l and o all carry 2^kPShift.
-template <bool TAIL>
-__device__ __forceinline__ void attend_tile(const uint8_t* kt, const uint8_t* vt, int r, int q,
-                                            int valid_tokens, float xs, float vs,
+// Two consecutive tiles a and b of a segment (32 tokens).  Lane (r = lane / 4, q = lane % 4):
+// MMA row r is query head r of the group (rows past it are zero).  Along the dims, MMA step j
+// takes dims 16q + 4j .. + 3 of lane q, for K and Q alike; output n-tile j holds dims 16q + j
+// and 16q + 8 + j of head r.  m is the running reference maximum (log2 units, raised only when
+// a score exceeds it by more than 2^8), l this lane's share of the sum of p; p, l and o all
+// carry 2^kPShift.  MASK: only the first `valid` tokens count; the rest may hold anything.
+template <bool MASK>
+__device__ __forceinline__ void attend_pair(const uint8_t* ta, const uint8_t* tb, int r, int q,
+                                            int valid, const float (&xs)[2], const float (&vs)[2],
                                             const uint32_t (&qa0)[4], const uint32_t (&qa2)[4],
-                                            float& m, float& l, float (&o)[8][2]) {
-  const uint4 k0 = lds128(kt + token_of(r, 0) * kQ8RowBytes + 16 * q);
-  const uint4 k1 = lds128(kt + token_of(r, 1) * kQ8RowBytes + 16 * q);
+                                            float& m, float& l, float2 (&o)[8]) {
   const int t0 = token_of(2 * q, 0);
-  uint2 v[4];  // tokens t0, t0 + 2, t0 + 8, t0 + 10, codes of dims 8r .. 8r + 7
+  const int k_off = token_of(r, 0) * kQ8RowBytes + 16 * q;
+  const int v_off = kQ8TileBytes + t0 * kQ8RowBytes + 8 * r;
+  uint2 v[2][4];  // tokens t0, t0 + 2, t0 + 8, t0 + 10 of each tile, codes of dims 8r .. 8r + 7
+  float x[2][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    v[i] = *reinterpret_cast<const uint2*>(vt + (t0 + 2 * (i & 1) + 8 * (i >> 1)) * kQ8RowBytes + 8 * r);
-  float s0[4], s1[4];
-  {
+  for (int t = 0; t < 2; ++t) {
+    const uint8_t* tile = t ? tb : ta;
+    const uint4 k0 = lds128(tile + k_off);
+    const uint4 k1 = lds128(tile + k_off + 8 * kQ8RowBytes);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[t][i] = *reinterpret_cast<const uint2*>(tile + v_off + (2 * (i & 1) + 8 * (i >> 1)) * kQ8RowBytes);
     const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+    float s0[4], s1[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint32_t a, b, c, d;
@@ -125,53 +131,60 @@ __device__ __forceinline__ void attend_tile(const uint8_t* kt, const uint8_t* vt
         mma_f16(s1, qa0[j], qa2[j], c, d);
       }
     }
-  }
-  float x[4] = {s0[0] * xs, s0[1] * xs, s1[0] * xs, s1[1] * xs};
-  if (TAIL) {
+    x[t][0] = s0[0] * xs[t];
+    x[t][1] = s0[1] * xs[t];
+    x[t][2] = s1[0] * xs[t];
+    x[t][3] = s1[1] * xs[t];
+    if (MASK) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (t0 + 2 * (i & 1) + 8 * (i >> 1) >= valid_tokens) {
-        x[i] = -INFINITY;
-        v[i] = make_uint2(0u, 0u);  // rows past the context may hold anything
+      for (int i = 0; i < 4; ++i) {
+        if (16 * t + t0 + 2 * (i & 1) + 8 * (i >> 1) >= valid) {
+          x[t][i] = -INFINITY;
+          v[t][i] = make_uint2(0u, 0u);
+        }
       }
     }
   }
-  float mt = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+  float mt = fmaxf(max3f(x[0][0], x[0][1], x[0][2]), max3f(x[0][3], x[1][0], x[1][1]));
+  mt = max3f(mt, x[1][2], x[1][3]);
   mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
   mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
-  const bool grow = mt - m > kRescaleThreshold;  // first tile: m = -inf
+  const bool grow = mt - m > kRescaleThreshold;  // first pair: m = -inf
   if (__any_sync(0xffffffffu, grow)) {
     const float alpha = grow ? fast_exp2(m - mt) : 1.f;
     if (grow) m = mt;
     l *= alpha;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      o[j][0] *= alpha;
-      o[j][1] *= alpha;
+      o[j].x *= alpha;
+      o[j].y *= alpha;
     }
   }
   const float ref = m - kPShift;
-  const float p0 = fast_exp2(x[0] - ref), p1 = fast_exp2(x[1] - ref);
-  const float p2 = fast_exp2(x[2] - ref), p3 = fast_exp2(x[3] - ref);
-  l += (p0 + p1) + (p2 + p3);
-  const uint32_t pa0 = pack_half2(p0, p1), pa2 = pack_half2(p2, p3);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t a = h ? v[0].y : v[0].x, b = h ? v[1].y : v[1].x;
-    const uint32_t c = h ? v[2].y : v[2].x, d = h ? v[3].y : v[3].x;
+  for (int t = 0; t < 2; ++t) {
+    const float p0 = fast_exp2(x[t][0] - ref), p1 = fast_exp2(x[t][1] - ref);
+    const float p2 = fast_exp2(x[t][2] - ref), p3 = fast_exp2(x[t][3] - ref);
+    l += (p0 + p1) + (p2 + p3);
+    const uint32_t pa0 = pack_half2(p0, p1), pa2 = pack_half2(p2, p3);
+    const float2 vs2 = make_float2(MASK && t == 1 && valid <= kBlockSize ? 0.f : vs[t],
+                                   MASK && t == 1 && valid <= kBlockSize ? 0.f : vs[t]);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {  // bytes 2u, 2u + 1 of both tokens, interleaved
-      uint32_t b00, b01, b10, b11;
-      codes4_to_half2x2(__byte_perm(a, b, u ? 0x7362 : 0x5140), b00, b01);
-      codes4_to_half2x2(__byte_perm(c, d, u ? 0x7362 : 0x5140), b10, b11);
-      float acc[4];
-      const int j = 4 * h + 2 * u;
-      mma_f16_zero(acc, pa0, pa2, b00, b10);
-      o[j][0] += vs * acc[0];
-      o[j][1] += vs * acc[1];
-      mma_f16_zero(acc, pa0, pa2, b01, b11);
-      o[j + 1][0] += vs * acc[0];
-      o[j + 1][1] += vs * acc[1];
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t a = h ? v[t][0].y : v[t][0].x, b = h ? v[t][1].y : v[t][1].x;
+      const uint32_t c = h ? v[t][2].y : v[t][2].x, d = h ? v[t][3].y : v[t][3].x;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {  // bytes 2u, 2u + 1 of both tokens, interleaved
+        uint32_t b00, b01, b10, b11;
+        codes4_to_half2x2(__byte_perm(a, b, u ? 0x7362 : 0x5140), b00, b01);
+        codes4_to_half2x2(__byte_perm(c, d, u ? 0x7362 : 0x5140), b10, b11);
+        float acc[4];
+        const int j = 4 * h + 2 * u;
+        mma_f16_zero(acc, pa0, pa2, b00, b10);
+        o[j] = __ffma2_rn(make_float2(acc[0], acc[1]), vs2, o[j]);
+        mma_f16_zero(acc, pa0, pa2, b01, b11);
+        o[j + 1] = __ffma2_rn(make_float2(acc[0], acc[1]), vs2, o[j + 1]);
+      }
     }
   }
 }
@@ -245,14 +258,13 @@ paged_decode_q8_kernel(const KParams p, const Q8Params sp8) {
   // Scales of the window whose tiles are consumed (cur_*) and of the one being issued (nxt_*).
   // A run's windows are 32 tiles each but its last, so tile i of the run is entry i % 32 of
   // window i / 32 on both sides; the issue side is at most one window ahead.
-  int64_t tile64 = 0;
   float cur_ks = 0.f, cur_vs = 0.f, nxt_ks = 0.f, nxt_vs = 0.f;
   auto resolve_window = [&](Window& w) {
     const bool bad = lane < w.n && (w.tile < 0 || w.tile >= p.num_blocks);
     const bool live = lane < w.n && !bad;
-    tile64 = live ? static_cast<int64_t>(w.tile) * KV + w.g : -1;
-    nxt_ks = live ? __ldg(sp8.key_scale + tile64) : 0.f;
-    nxt_vs = live ? __ldg(sp8.value_scale + tile64) : 0.f;
+    w.tile = live ? w.tile * KV + w.g : -1;
+    nxt_ks = live ? __ldg(sp8.key_scale + w.tile) : 0.f;
+    nxt_vs = live ? __ldg(sp8.value_scale + w.tile) : 0.f;
     if (__any_sync(0xffffffffu, bad) && lane == 0) flag_error(p.status, PA_DEVFLAG_BAD_BLOCK);
   };
   Window cur = next_window();
@@ -260,6 +272,19 @@ paged_decode_q8_kernel(const KParams p, const Q8Params sp8) {
   resolve_window(cur);
   int cur_i = 0;
   int issued = 0;
+  // Lane `slot` (0 or 1) requests tile t into the ring's stage issued + slot.
+  auto request = [&](int32_t t, int slot) {
+    const int st = (issued + slot) % kStages;
+    if (t >= 0) {
+      mbar_arrive_expect_tx(&full_bar[st], kStageBytes);
+      uint8_t* dst = ring + st * kStageBytes;
+      const int64_t off = static_cast<int64_t>(t) * kQ8TileBytes;
+      bulk_load(dst, p.key_cache + off, kQ8TileBytes, &full_bar[st], policy);
+      bulk_load(dst + kQ8TileBytes, p.value_cache + off, kQ8TileBytes, &full_bar[st], policy);
+    } else {
+      mbar_arrive(&full_bar[st]);  // invalid block: release the stage with stale data
+    }
+  };
   auto issue_one = [&]() {
     if (cur_i >= cur.n) {
       cur = nxt;
@@ -268,28 +293,29 @@ paged_decode_q8_kernel(const KParams p, const Q8Params sp8) {
       resolve_window(cur);
       nxt = next_window();
     }
-    const int64_t t = __shfl_sync(0xffffffffu, tile64, cur_i);
-    const int st = issued % kStages;
-    if (lane == 0) {
-      if (t >= 0) {
-        mbar_arrive_expect_tx(&full_bar[st], kStageBytes);
-        uint8_t* dst = ring + st * kStageBytes;
-        bulk_load(dst, p.key_cache + t * kQ8TileBytes, kQ8TileBytes, &full_bar[st], policy);
-        bulk_load(dst + kQ8TileBytes, p.value_cache + t * kQ8TileBytes, kQ8TileBytes, &full_bar[st],
-                  policy);
-      } else {
-        mbar_arrive(&full_bar[st]);  // invalid block: release the stage with stale data
-      }
-    }
+    const int32_t t = __shfl_sync(0xffffffffu, cur.tile, cur_i);
+    if (lane == 0) request(t, 0);
     ++issued;
     ++cur_i;
+  };
+  auto issue_two = [&]() {
+    if (cur_i + 2 > cur.n) {
+      issue_one();
+      issue_one();
+      return;
+    }
+    const int32_t t = __shfl_sync(0xffffffffu, cur.tile, cur_i + (lane & 1));
+    if (lane < 2) request(t, lane);
+    issued += 2;
+    cur_i += 2;
   };
   for (int i = 0; i < kStages; ++i) issue_one();
   // with long runs, the next tiles are asked into L2 before the wait below
   if (p.prefetch_ok && total >= static_cast<int64_t>(kPrefetchMinTilesPerWarp) * p.grid &&
-      lane >= cur_i && lane < cur.n && lane < cur_i + kPrefetchTiles && tile64 >= 0) {
-    bulk_prefetch_l2(p.key_cache + tile64 * kQ8TileBytes, kQ8TileBytes, policy);
-    bulk_prefetch_l2(p.value_cache + tile64 * kQ8TileBytes, kQ8TileBytes, policy);
+      lane >= cur_i && lane < cur.n && lane < cur_i + kPrefetchTiles && cur.tile >= 0) {
+    const int64_t off = static_cast<int64_t>(cur.tile) * kQ8TileBytes;
+    bulk_prefetch_l2(p.key_cache + off, kQ8TileBytes, policy);
+    bulk_prefetch_l2(p.value_cache + off, kQ8TileBytes, policy);
   }
 
   // Everything above reads only block tables, contexts, scales and codes; queries are read and
@@ -353,36 +379,53 @@ paged_decode_q8_kernel(const KParams p, const Q8Params sp8) {
       }
     }
     float m = -INFINITY, l = 0.f;
-    float o[8][2];
+    float2 o[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = 0.f;
+    for (int j = 0; j < 8; ++j) o[j] = make_float2(0.f, 0.f);
 
-    for (int k = 0; k < ntiles && ok; ++k) {
-      const int st = waited % kStages;
-      const uint32_t phase = static_cast<uint32_t>((waited / kStages) & 1);
+    for (int k = 0; k < ntiles; k += 2) {
+      const bool two = k + 1 < ntiles;
+      const int sa = waited % kStages, sb = (waited + 1) % kStages;
+      float xs[2], vs[2];
       if ((waited & (kWindow - 1)) == 0) {
         cur_ks = nxt_ks;
         cur_vs = nxt_vs;
       }
-      const float xs = row_scale * __shfl_sync(0xffffffffu, cur_ks, waited & (kWindow - 1));
-      const float vs = __shfl_sync(0xffffffffu, cur_vs, waited & (kWindow - 1));
-      if (!__all_sync(0xffffffffu, mbar_wait(&full_bar[st], phase))) {
+      xs[0] = __shfl_sync(0xffffffffu, cur_ks, waited & (kWindow - 1));
+      vs[0] = __shfl_sync(0xffffffffu, cur_vs, waited & (kWindow - 1));
+      if (two && ((waited + 1) & (kWindow - 1)) == 0) {
+        cur_ks = nxt_ks;
+        cur_vs = nxt_vs;
+      }
+      xs[1] = __shfl_sync(0xffffffffu, cur_ks, (waited + 1) & (kWindow - 1));
+      vs[1] = __shfl_sync(0xffffffffu, cur_vs, (waited + 1) & (kWindow - 1));
+      xs[0] *= row_scale;
+      xs[1] *= row_scale;
+      bool here = mbar_wait(&full_bar[sa], static_cast<uint32_t>((waited / kStages) & 1));
+      if (two)
+        here &= mbar_wait(&full_bar[sb], static_cast<uint32_t>(((waited + 1) / kStages) & 1));
+      if (!__all_sync(0xffffffffu, here)) {
         if (lane == 0) flag_error(p.status, PA_DEVFLAG_TIMEOUT);
         ok = false;
         break;
       }
-      ++waited;
-      const uint8_t* kt = ring + st * kStageBytes;
-      const uint8_t* vt = kt + kQ8TileBytes;
+      const uint8_t* ta = ring + sa * kStageBytes;
+      const uint8_t* tb = two ? ring + sb * kStageBytes : ta;
       const int valid = L - (pc.b0 + k) * kBlockSize;
-      if (valid >= kBlockSize)
-        attend_tile<false>(kt, vt, r, q, kBlockSize, xs, vs, qa0, qa2, m, l, o);
+      if (two && valid >= 2 * kBlockSize)
+        attend_pair<false>(ta, tb, r, q, 2 * kBlockSize, xs, vs, qa0, qa2, m, l, o);
       else
-        attend_tile<true>(kt, vt, r, q, valid, xs, vs, qa0, qa2, m, l, o);
-      // Every lane's reads of this stage have completed (their values fed the arithmetic
-      // above); the warp barrier orders them before lane 0 issues the refill.
+        attend_pair<true>(ta, tb, r, q, two ? valid : min(valid, kBlockSize), xs, vs, qa0, qa2, m, l, o);
+      // Every lane's reads of these stages have completed (their values fed the arithmetic
+      // above); the warp barrier orders them before the refills.
       __syncwarp();
-      issue_one();
+      if (two) {
+        waited += 2;
+        issue_two();
+      } else {
+        waited += 1;
+        issue_one();
+      }
     }
     if (!ok) break;
 
@@ -396,8 +439,8 @@ paged_decode_q8_kernel(const KParams p, const Q8Params sp8) {
         uint32_t w[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          w[j] = pack_bf16x2(o[2 * j][0] * inv, o[2 * j + 1][0] * inv);
-          w[4 + j] = pack_bf16x2(o[2 * j][1] * inv, o[2 * j + 1][1] * inv);
+          w[j] = pack_bf16x2(o[2 * j].x * inv, o[2 * j + 1].x * inv);
+          w[4 + j] = pack_bf16x2(o[2 * j].y * inv, o[2 * j + 1].y * inv);
         }
         dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
         dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
@@ -406,8 +449,8 @@ paged_decode_q8_kernel(const KParams p, const Q8Params sp8) {
         float* dst = p.partials + ((gw * 2 + slot) * GROUP + r) * kPartialFloats;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          *reinterpret_cast<float2*>(dst + 16 * q + 2 * j) = make_float2(o[2 * j][0], o[2 * j + 1][0]);
-          *reinterpret_cast<float2*>(dst + 16 * q + 8 + 2 * j) = make_float2(o[2 * j][1], o[2 * j + 1][1]);
+          *reinterpret_cast<float2*>(dst + 16 * q + 2 * j) = make_float2(o[2 * j].x, o[2 * j + 1].x);
+          *reinterpret_cast<float2*>(dst + 16 * q + 8 + 2 * j) = make_float2(o[2 * j].y, o[2 * j + 1].y);
         }
         if (q == 0) {
           dst[kHeadDim] = m;
