@@ -63,6 +63,10 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l1(const void* p) {
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
+}
+
 // D (+)= A B for A with rows 8-15 zero, f16 in, fp32 accumulate.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a2, uint32_t b0,
                                         uint32_t b1) {
@@ -226,27 +230,27 @@ paged_decode_q8_kernel(const KParams p, const Q8Params sp8) {
   const int64_t total = static_cast<int64_t>(seq_base[S]) * KV;
   // From here on every warp works alone, on one run: the plan never makes more runs than
   // the grid has warps.
-  const int64_t gw = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  const int gw = blockIdx.x * kWarps + warp;
   if (gw >= p.grid) return;
   const uint64_t policy = l2_evict_first_policy();
   const int r = lane >> 2;
   const int q = lane & 3;
-  const int64_t start = run_start(gw, total, p.grid, 0);
-  const int64_t stop = run_start(gw + 1, total, p.grid, 0);
+  // (block_prefix keeps the tile count below 2^31)
+  const int start = static_cast<int>(run_start(gw, total, p.grid, 0));
+  const int stop = static_cast<int>(run_start(gw + 1, total, p.grid, 0));
 
   // ---- issue side: windows of 32 tiles of the run ----
-  int64_t wc_y = start;
+  int wc_y = start;
   auto next_window = [&]() -> Window {
     Window w;
     w.tile = 0;
     w.g = 0;
-    const int64_t left = stop - wc_y;
-    w.n = static_cast<int>(left < kWindow ? left : kWindow);
+    w.n = min(stop - wc_y, kWindow);
     if (lane < w.n) {
-      const int64_t y = wc_y + lane;
+      const int y = wc_y + lane;
       const int s = find_seq(seq_base, S, y, KV);
       const int nb = seq_base[s + 1] - seq_base[s];
-      const int off = static_cast<int>(y - static_cast<int64_t>(seq_base[s]) * KV);
+      const int off = y - seq_base[s] * KV;
       const int g = off / nb;
       const int b = off - g * nb;
       w.tile = __ldg(p.block_tables + static_cast<int64_t>(s) * p.max_blocks_per_seq + b);
@@ -285,31 +289,35 @@ paged_decode_q8_kernel(const KParams p, const Q8Params sp8) {
       mbar_arrive(&full_bar[st]);  // invalid block: release the stage with stale data
     }
   };
-  auto issue_one = [&]() {
-    if (cur_i >= cur.n) {
-      cur = nxt;
-      cur_i = 0;
-      if (cur.n == 0) return;  // nothing left to issue
-      resolve_window(cur);
-      nxt = next_window();
-    }
-    const int32_t t = __shfl_sync(0xffffffffu, cur.tile, cur_i);
-    if (lane == 0) request(t, 0);
-    ++issued;
-    ++cur_i;
-  };
-  auto issue_two = [&]() {
-    if (cur_i + 2 > cur.n) {
-      issue_one();
-      issue_one();
+  // Requests the next n (1 or 2) tiles of the run, as far as there are any.
+  auto issue = [&](int n) {
+    if (cur_i + n <= cur.n) {
+      const int32_t t = __shfl_sync(0xffffffffu, cur.tile, cur_i + (n - 1 & lane));
+      if (lane < n) request(t, lane);
+      issued += n;
+      cur_i += n;
       return;
     }
-    const int32_t t = __shfl_sync(0xffffffffu, cur.tile, cur_i + (lane & 1));
-    if (lane < 2) request(t, lane);
-    issued += 2;
-    cur_i += 2;
+#pragma unroll 1
+    for (; n > 0; --n) {
+      if (cur_i >= cur.n) {
+        cur = nxt;
+        cur_i = 0;
+        if (cur.n == 0) return;  // nothing left
+        resolve_window(cur);
+        nxt = next_window();
+      }
+      const int32_t t = __shfl_sync(0xffffffffu, cur.tile, cur_i);
+      if (lane == 0) request(t, 0);
+      ++issued;
+      ++cur_i;
+    }
   };
-  for (int i = 0; i < kStages; ++i) issue_one();
+  {  // the ring's first fill, one lane per stage (a first window below 32 tiles is the only one)
+    const int n0 = cur.n < kStages ? cur.n : kStages;
+    if (lane < n0) request(cur.tile, lane);
+    issued = cur_i = n0;
+  }
   // with long runs, the next tiles are asked into L2 before the wait below
   if (p.prefetch_ok && total >= static_cast<int64_t>(kPrefetchMinTilesPerWarp) * p.grid &&
       lane >= cur_i && lane < cur.n && lane < cur_i + kPrefetchTiles && cur.tile >= 0) {
@@ -318,48 +326,68 @@ paged_decode_q8_kernel(const KParams p, const Q8Params sp8) {
     bulk_prefetch_l2(p.value_cache + off, kQ8TileBytes, policy);
   }
 
+  Piece nx = {};
+  if (start < stop) nx = piece_at(seq_base, S, KV, start, stop);
+
   // Everything above reads only block tables, contexts, scales and codes; queries are read and
   // anything written only after the previous kernel in the stream has finished.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (blockIdx.x == 0 && warp == 0) {
-    for (int i = lane; i <= S; i += 32) p.ws_seq_base[i] = seq_base[i];
+    if (!p.fused_merge)  // for the merge kernel
+      for (int i = lane; i <= S; i += 32) p.ws_seq_base[i] = seq_base[i];
     if (lane == 0) {
       *p.ws_total = total;
       if (total > p.tile_bound) flag_error(p.status, PA_DEVFLAG_BAD_CONTEXT);
     }
-    if (p.fused_merge) {
-      // empty contexts: zero rows (no tile writes them)
-      const int row_elems = p.num_q_heads * kHeadDim;
-      for (int s0 = 0; s0 < S; ++s0) {
-        if (seq_base[s0 + 1] != seq_base[s0]) continue;
-        __nv_bfloat16* out = p.out + static_cast<int64_t>(s0) * row_elems;
-        for (int e = lane; e < row_elems; e += 32) out[e] = __float2bfloat16_rn(0.f);
-      }
+  }
+  if (p.fused_merge) {
+    // empty contexts: zero rows (no tile writes them), a sequence per warp of the grid
+    const int row_elems = p.num_q_heads * kHeadDim;
+    for (int s0 = gw; s0 < S; s0 += p.grid) {
+      if (seq_base[s0 + 1] != seq_base[s0]) continue;
+      __nv_bfloat16* out = p.out + static_cast<int64_t>(s0) * row_elems;
+      for (int e = lane; e < row_elems; e += 32) out[e] = __float2bfloat16_rn(0.f);
     }
   }
 
   // ---- consume side: piece by piece ----
+  // This lane's 16 dims of query head r of a piece (lanes past the group take the last head's
+  // and drop them).
+  auto query_of = [&](int s, int g) {
+    return reinterpret_cast<const uint4*>(
+        p.q + (static_cast<int64_t>(s) * p.num_q_heads + g * GROUP + min(r, GROUP - 1)) * kHeadDim) + 2 * q;
+  };
   int waited = 0;  // tiles whose data this warp has waited for
   bool ok = true;
-  for (int64_t y = start; y < stop && ok;) {
-    const Piece pc = piece_at(seq_base, S, KV, y, stop);
-    const int32_t L = p.context_lens[pc.s];
+  for (int y = start; y < stop && ok;) {
+    const Piece pc = nx;
+    const int32_t L = __ldg(p.context_lens + pc.s);
+    const uint4 qx = __ldg(query_of(pc.s, pc.g)), qy = __ldg(query_of(pc.s, pc.g) + 1);
     const bool whole = pc.b0 == 0 && pc.b1 == pc.nb;
     const bool first_piece = y == start;
     const int ntiles = pc.b1 - pc.b0;
+    const int left = stop - y - ntiles;
+    if (left > 0) {  // the next head of this sequence, or the next sequence that has tokens
+      if (++nx.g == KV) {
+        nx.g = 0;
+        do {
+          ++nx.s;
+          nx.nb = seq_base[nx.s + 1] - seq_base[nx.s];
+        } while (nx.nb == 0);
+      }
+      nx.b0 = 0;
+      nx.b1 = min(nx.nb, left);
+      // on their way to L1 while this piece streams
+      prefetch_l1(query_of(nx.s, nx.g));
+      prefetch_l1(p.context_lens + nx.s);
+    }
 
-    // This lane's 16 dims of query head r, to f16 under the row's power of two.
-    uint32_t qa0[4] = {0u, 0u, 0u, 0u}, qa2[4] = {0u, 0u, 0u, 0u};
+    // The query, to f16 under the row's power of two.
+    uint32_t qa0[4], qa2[4];
     float row_scale = p.q_scale;
     {
-      uint32_t w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-      if (r < GROUP) {
-        const uint4* qrow = reinterpret_cast<const uint4*>(
-            p.q + (static_cast<int64_t>(pc.s) * p.num_q_heads + pc.g * GROUP + r) * kHeadDim);
-        const uint4 a = __ldg(qrow + 2 * q), b = __ldg(qrow + 2 * q + 1);
-        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-      }
+      const uint32_t w[8] = {qx.x, qx.y, qx.z, qx.w, qy.x, qy.y, qy.z, qy.w};
+      const bool real = r < GROUP;
       uint32_t big = 0u;  // largest magnitude as bits (a NaN's bits exceed infinity's)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -374,8 +402,8 @@ paged_decode_q8_kernel(const KParams p, const Q8Params sp8) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 a = bf16x2_to_float2(w[2 * j]), b = bf16x2_to_float2(w[2 * j + 1]);
-        qa0[j] = pack_half2(a.x * up, a.y * up);
-        qa2[j] = pack_half2(b.x * up, b.y * up);
+        qa0[j] = real ? pack_half2(a.x * up, a.y * up) : 0u;
+        qa2[j] = real ? pack_half2(b.x * up, b.y * up) : 0u;
       }
     }
     float m = -INFINITY, l = 0.f;
@@ -383,6 +411,7 @@ paged_decode_q8_kernel(const KParams p, const Q8Params sp8) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[j] = make_float2(0.f, 0.f);
 
+#pragma unroll 1
     for (int k = 0; k < ntiles; k += 2) {
       const bool two = k + 1 < ntiles;
       const int sa = waited % kStages, sb = (waited + 1) % kStages;
@@ -419,13 +448,9 @@ paged_decode_q8_kernel(const KParams p, const Q8Params sp8) {
       // Every lane's reads of these stages have completed (their values fed the arithmetic
       // above); the warp barrier orders them before the refills.
       __syncwarp();
-      if (two) {
-        waited += 2;
-        issue_two();
-      } else {
-        waited += 1;
-        issue_one();
-      }
+      const int n = two ? 2 : 1;
+      waited += n;
+      issue(n);
     }
     if (!ok) break;
 
@@ -446,7 +471,7 @@ paged_decode_q8_kernel(const KParams p, const Q8Params sp8) {
         dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
       } else {
         const int slot = first_piece ? 0 : 1;
-        float* dst = p.partials + ((gw * 2 + slot) * GROUP + r) * kPartialFloats;
+        float* dst = p.partials + ((static_cast<int64_t>(gw) * 2 + slot) * GROUP + r) * kPartialFloats;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           *reinterpret_cast<float2*>(dst + 16 * q + 2 * j) = make_float2(o[2 * j].x, o[2 * j + 1].x);
