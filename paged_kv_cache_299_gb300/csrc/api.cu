@@ -664,7 +664,7 @@ pa_status pa_prefill_chunk_q8(void* out, const void* q, const int32_t* query_sta
   a.num_seqs = num_seqs;
   a.scale = scale;
   a.status = device_status;
-  return from_cuda(pkv::launch_attend_q8_rows(a, reinterpret_cast<cudaStream_t>(stream)),
+  return from_cuda(pkv::launch_prefill_q8(a, reinterpret_cast<cudaStream_t>(stream)),
                    "prefill_chunk_q8 launch");
 }
 

@@ -80,7 +80,7 @@ struct AttendQ8Args {
   int32_t* status;
 };
 
-cudaError_t launch_attend_q8_rows(const AttendQ8Args& a, cudaStream_t stream);
+cudaError_t launch_prefill_q8(const AttendQ8Args& a, cudaStream_t stream);
 
 // Work decomposition of one pa_decode call (identical in the size query and the call).
 struct DecodePlan {
@@ -142,6 +142,10 @@ cudaError_t launch_decode(const DecodeArgs& a, const DecodePlan& plan, cudaStrea
 // Tensor map of a [rows][64] bf16 array read in boxes of `box_rows` rows with the 128-byte
 // swizzle (the K/V pools, rows = blocks x kv heads x 16); false if the driver call fails.
 bool encode_pool_rows(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows);
+
+// Tensor map of q [tokens][heads][64] in boxes of box_tokens x box_heads rows, 128-byte swizzle.
+bool encode_query_tiles(CUtensorMap* map, const void* base, uint64_t tokens, uint64_t heads,
+                        uint32_t box_heads, uint32_t box_tokens);
 
 struct PrefillArgs {
   void* out;

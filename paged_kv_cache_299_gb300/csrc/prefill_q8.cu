@@ -1,0 +1,825 @@
+// Causal chunk attention over the 8-bit pools, on tcgen05 tensor cores.
+//
+// A sequence appends a chunk of q_len tokens to a context of L tokens (the chunk's own K/V
+// stored already); chunk row i sits at position L - q_len + i and attends keys 0 .. L - q_len
+// + i, K = code * key_scale and V = code * value_scale with one scale per (block, K/V head).
+// For key j of block b, with the value scale written as 2^e f, 1 <= f < 2:
+//   x_j = (scale key_scale_b) q . code_j
+//   p'_j = 2^(log2e x_j + log2 f_b - m)           (m the running maximum of log2e x)
+//   O += sum_j p'_j (2^e_b code_j),   l += sum_b (1 / f_b) sum_{j in b} p'_j,   out = O / l
+// so a block's scales cost no work per element: the score factor replaces the constant one,
+// f rides in the exponent, and 2^e is exact in the bf16 that V becomes on its way anyway.
+// K stays unscaled and becomes f16 (exact, one instruction per two codes); q becomes f16 too,
+// each row under a power of two that brings its largest element to [2^13, 2^14).
+//
+// GB300 design.  The bf16 chunk kernel is held by the chain of issuing and awaiting small MMAs
+// (a 64-key tile of 128 rows at a time), so this one makes the tiles four times as large:
+//   * A work unit is a pair of query tiles, 2 x 128 MMA rows (256 / GROUP tokens x GROUP heads
+//     that share a K/V head), of one sequence; every 128-key K/V tile, converted once, feeds
+//     both.  One CTA per SM, persistent, units dealt heaviest first as in the bf16 kernel.
+//   * Tensor memory (all 512 columns): scores S of each half 128 columns, P of each half 64,
+//     O of each half 64.  P has columns of its own, so the next tile's scores are issued as
+//     soon as the row warps have read this tile's into registers and are ready when they come
+//     back for them; the row warps never wait for the tensor core but at a unit's start.
+//   * Warps 0-3 and 4-7: the row warps of the two halves, one thread per row: read S, mask
+//     the diagonal tiles, maximum, exponentials, P as bf16, row sums in fp32; O is rescaled in
+//     place only when a row's maximum grows by more than 2^8.  At a unit's last tile they turn
+//     the next unit's Q into f16 in shared memory.
+//   * Warps 8-11: converters.  They read a landed tile of codes and write K (f16) and V
+//     (bf16) in the 128-byte-swizzled layout that the MMAs read, into rings of three each.
+//   * Warp 12: one thread issues S = Q K^T (M128 N128 K64) and O += P V (M128 N64 K128).
+//   * Warp 13: one bulk copy per (block, pool) into a ring of three raw tiles, the blocks'
+//     scales beside them by 4-byte asynchronous copies on the same mbarrier; Q by TMA.
+// Every mbarrier wait is bounded; on timeout the CTA records PA_DEVFLAG_TIMEOUT, drains its
+// own copies and MMAs, frees its tensor memory and returns.
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "prefill_plan.cuh"
+#include "q8.cuh"
+#include "tcgen05.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kTileM = 128;                       // MMA rows of one half
+constexpr int kTileN = 128;                       // keys per K/V tile
+constexpr int kBlocksPerTile = kTileN / kBlockSize;
+constexpr int kThreads = 512;
+constexpr int kRowWarps = 4;                      // per half
+constexpr int kConvWarps = 4;
+constexpr int kRing = 3;                          // stages of each of the three rings
+constexpr int kConstRing = 8;                     // tiles whose score constants are kept
+constexpr int kConsts = 3 * kBlocksPerTile;       // key scale, log2 f, 1 / f of every block
+constexpr int kQBytes = kTileM * kRowBytes;       // one half's Q: 16 KiB
+constexpr int kOpBytes = kTileN * kRowBytes;      // one converted K or V tile: 16 KiB
+constexpr int kRawBytes = 2 * kTileN * kQ8RowBytes;  // codes of K, then of V: 16 KiB
+constexpr int kQOff = 0;                          // [2 halves][2 buffers]
+constexpr int kKOff = kQOff + 4 * kQBytes;
+constexpr int kVOff = kKOff + kRing * kOpBytes;
+constexpr int kRawOff = kVOff + kRing * kOpBytes;
+constexpr int kRawScaleOff = kRawOff + kRing * kRawBytes;  // [kRing][2][8] floats
+constexpr int kConstOff = kRawScaleOff + kRing * 2 * kBlocksPerTile * 4;
+constexpr int kBarOff = kConstOff + kConstRing * kConsts * 4;
+constexpr int kNumBars = 4 + 4 + 2 + 6 * kRing + kConstRing + 5 * 2 + 1;
+constexpr int kMiscOff = kBarOff + (kNumBars + 1) / 2 * 16;
+constexpr int kUnitOff = kMiscOff + 128;
+constexpr int kSmemBytes = kUnitOff + 2 * kMaxUnitsPerCta * 4;
+static_assert(kSmemBytes <= 227 * 1024, "one CTA per SM");
+static_assert(sort_scratch_bytes(kThreads) <= kRawOff, "sort scratch fits below the raw ring");
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kSCol = 0;    // + 128 per half: fp32 scores
+constexpr uint32_t kPCol = 256;  // + 64 per half: bf16 pairs
+constexpr uint32_t kOCol = 384;  // + 64 per half: fp32
+constexpr float kRescaleThreshold = 8.0f;
+constexpr int kQExp = 13;  // exponent of a row's largest f16 query element
+// Register split (setmaxnreg): the row warps' 256 threads and the others' 256 share what the
+// CTA was launched with; the launcher checks that it suffices.
+constexpr int kRowRegs = 176;
+constexpr int kOtherRegs = 80;
+
+struct Pools {
+  const uint8_t* key;
+  const uint8_t* value;
+  const float* key_scale;
+  const float* value_scale;
+};
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_addr(dst)),
+      "l"(src), "r"(bytes), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void async_copy4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+// One arrival on `bar` (counted in its initial count) when this thread's asynchronous copies
+// so far have landed.
+__device__ __forceinline__ void async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// A shared-memory float, read where it is used (not held in a register from before).
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+
+// Instruction descriptor, kind::f16 with f16 A/B (both K-major) and fp32 accumulation.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n) {
+  return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// The tiles of K/V each half of a unit needs (the second half may have no tokens).
+template <int HALF_TOKENS>
+__device__ __forceinline__ int half_tiles(const Unit& u, int half) {
+  const int n = min(HALF_TOKENS, u.ntok - half * HALF_TOKENS);
+  if (n <= 0) return 0;
+  return (u.L - u.q_len + u.tok0 + half * HALF_TOKENS + n + kTileN - 1) / kTileN;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf2(float x, float y) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t mul_bf2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Four codes of a word as bf16 pairs times 2^-120 (exact): the code's exponent and
+// significand bits, three places down from the bf16's, under its sign.
+__device__ __forceinline__ void codes4_to_bf2x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);
+  lo = (a & 0x80008000u) | ((a >> 4) & 0x07f007f0u);
+  hi = (b & 0x80008000u) | ((b >> 4) & 0x07f007f0u);
+}
+
+// 2^e as a bf16 pair, -126 <= e <= 127.
+__device__ __forceinline__ uint32_t bf2_power(int e) {
+  return static_cast<uint32_t>(e + 127) * 0x00800080u;
+}
+
+// Chunk c (16 bytes) of row r in the 128-byte-swizzled layout of 128-byte rows.
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+  return static_cast<uint32_t>(r * kRowBytes + ((c ^ (r & 7)) << 4));
+}
+
+template <int GROUP>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams p, const Pools pools) {
+  constexpr int kHalfTokens = kTileM / GROUP;
+  constexpr int kUnitTokens = 2 * kHalfTokens;
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+  extern __shared__ __align__(1024) uint8_t smem[];  // 128-byte swizzle atoms need 1 KiB
+  if ((smem_addr(smem) & 1023u) != 0) {
+    if (tid == 0) flag_error(p.status, PA_DEVFLAG_LAYOUT);
+    return;
+  }
+  uint8_t* sq = smem + kQOff;
+  uint8_t* sk = smem + kKOff;
+  uint8_t* sv = smem + kVOff;
+  uint8_t* sraw = smem + kRawOff;
+  float* raw_scale = reinterpret_cast<float*>(smem + kRawScaleOff);
+  float* consts = reinterpret_cast<float*>(smem + kConstOff);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBarOff);
+  // A half that has no rows in a unit takes no part in it: Q buffers and phases count the units
+  // of each half by themselves.
+  uint64_t* q_full = bars;                   // [half][2] Q (bf16) landed in a buffer
+  uint64_t* q_empty = q_full + 4;            // [half][2] the last scores that read it are done
+  uint64_t* q_ready = q_empty + 4;           // [half] the half's next Q is f16
+  uint64_t* raw_full = q_ready + 2;          // [kRing] codes and scales landed
+  uint64_t* raw_empty = raw_full + kRing;    // [kRing] and were read
+  uint64_t* k_full = raw_empty + kRing;      // [kRing] K converted
+  uint64_t* k_empty = k_full + kRing;        // [kRing] scores that read it done
+  uint64_t* v_full = k_empty + kRing;
+  uint64_t* v_empty = v_full + kRing;
+  uint64_t* c_full = v_empty + kRing;        // [kConstRing] the tile's score constants
+  uint64_t* s_full = c_full + kConstRing;    // [half] scores in tensor memory
+  uint64_t* s_free = s_full + 2;             // [half] scores read into registers
+  uint64_t* p_full = s_free + 2;             // [half] P in tensor memory
+  uint64_t* pv_done = p_full + 2;            // [half] P V done: P free, O up to date
+  uint64_t* o_free = pv_done + 2;            // [half] O of a finished unit read out
+  uint64_t* drain = o_free + 2;
+  int* misc = reinterpret_cast<int*>(smem + kMiscOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
+  volatile int& abort_flag = *reinterpret_cast<volatile int*>(misc + 1);
+  int* n_units_s = misc + 2;
+  int* red = misc + 4;  // 24 ints of scan scratch
+  int32_t* unit_s = reinterpret_cast<int32_t*>(smem + kUnitOff);
+  int32_t* unit_tg = unit_s + kMaxUnitsPerCta;
+
+  if (tid == 0) {
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&q_ready[b], kRowWarps);
+      mbar_init(&s_full[b], 1);
+      mbar_init(&s_free[b], kRowWarps);
+      mbar_init(&p_full[b], kRowWarps);
+      mbar_init(&pv_done[b], 1);
+      mbar_init(&o_free[b], kRowWarps);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&raw_full[i], 1 + kBlocksPerTile);
+      mbar_init(&raw_empty[i], kConvWarps);
+      mbar_init(&k_full[i], kConvWarps);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], kConvWarps);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < kConstRing; ++i) mbar_init(&c_full[i], kConvWarps);
+    mbar_init(drain, 1);
+    fence_barrier_init();
+    abort_flag = 0;
+  }
+  if (warp == 12) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 13 && lane == 0) prefetch_tensormap(&tmap_q);
+  const int n_units = plan_units<kUnitTokens, kTileN, kThreads>(p, smem, red, unit_s, unit_tg);
+  if (tid == 0) *n_units_s = n_units;
+  fence_proxy_async_smem();  // the plan's scratch before copies and MMAs touch the buffers
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  Schedule sc;
+  sc.unit_s = unit_s;
+  sc.unit_tg = unit_tg;
+  sc.n_units = *n_units_s;
+
+  if (warp < 8) {
+    // ============================ row warps ============================
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
+    const int half = warp >> 2;
+    const int r = tid & 127;  // row of the half == TMEM lane
+    const int tt = r / GROUP, hh = r % GROUP;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t s_addr = lane_addr + kSCol + half * kTileN;
+    const uint32_t p_addr = lane_addr + kPCol + half * (kTileN / 2);
+    const uint32_t o_addr = lane_addr + kOCol + half * kHeadDim;
+    int k = 0;
+    int qc = 0;          // Qs this half has turned into f16
+    bool have_q = false;  // the coming unit's among them
+    float q_factor = 0.f, q_factor_next = 0.f;  // score factor of this row
+    // Turn this row of the half's next Q into f16, in place, under the row's power of two.
+    auto convert_q = [&]() -> bool {
+      const int b = 2 * half + (qc & 1);
+      bool ok = wait_or_abort(&q_full[b], static_cast<uint32_t>((qc >> 1) & 1), &abort_flag, p.status);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      uint8_t* q = sq + b * kQBytes;
+      uint4 w[8];
+      uint32_t big = 0u;  // largest magnitude as bits
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        w[c] = lds128(q + swz(r, c));
+        const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          big = max(big, max((x[i] << 16) & 0x7fff0000u, x[i] & 0x7fff0000u));
+      }
+      int shift = 0;
+      if (big != 0u && big < 0x7f800000u)
+        shift = min(126, kQExp + 127 - static_cast<int>(max(big >> 23, 1u)));
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+      q_factor_next = p.qk_scale * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+        uint32_t y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = bf16x2_to_float2(x[i]);
+          y[i] = pack_half2(f.x * up, f.y * up);
+        }
+        *reinterpret_cast<uint4*>(q + swz(r, c)) = make_uint4(y[0], y[1], y[2], y[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_ready[half]);
+      ++qc;
+      have_q = true;
+      return true;
+    };
+    bool ok = true;
+    int jt = 0;  // K/V tiles of the CTA before this unit
+    int c = 0;   // tiles of this half so far
+    while (ok) {
+      // of a unit, only what a row needs stays in registers
+      int n_mine, n_kv, pos, pos_lo;
+      bool row_ok, next_mine;
+      __nv_bfloat16* dst;
+      {
+        Unit u;
+        if (!next_unit<kUnitTokens, kTileN>(p, sc, k, u)) break;
+        n_mine = half_tiles<kHalfTokens>(u, half);
+        n_kv = u.n_kv;
+        const int token = u.tok0 + half * kHalfTokens + tt;
+        row_ok = token < u.q_len;
+        pos = u.L - u.q_len + min(token, u.q_len - 1);
+        pos_lo = u.L - u.q_len + u.tok0 + half * kHalfTokens;
+        dst = p.out + (static_cast<int64_t>(u.q0 + token) * p.num_q_heads + u.g * GROUP + hh) * kHeadDim;
+        int peek = k;
+        next_mine = next_unit<kUnitTokens, kTileN>(p, sc, peek, u) && half_tiles<kHalfTokens>(u, half) > 0;
+      }
+      if (n_mine > 0) {
+        if (!have_q && !(ok = convert_q())) break;
+        have_q = false;
+        q_factor = q_factor_next;
+        float m = -INFINITY, l = 0.f;
+        for (int j = 0; j < n_mine; ++j, ++c) {
+          ok = wait_or_abort(&s_full[half], static_cast<uint32_t>(c & 1), &abort_flag, p.status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          tc_fence_after_sync();
+          // The next unit's Q, before its first scores are wanted.  Only now: these scores
+          // show that the issuing thread has seen this unit's Q, so q_ready can complete a
+          // phase again.
+          if (j == n_mine - 1 && next_mine && !(ok = convert_q())) break;
+          uint32_t v[4][32];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32(s_addr + 32 * i, v[i]);
+          tmem_wait_ld();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_free[half]);
+          const int kb = j * kTileN;
+          if (kb + kTileN - 1 > pos_lo) {
+            // a tile on the causal diagonal: hide keys past each row's position
+#pragma unroll
+            for (int i = 0; i < kTileN; ++i)
+              if (kb + i > pos) v[i >> 5][i & 31] = __float_as_uint(-INFINITY);
+          }
+          const int slot = (jt + j) % kConstRing;
+          ok = wait_or_abort(&c_full[slot], static_cast<uint32_t>(((jt + j) / kConstRing) & 1),
+                             &abort_flag, p.status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          const uint32_t cs = smem_addr(consts + slot * kConsts);
+          float mt = -INFINITY;
+#pragma unroll
+          for (int b = 0; b < kBlocksPerTile; ++b) {
+            const uint32_t* x = &v[b >> 1][16 * (b & 1)];
+            float a0 = __uint_as_float(x[0]), a1 = __uint_as_float(x[1]);
+#pragma unroll
+            for (int i = 2; i < 14; i += 4) {
+              a0 = max3f(a0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+              a1 = max3f(a1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+            }
+            a0 = max3f(a0, __uint_as_float(x[14]), __uint_as_float(x[15]));
+            mt = fmaxf(mt, fmaxf(a0, a1) * (lds_f32(cs + 4 * b) * q_factor));
+          }
+          const float m_new = fmaxf(m, mt);
+          const bool grow = m_new - m > kRescaleThreshold;  // true on the first tile
+          float alpha = 1.f;
+          if (grow) {
+            alpha = fast_exp2(m - m_new);
+            m = m_new;
+          }
+          l *= alpha;
+          // p' two at a time, packed to bf16 over the scores
+#pragma unroll
+          for (int b = 0; b < kBlocksPerTile; ++b) {
+            const float f = lds_f32(cs + 4 * b) * q_factor;
+            const float nb = lds_f32(cs + 4 * (kBlocksPerTile + b)) - m;
+            const float2 fb = make_float2(f, f);
+            const float2 nb2 = make_float2(nb, nb);
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kBlockSize / 2; ++i) {
+              const int e = b * kBlockSize + 2 * i;
+              const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[e >> 5][e & 31]),
+                                                      __uint_as_float(v[e >> 5][(e & 31) + 1])),
+                                          fb, nb2);
+              const float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+              sum = __fadd2_rn(sum, y);
+              v[e >> 6][(e >> 1) & 31] = pack_bf2(y.x, y.y);
+            }
+            l += (sum.x + sum.y) * lds_f32(cs + 4 * (2 * kBlocksPerTile + b));
+          }
+          if (c > 0) {  // the previous P V: P's columns are free and O is up to date
+            ok = wait_or_abort(&pv_done[half], static_cast<uint32_t>((c - 1) & 1), &abort_flag,
+                               p.status);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            tc_fence_after_sync();
+          }
+          tmem_st32(p_addr, v[0]);
+          tmem_st32(p_addr + 32, v[1]);
+          if (j > 0 && __any_sync(0xffffffffu, grow)) {
+            const float2 a2 = make_float2(alpha, alpha);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t(&o)[32] = v[2 + h];
+              tmem_ld32(o_addr + 32 * h, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float2 x = __fmul2_rn(
+                    make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), a2);
+                o[2 * i] = __float_as_uint(x.x);
+                o[2 * i + 1] = __float_as_uint(x.y);
+              }
+              tmem_st32(o_addr + 32 * h, o);
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[half]);
+        }
+        if (!ok) break;
+        // ---- epilogue ----
+        ok = wait_or_abort(&pv_done[half], static_cast<uint32_t>((c - 1) & 1), &abort_flag, p.status);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_after_sync();
+        uint32_t o[2][32];
+        tmem_ld32(o_addr, o[0]);
+        tmem_ld32(o_addr + 32, o[1]);
+        tmem_wait_ld();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_free[half]);
+        const float inv = 1.f / l;
+        if (row_ok) {
+#pragma unroll
+          for (int q8 = 0; q8 < 8; ++q8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int i = q8 * 8 + 2 * e;
+              w[e] = pack_bf2(__uint_as_float(o[i >> 5][i & 31]) * inv,
+                              __uint_as_float(o[i >> 5][(i & 31) + 1]) * inv);
+            }
+            *reinterpret_cast<uint4*>(dst + 8 * q8) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      jt += n_kv;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp < 12) {
+      // ============================ converters ============================
+      const int cw = warp - 8;  // keys 32 cw .. 32 cw + 31 of every tile, blocks 2 cw and 2 cw + 1
+      int k = 0, jt = 0;
+      Unit cur;
+      bool ok = true;
+      while (ok && next_unit<kUnitTokens, kTileN>(p, sc, k, cur)) {
+        for (int j = 0; j < cur.n_kv; ++j, ++jt) {
+          const int st = jt % kRing;
+          const uint32_t ph = static_cast<uint32_t>((jt / kRing) & 1);
+          ok = wait_or_abort(&raw_full[st], ph, &abort_flag, p.status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          const uint8_t* raw = sraw + st * kRawBytes + cw * 32 * kQ8RowBytes + 16 * lane;
+          // score constants of this warp's two blocks
+          const int slot = jt % kConstRing;
+          const float* rs = raw_scale + st * 2 * kBlocksPerTile;
+          int e[2];  // exponents of the value scales; -1000: a scale of zero
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const int blk = 2 * cw + b;
+            const bool needed = j * kBlocksPerTile + blk < cur.blocks_needed;
+            const float ks = needed ? fmaxf(rs[blk], 1.17549435e-38f) : 1.f;
+            const float vs = needed ? rs[kBlocksPerTile + blk] : 1.f;
+            const uint32_t bits = __float_as_uint(vs);
+            e[b] = static_cast<int>((bits >> 23) & 0xffu) - 127;
+            float f = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+            if (e[b] == -127) {  // zero (or too small to matter)
+              e[b] = -1000;
+              f = 1.f;
+            }
+            if (lane == 0) {
+              float* cs = consts + slot * kConsts;
+              cs[blk] = ks;
+              cs[kBlocksPerTile + blk] = f == 1.f ? 0.f : __log2f(f);
+              cs[2 * kBlocksPerTile + blk] = 1.f / f;
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c_full[slot]);
+          // K: f16
+          ok = wait_or_abort(&k_empty[st], ph ^ 1u, &abort_flag, p.status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          uint8_t* dst = sk + st * kOpBytes;
+          const int row0 = cw * 32 + (lane >> 2);
+          const int c0 = 2 * (lane & 3);  // 16 codes of a row: two 16-byte chunks
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 w = lds128(raw + i * 512);
+            uint4 a, b;
+            codes4_to_half2x2(w.x, a.x, a.y);
+            codes4_to_half2x2(w.y, a.z, a.w);
+            codes4_to_half2x2(w.z, b.x, b.y);
+            codes4_to_half2x2(w.w, b.z, b.w);
+            *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * i, c0)) = a;
+            *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * i, c0 + 1)) = b;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&k_full[st]);
+          // V: bf16 times 2^e
+          ok = wait_or_abort(&v_empty[st], ph ^ 1u, &abort_flag, p.status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          dst = sv + st * kOpBytes;
+          raw += kTileN * kQ8RowBytes;
+          const int keys_left = cur.keys - j * kTileN;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint4 w = lds128(raw + i * 512);
+            const int eb = e[i >> 1];
+            // keys past the last needed one weigh nothing, but may hold anything
+            if (row0 + 8 * i >= keys_left || eb == -1000) w = make_uint4(0u, 0u, 0u, 0u);
+            uint4 a, b;
+            codes4_to_bf2x2(w.x, a.x, a.y);
+            codes4_to_bf2x2(w.y, a.z, a.w);
+            codes4_to_bf2x2(w.z, b.x, b.y);
+            codes4_to_bf2x2(w.w, b.z, b.w);
+            // 2^(120 + e) in one factor where it is a bf16, else in two
+            const uint32_t m0 = bf2_power(eb <= 7 ? max(120 + eb, -126) : 120);
+            a.x = mul_bf2(a.x, m0); a.y = mul_bf2(a.y, m0); a.z = mul_bf2(a.z, m0); a.w = mul_bf2(a.w, m0);
+            b.x = mul_bf2(b.x, m0); b.y = mul_bf2(b.y, m0); b.z = mul_bf2(b.z, m0); b.w = mul_bf2(b.w, m0);
+            if (eb > 7) {
+              const uint32_t m1 = bf2_power(min(eb, 127));
+              a.x = mul_bf2(a.x, m1); a.y = mul_bf2(a.y, m1); a.z = mul_bf2(a.z, m1); a.w = mul_bf2(a.w, m1);
+              b.x = mul_bf2(b.x, m1); b.y = mul_bf2(b.y, m1); b.z = mul_bf2(b.z, m1); b.w = mul_bf2(b.w, m1);
+            }
+            *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * i, c0)) = a;
+            *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * i, c0 + 1)) = b;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&v_full[st]);
+            mbar_arrive(&raw_empty[st]);
+          }
+        }
+      }
+    } else if (warp == 12) {
+      // ============================ MMA issuer ============================
+      if (lane == 0) {
+        constexpr uint32_t kIdescS = idesc_f16_f32(kTileM, kTileN);
+        constexpr uint32_t kIdescO = idesc_bf16_f32(kTileM, kHeadDim, true);
+        int s_issued[2] = {0, 0}, pv_issued[2] = {0, 0}, q_used[2] = {0, 0}, o_used[2] = {0, 0};
+        // scores of a unit's tile j (the CTA's tile jt), for the halves that need it
+        auto issue_s = [&](int n0, int n1, int j, int jt) -> bool {
+          const int st = jt % kRing;
+          if (!wait_or_abort(&k_full[st], static_cast<uint32_t>((jt / kRing) & 1), &abort_flag, p.status))
+            return false;
+          const uint64_t k_desc = sw128_desc(smem_addr(sk + st * kOpBytes), 16, 1024);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (j >= (h ? n1 : n0)) continue;
+            if (j == 0) {
+              if (!wait_or_abort(&q_ready[h], static_cast<uint32_t>(q_used[h] & 1), &abort_flag, p.status))
+                return false;
+              ++q_used[h];
+            }
+            if (s_issued[h] > 0 &&
+                !wait_or_abort(&s_free[h], static_cast<uint32_t>((s_issued[h] - 1) & 1), &abort_flag,
+                               p.status))
+              return false;
+            tc_fence_after_sync();
+            const int qb = 2 * h + ((q_used[h] - 1) & 1);
+            const uint64_t q_desc = sw128_desc(smem_addr(sq + qb * kQBytes), 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < kHeadDim / 16; ++kk)
+              umma_bf16(tmem + kSCol + h * kTileN, q_desc + 2 * kk, k_desc + 2 * kk, kIdescS,
+                        kk > 0 ? 1u : 0u);
+            umma_commit(&s_full[h]);
+            ++s_issued[h];
+            if (j == (h ? n1 : n0) - 1) umma_commit(&q_empty[qb]);
+          }
+          umma_commit(&k_empty[st]);
+          return true;
+        };
+        auto issue_pv = [&](int n0, int n1, int j, int jt) -> bool {
+          const int st = jt % kRing;
+          if (!wait_or_abort(&v_full[st], static_cast<uint32_t>((jt / kRing) & 1), &abort_flag, p.status))
+            return false;
+          const uint64_t v_desc = sw128_desc(smem_addr(sv + st * kOpBytes), 16, 1024);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (j >= (h ? n1 : n0)) continue;
+            if (!wait_or_abort(&p_full[h], static_cast<uint32_t>(pv_issued[h] & 1), &abort_flag, p.status))
+              return false;
+            if (j == 0) {  // O starts anew: the half's previous unit has been read out
+              if (o_used[h] > 0 &&
+                  !wait_or_abort(&o_free[h], static_cast<uint32_t>((o_used[h] - 1) & 1), &abort_flag,
+                                 p.status))
+                return false;
+              ++o_used[h];
+            }
+            tc_fence_after_sync();
+#pragma unroll
+            for (int kk = 0; kk < kTileN / 16; ++kk)  // 16 keys: 2 KiB of V, 8 columns of P
+              umma_bf16_ts(tmem + kOCol + h * kHeadDim, tmem + kPCol + h * (kTileN / 2) + kk * 8,
+                           v_desc + 128 * kk, kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
+            umma_commit(&pv_done[h]);
+            ++pv_issued[h];
+          }
+          umma_commit(&v_empty[st]);
+          return true;
+        };
+        int k = 0, jt = 0;
+        Unit cur, nxt;
+        bool have = next_unit<kUnitTokens, kTileN>(p, sc, k, cur);
+        bool have_next = have && next_unit<kUnitTokens, kTileN>(p, sc, k, nxt);
+        int n0 = 0, n1 = 0;
+        bool ok = have;
+        if (have) {
+          n0 = half_tiles<kHalfTokens>(cur, 0);
+          n1 = half_tiles<kHalfTokens>(cur, 1);
+          ok = issue_s(n0, n1, 0, 0);
+        }
+        while (ok && have) {
+          int m0 = 0, m1 = 0;
+          if (have_next) {
+            m0 = half_tiles<kHalfTokens>(nxt, 0);
+            m1 = half_tiles<kHalfTokens>(nxt, 1);
+          }
+          for (int j = 0; ok && j < cur.n_kv; ++j, ++jt) {
+            if (j + 1 < cur.n_kv)
+              ok = issue_s(n0, n1, j + 1, jt + 1);
+            else if (have_next)
+              ok = issue_s(m0, m1, 0, jt + 1);
+            if (ok) ok = issue_pv(n0, n1, j, jt);
+          }
+          cur = nxt;
+          n0 = m0;
+          n1 = m1;
+          have = have_next;
+          if (have) have_next = next_unit<kUnitTokens, kTileN>(p, sc, k, nxt);
+        }
+        // wait (bounded) until every MMA issued above has completed
+        umma_commit(drain);
+        if (!mbar_wait(drain, 0)) flag_error(p.status, PA_DEVFLAG_TIMEOUT);
+      }
+    } else if (warp == 13) {
+      // ============================ producer ============================
+      int k = 0;
+      Unit cur, nxt;
+      bool have = next_unit<kUnitTokens, kTileN>(p, sc, k, cur);
+      bool have_next = have && next_unit<kUnitTokens, kTileN>(p, sc, k, nxt);
+      int nq[2] = {0, 0};  // Qs requested for each half
+      auto load_q = [&](const Unit& u) {
+        bool ok = true;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (half_tiles<kHalfTokens>(u, h) == 0) continue;
+          const int b = 2 * h + (nq[h] & 1);
+          if (lane == 0 && ok) {
+            if (nq[h] >= 2)
+              ok = wait_or_abort(&q_empty[b], static_cast<uint32_t>(((nq[h] - 2) >> 1) & 1),
+                                 &abort_flag, p.status);
+            if (ok) {
+              mbar_arrive_expect_tx(&q_full[b], kQBytes);
+              tma_load_3d(sq + b * kQBytes, &tmap_q, 0, u.g * GROUP, u.q0 + u.tok0 + h * kHalfTokens,
+                          &q_full[b]);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (ok) ++nq[h];
+        }
+        return ok;
+      };
+      bool ok = !have || load_q(cur);
+      int jt = 0;
+      while (ok && have) {
+        const int32_t* row = p.block_tables + static_cast<int64_t>(cur.s) * p.max_blocks_per_seq;
+        // 32 table entries (four tiles) at a time, one per lane, the next window in flight
+        auto fetch = [&](int base) -> int32_t {
+          return base + lane < cur.blocks_needed ? __ldg(row + base + lane) : 0;
+        };
+        int win_base = 0;
+        int32_t win = fetch(0);
+        int32_t win_next = fetch(32);
+        for (int j = 0; j < cur.n_kv; ++j, ++jt) {
+          // the next unit's Q, once this unit's pipeline is under way
+          if (have_next && j == min(1, cur.n_kv - 1) && !(ok = load_q(nxt))) break;
+          const int st = jt % kRing;
+          const int lb0 = j * kBlocksPerTile;
+          if (lb0 >= win_base + 32) {
+            win_base += 32;
+            win = win_next;
+            win_next = fetch(win_base + 32);
+          }
+          const int lb = lb0 + lane;
+          const bool need = lane < kBlocksPerTile && lb < cur.blocks_needed;
+          const int32_t entry =
+              __shfl_sync(0xffffffffu, win, (lb0 - win_base) + (lane & (kBlocksPerTile - 1)));
+          const bool bad = need && (entry < 0 || entry >= p.num_blocks);
+          const bool load = need && !bad;
+          const unsigned mask = __ballot_sync(0xffffffffu, load);
+          if (__any_sync(0xffffffffu, bad) && lane == 0) flag_error(p.status, PA_DEVFLAG_BAD_BLOCK);
+          int go = 1;
+          if (lane == 0) {
+            go = wait_or_abort(&raw_empty[st], static_cast<uint32_t>((jt / kRing) & 1) ^ 1u, &abort_flag,
+                               p.status);
+            if (go) mbar_arrive_expect_tx(&raw_full[st], __popc(mask) * 2u * kQ8TileBytes);
+          }
+          go = __shfl_sync(0xffffffffu, go, 0);
+          if (!go) {
+            ok = false;
+            break;
+          }
+          if (lane < kBlocksPerTile) {
+            if (load) {
+              const int64_t tile = static_cast<int64_t>(entry) * p.num_kv_heads + cur.g;
+              uint8_t* dst = sraw + st * kRawBytes + lane * kQ8TileBytes;
+              bulk_load(dst, pools.key + tile * kQ8TileBytes, kQ8TileBytes, &raw_full[st]);
+              bulk_load(dst + kTileN * kQ8RowBytes, pools.value + tile * kQ8TileBytes, kQ8TileBytes,
+                        &raw_full[st]);
+              float* s = raw_scale + st * 2 * kBlocksPerTile + lane;
+              async_copy4(s, pools.key_scale + tile);
+              async_copy4(s + kBlocksPerTile, pools.value_scale + tile);
+            }
+            async_arrive(&raw_full[st]);
+          }
+        }
+        cur = nxt;
+        have = have_next;
+        if (have) have_next = next_unit<kUnitTokens, kTileN>(p, sc, k, nxt);
+      }
+      // leave no copy in flight: wait (bounded) for the last Q of each buffer and the last
+      // fill of each stage
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (lane == 0) {
+        for (int h = 0; h < 2; ++h) {
+          for (int b = 0; b < 2 && b < nq[h]; ++b) {
+            const int last = b + ((nq[h] - 1 - b) / 2) * 2;
+            if (!mbar_wait(&q_full[2 * h + b], static_cast<uint32_t>((last >> 1) & 1)))
+              flag_error(p.status, PA_DEVFLAG_TIMEOUT);
+          }
+        }
+        for (int st = 0; st < kRing && st < jt; ++st) {
+          const int last = st + ((jt - 1 - st) / kRing) * kRing;
+          if (!mbar_wait(&raw_full[st], static_cast<uint32_t>((last / kRing) & 1)))
+            flag_error(p.status, PA_DEVFLAG_TIMEOUT);
+        }
+      }
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 12) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int GROUP>
+cudaError_t launch(const AttendQ8Args& a, cudaStream_t stream) {
+  static bool ready = false;  // benign race: the calls are idempotent
+  cudaError_t e;
+  if (!ready) {
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, paged_chunk_q8_kernel<GROUP>);
+    if (e != cudaSuccess) return e;
+    // setmaxnreg waits for registers the launch never had: refuse instead
+    if (attr.numRegs * kThreads < (kThreads / 2) * (kRowRegs + kOtherRegs))
+      return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(paged_chunk_q8_kernel<GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmemBytes);
+    if (e != cudaSuccess) return e;
+    ready = true;
+  }
+  CUtensorMap tq;
+  if (!encode_query_tiles(&tq, a.q, static_cast<uint64_t>(a.num_query_tokens), a.num_q_heads, GROUP,
+                          kTileM / GROUP))
+    return cudaErrorInvalidValue;
+  PParams p = {};
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.query_start_loc = a.query_start_loc;
+  p.block_tables = a.block_tables;
+  p.max_blocks_per_seq = a.max_blocks_per_seq;
+  p.context_lens = a.context_lens;
+  p.num_blocks = a.num_blocks;
+  p.num_kv_heads = a.num_kv_heads;
+  p.num_q_heads = a.num_q_heads;
+  p.qk_scale = a.scale * 1.4426950408889634f;
+  p.status = a.status;
+  p.num_query_tokens = a.num_query_tokens;
+  p.num_seqs = a.num_seqs;
+  constexpr int kUnitTokens = 2 * kTileM / GROUP;
+  p.q_tiles = (a.max_query_len + kUnitTokens - 1) / kUnitTokens;
+  p.skip_single = 0;
+  const Pools pools = {static_cast<const uint8_t*>(a.key_cache), static_cast<const uint8_t*>(a.value_cache),
+                       a.key_scale, a.value_scale};
+  int dev = 0, sms = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * p.q_tiles;
+  const int64_t grid = units < sms ? units : sms;
+  if (grid < 1) return cudaSuccess;
+  paged_chunk_q8_kernel<GROUP><<<static_cast<unsigned>(grid), kThreads, kSmemBytes, stream>>>(tq, p, pools);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_q8(const AttendQ8Args& a, cudaStream_t stream) {
+  switch (a.num_q_heads / a.num_kv_heads) {
+    case 1: return launch<1>(a, stream);
+    case 2: return launch<2>(a, stream);
+    case 4: return launch<4>(a, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace pkv

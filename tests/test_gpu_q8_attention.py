@@ -221,6 +221,15 @@ def test_chunk_long():
     check_chunk(w, 1, 4)
 
 
+@pytest.mark.parametrize("hq,hkv", [(32, 8), (2, 2)])
+def test_chunk_many_units_per_cta(hq, hkv):
+    """Several units per CTA, of one K/V tile and of several, with one query tile and with two."""
+    rng = np.random.default_rng(hq)
+    new = np.where(rng.random(200) < 0.7, rng.integers(1, 9, size=200), rng.integers(20, 150, size=200))
+    w = wl.make_workload("units", rng.integers(0, 400, size=200), new, num_prefill=200, seed=hq)
+    check_chunk(w, hkv, hq)
+
+
 def test_chunk_many_short_ones():
     """More (sequence, tile) pairs than the kernel sorts: units in grid order."""
     new = np.random.default_rng(2).integers(1, 4, size=2200)
