@@ -103,6 +103,15 @@ __device__ __forceinline__ void async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
+// True in one lane of a converged warp (the same one on every call of the kernel).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
+
 // A shared-memory float, read where it is used (not held in a register from before).
 __device__ __forceinline__ float lds_f32(uint32_t addr) {
   float v;
@@ -550,104 +559,125 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
       }
     } else if (warp == 12) {
       // ============================ MMA issuer ============================
-      if (lane == 0) {
-        constexpr uint32_t kIdescS = idesc_f16_f32(kTileM, kTileN);
-        constexpr uint32_t kIdescO = idesc_bf16_f32(kTileM, kHeadDim, true);
-        int s_issued[2] = {0, 0}, pv_issued[2] = {0, 0}, q_used[2] = {0, 0}, o_used[2] = {0, 0};
-        // scores of a unit's tile j (the CTA's tile jt), for the halves that need it
-        auto issue_s = [&](int n0, int n1, int j, int jt) -> bool {
-          const int st = jt % kRing;
-          if (!wait_or_abort(&k_full[st], static_cast<uint32_t>((jt / kRing) & 1), &abort_flag, p.status))
-            return false;
-          const uint64_t k_desc = sw128_desc(smem_addr(sk + st * kOpBytes), 16, 1024);
+      // The whole warp walks the tiles, so that barriers, counters and descriptors stay
+      // warp-uniform (uniform registers feed the MMAs); one elected lane issues.
+      constexpr uint32_t kIdescS = idesc_f16_f32(kTileM, kTileN);
+      constexpr uint32_t kIdescO = idesc_bf16_f32(kTileM, kHeadDim, true);
+      const bool leader = elect_one();
+      const uint64_t q_desc0 = sw128_desc(smem_addr(sq), 16, 1024);
+      const uint64_t k_desc0 = sw128_desc(smem_addr(sk), 16, 1024);
+      const uint64_t v_desc0 = sw128_desc(smem_addr(sv), 16, 1024);
+      constexpr uint64_t kStageStep = kOpBytes >> 4;  // of a descriptor's start address
+      constexpr uint64_t kQStep = kQBytes >> 4;
+      int s_issued[2] = {0, 0}, pv_issued[2] = {0, 0}, q_used[2] = {0, 0}, o_used[2] = {0, 0};
+      int ks = 0, vs = 0;            // ring stages of the next K and V tile
+      uint32_t kph = 0, vph = 0;     // and their phases
+      // scores of a unit's tile j, for the halves that need it
+      auto issue_s = [&](int n0, int n1, int j) -> bool {
+        if (!wait_or_abort(&k_full[ks], kph, &abort_flag, p.status)) return false;
+        const uint64_t k_desc = k_desc0 + kStageStep * ks;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (j >= (h ? n1 : n0)) continue;
-            if (j == 0) {
-              if (!wait_or_abort(&q_ready[h], static_cast<uint32_t>(q_used[h] & 1), &abort_flag, p.status))
-                return false;
-              ++q_used[h];
-            }
-            if (s_issued[h] > 0 &&
-                !wait_or_abort(&s_free[h], static_cast<uint32_t>((s_issued[h] - 1) & 1), &abort_flag,
-                               p.status))
+        for (int h = 0; h < 2; ++h) {
+          const int n = h ? n1 : n0;
+          if (j >= n) continue;
+          if (j == 0) {
+            if (!wait_or_abort(&q_ready[h], static_cast<uint32_t>(q_used[h] & 1), &abort_flag, p.status))
               return false;
-            tc_fence_after_sync();
-            const int qb = 2 * h + ((q_used[h] - 1) & 1);
-            const uint64_t q_desc = sw128_desc(smem_addr(sq + qb * kQBytes), 16, 1024);
+            ++q_used[h];
+          }
+          if (s_issued[h] > 0 &&
+              !wait_or_abort(&s_free[h], static_cast<uint32_t>((s_issued[h] - 1) & 1), &abort_flag,
+                             p.status))
+            return false;
+          tc_fence_after_sync();
+          const int qb = 2 * h + ((q_used[h] - 1) & 1);
+          const uint64_t q_desc = q_desc0 + kQStep * qb;
+          if (leader) {
 #pragma unroll
             for (int kk = 0; kk < kHeadDim / 16; ++kk)
               umma_bf16(tmem + kSCol + h * kTileN, q_desc + 2 * kk, k_desc + 2 * kk, kIdescS,
                         kk > 0 ? 1u : 0u);
             umma_commit(&s_full[h]);
-            ++s_issued[h];
-            if (j == (h ? n1 : n0) - 1) umma_commit(&q_empty[qb]);
+            if (j == n - 1) umma_commit(&q_empty[qb]);
           }
-          umma_commit(&k_empty[st]);
-          return true;
-        };
-        auto issue_pv = [&](int n0, int n1, int j, int jt) -> bool {
-          const int st = jt % kRing;
-          if (!wait_or_abort(&v_full[st], static_cast<uint32_t>((jt / kRing) & 1), &abort_flag, p.status))
+          ++s_issued[h];
+        }
+        if (leader) umma_commit(&k_empty[ks]);
+        if (++ks == kRing) {
+          ks = 0;
+          kph ^= 1u;
+        }
+        return true;
+      };
+      auto issue_pv = [&](int n0, int n1, int j) -> bool {
+        if (!wait_or_abort(&v_full[vs], vph, &abort_flag, p.status)) return false;
+        const uint64_t v_desc = v_desc0 + kStageStep * vs;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (j >= (h ? n1 : n0)) continue;
+          if (!wait_or_abort(&p_full[h], static_cast<uint32_t>(pv_issued[h] & 1), &abort_flag, p.status))
             return false;
-          const uint64_t v_desc = sw128_desc(smem_addr(sv + st * kOpBytes), 16, 1024);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (j >= (h ? n1 : n0)) continue;
-            if (!wait_or_abort(&p_full[h], static_cast<uint32_t>(pv_issued[h] & 1), &abort_flag, p.status))
+          if (j == 0) {  // O starts anew: the half's previous unit has been read out
+            if (o_used[h] > 0 &&
+                !wait_or_abort(&o_free[h], static_cast<uint32_t>((o_used[h] - 1) & 1), &abort_flag,
+                               p.status))
               return false;
-            if (j == 0) {  // O starts anew: the half's previous unit has been read out
-              if (o_used[h] > 0 &&
-                  !wait_or_abort(&o_free[h], static_cast<uint32_t>((o_used[h] - 1) & 1), &abort_flag,
-                                 p.status))
-                return false;
-              ++o_used[h];
-            }
-            tc_fence_after_sync();
+            ++o_used[h];
+          }
+          tc_fence_after_sync();
+          if (leader) {
+            umma_bf16_ts(tmem + kOCol + h * kHeadDim, tmem + kPCol + h * (kTileN / 2), v_desc, kIdescO,
+                         j > 0 ? 1u : 0u);
 #pragma unroll
-            for (int kk = 0; kk < kTileN / 16; ++kk)  // 16 keys: 2 KiB of V, 8 columns of P
+            for (int kk = 1; kk < kTileN / 16; ++kk)  // 16 keys: 2 KiB of V, 8 columns of P
               umma_bf16_ts(tmem + kOCol + h * kHeadDim, tmem + kPCol + h * (kTileN / 2) + kk * 8,
-                           v_desc + 128 * kk, kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
+                           v_desc + 128 * kk, kIdescO, 1u);
             umma_commit(&pv_done[h]);
-            ++pv_issued[h];
           }
-          umma_commit(&v_empty[st]);
-          return true;
-        };
-        int k = 0, jt = 0;
-        Unit cur, nxt;
-        bool have = next_unit<kUnitTokens, kTileN>(p, sc, k, cur);
-        bool have_next = have && next_unit<kUnitTokens, kTileN>(p, sc, k, nxt);
-        int n0 = 0, n1 = 0;
-        bool ok = have;
-        if (have) {
-          n0 = half_tiles<kHalfTokens>(cur, 0);
-          n1 = half_tiles<kHalfTokens>(cur, 1);
-          ok = issue_s(n0, n1, 0, 0);
+          ++pv_issued[h];
         }
-        while (ok && have) {
-          int m0 = 0, m1 = 0;
-          if (have_next) {
-            m0 = half_tiles<kHalfTokens>(nxt, 0);
-            m1 = half_tiles<kHalfTokens>(nxt, 1);
-          }
-          for (int j = 0; ok && j < cur.n_kv; ++j, ++jt) {
-            if (j + 1 < cur.n_kv)
-              ok = issue_s(n0, n1, j + 1, jt + 1);
-            else if (have_next)
-              ok = issue_s(m0, m1, 0, jt + 1);
-            if (ok) ok = issue_pv(n0, n1, j, jt);
-          }
-          cur = nxt;
-          n0 = m0;
-          n1 = m1;
-          have = have_next;
-          if (have) have_next = next_unit<kUnitTokens, kTileN>(p, sc, k, nxt);
+        if (leader) umma_commit(&v_empty[vs]);
+        if (++vs == kRing) {
+          vs = 0;
+          vph ^= 1u;
         }
-        // wait (bounded) until every MMA issued above has completed
+        return true;
+      };
+      int k = 0;
+      Unit cur, nxt;
+      bool have = next_unit<kUnitTokens, kTileN>(p, sc, k, cur);
+      bool have_next = have && next_unit<kUnitTokens, kTileN>(p, sc, k, nxt);
+      int n0 = 0, n1 = 0;
+      bool ok = have;
+      if (have) {
+        n0 = half_tiles<kHalfTokens>(cur, 0);
+        n1 = half_tiles<kHalfTokens>(cur, 1);
+        ok = issue_s(n0, n1, 0);
+      }
+      while (ok && have) {
+        int m0 = 0, m1 = 0;
+        if (have_next) {
+          m0 = half_tiles<kHalfTokens>(nxt, 0);
+          m1 = half_tiles<kHalfTokens>(nxt, 1);
+        }
+        const int n_kv = cur.n_kv;
+        for (int j = 0; ok && j < n_kv; ++j) {
+          const bool last = j + 1 == n_kv;
+          if (!last || have_next) ok = issue_s(last ? m0 : n0, last ? m1 : n1, last ? 0 : j + 1);
+          if (ok) ok = issue_pv(n0, n1, j);
+        }
+        cur = nxt;
+        n0 = m0;
+        n1 = m1;
+        have = have_next;
+        if (have) have_next = next_unit<kUnitTokens, kTileN>(p, sc, k, nxt);
+      }
+      // wait (bounded) until every MMA issued above has completed
+      if (leader) {
         umma_commit(drain);
         if (!mbar_wait(drain, 0)) flag_error(p.status, PA_DEVFLAG_TIMEOUT);
       }
+      __syncwarp();
     } else if (warp == 13) {
       // ============================ producer ============================
       int k = 0;
