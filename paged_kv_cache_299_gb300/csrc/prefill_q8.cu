@@ -63,7 +63,7 @@ constexpr int kRawOff = kVOff + kRing * kOpBytes;
 constexpr int kRawScaleOff = kRawOff + kRing * kRawBytes;  // [kRing][2][8] floats
 constexpr int kConstOff = kRawScaleOff + kRing * 2 * kBlocksPerTile * 4;
 constexpr int kBarOff = kConstOff + kConstRing * kConsts * 4;
-constexpr int kNumBars = 4 + 4 + 2 + 6 * kRing + kConstRing + 5 * 2 + 1;
+constexpr int kNumBars = 4 + 4 + 2 + 6 * kRing + 5 * 2 + 1;
 constexpr int kMiscOff = kBarOff + (kNumBars + 1) / 2 * 16;
 constexpr int kUnitOff = kMiscOff + 128;
 constexpr int kSmemBytes = kUnitOff + 2 * kMaxUnitsPerCta * 4;
@@ -86,6 +86,12 @@ struct Pools {
   const float* key_scale;
   const float* value_scale;
 };
+
+// wait_or_abort whose usual case, a phase that has completed, is one try_wait.
+__device__ __forceinline__ bool wait_ready(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                           int32_t* status) {
+  return mbar_try_wait(bar, parity) || wait_or_abort(bar, parity, abort_flag, status);
+}
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile(
@@ -195,8 +201,9 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
   uint64_t* k_empty = k_full + kRing;        // [kRing] scores that read it done
   uint64_t* v_full = k_empty + kRing;
   uint64_t* v_empty = v_full + kRing;
-  uint64_t* c_full = v_empty + kRing;        // [kConstRing] the tile's score constants
-  uint64_t* s_full = c_full + kConstRing;    // [half] scores in tensor memory
+  // [half] scores in tensor memory: the MMAs' commit, and an arrival of the issuing warp, which
+  // has seen K's arrivals and so passes on what the converters wrote before them (the constants)
+  uint64_t* s_full = v_empty + kRing;
   uint64_t* s_free = s_full + 2;             // [half] scores read into registers
   uint64_t* p_full = s_free + 2;             // [half] P in tensor memory
   uint64_t* pv_done = p_full + 2;            // [half] P V done: P free, O up to date
@@ -217,7 +224,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&q_ready[b], kRowWarps);
-      mbar_init(&s_full[b], 1);
+      mbar_init(&s_full[b], 2);
       mbar_init(&s_free[b], kRowWarps);
       mbar_init(&p_full[b], kRowWarps);
       mbar_init(&pv_done[b], 1);
@@ -231,7 +238,6 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
       mbar_init(&v_full[i], kConvWarps);
       mbar_init(&v_empty[i], 1);
     }
-    for (int i = 0; i < kConstRing; ++i) mbar_init(&c_full[i], kConvWarps);
     mbar_init(drain, 1);
     fence_barrier_init();
     abort_flag = 0;
@@ -270,7 +276,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
     // Turn this row of the half's next Q into f16, in place, under the row's power of two.
     auto convert_q = [&]() -> bool {
       const int b = 2 * half + (qc & 1);
-      bool ok = wait_or_abort(&q_full[b], static_cast<uint32_t>((qc >> 1) & 1), &abort_flag, p.status);
+      bool ok = wait_ready(&q_full[b], static_cast<uint32_t>((qc >> 1) & 1), &abort_flag, p.status);
       if (!__all_sync(0xffffffffu, ok)) return false;
       uint8_t* q = sq + b * kQBytes;
       uint4 w[8];
@@ -333,7 +339,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
         q_factor = q_factor_next;
         float m = -INFINITY, l = 0.f;
         for (int j = 0; j < n_mine; ++j, ++c) {
-          ok = wait_or_abort(&s_full[half], static_cast<uint32_t>(c & 1), &abort_flag, p.status);
+          ok = wait_ready(&s_full[half], static_cast<uint32_t>(c & 1), &abort_flag, p.status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           tc_fence_after_sync();
           // The next unit's Q, before its first scores are wanted.  Only now: these scores
@@ -355,9 +361,6 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
               if (kb + i > pos) v[i >> 5][i & 31] = __float_as_uint(-INFINITY);
           }
           const int slot = (jt + j) % kConstRing;
-          ok = wait_or_abort(&c_full[slot], static_cast<uint32_t>(((jt + j) / kConstRing) & 1),
-                             &abort_flag, p.status);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
           const uint32_t cs = smem_addr(consts + slot * kConsts);
           float mt = -INFINITY;
 #pragma unroll
@@ -401,7 +404,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
             l += (sum.x + sum.y) * lds_f32(cs + 4 * (2 * kBlocksPerTile + b));
           }
           if (c > 0) {  // the previous P V: P's columns are free and O is up to date
-            ok = wait_or_abort(&pv_done[half], static_cast<uint32_t>((c - 1) & 1), &abort_flag,
+            ok = wait_ready(&pv_done[half], static_cast<uint32_t>((c - 1) & 1), &abort_flag,
                                p.status);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after_sync();
@@ -432,7 +435,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
         }
         if (!ok) break;
         // ---- epilogue ----
-        ok = wait_or_abort(&pv_done[half], static_cast<uint32_t>((c - 1) & 1), &abort_flag, p.status);
+        ok = wait_ready(&pv_done[half], static_cast<uint32_t>((c - 1) & 1), &abort_flag, p.status);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after_sync();
         uint32_t o[2][32];
@@ -471,7 +474,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
         for (int j = 0; j < cur.n_kv; ++j, ++jt) {
           const int st = jt % kRing;
           const uint32_t ph = static_cast<uint32_t>((jt / kRing) & 1);
-          ok = wait_or_abort(&raw_full[st], ph, &abort_flag, p.status);
+          ok = wait_ready(&raw_full[st], ph, &abort_flag, p.status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           const uint8_t* raw = sraw + st * kRawBytes + cw * 32 * kQ8RowBytes + 16 * lane;
           // score constants of this warp's two blocks
@@ -498,10 +501,8 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
               cs[2 * kBlocksPerTile + blk] = 1.f / f;
             }
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&c_full[slot]);
           // K: f16
-          ok = wait_or_abort(&k_empty[st], ph ^ 1u, &abort_flag, p.status);
+          ok = wait_ready(&k_empty[st], ph ^ 1u, &abort_flag, p.status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           uint8_t* dst = sk + st * kOpBytes;
           const int row0 = cw * 32 + (lane >> 2);
@@ -521,7 +522,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
           __syncwarp();
           if (lane == 0) mbar_arrive(&k_full[st]);
           // V: bf16 times 2^e
-          ok = wait_or_abort(&v_empty[st], ph ^ 1u, &abort_flag, p.status);
+          ok = wait_ready(&v_empty[st], ph ^ 1u, &abort_flag, p.status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           dst = sv + st * kOpBytes;
           raw += kTileN * kQ8RowBytes;
@@ -574,19 +575,19 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
       uint32_t kph = 0, vph = 0;     // and their phases
       // scores of a unit's tile j, for the halves that need it
       auto issue_s = [&](int n0, int n1, int j) -> bool {
-        if (!wait_or_abort(&k_full[ks], kph, &abort_flag, p.status)) return false;
+        if (!wait_ready(&k_full[ks], kph, &abort_flag, p.status)) return false;
         const uint64_t k_desc = k_desc0 + kStageStep * ks;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int n = h ? n1 : n0;
           if (j >= n) continue;
           if (j == 0) {
-            if (!wait_or_abort(&q_ready[h], static_cast<uint32_t>(q_used[h] & 1), &abort_flag, p.status))
+            if (!wait_ready(&q_ready[h], static_cast<uint32_t>(q_used[h] & 1), &abort_flag, p.status))
               return false;
             ++q_used[h];
           }
           if (s_issued[h] > 0 &&
-              !wait_or_abort(&s_free[h], static_cast<uint32_t>((s_issued[h] - 1) & 1), &abort_flag,
+              !wait_ready(&s_free[h], static_cast<uint32_t>((s_issued[h] - 1) & 1), &abort_flag,
                              p.status))
             return false;
           tc_fence_after_sync();
@@ -598,6 +599,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
               umma_bf16(tmem + kSCol + h * kTileN, q_desc + 2 * kk, k_desc + 2 * kk, kIdescS,
                         kk > 0 ? 1u : 0u);
             umma_commit(&s_full[h]);
+            mbar_arrive(&s_full[h]);
             if (j == n - 1) umma_commit(&q_empty[qb]);
           }
           ++s_issued[h];
@@ -610,16 +612,16 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
         return true;
       };
       auto issue_pv = [&](int n0, int n1, int j) -> bool {
-        if (!wait_or_abort(&v_full[vs], vph, &abort_flag, p.status)) return false;
+        if (!wait_ready(&v_full[vs], vph, &abort_flag, p.status)) return false;
         const uint64_t v_desc = v_desc0 + kStageStep * vs;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (j >= (h ? n1 : n0)) continue;
-          if (!wait_or_abort(&p_full[h], static_cast<uint32_t>(pv_issued[h] & 1), &abort_flag, p.status))
+          if (!wait_ready(&p_full[h], static_cast<uint32_t>(pv_issued[h] & 1), &abort_flag, p.status))
             return false;
           if (j == 0) {  // O starts anew: the half's previous unit has been read out
             if (o_used[h] > 0 &&
-                !wait_or_abort(&o_free[h], static_cast<uint32_t>((o_used[h] - 1) & 1), &abort_flag,
+                !wait_ready(&o_free[h], static_cast<uint32_t>((o_used[h] - 1) & 1), &abort_flag,
                                p.status))
               return false;
             ++o_used[h];
@@ -693,7 +695,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
           const int b = 2 * h + (nq[h] & 1);
           if (lane == 0 && ok) {
             if (nq[h] >= 2)
-              ok = wait_or_abort(&q_empty[b], static_cast<uint32_t>(((nq[h] - 2) >> 1) & 1),
+              ok = wait_ready(&q_empty[b], static_cast<uint32_t>(((nq[h] - 2) >> 1) & 1),
                                  &abort_flag, p.status);
             if (ok) {
               mbar_arrive_expect_tx(&q_full[b], kQBytes);
@@ -737,7 +739,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
           if (__any_sync(0xffffffffu, bad) && lane == 0) flag_error(p.status, PA_DEVFLAG_BAD_BLOCK);
           int go = 1;
           if (lane == 0) {
-            go = wait_or_abort(&raw_empty[st], static_cast<uint32_t>((jt / kRing) & 1) ^ 1u, &abort_flag,
+            go = wait_ready(&raw_empty[st], static_cast<uint32_t>((jt / kRing) & 1) ^ 1u, &abort_flag,
                                p.status);
             if (go) mbar_arrive_expect_tx(&raw_full[st], __popc(mask) * 2u * kQ8TileBytes);
           }
