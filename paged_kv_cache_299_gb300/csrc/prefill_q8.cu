@@ -47,9 +47,11 @@ namespace {
 constexpr int kTileM = 128;                       // MMA rows of one half
 constexpr int kTileN = 128;                       // keys per K/V tile
 constexpr int kBlocksPerTile = kTileN / kBlockSize;
-constexpr int kThreads = 512;
-constexpr int kRowWarps = 4;                      // per half
+constexpr int kThreads = 768;
+constexpr int kRowWarps = 8;                      // per half: four for each half of a tile's keys
+constexpr int kRowThreads = 2 * kRowWarps * 32;
 constexpr int kConvWarps = 4;
+constexpr int kConvWarp0 = 16, kMmaWarp = 20, kProducerWarp = 21;  // 22 and 23 idle
 constexpr int kRing = 3;                          // stages of each of the three rings
 constexpr int kConstRing = 8;                     // tiles whose score constants are kept
 constexpr int kConsts = 3 * kBlocksPerTile;       // key scale, log2 f, 1 / f of every block
@@ -62,10 +64,11 @@ constexpr int kVOff = kKOff + kRing * kOpBytes;
 constexpr int kRawOff = kVOff + kRing * kOpBytes;
 constexpr int kRawScaleOff = kRawOff + kRing * kRawBytes;  // [kRing][2][8] floats
 constexpr int kConstOff = kRawScaleOff + kRing * 2 * kBlocksPerTile * 4;
-constexpr int kBarOff = kConstOff + kConstRing * kConsts * 4;
+constexpr int kXchOff = kConstOff + kConstRing * kConsts * 4;  // [half][3][2][128] floats
+constexpr int kBarOff = kXchOff + 2 * 3 * 2 * kTileM * 4;
 constexpr int kNumBars = 4 + 4 + 2 + 6 * kRing + 5 * 2 + 1;
 constexpr int kMiscOff = kBarOff + (kNumBars + 1) / 2 * 16;
-constexpr int kUnitOff = kMiscOff + 128;
+constexpr int kUnitOff = kMiscOff + 160;
 constexpr int kSmemBytes = kUnitOff + 2 * kMaxUnitsPerCta * 4;
 static_assert(kSmemBytes <= 227 * 1024, "one CTA per SM");
 static_assert(sort_scratch_bytes(kThreads) <= kRawOff, "sort scratch fits below the raw ring");
@@ -75,10 +78,10 @@ constexpr uint32_t kPCol = 256;  // + 64 per half: bf16 pairs
 constexpr uint32_t kOCol = 384;  // + 64 per half: fp32
 constexpr float kRescaleThreshold = 8.0f;
 constexpr int kQExp = 13;  // exponent of a row's largest f16 query element
-// Register split (setmaxnreg): the row warps' 256 threads and the others' 256 share what the
-// CTA was launched with; the launcher checks that it suffices.
-constexpr int kRowRegs = 176;
-constexpr int kOtherRegs = 80;
+// Register split (setmaxnreg): the row warps' threads and the others' share what the CTA was
+// launched with; the launcher checks that it suffices.
+constexpr int kRowRegs = 96;
+constexpr int kOtherRegs = 48;
 
 struct Pools {
   const uint8_t* key;
@@ -189,6 +192,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
   uint8_t* sraw = smem + kRawOff;
   float* raw_scale = reinterpret_cast<float*>(smem + kRawScaleOff);
   float* consts = reinterpret_cast<float*>(smem + kConstOff);
+  float* xch = reinterpret_cast<float*>(smem + kXchOff);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBarOff);
   // A half that has no rows in a unit takes no part in it: Q buffers and phases count the units
   // of each half by themselves.
@@ -213,7 +217,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
   volatile int& abort_flag = *reinterpret_cast<volatile int*>(misc + 1);
   int* n_units_s = misc + 2;
-  int* red = misc + 4;  // 24 ints of scan scratch
+  int* red = misc + 4;  // 32 ints of scan scratch
   int32_t* unit_s = reinterpret_cast<int32_t*>(smem + kUnitOff);
   int32_t* unit_tg = unit_s + kMaxUnitsPerCta;
 
@@ -242,11 +246,11 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
     fence_barrier_init();
     abort_flag = 0;
   }
-  if (warp == 12) {
+  if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
-  if (warp == 13 && lane == 0) prefetch_tensormap(&tmap_q);
+  if (warp == kProducerWarp && lane == 0) prefetch_tensormap(&tmap_q);
   const int n_units = plan_units<kUnitTokens, kTileN, kThreads>(p, smem, red, unit_s, unit_tg);
   if (tid == 0) *n_units_s = n_units;
   fence_proxy_async_smem();  // the plan's scratch before copies and MMAs touch the buffers
@@ -259,43 +263,62 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
   sc.unit_tg = unit_tg;
   sc.n_units = *n_units_s;
 
-  if (warp < 8) {
+  if (warp < 2 * kRowWarps) {
     // ============================ row warps ============================
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
-    const int half = warp >> 2;
-    const int r = tid & 127;  // row of the half == TMEM lane
+    const int half = warp >> 3;
+    const int part = (warp >> 2) & 1;  // keys 64 part .. 64 part + 63 of every tile
+    const int r = (warp & 3) * 32 + lane;  // row of the half == TMEM lane
     const int tt = r / GROUP, hh = r % GROUP;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t s_addr = lane_addr + kSCol + half * kTileN;
-    const uint32_t p_addr = lane_addr + kPCol + half * (kTileN / 2);
-    const uint32_t o_addr = lane_addr + kOCol + half * kHeadDim;
+    const uint32_t s_addr = lane_addr + kSCol + half * kTileN + part * (kTileN / 2);
+    const uint32_t p_addr = lane_addr + kPCol + half * (kTileN / 2) + part * (kTileN / 4);
+    const uint32_t o_addr = lane_addr + kOCol + half * kHeadDim + part * (kHeadDim / 2);
+    // The two warps of the same rows exchange a float per row (slot 0 or 1: a tile's maximum;
+    // 2: the sum at the end) and go on together.  A warp that gives up (for a
+    // timeout somewhere) arrives once more, so that its partner is not left waiting, and the
+    // partner then sees the flag.
+    float* const my_xch = xch + (half * 3 * 2 + part) * kTileM + r;
+    const int pair_bar = 1 + half * 4 + (warp & 3);
+    auto exchange = [&](int slot, float mine, float& other) -> bool {
+      my_xch[slot * 2 * kTileM] = mine;
+      named_barrier_sync(pair_bar, 64);
+      other = my_xch[slot * 2 * kTileM + (part ? -kTileM : kTileM)];
+      return __all_sync(0xffffffffu, abort_flag == 0);
+    };
+    auto wait_row = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, wait_ready(bar, parity, &abort_flag, p.status));
+    };
     int k = 0;
     int qc = 0;          // Qs this half has turned into f16
     bool have_q = false;  // the coming unit's among them
     float q_factor = 0.f, q_factor_next = 0.f;  // score factor of this row
-    // Turn this row of the half's next Q into f16, in place, under the row's power of two.
+    // Turn this row of the half's next Q into f16, in place, under the row's power of two: both
+    // warps look at the whole row, each writes half of it.
     auto convert_q = [&]() -> bool {
       const int b = 2 * half + (qc & 1);
-      bool ok = wait_ready(&q_full[b], static_cast<uint32_t>((qc >> 1) & 1), &abort_flag, p.status);
-      if (!__all_sync(0xffffffffu, ok)) return false;
+      if (!wait_row(&q_full[b], static_cast<uint32_t>((qc >> 1) & 1))) return false;
       uint8_t* q = sq + b * kQBytes;
-      uint4 w[8];
+      uint4 w[4];
       uint32_t big = 0u;  // largest magnitude as bits
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        w[c] = lds128(q + swz(r, c));
-        const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+        const uint4 x = lds128(q + swz(r, c ^ (4 * part)));  // its own half first
+        if (c < 4) w[c] = x;
+        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          big = max(big, max((x[i] << 16) & 0x7fff0000u, x[i] & 0x7fff0000u));
+          big = max(big, max((y[i] << 16) & 0x7fff0000u, y[i] & 0x7fff0000u));
       }
       int shift = 0;
       if (big != 0u && big < 0x7f800000u)
         shift = min(126, kQExp + 127 - static_cast<int>(max(big >> 23, 1u)));
       const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
       q_factor_next = p.qk_scale * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+      named_barrier_sync(pair_bar, 64);  // both have read
+      if (!__all_sync(0xffffffffu, abort_flag == 0)) return false;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
+      for (int c = 0; c < 4; ++c) {
         const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
         uint32_t y[4];
 #pragma unroll
@@ -303,7 +326,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
           const float2 f = bf16x2_to_float2(x[i]);
           y[i] = pack_half2(f.x * up, f.y * up);
         }
-        *reinterpret_cast<uint4*>(q + swz(r, c)) = make_uint4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<uint4*>(q + swz(r, c ^ (4 * part))) = make_uint4(y[0], y[1], y[2], y[3]);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -329,7 +352,8 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
         row_ok = token < u.q_len;
         pos = u.L - u.q_len + min(token, u.q_len - 1);
         pos_lo = u.L - u.q_len + u.tok0 + half * kHalfTokens;
-        dst = p.out + (static_cast<int64_t>(u.q0 + token) * p.num_q_heads + u.g * GROUP + hh) * kHeadDim;
+        dst = p.out + (static_cast<int64_t>(u.q0 + token) * p.num_q_heads + u.g * GROUP + hh) * kHeadDim +
+              part * (kHeadDim / 2);
         int peek = k;
         next_mine = next_unit<kUnitTokens, kTileN>(p, sc, peek, u) && half_tiles<kHalfTokens>(u, half) > 0;
       }
@@ -339,32 +363,31 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
         q_factor = q_factor_next;
         float m = -INFINITY, l = 0.f;
         for (int j = 0; j < n_mine; ++j, ++c) {
-          ok = wait_ready(&s_full[half], static_cast<uint32_t>(c & 1), &abort_flag, p.status);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (!(ok = wait_row(&s_full[half], static_cast<uint32_t>(c & 1)))) break;
           tc_fence_after_sync();
           // The next unit's Q, before its first scores are wanted.  Only now: these scores
           // show that the issuing thread has seen this unit's Q, so q_ready can complete a
           // phase again.
           if (j == n_mine - 1 && next_mine && !(ok = convert_q())) break;
-          uint32_t v[4][32];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld32(s_addr + 32 * i, v[i]);
+          uint32_t v[2][32];
+          tmem_ld32(s_addr, v[0]);
+          tmem_ld32(s_addr + 32, v[1]);
           tmem_wait_ld();
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(&s_free[half]);
-          const int kb = j * kTileN;
-          if (kb + kTileN - 1 > pos_lo) {
+          const int kb = j * kTileN + part * (kTileN / 2);
+          if (kb + kTileN / 2 - 1 > pos_lo) {
             // a tile on the causal diagonal: hide keys past each row's position
 #pragma unroll
-            for (int i = 0; i < kTileN; ++i)
+            for (int i = 0; i < kTileN / 2; ++i)
               if (kb + i > pos) v[i >> 5][i & 31] = __float_as_uint(-INFINITY);
           }
           const int slot = (jt + j) % kConstRing;
-          const uint32_t cs = smem_addr(consts + slot * kConsts);
+          const uint32_t cs = smem_addr(consts + slot * kConsts + part * (kBlocksPerTile / 2));
           float mt = -INFINITY;
 #pragma unroll
-          for (int b = 0; b < kBlocksPerTile; ++b) {
+          for (int b = 0; b < kBlocksPerTile / 2; ++b) {
             const uint32_t* x = &v[b >> 1][16 * (b & 1)];
             float a0 = __uint_as_float(x[0]), a1 = __uint_as_float(x[1]);
 #pragma unroll
@@ -375,7 +398,9 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
             a0 = max3f(a0, __uint_as_float(x[14]), __uint_as_float(x[15]));
             mt = fmaxf(mt, fmaxf(a0, a1) * (lds_f32(cs + 4 * b) * q_factor));
           }
-          const float m_new = fmaxf(m, mt);
+          float theirs;
+          if (!(ok = exchange(c & 1, mt, theirs))) break;
+          const float m_new = max3f(m, mt, theirs);
           const bool grow = m_new - m > kRescaleThreshold;  // true on the first tile
           float alpha = 1.f;
           if (grow) {
@@ -385,7 +410,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
           l *= alpha;
           // p' two at a time, packed to bf16 over the scores
 #pragma unroll
-          for (int b = 0; b < kBlocksPerTile; ++b) {
+          for (int b = 0; b < kBlocksPerTile / 2; ++b) {
             const float f = lds_f32(cs + 4 * b) * q_factor;
             const float nb = lds_f32(cs + 4 * (kBlocksPerTile + b)) - m;
             const float2 fb = make_float2(f, f);
@@ -399,34 +424,28 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
                                           fb, nb2);
               const float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
               sum = __fadd2_rn(sum, y);
-              v[e >> 6][(e >> 1) & 31] = pack_bf2(y.x, y.y);
+              v[0][e >> 1] = pack_bf2(y.x, y.y);
             }
             l += (sum.x + sum.y) * lds_f32(cs + 4 * (2 * kBlocksPerTile + b));
           }
           if (c > 0) {  // the previous P V: P's columns are free and O is up to date
-            ok = wait_ready(&pv_done[half], static_cast<uint32_t>((c - 1) & 1), &abort_flag,
-                               p.status);
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            if (!(ok = wait_row(&pv_done[half], static_cast<uint32_t>((c - 1) & 1)))) break;
             tc_fence_after_sync();
           }
           tmem_st32(p_addr, v[0]);
-          tmem_st32(p_addr + 32, v[1]);
           if (j > 0 && __any_sync(0xffffffffu, grow)) {
             const float2 a2 = make_float2(alpha, alpha);
+            uint32_t(&o)[32] = v[1];  // this warp's 32 columns of O
+            tmem_ld32(o_addr, o);
+            tmem_wait_ld();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t(&o)[32] = v[2 + h];
-              tmem_ld32(o_addr + 32 * h, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float2 x = __fmul2_rn(
-                    make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), a2);
-                o[2 * i] = __float_as_uint(x.x);
-                o[2 * i + 1] = __float_as_uint(x.y);
-              }
-              tmem_st32(o_addr + 32 * h, o);
+            for (int i = 0; i < 16; ++i) {
+              const float2 x = __fmul2_rn(
+                  make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), a2);
+              o[2 * i] = __float_as_uint(x.x);
+              o[2 * i + 1] = __float_as_uint(x.y);
             }
+            tmem_st32(o_addr, o);
           }
           tmem_wait_st();
           tc_fence_before_sync();
@@ -434,27 +453,26 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
           if (lane == 0) mbar_arrive(&p_full[half]);
         }
         if (!ok) break;
-        // ---- epilogue ----
-        ok = wait_ready(&pv_done[half], static_cast<uint32_t>((c - 1) & 1), &abort_flag, p.status);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        // ---- epilogue: this warp's 32 dims ----
+        float theirs;
+        if (!(ok = exchange(2, l, theirs))) break;
+        if (!(ok = wait_row(&pv_done[half], static_cast<uint32_t>((c - 1) & 1)))) break;
         tc_fence_after_sync();
-        uint32_t o[2][32];
-        tmem_ld32(o_addr, o[0]);
-        tmem_ld32(o_addr + 32, o[1]);
+        uint32_t o[32];
+        tmem_ld32(o_addr, o);
         tmem_wait_ld();
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&o_free[half]);
-        const float inv = 1.f / l;
+        const float inv = 1.f / (l + theirs);
         if (row_ok) {
 #pragma unroll
-          for (int q8 = 0; q8 < 8; ++q8) {
+          for (int q8 = 0; q8 < 4; ++q8) {
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int i = q8 * 8 + 2 * e;
-              w[e] = pack_bf2(__uint_as_float(o[i >> 5][i & 31]) * inv,
-                              __uint_as_float(o[i >> 5][(i & 31) + 1]) * inv);
+              w[e] = pack_bf2(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
             }
             *reinterpret_cast<uint4*>(dst + 8 * q8) = make_uint4(w[0], w[1], w[2], w[3]);
           }
@@ -462,11 +480,13 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
       }
       jt += n_kv;
     }
+    if (!ok) asm volatile("bar.arrive %0, 64;" ::"r"(pair_bar) : "memory");
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp < 12) {
+    if (warp < kMmaWarp) {
       // ============================ converters ============================
-      const int cw = warp - 8;  // keys 32 cw .. 32 cw + 31 of every tile, blocks 2 cw and 2 cw + 1
+      const int cw = warp - kConvWarp0;  // keys 64 cw .. 64 cw + 63 of every tile, blocks 4 cw .. + 3
+      constexpr int kMyBlocks = kBlocksPerTile / kConvWarps;
       int k = 0, jt = 0;
       Unit cur;
       bool ok = true;
@@ -476,39 +496,37 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
           const uint32_t ph = static_cast<uint32_t>((jt / kRing) & 1);
           ok = wait_ready(&raw_full[st], ph, &abort_flag, p.status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          const uint8_t* raw = sraw + st * kRawBytes + cw * 32 * kQ8RowBytes + 16 * lane;
-          // score constants of this warp's two blocks
+          const uint8_t* raw = sraw + st * kRawBytes + cw * kMyBlocks * kQ8TileBytes + 16 * lane;
+          // score constants of this warp's blocks
           const int slot = jt % kConstRing;
           const float* rs = raw_scale + st * 2 * kBlocksPerTile;
-          int e[2];  // exponents of the value scales; -1000: a scale of zero
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const int blk = 2 * cw + b;
+          int my_e = 0;  // lane b: exponent of block b's value scale; -1000: a scale of zero
+          if (lane < kMyBlocks) {
+            const int blk = kMyBlocks * cw + lane;
             const bool needed = j * kBlocksPerTile + blk < cur.blocks_needed;
             const float ks = needed ? fmaxf(rs[blk], 1.17549435e-38f) : 1.f;
             const float vs = needed ? rs[kBlocksPerTile + blk] : 1.f;
             const uint32_t bits = __float_as_uint(vs);
-            e[b] = static_cast<int>((bits >> 23) & 0xffu) - 127;
+            my_e = static_cast<int>((bits >> 23) & 0xffu) - 127;
             float f = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
-            if (e[b] == -127) {  // zero (or too small to matter)
-              e[b] = -1000;
+            if (my_e == -127) {  // zero (or too small to matter)
+              my_e = -1000;
               f = 1.f;
             }
-            if (lane == 0) {
-              float* cs = consts + slot * kConsts;
-              cs[blk] = ks;
-              cs[kBlocksPerTile + blk] = f == 1.f ? 0.f : __log2f(f);
-              cs[2 * kBlocksPerTile + blk] = 1.f / f;
-            }
+            float* cs = consts + slot * kConsts + blk;
+            cs[0] = ks;
+            cs[kBlocksPerTile] = f == 1.f ? 0.f : __log2f(f);
+            cs[2 * kBlocksPerTile] = f == 1.f ? 1.f : 1.f / f;
           }
+          __syncwarp();  // before lane 0's arrival below
           // K: f16
           ok = wait_ready(&k_empty[st], ph ^ 1u, &abort_flag, p.status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           uint8_t* dst = sk + st * kOpBytes;
-          const int row0 = cw * 32 + (lane >> 2);
+          const int row0 = cw * kMyBlocks * kBlockSize + (lane >> 2);
           const int c0 = 2 * (lane & 3);  // 16 codes of a row: two 16-byte chunks
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 2 * kMyBlocks; ++i) {
             const uint4 w = lds128(raw + i * 512);
             uint4 a, b;
             codes4_to_half2x2(w.x, a.x, a.y);
@@ -528,9 +546,9 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
           raw += kTileN * kQ8RowBytes;
           const int keys_left = cur.keys - j * kTileN;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 2 * kMyBlocks; ++i) {
             uint4 w = lds128(raw + i * 512);
-            const int eb = e[i >> 1];
+            const int eb = __shfl_sync(0xffffffffu, my_e, i >> 1);
             // keys past the last needed one weigh nothing, but may hold anything
             if (row0 + 8 * i >= keys_left || eb == -1000) w = make_uint4(0u, 0u, 0u, 0u);
             uint4 a, b;
@@ -558,7 +576,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
           }
         }
       }
-    } else if (warp == 12) {
+    } else if (warp == kMmaWarp) {
       // ============================ MMA issuer ============================
       // The whole warp walks the tiles, so that barriers, counters and descriptors stay
       // warp-uniform (uniform registers feed the MMAs); one elected lane issues.
@@ -680,7 +698,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
         if (!mbar_wait(drain, 0)) flag_error(p.status, PA_DEVFLAG_TIMEOUT);
       }
       __syncwarp();
-    } else if (warp == 13) {
+    } else if (warp == kProducerWarp) {
       // ============================ producer ============================
       int k = 0;
       Unit cur, nxt;
@@ -788,7 +806,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
 
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kMmaWarp) {
     __syncwarp();
     tc_fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
@@ -804,7 +822,7 @@ cudaError_t launch(const AttendQ8Args& a, cudaStream_t stream) {
     e = cudaFuncGetAttributes(&attr, paged_chunk_q8_kernel<GROUP>);
     if (e != cudaSuccess) return e;
     // setmaxnreg waits for registers the launch never had: refuse instead
-    if (attr.numRegs * kThreads < (kThreads / 2) * (kRowRegs + kOtherRegs))
+    if (attr.numRegs * kThreads < kRowThreads * kRowRegs + (kThreads - kRowThreads) * kOtherRegs)
       return cudaErrorInvalidConfiguration;
     e = cudaFuncSetAttribute(paged_chunk_q8_kernel<GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmemBytes);
