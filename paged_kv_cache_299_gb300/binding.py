@@ -426,32 +426,74 @@ def pa_copy_blocks(key_cache, value_cache, block_mapping, device_status=None, st
     _check(st, "pa_copy_blocks")
 
 
+# The calls below run once per layer and decode step, where a step's kernels take a few
+# microseconds: their checks read each attribute once, pointers and streams travel as plain
+# integers, and descriptors are kept by geometry.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+_descs = {}
+
+
+def _current_stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None or _get_device is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(_get_device())
+
+
+def _kept_desc(shape):
+    d = _descs.get(shape)
+    if d is None:
+        nb, hkv, bs, dim = shape
+        d = _descs[shape] = CacheDesc(nb, hkv, dim, bs)
+    return d
+
+
+def _check_tensor(t, name, dtype, ndim):
+    """_need with a quick way through for tensors that are as they should be; the pointer."""
+    try:
+        if t.dtype is dtype and t.is_cuda and t.dim() == ndim and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, name, dtype, ndim)
+    return t.data_ptr()
+
+
+def _status_ptr(device_status):
+    return None if device_status is None else device_status.data_ptr()
+
+
 def _need_rows(t, name, heads=None):
     """bf16 [T, heads, 64] whose rows are contiguous per token; returns the token stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != 64 or (heads is not None and t.shape[1] != heads):
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != 64 or (heads is not None and shape[1] != heads):
         raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, 64], "
-                         f"got {tuple(t.shape)}")
+                         f"got {tuple(shape)}")
     stride, row, one = t.stride()
-    heads = t.shape[1]
+    heads = shape[1]
     if one != 1 or (row != 64 and heads > 1):
         raise ValueError(f"{name}: the head rows of a token must be contiguous")
-    return max(stride, heads * 64) if t.shape[0] <= 1 else stride
+    return max(stride, heads * 64) if shape[0] <= 1 else stride
 
 
 def _need_q8(key_cache, value_cache, key_scale, value_scale):
-    for t, name in ((key_cache, "key_cache"), (value_cache, "value_cache")):
-        _need(t, name, torch.float8_e4m3fn, 4)
-    for t, name in ((key_scale, "key_scale"), (value_scale, "value_scale")):
-        _need(t, name, torch.float32, 2)
-    if key_cache.shape != value_cache.shape or key_scale.shape != value_scale.shape or \
-            key_scale.shape != key_cache.shape[:2]:
+    """Pointers of an 8-bit cache's four tensors, and its shape."""
+    kc = _check_tensor(key_cache, "key_cache", torch.float8_e4m3fn, 4)
+    vc = _check_tensor(value_cache, "value_cache", torch.float8_e4m3fn, 4)
+    ks = _check_tensor(key_scale, "key_scale", torch.float32, 2)
+    vs = _check_tensor(value_scale, "value_scale", torch.float32, 2)
+    shape, scales = key_cache.shape, key_scale.shape
+    if value_cache.shape != shape or value_scale.shape != scales or scales != shape[:2]:
         raise ValueError("8-bit pools are [blocks, heads, 16, 64] with scales [blocks, heads]")
+    return kc, vc, ks, vs, shape
 
 
 def new_q8_cache(num_blocks, num_kv_heads, device=None):
@@ -465,14 +507,14 @@ def new_q8_cache(num_blocks, num_kv_heads, device=None):
     return (*pools, *scales)
 
 
-def _rope_append_args(q, key, value, cos_sin, key_cache, block_tables, context_lens,
-                      query_start_loc, q_out, interleaved):
-    hkv = key_cache.shape[1]
+def _rope_append_args(q, key, value, cos_sin, hkv, block_tables, context_lens, query_start_loc,
+                      q_out, interleaved):
     ks, vs = _need_rows(key, "key", hkv), _need_rows(value, "value", hkv)
     tokens = key.shape[0]
     if value.shape[0] != tokens:
         raise ValueError("key and value disagree on the token count")
     qs = os_ = hq = 0
+    q_ptr = out_ptr = table = starts = None
     if q is not None:
         qs = _need_rows(q, "q")
         hq = q.shape[1]
@@ -481,27 +523,27 @@ def _rope_append_args(q, key, value, cos_sin, key_cache, block_tables, context_l
         os_ = _need_rows(q_out, "q_out", hq)
         if q.shape[0] != tokens or q_out.shape[0] != tokens:
             raise ValueError("q, q_out and key disagree on the token count")
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
     positions = 0
     if cos_sin is not None:
-        _need(cos_sin, "cos_sin", torch.float32, 2)
-        if cos_sin.shape[1] != 64:
+        table = _check_tensor(cos_sin, "cos_sin", torch.float32, 2)
+        positions, width = cos_sin.shape
+        if width != 64:
             raise ValueError("cos_sin must be [positions, 64]: 32 cosines, then 32 sines")
-        positions = cos_sin.shape[0]
-    _need(block_tables, "block_tables", torch.int32, 2)
-    _need(context_lens, "context_lens", torch.int32, 1)
+    bt = _check_tensor(block_tables, "block_tables", torch.int32, 2)
+    ctx = _check_tensor(context_lens, "context_lens", torch.int32, 1)
+    rows, width = block_tables.shape
     seqs = context_lens.shape[0]
-    if block_tables.shape[0] != seqs:
+    if rows != seqs:
         raise ValueError("block_tables and context_lens disagree on the sequence count")
     if query_start_loc is not None:
-        _need(query_start_loc, "query_start_loc", torch.int32, 1)
+        starts = _check_tensor(query_start_loc, "query_start_loc", torch.int32, 1)
         if query_start_loc.shape[0] != seqs + 1:
             raise ValueError("query_start_loc must have one entry more than context_lens")
-    args = (_ptr(q), qs, _ptr(q_out), os_, hq, _ptr(key), ks, _ptr(value), vs, _ptr(cos_sin),
-            positions, int(bool(interleaved)), _ptr(block_tables), block_tables.shape[1],
-            _ptr(context_lens), _ptr(query_start_loc), seqs, tokens)
-    return q_out, args
+    return q_out, (q_ptr, qs, out_ptr, os_, hq, key.data_ptr(), ks, value.data_ptr(), vs, table,
+                   positions, 1 if interleaved else 0, bt, width, ctx, starts, seqs, tokens)
 
 
 def pa_rope_append(q, key, value, cos_sin, key_cache, value_cache, block_tables, context_lens,
@@ -510,15 +552,17 @@ def pa_rope_append(q, key, value, cos_sin, key_cache, value_cache, block_tables,
     """Rotate q [T, Hq, 64] and key [T, Hkv, 64] by their positions and store key and value into
     the bf16 pools; returns the rotated queries (q_out, which may be q; None without q).  The
     rows of a token must be contiguous, the tokens may be strided; see include/pagedkv.h."""
-    _need(key_cache, "key_cache", torch.bfloat16, 4)
-    _need(value_cache, "value_cache", torch.bfloat16, 4)
-    if key_cache.shape != value_cache.shape:
+    kc = _check_tensor(key_cache, "key_cache", torch.bfloat16, 4)
+    vc = _check_tensor(value_cache, "value_cache", torch.bfloat16, 4)
+    shape = key_cache.shape
+    if value_cache.shape != shape:
         raise ValueError("cache shapes differ")
-    q_out, args = _rope_append_args(q, key, value, cos_sin, key_cache, block_tables,
-                                    context_lens, query_start_loc, q_out, interleaved)
-    st = load().pa_rope_append(*args, _ptr(key_cache), _ptr(value_cache), cache_desc(key_cache),
-                               _ptr(device_status), _stream(stream))
-    _check(st, "pa_rope_append")
+    q_out, args = _rope_append_args(q, key, value, cos_sin, shape[1], block_tables, context_lens,
+                                    query_start_loc, q_out, interleaved)
+    st = (_lib or load()).pa_rope_append(*args, kc, vc, _kept_desc(shape),
+                                         _status_ptr(device_status), _current_stream(stream))
+    if st:
+        _check(st, "pa_rope_append")
     return q_out
 
 
@@ -527,13 +571,13 @@ def pa_rope_append_q8(q, key, value, cos_sin, key_cache, value_cache, key_scale,
                       interleaved=False, device_status=None, stream=None):
     """pa_rope_append into the 8-bit pools (e4m3 codes, one scale per block and head).  cos_sin
     None stores the keys as they are (q must be None then); see include/pagedkv.h."""
-    _need_q8(key_cache, value_cache, key_scale, value_scale)
-    q_out, args = _rope_append_args(q, key, value, cos_sin, key_cache, block_tables,
-                                    context_lens, query_start_loc, q_out, interleaved)
-    st = load().pa_rope_append_q8(*args, _ptr(key_cache), _ptr(value_cache), _ptr(key_scale),
-                                  _ptr(value_scale), cache_desc(key_cache), _ptr(device_status),
-                                  _stream(stream))
-    _check(st, "pa_rope_append_q8")
+    kc, vc, ks, vs, shape = _need_q8(key_cache, value_cache, key_scale, value_scale)
+    q_out, args = _rope_append_args(q, key, value, cos_sin, shape[1], block_tables, context_lens,
+                                    query_start_loc, q_out, interleaved)
+    st = (_lib or load()).pa_rope_append_q8(*args, kc, vc, ks, vs, _kept_desc(shape),
+                                            _status_ptr(device_status), _current_stream(stream))
+    if st:
+        _check(st, "pa_rope_append_q8")
     return q_out
 
 
@@ -547,26 +591,27 @@ def pa_decode_q8(out, q, key_cache, value_cache, key_scale, value_scale, block_t
                  stream=None, launch_flags=PA_LAUNCH_DEFAULT):
     """Paged decode attention over the 8-bit pools; writes out [S, Hq, D] (bf16).  launch_flags:
     those of pa_decode."""
-    _need(out, "out", torch.bfloat16, 3)
-    _need(q, "q", torch.bfloat16, 3)
-    _need_q8(key_cache, value_cache, key_scale, value_scale)
-    _need(block_tables, "block_tables", torch.int32, 2)
-    _need(context_lens, "context_lens", torch.int32, 1)
-    num_seqs, hq, d = q.shape
-    if out.shape != q.shape or d != key_cache.shape[3] or block_tables.shape[0] != num_seqs or \
+    op = _check_tensor(out, "out", torch.bfloat16, 3)
+    qp = _check_tensor(q, "q", torch.bfloat16, 3)
+    kc, vc, ks, vs, shape = _need_q8(key_cache, value_cache, key_scale, value_scale)
+    bt = _check_tensor(block_tables, "block_tables", torch.int32, 2)
+    ctx = _check_tensor(context_lens, "context_lens", torch.int32, 1)
+    q_shape = q.shape
+    num_seqs, hq, d = q_shape
+    rows, width = block_tables.shape
+    if out.shape != q_shape or d != shape[3] or rows != num_seqs or \
             context_lens.shape[0] != num_seqs:
         raise ValueError("q/out/block_tables/context_lens disagree on the sequence count")
     if workspace is None:
-        need = pa_decode_q8_workspace_size(num_seqs, key_cache.shape[1], hq, max_context_len)
+        need = pa_decode_q8_workspace_size(num_seqs, shape[1], hq, max_context_len)
         workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device)
-    _need(workspace, "workspace", torch.uint8, 1)
-    st = load().pa_decode_q8(_ptr(out), _ptr(q), _ptr(key_cache), _ptr(value_cache),
-                             _ptr(key_scale), _ptr(value_scale), cache_desc(key_cache),
-                             _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
-                             num_seqs, hq, float(scale), int(max_context_len), _ptr(workspace),
-                             workspace.numel(), int(launch_flags), _ptr(device_status),
-                             _stream(stream))
-    _check(st, "pa_decode_q8")
+    ws = _check_tensor(workspace, "workspace", torch.uint8, 1)
+    st = (_lib or load()).pa_decode_q8(
+        op, qp, kc, vc, ks, vs, _kept_desc(shape), bt, width, ctx, num_seqs, hq, scale,
+        max_context_len, ws, workspace.shape[0], launch_flags, _status_ptr(device_status),
+        _current_stream(stream))
+    if st:
+        _check(st, "pa_decode_q8")
     return out
 
 
@@ -574,22 +619,24 @@ def pa_prefill_chunk_q8(out, q, query_start_loc, max_query_len, key_cache, value
                         key_scale, value_scale, block_tables, context_lens, scale,
                         device_status=None, stream=None):
     """Causal chunked-prefill attention over the 8-bit pools; writes out [Tq, Hq, D] (bf16)."""
-    _need(out, "out", torch.bfloat16, 3)
-    _need(q, "q", torch.bfloat16, 3)
-    _need(query_start_loc, "query_start_loc", torch.int32, 1)
-    _need_q8(key_cache, value_cache, key_scale, value_scale)
-    _need(block_tables, "block_tables", torch.int32, 2)
-    _need(context_lens, "context_lens", torch.int32, 1)
+    op = _check_tensor(out, "out", torch.bfloat16, 3)
+    qp = _check_tensor(q, "q", torch.bfloat16, 3)
+    starts = _check_tensor(query_start_loc, "query_start_loc", torch.int32, 1)
+    kc, vc, ks, vs, shape = _need_q8(key_cache, value_cache, key_scale, value_scale)
+    bt = _check_tensor(block_tables, "block_tables", torch.int32, 2)
+    ctx = _check_tensor(context_lens, "context_lens", torch.int32, 1)
+    q_shape = q.shape
+    tokens, hq, d = q_shape
+    rows, width = block_tables.shape
     num_seqs = context_lens.shape[0]
-    if out.shape != q.shape or q.shape[2] != key_cache.shape[3] or \
-            query_start_loc.shape[0] != num_seqs + 1 or block_tables.shape[0] != num_seqs:
+    if out.shape != q_shape or d != shape[3] or query_start_loc.shape[0] != num_seqs + 1 or \
+            rows != num_seqs:
         raise ValueError("prefill argument shapes disagree")
-    st = load().pa_prefill_chunk_q8(
-        _ptr(out), _ptr(q), _ptr(query_start_loc), q.shape[0], int(max_query_len),
-        _ptr(key_cache), _ptr(value_cache), _ptr(key_scale), _ptr(value_scale),
-        cache_desc(key_cache), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
-        num_seqs, q.shape[1], float(scale), _ptr(device_status), _stream(stream))
-    _check(st, "pa_prefill_chunk_q8")
+    st = (_lib or load()).pa_prefill_chunk_q8(
+        op, qp, starts, tokens, max_query_len, kc, vc, ks, vs, _kept_desc(shape), bt, width, ctx,
+        num_seqs, hq, scale, _status_ptr(device_status), _current_stream(stream))
+    if st:
+        _check(st, "pa_prefill_chunk_q8")
     return out
 
 
@@ -597,14 +644,15 @@ def pa_copy_blocks_q8(key_cache, value_cache, key_scale, value_scale, block_mapp
                       device_status=None, stream=None):
     """Copy whole physical blocks of the 8-bit pools with their scales: block_mapping int64
     [n, 2] (src, dst)."""
-    _need_q8(key_cache, value_cache, key_scale, value_scale)
-    _need(block_mapping, "block_mapping", torch.int64, 2)
-    if block_mapping.shape[1] != 2:
+    kc, vc, ks, vs, shape = _need_q8(key_cache, value_cache, key_scale, value_scale)
+    pairs = _check_tensor(block_mapping, "block_mapping", torch.int64, 2)
+    n, two = block_mapping.shape
+    if two != 2:
         raise ValueError("block_mapping is not [n, 2]")
-    st = load().pa_copy_blocks_q8(_ptr(key_cache), _ptr(value_cache), _ptr(key_scale),
-                                  _ptr(value_scale), cache_desc(key_cache), _ptr(block_mapping),
-                                  block_mapping.shape[0], _ptr(device_status), _stream(stream))
-    _check(st, "pa_copy_blocks_q8")
+    st = (_lib or load()).pa_copy_blocks_q8(kc, vc, ks, vs, _kept_desc(shape), pairs, n,
+                                            _status_ptr(device_status), _current_stream(stream))
+    if st:
+        _check(st, "pa_copy_blocks_q8")
 
 
 class BlockManager:
