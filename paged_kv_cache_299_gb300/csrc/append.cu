@@ -7,8 +7,9 @@
 //   (a cos - b sin, b cos + a sin),   cos = table[p][i], sin = table[p][32 + i],
 // evaluated in fp32 and rounded once to what is stored (bf16, or a code of the 8-bit pools).
 //
-// Memory-bound: every row is read once and written once.  Eight lanes carry one head row (16
-// bytes each); the partner dims of the (i, i + 32) form sit four lanes away.
+// Memory-bound: every row is read once and written once.  Four lanes carry one head row, each
+// both members of eight pairs, so a row's rotation needs no exchange and a lane's cosines and
+// sines serve all the heads of its token.
 #include <math.h>
 
 #include "common.cuh"
@@ -21,10 +22,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarpsPerCta = kThreads / 32;
-constexpr int kChunkDims = 8;                       // dims per lane (16 bytes of bf16)
-constexpr int kLanesPerRow = kHeadDim / kChunkDims;  // 8
-constexpr int kRowsPerWarp = 32 / kLanesPerRow;     // 4 head rows side by side
 constexpr int kPairs = kHeadDim / 2;
+constexpr int kLanePairs = 8;                     // rotation pairs per lane: 16 dims, 32 bytes
+constexpr int kLanesPerRow = kPairs / kLanePairs;  // 4
+constexpr int kRowsPerWarp = 32 / kLanesPerRow;   // 8 head rows side by side
+constexpr int kUnroll = 3;  // rows a lane has in flight: 48 rows (32 + 2 x 8 heads) in two rounds
 
 // Sequence of token t (the last s with query_start_loc[s] <= t; without query_start_loc,
 // sequence t) and its logical position.  false: the token is padding (at or past
@@ -60,50 +62,48 @@ __device__ __forceinline__ bool locate(const AppendArgs& a, int32_t t, bool repo
   return true;
 }
 
-// The cosines and (signed) sines a lane applies to its eight dims, y = own * c + other * s:
-// kInterleaved: four pairs, c[i] / s[i] of pair 4 * lane + i.  Otherwise eight, those of dims
-// 8 * (lane & 3) .. + 7, the sines negated in the first half of the row.
+// A lane's 16 dims of a head row: both members of pairs 8 l .. 8 l + 7 (l = lane % 4), so no
+// value has to travel between lanes.  kInterleaved: dims 16 l .. 16 l + 15; otherwise dims 8 l
+// .. 8 l + 7 and 32 + 8 l .. 32 + 8 l + 7.  first / second: byte offsets / 16 of its two chunks.
+template <bool kInterleaved>
+__device__ __forceinline__ int first_chunk(int l) { return kInterleaved ? 2 * l : l; }
+template <bool kInterleaved>
+__device__ __forceinline__ int second_chunk(int l) { return kInterleaved ? 2 * l + 1 : 4 + l; }
+
 struct Angles {
-  float c[kChunkDims], s[kChunkDims];
+  float c[kLanePairs], s[kLanePairs];
 };
 
-template <bool kInterleaved>
-__device__ __forceinline__ void load_angles(const float* __restrict__ row, int chunk, Angles& g) {
-  if (kInterleaved) {
-    const float4 c = __ldg(reinterpret_cast<const float4*>(row + 4 * chunk));
-    const float4 s = __ldg(reinterpret_cast<const float4*>(row + kPairs + 4 * chunk));
-    g.c[0] = c.x; g.c[1] = c.y; g.c[2] = c.z; g.c[3] = c.w;
-    g.s[0] = s.x; g.s[1] = s.y; g.s[2] = s.z; g.s[3] = s.w;
-  } else {
-    const int i0 = kChunkDims * (chunk & 3);
-    const float sign = chunk < 4 ? -1.f : 1.f;
+__device__ __forceinline__ void load_angles(const float* __restrict__ row, int l, Angles& g) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(row + i0 + 4 * h));
-      const float4 s = __ldg(reinterpret_cast<const float4*>(row + kPairs + i0 + 4 * h));
-      g.c[4 * h] = c.x; g.c[4 * h + 1] = c.y; g.c[4 * h + 2] = c.z; g.c[4 * h + 3] = c.w;
-      g.s[4 * h] = sign * s.x; g.s[4 * h + 1] = sign * s.y;
-      g.s[4 * h + 2] = sign * s.z; g.s[4 * h + 3] = sign * s.w;
-    }
+  for (int h = 0; h < 2; ++h) {
+    const float4 c = __ldg(reinterpret_cast<const float4*>(row + kLanePairs * l + 4 * h));
+    const float4 s = __ldg(reinterpret_cast<const float4*>(row + kPairs + kLanePairs * l + 4 * h));
+    g.c[4 * h] = c.x; g.c[4 * h + 1] = c.y; g.c[4 * h + 2] = c.z; g.c[4 * h + 3] = c.w;
+    g.s[4 * h] = s.x; g.s[4 * h + 1] = s.y; g.s[4 * h + 2] = s.z; g.s[4 * h + 3] = s.w;
   }
 }
 
-// Eight dims of a row, rotated, in fp32.  All 32 lanes take part (the partner dims travel by
-// shuffles); x is this lane's 16 bytes.
-template <bool kInterleaved>
-__device__ __forceinline__ void rotate8(const uint4 x, const Angles& g, float (&y)[kChunkDims]) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+// The lane's 16 dims in fp32: y[0..7] its first chunk, y[8..15] its second.
+__device__ __forceinline__ void unpack16(const uint4& a, const uint4& b, float (&y)[16]) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; ++i) {
     const float2 v = bf16x2_to_float2(w[i]);
-    if (kInterleaved) {
-      y[2 * i] = v.x * g.c[i] - v.y * g.s[i];
-      y[2 * i + 1] = v.y * g.c[i] + v.x * g.s[i];
-    } else {
-      const float2 o = bf16x2_to_float2(__shfl_xor_sync(0xffffffffu, w[i], 4));
-      y[2 * i] = v.x * g.c[2 * i] + o.x * g.s[2 * i];
-      y[2 * i + 1] = v.y * g.c[2 * i + 1] + o.y * g.s[2 * i + 1];
-    }
+    y[2 * i] = v.x;
+    y[2 * i + 1] = v.y;
+  }
+}
+
+template <bool kInterleaved>
+__device__ __forceinline__ void rotate16(const Angles& g, float (&y)[16]) {
+#pragma unroll
+  for (int i = 0; i < kLanePairs; ++i) {
+    float& a = y[kInterleaved ? 2 * i : i];
+    float& b = y[kInterleaved ? 2 * i + 1 : 8 + i];
+    const float x = a;
+    a = x * g.c[i] - b * g.s[i];
+    b = b * g.c[i] + x * g.s[i];
   }
 }
 
@@ -111,18 +111,22 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ uint4 pack8(const float (&y)[kChunkDims]) {
+__device__ __forceinline__ uint4 pack8(const float* y) {
   return make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
 }
 
-// One warp serves rows part, part + parts, ... (four at a time) of token t: its query rows,
-// then, with kStore, its key and its value rows.
+// One warp serves rows part, part + parts, ... (eight at a time) of token t: its query rows,
+// then, with kStore, its key and its value rows.  kUnroll rows a lane are loaded before the
+// first is written.
 template <bool kInterleaved, bool kStore>
 __device__ void token_rows(const AppendArgs& a, int32_t t, int part, int parts, int lane) {
   int32_t seq;
   int64_t pos;
   if (!locate(a, t, part == 0 && lane == 0, &seq, &pos)) return;
-  const int chunk = lane % kLanesPerRow;
+  const int l = lane % kLanesPerRow;
+  const int c0 = first_chunk<kInterleaved>(l), c1 = second_chunk<kInterleaved>(l);
+  Angles g;
+  load_angles(a.cos_sin + pos * kHeadDim, l, g);
   int64_t tile0 = 0;  // first (block, head) tile of the token's block
   if (kStore) {
     const int32_t phys =
@@ -133,37 +137,47 @@ __device__ void token_rows(const AppendArgs& a, int32_t t, int part, int parts, 
     }
     tile0 = static_cast<int64_t>(phys) * a.num_kv_heads;
   }
-  Angles g;
-  load_angles<kInterleaved>(a.cos_sin + pos * kHeadDim, chunk, g);
   const int hq = a.num_q_heads, hkv = a.num_kv_heads;
   const int rows = kStore ? hq + 2 * hkv : hq;
-  for (int r0 = part * kRowsPerWarp; r0 < rows; r0 += parts * kRowsPerWarp) {
-    const int r = r0 + lane / kLanesPerRow;
-    const bool valid = r < rows;
-    const __nv_bfloat16* src = nullptr;
-    __nv_bfloat16* dst = nullptr;
-    bool turn = true;
-    if (valid) {
-      if (r < hq) {
-        src = static_cast<const __nv_bfloat16*>(a.q) + t * a.q_stride + r * kHeadDim;
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + t * a.q_stride;
+  const __nv_bfloat16* key = static_cast<const __nv_bfloat16*>(a.key) + t * a.key_stride;
+  const __nv_bfloat16* value = static_cast<const __nv_bfloat16*>(a.value) + t * a.value_stride;
+  const int step = parts * kRowsPerWarp;
+  for (int r0 = part * kRowsPerWarp + lane / kLanesPerRow; r0 < rows; r0 += kUnroll * step) {
+    uint4 x[kUnroll][2];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int r = r0 + u * step;
+      if (r >= rows) continue;
+      const __nv_bfloat16* src = q + r * kHeadDim;
+      if (kStore && r >= hq) src = r < hq + hkv ? key + (r - hq) * kHeadDim : value + (r - hq - hkv) * kHeadDim;
+      // plain loads: q_out may be q itself
+      x[u][0] = reinterpret_cast<const uint4*>(src)[c0];
+      x[u][1] = reinterpret_cast<const uint4*>(src)[c1];
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int r = r0 + u * step;
+      if (r >= rows) continue;
+      __nv_bfloat16* dst;
+      if (!kStore || r < hq) {
         dst = static_cast<__nv_bfloat16*>(a.q_out) + t * a.q_out_stride + r * kHeadDim;
       } else {
         const bool is_k = r < hq + hkv;
         const int h = r - hq - (is_k ? 0 : hkv);
-        src = is_k ? static_cast<const __nv_bfloat16*>(a.key) + t * a.key_stride
-                   : static_cast<const __nv_bfloat16*>(a.value) + t * a.value_stride;
-        src += h * kHeadDim;
         dst = static_cast<__nv_bfloat16*>(is_k ? a.key_cache : a.value_cache) +
               ((tile0 + h) * kBlockSize + pos % kBlockSize) * kHeadDim;
-        turn = is_k;
       }
+      if (!kStore || r < hq + hkv) {
+        float y[16];
+        unpack16(x[u][0], x[u][1], y);
+        rotate16<kInterleaved>(g, y);
+        x[u][0] = pack8(y);
+        x[u][1] = pack8(y + 8);
+      }
+      reinterpret_cast<uint4*>(dst)[c0] = x[u][0];
+      reinterpret_cast<uint4*>(dst)[c1] = x[u][1];
     }
-    // plain loads: q_out may be q itself
-    uint4 x = valid ? reinterpret_cast<const uint4*>(src)[chunk] : make_uint4(0, 0, 0, 0);
-    float y[kChunkDims];
-    rotate8<kInterleaved>(x, g, y);
-    if (turn) x = pack8(y);
-    if (valid) reinterpret_cast<uint4*>(dst)[chunk] = x;
   }
 }
 
@@ -183,11 +197,11 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// Largest finite magnitude of eight values; *bad is set where one is not finite.
-__device__ __forceinline__ float amax8(const float (&y)[kChunkDims], bool* bad) {
+// Largest finite magnitude of sixteen values; *bad is set where one is not finite.
+__device__ __forceinline__ float amax16(const float (&y)[16], bool* bad) {
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < kChunkDims; ++i) {
+  for (int i = 0; i < 16; ++i) {
     const float v = fabsf(y[i]);
     if (v < INFINITY) m = fmaxf(m, v); else *bad = true;
   }
@@ -195,7 +209,7 @@ __device__ __forceinline__ float amax8(const float (&y)[kChunkDims], bool* bad) 
 }
 
 // Eight values -> eight codes of y * inv; NaN becomes 0, infinities saturate.
-__device__ __forceinline__ uint2 codes8(const float (&y)[kChunkDims], float inv) {
+__device__ __forceinline__ uint2 codes8(const float* y, float inv) {
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -211,7 +225,7 @@ __device__ __forceinline__ uint2 codes8(const float (&y)[kChunkDims], float inv)
   return make_uint2(w[0], w[1]);
 }
 
-constexpr int kRowSteps = kBlockSize / kRowsPerWarp;  // 4 rows of the block per lane
+constexpr int kRowSteps = kBlockSize / kRowsPerWarp;  // 2 rows of the block per lane
 
 // Scale of a block that receives new values of largest magnitude amax, and the rescaling of
 // the codes it holds already (rows 0 .. o0-1).  A block whose first token is written now
@@ -227,19 +241,19 @@ __device__ __forceinline__ float settle_scale(float old, uint8_t* tile, float am
       for (int k = 0; k < kRowSteps; ++k) {
         const int row = k * kRowsPerWarp + lane / kLanesPerRow;
         if (row >= o0) continue;
-        uint2* p = reinterpret_cast<uint2*>(tile + row * kQ8RowBytes) + lane % kLanesPerRow;
-        const uint2 c = *p;
-        const uint32_t in[2] = {c.x, c.y};
-        uint32_t out[2];
+        uint4* p = reinterpret_cast<uint4*>(tile + row * kQ8RowBytes) + lane % kLanesPerRow;
+        const uint4 c = *p;
+        const uint32_t in[4] = {c.x, c.y, c.z, c.w};
+        uint32_t out[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 4; ++h) {
           uint32_t lo, hi;
           codes4_to_half2x2(in[h], lo, hi);
           const float2 a = half2_to_float2(lo), b = half2_to_float2(hi);
           out[h] = floats_to_codes2(a.x * ratio, a.y * ratio) |
                    (static_cast<uint32_t>(floats_to_codes2(b.x * ratio, b.y * ratio)) << 16);
         }
-        *p = make_uint2(out[0], out[1]);
+        *p = make_uint4(out[0], out[1], out[2], out[3]);
       }
     } else {
       s = old;
@@ -248,12 +262,14 @@ __device__ __forceinline__ float settle_scale(float old, uint8_t* tile, float am
   return s;
 }
 
-// One warp serves one (sequence, block it appends to, K/V head): it holds the block's new
-// rows of K and V (at most 16 each) in registers, finds their largest magnitudes, settles
-// the two scales and writes codes.  The tokens of a block are all this warp's, so nothing is
-// shared between warps and results do not depend on any order.
+// One warp serves one (sequence, block it appends to, K/V head, pool): it holds the block's
+// new rows (at most 16) in registers, finds their largest magnitude, settles the scale and
+// writes codes.  The tokens of a block are all this warp's, so nothing is shared between warps
+// and results do not depend on any order.
 template <bool kRotate, bool kInterleaved>
 __device__ void block_rows(const AppendArgs& a, int64_t item, int lane) {
+  const bool is_k = (item & 1) == 0;
+  item >>= 1;
   const int head = static_cast<int>(item % a.num_kv_heads);
   const int64_t v = item / a.num_kv_heads;
   int32_t s;
@@ -281,7 +297,7 @@ __device__ void block_rows(const AppendArgs& a, int64_t item, int lane) {
   }
   const int64_t ctx = a.context_lens[s];
   const int64_t p0 = ctx - q_len;  // position of the first new token
-  const bool tell = lane == 0 && head == 0 && index == 0;
+  const bool tell = lane == 0 && head == 0 && index == 0 && is_k;
   if (first < 0 || static_cast<int64_t>(first) + q_len > a.num_tokens || p0 < 0 ||
       ctx > static_cast<int64_t>(a.max_blocks_per_seq) * kBlockSize ||
       (kRotate && ctx > a.max_positions)) {
@@ -294,89 +310,65 @@ __device__ void block_rows(const AppendArgs& a, int64_t item, int lane) {
   const int o1 = static_cast<int>(ctx - b * kBlockSize < kBlockSize ? ctx - b * kBlockSize : kBlockSize);
   const int32_t phys = a.block_tables[static_cast<int64_t>(s) * a.max_blocks_per_seq + b];
   if (phys < 0 || phys >= a.num_blocks) {
-    if (lane == 0 && head == 0) flag_error(a.status, PA_DEVFLAG_BAD_BLOCK);
+    if (lane == 0 && head == 0 && is_k) flag_error(a.status, PA_DEVFLAG_BAD_BLOCK);
     return;
   }
   const int64_t tile = static_cast<int64_t>(phys) * a.num_kv_heads + head;
-  const int chunk = lane % kLanesPerRow;
+  const int l = lane % kLanesPerRow;
+  const int c0 = first_chunk<kInterleaved>(l), c1 = second_chunk<kInterleaved>(l);
   const int64_t t0 = first + (b * kBlockSize - p0);  // token of row 0 (may precede the chunk)
-  const float k_old = a.key_scale[tile], v_old = a.value_scale[tile];
-  uint4 kx[kRowSteps], vx[kRowSteps];
+  float* const scale = (is_k ? a.key_scale : a.value_scale) + tile;
+  uint8_t* const codes = static_cast<uint8_t*>(is_k ? a.key_cache : a.value_cache) + tile * kQ8TileBytes;
+  const __nv_bfloat16* const src = static_cast<const __nv_bfloat16*>(is_k ? a.key : a.value) + head * kHeadDim;
+  const int64_t stride = is_k ? a.key_stride : a.value_stride;
+  const float old = *scale;
+  uint4 x[kRowSteps][2];
 #pragma unroll
   for (int k = 0; k < kRowSteps; ++k) {
     const int row = k * kRowsPerWarp + lane / kLanesPerRow;
-    const bool valid = row >= o0 && row < o1;
-    kx[k] = vx[k] = make_uint4(0, 0, 0, 0);
-    if (valid) {
-      kx[k] = ldg_nc128(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.key) +
-                                                       (t0 + row) * a.key_stride + head * kHeadDim) + chunk);
-      vx[k] = ldg_nc128(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.value) +
-                                                       (t0 + row) * a.value_stride + head * kHeadDim) + chunk);
+    x[k][0] = x[k][1] = make_uint4(0, 0, 0, 0);
+    if (row >= o0 && row < o1) {
+      const uint4* p = reinterpret_cast<const uint4*>(src + (t0 + row) * stride);
+      x[k][0] = ldg_nc128(p + c0);
+      x[k][1] = ldg_nc128(p + c1);
     }
   }
-  float ky[kRowSteps][kChunkDims];
-  float kmax = 0.f, vmax = 0.f;
+  float y[kRowSteps][16];
+  float amax = 0.f;
   bool bad = false;
 #pragma unroll
   for (int k = 0; k < kRowSteps; ++k) {
     const int row = k * kRowsPerWarp + lane / kLanesPerRow;
-    if (kRotate) {
-      const bool valid = row >= o0 && row < o1;
-      Angles g = {};
-      if (valid) load_angles<kInterleaved>(a.cos_sin + (b * kBlockSize + row) * kHeadDim, chunk, g);
-      rotate8<kInterleaved>(kx[k], g, ky[k]);
-    } else {
-      const uint32_t w[4] = {kx[k].x, kx[k].y, kx[k].z, kx[k].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = bf16x2_to_float2(w[i]);
-        ky[k][2 * i] = f.x;
-        ky[k][2 * i + 1] = f.y;
-      }
-    }
-    kmax = fmaxf(kmax, amax8(ky[k], &bad));
-    float vy[kChunkDims];
-    const uint32_t w[4] = {vx[k].x, vx[k].y, vx[k].z, vx[k].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = bf16x2_to_float2(w[i]);
-      vy[2 * i] = f.x;
-      vy[2 * i + 1] = f.y;
-    }
-    vmax = fmaxf(vmax, amax8(vy, &bad));
+    Angles g = {};
+    const bool turn = kRotate && is_k && row >= o0 && row < o1;
+    if (turn) load_angles(a.cos_sin + (b * kBlockSize + row) * kHeadDim, l, g);
+    unpack16(x[k][0], x[k][1], y[k]);
+    if (turn) rotate16<kInterleaved>(g, y[k]);
+    amax = fmaxf(amax, amax16(y[k], &bad));
   }
-  kmax = warp_max(kmax);
-  vmax = warp_max(vmax);
+  amax = warp_max(amax);
   if (__any_sync(0xffffffffu, bad) && lane == 0) flag_error(a.status, PA_DEVFLAG_NONFINITE);
-  uint8_t* kt = static_cast<uint8_t*>(a.key_cache) + tile * kQ8TileBytes;
-  uint8_t* vt = static_cast<uint8_t*>(a.value_cache) + tile * kQ8TileBytes;
-  if (o0 > 0 && !(scale_ok(k_old) && scale_ok(v_old))) {
+  if (o0 > 0 && !scale_ok(old)) {
     if (lane == 0) flag_error(a.status, PA_DEVFLAG_BAD_SCALE);
     return;
   }
-  const float ks = settle_scale(k_old, kt, kmax, o0, lane);
-  const float vs = settle_scale(v_old, vt, vmax, o0, lane);
-  const float ki = 1.f / ks, vi = 1.f / vs;
+  const float now = settle_scale(old, codes, amax, o0, lane);
+  const float inv = 1.f / now;
 #pragma unroll
   for (int k = 0; k < kRowSteps; ++k) {
     const int row = k * kRowsPerWarp + lane / kLanesPerRow;
     if (row < o0 || row >= o1) continue;
-    float vy[kChunkDims];
-    const uint32_t w[4] = {vx[k].x, vx[k].y, vx[k].z, vx[k].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = bf16x2_to_float2(w[i]);
-      vy[2 * i] = f.x;
-      vy[2 * i + 1] = f.y;
+    const uint2 w0 = codes8(y[k], inv), w1 = codes8(y[k] + 8, inv);
+    uint2* dst = reinterpret_cast<uint2*>(codes + row * kQ8RowBytes);
+    if (kInterleaved) {
+      reinterpret_cast<uint4*>(dst)[l] = make_uint4(w0.x, w0.y, w1.x, w1.y);
+    } else {
+      dst[c0] = w0;
+      dst[c1] = w1;
     }
-    reinterpret_cast<uint2*>(kt + row * kQ8RowBytes)[chunk] = codes8(ky[k], ki);
-    reinterpret_cast<uint2*>(vt + row * kQ8RowBytes)[chunk] = codes8(vy, vi);
   }
-  __syncwarp();  // every lane has read the old scales
-  if (lane == 0) {
-    a.key_scale[tile] = ks;
-    a.value_scale[tile] = vs;
-  }
+  __syncwarp();  // every lane has read the old scale
+  if (lane == 0) *scale = now;
 }
 
 // Warps 0 .. items-1 serve the blocks, the rest the query rows.
@@ -422,7 +414,7 @@ cudaError_t launch_rope_append_q8(const AppendArgs& a, cudaStream_t stream) {
   const int64_t blocks = a.query_start_loc == nullptr
                              ? a.num_seqs
                              : (static_cast<int64_t>(a.num_tokens) >> 4) + 2ll * a.num_seqs;
-  const int64_t items = blocks * a.num_kv_heads;
+  const int64_t items = blocks * a.num_kv_heads * 2;  // K and V
   const int64_t item_ctas = (items + kWarpsPerCta - 1) / kWarpsPerCta;
   int parts = 1;
   int64_t q_ctas = 0;
