@@ -226,7 +226,7 @@ __device__ __forceinline__ float2 ld_partial2(const float2* a) {
   return kLocal ? *a : __ldcg(a);
 }
 
-template <int GROUP, bool kLocal, bool kRows>
+template <int GROUP, bool kLocal, bool kRows, int UNROLL = 4>
 __device__ void merge_segment_in_warp(const KParams& p, const SegmentPieces& sp, int64_t x0,
                                       int64_t x1, int64_t total, int s, int g, int lane) {
   const int n = segment_piece_count(sp, x0, x1, total, p.grid);
@@ -317,13 +317,13 @@ __device__ void merge_segment_in_warp(const KParams& p, const SegmentPieces& sp,
       acc[h].y *= keep;
       M[h] = nm;
     }
-    // output slices: 4 pieces x GROUP heads of loads in flight per round
+    // output slices: UNROLL pieces x GROUP heads of loads in flight per round
     const int cnt = min(32, n - base);
-    for (int j0 = 0; j0 < cnt; j0 += 4) {
-      float2 v[4][GROUP];
-      float w[4][GROUP];
+    for (int j0 = 0; j0 < cnt; j0 += UNROLL) {
+      float2 v[UNROLL][GROUP];
+      float w[UNROLL][GROUP];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < UNROLL; ++u) {
         const int j = j0 + u < cnt ? j0 + u : j0;  // clamp; weight zeroed below
         const float* rj = reinterpret_cast<const float*>(
             __shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(rec), j));
@@ -335,7 +335,7 @@ __device__ void merge_segment_in_warp(const KParams& p, const SegmentPieces& sp,
         }
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < UNROLL; ++u) {
 #pragma unroll
         for (int h = 0; h < GROUP; ++h) {
           acc[h].x += w[u][h] * v[u][h].x;
@@ -354,6 +354,15 @@ __device__ void merge_segment_in_warp(const KParams& p, const SegmentPieces& sp,
   }
 }
 
+// Splits weighted by segment: every (sequence, kv head) segment counts EXTRA units on top of its
+// tiles (what starting and publishing a piece costs, in tiles), EXTRA also where it has none,
+// and the runs divide the units evenly.  Units of sequence s start at unit_base(s), those of its
+// segment g at + g (nb + EXTRA), its tiles' at + EXTRA.
+template <int EXTRA>
+__device__ __forceinline__ int64_t unit_base(const int32_t* base, int s, int kv) {
+  return static_cast<int64_t>(kv) * (static_cast<int64_t>(base[s]) + static_cast<int64_t>(EXTRA) * s);
+}
+
 // Combines the partials of every (sequence, kv head) whose tiles were split across CTAs,
 // and writes zero rows for empty contexts.  One CTA per (sequence, kv head, HPC of the
 // head's GROUP query heads): HPC = GROUP when segments have few pieces, 1 when they have
@@ -361,7 +370,7 @@ __device__ void merge_segment_in_warp(const KParams& p, const SegmentPieces& sp,
 // its partials into a running (maximum, sum, o) per query head, rescaling by the
 // log-sum-exp weights as the maximum grows, with U partials' loads in flight per round;
 // the warps' states are then combined the same way.
-template <int GROUP, int HPC, bool kRows>
+template <int GROUP, int HPC, bool kRows, int EXTRA>
 __global__ void __launch_bounds__(kMergeThreads)
 merge_partials_kernel(const KParams p) {
   constexpr int kWarps = kMergeThreads / 32;
@@ -389,7 +398,8 @@ merge_partials_kernel(const KParams p) {
     return;
   }
   const int64_t total = *p.ws_total;
-  const int64_t x0 = static_cast<int64_t>(base) * KV + static_cast<int64_t>(g) * nb;
+  const int64_t x0 = static_cast<int64_t>(KV) * (base + static_cast<int64_t>(EXTRA) * s) +
+                     static_cast<int64_t>(g) * (nb + EXTRA) + EXTRA;
   const int64_t x1 = x0 + nb;
   const int64_t c_first = run_of(x0, total, p.grid, p.chunk);
   const int64_t c_last = run_of(x1 - 1, total, p.grid, p.chunk);
@@ -399,7 +409,8 @@ merge_partials_kernel(const KParams p) {
   }
   if (c_first == c_last) return;  // written directly by the attention kernel
   const int n = static_cast<int>(c_last - c_first + 1);
-  const int first_slot = x0 == run_start(c_first, total, p.grid, p.chunk) ? 0 : 1;
+  int first_slot = x0 == run_start(c_first, total, p.grid, p.chunk) ? 0 : 1;
+  if (EXTRA > 0) first_slot = 1;  // the weighted kernel's rule
 
   auto record = [&](int k, int h) -> const float* {
     const int64_t c = c_first + k;
@@ -493,20 +504,20 @@ merge_partials_kernel(const KParams p) {
 }
 
 // The merge kernel behind an attention launch that left its split segments' partials.
-template <int GROUP>
+template <int GROUP, int EXTRA = 0>
 cudaError_t launch_merge(const KParams& p, const DecodePlan& plan, bool rows, cudaStream_t stream) {
   if (plan.merge_split_heads && GROUP > 1) {  // one CTA per query head
     const dim3 mgrid(p.num_kv_heads * GROUP, p.num_seqs);
     if (rows)
-      merge_partials_kernel<GROUP, 1, true><<<mgrid, kMergeThreads, 0, stream>>>(p);
+      merge_partials_kernel<GROUP, 1, true, EXTRA><<<mgrid, kMergeThreads, 0, stream>>>(p);
     else
-      merge_partials_kernel<GROUP, 1, false><<<mgrid, kMergeThreads, 0, stream>>>(p);
+      merge_partials_kernel<GROUP, 1, false, EXTRA><<<mgrid, kMergeThreads, 0, stream>>>(p);
   } else {  // one CTA per kv head
     const dim3 mgrid(p.num_kv_heads, p.num_seqs);
     if (rows)
-      merge_partials_kernel<GROUP, GROUP, true><<<mgrid, kMergeThreads, 0, stream>>>(p);
+      merge_partials_kernel<GROUP, GROUP, true, EXTRA><<<mgrid, kMergeThreads, 0, stream>>>(p);
     else
-      merge_partials_kernel<GROUP, GROUP, false><<<mgrid, kMergeThreads, 0, stream>>>(p);
+      merge_partials_kernel<GROUP, GROUP, false, EXTRA><<<mgrid, kMergeThreads, 0, stream>>>(p);
   }
   return cudaGetLastError();
 }

@@ -42,7 +42,9 @@ constexpr int kStageBytes = 2 * kQ8TileBytes;
 constexpr int kWindow = 32;  // tiles whose block ids and scales are held in the lanes
 constexpr int kMinTilesPerRun = 2;
 constexpr int kOneSeqMaxTilesPerWarp = 4;     // one sequence up to this: one CTA per head
-constexpr int kFusedMergeMaxContext = 8192;   // longer ones merge in the parallel merge kernel
+constexpr int kFusedMergeMaxContext = 8192;   // longer ones merge in the parallel merge kernel,
+constexpr int kFusedMergeMaxPieces = 24;      // as do segments of more pieces than this
+constexpr int kSegmentUnits = 2;  // what a piece costs besides its tiles, in tiles
 constexpr float kPShift = 7.f;                // log2 of the factor on p
 constexpr int kQExp = 13;                     // exponent of a row's largest f16 query element
 constexpr int kPrefetchTiles = 8;
@@ -193,9 +195,49 @@ __device__ __forceinline__ void attend_pair(const uint8_t* ta, const uint8_t* tb
   }
 }
 
+// Publishes a piece whose partial this warp has written; the warp that publishes the segment's
+// last piece merges them all, with CTA-scope ordering when they all ran on this CTA.  Not
+// inlined: the tile loop's registers are allocated without it.
+template <int GROUP>
+__device__ __forceinline__ void publish_piece(const KParams& p, const int32_t* seq_base,
+                                           int* cta_seg_count, int s, int g, int nb, int64_t units,
+                                           int lane) {
+  const int KV = p.num_kv_heads;
+  const int64_t x0 = unit_base<kSegmentUnits>(seq_base, s, KV) +
+                     static_cast<int64_t>(g) * (nb + kSegmentUnits) + kSegmentUnits;
+  const int64_t x1 = x0 + nb;  // units of the segment's tiles
+  SegmentPieces sp;
+  sp.c_first = run_of(x0, units, p.grid, 0);
+  sp.c_last = run_of(x1 - 1, units, p.grid, 0);
+  sp.first_slot = 1;  // as its writer chose
+  const int n = segment_piece_count(sp, x0, x1, units, p.grid);
+  int last = 0;
+  if (sp.c_first / kWarps == sp.c_last / kWarps) {
+    int* count = &cta_seg_count[sp.c_first % kWarps];
+    __threadfence_block();
+    __syncwarp();
+    if (lane == 0) last = atomicAdd(count, 1) == n - 1;
+    if (__shfl_sync(0xffffffffu, last, 0)) {
+      __threadfence_block();
+      merge_segment_in_warp<GROUP, true, false, 4>(p, sp, x0, x1, units, s, g, lane);
+      if (lane == 0) *count = 0;
+    }
+  } else {
+    int32_t* count = &p.seg_count[s * KV + g];
+    __threadfence();
+    __syncwarp();
+    if (lane == 0) last = atomicAdd(count, 1) == n - 1;
+    if (__shfl_sync(0xffffffffu, last, 0)) {
+      __threadfence();
+      merge_segment_in_warp<GROUP, false, false, 4>(p, sp, x0, x1, units, s, g, lane);
+      if (lane == 0) *count = 0;  // ready for the next call
+    }
+  }
+}
+
 template <int GROUP>
 __global__ void __launch_bounds__(kWarps * 32, 1)
-paged_decode_q8_kernel(const KParams p, const Q8Params sp8) {
+paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
   constexpr int kThreads = kWarps * 32;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ __align__(128) uint8_t smem[];
@@ -235,9 +277,47 @@ paged_decode_q8_kernel(const KParams p, const Q8Params sp8) {
   const uint64_t policy = l2_evict_first_policy();
   const int r = lane >> 2;
   const int q = lane & 3;
-  // (block_prefix keeps the tile count below 2^31)
-  const int start = static_cast<int>(run_start(gw, total, p.grid, 0));
-  const int stop = static_cast<int>(run_start(gw + 1, total, p.grid, 0));
+  // The run's tiles: lane 0 locates its first unit, lane 1 the next run's, in one search.
+  // (block_prefix keeps the tile count below 2^31, so units fit 32 unsigned bits.)
+  const int64_t units = unit_base<kSegmentUnits>(seq_base, S, KV);
+  int start, stop;
+  int wc_s, wc_off;  // sequence of tile wc_y and its place among the sequence's KV x nb tiles
+  {
+    const uint32_t u32 = static_cast<uint32_t>(units), n = static_cast<uint32_t>(p.grid);
+    const uint32_t c = static_cast<uint32_t>(gw + (lane & 1));
+    const uint32_t each = u32 / n;
+    // c * units / n without 64 bits (n stays below 2^16)
+    const uint32_t y = c * each + c * (u32 - each * n) / n;
+    int lo = 0, hi = S - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (static_cast<uint32_t>(KV * (seq_base[mid] + kSegmentUnits * mid)) <= y) lo = mid; else hi = mid - 1;
+    }
+    const int nb = seq_base[lo + 1] - seq_base[lo];
+    const int off = static_cast<int>(y - static_cast<uint32_t>(KV * (seq_base[lo] + kSegmentUnits * lo)));
+    int g = off / (nb + kSegmentUnits);
+    int place = g * nb + max(0, off - g * (nb + kSegmentUnits) - kSegmentUnits);
+    if (g >= KV) place = KV * nb;  // past the last unit
+    const int t = seq_base[lo] * KV + place;
+    start = __shfl_sync(0xffffffffu, t, 0);
+    stop = __shfl_sync(0xffffffffu, t, 1);
+    wc_s = __shfl_sync(0xffffffffu, lo, 0);
+    wc_off = __shfl_sync(0xffffffffu, place, 0);
+  }
+  // past the end of its sequence, a place moves to the next one that has tiles
+  auto settle = [&](int& s, int& off) {
+    while (s + 1 < S && off >= (seq_base[s + 1] - seq_base[s]) * KV) {
+      off = 0;
+      ++s;
+    }
+  };
+  settle(wc_s, wc_off);
+  Piece nx;  // the first piece
+  nx.s = wc_s;
+  nx.nb = max(1, seq_base[wc_s + 1] - seq_base[wc_s]);
+  nx.g = wc_off / nx.nb;
+  nx.b0 = wc_off - nx.g * nx.nb;
+  nx.b1 = min(nx.nb, nx.b0 + stop - start);
 
   // ---- issue side: windows of 32 tiles of the run ----
   int wc_y = start;
@@ -246,17 +326,22 @@ paged_decode_q8_kernel(const KParams p, const Q8Params sp8) {
     w.tile = 0;
     w.g = 0;
     w.n = min(stop - wc_y, kWindow);
+    int s = wc_s, off = wc_off + lane;
     if (lane < w.n) {
-      const int y = wc_y + lane;
-      const int s = find_seq(seq_base, S, y, KV);
+      if (off >= (seq_base[s + 1] - seq_base[s]) * KV) {
+        s = find_seq(seq_base, S, wc_y + lane, KV);
+        off = wc_y + lane - seq_base[s] * KV;
+      }
       const int nb = seq_base[s + 1] - seq_base[s];
-      const int off = y - seq_base[s] * KV;
-      const int g = off / nb;
-      const int b = off - g * nb;
-      w.tile = __ldg(p.block_tables + static_cast<int64_t>(s) * p.max_blocks_per_seq + b);
-      w.g = g;
+      w.g = off / nb;
+      w.tile = __ldg(p.block_tables + static_cast<int64_t>(s) * p.max_blocks_per_seq + off - w.g * nb);
     }
-    wc_y += w.n;
+    if (w.n > 0) {
+      wc_y += w.n;
+      wc_s = __shfl_sync(0xffffffffu, s, w.n - 1);
+      wc_off = __shfl_sync(0xffffffffu, off, w.n - 1) + 1;
+      settle(wc_s, wc_off);
+    }
     return w;
   };
   // Scales of the window whose tiles are consumed (cur_*) and of the one being issued (nxt_*).
@@ -326,9 +411,6 @@ paged_decode_q8_kernel(const KParams p, const Q8Params sp8) {
     bulk_prefetch_l2(p.value_cache + off, kQ8TileBytes, policy);
   }
 
-  Piece nx = {};
-  if (start < stop) nx = piece_at(seq_base, S, KV, start, stop);
-
   // Everything above reads only block tables, contexts, scales and codes; queries are read and
   // anything written only after the previous kernel in the stream has finished.
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -336,7 +418,7 @@ paged_decode_q8_kernel(const KParams p, const Q8Params sp8) {
     if (!p.fused_merge)  // for the merge kernel
       for (int i = lane; i <= S; i += 32) p.ws_seq_base[i] = seq_base[i];
     if (lane == 0) {
-      *p.ws_total = total;
+      *p.ws_total = units;
       if (total > p.tile_bound) flag_error(p.status, PA_DEVFLAG_BAD_CONTEXT);
     }
   }
@@ -364,7 +446,6 @@ paged_decode_q8_kernel(const KParams p, const Q8Params sp8) {
     const int32_t L = __ldg(p.context_lens + pc.s);
     const uint4 qx = __ldg(query_of(pc.s, pc.g)), qy = __ldg(query_of(pc.s, pc.g) + 1);
     const bool whole = pc.b0 == 0 && pc.b1 == pc.nb;
-    const bool first_piece = y == start;
     const int ntiles = pc.b1 - pc.b0;
     const int left = stop - y - ntiles;
     if (left > 0) {  // the next head of this sequence, or the next sequence that has tokens
@@ -411,47 +492,74 @@ paged_decode_q8_kernel(const KParams p, const Q8Params sp8) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[j] = make_float2(0.f, 0.f);
 
+    const int full = min(ntiles, L / kBlockSize - pc.b0);  // tiles without a masked token
 #pragma unroll 1
-    for (int k = 0; k < ntiles; k += 2) {
-      const bool two = k + 1 < ntiles;
-      const int sa = waited % kStages, sb = (waited + 1) % kStages;
-      float xs[2], vs[2];
+    for (int k = 0; k < ntiles;) {
       if ((waited & (kWindow - 1)) == 0) {
         cur_ks = nxt_ks;
         cur_vs = nxt_vs;
       }
-      xs[0] = __shfl_sync(0xffffffffu, cur_ks, waited & (kWindow - 1));
+      // Pairs of full tiles whose scales and refills come from the windows at hand: the tight
+      // loop, without a test but for the data.
+      const int before = waited;
+      int pairs = min(min(full - k, kWindow - (waited & (kWindow - 1))), cur.n - cur_i) >> 1;
+#pragma unroll 1
+      for (; pairs > 0; --pairs) {
+        const int sa = waited % kStages, sb = (waited + 1) % kStages;
+        const int w = waited & (kWindow - 1);
+        const float xs[2] = {row_scale * __shfl_sync(0xffffffffu, cur_ks, w),
+                             row_scale * __shfl_sync(0xffffffffu, cur_ks, w + 1)};
+        const float vs[2] = {__shfl_sync(0xffffffffu, cur_vs, w), __shfl_sync(0xffffffffu, cur_vs, w + 1)};
+        const int32_t t = __shfl_sync(0xffffffffu, cur.tile, cur_i + (lane & 1));
+        bool here = mbar_wait(&full_bar[sa], static_cast<uint32_t>((waited / kStages) & 1));
+        here &= mbar_wait(&full_bar[sb], static_cast<uint32_t>(((waited + 1) / kStages) & 1));
+        if (!__all_sync(0xffffffffu, here)) {
+          ok = false;
+          break;
+        }
+        attend_pair<false>(ring + sa * kStageBytes, ring + sb * kStageBytes, r, q, 2 * kBlockSize, xs, vs,
+                           qa0, qa2, m, l, o);
+        // Every lane's reads of these stages have completed (their values fed the arithmetic
+        // above); the warp barrier orders them before the refills.
+        __syncwarp();
+        if (lane < 2) request(t, lane);
+        issued += 2;
+        cur_i += 2;
+        waited += 2;
+        k += 2;
+      }
+      if (!ok || k >= ntiles) break;
+      if (waited != before && (waited & (kWindow - 1)) == 0) continue;  // the next window's scales first
+      // One pair, or a single tile, with everything that can happen at an edge.
+      const bool two = k + 1 < ntiles;
+      const int sa = waited % kStages, sb = (waited + 1) % kStages;
+      float xs[2], vs[2];
+      xs[0] = row_scale * __shfl_sync(0xffffffffu, cur_ks, waited & (kWindow - 1));
       vs[0] = __shfl_sync(0xffffffffu, cur_vs, waited & (kWindow - 1));
       if (two && ((waited + 1) & (kWindow - 1)) == 0) {
         cur_ks = nxt_ks;
         cur_vs = nxt_vs;
       }
-      xs[1] = __shfl_sync(0xffffffffu, cur_ks, (waited + 1) & (kWindow - 1));
+      xs[1] = row_scale * __shfl_sync(0xffffffffu, cur_ks, (waited + 1) & (kWindow - 1));
       vs[1] = __shfl_sync(0xffffffffu, cur_vs, (waited + 1) & (kWindow - 1));
-      xs[0] *= row_scale;
-      xs[1] *= row_scale;
       bool here = mbar_wait(&full_bar[sa], static_cast<uint32_t>((waited / kStages) & 1));
       if (two)
         here &= mbar_wait(&full_bar[sb], static_cast<uint32_t>(((waited + 1) / kStages) & 1));
       if (!__all_sync(0xffffffffu, here)) {
-        if (lane == 0) flag_error(p.status, PA_DEVFLAG_TIMEOUT);
         ok = false;
         break;
       }
       const uint8_t* ta = ring + sa * kStageBytes;
-      const uint8_t* tb = two ? ring + sb * kStageBytes : ta;
       const int valid = L - (pc.b0 + k) * kBlockSize;
-      if (two && valid >= 2 * kBlockSize)
-        attend_pair<false>(ta, tb, r, q, 2 * kBlockSize, xs, vs, qa0, qa2, m, l, o);
-      else
-        attend_pair<true>(ta, tb, r, q, two ? valid : min(valid, kBlockSize), xs, vs, qa0, qa2, m, l, o);
-      // Every lane's reads of these stages have completed (their values fed the arithmetic
-      // above); the warp barrier orders them before the refills.
+      attend_pair<true>(ta, two ? ring + sb * kStageBytes : ta, r, q, two ? valid : min(valid, kBlockSize),
+                        xs, vs, qa0, qa2, m, l, o);
       __syncwarp();
       const int n = two ? 2 : 1;
       waited += n;
+      k += n;
       issue(n);
     }
+    if (!ok && lane == 0) flag_error(p.status, PA_DEVFLAG_TIMEOUT);
     if (!ok) break;
 
     l += __shfl_xor_sync(0xffffffffu, l, 1);
@@ -470,7 +578,9 @@ paged_decode_q8_kernel(const KParams p, const Q8Params sp8) {
         dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
         dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
       } else {
-        const int slot = first_piece ? 0 : 1;
+        // A run writes at most two partials: of the segment it begins inside (slot 0), and of
+        // the one that begins in it and goes on in the next run (slot 1).
+        const int slot = pc.b0 > 0 ? 0 : 1;
         float* dst = p.partials + ((static_cast<int64_t>(gw) * 2 + slot) * GROUP + r) * kPartialFloats;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -483,39 +593,8 @@ paged_decode_q8_kernel(const KParams p, const Q8Params sp8) {
         }
       }
     }
-    if (!whole && p.fused_merge) {
-      // Publish this piece; the warp that publishes the segment's last piece merges it, with
-      // CTA-scope ordering when all the segment's pieces ran on this CTA.
-      const int64_t x0 = static_cast<int64_t>(seq_base[pc.s]) * KV + static_cast<int64_t>(pc.g) * pc.nb;
-      const SegmentPieces sp = segment_pieces(x0, x0 + pc.nb, total, p.grid, 0);
-      const bool local = sp.c_first / kWarps == sp.c_last / kWarps;
-      int last = 0;
-      if (local) {
-        __threadfence_block();
-        __syncwarp();
-        if (lane == 0) {
-          const int n = segment_piece_count(sp, x0, x0 + pc.nb, total, p.grid);
-          last = atomicAdd(&cta_seg_count[sp.c_first % kWarps], 1) == n - 1;
-        }
-        if (__shfl_sync(0xffffffffu, last, 0)) {
-          __threadfence_block();
-          merge_segment_in_warp<GROUP, true, false>(p, sp, x0, x0 + pc.nb, total, pc.s, pc.g, lane);
-          if (lane == 0) cta_seg_count[sp.c_first % kWarps] = 0;
-        }
-      } else {
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) {
-          const int n = segment_piece_count(sp, x0, x0 + pc.nb, total, p.grid);
-          last = atomicAdd(&p.seg_count[pc.s * KV + pc.g], 1) == n - 1;
-        }
-        if (__shfl_sync(0xffffffffu, last, 0)) {
-          __threadfence();
-          merge_segment_in_warp<GROUP, false, false>(p, sp, x0, x0 + pc.nb, total, pc.s, pc.g, lane);
-          if (lane == 0) p.seg_count[pc.s * KV + pc.g] = 0;
-        }
-      }
-    }
+    if (!whole && p.fused_merge)
+      publish_piece<GROUP>(p, seq_base, cta_seg_count, pc.s, pc.g, pc.nb, units, lane);
     y += ntiles;
   }
   // After a timeout, leave no copy in flight into this warp's ring (bounded waits).
@@ -589,7 +668,7 @@ cudaError_t launch(const AttendQ8Args& a, const DecodePlan& plan, void* workspac
   e = cudaLaunchKernelEx(&cfg, paged_decode_q8_kernel<GROUP>, p, s);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess || plan.fused_merge) return e;
-  return launch_merge<GROUP>(p, plan, false, stream);
+  return launch_merge<GROUP, kSegmentUnits>(p, plan, false, stream);
 }
 
 }  // namespace
@@ -620,8 +699,8 @@ cudaError_t plan_decode_q8(int32_t num_seqs, int32_t num_kv_heads, int32_t num_q
   plan->tile_bound = tiles_upper;
   plan->grid = static_cast<int>((runs + kWarps - 1) / kWarps);
   plan->smem_bytes = smem_bytes(num_seqs);
-  plan->fused_merge = max_context_len <= kFusedMergeMaxContext;
   const int64_t seg_pieces = runs / (static_cast<int64_t>(num_seqs) * num_kv_heads) + 2;
+  plan->fused_merge = max_context_len <= kFusedMergeMaxContext && seg_pieces <= kFusedMergeMaxPieces;
   plan->merge_split_heads = !plan->fused_merge && seg_pieces >= kMergeSplitPieces;
   plan->prefetch_ok = !(max_sms > 0 && max_sms < sms);
   plan->ws_count_offset = (16 + sizeof(int32_t) * (num_seqs + 1) + 255) / 256 * 256;
