@@ -128,6 +128,12 @@ __device__ __forceinline__ float lds_f32(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ void lds_f32x4(uint32_t addr, float (&v)[4]) {
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(addr));
+}
+
 // Instruction descriptor, kind::f16 with f16 A/B (both K-major) and fp32 accumulation.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n) {
   return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
@@ -280,11 +286,11 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
     // partner then sees the flag.
     float* const my_xch = xch + (half * 3 * 2 + part) * kTileM + r;
     const int pair_bar = 1 + half * 4 + (warp & 3);
-    auto exchange = [&](int slot, float mine, float& other) -> bool {
+    auto exchange = [&](int slot, float mine, int& gone) -> float {
       my_xch[slot * 2 * kTileM] = mine;
       named_barrier_sync(pair_bar, 64);
-      other = my_xch[slot * 2 * kTileM + (part ? -kTileM : kTileM)];
-      return __all_sync(0xffffffffu, abort_flag == 0);
+      gone = abort_flag;  // tested before the next barrier of the pair
+      return my_xch[slot * 2 * kTileM + (part ? -kTileM : kTileM)];
     };
     auto wait_row = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, wait_ready(bar, parity, &abort_flag, p.status));
@@ -385,6 +391,10 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
           }
           const int slot = (jt + j) % kConstRing;
           const uint32_t cs = smem_addr(consts + slot * kConsts + part * (kBlocksPerTile / 2));
+          float f[kBlocksPerTile / 2];  // score factors of this warp's blocks
+          lds_f32x4(cs, f);
+#pragma unroll
+          for (int b = 0; b < kBlocksPerTile / 2; ++b) f[b] *= q_factor;
           float mt = -INFINITY;
 #pragma unroll
           for (int b = 0; b < kBlocksPerTile / 2; ++b) {
@@ -396,10 +406,10 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
               a1 = max3f(a1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
             }
             a0 = max3f(a0, __uint_as_float(x[14]), __uint_as_float(x[15]));
-            mt = fmaxf(mt, fmaxf(a0, a1) * (lds_f32(cs + 4 * b) * q_factor));
+            mt = fmaxf(mt, fmaxf(a0, a1) * f[b]);
           }
-          float theirs;
-          if (!(ok = exchange(c & 1, mt, theirs))) break;
+          int gone;
+          const float theirs = exchange(c & 1, mt, gone);
           const float m_new = max3f(m, mt, theirs);
           const bool grow = m_new - m > kRescaleThreshold;  // true on the first tile
           float alpha = 1.f;
@@ -409,11 +419,12 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
           }
           l *= alpha;
           // p' two at a time, packed to bf16 over the scores
+          float lf[kBlocksPerTile / 2];
+          lds_f32x4(cs + 4 * kBlocksPerTile, lf);
 #pragma unroll
           for (int b = 0; b < kBlocksPerTile / 2; ++b) {
-            const float f = lds_f32(cs + 4 * b) * q_factor;
-            const float nb = lds_f32(cs + 4 * (kBlocksPerTile + b)) - m;
-            const float2 fb = make_float2(f, f);
+            const float nb = lf[b] - m;
+            const float2 fb = make_float2(f[b], f[b]);
             const float2 nb2 = make_float2(nb, nb);
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
@@ -428,6 +439,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
             }
             l += (sum.x + sum.y) * lds_f32(cs + 4 * (2 * kBlocksPerTile + b));
           }
+          if (!(ok = __all_sync(0xffffffffu, gone == 0))) break;
           if (c > 0) {  // the previous P V: P's columns are free and O is up to date
             if (!(ok = wait_row(&pv_done[half], static_cast<uint32_t>((c - 1) & 1)))) break;
             tc_fence_after_sync();
@@ -454,8 +466,9 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
         }
         if (!ok) break;
         // ---- epilogue: this warp's 32 dims ----
-        float theirs;
-        if (!(ok = exchange(2, l, theirs))) break;
+        int gone;
+        const float theirs = exchange(2, l, gone);
+        if (!(ok = __all_sync(0xffffffffu, gone == 0))) break;
         if (!(ok = wait_row(&pv_done[half], static_cast<uint32_t>((c - 1) & 1)))) break;
         tc_fence_after_sync();
         uint32_t o[32];
@@ -500,18 +513,21 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
           // score constants of this warp's blocks
           const int slot = jt % kConstRing;
           const float* rs = raw_scale + st * 2 * kBlocksPerTile;
-          int my_e = 0;  // lane b: exponent of block b's value scale; -1000: a scale of zero
+          uint32_t my_m = 0u;  // lane b: 2^(120 + e) of block b's value scale, a bf16 pair
+          int my_high = 0;     // e where 120 + e is beyond bf16: then my_m is 2^120
           if (lane < kMyBlocks) {
             const int blk = kMyBlocks * cw + lane;
             const bool needed = j * kBlocksPerTile + blk < cur.blocks_needed;
             const float ks = needed ? fmaxf(rs[blk], 1.17549435e-38f) : 1.f;
             const float vs = needed ? rs[kBlocksPerTile + blk] : 1.f;
             const uint32_t bits = __float_as_uint(vs);
-            my_e = static_cast<int>((bits >> 23) & 0xffu) - 127;
+            const int e = static_cast<int>((bits >> 23) & 0xffu) - 127;
             float f = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
-            if (my_e == -127) {  // zero (or too small to matter)
-              my_e = -1000;
+            if (e == -127) {  // zero (or too small to matter)
               f = 1.f;
+            } else {
+              my_high = e > 7 ? min(e, 127) : 0;
+              my_m = bf2_power(e > 7 ? 120 : 120 + e);
             }
             float* cs = consts + slot * kConsts + blk;
             cs[0] = ks;
@@ -519,6 +535,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
             cs[2 * kBlocksPerTile] = f == 1.f ? 1.f : 1.f / f;
           }
           __syncwarp();  // before lane 0's arrival below
+          const bool any_high = __any_sync(0xffffffffu, my_high != 0);
           // K: f16
           ok = wait_ready(&k_empty[st], ph ^ 1u, &abort_flag, p.status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -544,24 +561,22 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           dst = sv + st * kOpBytes;
           raw += kTileN * kQ8RowBytes;
-          const int keys_left = cur.keys - j * kTileN;
+          const int keys_left = cur.keys - j * kTileN - row0;
 #pragma unroll
           for (int i = 0; i < 2 * kMyBlocks; ++i) {
             uint4 w = lds128(raw + i * 512);
-            const int eb = __shfl_sync(0xffffffffu, my_e, i >> 1);
             // keys past the last needed one weigh nothing, but may hold anything
-            if (row0 + 8 * i >= keys_left || eb == -1000) w = make_uint4(0u, 0u, 0u, 0u);
+            if (8 * i >= keys_left) w = make_uint4(0u, 0u, 0u, 0u);
             uint4 a, b;
             codes4_to_bf2x2(w.x, a.x, a.y);
             codes4_to_bf2x2(w.y, a.z, a.w);
             codes4_to_bf2x2(w.z, b.x, b.y);
             codes4_to_bf2x2(w.w, b.z, b.w);
-            // 2^(120 + e) in one factor where it is a bf16, else in two
-            const uint32_t m0 = bf2_power(eb <= 7 ? max(120 + eb, -126) : 120);
+            const uint32_t m0 = __shfl_sync(0xffffffffu, my_m, i >> 1);
             a.x = mul_bf2(a.x, m0); a.y = mul_bf2(a.y, m0); a.z = mul_bf2(a.z, m0); a.w = mul_bf2(a.w, m0);
             b.x = mul_bf2(b.x, m0); b.y = mul_bf2(b.y, m0); b.z = mul_bf2(b.z, m0); b.w = mul_bf2(b.w, m0);
-            if (eb > 7) {
-              const uint32_t m1 = bf2_power(min(eb, 127));
+            if (any_high) {  // a scale above 2^7: the rest of it
+              const uint32_t m1 = bf2_power(__shfl_sync(0xffffffffu, my_high, i >> 1));
               a.x = mul_bf2(a.x, m1); a.y = mul_bf2(a.y, m1); a.z = mul_bf2(a.z, m1); a.w = mul_bf2(a.w, m1);
               b.x = mul_bf2(b.x, m1); b.y = mul_bf2(b.y, m1); b.z = mul_bf2(b.z, m1); b.w = mul_bf2(b.w, m1);
             }
