@@ -242,7 +242,8 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x;
-  const int warp = tid >> 5;
+  // (through a shuffle, so that what depends on it stays in uniform registers)
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int lane = tid & 31;
   const int S = p.num_seqs;
   const int KV = p.num_kv_heads;

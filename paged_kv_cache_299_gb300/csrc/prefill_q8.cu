@@ -185,7 +185,8 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
   constexpr int kHalfTokens = kTileM / GROUP;
   constexpr int kUnitTokens = 2 * kHalfTokens;
   const int tid = threadIdx.x;
-  const int warp = tid >> 5;
+  // (through a shuffle, so that what depends on it stays in uniform registers)
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int lane = tid & 31;
   extern __shared__ __align__(1024) uint8_t smem[];  // 128-byte swizzle atoms need 1 KiB
   if ((smem_addr(smem) & 1023u) != 0) {
