@@ -21,14 +21,15 @@
 //     O of each half 64.  P has columns of its own, so the next tile's scores are issued as
 //     soon as the row warps have read this tile's into registers and are ready when they come
 //     back for them; the row warps never wait for the tensor core but at a unit's start.
-//   * Warps 0-3 and 4-7: the row warps of the two halves, one thread per row: read S, mask
-//     the diagonal tiles, maximum, exponentials, P as bf16, row sums in fp32; O is rescaled in
-//     place only when a row's maximum grows by more than 2^8.  At a unit's last tile they turn
-//     the next unit's Q into f16 in shared memory.
-//   * Warps 8-11: converters.  They read a landed tile of codes and write K (f16) and V
-//     (bf16) in the 128-byte-swizzled layout that the MMAs read, into rings of three each.
-//   * Warp 12: one thread issues S = Q K^T (M128 N128 K64) and O += P V (M128 N64 K128).
-//   * Warp 13: one bulk copy per (block, pool) into a ring of three raw tiles, the blocks'
+//   * Warps 0-7 and 8-15: the row warps of the two halves, two threads per row (64 keys each):
+//     read S, mask the diagonal tiles, maximum (exchanged between the two), exponentials, P as
+//     bf16, row sums in fp32; O is rescaled in place only when a row's maximum grows by more
+//     than 2^8.  At a unit's last tile they turn the next unit's Q into f16 in shared memory.
+//   * Warps 16-19 (V, to bf16) and 22-23 (K, to f16): converters.  They read a landed tile of
+//     codes and write it in the 128-byte-swizzled layout that the MMAs read, into rings of
+//     three each.
+//   * Warp 20: one elected lane issues S = Q K^T (M128 N128 K64) and O += P V (M128 N64 K128).
+//   * Warp 21: one bulk copy per (block, pool) into a ring of three raw tiles, the blocks'
 //     scales beside them by 4-byte asynchronous copies on the same mbarrier; Q by TMA.
 // Every mbarrier wait is bounded; on timeout the CTA records PA_DEVFLAG_TIMEOUT, drains its
 // own copies and MMAs, frees its tensor memory and returns.
@@ -50,8 +51,8 @@ constexpr int kBlocksPerTile = kTileN / kBlockSize;
 constexpr int kThreads = 768;
 constexpr int kRowWarps = 8;                      // per half: four for each half of a tile's keys
 constexpr int kRowThreads = 2 * kRowWarps * 32;
-constexpr int kConvWarps = 4;
-constexpr int kConvWarp0 = 16, kMmaWarp = 20, kProducerWarp = 21;  // 22 and 23 idle
+constexpr int kVWarps = 4, kKWarps = 2;           // converters
+constexpr int kVWarp0 = 16, kMmaWarp = 20, kProducerWarp = 21, kKWarp0 = 22;
 constexpr int kRing = 3;                          // stages of each of the three rings
 constexpr int kConstRing = 8;                     // tiles whose score constants are kept
 constexpr int kConsts = 3 * kBlocksPerTile;       // key scale, log2 f, 1 / f of every block
@@ -243,10 +244,10 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&raw_full[i], 1 + kBlocksPerTile);
-      mbar_init(&raw_empty[i], kConvWarps);
-      mbar_init(&k_full[i], kConvWarps);
+      mbar_init(&raw_empty[i], kVWarps + kKWarps);
+      mbar_init(&k_full[i], kKWarps);
       mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], kConvWarps);
+      mbar_init(&v_full[i], kVWarps);
       mbar_init(&v_empty[i], 1);
     }
     mbar_init(drain, 1);
@@ -498,70 +499,34 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp < kMmaWarp) {
-      // ============================ converters ============================
-      const int cw = warp - kConvWarp0;  // keys 64 cw .. 64 cw + 63 of every tile, blocks 4 cw .. + 3
-      constexpr int kMyBlocks = kBlocksPerTile / kConvWarps;
-      int k = 0, jt = 0;
+      // ============================ V converters ============================
+      constexpr int kMyBlocks = kBlocksPerTile / kVWarps;
+      const int cw = warp - kVWarp0;  // blocks kMyBlocks cw .. of every tile
+      const int row0 = cw * kMyBlocks * kBlockSize + (lane >> 2);
+      const int c0 = 2 * (lane & 3);  // 16 codes of a row: two 16-byte chunks
+      int k = 0, st = 0;
+      uint32_t ph = 0;
       Unit cur;
       bool ok = true;
       while (ok && next_unit<kUnitTokens, kTileN>(p, sc, k, cur)) {
-        for (int j = 0; j < cur.n_kv; ++j, ++jt) {
-          const int st = jt % kRing;
-          const uint32_t ph = static_cast<uint32_t>((jt / kRing) & 1);
+        for (int j = 0; j < cur.n_kv; ++j) {
           ok = wait_ready(&raw_full[st], ph, &abort_flag, p.status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          const uint8_t* raw = sraw + st * kRawBytes + cw * kMyBlocks * kQ8TileBytes + 16 * lane;
-          // score constants of this warp's blocks
-          const int slot = jt % kConstRing;
-          const float* rs = raw_scale + st * 2 * kBlocksPerTile;
           uint32_t my_m = 0u;  // lane b: 2^(120 + e) of block b's value scale, a bf16 pair
           int my_high = 0;     // e where 120 + e is beyond bf16: then my_m is 2^120
           if (lane < kMyBlocks) {
-            const int blk = kMyBlocks * cw + lane;
-            const bool needed = j * kBlocksPerTile + blk < cur.blocks_needed;
-            const float ks = needed ? fmaxf(rs[blk], 1.17549435e-38f) : 1.f;
-            const float vs = needed ? rs[kBlocksPerTile + blk] : 1.f;
-            const uint32_t bits = __float_as_uint(vs);
-            const int e = static_cast<int>((bits >> 23) & 0xffu) - 127;
-            float f = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
-            if (e == -127) {  // zero (or too small to matter)
-              f = 1.f;
-            } else {
+            const int e = static_cast<int>((__float_as_uint(
+                              raw_scale[st * 2 * kBlocksPerTile + kBlocksPerTile + kMyBlocks * cw + lane]) >> 23) & 0xffu) - 127;
+            if (e > -127) {  // else zero (or too small to matter)
               my_high = e > 7 ? min(e, 127) : 0;
               my_m = bf2_power(e > 7 ? 120 : 120 + e);
             }
-            float* cs = consts + slot * kConsts + blk;
-            cs[0] = ks;
-            cs[kBlocksPerTile] = f == 1.f ? 0.f : __log2f(f);
-            cs[2 * kBlocksPerTile] = f == 1.f ? 1.f : 1.f / f;
           }
-          __syncwarp();  // before lane 0's arrival below
           const bool any_high = __any_sync(0xffffffffu, my_high != 0);
-          // K: f16
-          ok = wait_ready(&k_empty[st], ph ^ 1u, &abort_flag, p.status);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          uint8_t* dst = sk + st * kOpBytes;
-          const int row0 = cw * kMyBlocks * kBlockSize + (lane >> 2);
-          const int c0 = 2 * (lane & 3);  // 16 codes of a row: two 16-byte chunks
-#pragma unroll
-          for (int i = 0; i < 2 * kMyBlocks; ++i) {
-            const uint4 w = lds128(raw + i * 512);
-            uint4 a, b;
-            codes4_to_half2x2(w.x, a.x, a.y);
-            codes4_to_half2x2(w.y, a.z, a.w);
-            codes4_to_half2x2(w.z, b.x, b.y);
-            codes4_to_half2x2(w.w, b.z, b.w);
-            *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * i, c0)) = a;
-            *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * i, c0 + 1)) = b;
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&k_full[st]);
-          // V: bf16 times 2^e
           ok = wait_ready(&v_empty[st], ph ^ 1u, &abort_flag, p.status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          dst = sv + st * kOpBytes;
-          raw += kTileN * kQ8RowBytes;
+          const uint8_t* raw = sraw + st * kRawBytes + kTileN * kQ8RowBytes + cw * kMyBlocks * kQ8TileBytes + 16 * lane;
+          uint8_t* dst = sv + st * kOpBytes;
           const int keys_left = cur.keys - j * kTileN - row0;
 #pragma unroll
           for (int i = 0; i < 2 * kMyBlocks; ++i) {
@@ -590,6 +555,71 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
             mbar_arrive(&v_full[st]);
             mbar_arrive(&raw_empty[st]);
           }
+          if (++st == kRing) {
+            st = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+    } else if (warp >= kKWarp0) {
+      // ============================ K converters ============================
+      constexpr int kMyBlocks = kBlocksPerTile / kKWarps;
+      const int cw = warp - kKWarp0;  // blocks kMyBlocks cw .. of every tile
+      const int row0 = cw * kMyBlocks * kBlockSize + (lane >> 2);
+      const int c0 = 2 * (lane & 3);
+      int k = 0, st = 0, slot = 0;
+      uint32_t ph = 0;
+      Unit cur;
+      bool ok = true;
+      while (ok && next_unit<kUnitTokens, kTileN>(p, sc, k, cur)) {
+        for (int j = 0; j < cur.n_kv; ++j) {
+          ok = wait_ready(&raw_full[st], ph, &abort_flag, p.status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          // the row warps' constants of this warp's blocks
+          if (lane < kMyBlocks) {
+            const int blk = kMyBlocks * cw + lane;
+            const float* rs = raw_scale + st * 2 * kBlocksPerTile + blk;
+            const bool needed = j * kBlocksPerTile + blk < cur.blocks_needed;
+            const float ks = needed ? fmaxf(rs[0], 1.17549435e-38f) : 1.f;
+            const uint32_t bits = needed ? __float_as_uint(rs[kBlocksPerTile]) : 0u;
+            // 1.f of the value scale, 1 for a scale of zero (or too small to matter)
+            const float f = (bits & 0x7f800000u) ? __uint_as_float((bits & 0x7fffffu) | 0x3f800000u) : 1.f;
+            float* cs = consts + slot * kConsts + blk;
+            cs[0] = ks;
+            float lf = 0.f, fi = 1.f;
+            if (f != 1.f) {
+              lf = __log2f(f);
+              fi = 1.f / f;
+            }
+            cs[kBlocksPerTile] = lf;
+            cs[2 * kBlocksPerTile] = fi;
+          }
+          ok = wait_ready(&k_empty[st], ph ^ 1u, &abort_flag, p.status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;  // (and the constants precede the arrival)
+          const uint8_t* raw = sraw + st * kRawBytes + cw * kMyBlocks * kQ8TileBytes + 16 * lane;
+          uint8_t* dst = sk + st * kOpBytes;
+#pragma unroll
+          for (int i = 0; i < 2 * kMyBlocks; ++i) {
+            const uint4 w = lds128(raw + i * 512);
+            uint4 a, b;
+            codes4_to_half2x2(w.x, a.x, a.y);
+            codes4_to_half2x2(w.y, a.z, a.w);
+            codes4_to_half2x2(w.z, b.x, b.y);
+            codes4_to_half2x2(w.w, b.z, b.w);
+            *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * i, c0)) = a;
+            *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * i, c0 + 1)) = b;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&k_full[st]);
+            mbar_arrive(&raw_empty[st]);
+          }
+          if (++st == kRing) {
+            st = 0;
+            ph ^= 1u;
+          }
+          slot = (slot + 1) % kConstRing;
         }
       }
     } else if (warp == kMmaWarp) {
