@@ -378,8 +378,10 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
           // phase again.
           if (j == n_mine - 1 && next_mine && !(ok = convert_q())) break;
           uint32_t v[2][32];
-          tmem_ld32(s_addr, v[0]);
-          tmem_ld32(s_addr + 32, v[1]);
+          float bm[kBlocksPerTile / 2];  // largest raw score of each block
+#pragma unroll
+          for (int b = 0; b < kBlocksPerTile / 2; ++b)
+            tmem_ld16_max(s_addr + 16 * b, &v[b >> 1][16 * (b & 1)], bm[b]);
           tmem_wait_ld();
           tc_fence_before_sync();
           __syncwarp();
@@ -388,8 +390,14 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
           if (kb + kTileN / 2 - 1 > pos_lo) {
             // a tile on the causal diagonal: hide keys past each row's position
 #pragma unroll
-            for (int i = 0; i < kTileN / 2; ++i)
-              if (kb + i > pos) v[i >> 5][i & 31] = __float_as_uint(-INFINITY);
+            for (int b = 0; b < kBlocksPerTile / 2; ++b) {
+              bm[b] = -INFINITY;
+#pragma unroll
+              for (int i = 16 * b; i < 16 * b + 16; ++i) {
+                if (kb + i > pos) v[i >> 5][i & 31] = __float_as_uint(-INFINITY);
+                bm[b] = fmaxf(bm[b], __uint_as_float(v[i >> 5][i & 31]));
+              }
+            }
           }
           const int slot = (jt + j) % kConstRing;
           const uint32_t cs = smem_addr(consts + slot * kConsts + part * (kBlocksPerTile / 2));
@@ -397,19 +405,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
           lds_f32x4(cs, f);
 #pragma unroll
           for (int b = 0; b < kBlocksPerTile / 2; ++b) f[b] *= q_factor;
-          float mt = -INFINITY;
-#pragma unroll
-          for (int b = 0; b < kBlocksPerTile / 2; ++b) {
-            const uint32_t* x = &v[b >> 1][16 * (b & 1)];
-            float a0 = __uint_as_float(x[0]), a1 = __uint_as_float(x[1]);
-#pragma unroll
-            for (int i = 2; i < 14; i += 4) {
-              a0 = max3f(a0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-              a1 = max3f(a1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
-            }
-            a0 = max3f(a0, __uint_as_float(x[14]), __uint_as_float(x[15]));
-            mt = fmaxf(mt, fmaxf(a0, a1) * f[b]);
-          }
+          const float mt = fmaxf(max3f(bm[0] * f[0], bm[1] * f[1], bm[2] * f[2]), bm[3] * f[3]);
           int gone;
           const float theirs = exchange(c & 1, mt, gone);
           const float m_new = max3f(m, mt, theirs);
