@@ -13,7 +13,10 @@
 // into equal contiguous runs, one per warp of a persistent grid; each warp streams its run
 // through a private ring in shared memory, and split segments merge by log-sum-exp.  What
 // differs per tile:
-//   * one plain bulk copy per pool (a tile is contiguous), 8 stages of 2 KiB per warp;
+//   * one plain bulk copy per pool (a tile is contiguous), 4 stages of 2 KiB per warp: 15 MB in
+//     flight over the device.  8 stages measured slower (256 mixed contexts 46.8 us against
+//     44.8, 4 x 131072 tokens 99.3 against 96.6): what is read on the way (tables, scales,
+//     queries) then waits behind 30 MB of tiles; 3 leave the memory idle (49.7 us);
 //   * the two scales of each of the next 32 tiles sit in the lanes' registers, loaded when
 //     the first of them is issued, a ring's length before it is consumed;
 //   * codes become f16 (cvt.rn.f16x2.e4m3x2, exact: about 43 pairs per clock and SM measured,
@@ -37,7 +40,7 @@ namespace pkv {
 namespace {
 
 constexpr int kWarps = 12;   // streaming warps per CTA, one CTA per SM
-constexpr int kStages = 8;   // ring depth per warp: 16 KiB in flight
+constexpr int kStages = 4;   // ring depth per warp: 8 KiB in flight
 constexpr int kStageBytes = 2 * kQ8TileBytes;
 constexpr int kWindow = 32;  // tiles whose block ids and scales are held in the lanes
 constexpr int kMinTilesPerRun = 2;
@@ -47,8 +50,6 @@ constexpr int kFusedMergeMaxPieces = 24;      // as do segments of more pieces t
 constexpr int kSegmentUnits = 2;  // what a piece costs besides its tiles, in tiles
 constexpr float kPShift = 7.f;                // log2 of the factor on p
 constexpr int kQExp = 13;                     // exponent of a row's largest f16 query element
-constexpr int kPrefetchTiles = 8;
-constexpr int kPrefetchMinTilesPerWarp = 48;
 static_assert(kStages <= kWindow, "a window's scales are loaded a ring's length ahead");
 
 struct Q8Params {
@@ -63,10 +64,6 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       "[%0], [%1], %2, [%3], %4;" ::"r"(smem_addr(dst)),
       "l"(src), "r"(bytes), "r"(smem_addr(bar)), "l"(policy)
       : "memory");
-}
-
-__device__ __forceinline__ void prefetch_l1(const void* p) {
-  asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
 }
 
 // D (+)= A B for A with rows 8-15 zero, f16 in, fp32 accumulate.
@@ -404,14 +401,6 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
     if (lane < n0) request(cur.tile, lane);
     issued = cur_i = n0;
   }
-  // with long runs, the next tiles are asked into L2 before the wait below
-  if (p.prefetch_ok && total >= static_cast<int64_t>(kPrefetchMinTilesPerWarp) * p.grid &&
-      lane >= cur_i && lane < cur.n && lane < cur_i + kPrefetchTiles && cur.tile >= 0) {
-    const int64_t off = static_cast<int64_t>(cur.tile) * kQ8TileBytes;
-    bulk_prefetch_l2(p.key_cache + off, kQ8TileBytes, policy);
-    bulk_prefetch_l2(p.value_cache + off, kQ8TileBytes, policy);
-  }
-
   // Everything above reads only block tables, contexts, scales and codes; queries are read and
   // anything written only after the previous kernel in the stream has finished.
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -459,9 +448,6 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
       }
       nx.b0 = 0;
       nx.b1 = min(nx.nb, left);
-      // on their way to L1 while this piece streams
-      prefetch_l1(query_of(nx.s, nx.g));
-      prefetch_l1(p.context_lens + nx.s);
     }
 
     // The query, to f16 under the row's power of two.
@@ -653,7 +639,6 @@ cudaError_t launch(const AttendQ8Args& a, const DecodePlan& plan, void* workspac
   p.seg_count = reinterpret_cast<int32_t*>(ws + plan.ws_count_offset);
   p.partials = reinterpret_cast<float*>(ws + plan.ws_meta_bytes);
   p.fused_merge = plan.fused_merge ? 1 : 0;
-  p.prefetch_ok = plan.prefetch_ok ? 1 : 0;
   p.status = a.status;
   const Q8Params s = {a.key_scale, a.value_scale};
   cudaLaunchConfig_t cfg = {};
@@ -703,7 +688,7 @@ cudaError_t plan_decode_q8(int32_t num_seqs, int32_t num_kv_heads, int32_t num_q
   const int64_t seg_pieces = runs / (static_cast<int64_t>(num_seqs) * num_kv_heads) + 2;
   plan->fused_merge = max_context_len <= kFusedMergeMaxContext && seg_pieces <= kFusedMergeMaxPieces;
   plan->merge_split_heads = !plan->fused_merge && seg_pieces >= kMergeSplitPieces;
-  plan->prefetch_ok = !(max_sms > 0 && max_sms < sms);
+  plan->prefetch_ok = false;
   plan->ws_count_offset = (16 + sizeof(int32_t) * (num_seqs + 1) + 255) / 256 * 256;
   plan->ws_meta_bytes = plan->ws_count_offset +
                         (sizeof(int32_t) * num_seqs * num_kv_heads + 255) / 256 * 256;
