@@ -393,8 +393,8 @@ pa_status pa_rope_append(const void* q, int64_t q_stride, void* q_out, int64_t q
  * turn subnormal); new ones are value / scale, rounded to nearest even once from fp32.  So a
  * chunked append and a token-by-token one of the same tokens may round small values
  * differently.  A NaN is stored as 0 and an infinity as the largest code of its sign; both set
- * PA_DEVFLAG_NONFINITE.  A block with earlier tokens whose scale is not a positive finite
- * number sets PA_DEVFLAG_BAD_SCALE and is left as it is.  Blocks that two sequences of the
+ * PA_DEVFLAG_NONFINITE.  A block with earlier tokens whose scale in a pool is not a positive
+ * finite number sets PA_DEVFLAG_BAD_SCALE and is left as it is in that pool.  Blocks that two sequences of the
  * call append to must differ (pa_copy_blocks_q8 before writing to shared blocks).  The other
  * arguments, checks and no-ops are pa_rope_append's; a sequence with any position out of range
  * stores nothing. */
@@ -419,9 +419,13 @@ size_t pa_decode_q8_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32
 /* pa_decode over the 8-bit pools:
  *   out[s][h][:] = sum_j softmax_j(scale * q[s][h] . K_s[j]) V_s[j],   K = code * key_scale,
  * with the arguments, limits, launch flags and errors of pa_decode (without partition_tokens;
- * contexts above max_context_len are reported and undefined).  The codes 0x7f and 0xff, which
- * pa_rope_append_q8 never stores, read as NaN.  Scales are read as any floats, not only powers
- * of two.  key_cache, value_cache: e4m3; key_scale, value_scale: 4-byte aligned floats. */
+ * contexts above max_context_len are reported and undefined).  With PA_LAUNCH_OVERLAP_PREVIOUS
+ * the scales are read as early as the block tables.  The scales of blocks in use may be any
+ * non-negative finite floats, not only powers of two.  The codes 0x7f and 0xff, which
+ * pa_rope_append_q8 never stores, are not numbers: rows that see one are undefined.  Slots past
+ * a context, and scales of blocks without a token in use, may hold anything.  key_cache,
+ * value_cache: e4m3; key_scale, value_scale: 4-byte aligned floats; fewer than 2^31 (block,
+ * head) tiles per pool. */
 pa_status pa_decode_q8(void* out, const void* q, const void* key_cache, const void* value_cache,
                        const float* key_scale, const float* value_scale, pa_cache_desc cd,
                        const int32_t* block_tables, int32_t max_blocks_per_seq,

@@ -450,27 +450,53 @@ def _kept_desc(shape):
     return d
 
 
-def _check_tensor(t, name, dtype, ndim):
-    """_need with a quick way through for tensors that are as they should be; the pointer."""
+def _current_device():
+    """Index of the current CUDA device; -2 (no tensor's) without one."""
     try:
-        if t.dtype is dtype and t.is_cuda and t.dim() == ndim and t.is_contiguous():
+        return _get_device() if _get_device is not None else torch.cuda.current_device()
+    except RuntimeError:
+        return -2
+
+
+def _wrong_device(t, name, dev):
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}: the kernels run "
+                     "on the current device")
+
+
+def _check_tensor(t, name, dtype, ndim, dev):
+    """_need, and the current device, with a quick way through for tensors that are as they
+    should be; the pointer."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.dim() == ndim and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
     _need(t, name, dtype, ndim)
-    return t.data_ptr()
+    _wrong_device(t, name, dev)
 
 
-def _status_ptr(device_status):
-    return None if device_status is None else device_status.data_ptr()
+def _on_stream(stream, make):
+    """make() with its allocation and its work on the stream the kernel will run on."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        return make()
 
 
-def _need_rows(t, name, heads=None):
+def _status_ptr(device_status, dev):
+    if device_status is None:
+        return None
+    return _check_tensor(device_status, "device_status", torch.int32, 1, dev)
+
+
+def _need_rows(t, name, dev, heads=None):
     """bf16 [T, heads, 64] whose rows are contiguous per token; returns the token stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        _wrong_device(t, name, dev)
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     shape = t.shape
@@ -484,12 +510,12 @@ def _need_rows(t, name, heads=None):
     return max(stride, heads * 64) if shape[0] <= 1 else stride
 
 
-def _need_q8(key_cache, value_cache, key_scale, value_scale):
+def _need_q8(key_cache, value_cache, key_scale, value_scale, dev):
     """Pointers of an 8-bit cache's four tensors, and its shape."""
-    kc = _check_tensor(key_cache, "key_cache", torch.float8_e4m3fn, 4)
-    vc = _check_tensor(value_cache, "value_cache", torch.float8_e4m3fn, 4)
-    ks = _check_tensor(key_scale, "key_scale", torch.float32, 2)
-    vs = _check_tensor(value_scale, "value_scale", torch.float32, 2)
+    kc = _check_tensor(key_cache, "key_cache", torch.float8_e4m3fn, 4, dev)
+    vc = _check_tensor(value_cache, "value_cache", torch.float8_e4m3fn, 4, dev)
+    ks = _check_tensor(key_scale, "key_scale", torch.float32, 2, dev)
+    vs = _check_tensor(value_scale, "value_scale", torch.float32, 2, dev)
     shape, scales = key_cache.shape, key_scale.shape
     if value_cache.shape != shape or value_scale.shape != scales or scales != shape[:2]:
         raise ValueError("8-bit pools are [blocks, heads, 16, 64] with scales [blocks, heads]")
@@ -508,19 +534,19 @@ def new_q8_cache(num_blocks, num_kv_heads, device=None):
 
 
 def _rope_append_args(q, key, value, cos_sin, hkv, block_tables, context_lens, query_start_loc,
-                      q_out, interleaved):
-    ks, vs = _need_rows(key, "key", hkv), _need_rows(value, "value", hkv)
+                      q_out, interleaved, stream, dev):
+    ks, vs = _need_rows(key, "key", dev, hkv), _need_rows(value, "value", dev, hkv)
     tokens = key.shape[0]
     if value.shape[0] != tokens:
         raise ValueError("key and value disagree on the token count")
     qs = os_ = hq = 0
     q_ptr = out_ptr = table = starts = None
     if q is not None:
-        qs = _need_rows(q, "q")
+        qs = _need_rows(q, "q", dev)
         hq = q.shape[1]
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        os_ = _need_rows(q_out, "q_out", hq)
+            q_out = _on_stream(stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
+        os_ = _need_rows(q_out, "q_out", dev, hq)
         if q.shape[0] != tokens or q_out.shape[0] != tokens:
             raise ValueError("q, q_out and key disagree on the token count")
         q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
@@ -528,18 +554,18 @@ def _rope_append_args(q, key, value, cos_sin, hkv, block_tables, context_lens, q
         raise ValueError("q_out without q")
     positions = 0
     if cos_sin is not None:
-        table = _check_tensor(cos_sin, "cos_sin", torch.float32, 2)
+        table = _check_tensor(cos_sin, "cos_sin", torch.float32, 2, dev)
         positions, width = cos_sin.shape
         if width != 64:
             raise ValueError("cos_sin must be [positions, 64]: 32 cosines, then 32 sines")
-    bt = _check_tensor(block_tables, "block_tables", torch.int32, 2)
-    ctx = _check_tensor(context_lens, "context_lens", torch.int32, 1)
+    bt = _check_tensor(block_tables, "block_tables", torch.int32, 2, dev)
+    ctx = _check_tensor(context_lens, "context_lens", torch.int32, 1, dev)
     rows, width = block_tables.shape
     seqs = context_lens.shape[0]
     if rows != seqs:
         raise ValueError("block_tables and context_lens disagree on the sequence count")
     if query_start_loc is not None:
-        starts = _check_tensor(query_start_loc, "query_start_loc", torch.int32, 1)
+        starts = _check_tensor(query_start_loc, "query_start_loc", torch.int32, 1, dev)
         if query_start_loc.shape[0] != seqs + 1:
             raise ValueError("query_start_loc must have one entry more than context_lens")
     return q_out, (q_ptr, qs, out_ptr, os_, hq, key.data_ptr(), ks, value.data_ptr(), vs, table,
@@ -552,15 +578,16 @@ def pa_rope_append(q, key, value, cos_sin, key_cache, value_cache, block_tables,
     """Rotate q [T, Hq, 64] and key [T, Hkv, 64] by their positions and store key and value into
     the bf16 pools; returns the rotated queries (q_out, which may be q; None without q).  The
     rows of a token must be contiguous, the tokens may be strided; see include/pagedkv.h."""
-    kc = _check_tensor(key_cache, "key_cache", torch.bfloat16, 4)
-    vc = _check_tensor(value_cache, "value_cache", torch.bfloat16, 4)
+    dev = _current_device()
+    kc = _check_tensor(key_cache, "key_cache", torch.bfloat16, 4, dev)
+    vc = _check_tensor(value_cache, "value_cache", torch.bfloat16, 4, dev)
     shape = key_cache.shape
     if value_cache.shape != shape:
         raise ValueError("cache shapes differ")
     q_out, args = _rope_append_args(q, key, value, cos_sin, shape[1], block_tables, context_lens,
-                                    query_start_loc, q_out, interleaved)
+                                    query_start_loc, q_out, interleaved, stream, dev)
     st = (_lib or load()).pa_rope_append(*args, kc, vc, _kept_desc(shape),
-                                         _status_ptr(device_status), _current_stream(stream))
+                                         _status_ptr(device_status, dev), _current_stream(stream))
     if st:
         _check(st, "pa_rope_append")
     return q_out
@@ -571,11 +598,12 @@ def pa_rope_append_q8(q, key, value, cos_sin, key_cache, value_cache, key_scale,
                       interleaved=False, device_status=None, stream=None):
     """pa_rope_append into the 8-bit pools (e4m3 codes, one scale per block and head).  cos_sin
     None stores the keys as they are (q must be None then); see include/pagedkv.h."""
-    kc, vc, ks, vs, shape = _need_q8(key_cache, value_cache, key_scale, value_scale)
+    dev = _current_device()
+    kc, vc, ks, vs, shape = _need_q8(key_cache, value_cache, key_scale, value_scale, dev)
     q_out, args = _rope_append_args(q, key, value, cos_sin, shape[1], block_tables, context_lens,
-                                    query_start_loc, q_out, interleaved)
+                                    query_start_loc, q_out, interleaved, stream, dev)
     st = (_lib or load()).pa_rope_append_q8(*args, kc, vc, ks, vs, _kept_desc(shape),
-                                            _status_ptr(device_status), _current_stream(stream))
+                                            _status_ptr(device_status, dev), _current_stream(stream))
     if st:
         _check(st, "pa_rope_append_q8")
     return q_out
@@ -591,11 +619,12 @@ def pa_decode_q8(out, q, key_cache, value_cache, key_scale, value_scale, block_t
                  stream=None, launch_flags=PA_LAUNCH_DEFAULT):
     """Paged decode attention over the 8-bit pools; writes out [S, Hq, D] (bf16).  launch_flags:
     those of pa_decode."""
-    op = _check_tensor(out, "out", torch.bfloat16, 3)
-    qp = _check_tensor(q, "q", torch.bfloat16, 3)
-    kc, vc, ks, vs, shape = _need_q8(key_cache, value_cache, key_scale, value_scale)
-    bt = _check_tensor(block_tables, "block_tables", torch.int32, 2)
-    ctx = _check_tensor(context_lens, "context_lens", torch.int32, 1)
+    dev = _current_device()
+    op = _check_tensor(out, "out", torch.bfloat16, 3, dev)
+    qp = _check_tensor(q, "q", torch.bfloat16, 3, dev)
+    kc, vc, ks, vs, shape = _need_q8(key_cache, value_cache, key_scale, value_scale, dev)
+    bt = _check_tensor(block_tables, "block_tables", torch.int32, 2, dev)
+    ctx = _check_tensor(context_lens, "context_lens", torch.int32, 1, dev)
     q_shape = q.shape
     num_seqs, hq, d = q_shape
     rows, width = block_tables.shape
@@ -604,11 +633,12 @@ def pa_decode_q8(out, q, key_cache, value_cache, key_scale, value_scale, block_t
         raise ValueError("q/out/block_tables/context_lens disagree on the sequence count")
     if workspace is None:
         need = pa_decode_q8_workspace_size(num_seqs, shape[1], hq, max_context_len)
-        workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device)
-    ws = _check_tensor(workspace, "workspace", torch.uint8, 1)
+        workspace = _on_stream(stream, lambda: torch.zeros(max(need, 16), dtype=torch.uint8,
+                                                           device=q.device))
+    ws = _check_tensor(workspace, "workspace", torch.uint8, 1, dev)
     st = (_lib or load()).pa_decode_q8(
-        op, qp, kc, vc, ks, vs, _kept_desc(shape), bt, width, ctx, num_seqs, hq, scale,
-        max_context_len, ws, workspace.shape[0], launch_flags, _status_ptr(device_status),
+        op, qp, kc, vc, ks, vs, _kept_desc(shape), bt, width, ctx, num_seqs, hq, float(scale),
+        int(max_context_len), ws, workspace.shape[0], int(launch_flags), _status_ptr(device_status, dev),
         _current_stream(stream))
     if st:
         _check(st, "pa_decode_q8")
@@ -619,12 +649,13 @@ def pa_prefill_chunk_q8(out, q, query_start_loc, max_query_len, key_cache, value
                         key_scale, value_scale, block_tables, context_lens, scale,
                         device_status=None, stream=None):
     """Causal chunked-prefill attention over the 8-bit pools; writes out [Tq, Hq, D] (bf16)."""
-    op = _check_tensor(out, "out", torch.bfloat16, 3)
-    qp = _check_tensor(q, "q", torch.bfloat16, 3)
-    starts = _check_tensor(query_start_loc, "query_start_loc", torch.int32, 1)
-    kc, vc, ks, vs, shape = _need_q8(key_cache, value_cache, key_scale, value_scale)
-    bt = _check_tensor(block_tables, "block_tables", torch.int32, 2)
-    ctx = _check_tensor(context_lens, "context_lens", torch.int32, 1)
+    dev = _current_device()
+    op = _check_tensor(out, "out", torch.bfloat16, 3, dev)
+    qp = _check_tensor(q, "q", torch.bfloat16, 3, dev)
+    starts = _check_tensor(query_start_loc, "query_start_loc", torch.int32, 1, dev)
+    kc, vc, ks, vs, shape = _need_q8(key_cache, value_cache, key_scale, value_scale, dev)
+    bt = _check_tensor(block_tables, "block_tables", torch.int32, 2, dev)
+    ctx = _check_tensor(context_lens, "context_lens", torch.int32, 1, dev)
     q_shape = q.shape
     tokens, hq, d = q_shape
     rows, width = block_tables.shape
@@ -633,8 +664,8 @@ def pa_prefill_chunk_q8(out, q, query_start_loc, max_query_len, key_cache, value
             rows != num_seqs:
         raise ValueError("prefill argument shapes disagree")
     st = (_lib or load()).pa_prefill_chunk_q8(
-        op, qp, starts, tokens, max_query_len, kc, vc, ks, vs, _kept_desc(shape), bt, width, ctx,
-        num_seqs, hq, scale, _status_ptr(device_status), _current_stream(stream))
+        op, qp, starts, tokens, int(max_query_len), kc, vc, ks, vs, _kept_desc(shape), bt, width, ctx,
+        num_seqs, hq, float(scale), _status_ptr(device_status, dev), _current_stream(stream))
     if st:
         _check(st, "pa_prefill_chunk_q8")
     return out
@@ -644,13 +675,14 @@ def pa_copy_blocks_q8(key_cache, value_cache, key_scale, value_scale, block_mapp
                       device_status=None, stream=None):
     """Copy whole physical blocks of the 8-bit pools with their scales: block_mapping int64
     [n, 2] (src, dst)."""
-    kc, vc, ks, vs, shape = _need_q8(key_cache, value_cache, key_scale, value_scale)
-    pairs = _check_tensor(block_mapping, "block_mapping", torch.int64, 2)
+    dev = _current_device()
+    kc, vc, ks, vs, shape = _need_q8(key_cache, value_cache, key_scale, value_scale, dev)
+    pairs = _check_tensor(block_mapping, "block_mapping", torch.int64, 2, dev)
     n, two = block_mapping.shape
     if two != 2:
         raise ValueError("block_mapping is not [n, 2]")
     st = (_lib or load()).pa_copy_blocks_q8(kc, vc, ks, vs, _kept_desc(shape), pairs, n,
-                                            _status_ptr(device_status), _current_stream(stream))
+                                            _status_ptr(device_status, dev), _current_stream(stream))
     if st:
         _check(st, "pa_copy_blocks_q8")
 

@@ -286,13 +286,16 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
     const uint32_t each = u32 / n;
     // c * units / n without 64 bits (n stays below 2^16)
     const uint32_t y = c * each + c * (u32 - each * n) / n;
+    auto units_before = [&](int s) {  // of sequence s
+      return static_cast<uint32_t>(KV) * static_cast<uint32_t>(seq_base[s] + kSegmentUnits * s);
+    };
     int lo = 0, hi = S - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (static_cast<uint32_t>(KV * (seq_base[mid] + kSegmentUnits * mid)) <= y) lo = mid; else hi = mid - 1;
+      if (units_before(mid) <= y) lo = mid; else hi = mid - 1;
     }
     const int nb = seq_base[lo + 1] - seq_base[lo];
-    const int off = static_cast<int>(y - static_cast<uint32_t>(KV * (seq_base[lo] + kSegmentUnits * lo)));
+    const int off = static_cast<int>(y - units_before(lo));
     int g = off / (nb + kSegmentUnits);
     int place = g * nb + max(0, off - g * (nb + kSegmentUnits) - kSegmentUnits);
     if (g >= KV) place = KV * nb;  // past the last unit
@@ -431,7 +434,7 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
   };
   int waited = 0;  // tiles whose data this warp has waited for
   bool ok = true;
-  for (int y = start; y < stop && ok;) {
+  for (int y = start; y < stop;) {
     const Piece pc = nx;
     const int32_t L = __ldg(p.context_lens + pc.s);
     const uint4 qx = __ldg(query_of(pc.s, pc.g)), qy = __ldg(query_of(pc.s, pc.g) + 1);
@@ -481,7 +484,7 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
 
     const int full = min(ntiles, L / kBlockSize - pc.b0);  // tiles without a masked token
 #pragma unroll 1
-    for (int k = 0; k < ntiles;) {
+    for (int k = 0; k < ntiles && ok;) {
       if ((waited & (kWindow - 1)) == 0) {
         cur_ks = nxt_ks;
         cur_vs = nxt_vs;
@@ -501,7 +504,7 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
         bool here = mbar_wait(&full_bar[sa], static_cast<uint32_t>((waited / kStages) & 1));
         here &= mbar_wait(&full_bar[sb], static_cast<uint32_t>(((waited + 1) / kStages) & 1));
         if (!__all_sync(0xffffffffu, here)) {
-          ok = false;
+          ok = false;  // (the pieces left are published without their tiles)
           break;
         }
         attend_pair<false>(ring + sa * kStageBytes, ring + sb * kStageBytes, r, q, 2 * kBlockSize, xs, vs,
@@ -546,9 +549,6 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
       k += n;
       issue(n);
     }
-    if (!ok && lane == 0) flag_error(p.status, PA_DEVFLAG_TIMEOUT);
-    if (!ok) break;
-
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
     if (r < GROUP) {
@@ -586,6 +586,7 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
   }
   // After a timeout, leave no copy in flight into this warp's ring (bounded waits).
   if (!ok && lane == 0) {
+    flag_error(p.status, PA_DEVFLAG_TIMEOUT);
     for (int t = waited; t < issued; ++t) {
       if (!mbar_wait(&full_bar[t % kStages], static_cast<uint32_t>((t / kStages) & 1))) break;
     }
@@ -599,16 +600,19 @@ size_t smem_bytes(int num_seqs) {
 
 template <int GROUP>
 cudaError_t prepare_kernel() {
-  static bool done = false;  // benign race: the attribute calls are idempotent
-  if (done) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(paged_decode_q8_kernel<GROUP>,
+  static bool done[kMaxDevices] = {};  // benign race: the attribute calls are idempotent
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < kMaxDevices && done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(paged_decode_q8_kernel<GROUP>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem_bytes(kMaxSeqs)));
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(paged_decode_q8_kernel<GROUP>,
                              cudaFuncAttributePreferredSharedMemoryCarveout,
                              cudaSharedmemCarveoutMaxShared);
-  if (e == cudaSuccess) done = true;
+  if (e == cudaSuccess && dev < kMaxDevices) done[dev] = true;
   return e;
 }
 

@@ -10,6 +10,8 @@
 
 namespace pkv {
 
+constexpr int kMaxDevices = 64;  // devices whose kernel attributes are remembered as set
+
 cudaError_t launch_slot_mapping(const int32_t* block_tables, int32_t max_blocks_per_seq,
                                 const int32_t* context_lens, const int32_t* query_start_loc,
                                 int32_t num_seqs, int32_t num_tokens, int32_t num_blocks,

@@ -857,9 +857,11 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
 
 template <int GROUP>
 cudaError_t launch(const AttendQ8Args& a, cudaStream_t stream) {
-  static bool ready = false;  // benign race: the calls are idempotent
-  cudaError_t e;
-  if (!ready) {
+  static bool ready[kMaxDevices] = {};  // benign race: the calls are idempotent
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= kMaxDevices || !ready[dev]) {
     cudaFuncAttributes attr;
     e = cudaFuncGetAttributes(&attr, paged_chunk_q8_kernel<GROUP>);
     if (e != cudaSuccess) return e;
@@ -869,7 +871,7 @@ cudaError_t launch(const AttendQ8Args& a, cudaStream_t stream) {
     e = cudaFuncSetAttribute(paged_chunk_q8_kernel<GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmemBytes);
     if (e != cudaSuccess) return e;
-    ready = true;
+    if (dev < kMaxDevices) ready[dev] = true;
   }
   CUtensorMap tq;
   if (!encode_query_tiles(&tq, a.q, static_cast<uint64_t>(a.num_query_tokens), a.num_q_heads, GROUP,
@@ -893,8 +895,6 @@ cudaError_t launch(const AttendQ8Args& a, cudaStream_t stream) {
   p.skip_single = 0;
   const Pools pools = {static_cast<const uint8_t*>(a.key_cache), static_cast<const uint8_t*>(a.value_cache),
                        a.key_scale, a.value_scale};
-  int dev = 0, sms = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * p.q_tiles;
   const int64_t grid = units < sms ? units : sms;

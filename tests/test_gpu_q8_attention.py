@@ -185,6 +185,51 @@ def test_decode_launch_flags():
     assert all(st.ok() for st in layers)
 
 
+def test_other_streams_allocate_and_run_in_order():
+    """A stream of the caller's, with the call's own workspace and output: both belong to it."""
+    w = wl.random_small(33, num_seqs=12, max_ctx=700)
+    st = State(w, 8, 32)
+    want = st.decode()
+    q, out = st.q.cuda(), torch.empty_like(want)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        out.zero_()
+        side.wait_stream(torch.cuda.current_stream())
+        pa.pa_decode_q8(out, q, *st.dev, st.bt, st.ctx, st.scale, st.max_ctx, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(out, want)
+    kc, vc, ks, vs = pa.new_q8_cache(w.num_blocks, 8)
+    k = st.q[:, :8].contiguous().cuda()
+    table = angles(800).cuda()
+    torch.cuda.synchronize()
+    rot = pa.pa_rope_append_q8(q, k, k, table, kc, vc, ks, vs, st.bt, st.ctx, stream=side)
+    side.synchronize()
+    ref = pa.pa_rope_append_q8(q, k, k, table, kc, vc, ks, vs, st.bt, st.ctx)
+    assert torch.equal(rot, ref)
+
+
+def test_wrong_device_is_refused(monkeypatch):
+    """Tensors of another device than the current one never reach a kernel."""
+    w = wl.random_small(34, num_seqs=2, max_ctx=30)
+    st = State(w, 8, 32)
+    q, out = st.q.cuda(), torch.empty_like(st.q, device="cuda")
+    k, table = st.q[:, :8].contiguous().cuda(), angles(40).cuda()
+    monkeypatch.setattr(pa, "_get_device", lambda: 1)
+    for call in (lambda: pa.pa_decode_q8(out, q, *st.dev, st.bt, st.ctx, 0.125, st.max_ctx),
+                 lambda: pa.pa_prefill_chunk_q8(out, q, i32([0, 1, 2]), 1, *st.dev, st.bt, st.ctx, 0.125),
+                 lambda: pa.pa_rope_append_q8(q, k, k, table, *st.dev, st.bt, st.ctx),
+                 lambda: pa.pa_copy_blocks_q8(*st.dev, torch.zeros(1, 2, dtype=torch.int64, device="cuda"))):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+    monkeypatch.undo()
+    with pytest.raises(ValueError):  # a status word on the host
+        pa.pa_decode_q8(out, q, *st.dev, st.bt, st.ctx, 0.125, st.max_ctx,
+                        device_status=torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError):  # not contiguous
+        pa.pa_decode_q8(out, q.transpose(0, 1), *st.dev, st.bt, st.ctx, 0.125, st.max_ctx)
+
+
 def test_decode_bad_entries_are_reported():
     w = wl.make_workload("bad", [40, 100], [1, 1], seed=12, pool_slack=0.5)
     st = State(w, 8, 32)
@@ -214,6 +259,13 @@ def test_chunk_lengths(prior):
     w = wl.make_workload("lengths", np.full(len(new), prior), new, num_prefill=len(new), seed=prior, pool_slack=0.2)
     check_chunk(w, 2, 8)
     check_chunk(w, 2, 2)
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (2, 1), (4, 1), (32, 8)])
+def test_chunk_of_one_row(hq, hkv):
+    """The smallest call: one row (a query box larger than the tensor), alone and with a prior."""
+    check_chunk(wl.make_workload("first", [0], [1], num_prefill=1, seed=hq, pool_slack=2.0), hkv, hq)
+    check_chunk(wl.make_workload("later", [333], [1], num_prefill=1, seed=hq, pool_slack=1.0), hkv, hq)
 
 
 def test_chunk_long():
@@ -286,6 +338,66 @@ def test_chunk_bad_entries_are_reported():
     st.status.zero_()
     st.chunk()
     assert int(st.status.item()) == pa.DEVFLAG_BAD_CONTEXT
+
+
+# ---- against the oracle, and far into a large pool --------------------------------------------
+def test_agrees_with_the_oracle_on_the_dequantised_cache():
+    """A code times a power of two is a bf16 value, so the oracle can read the same cache."""
+    import oracle
+    w = wl.make_workload("oracle", [100, 37, 300], [50, 40, 1], num_prefill=3, seed=14, pool_slack=0.3)
+    st = State(w, 8, 32, rows=91)
+    kc, vc = (torch.nan_to_num(x).to(torch.bfloat16) for x in (st.k64, st.v64))
+    ref, err = oracle.prefill_chunk(wl.bf16_bits(st.q), w.new_start_loc, wl.bf16_bits(kc), wl.bf16_bits(vc),
+                                    w.block_tables, w.context_lens, 0.125)
+    assert err == 0
+    diff = np.abs(st.chunk().float().cpu().numpy().astype(np.float64) - ref)
+    assert diff.max() <= 2e-2 and diff.mean() <= 2e-3
+    last = st.q[w.new_start_loc[1:] - 1]
+    ref, err = oracle.decode(wl.bf16_bits(last), wl.bf16_bits(kc), wl.bf16_bits(vc), w.block_tables, w.context_lens,
+                             0.125)
+    assert err == 0
+    st.q = last
+    diff = np.abs(st.decode().float().cpu().numpy().astype(np.float64) - ref)
+    assert diff.max() <= 2e-2 and diff.mean() <= 2e-3
+
+
+def test_blocks_far_into_a_large_pool():
+    """Pools above 4 GiB: append, copy, decode and chunk at their far end, bf16 append too."""
+    nb, hkv, hq = 600_000, 8, 32
+    kc, vc = (torch.empty(nb, hkv, 16, 64, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+              for _ in range(2))
+    ks, vs = (torch.full((nb, hkv), float("nan"), device="cuda") for _ in range(2))
+    g = torch.Generator().manual_seed(2)
+    n = 75
+    far = np.array([[nb - 1, 3, nb - 200, nb - 2, nb - 77]], np.int32)
+    near = np.array([[0, 1, 2, 3, 4]], np.int32)
+    k, v, q = (torch.randn(n, h, 64, generator=g).to(torch.bfloat16).cuda() for h in (hkv, hkv, hq))
+    small = pa.new_q8_cache(5, hkv)
+    status = pa.new_device_status()
+    table, ctx, qsl = angles(n).cuda(), i32([n]), i32([0, n])
+    outs = []
+    for cache, bt in (((kc, vc, ks, vs), far), (small, near)):
+        qr = pa.pa_rope_append_q8(q, k, v, table, *cache, i32(bt), ctx, qsl, device_status=status)
+        if bt is far:  # one block moves, to the far end as well
+            pa.pa_copy_blocks_q8(*cache, torch.tensor([[nb - 200, nb - 4]]).cuda(), device_status=status)
+            bt = bt.copy()
+            bt[0, 2] = nb - 4
+        chunk, one = torch.empty_like(qr), torch.empty_like(qr[-1:])
+        pa.pa_prefill_chunk_q8(chunk, qr, qsl, n, *cache, i32(bt), ctx, 0.125, device_status=status)
+        pa.pa_decode_q8(one, qr[-1:].contiguous(), *cache, i32(bt), ctx, 0.125, n, device_status=status)
+        outs.append((qr, chunk, one))
+    assert pa.pa_check_device_status(status) == pa.PA_OK
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    del kc, vc
+    big = [torch.empty(nb // 2, hkv, 16, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    bt = np.array([[nb // 2 - 1, 5, nb // 2 - 3, nb // 2 - 9, 6]], np.int32)
+    pa.pa_rope_append(None, k, v, table, *big, i32(bt), ctx, qsl, device_status=status)
+    low = [torch.empty(5, hkv, 16, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    pa.pa_rope_append(None, k, v, table, *low, i32(near), ctx, qsl, device_status=status)
+    for x, y in zip(big, low):
+        for i in range(n):
+            assert torch.equal(x[int(bt[0, i // 16]), :, i % 16], y[i // 16, :, i % 16])
+    assert pa.pa_check_device_status(status) == pa.PA_OK
 
 
 # ---- together -------------------------------------------------------------------------------

@@ -132,9 +132,9 @@ def test_status_of_values():
 def test_binding_refuses_host_tensors():
     x = torch.zeros(2, 8, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
-        pa._need_rows(x, "key")
+        pa._need_rows(x, "key", 0)
     with pytest.raises(TypeError):
-        pa._need_rows([1], "key")
+        pa._need_rows([1], "key", 0)
     codes = torch.zeros(2, 8, 16, 64, dtype=torch.uint8).view(torch.float8_e4m3fn)
     with pytest.raises(ValueError):
-        pa._need_q8(codes, codes, torch.ones(2, 8), torch.ones(2, 8))
+        pa._need_q8(codes, codes, torch.ones(2, 8), torch.ones(2, 8), 0)
