@@ -484,7 +484,7 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
 
     const int full = min(ntiles, L / kBlockSize - pc.b0);  // tiles without a masked token
 #pragma unroll 1
-    for (int k = 0; k < ntiles && ok;) {
+    for (int k = ok ? 0 : ntiles; k < ntiles;) {
       if ((waited & (kWindow - 1)) == 0) {
         cur_ks = nxt_ks;
         cur_vs = nxt_vs;
