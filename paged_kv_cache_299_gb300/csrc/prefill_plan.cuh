@@ -90,9 +90,13 @@ struct Schedule {
   const int32_t* unit_s;   // shared memory (sorted mode)
   const int32_t* unit_tg;  // tile * 64 + g
   int n_units;             // sorted mode: this CTA's unit count; -1: grid order
+  // sorted mode, where the plan kept them: first row, rows and context of each unit's sequence
+  const int32_t* unit_q0 = nullptr;
+  const int32_t* unit_len = nullptr;
+  const int32_t* unit_L = nullptr;
 };
 
-template <int TOKENS, int KEYS>
+template <int TOKENS, int KEYS, bool KEPT = false>
 __device__ __forceinline__ bool next_unit(const PParams& p, const Schedule& sc, int& k, Unit& u) {
   if (sc.n_units >= 0) {
     if (k >= sc.n_units) return false;
@@ -100,8 +104,14 @@ __device__ __forceinline__ bool next_unit(const PParams& p, const Schedule& sc, 
     const int tg = sc.unit_tg[k];
     u.tile = tg >> 6;
     u.g = tg & 63;
+    if (KEPT) {
+      u.q0 = sc.unit_q0[k];
+      u.q_len = sc.unit_len[k];
+      u.L = sc.unit_L[k];
+    } else {
+      sequence_ok(p, u.s, &u.q0, &u.q_len, &u.L, false);
+    }
     ++k;
-    sequence_ok(p, u.s, &u.q0, &u.q_len, &u.L, false);
     fill_unit<TOKENS, KEYS>(u);
     return true;
   }
@@ -151,9 +161,13 @@ __device__ __forceinline__ int block_exclusive_scan(int v, int* scratch, int* to
 // first (a stable counting sort on 64 buckets: ranks within a bucket come from warp matches
 // in pair order, THREADS pairs per round), and take this CTA's units.  Returns the unit count, or
 // -1 when the batch has more pairs than the sort handles (grid order then).
-template <int TOKENS, int KEYS, int THREADS>
+// RANK_PAIRS > 0: up to that many pairs are ranked directly, each thread counting the pairs that
+// come before its own (fewer barriers than the counting sort), and unit_q0 / unit_len / unit_L
+// keep each unit's sequence for next_unit<.., true>.
+template <int TOKENS, int KEYS, int THREADS, int RANK_PAIRS = 0>
 __device__ int plan_units(const PParams& p, uint8_t* scratch, int* red, int32_t* unit_s,
-                          int32_t* unit_tg) {
+                          int32_t* unit_tg, int32_t* unit_q0 = nullptr, int32_t* unit_len = nullptr,
+                          int32_t* unit_L = nullptr) {
   const int tid = threadIdx.x;
   const int lane = tid & 31, warp = tid >> 5;
   constexpr int kWarpsP = THREADS / 32;
@@ -185,61 +199,77 @@ __device__ int plan_units(const PParams& p, uint8_t* scratch, int* red, int32_t*
   const int units = n * p.num_kv_heads;
   const int G = gridDim.x;
   if (n > kMaxSortPairs || (units + G - 1) / G > kMaxUnitsPerCta) return -1;
-  for (int i = tid; i < kSortBuckets * (kWarpsP + 1); i += THREADS) base[i] = 0;  // + wcnt
-  __syncthreads();  // the pairs written above are read by other threads below
-  // 2. largest work, then bucket = work scaled to 0..63 (heavier = higher)
-  int wmax = 0;
-  for (int i = tid; i < n; i += THREADS) wmax = max(wmax, pair_w[i]);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) wmax = max(wmax, __shfl_xor_sync(0xffffffffu, wmax, d));
-  if (lane == 0) red[8 + warp] = wmax;
-  __syncthreads();
-  wmax = 0;
-  for (int w = 0; w < kWarpsP; ++w) wmax = max(wmax, red[8 + w]);
-  auto bucket = [&](int i) {
-    const int b = static_cast<int>((static_cast<int64_t>(pair_w[i]) * kSortBuckets) / (wmax + 1));
-    return min(max(b, 0), kSortBuckets - 1);
-  };
-  for (int i = tid; i < n; i += THREADS) atomicAdd(&base[bucket(i)], 1);
-  __syncthreads();
-  // 3. bucket starts, heaviest bucket first (one warp, two buckets per lane)
-  if (warp == 0) {
-    const int hi = base[kSortBuckets - 1 - 2 * lane], lo = base[kSortBuckets - 2 - 2 * lane];
-    int incl = hi + lo;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += x;
-    }
-    const int start = incl - hi - lo;
-    base[kSortBuckets - 1 - 2 * lane] = start;
-    base[kSortBuckets - 2 - 2 * lane] = start + hi;
-  }
-  __syncthreads();
-  // 4. stable placement, pair i = round * THREADS + tid: its rank in its bucket counts the pairs of
-  // earlier rounds (base), of earlier warps in this round (wcnt) and of lower lanes (match)
-  for (int r0 = 0; r0 < n; r0 += THREADS) {
-    const int i = r0 + tid;
-    const int b = i < n ? bucket(i) : kSortBuckets;  // kSortBuckets: no pair
-    const unsigned same = __match_any_sync(0xffffffffu, b);
-    const int rank = __popc(same & ((1u << lane) - 1u));
-    if (b < kSortBuckets && rank == 0) wcnt[warp * kSortBuckets + b] = __popc(same);
+  const bool rank = n <= RANK_PAIRS;  // uniform
+  if (rank) {
     __syncthreads();
-    if (b < kSortBuckets) {
-      int before = base[b] + rank;
-      for (int w = 0; w < warp; ++w) before += wcnt[w * kSortBuckets + b];
+    for (int i = tid; i < n; i += THREADS) {
+      const int w = pair_w[i];
+      int before = 0;
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) {
+        const int x = pair_w[j];
+        before += x > w || (x == w && j < i);
+      }
       sorted[before] = i;
     }
     __syncthreads();
-    if (tid < kSortBuckets) {
-      int add = 0;
-      for (int w = 0; w < kWarpsP; ++w) {
-        add += wcnt[w * kSortBuckets + tid];
-        wcnt[w * kSortBuckets + tid] = 0;
+  } else {
+    for (int i = tid; i < kSortBuckets * (kWarpsP + 1); i += THREADS) base[i] = 0;  // + wcnt
+    __syncthreads();  // the pairs written above are read by other threads below
+    // 2. largest work, then bucket = work scaled to 0..63 (heavier = higher)
+    int wmax = 0;
+    for (int i = tid; i < n; i += THREADS) wmax = max(wmax, pair_w[i]);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) wmax = max(wmax, __shfl_xor_sync(0xffffffffu, wmax, d));
+    if (lane == 0) red[8 + warp] = wmax;
+    __syncthreads();
+    wmax = 0;
+    for (int w = 0; w < kWarpsP; ++w) wmax = max(wmax, red[8 + w]);
+    auto bucket = [&](int i) {
+      const int b = static_cast<int>((static_cast<int64_t>(pair_w[i]) * kSortBuckets) / (wmax + 1));
+      return min(max(b, 0), kSortBuckets - 1);
+    };
+    for (int i = tid; i < n; i += THREADS) atomicAdd(&base[bucket(i)], 1);
+    __syncthreads();
+    // 3. bucket starts, heaviest bucket first (one warp, two buckets per lane)
+    if (warp == 0) {
+      const int hi = base[kSortBuckets - 1 - 2 * lane], lo = base[kSortBuckets - 2 - 2 * lane];
+      int incl = hi + lo;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += x;
       }
-      base[tid] += add;
+      const int start = incl - hi - lo;
+      base[kSortBuckets - 1 - 2 * lane] = start;
+      base[kSortBuckets - 2 - 2 * lane] = start + hi;
     }
     __syncthreads();
+    // 4. stable placement, pair i = round * THREADS + tid: its rank in its bucket counts the pairs of
+    // earlier rounds (base), of earlier warps in this round (wcnt) and of lower lanes (match)
+    for (int r0 = 0; r0 < n; r0 += THREADS) {
+      const int i = r0 + tid;
+      const int b = i < n ? bucket(i) : kSortBuckets;  // kSortBuckets: no pair
+      const unsigned same = __match_any_sync(0xffffffffu, b);
+      const int rank = __popc(same & ((1u << lane) - 1u));
+      if (b < kSortBuckets && rank == 0) wcnt[warp * kSortBuckets + b] = __popc(same);
+      __syncthreads();
+      if (b < kSortBuckets) {
+        int before = base[b] + rank;
+        for (int w = 0; w < warp; ++w) before += wcnt[w * kSortBuckets + b];
+        sorted[before] = i;
+      }
+      __syncthreads();
+      if (tid < kSortBuckets) {
+        int add = 0;
+        for (int w = 0; w < kWarpsP; ++w) {
+          add += wcnt[w * kSortBuckets + tid];
+          wcnt[w * kSortBuckets + tid] = 0;
+        }
+        base[tid] += add;
+      }
+      __syncthreads();
+    }
   }
   // 5. this CTA's units: a snake over the sorted order, K/V head fastest
   const int c = blockIdx.x;
@@ -254,6 +284,7 @@ __device__ int plan_units(const PParams& p, uint8_t* scratch, int* red, int32_t*
     const int pr = sorted[pos / p.num_kv_heads];
     unit_s[k] = pair_s[pr];
     unit_tg[k] = pair_t[pr] * 64 + pos % p.num_kv_heads;
+    if (unit_q0 != nullptr) sequence_ok(p, pair_s[pr], &unit_q0[k], &unit_len[k], &unit_L[k], false);
   }
   return mine;
 }

@@ -70,7 +70,8 @@ constexpr int kBarOff = kXchOff + 2 * 3 * 2 * kTileM * 4;
 constexpr int kNumBars = 4 + 4 + 2 + 6 * kRing + 5 * 2 + 1;
 constexpr int kMiscOff = kBarOff + (kNumBars + 1) / 2 * 16;
 constexpr int kUnitOff = kMiscOff + 160;
-constexpr int kSmemBytes = kUnitOff + 2 * kMaxUnitsPerCta * 4;
+constexpr int kSmemBytes = kUnitOff + 5 * kMaxUnitsPerCta * 4;
+constexpr int kRankPairs = 256;  // up to this many (sequence, tile) pairs are ranked by counting
 static_assert(kSmemBytes <= 227 * 1024, "one CTA per SM");
 static_assert(sort_scratch_bytes(kThreads) <= kRawOff, "sort scratch fits below the raw ring");
 constexpr uint32_t kTmemCols = 512;
@@ -228,6 +229,9 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
   int* red = misc + 4;  // 32 ints of scan scratch
   int32_t* unit_s = reinterpret_cast<int32_t*>(smem + kUnitOff);
   int32_t* unit_tg = unit_s + kMaxUnitsPerCta;
+  int32_t* unit_q0 = unit_tg + kMaxUnitsPerCta;
+  int32_t* unit_len = unit_q0 + kMaxUnitsPerCta;
+  int32_t* unit_L = unit_len + kMaxUnitsPerCta;
 
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
@@ -259,7 +263,8 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
     tmem_relinquish();
   }
   if (warp == kProducerWarp && lane == 0) prefetch_tensormap(&tmap_q);
-  const int n_units = plan_units<kUnitTokens, kTileN, kThreads>(p, smem, red, unit_s, unit_tg);
+  const int n_units = plan_units<kUnitTokens, kTileN, kThreads, kRankPairs>(
+      p, smem, red, unit_s, unit_tg, unit_q0, unit_len, unit_L);
   if (tid == 0) *n_units_s = n_units;
   fence_proxy_async_smem();  // the plan's scratch before copies and MMAs touch the buffers
   tc_fence_before_sync();
@@ -270,6 +275,9 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
   sc.unit_s = unit_s;
   sc.unit_tg = unit_tg;
   sc.n_units = *n_units_s;
+  sc.unit_q0 = unit_q0;
+  sc.unit_len = unit_len;
+  sc.unit_L = unit_L;
 
   if (warp < 2 * kRowWarps) {
     // ============================ row warps ============================
@@ -353,7 +361,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
       __nv_bfloat16* dst;
       {
         Unit u;
-        if (!next_unit<kUnitTokens, kTileN>(p, sc, k, u)) break;
+        if (!next_unit<kUnitTokens, kTileN, true>(p, sc, k, u)) break;
         n_mine = half_tiles<kHalfTokens>(u, half);
         n_kv = u.n_kv;
         const int token = u.tok0 + half * kHalfTokens + tt;
@@ -363,7 +371,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
         dst = p.out + (static_cast<int64_t>(u.q0 + token) * p.num_q_heads + u.g * GROUP + hh) * kHeadDim +
               part * (kHeadDim / 2);
         int peek = k;
-        next_mine = next_unit<kUnitTokens, kTileN>(p, sc, peek, u) && half_tiles<kHalfTokens>(u, half) > 0;
+        next_mine = next_unit<kUnitTokens, kTileN, true>(p, sc, peek, u) && half_tiles<kHalfTokens>(u, half) > 0;
       }
       if (n_mine > 0) {
         if (!have_q && !(ok = convert_q())) break;
@@ -504,7 +512,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
       uint32_t ph = 0;
       Unit cur;
       bool ok = true;
-      while (ok && next_unit<kUnitTokens, kTileN>(p, sc, k, cur)) {
+      while (ok && next_unit<kUnitTokens, kTileN, true>(p, sc, k, cur)) {
         for (int j = 0; j < cur.n_kv; ++j) {
           ok = wait_ready(&raw_full[st], ph, &abort_flag, p.status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -567,7 +575,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
       uint32_t ph = 0;
       Unit cur;
       bool ok = true;
-      while (ok && next_unit<kUnitTokens, kTileN>(p, sc, k, cur)) {
+      while (ok && next_unit<kUnitTokens, kTileN, true>(p, sc, k, cur)) {
         for (int j = 0; j < cur.n_kv; ++j) {
           ok = wait_ready(&raw_full[st], ph, &abort_flag, p.status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -707,8 +715,8 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
       };
       int k = 0;
       Unit cur, nxt;
-      bool have = next_unit<kUnitTokens, kTileN>(p, sc, k, cur);
-      bool have_next = have && next_unit<kUnitTokens, kTileN>(p, sc, k, nxt);
+      bool have = next_unit<kUnitTokens, kTileN, true>(p, sc, k, cur);
+      bool have_next = have && next_unit<kUnitTokens, kTileN, true>(p, sc, k, nxt);
       int n0 = 0, n1 = 0;
       bool ok = have;
       if (have) {
@@ -732,7 +740,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
         n0 = m0;
         n1 = m1;
         have = have_next;
-        if (have) have_next = next_unit<kUnitTokens, kTileN>(p, sc, k, nxt);
+        if (have) have_next = next_unit<kUnitTokens, kTileN, true>(p, sc, k, nxt);
       }
       // wait (bounded) until every MMA issued above has completed
       if (leader) {
@@ -744,8 +752,8 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
       // ============================ producer ============================
       int k = 0;
       Unit cur, nxt;
-      bool have = next_unit<kUnitTokens, kTileN>(p, sc, k, cur);
-      bool have_next = have && next_unit<kUnitTokens, kTileN>(p, sc, k, nxt);
+      bool have = next_unit<kUnitTokens, kTileN, true>(p, sc, k, cur);
+      bool have_next = have && next_unit<kUnitTokens, kTileN, true>(p, sc, k, nxt);
       int nq[2] = {0, 0};  // Qs requested for each half
       auto load_q = [&](const Unit& u) {
         bool ok = true;
@@ -824,7 +832,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
         }
         cur = nxt;
         have = have_next;
-        if (have) have_next = next_unit<kUnitTokens, kTileN>(p, sc, k, nxt);
+        if (have) have_next = next_unit<kUnitTokens, kTileN, true>(p, sc, k, nxt);
       }
       // leave no copy in flight: wait (bounded) for the last Q of each buffer and the last
       // fill of each stage
