@@ -149,6 +149,9 @@ bool encode_pool_rows(CUtensorMap* map, const void* base, uint64_t rows, uint32_
 bool encode_query_tiles(CUtensorMap* map, const void* base, uint64_t tokens, uint64_t heads,
                         uint32_t box_heads, uint32_t box_tokens);
 
+// Tensor map of an 8-bit pool as [tiles][1 KiB], for loads that gather four tiles.
+bool encode_tile_rows(CUtensorMap* map, const void* base, uint64_t tiles);
+
 struct PrefillArgs {
   void* out;
   const void* q;

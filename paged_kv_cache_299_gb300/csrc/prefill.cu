@@ -587,6 +587,20 @@ bool encode_pool_rows(CUtensorMap* map, const void* base, uint64_t rows, uint32_
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The 8-bit pool as [tiles][1 KiB] rows (of 256 32-bit words), one row per box: for gathering
+// loads of four rows.
+bool encode_tile_rows(CUtensorMap* map, const void* base, uint64_t tiles) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {256, tiles};
+  cuuint64_t strides[1] = {1024};
+  cuuint32_t box[2] = {256, 1};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // q as [tokens][heads][64] in boxes of box_tokens tokens x box_heads heads (the MMA rows of a
 // query tile), 128-byte swizzle.
 bool encode_query_tiles(CUtensorMap* map, const void* base, uint64_t tokens, uint64_t heads,

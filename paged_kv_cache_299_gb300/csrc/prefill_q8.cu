@@ -29,8 +29,10 @@
 //     codes and write it in the 128-byte-swizzled layout that the MMAs read, into rings of
 //     three each.
 //   * Warp 20: one elected lane issues S = Q K^T (M128 N128 K64) and O += P V (M128 N64 K128).
-//   * Warp 21: one bulk copy per (block, pool) into a ring of three raw tiles, the blocks'
-//     scales beside them by 4-byte asynchronous copies on the same mbarrier; Q by TMA.
+//   * Warp 21: four gathering TMA copies per tile (four blocks of one pool each) into a ring of
+//     three raw tiles, the blocks' scales beside them by 4-byte asynchronous copies on the same
+//     mbarrier; Q by TMA.  (One bulk copy per block and pool took some 1,600 cycles a tile to
+//     issue.)
 // Every mbarrier wait is bounded; on timeout the CTA records PA_DEVFLAG_TIMEOUT, drains its
 // own copies and MMAs, frees its tensor memory and returns.
 #include <cuda_fp16.h>
@@ -86,8 +88,6 @@ constexpr int kRowRegs = 96;
 constexpr int kOtherRegs = 48;
 
 struct Pools {
-  const uint8_t* key;
-  const uint8_t* value;
   const float* key_scale;
   const float* value_scale;
 };
@@ -98,11 +98,14 @@ __device__ __forceinline__ bool wait_ready(uint64_t* bar, uint32_t parity, volat
   return mbar_try_wait(bar, parity) || wait_or_abort(bar, parity, abort_flag, status);
 }
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+// Four 1 KiB tiles of a pool, rows[0..3] of its [tiles][1 KiB] view, by one copy.
+__device__ __forceinline__ void gather4(void* dst, const CUtensorMap* map, const int32_t* rows,
+                                        uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_addr(dst)),
-      "l"(src), "r"(bytes), "r"(smem_addr(bar))
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(rows[0]), "r"(rows[1]), "r"(rows[2]),
+      "r"(rows[3]), "r"(smem_addr(bar))
       : "memory");
 }
 __device__ __forceinline__ void async_copy4(void* dst, const void* src) {
@@ -183,7 +186,9 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
 
 template <int GROUP>
 __global__ void __launch_bounds__(kThreads, 1)
-paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams p, const Pools pools) {
+paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                      const __grid_constant__ CUtensorMap tmap_k,
+                      const __grid_constant__ CUtensorMap tmap_v, const PParams p, const Pools pools) {
   constexpr int kHalfTokens = kTileM / GROUP;
   constexpr int kUnitTokens = 2 * kHalfTokens;
   const int tid = threadIdx.x;
@@ -262,7 +267,11 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
-  if (warp == kProducerWarp && lane == 0) prefetch_tensormap(&tmap_q);
+  if (warp == kProducerWarp && lane == 0) {
+    prefetch_tensormap(&tmap_q);
+    prefetch_tensormap(&tmap_k);
+    prefetch_tensormap(&tmap_v);
+  }
   const int n_units = plan_units<kUnitTokens, kTileN, kThreads, kRankPairs>(
       p, smem, red, unit_s, unit_tg, unit_q0, unit_len, unit_L);
   if (tid == 0) *n_units_s = n_units;
@@ -750,6 +759,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
       __syncwarp();
     } else if (warp == kProducerWarp) {
       // ============================ producer ============================
+      const bool leader = elect_one();
       int k = 0;
       Unit cur, nxt;
       bool have = next_unit<kUnitTokens, kTileN, true>(p, sc, k, cur);
@@ -802,31 +812,27 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const PParams 
           const int32_t entry =
               __shfl_sync(0xffffffffu, win, (lb0 - win_base) + (lane & (kBlocksPerTile - 1)));
           const bool bad = need && (entry < 0 || entry >= p.num_blocks);
-          const bool load = need && !bad;
-          const unsigned mask = __ballot_sync(0xffffffffu, load);
           if (__any_sync(0xffffffffu, bad) && lane == 0) flag_error(p.status, PA_DEVFLAG_BAD_BLOCK);
-          int go = 1;
-          if (lane == 0) {
-            go = wait_ready(&raw_empty[st], static_cast<uint32_t>((jt / kRing) & 1) ^ 1u, &abort_flag,
-                               p.status);
-            if (go) mbar_arrive_expect_tx(&raw_full[st], __popc(mask) * 2u * kQ8TileBytes);
-          }
-          go = __shfl_sync(0xffffffffu, go, 0);
-          if (!go) {
-            ok = false;
-            break;
+          // tile (row) of each block; one that is not needed, or bad, brings the pool's first
+          const int32_t tile = need && !bad ? entry * p.num_kv_heads + cur.g : 0;
+          int32_t rows[kBlocksPerTile];
+#pragma unroll
+          for (int b = 0; b < kBlocksPerTile; ++b) rows[b] = __shfl_sync(0xffffffffu, tile, b);
+          ok = wait_ready(&raw_empty[st], static_cast<uint32_t>((jt / kRing) & 1) ^ 1u, &abort_flag, p.status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (leader) {
+            mbar_arrive_expect_tx(&raw_full[st], kRawBytes);
+            uint8_t* dst = sraw + st * kRawBytes;
+#pragma unroll
+            for (int b = 0; b < kBlocksPerTile; b += 4) {
+              gather4(dst + b * kQ8TileBytes, &tmap_k, &rows[b], &raw_full[st]);
+              gather4(dst + (kBlocksPerTile + b) * kQ8TileBytes, &tmap_v, &rows[b], &raw_full[st]);
+            }
           }
           if (lane < kBlocksPerTile) {
-            if (load) {
-              const int64_t tile = static_cast<int64_t>(entry) * p.num_kv_heads + cur.g;
-              uint8_t* dst = sraw + st * kRawBytes + lane * kQ8TileBytes;
-              bulk_load(dst, pools.key + tile * kQ8TileBytes, kQ8TileBytes, &raw_full[st]);
-              bulk_load(dst + kTileN * kQ8RowBytes, pools.value + tile * kQ8TileBytes, kQ8TileBytes,
-                        &raw_full[st]);
-              float* s = raw_scale + st * 2 * kBlocksPerTile + lane;
-              async_copy4(s, pools.key_scale + tile);
-              async_copy4(s + kBlocksPerTile, pools.value_scale + tile);
-            }
+            float* s = raw_scale + st * 2 * kBlocksPerTile + lane;
+            async_copy4(s, pools.key_scale + tile);
+            async_copy4(s + kBlocksPerTile, pools.value_scale + tile);
             async_arrive(&raw_full[st]);
           }
         }
@@ -885,6 +891,10 @@ cudaError_t launch(const AttendQ8Args& a, cudaStream_t stream) {
   if (!encode_query_tiles(&tq, a.q, static_cast<uint64_t>(a.num_query_tokens), a.num_q_heads, GROUP,
                           kTileM / GROUP))
     return cudaErrorInvalidValue;
+  CUtensorMap tk, tv;
+  const uint64_t tiles = static_cast<uint64_t>(a.num_blocks) * a.num_kv_heads;
+  if (!encode_tile_rows(&tk, a.key_cache, tiles) || !encode_tile_rows(&tv, a.value_cache, tiles))
+    return cudaErrorInvalidValue;
   PParams p = {};
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.query_start_loc = a.query_start_loc;
@@ -901,13 +911,12 @@ cudaError_t launch(const AttendQ8Args& a, cudaStream_t stream) {
   constexpr int kUnitTokens = 2 * kTileM / GROUP;
   p.q_tiles = (a.max_query_len + kUnitTokens - 1) / kUnitTokens;
   p.skip_single = 0;
-  const Pools pools = {static_cast<const uint8_t*>(a.key_cache), static_cast<const uint8_t*>(a.value_cache),
-                       a.key_scale, a.value_scale};
+  const Pools pools = {a.key_scale, a.value_scale};
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * p.q_tiles;
   const int64_t grid = units < sms ? units : sms;
   if (grid < 1) return cudaSuccess;
-  paged_chunk_q8_kernel<GROUP><<<static_cast<unsigned>(grid), kThreads, kSmemBytes, stream>>>(tq, p, pools);
+  paged_chunk_q8_kernel<GROUP><<<static_cast<unsigned>(grid), kThreads, kSmemBytes, stream>>>(tq, tk, tv, p, pools);
   return cudaGetLastError();
 }
 
