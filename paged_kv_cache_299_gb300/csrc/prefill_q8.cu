@@ -525,6 +525,10 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q,
         for (int j = 0; j < cur.n_kv; ++j) {
           ok = wait_ready(&raw_full[st], ph, &abort_flag, p.status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          const uint8_t* raw = sraw + st * kRawBytes + kTileN * kQ8RowBytes + cw * kMyBlocks * kQ8TileBytes + 16 * lane;
+          uint4 in[2 * kMyBlocks];
+#pragma unroll
+          for (int i = 0; i < 2 * kMyBlocks; ++i) in[i] = lds128(raw + i * 512);
           uint32_t my_m = 0u;  // lane b: 2^(120 + e) of block b's value scale, a bf16 pair
           int my_high = 0;     // e where 120 + e is beyond bf16: then my_m is 2^120
           if (lane < kMyBlocks) {
@@ -538,12 +542,11 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q,
           const bool any_high = __any_sync(0xffffffffu, my_high != 0);
           ok = wait_ready(&v_empty[st], ph ^ 1u, &abort_flag, p.status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          const uint8_t* raw = sraw + st * kRawBytes + kTileN * kQ8RowBytes + cw * kMyBlocks * kQ8TileBytes + 16 * lane;
           uint8_t* dst = sv + st * kOpBytes;
           const int keys_left = cur.keys - j * kTileN - row0;
 #pragma unroll
           for (int i = 0; i < 2 * kMyBlocks; ++i) {
-            uint4 w = lds128(raw + i * 512);
+            uint4 w = in[i];
             // keys past the last needed one weigh nothing, but may hold anything
             if (8 * i >= keys_left) w = make_uint4(0u, 0u, 0u, 0u);
             uint4 a, b;
