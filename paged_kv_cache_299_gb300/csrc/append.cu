@@ -20,7 +20,7 @@ namespace pkv {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;  // (256: 36.3 us against 35.1 for 16k prompt tokens into the 8-bit pools)
 constexpr int kWarpsPerCta = kThreads / 32;
 constexpr int kPairs = kHeadDim / 2;
 constexpr int kLanePairs = 8;                     // rotation pairs per lane: 16 dims, 32 bytes
