@@ -27,7 +27,9 @@
 //     [2^13, 2^14): a bf16 significand fits, and elements down to 2^-27 of the largest keep
 //     all their bits;
 //   * p enters as f16 times 2^7 (at most 2^15 under the lazy maximum), so weights down to
-//     2^-31 of the largest survive; half a step of f16, 2^-12, is their rounding.
+//     2^-31 of the largest survive; half a step of f16, 2^-12, is their rounding.  The value
+//     scales carry 2^-15 (a power of two, so exact), which keeps the sums of p V at the size of
+//     the values: they would pass fp32's range 2^15 earlier otherwise.
 #include <math.h>
 
 #include "common.cuh"
@@ -49,6 +51,7 @@ constexpr int kFusedMergeMaxContext = 8192;   // longer ones merge in the parall
 constexpr int kFusedMergeMaxPieces = 24;      // as do segments of more pieces than this
 constexpr int kSegmentUnits = 2;  // what a piece costs besides its tiles, in tiles
 constexpr float kPShift = 7.f;                // log2 of the factor on p
+constexpr float kVFactor = 1.f / 32768.f;     // 2^-(kPShift + 8): on the value scales, and on l
 constexpr int kQExp = 13;                     // exponent of a row's largest f16 query element
 static_assert(kStages <= kWindow, "a window's scales are loaded a ring's length ahead");
 
@@ -193,8 +196,8 @@ __device__ __forceinline__ void attend_pair(const uint8_t* ta, const uint8_t* tb
 }
 
 // Publishes a piece whose partial this warp has written; the warp that publishes the segment's
-// last piece merges them all, with CTA-scope ordering when they all ran on this CTA.  Not
-// inlined: the tile loop's registers are allocated without it.
+// last piece merges them all, with CTA-scope ordering when they all ran on this CTA.  (A call
+// in its place measured slower.)
 template <int GROUP>
 __device__ __forceinline__ void publish_piece(const KParams& p, const int32_t* seq_base,
                                            int* cta_seg_count, int s, int g, int nb, int64_t units,
@@ -354,7 +357,7 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
     const bool live = lane < w.n && !bad;
     w.tile = live ? w.tile * KV + w.g : -1;
     nxt_ks = live ? __ldg(sp8.key_scale + w.tile) : 0.f;
-    nxt_vs = live ? __ldg(sp8.value_scale + w.tile) : 0.f;
+    nxt_vs = live ? __ldg(sp8.value_scale + w.tile) * kVFactor : 0.f;
     if (__any_sync(0xffffffffu, bad) && lane == 0) flag_error(p.status, PA_DEVFLAG_BAD_BLOCK);
   };
   Window cur = next_window();
@@ -551,6 +554,7 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
     }
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
+    l *= kVFactor;  // as o, through the value scales
     if (r < GROUP) {
       if (whole) {
         const float inv = 1.f / l;

@@ -171,6 +171,7 @@ __device__ int plan_units(const PParams& p, uint8_t* scratch, int* red, int32_t*
   const int tid = threadIdx.x;
   const int lane = tid & 31, warp = tid >> 5;
   constexpr int kWarpsP = THREADS / 32;
+  static_assert(kWarpsP <= 24, "red holds 32 ints, the warps' from the ninth on");
   int* pair_s = reinterpret_cast<int*>(scratch);  // [kMaxSortPairs]
   int* pair_t = pair_s + kMaxSortPairs;
   int* pair_w = pair_t + kMaxSortPairs;

@@ -80,7 +80,10 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 0;    // + 128 per half: fp32 scores
 constexpr uint32_t kPCol = 256;  // + 64 per half: bf16 pairs
 constexpr uint32_t kOCol = 384;  // + 64 per half: fp32
-constexpr float kRescaleThreshold = 8.0f;
+// The exponent reference m is set this much (log2) above the largest score so far and raised
+// when a score passes it: weights stay below 2, so the sums of p V keep the size of the values,
+// and a row rescales only when its maximum grows by more than 2^8.
+constexpr float kHeadroom = 8.0f;
 constexpr int kQExp = 13;  // exponent of a row's largest f16 query element
 // Register split (setmaxnreg): the row warps' threads and the others' share what the CTA was
 // launched with; the launcher checks that it suffices.
@@ -421,16 +424,17 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q,
           float f[kBlocksPerTile / 2];  // score factors of this warp's blocks
           lds_f32x4(cs, f);
 #pragma unroll
-          for (int b = 0; b < kBlocksPerTile / 2; ++b) f[b] *= q_factor;
+          for (int b = 0; b < kBlocksPerTile / 2; ++b)
+            f[b] = fmaxf(f[b] * q_factor, 1.17549435e-38f);  // not 0: -inf (hidden) * 0 is a NaN
           const float mt = fmaxf(max3f(bm[0] * f[0], bm[1] * f[1], bm[2] * f[2]), bm[3] * f[3]);
           int gone;
           const float theirs = exchange(c & 1, mt, gone);
           const float m_new = max3f(m, mt, theirs);
-          const bool grow = m_new - m > kRescaleThreshold;  // true on the first tile
+          const bool grow = m_new > m;  // true on the first tile
           float alpha = 1.f;
           if (grow) {
-            alpha = fast_exp2(m - m_new);
-            m = m_new;
+            alpha = fast_exp2(m - (m_new + kHeadroom));
+            m = m_new + kHeadroom;
           }
           l *= alpha;
           // p' two at a time, packed to bf16 over the scores

@@ -340,6 +340,40 @@ def test_chunk_bad_entries_are_reported():
     assert int(st.status.item()) == pa.DEVFLAG_BAD_CONTEXT
 
 
+@pytest.mark.parametrize("q_exp,key_exp,value_exp", [
+    (-14, "smallest", 0), (-30, "smallest", -126), (-14, "zero", 0), (-100, 100, 100), (-110, 110, -60),
+    (60, -70, 118), (0, -126, 0)])
+def test_extreme_scales(q_exp, key_exp, value_exp):
+    """Queries and scales far apart: products of a block's scale and a row's that vanish (blocks
+    of zero keys, whose scale is the smallest there is, or a scale of zero), and ones that meet
+    again from both ends of the range."""
+    w = wl.make_workload("far", [0, 40, 300, 7], [1, 130, 33, 16], num_prefill=4, seed=17, pool_slack=0.5)
+    st = State(w, 2, 8, rows=180, spread=0.0)
+    st.q = (st.q.double() * 2.0 ** q_exp).to(torch.bfloat16)
+    k, v, ks, vs = (x.cpu() for x in st.dev)
+    live = ~torch.isnan(ks)
+    if key_exp == "smallest":
+        zero = live[..., None, None] & (k.view(torch.uint8) != 0x7f)
+        k = torch.where(zero, torch.zeros((), dtype=torch.uint8), k.view(torch.uint8)).view(torch.float8_e4m3fn)
+        ks = torch.where(live, torch.full_like(ks, 2.0 ** -126), ks)
+    elif key_exp == "zero":
+        ks = torch.where(live, torch.zeros_like(ks), ks)
+    else:
+        ks = ks * 2.0 ** key_exp
+    vs = vs * 2.0 ** (value_exp + (8 if value_exp < -100 else 0))  # (normal floats)
+    st.dev = [x.cuda() for x in (k, v, ks, vs)]
+    st.k64, st.v64 = dequantise(k, ks), dequantise(v, vs)
+    ref, tol = attend(st.q, st.k64, st.v64, w.block_tables, w.context_lens, st.scale, w.new_lens)
+    got = st.chunk()
+    assert st.ok()
+    close(got, ref, tol + 2.0 ** -126, "chunk")  # (what falls below the normal floats may vanish)
+    last = torch.tensor(np.cumsum(w.new_lens) - 1)
+    st.q = st.q[last]
+    got = st.decode()
+    assert st.ok()
+    close(got, ref[last], tol[last] + 2.0 ** -126, "decode")
+
+
 # ---- against the oracle, and far into a large pool --------------------------------------------
 def test_agrees_with_the_oracle_on_the_dequantised_cache():
     """A code times a power of two is a bf16 value, so the oracle can read the same cache."""
