@@ -364,8 +364,9 @@ pa_status pa_copy_blocks(void* key_cache, void* value_cache, pa_cache_desc cd,
  *                    num_tokens == num_seqs, and a context of 0 marks a padding row)
  *   num_tokens       rows of q, key and value.  Rows at or past query_start_loc[num_seqs] are
  *                    padding: neither read nor written
- * A token whose position is negative, past its block-table row or at or past max_positions
- * sets PA_DEVFLAG_BAD_CONTEXT, a bad block id PA_DEVFLAG_BAD_BLOCK; such tokens are skipped.
+ * A token whose position is negative, past its block-table row or at or past max_positions, or
+ * of a sequence with rows at or past num_tokens, sets PA_DEVFLAG_BAD_CONTEXT, a bad block id
+ * PA_DEVFLAG_BAD_BLOCK; such tokens are skipped.
  * Two tokens of one call must not share a slot (the winner is undefined).
  * num_tokens == 0 is a no-op. */
 pa_status pa_rope_append(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,

@@ -30,7 +30,8 @@ constexpr int kUnroll = 3;  // rows a lane has in flight: 48 rows (32 + 2 x 8 he
 
 // Sequence of token t (the last s with query_start_loc[s] <= t; without query_start_loc,
 // sequence t) and its logical position.  false: the token is padding (at or past
-// query_start_loc[num_seqs], or a context of 0 in the one-token form) or was flagged.
+// query_start_loc[num_seqs], or a context of 0 in the one-token form) or was flagged.  (Rows past
+// num_tokens are flagged through token 0, as their own have no warp.)
 __device__ __forceinline__ bool locate(const AppendArgs& a, int32_t t, bool report, int32_t* seq,
                                        int64_t* pos) {
   int32_t s, first, q_len;
@@ -40,7 +41,9 @@ __device__ __forceinline__ bool locate(const AppendArgs& a, int32_t t, bool repo
     q_len = 1;
     if (a.context_lens[s] == 0) return false;
   } else {
-    if (t >= a.query_start_loc[a.num_seqs]) return false;
+    const int32_t end = a.query_start_loc[a.num_seqs];
+    if (t == 0 && report && end > a.num_tokens) flag_error(a.status, PA_DEVFLAG_BAD_CONTEXT);
+    if (t >= end) return false;
     int32_t lo = 0, hi = a.num_seqs - 1;
     while (lo < hi) {
       const int32_t mid = (lo + hi + 1) >> 1;
@@ -51,7 +54,7 @@ __device__ __forceinline__ bool locate(const AppendArgs& a, int32_t t, bool repo
     q_len = a.query_start_loc[s + 1] - first;
   }
   const int64_t p = static_cast<int64_t>(a.context_lens[s]) - q_len + (t - first);
-  if (p < 0 || t < first || t - first >= q_len ||
+  if (p < 0 || t < first || t - first >= q_len || q_len > a.num_tokens - first ||
       p >= static_cast<int64_t>(a.max_blocks_per_seq) * kBlockSize ||
       (a.cos_sin != nullptr && p >= a.max_positions) || a.context_lens[s] < q_len) {
     if (report) flag_error(a.status, PA_DEVFLAG_BAD_CONTEXT);
@@ -293,6 +296,8 @@ __device__ void block_rows(const AppendArgs& a, int64_t item, int lane) {
     first = a.query_start_loc[s];
     q_len = a.query_start_loc[s + 1] - first;
     index = v - ((first >> 4) + 2ll * s);
+    if (item == 0 && is_k && lane == 0 && a.query_start_loc[a.num_seqs] > a.num_tokens)
+      flag_error(a.status, PA_DEVFLAG_BAD_CONTEXT);
     if (q_len <= 0) return;
   }
   const int64_t ctx = a.context_lens[s];

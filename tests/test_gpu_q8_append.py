@@ -204,6 +204,20 @@ def test_bad_entries_are_reported_and_skipped():
         assert go(w.block_tables, w.context_lens, None, bad) == (pa.DEVFLAG_BAD_SCALE, 0)
 
 
+@pytest.mark.parametrize("starts", [[0, 3, 9], [0, 7, 9], [0, 9, 12]])
+def test_rows_past_the_buffer_are_reported(starts):
+    """Seven rows, and sequences that claim more: what lies past the buffer is reported and skipped."""
+    w = wl.make_workload("past", [10, 20], [9, 9], seed=11, pool_slack=0.5)
+    k = rows(7, 2, 1).cuda()
+    ctx = [10 + starts[1], 20 + starts[2] - starts[1]]
+    for table in (None, angles(64).cuda()):
+        status, c = pa.new_device_status(), pa.new_q8_cache(w.num_blocks, 2)
+        pa.pa_rope_append_q8(None, k, k, table, *c, i32(w.block_tables), i32(ctx), i32(starts), device_status=status)
+        assert int(status.item()) == pa.DEVFLAG_BAD_CONTEXT
+        stored = 0 if starts[1] > 7 else starts[1]  # the first sequence, where it ends within the rows
+        assert int((c[0].float() != 0).any(dim=3).sum()) == 2 * stored
+
+
 def test_repeat_graph_and_stream_are_bit_identical():
     w = wl.make_workload("side", [11, 300], [100, 257], seed=13, pool_slack=0.2)
     n = int(w.new_lens.sum())

@@ -138,6 +138,21 @@ def test_bad_entries_are_reported_and_skipped():
     assert int((kc != 0).any(dim=3).sum()) == (3 + 2) * 2
 
 
+@pytest.mark.parametrize("starts", [[0, 3, 9], [0, 7, 9], [0, 9, 12]])
+def test_rows_past_the_buffer_are_reported(starts):
+    """Seven rows, and sequences that claim more: what lies past the buffer is reported and skipped."""
+    w = wl.make_workload("past", [10, 20], [9, 9], seed=11, pool_slack=0.5)
+    k, table = rows(7, 2, 1).cuda(), angles(64).cuda()
+    status = pa.new_device_status()
+    kc = torch.zeros(w.num_blocks, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    ctx = [10 + starts[1], 20 + starts[2] - starts[1]]
+    pa.pa_rope_append(None, k, k, table, kc, vc, i32(w.block_tables), i32(ctx), i32(starts), device_status=status)
+    assert int(status.item()) == pa.DEVFLAG_BAD_CONTEXT
+    stored = 0 if starts[1] > 7 else starts[1]  # the first sequence, where it ends within the rows
+    assert int((kc != 0).any(dim=3).sum()) == 2 * stored
+
+
 def test_non_finite_rows_pass_through():
     """bf16 pools hold what the arithmetic gives: a NaN stays in its pair, the rest is exact."""
     w = wl.make_workload("nan", [0], [4], seed=12, pool_slack=1.0)
