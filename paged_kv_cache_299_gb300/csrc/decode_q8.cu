@@ -45,10 +45,8 @@ constexpr int kWarps = 12;   // streaming warps per CTA, one CTA per SM
 constexpr int kStages = 4;   // ring depth per warp: 8 KiB in flight
 constexpr int kStageBytes = 2 * kQ8TileBytes;
 constexpr int kWindow = 32;  // tiles whose block ids and scales are held in the lanes
-constexpr int kMinTilesPerRun = 2;
-constexpr int kOneSeqMaxTilesPerWarp = 4;     // one sequence up to this: one CTA per head
-constexpr int kFusedMergeMaxContext = 8192;   // longer ones merge in the parallel merge kernel,
-constexpr int kFusedMergeMaxPieces = 24;      // as do segments of more pieces than this
+constexpr int kMinUnitsPerRun = 2;
+constexpr int kOneSeqMaxUnits = 50;  // one sequence of up to 768 tokens: one CTA per head
 constexpr int kSegmentUnits = 2;  // what a piece costs besides its tiles, in tiles
 constexpr float kPShift = 7.f;                // log2 of the factor on p
 constexpr float kVFactor = 1.f / 32768.f;     // 2^-(kPShift + 8): on the value scales, and on l
@@ -195,44 +193,197 @@ __device__ __forceinline__ void attend_pair(const uint8_t* ta, const uint8_t* tb
   }
 }
 
-// Publishes a piece whose partial this warp has written; the warp that publishes the segment's
-// last piece merges them all, with CTA-scope ordering when they all ran on this CTA.  (A call
-// in its place measured slower.)
+// A piece's partial: per query head 64 floats of o, the maximum (log2 units) and the sum,
+// padded to 16 bytes.
+constexpr int kRecordFloats = kHeadDim + 4;
+
+// Folds n records of GROUP heads into (M, L) per head and acc, of dims 4 (lane % 16) .. + 3:
+// record k (k > 0) is at rec0 + k * step, record 0 at rec0 + off0.  Half warps take every other
+// record's rows, eight records a round.
 template <int GROUP>
-__device__ __forceinline__ void publish_piece(const KParams& p, const int32_t* seq_base,
-                                           int* cta_seg_count, int s, int g, int nb, int64_t units,
-                                           int lane) {
-  const int KV = p.num_kv_heads;
-  const int64_t x0 = unit_base<kSegmentUnits>(seq_base, s, KV) +
-                     static_cast<int64_t>(g) * (nb + kSegmentUnits) + kSegmentUnits;
-  const int64_t x1 = x0 + nb;  // units of the segment's tiles
-  SegmentPieces sp;
-  sp.c_first = run_of(x0, units, p.grid, 0);
-  sp.c_last = run_of(x1 - 1, units, p.grid, 0);
-  sp.first_slot = 1;  // as its writer chose
-  const int n = segment_piece_count(sp, x0, x1, units, p.grid);
-  int last = 0;
-  if (sp.c_first / kWarps == sp.c_last / kWarps) {
-    int* count = &cta_seg_count[sp.c_first % kWarps];
-    __threadfence_block();
-    __syncwarp();
-    if (lane == 0) last = atomicAdd(count, 1) == n - 1;
-    if (__shfl_sync(0xffffffffu, last, 0)) {
-      __threadfence_block();
-      merge_segment_in_warp<GROUP, true, false, 4>(p, sp, x0, x1, units, s, g, lane);
-      if (lane == 0) *count = 0;
+__device__ __forceinline__ void fold_records(const float* rec0, int64_t off0, int64_t step, int n,
+                                             int lane, float (&M)[GROUP], float (&L)[GROUP],
+                                             float4 (&acc)[GROUP]) {
+  const int hw = lane >> 4;
+  auto record = [&](int k) { return rec0 + (k == 0 ? off0 : k * step); };
+  float4 v[4][GROUP];
+  auto load_rows = [&](int k0, int last) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float* r = record(min(k0 + 2 * u + hw, last));
+#pragma unroll
+      for (int h = 0; h < GROUP; ++h)
+        v[u][h] = *reinterpret_cast<const float4*>(r + h * kRecordFloats + 4 * (lane & 15));
     }
-  } else {
-    int32_t* count = &p.seg_count[s * KV + g];
-    __threadfence();
-    __syncwarp();
-    if (lane == 0) last = atomicAdd(count, 1) == n - 1;
-    if (__shfl_sync(0xffffffffu, last, 0)) {
-      __threadfence();
-      merge_segment_in_warp<GROUP, false, false, 4>(p, sp, x0, x1, units, s, g, lane);
-      if (lane == 0) *count = 0;  // ready for the next call
+  };
+#pragma unroll
+  for (int h = 0; h < GROUP; ++h) {
+    M[h] = -INFINITY;
+    L[h] = 0.f;
+    acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll 1
+  for (int k0 = 0; k0 < n; k0 += 32) {  // lane k weighs record k0 + k
+    const int cnt = min(32, n - k0);
+    load_rows(k0, n - 1);
+    const float* mine = record(k0 + min(lane, cnt - 1));
+    float2 ml[GROUP];
+    float wk[GROUP];
+#pragma unroll
+    for (int h = 0; h < GROUP; ++h)
+      ml[h] = *reinterpret_cast<const float2*>(mine + h * kRecordFloats + kHeadDim);
+#pragma unroll
+    for (int h = 0; h < GROUP; ++h) {
+      float nm = ml[h].x;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, d));
+      nm = fmaxf(nm, M[h]);
+      const float keep = k0 == 0 ? 0.f : fast_exp2(M[h] - nm);
+      wk[h] = lane < cnt ? fast_exp2(ml[h].x - nm) : 0.f;
+      float lw = wk[h] * ml[h].y;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, d);
+      L[h] = L[h] * keep + lw;
+      acc[h].x *= keep;
+      acc[h].y *= keep;
+      acc[h].z *= keep;
+      acc[h].w *= keep;
+      M[h] = nm;
+    }
+#pragma unroll 1
+    for (int j0 = 0; j0 < cnt; j0 += 8) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int j = j0 + 2 * u + hw;
+#pragma unroll
+        for (int h = 0; h < GROUP; ++h) {
+          float w = __shfl_sync(0xffffffffu, wk[h], j & 31);
+          if (j >= cnt) w = 0.f;
+          acc[h].x += w * v[u][h].x;
+          acc[h].y += w * v[u][h].y;
+          acc[h].z += w * v[u][h].z;
+          acc[h].w += w * v[u][h].w;
+        }
+      }
+      if (j0 + 8 < cnt) load_rows(k0 + j0 + 8, n - 1);
     }
   }
+#pragma unroll
+  for (int h = 0; h < GROUP; ++h) {  // the two half warps' shares
+    acc[h].x += __shfl_xor_sync(0xffffffffu, acc[h].x, 16);
+    acc[h].y += __shfl_xor_sync(0xffffffffu, acc[h].y, 16);
+    acc[h].z += __shfl_xor_sync(0xffffffffu, acc[h].z, 16);
+    acc[h].w += __shfl_xor_sync(0xffffffffu, acc[h].w, 16);
+  }
+}
+
+// Where the partial of a split segment's piece goes, and how its pieces meet: those of one CTA
+// (its runs are consecutive) in shared memory, the CTAs' records in the workspace.
+struct Meeting {
+  int c_first;  // the segment's first run
+  int n_cta;    // CTAs it spans
+  int lo;       // this CTA's first run of it, and how many there are
+  int n_here;
+};
+
+__device__ __forceinline__ Meeting meeting_of(const int32_t* seq_base, int KV, const Piece& pc,
+                                              int64_t units, int runs) {
+  const int64_t x0 = unit_base<kSegmentUnits>(seq_base, pc.s, KV) +
+                     static_cast<int64_t>(pc.g) * (pc.nb + kSegmentUnits) + kSegmentUnits;
+  Meeting m;
+  m.c_first = static_cast<int>(run_of(x0, units, runs, 0));
+  const int c_last = static_cast<int>(run_of(x0 + pc.nb - 1, units, runs, 0));
+  m.n_cta = c_last / kWarps - m.c_first / kWarps + 1;
+  const int here = static_cast<int>(blockIdx.x) * kWarps;
+  m.lo = max(m.c_first, here);
+  m.n_here = min(c_last, here + kWarps - 1) - m.lo + 1;
+  return m;
+}
+
+// Record of run c: a run writes at most two partials, of the segment that it begins inside
+// (slot 0) and of the one that begins in it and goes on in the next run (slot 1).
+template <int GROUP>
+__device__ __forceinline__ int64_t record_of(int64_t c, bool begins) {
+  return (c * 2 + (begins ? 1 : 0)) * GROUP * kRecordFloats;
+}
+
+// Publishes a piece whose partial this warp has written.  The last of a CTA's pieces folds them
+// into one record; the last CTA folds the CTAs' records and writes the rows.  A segment within
+// one CTA is done after the first meeting.  Serial work per segment is thus a dozen records in
+// shared memory and one per CTA, however long the context, and no second kernel is needed.  The
+// order of the sums is that of the runs, whoever comes last.
+template <int GROUP>
+__device__ __forceinline__ void publish_piece(const KParams& p, const Meeting& m, const float* local,
+                                              int* cta_seg_count, int s, int g, int lane) {
+  const int here = static_cast<int>(blockIdx.x) * kWarps;
+#pragma unroll 1
+  for (int level = m.n_here > 1 ? 0 : 1; level < 2; ++level) {
+    int last = 0;
+    if (level == 0) {
+      // two segments with two runs each on this CTA never share the first of them
+      int* count = &cta_seg_count[m.lo - here];
+      __threadfence_block();
+      __syncwarp();
+      if (lane == 0) {
+        last = atomicAdd(count, 1) == m.n_here - 1;
+        if (last) *count = 0;
+      }
+    } else {
+      int32_t* count = &p.seg_count[s * p.num_kv_heads + g];
+      __threadfence();
+      __syncwarp();
+      if (lane == 0) {
+        last = atomicAdd(count, 1) == m.n_cta - 1;
+        if (last) *count = 0;  // ready for the next call
+      }
+    }
+    if (!__shfl_sync(0xffffffffu, last, 0)) return;
+    if (level == 0) __threadfence_block(); else __threadfence();
+    // (plain loads: the fence orders them after the counts of the records' writers)
+    float M[GROUP], L[GROUP];
+    float4 acc[GROUP];
+    const int64_t run_step = record_of<GROUP>(1, false);
+    if (level == 0)
+      fold_records<GROUP>(local + (m.lo - here) * run_step, m.lo == m.c_first ? run_step / 2 : 0, run_step,
+                          m.n_here, lane, M, L, acc);
+    else
+      fold_records<GROUP>(p.partials + m.c_first / kWarps * kWarps * run_step,
+                          m.c_first % kWarps * run_step + run_step / 2, kWarps * run_step, m.n_cta, lane, M,
+                          L, acc);
+    if (level == 1 || m.n_cta == 1) {
+      if (lane < 16) {
+#pragma unroll
+        for (int h = 0; h < GROUP; ++h) {
+          const float inv = 1.f / L[h];
+          __nv_bfloat16* out = p.out + (static_cast<int64_t>(s) * p.num_q_heads + g * GROUP + h) * kHeadDim;
+          *reinterpret_cast<uint2*>(out + 4 * lane) =
+              make_uint2(pack_bf16x2(acc[h].x * inv, acc[h].y * inv), pack_bf16x2(acc[h].z * inv, acc[h].w * inv));
+        }
+      }
+      return;
+    }
+    float* rec = p.partials + record_of<GROUP>(m.lo, m.lo == m.c_first);
+#pragma unroll
+    for (int h = 0; h < GROUP; ++h) {
+      if (lane < 16) *reinterpret_cast<float4*>(rec + h * kRecordFloats + 4 * lane) = acc[h];
+      if (lane == 16) *reinterpret_cast<float2*>(rec + h * kRecordFloats + kHeadDim) = make_float2(M[h], L[h]);
+    }
+  }
+}
+
+// Runs the units are divided into, of the p.grid that there is room for: at least kMinUnitsPerRun
+// units each.  A single short sequence takes a divisor of the CTA's warps per K/V head, so that
+// every head's pieces meet on one CTA.
+__device__ __forceinline__ int run_count(const KParams& p, int64_t units) {
+  if (p.num_seqs == 1) {
+    const int per_head = static_cast<int>(units / p.num_kv_heads);
+    if (per_head <= kOneSeqMaxUnits && p.num_kv_heads * kWarps <= p.grid) {
+      int d = kWarps;
+      while (d > per_head || kWarps % d != 0) --d;
+      return d * p.num_kv_heads;
+    }
+  }
+  return static_cast<int>(max(int64_t{1}, min(static_cast<int64_t>(p.grid), units / kMinUnitsPerRun)));
 }
 
 template <int GROUP>
@@ -251,7 +402,8 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
   uint8_t* ring = smem + warp * (kStages * kStageBytes);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kWarps * kStages * kStageBytes);
   uint64_t* full_bar = bars + warp * kStages;
-  int32_t* seq_base = reinterpret_cast<int32_t*>(bars + kWarps * kStages);
+  float* local = reinterpret_cast<float*>(bars + kWarps * kStages);  // [warp][2][GROUP] records
+  int32_t* seq_base = reinterpret_cast<int32_t*>(local + record_of<GROUP>(kWarps, false));
   __shared__ int64_t warp_sums[kWarps];
   // piece counters of split segments whose pieces all run on this CTA, by the segment's
   // first run modulo kWarps (two such segments never share a first run)
@@ -274,17 +426,18 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
   // From here on every warp works alone, on one run: the plan never makes more runs than
   // the grid has warps.
   const int gw = blockIdx.x * kWarps + warp;
-  if (gw >= p.grid) return;
+  const int64_t units = unit_base<kSegmentUnits>(seq_base, S, KV);
+  const int runs = run_count(p, units);
+  if (gw >= runs) return;
   const uint64_t policy = l2_evict_first_policy();
   const int r = lane >> 2;
   const int q = lane & 3;
   // The run's tiles: lane 0 locates its first unit, lane 1 the next run's, in one search.
   // (block_prefix keeps the tile count below 2^31, so units fit 32 unsigned bits.)
-  const int64_t units = unit_base<kSegmentUnits>(seq_base, S, KV);
   int start, stop;
   int wc_s, wc_off;  // sequence of tile wc_y and its place among the sequence's KV x nb tiles
   {
-    const uint32_t u32 = static_cast<uint32_t>(units), n = static_cast<uint32_t>(p.grid);
+    const uint32_t u32 = static_cast<uint32_t>(units), n = static_cast<uint32_t>(runs);
     const uint32_t c = static_cast<uint32_t>(gw + (lane & 1));
     const uint32_t each = u32 / n;
     // c * units / n without 64 bits (n stays below 2^16)
@@ -410,18 +563,11 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
   // Everything above reads only block tables, contexts, scales and codes; queries are read and
   // anything written only after the previous kernel in the stream has finished.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (blockIdx.x == 0 && warp == 0) {
-    if (!p.fused_merge)  // for the merge kernel
-      for (int i = lane; i <= S; i += 32) p.ws_seq_base[i] = seq_base[i];
-    if (lane == 0) {
-      *p.ws_total = units;
-      if (total > p.tile_bound) flag_error(p.status, PA_DEVFLAG_BAD_CONTEXT);
-    }
-  }
-  if (p.fused_merge) {
+  if (gw == 0 && lane == 0 && total > p.tile_bound) flag_error(p.status, PA_DEVFLAG_BAD_CONTEXT);
+  {
     // empty contexts: zero rows (no tile writes them), a sequence per warp of the grid
     const int row_elems = p.num_q_heads * kHeadDim;
-    for (int s0 = gw; s0 < S; s0 += p.grid) {
+    for (int s0 = gw; s0 < S; s0 += runs) {
       if (seq_base[s0 + 1] != seq_base[s0]) continue;
       __nv_bfloat16* out = p.out + static_cast<int64_t>(s0) * row_elems;
       for (int e = lane; e < row_elems; e += 32) out[e] = __float2bfloat16_rn(0.f);
@@ -555,6 +701,8 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
     l *= kVFactor;  // as o, through the value scales
+    Meeting meet = {};
+    if (!whole) meet = meeting_of(seq_base, KV, pc, units, runs);
     if (r < GROUP) {
       if (whole) {
         const float inv = 1.f / l;
@@ -569,23 +717,18 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
         dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
         dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
       } else {
-        // A run writes at most two partials: of the segment it begins inside (slot 0), and of
-        // the one that begins in it and goes on in the next run (slot 1).
-        const int slot = pc.b0 > 0 ? 0 : 1;
-        float* dst = p.partials + ((static_cast<int64_t>(gw) * 2 + slot) * GROUP + r) * kPartialFloats;
+        const bool begins = pc.b0 == 0;
+        float* dst = (meet.n_here > 1 ? local + record_of<GROUP>(warp, begins)
+                                      : p.partials + record_of<GROUP>(gw, begins)) + r * kRecordFloats;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           *reinterpret_cast<float2*>(dst + 16 * q + 2 * j) = make_float2(o[2 * j].x, o[2 * j + 1].x);
           *reinterpret_cast<float2*>(dst + 16 * q + 8 + 2 * j) = make_float2(o[2 * j].y, o[2 * j + 1].y);
         }
-        if (q == 0) {
-          dst[kHeadDim] = m;
-          dst[kHeadDim + 1] = l;
-        }
+        if (q == 0) *reinterpret_cast<float2*>(dst + kHeadDim) = make_float2(m, l);
       }
     }
-    if (!whole && p.fused_merge)
-      publish_piece<GROUP>(p, seq_base, cta_seg_count, pc.s, pc.g, pc.nb, units, lane);
+    if (!whole) publish_piece<GROUP>(p, meet, local, cta_seg_count, pc.s, pc.g, lane);
     y += ntiles;
   }
   // After a timeout, leave no copy in flight into this warp's ring (bounded waits).
@@ -597,8 +740,9 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
   }
 }
 
-size_t smem_bytes(int num_seqs) {
+size_t smem_bytes(int num_seqs, int group) {
   return static_cast<size_t>(kWarps) * kStages * (kStageBytes + sizeof(uint64_t)) +
+         static_cast<size_t>(kWarps) * 2 * group * kRecordFloats * sizeof(float) +
          sizeof(int32_t) * (num_seqs + 1);
 }
 
@@ -611,7 +755,7 @@ cudaError_t prepare_kernel() {
   if (dev < kMaxDevices && done[dev]) return cudaSuccess;
   e = cudaFuncSetAttribute(paged_decode_q8_kernel<GROUP>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem_bytes(kMaxSeqs)));
+                                       static_cast<int>(smem_bytes(kMaxSeqs, GROUP)));
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(paged_decode_q8_kernel<GROUP>,
                              cudaFuncAttributePreferredSharedMemoryCarveout,
@@ -642,11 +786,8 @@ cudaError_t launch(const AttendQ8Args& a, const DecodePlan& plan, void* workspac
   p.chunk = 0;
   p.tile_bound = plan.tile_bound;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.ws_total = reinterpret_cast<int64_t*>(ws);
-  p.ws_seq_base = reinterpret_cast<int32_t*>(ws + 16);
   p.seg_count = reinterpret_cast<int32_t*>(ws + plan.ws_count_offset);
   p.partials = reinterpret_cast<float*>(ws + plan.ws_meta_bytes);
-  p.fused_merge = plan.fused_merge ? 1 : 0;
   p.status = a.status;
   const Q8Params s = {a.key_scale, a.value_scale};
   cudaLaunchConfig_t cfg = {};
@@ -660,9 +801,7 @@ cudaError_t launch(const AttendQ8Args& a, const DecodePlan& plan, void* workspac
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, paged_decode_q8_kernel<GROUP>, p, s);
-  if (e == cudaSuccess) e = cudaGetLastError();
-  if (e != cudaSuccess || plan.fused_merge) return e;
-  return launch_merge<GROUP, kSegmentUnits>(p, plan, false, stream);
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace
@@ -680,22 +819,18 @@ cudaError_t plan_decode_q8(int32_t num_seqs, int32_t num_kv_heads, int32_t num_q
   // one CTA per SM (the ring takes most of its shared memory)
   const int64_t resident = max_sms > 0 && max_sms < sms ? max_sms : sms;
   int64_t runs = resident * kWarps;
-  const int64_t by_size = (tiles_upper + kMinTilesPerRun - 1) / kMinTilesPerRun;
+  const int64_t by_size = num_seqs == 1 && num_kv_heads <= resident
+                              ? tiles_upper + num_kv_heads * kWarps  // (room for a CTA per head)
+                              : (tiles_upper + num_seqs * num_kv_heads * kSegmentUnits) / kMinUnitsPerRun;
   if (by_size < runs) runs = by_size;
-  // One short sequence: one CTA per K/V head, so that every segment's pieces publish and
-  // merge with CTA-scope ordering.
-  if (num_seqs == 1 && num_kv_heads <= resident &&
-      tiles_upper <= static_cast<int64_t>(kOneSeqMaxTilesPerWarp) * num_kv_heads * kWarps)
-    runs = static_cast<int64_t>(num_kv_heads) * kWarps;
   if (runs < 1) runs = 1;
   plan->runs = static_cast<int>(runs);
   plan->chunk = 0;
   plan->tile_bound = tiles_upper;
   plan->grid = static_cast<int>((runs + kWarps - 1) / kWarps);
-  plan->smem_bytes = smem_bytes(num_seqs);
-  const int64_t seg_pieces = runs / (static_cast<int64_t>(num_seqs) * num_kv_heads) + 2;
-  plan->fused_merge = max_context_len <= kFusedMergeMaxContext && seg_pieces <= kFusedMergeMaxPieces;
-  plan->merge_split_heads = !plan->fused_merge && seg_pieces >= kMergeSplitPieces;
+  plan->smem_bytes = smem_bytes(num_seqs, group);
+  plan->fused_merge = true;
+  plan->merge_split_heads = false;
   plan->prefetch_ok = false;
   plan->ws_count_offset = (16 + sizeof(int32_t) * (num_seqs + 1) + 255) / 256 * 256;
   plan->ws_meta_bytes = plan->ws_count_offset +
@@ -704,7 +839,7 @@ cudaError_t plan_decode_q8(int32_t num_seqs, int32_t num_kv_heads, int32_t num_q
   const int64_t runs_full = runs > static_cast<int64_t>(sms) * kWarps
                                 ? runs : static_cast<int64_t>(sms) * kWarps;
   plan->workspace_bytes = plan->ws_meta_bytes +
-                          static_cast<size_t>(runs_full) * 2 * group * kPartialFloats * sizeof(float);
+                          static_cast<size_t>(runs_full) * 2 * group * kRecordFloats * sizeof(float);
   return cudaSuccess;
 }
 
