@@ -50,6 +50,7 @@ namespace {
 constexpr int kWarps = 12;          // streaming warps per CTA, 3 per SM sub-partition
 constexpr int kStagesPerWarp = 4;   // private ring depth: 16 KiB in flight per warp
 constexpr int kWindow = 32;         // block-table entries fetched per window
+constexpr int kPartialFloats = kHeadDim + 2;  // o[64], max (log2 units), sum
 constexpr int kMinTilesPerRun = 2;
 constexpr int kOneSeqMaxTilesPerWarp = 4;  // a single sequence up to this: one CTA per head
 // Before its dependency wait a warp asks L2 for up to kPrefetchTiles tiles past its ring
@@ -63,6 +64,37 @@ constexpr int kPrefetchShortMinTilesPerWarp = 12;
 // Longest context whose split segments are merged inside the attention kernel; longer ones
 // (many pieces per segment) go to the parallel merge kernel.
 constexpr int kFusedMergeMaxContext = 8192;
+constexpr int kMergeThreads = 512;
+constexpr int kMergeUnroll = 4;  // partials whose loads one warp has in flight at once
+constexpr int kMergeSplitPieces = 16;  // segments with this many pieces merge per query head
+
+// Query / output row of sequence s (kRows: the mixed-batch form, a separate instantiation
+// so that the plain decode path compiles without it).
+template <bool kRows>
+__device__ __forceinline__ int64_t row_of(const KParams& p, int s) {
+  if (kRows) return p.q_rows[s];
+  return s;
+}
+
+__device__ __forceinline__ int64_t run_start(int64_t c, int64_t total, int32_t grid,
+                                             int32_t chunk) {
+  if (chunk > 0) return c * chunk < total ? c * chunk : total;
+  return c * total / grid;
+}
+
+__device__ __forceinline__ Piece piece_at(const int32_t* base, int num_seqs, int kv, int64_t y,
+                                          int64_t run_end) {
+  Piece pc;
+  pc.s = find_seq(base, num_seqs, y, kv);
+  pc.nb = base[pc.s + 1] - base[pc.s];
+  const int64_t off = y - static_cast<int64_t>(base[pc.s]) * kv;
+  pc.g = static_cast<int>(off / pc.nb);
+  pc.b0 = static_cast<int>(off % pc.nb);
+  const int64_t left = run_end - y;
+  pc.b1 = (pc.nb - pc.b0 <= left) ? pc.nb : pc.b0 + static_cast<int>(left);
+  return pc;
+}
+
 __device__ __forceinline__ void tma_load_2d_hint(void* dst, const CUtensorMap* map, int c0, int c1,
                                                  uint64_t* bar, uint64_t policy) {
   asm volatile(
@@ -183,6 +215,182 @@ constexpr size_t decode_smem_fixed() {
          (kStagesPerWarp * 2 * kTileBytes          // private K+V rings
           + kStagesPerWarp * sizeof(uint64_t)      // full barriers
           + kStagesPerWarp * sizeof(int32_t));     // tile id held by each stage
+}
+
+// Pieces of segment [x0, x1) (one (sequence, kv head)): the non-empty runs it touches.  The
+// first piece sits in slot 0 of its run when the segment starts the run, else in slot 1;
+// every later piece starts its run (slot 0).
+struct SegmentPieces {
+  int64_t c_first, c_last;
+  int first_slot;
+};
+
+__device__ __forceinline__ SegmentPieces segment_pieces(int64_t x0, int64_t x1, int64_t total,
+                                                        int32_t runs, int32_t chunk) {
+  SegmentPieces sp;
+  sp.c_first = run_of(x0, total, runs, chunk);
+  sp.c_last = run_of(x1 - 1, total, runs, chunk);
+  sp.first_slot = x0 == run_start(sp.c_first, total, runs, chunk) ? 0 : 1;
+  return sp;
+}
+
+// Number of pieces of a segment, and the run holding piece k (balanced splits only, which
+// is the only mode that merges inside the attention kernel).  With at least one tile per
+// run (total >= runs) every run is non-empty and piece k lies in run c_first + k; otherwise
+// every non-empty run holds exactly one tile and piece k is the run of tile x0 + k.
+__device__ __forceinline__ int segment_piece_count(const SegmentPieces& sp, int64_t x0, int64_t x1,
+                                                   int64_t total, int32_t runs) {
+  return total >= runs ? static_cast<int>(sp.c_last - sp.c_first + 1) : static_cast<int>(x1 - x0);
+}
+__device__ __forceinline__ int64_t segment_piece_run(const SegmentPieces& sp, int64_t x0, int k,
+                                                     int64_t total, int32_t runs, int32_t chunk) {
+  return total >= runs ? sp.c_first + k : run_of(x0 + k, total, runs, chunk);
+}
+
+// One warp combines all pieces of a split segment (log-sum-exp weights) and writes the bf16
+// rows of its GROUP query heads.  Lane k reads piece k's (max, sum), so the pieces' loads
+// overlap; chunks of 32 pieces are combined with a running maximum.  Partials were written
+// by other warps in this launch, so they are read through L2 (__ldcg), after the caller's
+// acquire fence.
+constexpr int kFewPieces = 4;  // segments of up to this many pieces merge in one load round
+
+// Partials written by warps of this CTA (published with CTA-scope ordering) are read with
+// plain loads; partials from other SMs through L2.
+template <bool kLocal>
+__device__ __forceinline__ float ld_partial(const float* a) {
+  return kLocal ? *a : __ldcg(a);
+}
+template <bool kLocal>
+__device__ __forceinline__ float2 ld_partial2(const float2* a) {
+  return kLocal ? *a : __ldcg(a);
+}
+
+template <int GROUP, bool kLocal, bool kRows>
+__device__ void merge_segment_in_warp(const KParams& p, const SegmentPieces& sp, int64_t x0,
+                                      int64_t x1, int64_t total, int s, int g, int lane) {
+  const int n = segment_piece_count(sp, x0, x1, total, p.grid);
+  if (n <= kFewPieces) {
+    // Few pieces (the usual case): every lane loads the (max, sum) of all pieces and its
+    // own output slice of each, all in one round of loads, and combines them in registers.
+    float mk[kFewPieces][GROUP], lk[kFewPieces][GROUP];
+    float2 vk[kFewPieces][GROUP];
+#pragma unroll
+    for (int k = 0; k < kFewPieces; ++k) {
+      if (k < n) {
+        const int64_t c = segment_piece_run(sp, x0, k, total, p.grid, p.chunk);
+        const int slot = k == 0 ? sp.first_slot : 0;
+        const float* rec = p.partials + (c * 2 + slot) * GROUP * kPartialFloats;
+#pragma unroll
+        for (int h = 0; h < GROUP; ++h) {
+          mk[k][h] = ld_partial<kLocal>(rec + h * kPartialFloats + kHeadDim);
+          lk[k][h] = ld_partial<kLocal>(rec + h * kPartialFloats + kHeadDim + 1);
+          vk[k][h] = ld_partial2<kLocal>(reinterpret_cast<const float2*>(rec + h * kPartialFloats) + lane);
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < GROUP; ++h) {
+          mk[k][h] = -INFINITY;
+          lk[k][h] = 0.f;
+          vk[k][h] = make_float2(0.f, 0.f);
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < GROUP; ++h) {
+      float mh = mk[0][h];
+#pragma unroll
+      for (int k = 1; k < kFewPieces; ++k) mh = fmaxf(mh, mk[k][h]);
+      float lh = 0.f;
+      float2 ah = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kFewPieces; ++k) {
+        const float wgt = k < n ? fast_exp2(mk[k][h] - mh) : 0.f;
+        lh += wgt * lk[k][h];
+        ah.x += wgt * vk[k][h].x;
+        ah.y += wgt * vk[k][h].y;
+      }
+      const float inv = 1.f / lh;
+      __nv_bfloat16* out =
+          p.out + (row_of<kRows>(p, s) * p.num_q_heads + g * GROUP + h) * kHeadDim;
+      reinterpret_cast<__nv_bfloat162*>(out)[lane] = __floats2bfloat162_rn(ah.x * inv, ah.y * inv);
+    }
+    return;
+  }
+  float M[GROUP], L[GROUP];
+  float2 acc[GROUP];
+#pragma unroll
+  for (int h = 0; h < GROUP; ++h) {
+    M[h] = -INFINITY;
+    L[h] = 0.f;
+    acc[h] = make_float2(0.f, 0.f);
+  }
+  for (int base = 0; base < n; base += 32) {
+    const int k = base + lane;
+    const bool valid = k < n;
+    const float* rec = p.partials;
+    if (valid) {
+      const int64_t c = segment_piece_run(sp, x0, k, total, p.grid, p.chunk);
+      const int slot = k == 0 ? sp.first_slot : 0;
+      rec = p.partials + (c * 2 + slot) * GROUP * kPartialFloats;
+    }
+    // every head's (max, sum) of piece k, all loads in flight together
+    float mk[GROUP], lk[GROUP], wk[GROUP];
+#pragma unroll
+    for (int h = 0; h < GROUP; ++h) {
+      mk[h] = valid ? ld_partial<kLocal>(rec + h * kPartialFloats + kHeadDim) : -INFINITY;
+      lk[h] = valid ? ld_partial<kLocal>(rec + h * kPartialFloats + kHeadDim + 1) : 0.f;
+    }
+#pragma unroll
+    for (int h = 0; h < GROUP; ++h) {
+      float cm = mk[h];
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, off));
+      const float nm = fmaxf(M[h], cm);
+      const float keep = M[h] == -INFINITY ? 0.f : fast_exp2(M[h] - nm);
+      wk[h] = valid ? fast_exp2(mk[h] - nm) : 0.f;
+      float lw = wk[h] * lk[h];
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, off);
+      L[h] = L[h] * keep + lw;
+      acc[h].x *= keep;
+      acc[h].y *= keep;
+      M[h] = nm;
+    }
+    // output slices: 4 pieces x GROUP heads of loads in flight per round
+    const int cnt = min(32, n - base);
+    for (int j0 = 0; j0 < cnt; j0 += 4) {
+      float2 v[4][GROUP];
+      float w[4][GROUP];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int j = j0 + u < cnt ? j0 + u : j0;  // clamp; weight zeroed below
+        const float* rj = reinterpret_cast<const float*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(rec), j));
+#pragma unroll
+        for (int h = 0; h < GROUP; ++h) {
+          w[u][h] = __shfl_sync(0xffffffffu, wk[h], j);
+          if (j0 + u >= cnt) w[u][h] = 0.f;
+          v[u][h] = ld_partial2<kLocal>(reinterpret_cast<const float2*>(rj + h * kPartialFloats) + lane);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+#pragma unroll
+        for (int h = 0; h < GROUP; ++h) {
+          acc[h].x += w[u][h] * v[u][h].x;
+          acc[h].y += w[u][h] * v[u][h].y;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < GROUP; ++h) {
+    const float inv = 1.f / L[h];
+    __nv_bfloat16* out =
+        p.out + (row_of<kRows>(p, s) * p.num_q_heads + g * GROUP + h) * kHeadDim;
+    reinterpret_cast<__nv_bfloat162*>(out)[lane] =
+        __floats2bfloat162_rn(acc[h].x * inv, acc[h].y * inv);
+  }
 }
 
 template <int GROUP, bool kRows>
@@ -514,6 +722,144 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
   }
 }
 
+// Combines the partials of every (sequence, kv head) whose tiles were split across CTAs,
+// and writes zero rows for empty contexts.  One CTA per (sequence, kv head, HPC of the
+// head's GROUP query heads): HPC = GROUP when segments have few pieces, 1 when they have
+// many (long contexts), so that GROUP times as many CTAs share the loads.  Each warp folds
+// its partials into a running (maximum, sum, o) per query head, rescaling by the
+// log-sum-exp weights as the maximum grows, with U partials' loads in flight per round;
+// the warps' states are then combined the same way.
+template <int GROUP, int HPC, bool kRows>
+__global__ void __launch_bounds__(kMergeThreads)
+merge_partials_kernel(const KParams p) {
+  constexpr int kWarps = kMergeThreads / 32;
+  constexpr int kSplit = GROUP / HPC;
+  constexpr int U = HPC == 1 ? 2 * kMergeUnroll : kMergeUnroll;
+  __shared__ float red_m[kWarps][HPC];
+  __shared__ float red_l[kWarps][HPC];
+  __shared__ float red_o[kWarps][HPC][kHeadDim];
+  const int g = blockIdx.x / kSplit;
+  const int h0 = (blockIdx.x % kSplit) * HPC;
+  const int s = blockIdx.y;
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+  const int KV = p.num_kv_heads;
+  __nv_bfloat16* out =
+      p.out + (row_of<kRows>(p, s) * p.num_q_heads + g * GROUP + h0) * kHeadDim;
+  const int32_t base = p.ws_seq_base[s];
+  const int nb = p.ws_seq_base[s + 1] - base;
+  if (nb == 0) {
+    // an empty context gives a zero row; in a mixed batch nb == 0 means the sequence is not
+    // a decode row (or was flagged), and its row is left alone
+    if (!kRows)
+      for (int e = tid; e < HPC * kHeadDim; e += kMergeThreads) out[e] = __float2bfloat16_rn(0.f);
+    return;
+  }
+  const int64_t total = *p.ws_total;
+  const int64_t x0 = static_cast<int64_t>(base) * KV + static_cast<int64_t>(g) * nb;
+  const int64_t x1 = x0 + nb;
+  const int64_t c_first = run_of(x0, total, p.grid, p.chunk);
+  const int64_t c_last = run_of(x1 - 1, total, p.grid, p.chunk);
+  if (c_last >= p.grid) {  // tiles beyond the grid (contexts above max_context_len)
+    if (tid == 0) flag_error(p.status, PA_DEVFLAG_BAD_CONTEXT);
+    return;
+  }
+  if (c_first == c_last) return;  // written directly by the attention kernel
+  const int n = static_cast<int>(c_last - c_first + 1);
+  const int first_slot = x0 == run_start(c_first, total, p.grid, p.chunk) ? 0 : 1;
+
+  auto record = [&](int k, int h) -> const float* {
+    const int64_t c = c_first + k;
+    const int slot = k == 0 ? first_slot : 0;
+    return p.partials + ((c * 2 + slot) * GROUP + h0 + h) * kPartialFloats;
+  };
+  // With at least one tile per run (the usual case) no run is empty and the test is skipped.
+  const bool maybe_empty = total < p.grid;
+  auto empty_run = [&](int k) -> bool {
+    if (!maybe_empty) return false;
+    const int64_t c = c_first + k;
+    return run_start(c, total, p.grid, p.chunk) == run_start(c + 1, total, p.grid, p.chunk);
+  };
+
+  float M[HPC], L[HPC];
+  float2 A[HPC];
+#pragma unroll
+  for (int h = 0; h < HPC; ++h) {
+    M[h] = -INFINITY;
+    L[h] = 0.f;
+    A[h] = make_float2(0.f, 0.f);
+  }
+  // Each warp takes U partials per round and issues all their loads before combining them,
+  // so a round costs one memory latency.
+  for (int k0 = warp * U; k0 < n; k0 += kWarps * U) {
+    float mk[U][HPC], lk[U][HPC];
+    float2 vk[U][HPC];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u;
+      const bool use = k < n && !empty_run(k);
+#pragma unroll
+      for (int h = 0; h < HPC; ++h) {
+        if (use) {
+          const float* r = record(k, h);
+          mk[u][h] = r[kHeadDim];
+          lk[u][h] = r[kHeadDim + 1];
+          vk[u][h] = *reinterpret_cast<const float2*>(r + 2 * lane);
+        } else {
+          mk[u][h] = -INFINITY;
+          lk[u][h] = 0.f;
+          vk[u][h] = make_float2(0.f, 0.f);
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < HPC; ++h) {
+      float mu = mk[0][h];
+#pragma unroll
+      for (int u = 1; u < U; ++u) mu = fmaxf(mu, mk[u][h]);
+      const float nm = fmaxf(M[h], mu);
+      if (nm == -INFINITY) continue;  // nothing of this head loaded yet
+      const float keep = M[h] == -INFINITY ? 0.f : fast_exp2(M[h] - nm);
+      L[h] *= keep;
+      A[h].x *= keep;
+      A[h].y *= keep;
+      M[h] = nm;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float wgt = mk[u][h] == -INFINITY ? 0.f : fast_exp2(mk[u][h] - nm);
+        L[h] += wgt * lk[u][h];
+        A[h].x += wgt * vk[u][h].x;
+        A[h].y += wgt * vk[u][h].y;
+      }
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < HPC; ++h) {
+    red_o[warp][h][2 * lane] = A[h].x;
+    red_o[warp][h][2 * lane + 1] = A[h].y;
+    if (lane == 0) {
+      red_m[warp][h] = M[h];
+      red_l[warp][h] = L[h];
+    }
+  }
+  __syncthreads();
+  for (int e = tid; e < HPC * kHeadDim; e += kMergeThreads) {
+    const int h = e / kHeadDim;
+    const int d = e % kHeadDim;
+    float gm = -INFINITY;
+    for (int w = 0; w < kWarps; ++w) gm = fmaxf(gm, red_m[w][h]);
+    float o = 0.f, lsum = 0.f;
+    for (int w = 0; w < kWarps; ++w) {
+      if (red_m[w][h] == -INFINITY) continue;  // a warp without partials
+      const float wgt = fast_exp2(red_m[w][h] - gm);
+      o += wgt * red_o[w][h][d];
+      lsum += wgt * red_l[w][h];
+    }
+    out[e] = __float2bfloat16_rn(o / lsum);
+  }
+}
+
 template <int GROUP>
 size_t smem_bytes(int num_seqs) {
   return decode_smem_fixed<GROUP>() + sizeof(int32_t) * (num_seqs + 1);
@@ -605,7 +951,20 @@ cudaError_t launch(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t str
     if (e == cudaSuccess) e = cudaGetLastError();
   }
   if (e != cudaSuccess || plan.fused_merge) return e;
-  return launch_merge<GROUP>(p, plan, a.q_rows != nullptr, stream);
+  if (plan.merge_split_heads && GROUP > 1) {  // one CTA per query head
+    const dim3 mgrid(a.num_kv_heads * GROUP, a.num_seqs);
+    if (a.q_rows != nullptr)
+      merge_partials_kernel<GROUP, 1, true><<<mgrid, kMergeThreads, 0, stream>>>(p);
+    else
+      merge_partials_kernel<GROUP, 1, false><<<mgrid, kMergeThreads, 0, stream>>>(p);
+  } else {  // one CTA per kv head
+    const dim3 mgrid(a.num_kv_heads, a.num_seqs);
+    if (a.q_rows != nullptr)
+      merge_partials_kernel<GROUP, GROUP, true><<<mgrid, kMergeThreads, 0, stream>>>(p);
+    else
+      merge_partials_kernel<GROUP, GROUP, false><<<mgrid, kMergeThreads, 0, stream>>>(p);
+  }
+  return cudaGetLastError();
 }
 
 }  // namespace

@@ -193,6 +193,14 @@ __device__ __forceinline__ void attend_pair(const uint8_t* ta, const uint8_t* tb
   }
 }
 
+// Splits weighted by segment: every (sequence, kv head) segment counts kSegmentUnits units on top of its
+// tiles (what starting and publishing a piece costs, in tiles), kSegmentUnits also where it has none,
+// and the runs divide the units evenly.  Units of sequence s start at unit_base(s), those of its
+// segment g at + g (nb + kSegmentUnits), its tiles' at + kSegmentUnits.
+__device__ __forceinline__ int64_t unit_base(const int32_t* base, int s, int kv) {
+  return static_cast<int64_t>(kv) * (static_cast<int64_t>(base[s]) + static_cast<int64_t>(kSegmentUnits) * s);
+}
+
 // A piece's partial: per query head 64 floats of o, the maximum (log2 units) and the sum,
 // padded to 16 bytes.
 constexpr int kRecordFloats = kHeadDim + 4;
@@ -288,7 +296,7 @@ struct Meeting {
 
 __device__ __forceinline__ Meeting meeting_of(const int32_t* seq_base, int KV, const Piece& pc,
                                               int64_t units, int runs) {
-  const int64_t x0 = unit_base<kSegmentUnits>(seq_base, pc.s, KV) +
+  const int64_t x0 = unit_base(seq_base, pc.s, KV) +
                      static_cast<int64_t>(pc.g) * (pc.nb + kSegmentUnits) + kSegmentUnits;
   Meeting m;
   m.c_first = static_cast<int>(run_of(x0, units, runs, 0));
@@ -426,7 +434,7 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
   // From here on every warp works alone, on one run: the plan never makes more runs than
   // the grid has warps.
   const int gw = blockIdx.x * kWarps + warp;
-  const int64_t units = unit_base<kSegmentUnits>(seq_base, S, KV);
+  const int64_t units = unit_base(seq_base, S, KV);
   const int runs = run_count(p, units);
   if (gw >= runs) return;
   const uint64_t policy = l2_evict_first_policy();
