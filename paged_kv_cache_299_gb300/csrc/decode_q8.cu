@@ -10,13 +10,20 @@
 //
 // GB300 design.  HBM-bound: a tile is 1 KiB of K and 1 KiB of V, half the bf16 cache's.  The
 // frame is the bf16 decode kernel's: the flattened (sequence, K/V head, block) tiles are cut
-// into equal contiguous runs, one per warp of a persistent grid; each warp streams its run
-// through a private ring in shared memory, and split segments merge by log-sum-exp.  What
-// differs per tile:
+// into equal contiguous runs, one per warp of a persistent grid, and each warp streams its run
+// through a private ring in shared memory.  Measured, one launch: 4 x 131072 tokens (539 MB)
+// 91.2 us, 5.9 TB/s, 0.87 of the measured copy rate; 256 contexts of 1 to 8192 tokens (208 MB)
+// 42.6 us, 4.9 TB/s; one of 300 tokens 6.9 us.  What bounds it: the stream of tiles for the
+// first; start-up (tables, then tiles), uneven ends of the warps and publishing for the second;
+// three dependent memory latencies and the launch for the third.  What differs from the bf16
+// kernel:
 //   * one plain bulk copy per pool (a tile is contiguous), 4 stages of 2 KiB per warp: 15 MB in
-//     flight over the device.  8 stages measured slower (256 mixed contexts 46.8 us against
-//     44.8, 4 x 131072 tokens 99.3 against 96.6): what is read on the way (tables, scales,
-//     queries) then waits behind 30 MB of tiles; 3 leave the memory idle (49.7 us);
+//     flight over the device.  Measured with 3 / 4 / 5 / 6 stages: 4 x 131072 tokens 105.9 /
+//     91.3 / 95.1 / 92.6 us, 256 mixed contexts 47.8 / 42.5 / 43.8 / 43.8 (fewer leave the memory
+//     idle; with more, the tables, scales and queries read on the way wait behind the tiles);
+//   * the split counts a segment as two tiles more than it has, for what a piece costs besides
+//     its tiles; pieces meet on their CTA first, then one record per CTA (publish_piece);
+//   * a few short contexts get a CTA per segment instead (cta_per_segment);
 //   * the two scales of each of the next 32 tiles sit in the lanes' registers, loaded when
 //     the first of them is issued, a ring's length before it is consumed;
 //   * codes become f16 (cvt.rn.f16x2.e4m3x2, exact: about 43 pairs per clock and SM measured,
@@ -42,12 +49,20 @@ namespace pkv {
 namespace {
 
 constexpr int kWarps = 12;   // streaming warps per CTA, one CTA per SM
-constexpr int kStages = 4;   // ring depth per warp: 8 KiB in flight
+constexpr int kStages = 4;   // ring depth per warp: 8 KiB in flight (figures above)
 constexpr int kStageBytes = 2 * kQ8TileBytes;
 constexpr int kWindow = 32;  // tiles whose block ids and scales are held in the lanes
+// Units (tiles, and kSegmentUnits per segment) a run has at least: 2, against 4, 3000 tokens of
+// one sequence 10.3 and 11.6 us, 16 sequences of 200 without a CTA per segment 9.9 and 11.3.
 constexpr int kMinUnitsPerRun = 2;
-constexpr int kOneSeqMaxUnits = 50;  // one sequence of up to 768 tokens: one CTA per head
-constexpr int kSegmentUnits = 2;  // what a piece costs besides its tiles, in tiles
+// What a piece costs besides its tiles, in tiles: with 1 / 2 / 3, 256 mixed contexts take 44.6 /
+// 42.5 / 43.0 us, 200 of up to 64000 tokens 126.8 / 124.6 / 125.0.
+constexpr int kSegmentUnits = 2;
+// Tiles that a CTA per segment may cost the longest one's warps (cta_per_segment).  With such
+// CTAs, and without: one sequence of 300 tokens 6.9 and 9.6 us, 16 of 200 7.3 and 10.2, 16 of
+// 1500 11.6 and 15.0; 7 tiles of slack instead of 5 lose on 4 x 1500 tokens (11.0 us against
+// 10.4), 4 lose on 8 x 1500 (11.9 against 11.1).
+constexpr int kOwnCtaSlack = 5;
 constexpr float kPShift = 7.f;                // log2 of the factor on p
 constexpr float kVFactor = 1.f / 32768.f;     // 2^-(kPShift + 8): on the value scales, and on l
 constexpr int kQExp = 13;                     // exponent of a row's largest f16 query element
@@ -295,14 +310,15 @@ struct Meeting {
 };
 
 __device__ __forceinline__ Meeting meeting_of(const int32_t* seq_base, int KV, const Piece& pc,
-                                              int64_t units, int runs) {
+                                              int64_t units, int runs, bool own) {
+  const int here = static_cast<int>(blockIdx.x) * kWarps;
+  if (own) return {here, 1, here, min(pc.nb, kWarps)};
   const int64_t x0 = unit_base(seq_base, pc.s, KV) +
                      static_cast<int64_t>(pc.g) * (pc.nb + kSegmentUnits) + kSegmentUnits;
   Meeting m;
   m.c_first = static_cast<int>(run_of(x0, units, runs, 0));
   const int c_last = static_cast<int>(run_of(x0 + pc.nb - 1, units, runs, 0));
   m.n_cta = c_last / kWarps - m.c_first / kWarps + 1;
-  const int here = static_cast<int>(blockIdx.x) * kWarps;
   m.lo = max(m.c_first, here);
   m.n_here = min(c_last, here + kWarps - 1) - m.lo + 1;
   return m;
@@ -315,7 +331,10 @@ __device__ __forceinline__ int64_t record_of(int64_t c, bool begins) {
   return (c * 2 + (begins ? 1 : 0)) * GROUP * kRecordFloats;
 }
 
-// Publishes a piece whose partial this warp has written.  The last of a CTA's pieces folds them
+// Publishes a piece whose partial this warp has written.  (One meeting of all pieces by the last
+// warp cost 0.15 us per piece: one sequence of 8000 tokens, 228 pieces per segment, 44 us against
+// 12; a merge kernel behind the attention cost 200 sequences of up to 16000 tokens 105 us against
+// 86.)  The last of a CTA's pieces folds them
 // into one record; the last CTA folds the CTAs' records and writes the rows.  A segment within
 // one CTA is done after the first meeting.  Serial work per segment is thus a dozen records in
 // shared memory and one per CTA, however long the context, and no second kernel is needed.  The
@@ -379,19 +398,16 @@ __device__ __forceinline__ void publish_piece(const KParams& p, const Meeting& m
   }
 }
 
-// Runs the units are divided into, of the p.grid that there is room for: at least kMinUnitsPerRun
-// units each.  A single short sequence takes a divisor of the CTA's warps per K/V head, so that
-// every head's pieces meet on one CTA.
-__device__ __forceinline__ int run_count(const KParams& p, int64_t units) {
-  if (p.num_seqs == 1) {
-    const int per_head = static_cast<int>(units / p.num_kv_heads);
-    if (per_head <= kOneSeqMaxUnits && p.num_kv_heads * kWarps <= p.grid) {
-      int d = kWarps;
-      while (d > per_head || kWarps % d != 0) --d;
-      return d * p.num_kv_heads;
-    }
-  }
-  return static_cast<int>(max(int64_t{1}, min(static_cast<int64_t>(p.grid), units / kMinUnitsPerRun)));
+// Whether every segment gets a CTA of its own, whose warps share its tiles: all pieces then meet
+// in shared memory.  For batches of no more segments than CTAs in which that costs the longest
+// segment's warps at most kOwnCtaSlack tiles more than the even split would give them.
+__device__ __forceinline__ bool cta_per_segment(const KParams& p, const int32_t* seq_base, int64_t units,
+                                                int lane) {
+  if (static_cast<int64_t>(p.num_seqs) * p.num_kv_heads * kWarps > p.grid) return false;
+  int most = 0;
+  for (int s = lane; s < p.num_seqs; s += 32) most = max(most, seq_base[s + 1] - seq_base[s]);
+  most = __reduce_max_sync(0xffffffffu, most);
+  return static_cast<int64_t>(most) * p.grid <= (units + static_cast<int64_t>(kOwnCtaSlack) * p.grid) * kWarps;
 }
 
 template <int GROUP>
@@ -435,7 +451,9 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
   // the grid has warps.
   const int gw = blockIdx.x * kWarps + warp;
   const int64_t units = unit_base(seq_base, S, KV);
-  const int runs = run_count(p, units);
+  const bool own = cta_per_segment(p, seq_base, units, lane);
+  const int runs = own ? S * KV * kWarps
+                       : static_cast<int>(max(int64_t{1}, min(static_cast<int64_t>(p.grid), units / kMinUnitsPerRun)));
   if (gw >= runs) return;
   const uint64_t policy = l2_evict_first_policy();
   const int r = lane >> 2;
@@ -444,7 +462,16 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
   // (block_prefix keeps the tile count below 2^31, so units fit 32 unsigned bits.)
   int start, stop;
   int wc_s, wc_off;  // sequence of tile wc_y and its place among the sequence's KV x nb tiles
-  {
+  if (own) {
+    wc_s = static_cast<int>(blockIdx.x) / KV;
+    const int nb = seq_base[wc_s + 1] - seq_base[wc_s];
+    const int d = max(1, min(nb, kWarps));  // warps with tiles
+    wc_off = (static_cast<int>(blockIdx.x) % KV) * nb;
+    start = seq_base[wc_s] * KV + wc_off;
+    stop = start + min(warp + 1, d) * nb / d;
+    start += min(warp, d) * nb / d;
+    wc_off += min(warp, d) * nb / d;
+  } else {
     const uint32_t u32 = static_cast<uint32_t>(units), n = static_cast<uint32_t>(runs);
     const uint32_t c = static_cast<uint32_t>(gw + (lane & 1));
     const uint32_t each = u32 / n;
@@ -710,7 +737,7 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
     l += __shfl_xor_sync(0xffffffffu, l, 2);
     l *= kVFactor;  // as o, through the value scales
     Meeting meet = {};
-    if (!whole) meet = meeting_of(seq_base, KV, pc, units, runs);
+    if (!whole) meet = meeting_of(seq_base, KV, pc, units, runs, own);
     if (r < GROUP) {
       if (whole) {
         const float inv = 1.f / l;
@@ -827,9 +854,9 @@ cudaError_t plan_decode_q8(int32_t num_seqs, int32_t num_kv_heads, int32_t num_q
   // one CTA per SM (the ring takes most of its shared memory)
   const int64_t resident = max_sms > 0 && max_sms < sms ? max_sms : sms;
   int64_t runs = resident * kWarps;
-  const int64_t by_size = num_seqs == 1 && num_kv_heads <= resident
-                              ? tiles_upper + num_kv_heads * kWarps  // (room for a CTA per head)
-                              : (tiles_upper + num_seqs * num_kv_heads * kSegmentUnits) / kMinUnitsPerRun;
+  const int64_t segments = static_cast<int64_t>(num_seqs) * num_kv_heads;
+  int64_t by_size = (tiles_upper + segments * kSegmentUnits) / kMinUnitsPerRun;
+  if (segments <= resident && by_size < segments * kWarps) by_size = segments * kWarps;  // a CTA each
   if (by_size < runs) runs = by_size;
   if (runs < 1) runs = 1;
   plan->runs = static_cast<int>(runs);

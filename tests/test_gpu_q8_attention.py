@@ -114,7 +114,27 @@ def test_decode_batches():
     check_decode(wl.make_workload("b300", ctx - 1, np.ones_like(ctx), seed=6), 2, 8)
 
 
-def test_decode_long_contexts_merge_kernel():
+@pytest.mark.parametrize("hq,hkv,lens", [
+    (4, 1, [40000]),                          # one segment over more than 32 CTAs
+    (2, 1, [33000, 1, 0, 500]),
+    (8, 2, [20000] + [30] * 40),              # one long among short ones
+    (8, 2, [30, 0, 0, 9000, 17, 0, 700]),
+    (32, 8, [600, 0, 1, 90] + [16] * 9),      # a CTA per segment, some with fewer tiles than warps
+    (4, 1, list(range(0, 150))),
+    (2, 2, [190] * 76),                       # as many segments as a 152-SM device has CTAs
+    (2, 2, [190] * 77)])
+def test_decode_uneven_batches(hq, hkv, lens):
+    """Every way pieces meet: whole segments, within a CTA, over many, and a CTA per segment."""
+    w = wl.make_workload("uneven", lens, np.zeros(len(lens), int), num_prefill=0, seed=len(lens), pool_slack=0.2)
+    st, got = check_decode(w, hkv, hq)
+    ws = torch.zeros(pa.pa_decode_q8_workspace_size(len(lens), hkv, hq, 131072), dtype=torch.uint8, device="cuda")
+    st.max_ctx = 131072  # planned for longer contexts than there are
+    for _ in range(2):
+        ref, tol = attend(st.q, st.k64, st.v64, w.block_tables, w.context_lens, st.scale)
+        close(st.decode(workspace=ws), ref, tol, "planned longer")
+
+
+def test_decode_long_contexts():
     check_decode(wl.make_workload("long", [20000, 3, 33333, 8191], [1, 1, 1, 1], seed=7), 4, 16)
 
 
