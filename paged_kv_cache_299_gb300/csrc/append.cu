@@ -230,39 +230,106 @@ __device__ __forceinline__ uint2 codes8(const float* y, float inv) {
 
 constexpr int kRowSteps = kBlockSize / kRowsPerWarp;  // 2 rows of the block per lane
 
-// Scale of a block that receives new values of largest magnitude amax, and the rescaling of
-// the codes it holds already (rows 0 .. o0-1).  A block whose first token is written now
-// starts with a scale of its own; otherwise the scale only grows from `old`.  Powers of two
-// keep the rescaled codes exact down to the subnormal codes.
-__device__ __forceinline__ float settle_scale(float old, uint8_t* tile, float amax, int o0,
-                                              int lane) {
-  float s = scale_for(amax);
-  if (o0 > 0) {
-    if (s > old) {
-      const float ratio = old / s;
+// Multiplies the codes of a tile's rows 0 .. o0-1 by `ratio` (below 1), rounding once.  Powers
+// of two keep them exact down to the subnormal codes.  By a whole warp.
+__device__ __forceinline__ void rescale_rows(uint8_t* tile, float ratio, int o0, int lane) {
 #pragma unroll
-      for (int k = 0; k < kRowSteps; ++k) {
-        const int row = k * kRowsPerWarp + lane / kLanesPerRow;
-        if (row >= o0) continue;
-        uint4* p = reinterpret_cast<uint4*>(tile + row * kQ8RowBytes) + lane % kLanesPerRow;
-        const uint4 c = *p;
-        const uint32_t in[4] = {c.x, c.y, c.z, c.w};
-        uint32_t out[4];
+  for (int k = 0; k < kRowSteps; ++k) {
+    const int row = k * kRowsPerWarp + lane / kLanesPerRow;
+    if (row >= o0) continue;
+    uint4* p = reinterpret_cast<uint4*>(tile + row * kQ8RowBytes) + lane % kLanesPerRow;
+    const uint4 c = *p;
+    const uint32_t in[4] = {c.x, c.y, c.z, c.w};
+    uint32_t out[4];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          uint32_t lo, hi;
-          codes4_to_half2x2(in[h], lo, hi);
-          const float2 a = half2_to_float2(lo), b = half2_to_float2(hi);
-          out[h] = floats_to_codes2(a.x * ratio, a.y * ratio) |
-                   (static_cast<uint32_t>(floats_to_codes2(b.x * ratio, b.y * ratio)) << 16);
-        }
-        *p = make_uint4(out[0], out[1], out[2], out[3]);
-      }
-    } else {
-      s = old;
+    for (int h = 0; h < 4; ++h) {
+      uint32_t lo, hi;
+      codes4_to_half2x2(in[h], lo, hi);
+      const float2 a = half2_to_float2(lo), b = half2_to_float2(hi);
+      out[h] = floats_to_codes2(a.x * ratio, a.y * ratio) |
+               (static_cast<uint32_t>(floats_to_codes2(b.x * ratio, b.y * ratio)) << 16);
     }
+    *p = make_uint4(out[0], out[1], out[2], out[3]);
   }
-  return s;
+}
+
+// A lane's sixteen values as codes, into its places of a row of a tile.
+template <bool kInterleaved>
+__device__ __forceinline__ void store_codes(uint8_t* row, const float* y, float inv, int l) {
+  const uint2 w0 = codes8(y, inv), w1 = codes8(y + 8, inv);
+  if (kInterleaved) {
+    reinterpret_cast<uint4*>(row)[l] = make_uint4(w0.x, w0.y, w1.x, w1.y);
+  } else {
+    reinterpret_cast<uint2*>(row)[first_chunk<false>(l)] = w0;
+    reinterpret_cast<uint2*>(row)[second_chunk<false>(l)] = w1;
+  }
+}
+
+// Decode steps (one token per sequence): one warp serves a token's rows of eight heads in one
+// pool, four lanes each.  A block with earlier tokens whose scale has to grow is rescaled by
+// the whole warp.  (A warp per head and pool, as chunks have it, took 4.5 us for 256
+// sequences and 12.1 for 1024, this 2.5 and 3.2.)
+template <bool kRotate, bool kInterleaved>
+__device__ void step_rows(const AppendArgs& a, int64_t item, int lane) {
+  const bool is_k = (item & 1) == 0;
+  item >>= 1;
+  const int groups = (a.num_kv_heads + kRowsPerWarp - 1) / kRowsPerWarp;
+  const int h0 = static_cast<int>(item % groups) * kRowsPerWarp;
+  const int64_t t = item / groups;
+  const bool tell = lane == 0 && h0 == 0 && is_k;
+  const int32_t ctx = a.context_lens[t];
+  if (ctx == 0) return;  // padding
+  if (ctx < 0 || static_cast<int64_t>(ctx) > static_cast<int64_t>(a.max_blocks_per_seq) * kBlockSize ||
+      (kRotate && ctx > a.max_positions)) {
+    if (tell) flag_error(a.status, PA_DEVFLAG_BAD_CONTEXT);
+    return;
+  }
+  const int32_t pos = ctx - 1;
+  const int o = pos % kBlockSize;
+  const int head = min(h0 + lane / kLanesPerRow, a.num_kv_heads - 1);
+  const bool active = h0 + lane / kLanesPerRow < a.num_kv_heads;
+  const int l = lane % kLanesPerRow;
+  const __nv_bfloat16* const src = static_cast<const __nv_bfloat16*>(is_k ? a.key : a.value) +
+                                   t * (is_k ? a.key_stride : a.value_stride) + head * kHeadDim;
+  const uint4 x0 = ldg_nc128(reinterpret_cast<const uint4*>(src) + first_chunk<kInterleaved>(l));
+  const uint4 x1 = ldg_nc128(reinterpret_cast<const uint4*>(src) + second_chunk<kInterleaved>(l));
+  const bool turn = kRotate && is_k;
+  Angles g = {};
+  if (turn) load_angles(a.cos_sin + static_cast<int64_t>(pos) * kHeadDim, l, g);
+  const int32_t phys = a.block_tables[t * a.max_blocks_per_seq + pos / kBlockSize];
+  if (phys < 0 || phys >= a.num_blocks) {
+    if (tell) flag_error(a.status, PA_DEVFLAG_BAD_BLOCK);
+    return;
+  }
+  const int64_t tile = static_cast<int64_t>(phys) * a.num_kv_heads + head;
+  float* const scale = (is_k ? a.key_scale : a.value_scale) + tile;
+  uint8_t* const pool = static_cast<uint8_t*>(is_k ? a.key_cache : a.value_cache);
+  const float old = *scale;
+  float y[16];
+  bool bad = false;
+  unpack16(x0, x1, y);
+  if (turn) rotate16<kInterleaved>(g, y);
+  float amax = amax16(y, &bad);
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  if (__any_sync(0xffffffffu, bad) && lane == 0) flag_error(a.status, PA_DEVFLAG_NONFINITE);
+  const bool held = o > 0;  // the block has earlier tokens
+  const bool usable = !held || scale_ok(old);
+  if (__any_sync(0xffffffffu, !usable) && lane == 0) flag_error(a.status, PA_DEVFLAG_BAD_SCALE);
+  const float need = scale_for(amax);
+  const float now = held && !(need > old) ? old : need;
+  unsigned grow = __ballot_sync(0xffffffffu, active && usable && held && need > old && l == 0);
+  const float ratio = old / now;
+  while (grow != 0u) {
+    const int from = __ffs(grow) - 1;
+    grow &= grow - 1u;
+    rescale_rows(pool + __shfl_sync(0xffffffffu, tile, from) * kQ8TileBytes,
+                 __shfl_sync(0xffffffffu, ratio, from), o, lane);
+  }
+  if (active && usable) {
+    store_codes<kInterleaved>(pool + tile * kQ8TileBytes + o * kQ8RowBytes, y, 1.f / now, l);
+    if (l == 0) *scale = now;  // (its four lanes have read the old one)
+  }
 }
 
 // One warp serves one (sequence, block it appends to, K/V head, pool): it holds the block's
@@ -278,13 +345,7 @@ __device__ void block_rows(const AppendArgs& a, int64_t item, int lane) {
   int32_t s;
   int64_t index;  // of the block among those the sequence appends to
   int32_t first, q_len;
-  if (a.query_start_loc == nullptr) {
-    s = static_cast<int32_t>(v);
-    index = 0;
-    first = s;
-    q_len = 1;
-    if (a.context_lens[s] == 0) return;  // padding
-  } else {
+  {
     // sequence s owns indices base(s) .. base(s+1)-1 with base(s) = start(s) / 16 + 2 s, at
     // least as many as the blocks its tokens can touch
     int32_t lo = 0, hi = a.num_seqs - 1;
@@ -357,20 +418,19 @@ __device__ void block_rows(const AppendArgs& a, int64_t item, int lane) {
     if (lane == 0) flag_error(a.status, PA_DEVFLAG_BAD_SCALE);
     return;
   }
-  const float now = settle_scale(old, codes, amax, o0, lane);
+  // A block whose first token is written now starts with a scale of its own; otherwise it grows.
+  float now = scale_for(amax);
+  if (o0 > 0) {
+    if (now > old)
+      rescale_rows(codes, old / now, o0, lane);
+    else
+      now = old;
+  }
   const float inv = 1.f / now;
 #pragma unroll
   for (int k = 0; k < kRowSteps; ++k) {
     const int row = k * kRowsPerWarp + lane / kLanesPerRow;
-    if (row < o0 || row >= o1) continue;
-    const uint2 w0 = codes8(y[k], inv), w1 = codes8(y[k] + 8, inv);
-    uint2* dst = reinterpret_cast<uint2*>(codes + row * kQ8RowBytes);
-    if (kInterleaved) {
-      reinterpret_cast<uint4*>(dst)[l] = make_uint4(w0.x, w0.y, w1.x, w1.y);
-    } else {
-      dst[c0] = w0;
-      dst[c1] = w1;
-    }
+    if (row >= o0 && row < o1) store_codes<kInterleaved>(codes + row * kQ8RowBytes, y[k], inv, l);
   }
   __syncwarp();  // every lane has read the old scale
   if (lane == 0) *scale = now;
@@ -383,7 +443,11 @@ rope_append_q8_kernel(const AppendArgs a, int64_t items, int64_t item_ctas, int 
   const int lane = threadIdx.x & 31;
   if (blockIdx.x < item_ctas) {
     const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarpsPerCta + (threadIdx.x >> 5);
-    if (w < items) block_rows<kRotate, kInterleaved>(a, w, lane);
+    if (w >= items) return;
+    if (a.query_start_loc == nullptr)
+      step_rows<kRotate, kInterleaved>(a, w, lane);
+    else
+      block_rows<kRotate, kInterleaved>(a, w, lane);
     return;
   }
   if (kRotate) {
@@ -416,10 +480,10 @@ cudaError_t launch_rope_append(const AppendArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_rope_append_q8(const AppendArgs& a, cudaStream_t stream) {
-  const int64_t blocks = a.query_start_loc == nullptr
-                             ? a.num_seqs
-                             : (static_cast<int64_t>(a.num_tokens) >> 4) + 2ll * a.num_seqs;
-  const int64_t items = blocks * a.num_kv_heads * 2;  // K and V
+  const int64_t items =  // K and V
+      2 * (a.query_start_loc == nullptr
+               ? static_cast<int64_t>(a.num_seqs) * ((a.num_kv_heads + kRowsPerWarp - 1) / kRowsPerWarp)
+               : ((static_cast<int64_t>(a.num_tokens) >> 4) + 2ll * a.num_seqs) * a.num_kv_heads);
   const int64_t item_ctas = (items + kWarpsPerCta - 1) / kWarpsPerCta;
   int parts = 1;
   int64_t q_ctas = 0;

@@ -204,6 +204,38 @@ def test_bad_entries_are_reported_and_skipped():
         assert go(w.block_tables, w.context_lens, None, bad) == (pa.DEVFLAG_BAD_SCALE, 0)
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("hq,hkv", [(2, 1), (6, 3), (16, 8), (9, 9), (20, 20)])
+def test_one_token_form_equals_chunks_of_one(hq, hkv, interleaved):
+    """Without query_start_loc, against the checked definition and bit for bit against chunks of
+    one token, with blocks that start, grow, hold a bad scale and receive non-finite rows."""
+    n = 70
+    w = wl.make_workload("ones", np.arange(n) % 37, np.ones(n, int), seed=hkv, pool_slack=0.3)
+    run_case(w, hq, hkv, interleaved, one_each=True, spread=2.5)
+    table = angles(40).cuda()
+    c = Cache(w, hkv)
+    k, v = rows(n, hkv, 2, 2.5), rows(n, hkv, 3, 2.5)
+    k[5, 0, 3], v[6, -1, 60], v[7, 0, 0] = float("nan"), float("inf"), float("-inf")
+    c.ks[int(w.block_tables[20, 1]), -1] = -1.0  # position 20
+    c.vs[int(w.block_tables[16, 1]), 0] = float("nan")  # position 16 starts its block
+    c.vs[int(w.block_tables[40, 0]), 0] = 0.0  # position 3
+    bt = w.block_tables.copy()
+    bt[9, 0] = w.num_blocks
+    ctx = w.context_lens.copy()
+    ctx[30], ctx[31], ctx[32] = 41, -1, 5000  # beyond the angles, negative, beyond the table row
+    got = []
+    for qsl in (None, i32(np.arange(n + 1))):
+        cache = [x.clone() for x in (c.kc, c.vc, c.ks, c.vs)]
+        status = pa.new_device_status()
+        pa.pa_rope_append_q8(None, k.cuda(), v.cuda(), table, *cache, i32(bt), i32(ctx), qsl,
+                             interleaved=interleaved, device_status=status)
+        got.append(([x.cpu() for x in cache], int(status.item())))
+    assert got[0][1] == got[1][1] == (pa.DEVFLAG_NONFINITE | pa.DEVFLAG_BAD_SCALE | pa.DEVFLAG_BAD_BLOCK
+                                      | pa.DEVFLAG_BAD_CONTEXT)
+    for a, b in zip(got[0][0], got[1][0]):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
 @pytest.mark.parametrize("starts", [[0, 3, 9], [0, 7, 9], [0, 9, 12]])
 def test_rows_past_the_buffer_are_reported(starts):
     """Seven rows, and sequences that claim more: what lies past the buffer is reported and skipped."""
