@@ -73,15 +73,6 @@ struct Q8Params {
   const float* value_scale;
 };
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar,
-                                          uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
-      "[%0], [%1], %2, [%3], %4;" ::"r"(smem_addr(dst)),
-      "l"(src), "r"(bytes), "r"(smem_addr(bar)), "l"(policy)
-      : "memory");
-}
-
 // D (+)= A B for A with rows 8-15 zero, f16 in, fp32 accumulate.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a2, uint32_t b0,
                                         uint32_t b1) {
@@ -98,19 +89,6 @@ __device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_
       : "r"(a0), "r"(0u), "r"(a2), "r"(0u), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-__device__ __forceinline__ uint32_t pack_half2(float x, float y) {
-  const __half2 h = __floats2half2_rn(x, y);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Token of column n (0..7) of score n-tile i.  Lane q of a quad owns columns 2q and 2q + 1, so
-// its tokens are t, t + 2, t + 8 and t + 10 with t = (q & 1) + 4 (q >> 1): their 64-byte rows
-// fall on both halves of the shared-memory banks, which leaves two wavefronts per 128 bytes
-// for the 8-byte V reads and the 16-byte K reads alike (the natural order leaves four and one).
-__device__ __forceinline__ int token_of(int n, int i) {
-  return ((n >> 1) & 1) + 2 * (n & 1) + 4 * (n >> 2) + 8 * i;
-}
-
 // Two consecutive tiles a and b of a segment (32 tokens).  Lane (r = lane / 4, q = lane % 4):
 // MMA row r is query head r of the group (rows past it are zero).  Along the dims, MMA step j
 // takes dims 16q + 4j .. + 3 of lane q, for K and Q alike; output n-tile j holds dims 16q + j
@@ -122,8 +100,8 @@ __device__ __forceinline__ void attend_pair(const uint8_t* ta, const uint8_t* tb
                                             int valid, const float (&xs)[2], const float (&vs)[2],
                                             const uint32_t (&qa0)[4], const uint32_t (&qa2)[4],
                                             float& m, float& l, float2 (&o)[8]) {
-  const int t0 = token_of(2 * q, 0);
-  const int k_off = token_of(r, 0) * kQ8RowBytes + 16 * q;
+  const int t0 = q8_token_of(2 * q, 0);
+  const int k_off = q8_token_of(r, 0) * kQ8RowBytes + 16 * q;
   const int v_off = kQ8TileBytes + t0 * kQ8RowBytes + 8 * r;
   uint2 v[2][4];  // tokens t0, t0 + 2, t0 + 8, t0 + 10 of each tile, codes of dims 8r .. 8r + 7
   float x[2][4];
@@ -185,7 +163,7 @@ __device__ __forceinline__ void attend_pair(const uint8_t* ta, const uint8_t* tb
     const float p0 = fast_exp2(x[t][0] - ref), p1 = fast_exp2(x[t][1] - ref);
     const float p2 = fast_exp2(x[t][2] - ref), p3 = fast_exp2(x[t][3] - ref);
     l += (p0 + p1) + (p2 + p3);
-    const uint32_t pa0 = pack_half2(p0, p1), pa2 = pack_half2(p2, p3);
+    const uint32_t pa0 = pack_half2_rn(p0, p1), pa2 = pack_half2_rn(p2, p3);
     const float2 vs2 = make_float2(MASK && t == 1 && valid <= kBlockSize ? 0.f : vs[t],
                                    MASK && t == 1 && valid <= kBlockSize ? 0.f : vs[t]);
 #pragma unroll
@@ -657,8 +635,8 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 a = bf16x2_to_float2(w[2 * j]), b = bf16x2_to_float2(w[2 * j + 1]);
-        qa0[j] = real ? pack_half2(a.x * up, a.y * up) : 0u;
-        qa2[j] = real ? pack_half2(b.x * up, b.y * up) : 0u;
+        qa0[j] = real ? pack_half2_rn(a.x * up, a.y * up) : 0u;
+        qa2[j] = real ? pack_half2_rn(b.x * up, b.y * up) : 0u;
       }
     }
     float m = -INFINITY, l = 0.f;

@@ -930,6 +930,7 @@ cudaError_t launch(const AttendQ8Args& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_prefill_q8(const AttendQ8Args& a, cudaStream_t stream) {
+  if (rows_q8_takes(a)) return launch_rows_q8(a, stream);
   switch (a.num_q_heads / a.num_kv_heads) {
     case 1: return launch<1>(a, stream);
     case 2: return launch<2>(a, stream);

@@ -50,6 +50,29 @@ __device__ __forceinline__ float scale_for(float amax) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+// One tile of a pool into shared memory, by one asynchronous copy.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar,
+                                          uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1], %2, [%3], %4;" ::"r"(smem_addr(dst)),
+      "l"(src), "r"(bytes), "r"(smem_addr(bar)), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_half2_rn(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Token of column n (0..7) of score n-tile i.  Lane q of a quad owns columns 2q and 2q + 1, so
+// its tokens are t, t + 2, t + 8 and t + 10 with t = (q & 1) + 4 (q >> 1): their 64-byte rows
+// fall on both halves of the shared-memory banks, which leaves two wavefronts per 128 bytes
+// for the 8-byte V reads and the 16-byte K reads alike (the natural order leaves four and one).
+__device__ __forceinline__ int q8_token_of(int n, int i) {
+  return ((n >> 1) & 1) + 2 * (n & 1) + 4 * (n >> 2) + 8 * i;
+}
+
 __device__ __forceinline__ bool scale_ok(float s) { return s > 0.f && s < INFINITY; }
 
 }  // namespace pkv
