@@ -7,10 +7,18 @@
 //
 // GB300 design.  With so few rows a K/V tile's bytes, not its products, are the work, and a
 // 128-row tensor-memory tile would be mostly padding: the warp-level tensor-core instruction
-// takes 16 rows, MT = 1 or 2 of them per K/V head.  A segment (sequence, K/V head) belongs to a
-// cluster of 1 to 8 CTAs; its tiles are cut into equal runs, one per warp, each streamed through
-// a ring of its own as in the decode, and the warps' partial outputs meet in shared memory, the
-// CTAs' in the cluster's.  So nothing is kept outside the launch: the call needs no workspace.
+// takes rows by eights (NT = 1 to 4 groups).  A segment (sequence, K/V head) belongs to a cluster
+// of 1 to 8 CTAs; its tiles are cut into equal runs, one per warp, each streamed through a ring
+// of its own as in the decode, and the warps' partial outputs meet in shared memory, the CTAs'
+// in the cluster's.  So nothing is kept outside the launch: the call needs no workspace.
+//
+// Measured, against the tensor-memory kernel on the same calls: a verify step of 32 x 5 rows,
+// contexts 487-1022, 16.6 us against 22.4; 32 x 5 rows at 800 tokens 12.8 against 24.9, 256 x 5 at
+// 1000 92 against 152, 4 x 5 at 131072 160 (3.4 TB/s) against 946; 128 x 8 at 4000 181 against
+// 242.  Bound: by the latency of the chain score, exponential, product per tile, of which an SM
+// holds twelve (38 % of the issue slots and 33 % of DRAM busy at 4 x 131072 tokens); small batches
+// by start-up.  12 warps on one CTA, or 15 on three (the registers spill), were slower: 256 x 5 at
+// 1000 124 and 107 us.
 #include <math.h>
 
 #include "common.cuh"
@@ -27,6 +35,10 @@ constexpr int kStages = 4;   // ring depth per warp
 constexpr int kStageBytes = 2 * kQ8TileBytes;
 constexpr int kWindow = 32;  // tiles whose block ids and scales are held in the lanes
 constexpr int kMaxCluster = 8;
+// Up to this many groups of eight rows, tiles are taken in pairs (more work side by side; beyond,
+// the registers spill).  Pairs and single tiles: 32 x 2 rows at 800 tokens (one group) 8.6 and 9.1
+// us, 256 x 3 at 1000 (two) 71.8 and 73.5, 256 x 5 (three) 97.3 and 92.1, 32 x 8 (four) 16.5, 15.2.
+constexpr int kPairGroups = 2;
 constexpr int kRecordFloats = kHeadDim + 4;  // o, maximum (log2 units), sum, padded to 16 bytes
 constexpr float kRescaleThreshold = 8.f;     // as in the decode, like the factors below
 constexpr float kPShift = 7.f;
@@ -95,106 +107,136 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
   return v;
 }
 
-// Running state of a lane's rows: row 16 mt + r (index 0) and + 8 (index 1), r = lane / 4.
-template <int MT>
+// Running state of a lane (r = lane / 4, q = lane % 4) for NT groups of eight rows: maximum and
+// sum of row 8 nt + r (the sum over the lane's own tokens), output dims 8 r .. 8 r + 7 of rows
+// 8 nt + 2 q and 8 nt + 2 q + 1 (o[nt][j]: dims 8 r + 2 j, + 1, both rows each).
+template <int NT>
 struct Rows {
-  uint32_t q[MT][4][4];   // f16 query fragments
-  float factor[MT][2];    // score factor of the row
-  float m[MT][2], l[MT][2];
-  float2 o[MT][2][8];
+  uint32_t q[(NT + 1) / 2][4][4];  // f16 query fragments, 16 rows each
+  float factor[NT];                // score factor of row 8 nt + r
+  int pos[NT];                     // last key that row sees
+  float m[NT], l[NT];
+  float2 o[NT][4][2];
 };
 
-// One tile (16 tokens).  Fragments and dims as in the 8-bit decode; MASK: row x of the lane sees
-// tokens 0 .. last[x] of the tile (none if negative), and tokens past `held` may hold anything.
-template <int MT, bool MASK>
-__device__ __forceinline__ void attend_tile(const uint8_t* tile, int r, int q, float ks, float vs,
-                                            const int (&last)[MT][2], int held, Rows<MT>& w) {
+// T tiles (16 tokens each) at a time.  Scores are Q K^T with 16 rows a fragment, so P arrives
+// with a row's neighbouring tokens in one register, which is what the second factor of O^T = V^T
+// P^T wants: 16 dims by 8 rows, no padding beyond the eighth row.  Fragments and the order of
+// dims and tokens as in the 8-bit decode.  MASK: row x sees tokens up to pos[x], tile t holds
+// tokens from first[t] on, and tokens past `end` may hold anything.
+template <int NT, int T, bool MASK>
+__device__ __forceinline__ void attend_tiles(const uint8_t* const (&tiles)[T], int r, int q,
+                                             const float (&ks)[T], const float (&vs)[T],
+                                             const int (&first)[T], int end, Rows<NT>& w) {
+  constexpr int MT = (NT + 1) / 2;
   const int t0 = q8_token_of(2 * q, 0);
-  const uint8_t* kp = tile + q8_token_of(r, 0) * kQ8RowBytes + 16 * q;
-  const uint8_t* vp = tile + kQ8TileBytes + t0 * kQ8RowBytes + 8 * r;
-  const uint4 k0 = lds128(kp), k1 = lds128(kp + 8 * kQ8RowBytes);
-  uint2 v[4];  // tokens t0, t0 + 2, t0 + 8, t0 + 10
+  uint2 v[T][4];  // tokens t0, t0 + 2, t0 + 8, t0 + 10
+  float x[T][NT][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    v[i] = *reinterpret_cast<const uint2*>(vp + (2 * (i & 1) + 8 * (i >> 1)) * kQ8RowBytes);
-  const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
-  float s0[MT][4], s1[MT][4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t a, b, c, d;
-    codes4_to_half2x2(w0[j], a, b);
-    codes4_to_half2x2(w1[j], c, d);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      if (j == 0) {
-        mma_rows_zero(s0[mt], w.q[mt][j], a, b);
-        mma_rows_zero(s1[mt], w.q[mt][j], c, d);
-      } else {
-        mma_rows(s0[mt], w.q[mt][j], a, b);
-        mma_rows(s1[mt], w.q[mt][j], c, d);
-      }
-    }
-  }
-  if (MASK) {
+  for (int t = 0; t < T; ++t) {
+    const uint8_t* kp = tiles[t] + q8_token_of(r, 0) * kQ8RowBytes + 16 * q;
+    const uint8_t* vp = tiles[t] + kQ8TileBytes + t0 * kQ8RowBytes + 8 * r;
+    const uint4 k0 = lds128(kp), k1 = lds128(kp + 8 * kQ8RowBytes);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (t0 + 2 * (i & 1) + 8 * (i >> 1) > held) v[i] = make_uint2(0u, 0u);
-  }
-  uint32_t p[MT][4];
+      v[t][i] = *reinterpret_cast<const uint2*>(vp + (2 * (i & 1) + 8 * (i >> 1)) * kQ8RowBytes);
+    const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+    float s0[MT][4], s1[MT][4];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      const float f = w.factor[mt][y] * ks;
-      float x[4] = {s0[mt][2 * y] * f, s0[mt][2 * y + 1] * f, s1[mt][2 * y] * f, s1[mt][2 * y + 1] * f};
-      if (MASK) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (t0 + 2 * (i & 1) + 8 * (i >> 1) > last[mt][y]) x[i] = -INFINITY;
-      }
-      float t = fmaxf(max3f(x[0], x[1], x[2]), x[3]);
-      t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-      t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-      const bool grow = t - w.m[mt][y] > kRescaleThreshold;  // (-inf - -inf is not)
-      if (__any_sync(0xffffffffu, grow)) {
-        const float alpha = grow ? fast_exp2(w.m[mt][y] - t) : 1.f;
-        if (grow) w.m[mt][y] = t;
-        w.l[mt][y] *= alpha;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          w.o[mt][y][j].x *= alpha;
-          w.o[mt][y][j].y *= alpha;
-        }
-      }
-      // a row that has seen no token yet has only weights of 0
-      const float ref = (MASK && w.m[mt][y] == -INFINITY ? 0.f : w.m[mt][y]) - kPShift;
-      const float p0 = fast_exp2(x[0] - ref), p1 = fast_exp2(x[1] - ref);
-      const float p2 = fast_exp2(x[2] - ref), p3 = fast_exp2(x[3] - ref);
-      w.l[mt][y] += (p0 + p1) + (p2 + p3);
-      p[mt][y] = pack_half2_rn(p0, p1);
-      p[mt][2 + y] = pack_half2_rn(p2, p3);
-    }
-  }
-  const float2 vs2 = make_float2(vs, vs);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t a = h ? v[0].y : v[0].x, b = h ? v[1].y : v[1].x;
-    const uint32_t c = h ? v[2].y : v[2].x, d = h ? v[3].y : v[3].x;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      uint32_t b00, b01, b10, b11;
-      codes4_to_half2x2(__byte_perm(a, b, u ? 0x7362 : 0x5140), b00, b01);
-      codes4_to_half2x2(__byte_perm(c, d, u ? 0x7362 : 0x5140), b10, b11);
-      const int j = 4 * h + 2 * u;
+    for (int j = 0; j < 4; ++j) {
+      uint32_t a, b, c, d;
+      codes4_to_half2x2(w0[j], a, b);
+      codes4_to_half2x2(w1[j], c, d);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        float acc[4];
-        mma_rows_zero(acc, p[mt], b00, b10);
-        w.o[mt][0][j] = __ffma2_rn(make_float2(acc[0], acc[1]), vs2, w.o[mt][0][j]);
-        w.o[mt][1][j] = __ffma2_rn(make_float2(acc[2], acc[3]), vs2, w.o[mt][1][j]);
-        mma_rows_zero(acc, p[mt], b01, b11);
-        w.o[mt][0][j + 1] = __ffma2_rn(make_float2(acc[0], acc[1]), vs2, w.o[mt][0][j + 1]);
-        w.o[mt][1][j + 1] = __ffma2_rn(make_float2(acc[2], acc[3]), vs2, w.o[mt][1][j + 1]);
+        if (j == 0) {
+          mma_rows_zero(s0[mt], w.q[mt][j], a, b);
+          mma_rows_zero(s1[mt], w.q[mt][j], c, d);
+        } else {
+          mma_rows(s0[mt], w.q[mt][j], a, b);
+          mma_rows(s1[mt], w.q[mt][j], c, d);
+        }
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float f = w.factor[nt] * ks[t];
+      x[t][nt][0] = s0[nt >> 1][2 * (nt & 1)] * f;
+      x[t][nt][1] = s0[nt >> 1][2 * (nt & 1) + 1] * f;
+      x[t][nt][2] = s1[nt >> 1][2 * (nt & 1)] * f;
+      x[t][nt][3] = s1[nt >> 1][2 * (nt & 1) + 1] * f;
+    }
+    if (MASK) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int token = first[t] + t0 + 2 * (i & 1) + 8 * (i >> 1);
+        if (token > end) v[t][i] = make_uint2(0u, 0u);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          if (token > w.pos[nt]) x[t][nt][i] = -INFINITY;
+      }
+    }
+  }
+  float top[NT];
+  bool any = false;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float y = fmaxf(max3f(x[0][nt][0], x[0][nt][1], x[0][nt][2]), x[0][nt][3]);
+    if (T == 2) y = max3f(max3f(y, x[T - 1][nt][0], x[T - 1][nt][1]), x[T - 1][nt][2], x[T - 1][nt][3]);
+    y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
+    top[nt] = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
+    any |= top[nt] - w.m[nt] > kRescaleThreshold;  // (-inf - -inf is not)
+  }
+  if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool grow = top[nt] - w.m[nt] > kRescaleThreshold;
+      const float alpha = grow ? fast_exp2(w.m[nt] - top[nt]) : 1.f;
+      if (grow) w.m[nt] = top[nt];
+      w.l[nt] *= alpha;
+      const float2 a2 = make_float2(__shfl_sync(0xffffffffu, alpha, 8 * q),  // rows 2 q and 2 q + 1
+                                    __shfl_sync(0xffffffffu, alpha, 8 * q + 4));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w.o[nt][j][0] = __fmul2_rn(w.o[nt][j][0], a2);
+        w.o[nt][j][1] = __fmul2_rn(w.o[nt][j][1], a2);
+      }
+    }
+  }
+  uint32_t p[T][NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    // a row that has seen no token yet has only weights of 0
+    const float ref = (MASK && w.m[nt] == -INFINITY ? 0.f : w.m[nt]) - kPShift;
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      const float p0 = fast_exp2(x[t][nt][0] - ref), p1 = fast_exp2(x[t][nt][1] - ref);
+      const float p2 = fast_exp2(x[t][nt][2] - ref), p3 = fast_exp2(x[t][nt][3] - ref);
+      w.l[nt] += (p0 + p1) + (p2 + p3);
+      p[t][nt][0] = pack_half2_rn(p0, p1);
+      p[t][nt][1] = pack_half2_rn(p2, p3);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const float2 vs2 = make_float2(vs[t], vs[t]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t a = h ? v[t][0].y : v[t][0].x, b = h ? v[t][1].y : v[t][1].x;
+      const uint32_t c = h ? v[t][2].y : v[t][2].x, d = h ? v[t][3].y : v[t][3].x;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t f[4];  // dims 8 r + 4 h + 2 u (and + 1) by the lane's four tokens
+        codes4_to_half2x2(__byte_perm(a, b, u ? 0x7362 : 0x5140), f[0], f[1]);
+        codes4_to_half2x2(__byte_perm(c, d, u ? 0x7362 : 0x5140), f[2], f[3]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float acc[4];
+          mma_rows_zero(acc, f, p[t][nt][0], p[t][nt][1]);
+          float2(&o)[2] = w.o[nt][2 * h + u];
+          o[0] = __ffma2_rn(make_float2(acc[0], acc[1]), vs2, o[0]);
+          o[1] = __ffma2_rn(make_float2(acc[2], acc[3]), vs2, o[1]);
+        }
       }
     }
   }
@@ -227,12 +269,12 @@ __device__ __forceinline__ void fold(int n, const ML& ml, const Row& row, float&
   }
 }
 
-template <int MT>
+template <int NT>
 constexpr int smem_bytes() {
-  return kWarps * kStages * (kStageBytes + 8) + (kWarps + 1) * 16 * MT * kRecordFloats * 4;
+  return kWarps * kStages * (kStageBytes + 8) + (kWarps + 1) * 8 * NT * kRecordFloats * 4;
 }
 
-template <int MT>
+template <int NT>
 __global__ void __launch_bounds__(kThreads, 2)
 paged_rows_q8_kernel(const __grid_constant__ RowsParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -243,7 +285,7 @@ paged_rows_q8_kernel(const __grid_constant__ RowsParams p) {
   uint8_t* ring = smem + warp * (kStages * kStageBytes);
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + kWarps * kStages * kStageBytes) + warp * kStages;
   float* records = reinterpret_cast<float*>(smem + kWarps * kStages * (kStageBytes + 8));  // [warp][row]
-  float* folded = records + kWarps * 16 * MT * kRecordFloats;                             // [row]
+  float* folded = records + kWarps * 8 * NT * kRecordFloats;                             // [row]
   const int rank = static_cast<int>(cluster_rank()), ctas = static_cast<int>(cluster_size());
   const int seg = static_cast<int>(blockIdx.x) / ctas;
   const int KV = p.num_kv_heads;
@@ -259,7 +301,7 @@ paged_rows_q8_kernel(const __grid_constant__ RowsParams p) {
     if (g == 0 && rank == 0 && tid == 0) flag_error(p.status, PA_DEVFLAG_BAD_CONTEXT);
     return;
   }
-  const int rows = q_len * p.group;  // <= 16 MT
+  const int rows = q_len * p.group;  // <= 8 NT
   // this warp's blocks of the segment
   const int nb = (L + kBlockSize - 1) / kBlockSize;
   const int parts = ctas * kWarps, part = rank * kWarps + warp;
@@ -292,6 +334,7 @@ paged_rows_q8_kernel(const __grid_constant__ RowsParams p) {
     if (__any_sync(0xffffffffu, bad) && lane == 0) flag_error(p.status, PA_DEVFLAG_BAD_BLOCK);
     return w;
   };
+  constexpr int T = NT <= kPairGroups ? 2 : 1;  // tiles per step
   const uint64_t policy = l2_evict_first_policy();
   auto request = [&](int32_t tile, int st) {
     if (tile >= 0) {
@@ -309,98 +352,108 @@ paged_rows_q8_kernel(const __grid_constant__ RowsParams p) {
   if (lane < issued) request(cur.tile, lane);
   Window nxt = window(kWindow);
 
-  Rows<MT> w;
+  Rows<NT> w;
   // The queries, to f16 under each row's power of two (rows past the last repeat it).
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
+  for (int nt = 0; nt < (NT + 1) / 2 * 2; ++nt) {
+    const int mt = nt >> 1, y = nt & 1;
+    const int row = min(8 * nt + r, rows - 1);
+    const uint4* src = reinterpret_cast<const uint4*>(
+        p.q + (static_cast<int64_t>(q0 + row / p.group) * p.num_q_heads + g * p.group + row % p.group) * kHeadDim) + 2 * q;
+    const uint4 a = __ldg(src), b = __ldg(src + 1);
+    const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t big = 0u;
 #pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      const int row = min(16 * mt + 8 * y + r, rows - 1);
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.q + (static_cast<int64_t>(q0 + row / p.group) * p.num_q_heads + g * p.group + row % p.group) * kHeadDim) + 2 * q;
-      const uint4 a = __ldg(src), b = __ldg(src + 1);
-      const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      uint32_t big = 0u;
+    for (int i = 0; i < 8; ++i) big = max(big, max((x[i] << 16) & 0x7fff0000u, x[i] & 0x7fff0000u));
+    big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+    big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+    int shift = 0;
+    if (big != 0u && big < 0x7f800000u)
+      shift = min(126, kQExp + 127 - static_cast<int>(max(big >> 23, 1u)));
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) big = max(big, max((x[i] << 16) & 0x7fff0000u, x[i] & 0x7fff0000u));
-      big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-      big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-      int shift = 0;
-      if (big != 0u && big < 0x7f800000u)
-        shift = min(126, kQExp + 127 - static_cast<int>(max(big >> 23, 1u)));
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
-      w.factor[mt][y] = p.q_scale * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+    for (int j = 0; j < 4; ++j) {
+      const float2 c = bf16x2_to_float2(x[2 * j]), d = bf16x2_to_float2(x[2 * j + 1]);
+      w.q[mt][j][y] = nt < NT ? pack_half2_rn(c.x * up, c.y * up) : 0u;
+      w.q[mt][j][2 + y] = nt < NT ? pack_half2_rn(d.x * up, d.y * up) : 0u;
+    }
+    if (nt < NT) {
+      w.factor[nt] = p.q_scale * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+      w.pos[nt] = L - q_len + row / p.group;
+      w.m[nt] = -INFINITY;
+      w.l[nt] = 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 c = bf16x2_to_float2(x[2 * j]), d = bf16x2_to_float2(x[2 * j + 1]);
-        w.q[mt][j][y] = pack_half2_rn(c.x * up, c.y * up);
-        w.q[mt][j][2 + y] = pack_half2_rn(d.x * up, d.y * up);
-      }
-      w.m[mt][y] = -INFINITY;
-      w.l[mt][y] = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w.o[mt][y][j] = make_float2(0.f, 0.f);
+      for (int j = 0; j < 4; ++j) w.o[nt][j][0] = w.o[nt][j][1] = make_float2(0.f, 0.f);
     }
   }
 
   // blocks below this one are seen whole by every row
-  const int whole = (L - q_len + 1) / kBlockSize;
+  const int whole = (L - q_len + 1) / kBlockSize - b_lo;
   bool ok = true;
   int k = 0;
 #pragma unroll 1
-  for (; k < n; ++k) {
+  while (k < n) {
     if (k > 0 && (k & (kWindow - 1)) == 0) {
       cur = nxt;
       nxt = window(k + kWindow);
     }
-    const int st = k % kStages;
-    const bool here = mbar_wait(&full_bar[st], static_cast<uint32_t>((k / kStages) & 1));
+    // (windows and rings hold an even number of tiles and the steps but the last are of T, so a
+    // step's tiles lie in one window)
+    const int left = n - k;
+    const uint8_t* tiles[T];
+    float ks[T], vs[T];
+    int first[T];
+    bool here = true;
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      const int at = t < left ? k + t : k;  // a step short of tiles repeats the first, unseen
+      here &= mbar_wait(&full_bar[at % kStages], static_cast<uint32_t>((at / kStages) & 1));
+      tiles[t] = ring + at % kStages * kStageBytes;
+      ks[t] = __shfl_sync(0xffffffffu, cur.ks, at & (kWindow - 1));
+      vs[t] = __shfl_sync(0xffffffffu, cur.vs, at & (kWindow - 1));
+      first[t] = t < left ? (b_lo + at) * kBlockSize : 0x7fffff00;
+    }
     if (!(ok = __all_sync(0xffffffffu, here))) break;
-    const float ks = __shfl_sync(0xffffffffu, cur.ks, k & (kWindow - 1));
-    const float vs = __shfl_sync(0xffffffffu, cur.vs, k & (kWindow - 1));
-    const uint8_t* tile = ring + st * kStageBytes;
-    int last[MT][2] = {};
-    const int first = (b_lo + k) * kBlockSize;  // token 0 of the tile
-    if (b_lo + k < whole) {
-      attend_tile<MT, false>(tile, r, q, ks, vs, last, kBlockSize - 1, w);
+    if (k + T <= min(whole, n)) {
+      attend_tiles<NT, T, false>(tiles, r, q, ks, vs, first, 0, w);
     } else {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-          last[mt][y] = L - q_len + min(16 * mt + 8 * y + r, rows - 1) / p.group - first;
-      attend_tile<MT, true>(tile, r, q, ks, vs, last, L - 1 - first, w);
+      for (int t = 1; t < T; ++t)
+        if (t >= left) vs[t] = 0.f;
+      attend_tiles<NT, T, true>(tiles, r, q, ks, vs, first, L - 1, w);
     }
-    __syncwarp();  // every lane has read the stage
-    if (issued < n) {
-      const int32_t a = __shfl_sync(0xffffffffu, cur.tile, issued & (kWindow - 1));
-      const int32_t b = __shfl_sync(0xffffffffu, nxt.tile, issued & (kWindow - 1));
-      if (lane == 0) request((issued ^ k) & ~(kWindow - 1) ? b : a, st);
-      ++issued;
+    __syncwarp();  // every lane has read the stages
+    k += T;
+    const int more = min(T, n - issued);
+    if (more > 0) {
+      const int i = issued + min(lane, more - 1);
+      const int32_t a = __shfl_sync(0xffffffffu, cur.tile, i & (kWindow - 1));
+      const int32_t b = __shfl_sync(0xffffffffu, nxt.tile, i & (kWindow - 1));
+      if (lane < more) request(((issued ^ (k - T)) & ~(kWindow - 1)) != 0 ? b : a, i % kStages);
+      issued += more;
     }
   }
   if (!ok && lane == 0) {  // leave no copy in flight (bounded waits)
     flag_error(p.status, PA_DEVFLAG_TIMEOUT);
-    for (int t = k; t < issued; ++t)
+    for (int t = k; t < issued; ++t)  // (the step's own first)
       if (!mbar_wait(&full_bar[t % kStages], static_cast<uint32_t>((t / kStages) & 1))) break;
   }
 
   // ---- the warps' shares meet ----
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      float l = w.l[mt][y];
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      float* dst = records + (warp * 16 * MT + 16 * mt + 8 * y + r) * kRecordFloats;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        *reinterpret_cast<float2*>(dst + 16 * q + 2 * j) = make_float2(w.o[mt][y][2 * j].x, w.o[mt][y][2 * j + 1].x);
-        *reinterpret_cast<float2*>(dst + 16 * q + 8 + 2 * j) = make_float2(w.o[mt][y][2 * j].y, w.o[mt][y][2 * j + 1].y);
-      }
-      if (q == 0) *reinterpret_cast<float2*>(dst + kHeadDim) = make_float2(w.m[mt][y], l * kVFactor);
-    }
+  for (int nt = 0; nt < NT; ++nt) {
+    float l = w.l[nt];
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    float* rec = records + (warp * 8 * NT + 8 * nt) * kRecordFloats;
+    if (q == 0) *reinterpret_cast<float2*>(rec + r * kRecordFloats + kHeadDim) = make_float2(w.m[nt], l * kVFactor);
+    const auto& o = w.o[nt];
+    float4* dst = reinterpret_cast<float4*>(rec + 2 * q * kRecordFloats + 8 * r);
+    dst[0] = make_float4(o[0][0].x, o[0][1].x, o[1][0].x, o[1][1].x);
+    dst[1] = make_float4(o[2][0].x, o[2][1].x, o[3][0].x, o[3][1].x);
+    dst += kRecordFloats / 4;
+    dst[0] = make_float4(o[0][0].y, o[0][1].y, o[1][0].y, o[1][1].y);
+    dst[1] = make_float4(o[2][0].y, o[2][1].y, o[3][0].y, o[3][1].y);
   }
   __syncthreads();
   auto finish = [&](int row, int c, float Lsum, const float4& acc) {
@@ -418,8 +471,8 @@ paged_rows_q8_kernel(const __grid_constant__ RowsParams p) {
     const int row = i >> 4, c = i & 15;
     const float* rec = records + row * kRecordFloats;
     fold<kWarps>(
-        kWarps, [&](int x) { return *reinterpret_cast<const float2*>(rec + x * 16 * MT * kRecordFloats + kHeadDim); },
-        [&](int x) { return *reinterpret_cast<const float4*>(rec + x * 16 * MT * kRecordFloats + 4 * c); }, M, Ls, acc);
+        kWarps, [&](int x) { return *reinterpret_cast<const float2*>(rec + x * 8 * NT * kRecordFloats + kHeadDim); },
+        [&](int x) { return *reinterpret_cast<const float4*>(rec + x * 8 * NT * kRecordFloats + 4 * c); }, M, Ls, acc);
     if (ctas == 1) {
       finish(row, c, Ls, acc);
     } else {
@@ -441,16 +494,16 @@ paged_rows_q8_kernel(const __grid_constant__ RowsParams p) {
   cluster_sync();  // this CTA's shared memory outlives the others' reads
 }
 
-template <int MT>
+template <int NT>
 cudaError_t launch(const RowsParams& p, int64_t segments, int cluster, cudaStream_t stream) {
   static bool done[kMaxDevices] = {};  // benign race: the attribute calls are idempotent
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= kMaxDevices || !done[dev]) {
-    e = cudaFuncSetAttribute(paged_rows_q8_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<MT>());
+    e = cudaFuncSetAttribute(paged_rows_q8_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NT>());
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(paged_rows_q8_kernel<MT>, cudaFuncAttributePreferredSharedMemoryCarveout,
+      e = cudaFuncSetAttribute(paged_rows_q8_kernel<NT>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
     if (dev < kMaxDevices) done[dev] = true;
@@ -458,7 +511,7 @@ cudaError_t launch(const RowsParams& p, int64_t segments, int cluster, cudaStrea
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(segments * cluster));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes<MT>();
+  cfg.dynamicSmemBytes = smem_bytes<NT>();
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -467,7 +520,7 @@ cudaError_t launch(const RowsParams& p, int64_t segments, int cluster, cudaStrea
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, paged_rows_q8_kernel<MT>, p);
+  e = cudaLaunchKernelEx(&cfg, paged_rows_q8_kernel<NT>, p);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
@@ -503,14 +556,19 @@ cudaError_t launch_rows_q8(const AttendQ8Args& a, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  // CTAs per segment: as many as run side by side and have a few tiles per warp each.
+  // CTAs per segment: as many as run side by side, two per SM, and may have a tile per warp each
+  // (5 rows at 1000 tokens 6.7 us with clusters up to that, 9.0 where it takes four tiles).
   const int64_t segments = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
   int cluster = 1;
   while (cluster < kMaxCluster && segments * cluster * 2 <= 2 * sms &&
-         a.max_blocks_per_seq >= 2 * cluster * kWarps * kStages)
+         a.max_blocks_per_seq >= 2 * cluster * kWarps)
     cluster *= 2;
-  return p.max_query_len * p.group <= 16 ? launch<1>(p, segments, cluster, stream)
-                                         : launch<2>(p, segments, cluster, stream);
+  switch ((p.max_query_len * p.group + 7) / 8) {  // groups of eight rows
+    case 1: return launch<1>(p, segments, cluster, stream);
+    case 2: return launch<2>(p, segments, cluster, stream);
+    case 3: return launch<3>(p, segments, cluster, stream);
+    default: return launch<4>(p, segments, cluster, stream);
+  }
 }
 
 }  // namespace pkv

@@ -288,6 +288,40 @@ def test_chunk_of_one_row(hq, hkv):
     check_chunk(wl.make_workload("later", [333], [1], num_prefill=1, seed=hq, pool_slack=1.0), hkv, hq)
 
 
+@pytest.mark.parametrize("hq,hkv,most", [(32, 8, 8), (32, 8, 5), (4, 1, 4), (4, 1, 2), (2, 1, 16), (2, 2, 32),
+                                         (3, 3, 9)])
+def test_chunk_of_few_rows(hq, hkv, most):
+    """At most 32 rows per K/V head, every count of them, at every place in a block; from one
+    segment (a cluster of CTAs) to many."""
+    rng = np.random.default_rng(most)
+    for seqs in (1, 3, 19, 90):
+        new = np.concatenate([[most], rng.integers(0, most + 1, size=seqs - 1)]).astype(int)
+        prior = rng.integers(0, 300, size=seqs)
+        prior[0] = 3000 if seqs < 19 else 700
+        w = wl.make_workload(f"few{seqs}", prior, new, num_prefill=seqs, seed=seqs, pool_slack=0.3)
+        check_chunk(w, hkv, hq)
+
+
+def test_chunk_of_few_rows_refuses_longer_ones_and_repeats():
+    w = wl.make_workload("longer", [100, 40, 2000], [5, 7, 3], num_prefill=3, seed=4, pool_slack=0.3)
+    st = State(w, 8, 32, rows=15)
+    ref, tol = attend(st.q, st.k64, st.v64, w.block_tables, w.context_lens, st.scale, w.new_lens)
+    got = st.chunk(5)  # the second chunk has more rows
+    assert int(st.status.item()) == pa.DEVFLAG_BAD_CONTEXT
+    assert bool(torch.isnan(got[5:12]).all())
+    close(got[:5], ref[:5], tol[:5], "first")
+    close(got[12:], ref[12:], tol[12:], "third")
+    st.status.zero_()
+    whole = st.chunk()
+    assert st.ok() and torch.equal(st.chunk(), whole)
+    close(whole, ref, tol, "all")
+    bt = w.block_tables.copy()
+    bt[1, 1], bt[2, 0] = w.num_blocks, -1
+    st.bt = i32(bt)
+    assert torch.equal(st.chunk()[:5], whole[:5])
+    assert int(st.status.item()) == pa.DEVFLAG_BAD_BLOCK
+
+
 def test_chunk_long():
     w = wl.make_workload("long", [1500, 0, 5000], [700, 1030, 3], num_prefill=3, seed=4)
     check_chunk(w, 1, 4)
