@@ -46,7 +46,9 @@ cudaError_t launch_copy_blocks(void* key_cache, void* value_cache, const int64_t
   return cudaGetLastError();
 }
 
-// The same for the 8-bit pools: a block is Hkv KiB of codes in each pool and Hkv scales.
+// The same for the 8-bit pools: a block is Hkv KiB of codes in each pool and Hkv scales.  4096
+// blocks of 8 heads 23.1 us, 5.8 TB/s or 0.86 of the measured copy rate (blocks of 8 KiB, and a
+// launch that ends after ten waves); two chunks per thread gave nothing.  16 blocks 1.8 us: the launch.
 __global__ void copy_blocks_q8_kernel(uint4* __restrict__ key_cache, uint4* __restrict__ value_cache,
                                       float* __restrict__ key_scale,
                                       float* __restrict__ value_scale,

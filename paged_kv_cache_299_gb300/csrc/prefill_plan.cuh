@@ -162,7 +162,8 @@ __device__ __forceinline__ int block_exclusive_scan(int v, int* scratch, int* to
 // in pair order, THREADS pairs per round), and take this CTA's units.  Returns the unit count, or
 // -1 when the batch has more pairs than the sort handles (grid order then).
 // RANK_PAIRS > 0: up to that many pairs are ranked directly, each thread counting the pairs that
-// come before its own (fewer barriers than the counting sort), and unit_q0 / unit_len / unit_L
+// come before its own (fewer barriers than the counting sort: 8 chunks of 512 rows 70.9 us against
+// 72.7), and unit_q0 / unit_len / unit_L
 // keep each unit's sequence for next_unit<.., true>.
 template <int TOKENS, int KEYS, int THREADS, int RANK_PAIRS = 0>
 __device__ int plan_units(const PParams& p, uint8_t* scratch, int* red, int32_t* unit_s,
