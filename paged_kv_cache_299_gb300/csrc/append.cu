@@ -32,11 +32,27 @@ constexpr int kLanesPerRow = kPairs / kLanePairs;  // 4
 constexpr int kRowsPerWarp = 32 / kLanesPerRow;   // 8 head rows side by side
 constexpr int kUnroll = 3;  // rows a lane has in flight: 48 rows (32 + 2 x 8 heads) in two rounds
 
+// The last i in [0, n) with value(i) <= key, for value rising and value(0) <= key (0 otherwise).  A
+// warp probes 32 places a step, so a batch of up to 32 sequences costs one load's latency.
+template <typename Value>
+__device__ __forceinline__ int32_t last_at_most(int32_t n, int64_t key, int lane, const Value& value) {
+  int32_t lo = 0;
+  while (n > 1) {
+    const int32_t step = (n + 31) / 32;
+    const int32_t i = lane * step;
+    const unsigned le = __ballot_sync(0xffffffffu, i < n && value(lo + i) <= key);
+    const int32_t skip = max(__popc(le) - 1, 0) * step;
+    lo += skip;
+    n = min(step, n - skip);
+  }
+  return lo;
+}
+
 // Sequence of token t (the last s with query_start_loc[s] <= t; without query_start_loc,
 // sequence t) and its logical position.  false: the token is padding (at or past
 // query_start_loc[num_seqs], or a context of 0 in the one-token form) or was flagged.  (Rows past
 // num_tokens are flagged through token 0, as their own have no warp.)
-__device__ __forceinline__ bool locate(const AppendArgs& a, int32_t t, bool report, int32_t* seq,
+__device__ __forceinline__ bool locate(const AppendArgs& a, int32_t t, int lane, bool report, int32_t* seq,
                                        int64_t* pos) {
   int32_t s, first, q_len;
   if (a.query_start_loc == nullptr) {
@@ -48,12 +64,7 @@ __device__ __forceinline__ bool locate(const AppendArgs& a, int32_t t, bool repo
     const int32_t end = a.query_start_loc[a.num_seqs];
     if (t == 0 && report && end > a.num_tokens) flag_error(a.status, PA_DEVFLAG_BAD_CONTEXT);
     if (t >= end) return false;
-    int32_t lo = 0, hi = a.num_seqs - 1;
-    while (lo < hi) {
-      const int32_t mid = (lo + hi + 1) >> 1;
-      if (a.query_start_loc[mid] <= t) lo = mid; else hi = mid - 1;
-    }
-    s = lo;
+    s = last_at_most(a.num_seqs, t, lane, [&](int32_t i) { return a.query_start_loc[i]; });
     first = a.query_start_loc[s];
     q_len = a.query_start_loc[s + 1] - first;
   }
@@ -129,7 +140,7 @@ template <bool kInterleaved, bool kStore>
 __device__ void token_rows(const AppendArgs& a, int32_t t, int part, int parts, int lane) {
   int32_t seq;
   int64_t pos;
-  if (!locate(a, t, part == 0 && lane == 0, &seq, &pos)) return;
+  if (!locate(a, t, lane, part == 0 && lane == 0, &seq, &pos)) return;
   const int l = lane % kLanesPerRow;
   const int c0 = first_chunk<kInterleaved>(l), c1 = second_chunk<kInterleaved>(l);
   Angles g;
@@ -352,12 +363,7 @@ __device__ void block_rows(const AppendArgs& a, int64_t item, int lane) {
   {
     // sequence s owns indices base(s) .. base(s+1)-1 with base(s) = start(s) / 16 + 2 s, at
     // least as many as the blocks its tokens can touch
-    int32_t lo = 0, hi = a.num_seqs - 1;
-    while (lo < hi) {
-      const int32_t mid = (lo + hi + 1) >> 1;
-      if ((a.query_start_loc[mid] >> 4) + 2ll * mid <= v) lo = mid; else hi = mid - 1;
-    }
-    s = lo;
+    s = last_at_most(a.num_seqs, v, lane, [&](int32_t i) { return (a.query_start_loc[i] >> 4) + 2ll * i; });
     first = a.query_start_loc[s];
     q_len = a.query_start_loc[s + 1] - first;
     index = v - ((first >> 4) + 2ll * s);
