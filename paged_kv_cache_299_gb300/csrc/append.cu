@@ -10,8 +10,8 @@
 // Memory-bound: every row is read once and written once.  Four lanes carry one head row, each
 // both members of eight pairs, so a row's rotation needs no exchange and a lane's cosines and
 // sines serve all the heads of its token.  Measured (32 query and 8 K/V heads): 16,000 prompt
-// tokens 32.7 us into the bf16 pools, 6.2 TB/s or 0.91 of the measured copy rate, 35.1 us into the
-// 8-bit ones, 5.1 TB/s (0.75; the block's maximum stands between its loads and its stores); a
+// tokens 32.7 us into the bf16 pools, 6.2 TB/s or 0.91 of the measured copy rate, 32.2 us into the
+// 8-bit ones, 5.6 TB/s (0.82; the block's maximum stands between its loads and its stores); a
 // decode step of 64 tokens 2.0 us and of 256 into the 8-bit pools 2.3, three dependent loads
 // (context, block table, scale) and the launch.
 #include <math.h>
@@ -446,13 +446,21 @@ __device__ void block_rows(const AppendArgs& a, int64_t item, int lane) {
   if (lane == 0) *scale = now;
 }
 
-// Warps 0 .. items-1 serve the blocks, the rest the query rows.
+// Item CTAs serve the blocks (or a step's tokens), the rest the query rows: the item CTAs first,
+// or, with share > 0, both kinds alternating in proportion (share: item CTAs per CTA, times 2^31).
 template <bool kRotate, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads)
-rope_append_q8_kernel(const AppendArgs a, int64_t items, int64_t item_ctas, int parts) {
+rope_append_q8_kernel(const AppendArgs a, int64_t items, uint32_t item_ctas, uint32_t share, int parts) {
   const int lane = threadIdx.x & 31;
-  if (blockIdx.x < item_ctas) {
-    const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarpsPerCta + (threadIdx.x >> 5);
+  uint32_t before = min(blockIdx.x, item_ctas);  // item CTAs before this one
+  bool item = blockIdx.x < item_ctas;
+  if (share > 0) {
+    const uint64_t mark = static_cast<uint64_t>(blockIdx.x) * share;
+    before = static_cast<uint32_t>(mark >> 31);
+    item = static_cast<uint32_t>((mark + share) >> 31) > before;
+  }
+  if (item) {
+    const int64_t w = static_cast<int64_t>(before) * kWarpsPerCta + (threadIdx.x >> 5);
     if (w >= items) return;
     if (a.query_start_loc == nullptr)
       step_rows<kRotate, kInterleaved>(a, w, lane);
@@ -461,7 +469,7 @@ rope_append_q8_kernel(const AppendArgs a, int64_t items, int64_t item_ctas, int 
     return;
   }
   if (kRotate) {
-    const int64_t w = (blockIdx.x - item_ctas) * kWarpsPerCta + (threadIdx.x >> 5);
+    const int64_t w = static_cast<int64_t>(blockIdx.x - before) * kWarpsPerCta + (threadIdx.x >> 5);
     const int64_t t = w / parts;
     if (t < a.num_tokens)
       token_rows<kInterleaved, false>(a, static_cast<int32_t>(t), static_cast<int>(w % parts),
@@ -502,13 +510,22 @@ cudaError_t launch_rope_append_q8(const AppendArgs& a, cudaStream_t stream) {
     parts = parts_for(a.num_tokens, a.num_q_heads);
     q_ctas = (static_cast<int64_t>(a.num_tokens) * parts + kWarpsPerCta - 1) / kWarpsPerCta;
   }
-  const unsigned grid = static_cast<unsigned>(item_ctas + q_ctas);
+  const int64_t ctas = item_ctas + q_ctas;
+  // In a batch of several waves the blocks' chains of loads run beside the queries' stream: 16,000
+  // prompt tokens 32.2 us against 34.4 with the item CTAs first.  Those start a small one earlier:
+  // 3000 tokens 9.8 us against 10.1, steps of 1024 tokens 3.3 against 3.6.
+  constexpr int64_t kAlternateCtas = 152 * 24;
+  // (rounded up: with fewer than 2^31 CTAs that adds no item CTA)
+  const uint32_t share =
+      ctas > kAlternateCtas && q_ctas > 0 ? static_cast<uint32_t>(((item_ctas << 31) + ctas - 1) / ctas) : 0;
+  const unsigned grid = static_cast<unsigned>(ctas);
+  const uint32_t first = static_cast<uint32_t>(item_ctas);
   if (a.cos_sin == nullptr)
-    rope_append_q8_kernel<false, false><<<grid, kThreads, 0, stream>>>(a, items, item_ctas, parts);
+    rope_append_q8_kernel<false, false><<<grid, kThreads, 0, stream>>>(a, items, first, share, parts);
   else if (a.interleaved)
-    rope_append_q8_kernel<true, true><<<grid, kThreads, 0, stream>>>(a, items, item_ctas, parts);
+    rope_append_q8_kernel<true, true><<<grid, kThreads, 0, stream>>>(a, items, first, share, parts);
   else
-    rope_append_q8_kernel<true, false><<<grid, kThreads, 0, stream>>>(a, items, item_ctas, parts);
+    rope_append_q8_kernel<true, false><<<grid, kThreads, 0, stream>>>(a, items, first, share, parts);
   return cudaGetLastError();
 }
 
