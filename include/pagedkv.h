@@ -346,8 +346,9 @@ pa_status pa_copy_blocks(void* key_cache, void* value_cache, pa_cache_desc cd,
  * context_lens[s] tokens, as in pa_compute_slot_mapping) have their query and key rows rotated
  * by their logical positions (rotary position embedding) and their key and value rows stored
  * to their slots, in one launch: slot mapping, rotation and pa_reshape_and_cache in one
- * ("vLLM" (blog.rlaisqls.com), section Optimized CUDA Kernels: fused kernels skip HBM round
- * trips; the pages describe no counterpart of the rotation itself).
+ * (the sin/cos rotation of q and k before the cache write: "tiny-vLLM overview"
+ * (agentlenshq.com), CUDA kernels, and "tiny-vllm (1)" (geonuchoi.com), RoPE; in one kernel:
+ * "vLLM" (blog.rlaisqls.com), section Optimized CUDA Kernels, fused kernels skip HBM round trips).
  * The token at position p turns the pair i (i = 0 .. 31) of every query and key head row,
  *   (a, b) -> (a cos - b sin, b cos + a sin),
  *   cos = cos_sin[p][i], sin = cos_sin[p][32 + i],
