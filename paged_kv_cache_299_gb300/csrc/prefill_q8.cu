@@ -32,8 +32,8 @@
 //     three raw tiles, the blocks' scales beside them by 4-byte asynchronous copies on the same
 //     mbarrier; Q by TMA.  (One bulk copy per block and pool took some 1,600 cycles a tile to
 //     issue.)
-// Measured: 3 chunks of some 4000 rows over 8000 tokens 668 us, 811 TFLOP/s or 0.42 of the measured
-// bf16 product rate; 8 chunks of 512 rows 69.8 us (566 TFLOP/s).  Bound: a 128-key tile of both
+// Measured: 3 chunks of some 4000 rows over 8000 tokens 662 us, 818 TFLOP/s or 0.43 of the measured
+// bf16 product rate; 8 chunks of 512 rows 68.4 us (578 TFLOP/s).  Bound: a 128-key tile of both
 // halves takes some 2,700 cycles, in which the tensor core works about 1,600 (24 small MMAs, 60
 // to 80 cycles each whatever their N) and the row warps about 2,200 (scores from tensor memory
 // 190, maximum and its exchange 350 to 500, 64 exponentials a thread with P 1,100, P's store 270);
@@ -193,6 +193,16 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
   return static_cast<uint32_t>(r * kRowBytes + ((c ^ (r & 7)) << 4));
 }
 
+// Lanes whose numbers differ in bit `d` exchange: the lower's b for the upper's a.
+__device__ __forceinline__ void swap_chunks(uint4& a, uint4& b, bool upper, int d) {
+  uint4 give = upper ? a : b;
+  give.x = __shfl_xor_sync(0xffffffffu, give.x, d);
+  give.y = __shfl_xor_sync(0xffffffffu, give.y, d);
+  give.z = __shfl_xor_sync(0xffffffffu, give.z, d);
+  give.w = __shfl_xor_sync(0xffffffffu, give.w, d);
+  if (upper) a = give; else b = give;
+}
+
 template <int GROUP>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q,
@@ -303,7 +313,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q,
     const int half = warp >> 3;
     const int part = (warp >> 2) & 1;  // keys 64 part .. 64 part + 63 of every tile
     const int r = (warp & 3) * 32 + lane;  // row of the half == TMEM lane
-    const int tt = r / GROUP, hh = r % GROUP;
+    const int tt = r / GROUP;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t s_addr = lane_addr + kSCol + half * kTileN + part * (kTileN / 2);
     const uint32_t p_addr = lane_addr + kPCol + half * (kTileN / 2) + part * (kTileN / 4);
@@ -375,19 +385,19 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q,
     while (ok) {
       // of a unit, only what a row needs stays in registers
       int n_mine, n_kv, pos, pos_lo;
-      bool row_ok, next_mine;
-      __nv_bfloat16* dst;
+      int out_token, out_left, out_head;  // the half's first output row, its rows left, the K/V head
+      bool next_mine;
       {
         Unit u;
         if (!next_unit<kUnitTokens, kTileN, true>(p, sc, k, u)) break;
         n_mine = half_tiles<kHalfTokens>(u, half);
         n_kv = u.n_kv;
         const int token = u.tok0 + half * kHalfTokens + tt;
-        row_ok = token < u.q_len;
         pos = u.L - u.q_len + min(token, u.q_len - 1);
         pos_lo = u.L - u.q_len + u.tok0 + half * kHalfTokens;
-        dst = p.out + (static_cast<int64_t>(u.q0 + token) * p.num_q_heads + u.g * GROUP + hh) * kHeadDim +
-              part * (kHeadDim / 2);
+        out_token = u.q0 + u.tok0 + half * kHalfTokens;
+        out_left = u.q_len - u.tok0 - half * kHalfTokens;
+        out_head = u.g;
         int peek = k;
         next_mine = next_unit<kUnitTokens, kTileN, true>(p, sc, peek, u) && half_tiles<kHalfTokens>(u, half) > 0;
       }
@@ -503,17 +513,27 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q,
         __syncwarp();
         if (lane == 0) mbar_arrive(&o_free[half]);
         const float inv = 1.f / (l + theirs);
-        if (row_ok) {
+        // Four lanes exchange what they hold (four rows by four 16-byte chunks), so that each store
+        // covers 64 bytes of eight rows: a lane's own row at a time touched 32 lines a store (8 x
+        // 512 rows 70.0 us against 68.4).
+        uint4 w[4];
 #pragma unroll
-          for (int q8 = 0; q8 < 4; ++q8) {
-            uint32_t w[4];
+        for (int c = 0; c < 4; ++c)
+          w[c] = make_uint4(pack_bf2(__uint_as_float(o[8 * c]) * inv, __uint_as_float(o[8 * c + 1]) * inv),
+                            pack_bf2(__uint_as_float(o[8 * c + 2]) * inv, __uint_as_float(o[8 * c + 3]) * inv),
+                            pack_bf2(__uint_as_float(o[8 * c + 4]) * inv, __uint_as_float(o[8 * c + 5]) * inv),
+                            pack_bf2(__uint_as_float(o[8 * c + 6]) * inv, __uint_as_float(o[8 * c + 7]) * inv));
+        swap_chunks(w[0], w[1], lane & 1, 1);
+        swap_chunks(w[2], w[3], lane & 1, 1);
+        swap_chunks(w[0], w[2], lane & 2, 2);
+        swap_chunks(w[1], w[3], lane & 2, 2);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int i = q8 * 8 + 2 * e;
-              w[e] = pack_bf2(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
-            }
-            *reinterpret_cast<uint4*>(dst + 8 * q8) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const int rr = (r & ~3) + i;
+          if (rr / GROUP < out_left)
+            *reinterpret_cast<uint4*>(
+                p.out + (static_cast<int64_t>(out_token + rr / GROUP) * p.num_q_heads + out_head * GROUP + rr % GROUP) *
+                            kHeadDim + part * (kHeadDim / 2) + 8 * (lane & 3)) = w[i];
         }
       }
       jt += n_kv;
