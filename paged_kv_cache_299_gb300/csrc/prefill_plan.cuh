@@ -2,6 +2,8 @@
 // a batch, ordered heaviest first and dealt to the CTAs of a persistent grid.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace pkv {
@@ -115,13 +117,14 @@ __device__ __forceinline__ bool next_unit(const PParams& p, const Schedule& sc, 
     fill_unit<TOKENS, KEYS>(u);
     return true;
   }
-  const int64_t per_tile = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads;
-  const int64_t total = per_tile * p.q_tiles;
+  using Index = std::conditional_t<KEPT, uint32_t, int64_t>;  // (KEPT: the host keeps the units below 2^31)
+  const Index per_tile = static_cast<Index>(p.num_seqs) * p.num_kv_heads;
+  const Index total = per_tile * p.q_tiles;
   for (;;) {
-    const int64_t x = blockIdx.x + static_cast<int64_t>(k) * gridDim.x;
+    const Index x = blockIdx.x + static_cast<Index>(k) * gridDim.x;
     if (x >= total) return false;
     ++k;
-    const int64_t rem = x % per_tile;
+    const Index rem = x % per_tile;
     u.tile = p.q_tiles - 1 - static_cast<int>(x / per_tile);
     u.g = static_cast<int>(rem / p.num_seqs);
     u.s = static_cast<int>(rem % p.num_seqs);
