@@ -637,6 +637,12 @@ pa_status pa_prefill_chunk_q8(void* out, const void* q, const int32_t* query_sta
   if (max_query_len > num_query_tokens)
     return fail(PA_ERR_INVALID_ARG, "max_query_len %d > num_query_tokens %d", max_query_len,
                 num_query_tokens);
+  const int64_t unit_tokens = 256 / group;
+  const int64_t units = static_cast<int64_t>(num_seqs) * cd.num_kv_heads *
+                        ((max_query_len + unit_tokens - 1) / unit_tokens);
+  if (units >= (int64_t{1} << 31))
+    return fail(PA_ERR_UNSUPPORTED, "%d sequences of up to %d rows: %lld work units (fewer than 2^31 supported)",
+                num_seqs, max_query_len, static_cast<long long>(units));
   if (!out || !q || !query_start_loc || !key_cache || !value_cache || !key_scale || !value_scale ||
       !block_tables || !context_lens)
     return fail(PA_ERR_INVALID_ARG, "null pointer");

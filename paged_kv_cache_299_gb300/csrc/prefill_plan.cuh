@@ -98,9 +98,10 @@ struct Schedule {
   const int32_t* unit_L = nullptr;
 };
 
-template <int TOKENS, int KEYS, bool KEPT = false>
+// LISTED: the batch is known to fit the list, and the code of the grid order is left out.
+template <int TOKENS, int KEYS, bool KEPT = false, bool LISTED = false>
 __device__ __forceinline__ bool next_unit(const PParams& p, const Schedule& sc, int& k, Unit& u) {
-  if (sc.n_units >= 0) {
+  if (LISTED || sc.n_units >= 0) {
     if (k >= sc.n_units) return false;
     u.s = sc.unit_s[k];
     const int tg = sc.unit_tg[k];
@@ -117,7 +118,8 @@ __device__ __forceinline__ bool next_unit(const PParams& p, const Schedule& sc, 
     fill_unit<TOKENS, KEYS>(u);
     return true;
   }
-  using Index = std::conditional_t<KEPT, uint32_t, int64_t>;  // (KEPT: the host keeps the units below 2^31)
+  using Index = std::conditional_t<KEPT, uint32_t, int64_t>;  // (KEPT: the caller keeps the units below 2^31; with
+  // 64-bit divisions inlined in every role, 3 chunks of some 4000 rows took 662 us against 645)
   const Index per_tile = static_cast<Index>(p.num_seqs) * p.num_kv_heads;
   const Index total = per_tile * p.q_tiles;
   for (;;) {

@@ -32,9 +32,9 @@
 //     three raw tiles, the blocks' scales beside them by 4-byte asynchronous copies on the same
 //     mbarrier; Q by TMA.  (One bulk copy per block and pool took some 1,600 cycles a tile to
 //     issue.)
-// Measured: 3 chunks of some 4000 rows over 8000 tokens 662 us, 818 TFLOP/s or 0.43 of the measured
-// bf16 product rate; 8 chunks of 512 rows 68.4 us (578 TFLOP/s).  Bound: a 128-key tile of both
-// halves takes some 2,700 cycles, in which the tensor core works about 1,600 (24 small MMAs, 60
+// Measured: 3 chunks of some 4000 rows over 8000 tokens 645 us, 840 TFLOP/s or 0.44 of the measured
+// bf16 product rate; 8 chunks of 512 rows 65.7 us (602 TFLOP/s).  Bound: a 128-key tile of both
+// halves takes some 2,600 cycles, in which the tensor core works about 1,600 (24 small MMAs, 60
 // to 80 cycles each whatever their N) and the row warps about 2,200 (scores from tensor memory
 // 190, maximum and its exchange 350 to 500, 64 exponentials a thread with P 1,100, P's store 270);
 // the rest is what each waits for the other.  Eight row warps instead of sixteen took 909 us (of

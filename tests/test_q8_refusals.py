@@ -105,6 +105,7 @@ def test_chunk_refuses():
     assert chunk(scale=0.0) == inv and chunk(scale=float("nan")) == inv
     assert chunk(cd=desc(nb=1 << 24)) == uns  # 2^31 rows per pool
     assert chunk(cd=desc(d=128)) == uns
+    assert chunk(seqs=1 << 26, tokens=1 << 20, mq=1 << 20) == uns  # work units past 2^31
 
 
 def test_copy_refuses():
