@@ -134,6 +134,11 @@ def test_decode_uneven_batches(hq, hkv, lens):
         close(st.decode(workspace=ws), ref, tol, "planned longer")
 
 
+def test_decode_most_sequences():
+    lens = np.random.default_rng(9).integers(0, 50, size=4096)
+    check_decode(wl.make_workload("most", lens, np.zeros(4096, int), seed=9), 1, 4)
+
+
 def test_decode_long_contexts():
     check_decode(wl.make_workload("long", [20000, 3, 33333, 8191], [1, 1, 1, 1], seed=7), 4, 16)
 
