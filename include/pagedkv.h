@@ -425,7 +425,8 @@ size_t pa_decode_q8_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32
  * the scales are read as early as the block tables.  The scales of blocks in use may be any
  * non-negative finite floats, not only powers of two.  The codes 0x7f and 0xff, which
  * pa_rope_append_q8 never stores, are not numbers: rows that see one are undefined.  The sums
- * are fp32: context length times largest magnitude of a value has to stay below 2^127.  Slots past
+ * are fp32: context length times largest magnitude of a value has to stay below 2^127, as has scale
+ * times largest |q| times largest key scale; outputs below 2^-126 may vanish.  Slots past
  * a context, and scales of blocks without a token in use, may hold anything.  key_cache,
  * value_cache: e4m3; key_scale, value_scale: 4-byte aligned floats; fewer than 2^31 (block,
  * head) tiles per pool. */

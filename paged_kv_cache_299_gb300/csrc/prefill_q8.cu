@@ -183,6 +183,13 @@ __device__ __forceinline__ void codes4_to_bf2x2(uint32_t w, uint32_t& lo, uint32
   hi = (b & 0x80008000u) | ((b >> 4) & 0x07f007f0u);
 }
 
+// f of a scale 2^e f, 1 <= f < 2, below the normal floats too; 1 for a scale of 0.
+__device__ __forceinline__ float significand(float s) {
+  const uint32_t b = __float_as_uint(s);
+  const int down = max(__clz(b) - 8, 0);  // places that a subnormal's first bit lies below the others'
+  return __uint_as_float(((b << down) & 0x7fffffu) | 0x3f800000u);
+}
+
 // 2^e as a bf16 pair, -126 <= e <= 127.
 __device__ __forceinline__ uint32_t bf2_power(int e) {
   return static_cast<uint32_t>(e + 127) * 0x00800080u;
@@ -441,7 +448,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q,
           lds_f32x4(cs, f);
 #pragma unroll
           for (int b = 0; b < kBlocksPerTile / 2; ++b)
-            f[b] = fmaxf(f[b] * q_factor, 1.17549435e-38f);  // not 0: -inf (hidden) * 0 is a NaN
+            f[b] = fmaxf(f[b] * q_factor, 1.17549435e-38f);  // (a hidden key's -inf * 0 is a NaN)
           const float mt = fmaxf(max3f(bm[0] * f[0], bm[1] * f[1], bm[2] * f[2]), bm[3] * f[3]);
           int gone;
           const float theirs = exchange(c & 1, mt, gone);
@@ -562,11 +569,14 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q,
           uint32_t my_m = 0u;  // lane b: 2^(120 + e) of block b's value scale, a bf16 pair
           int my_high = 0;     // e where 120 + e is beyond bf16: then my_m is 2^120
           if (lane < kMyBlocks) {
-            const int e = static_cast<int>((__float_as_uint(
-                              raw_scale[st * 2 * kBlocksPerTile + kBlocksPerTile + kMyBlocks * cw + lane]) >> 23) & 0xffu) - 127;
-            if (e > -127) {  // else zero (or too small to matter)
+            const uint32_t bits = __float_as_uint(
+                raw_scale[st * 2 * kBlocksPerTile + kBlocksPerTile + kMyBlocks * cw + lane]) & 0x7fffffffu;
+            const int e = static_cast<int>(bits >> 23) - 127;
+            if (e > -127) {
               my_high = e > 7 ? min(e, 127) : 0;
               my_m = bf2_power(e > 7 ? 120 : 120 + e);
+            } else if (bits != 0u) {  // below the normal floats: e = -118 - clz
+              my_m = bf2_power(2 - __clz(bits));
             }
           }
           const bool any_high = __any_sync(0xffffffffu, my_high != 0);
@@ -626,12 +636,9 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q,
             const int blk = kMyBlocks * cw + lane;
             const float* rs = raw_scale + st * 2 * kBlocksPerTile + blk;
             const bool needed = j * kBlocksPerTile + blk < cur.blocks_needed;
-            const float ks = needed ? fmaxf(rs[0], 1.17549435e-38f) : 1.f;
-            const uint32_t bits = needed ? __float_as_uint(rs[kBlocksPerTile]) : 0u;
-            // 1.f of the value scale, 1 for a scale of zero (or too small to matter)
-            const float f = (bits & 0x7f800000u) ? __uint_as_float((bits & 0x7fffffu) | 0x3f800000u) : 1.f;
+            const float f = significand(needed ? rs[kBlocksPerTile] : 1.f);  // of the value scale
             float* cs = consts + slot * kConsts + blk;
-            cs[0] = ks;
+            cs[0] = needed ? rs[0] : 1.f;
             float lf = 0.f, fi = 1.f;
             if (f != 1.f) {
               lf = __log2f(f);

@@ -1,0 +1,44 @@
+"""Ends of the 8-bit calls' contracts: scales of zero and below the normal floats."""
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_cache_299_gb300 import workloads as wl
+from _q8 import attend, dequantise
+from test_gpu_q8_attention import State, close
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- scales ---------------------------------------------------------------------------------
+@pytest.mark.parametrize("hq", [8, 4, 2])
+@pytest.mark.parametrize("q_exp,key_scales,value_scales", [
+    (118, [0.0], [1.0]),                                              # every score is zero
+    (112, [0.0, 2.0 ** -126, 1.37 * 2.0 ** -127, 2.0 ** -121], [1.0, 0.7]),
+    (116, [2.0 ** -140, 2.0 ** -149, 0.0, 1.6 * 2.0 ** -131], [0.3]),
+    (0, [0.05], [1.37 * 2.0 ** -127, 2.0 ** -128, 0.0, 1.9 * 2.0 ** -129]),
+    (0, [0.05], [2.0 ** -126, 1.6 * 2.0 ** -126, 1.99 * 2.0 ** -127])])
+def test_scales_of_zero_and_below_the_normal_floats(hq, q_exp, key_scales, value_scales):
+    """Any non-negative finite scale stands for itself, in long chunks, chunks of few rows and
+    decode rows alike; block b of the pool has the b-th of the listed scales, in turn."""
+    w = wl.make_workload("far", [0, 40, 300, 7], [1, 130, 33, 16], num_prefill=4, seed=17, pool_slack=0.5)
+    st = State(w, 2, hq, rows=180, spread=0.0)
+    st.q = (st.q.double() * 2.0 ** q_exp).to(torch.bfloat16)
+    k, v, ks, vs = (x.cpu() for x in st.dev)
+    for scales, values in ((ks, key_scales), (vs, value_scales)):
+        live = ~torch.isnan(scales)
+        turn = torch.tensor(values).float()[torch.arange(len(scales)) % len(values)]
+        scales[:] = torch.where(live, turn[:, None].expand_as(scales), scales)
+    st.dev = [x.cuda() for x in (k, v, ks, vs)]
+    st.k64, st.v64 = dequantise(k, ks), dequantise(v, vs)
+    ref, tol = attend(st.q, st.k64, st.v64, w.block_tables, w.context_lens, st.scale, w.new_lens)
+    tol = tol + 2.0 ** -126  # (what falls below the normal floats may vanish)
+    got = st.chunk()
+    assert st.ok()
+    close(got, ref, tol, "chunk")
+    last = torch.tensor(np.cumsum(w.new_lens) - 1)
+    st.q = st.q[last]
+    close(st.decode(), ref[last], tol[last], "decode")
+    st.w = wl.Workload("rows", w.context_lens - 1, np.ones(4, np.int32), 4, w.num_blocks, w.block_tables, 0)
+    close(st.chunk(), ref[last], tol[last], "few rows")
+    assert st.ok()
