@@ -411,10 +411,11 @@ pa_status pa_rope_append_q8(const void* q, int64_t q_stride, void* q_out, int64_
                             pa_cache_desc cd, int32_t* device_status, pa_stream_t stream);
 
 /* Bytes of device workspace pa_decode_q8 needs for these sizes on the current device (0 when
- * the sizes are invalid).  The rules of pa_decode_workspace_size hold: zero-fill it before its
- * first use and before a call whose num_seqs or num_kv_heads differ from those of the
- * previous call on it; calls that can overlap on the GPU (captured graphs that share it
- * included) need buffers of their own. */
+ * the sizes are invalid).  They depend on num_q_heads / num_kv_heads alone, and the buffer holds its
+ * counters in the same place for every call: zero-fill it once, before its first use, and calls of
+ * any sizes may follow one another on it (a buffer that pa_decode has used is zero-filled anew).
+ * Every call whose kernel runs to the end leaves the counters at zero.  Calls that can overlap on
+ * the GPU (captured graphs that share it included) need buffers of their own. */
 size_t pa_decode_q8_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t num_q_heads,
                                    int32_t max_context_len);
 

@@ -334,7 +334,8 @@ __device__ __forceinline__ void publish_piece(const KParams& p, const Meeting& m
         if (last) *count = 0;
       }
     } else {
-      int32_t* count = &p.seg_count[s * p.num_kv_heads + g];
+      // by the segment's first CTA: only one segment goes on past a CTA's last run
+      int32_t* count = &p.seg_count[m.c_first / kWarps];
       __threadfence();
       __syncwarp();
       if (lane == 0) {
@@ -799,7 +800,7 @@ cudaError_t launch(const AttendQ8Args& a, const DecodePlan& plan, void* workspac
   p.chunk = 0;
   p.tile_bound = plan.tile_bound;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.seg_count = reinterpret_cast<int32_t*>(ws + plan.ws_count_offset);
+  p.seg_count = reinterpret_cast<int32_t*>(ws + plan.ws_count_offset);  // [CTAs]
   p.partials = reinterpret_cast<float*>(ws + plan.ws_meta_bytes);
   p.status = a.status;
   const Q8Params s = {a.key_scale, a.value_scale};
@@ -845,9 +846,10 @@ cudaError_t plan_decode_q8(int32_t num_seqs, int32_t num_kv_heads, int32_t num_q
   plan->fused_merge = true;
   plan->merge_split_heads = false;
   plan->prefetch_ok = false;
-  plan->ws_count_offset = (16 + sizeof(int32_t) * (num_seqs + 1) + 255) / 256 * 256;
-  plan->ws_meta_bytes = plan->ws_count_offset +
-                        (sizeof(int32_t) * num_seqs * num_kv_heads + 255) / 256 * 256;
+  // A counter per CTA, then the records: neither place nor size depends on the call's sizes, so the
+  // counters that every call leaves at zero are the next one's, whatever batch that serves.
+  plan->ws_count_offset = 0;
+  plan->ws_meta_bytes = (sizeof(int32_t) * sms + 255) / 256 * 256;
   // sized for the whole device, so that any SM budget fits
   const int64_t runs_full = runs > static_cast<int64_t>(sms) * kWarps
                                 ? runs : static_cast<int64_t>(sms) * kWarps;

@@ -1,8 +1,11 @@
-"""Ends of the 8-bit calls' contracts: scales of zero and below the normal floats."""
+"""Ends of the 8-bit calls' contracts: scales of zero and below the normal floats, and one workspace
+under batches of every size."""
 import numpy as np
 import pytest
 import torch
 
+from paged_kv_cache_299_gb300 import binding as pa
+from paged_kv_cache_299_gb300 import graphs
 from paged_kv_cache_299_gb300 import workloads as wl
 from _q8 import attend, dequantise
 from test_gpu_q8_attention import State, close
@@ -42,3 +45,33 @@ def test_scales_of_zero_and_below_the_normal_floats(hq, q_exp, key_scales, value
     st.w = wl.Workload("rows", w.context_lens - 1, np.ones(4, np.int32), 4, w.num_blocks, w.block_tables, 0)
     close(st.chunk(), ref[last], tol[last], "few rows")
     assert st.ok()
+
+
+# ---- one workspace --------------------------------------------------------------------------
+def test_one_workspace_serves_batches_of_every_size():
+    """A program's one buffer, zeroed once, under batches that come and go: the counters of one call
+    never lie where another leaves its partials."""
+    ws = torch.zeros(16 << 20, dtype=torch.uint8, device="cuda")
+    states = []
+    for i, (hq, hkv, lens) in enumerate([(32, 8, [3000] * 5), (4, 1, [9000, 20]), (8, 8, [700] * 60), (32, 8, [40000]),
+                                         (2, 1, [500] * 300), (32, 8, [2000, 1, 0] * 40), (16, 8, [6000] * 9)]):
+        w = wl.make_workload("batch", lens, np.zeros(len(lens), int), seed=i, pool_slack=0.1)
+        st = State(w, hkv, hq, seed=i)
+        st.max_ctx = 65536
+        states.append((st, st.decode()))
+        need = pa.pa_decode_q8_workspace_size(len(lens), hkv, hq, 65536)
+        assert need <= ws.numel()
+        assert need == pa.pa_decode_q8_workspace_size(1, 1, hq // hkv, 1)  # nor does its size
+    order = np.random.default_rng(5).integers(0, len(states), size=40)
+    for i in order:
+        st, want = states[i]
+        assert torch.equal(st.decode(workspace=ws), want), f"batch {i}"
+    st, want = states[0]
+    q, out = st.q.cuda(), torch.empty_like(want)
+    graph = graphs.StepGraph(lambda: pa.pa_decode_q8(out, q, *st.dev, st.bt, st.ctx, st.scale, st.max_ctx, workspace=ws))
+    for i in order[:10]:
+        assert torch.equal(states[i][0].decode(workspace=ws), states[i][1])
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, want)
+    assert all(st.ok() for st, _ in states)
