@@ -422,7 +422,7 @@ size_t pa_decode_q8_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32
 /* pa_decode over the 8-bit pools:
  *   out[s][h][:] = sum_j softmax_j(scale * q[s][h] . K_s[j]) V_s[j],   K = code * key_scale,
  * with the arguments, limits, launch flags and errors of pa_decode (without partition_tokens;
- * contexts above max_context_len are reported and undefined).  With PA_LAUNCH_OVERLAP_PREVIOUS
+ * every context above max_context_len is reported).  With PA_LAUNCH_OVERLAP_PREVIOUS
  * the scales are read as early as the block tables.  The scales of blocks in use may be any
  * non-negative finite floats, not only powers of two.  The codes 0x7f and 0xff, which
  * pa_rope_append_q8 never stores, are not numbers: rows that see one are undefined.  The sums

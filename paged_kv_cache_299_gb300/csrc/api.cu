@@ -594,6 +594,7 @@ pa_status pa_decode_q8(void* out, const void* q, const void* key_cache, const vo
   a.query_start_loc = nullptr;
   a.num_query_tokens = num_seqs;
   a.max_query_len = 1;
+  a.max_context_len = max_context_len;
   a.key_cache = key_cache;
   a.value_cache = value_cache;
   a.key_scale = key_scale;
@@ -657,6 +658,7 @@ pa_status pa_prefill_chunk_q8(void* out, const void* q, const int32_t* query_sta
   a.query_start_loc = query_start_loc;
   a.num_query_tokens = num_query_tokens;
   a.max_query_len = max_query_len;
+  a.max_context_len = 0;
   a.key_cache = key_cache;
   a.value_cache = value_cache;
   a.key_scale = key_scale;

@@ -69,6 +69,7 @@ struct AttendQ8Args {
   const int32_t* query_start_loc;
   int32_t num_query_tokens;
   int32_t max_query_len;
+  int32_t max_context_len;  // the decode's alone
   const void* key_cache;
   const void* value_cache;
   const float* key_scale;

@@ -1,5 +1,5 @@
-"""Ends of the 8-bit calls' contracts: scales of zero and below the normal floats, and one workspace
-under batches of every size."""
+"""Ends of the 8-bit calls' contracts: scales of zero and below the normal floats, bounds that the
+caller states too small, one workspace under batches of every size."""
 import numpy as np
 import pytest
 import torch
@@ -45,6 +45,26 @@ def test_scales_of_zero_and_below_the_normal_floats(hq, q_exp, key_scales, value
     st.w = wl.Workload("rows", w.context_lens - 1, np.ones(4, np.int32), 4, w.num_blocks, w.block_tables, 0)
     close(st.chunk(), ref[last], tol[last], "few rows")
     assert st.ok()
+
+
+# ---- bounds that the caller states ----------------------------------------------------------
+def test_decode_reports_a_context_above_its_bound():
+    """One context above max_context_len among many far below it, in the same block as the
+    bound or far past it; every row is right all the same."""
+    lens = [20] * 20 + [500] + [100] * 3 + [0]
+    w = wl.make_workload("bound", lens, np.zeros(len(lens), int), seed=2, pool_slack=0.3)
+    st = State(w, 2, 8)
+    ref, tol = attend(st.q, st.k64, st.v64, w.block_tables, w.context_lens, st.scale)
+    for bound, told in ((100, True), (499, True), (500, False), (10 ** 6, False)):
+        st.max_ctx = bound
+        st.status.zero_()
+        close(st.decode(), ref, tol, f"bound {bound}")
+        assert int(st.status.item()) == (pa.DEVFLAG_BAD_CONTEXT if told else 0), bound
+    short = wl.make_workload("short", [300, 0], [0, 0], seed=3, pool_slack=0.3)
+    st = State(short, 8, 32)
+    st.max_ctx = 299  # the same number of blocks
+    st.decode()
+    assert int(st.status.item()) == pa.DEVFLAG_BAD_CONTEXT
 
 
 # ---- one workspace --------------------------------------------------------------------------
