@@ -441,9 +441,9 @@ pa_status pa_decode_q8(void* out, const void* q, const void* key_cache, const vo
 
 /* pa_prefill_chunk over the 8-bit pools: causal chunks of query rows, with that call's
  * arguments and errors, for num_q_heads / num_kv_heads in {1, 2, 4}.  Rows of q and out at or
- * past query_start_loc[num_seqs] are left alone.  Calls whose max_query_len makes at most 32 rows
- * per K/V head (verify steps) run on a kernel of their own, which reports a chunk longer than
- * max_query_len (PA_DEVFLAG_BAD_CONTEXT) and skips it.  num_seqs x Hkv x
+ * past query_start_loc[num_seqs] are left alone, and so are those of a chunk longer than
+ * max_query_len, which is reported (PA_DEVFLAG_BAD_CONTEXT).  Calls whose max_query_len makes at
+ * most 32 rows per K/V head (verify steps) run on a kernel of their own.  num_seqs x Hkv x
  * ceil(max_query_len x group / 256) must be below 2^31 (group = num_q_heads / num_kv_heads). */
 pa_status pa_prefill_chunk_q8(void* out, const void* q, const int32_t* query_start_loc,
                               int32_t num_query_tokens, int32_t max_query_len,

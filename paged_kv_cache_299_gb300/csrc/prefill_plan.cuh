@@ -30,6 +30,7 @@ struct PParams {
   float qk_scale;  // scale * log2(e)
   int32_t* status;
   int32_t num_query_tokens;
+  int32_t max_query_len;  // 8-bit kernel: longer chunks are reported and skipped
   int32_t num_seqs;
   int32_t q_tiles;  // query tiles of the longest chunk: ceil(max_query_len / 32)
   int32_t skip_single;  // 1: sequences with exactly one query row are served elsewhere
@@ -52,15 +53,16 @@ struct Unit {
 };
 
 // Whether sequence s has query rows to serve, and its rows / context.  Sequences with no rows
-// are skipped silently; rows outside q / out or a context shorter than the chunk or longer
-// than its block-table row are reported (when `report`) and skipped.
+// are skipped silently; rows outside q / out, more of them than max_query_len (BOUNDED), or a context
+// shorter than the chunk or longer than its block-table row are reported (when `report`) and skipped.
+template <bool BOUNDED>
 __device__ __forceinline__ bool sequence_ok(const PParams& p, int s, int* q0, int* q_len, int* L,
                                             bool report) {
   *q0 = p.query_start_loc[s];
   *q_len = p.query_start_loc[s + 1] - *q0;
   if (*q_len <= 0) return false;
   *L = p.context_lens[s];
-  if (*q0 < 0 || *q0 + *q_len > p.num_query_tokens || *L < *q_len ||
+  if (*q0 < 0 || *q0 + *q_len > p.num_query_tokens || (BOUNDED && *q_len > p.max_query_len) || *L < *q_len ||
       static_cast<int64_t>(*L) > static_cast<int64_t>(p.max_blocks_per_seq) * kBlockSize) {
     if (report) flag_error(p.status, PA_DEVFLAG_BAD_CONTEXT);
     return false;
@@ -98,6 +100,8 @@ struct Schedule {
   const int32_t* unit_L = nullptr;
 };
 
+// KEPT: the 8-bit kernel's form, from what the plan kept of the sequences, chunks bounded by
+// max_query_len (which the plan has reported by then).
 // LISTED: the batch is known to fit the list, and the code of the grid order is left out.
 template <int TOKENS, int KEYS, bool KEPT = false, bool LISTED = false>
 __device__ __forceinline__ bool next_unit(const PParams& p, const Schedule& sc, int& k, Unit& u) {
@@ -112,7 +116,7 @@ __device__ __forceinline__ bool next_unit(const PParams& p, const Schedule& sc, 
       u.q_len = sc.unit_len[k];
       u.L = sc.unit_L[k];
     } else {
-      sequence_ok(p, u.s, &u.q0, &u.q_len, &u.L, false);
+      sequence_ok<KEPT>(p, u.s, &u.q0, &u.q_len, &u.L, false);
     }
     ++k;
     fill_unit<TOKENS, KEYS>(u);
@@ -130,8 +134,8 @@ __device__ __forceinline__ bool next_unit(const PParams& p, const Schedule& sc, 
     u.tile = p.q_tiles - 1 - static_cast<int>(x / per_tile);
     u.g = static_cast<int>(rem / p.num_seqs);
     u.s = static_cast<int>(rem % p.num_seqs);
-    if (!sequence_ok(p, u.s, &u.q0, &u.q_len, &u.L, u.tile == 0 && u.g == 0)) continue;
-    if (u.tile * TOKENS >= u.q_len || (p.skip_single && u.q_len == 1)) continue;
+    if (!sequence_ok<false>(p, u.s, &u.q0, &u.q_len, &u.L, u.tile == 0 && u.g == 0)) continue;
+    if (u.tile * TOKENS >= u.q_len || (KEPT && u.q_len > p.max_query_len) || (p.skip_single && u.q_len == 1)) continue;
     fill_unit<TOKENS, KEYS>(u);
     return true;
   }
@@ -189,7 +193,7 @@ __device__ int plan_units(const PParams& p, uint8_t* scratch, int* red, int32_t*
   for (int s0 = 0; s0 < p.num_seqs; s0 += THREADS) {
     const int s = s0 + tid;
     int q0 = 0, q_len = 0, L = 0, tiles = 0;
-    if (s < p.num_seqs && sequence_ok(p, s, &q0, &q_len, &L, blockIdx.x == 0) &&
+    if (s < p.num_seqs && sequence_ok<(RANK_PAIRS > 0)>(p, s, &q0, &q_len, &L, blockIdx.x == 0) &&
         !(p.skip_single && q_len == 1))
       tiles = (q_len + TOKENS - 1) / TOKENS;
     int total;
@@ -291,7 +295,7 @@ __device__ int plan_units(const PParams& p, uint8_t* scratch, int* red, int32_t*
     const int pr = sorted[pos / p.num_kv_heads];
     unit_s[k] = pair_s[pr];
     unit_tg[k] = pair_t[pr] * 64 + pos % p.num_kv_heads;
-    if (unit_q0 != nullptr) sequence_ok(p, pair_s[pr], &unit_q0[k], &unit_len[k], &unit_L[k], false);
+    if (unit_q0 != nullptr) sequence_ok<(RANK_PAIRS > 0)>(p, pair_s[pr], &unit_q0[k], &unit_len[k], &unit_L[k], false);
   }
   return mine;
 }

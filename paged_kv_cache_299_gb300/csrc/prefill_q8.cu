@@ -947,6 +947,7 @@ cudaError_t launch(const AttendQ8Args& a, cudaStream_t stream) {
   p.qk_scale = a.scale * 1.4426950408889634f;
   p.status = a.status;
   p.num_query_tokens = a.num_query_tokens;
+  p.max_query_len = a.max_query_len;
   p.num_seqs = a.num_seqs;
   constexpr int kUnitTokens = 2 * kTileM / GROUP;
   p.q_tiles = (a.max_query_len + kUnitTokens - 1) / kUnitTokens;

@@ -67,6 +67,27 @@ def test_decode_reports_a_context_above_its_bound():
     assert int(st.status.item()) == pa.DEVFLAG_BAD_CONTEXT
 
 
+@pytest.mark.parametrize("hq,hkv,bound,lens", [
+    (8, 2, 20, [40, 20, 13]),                             # listed units
+    (2, 2, 64, [65, 64, 1]),
+    (4, 1, 64, [70] + [3] * 2100),                        # units in grid order: rows past the bound
+    (4, 1, 11, [12, 11, 64] + [3] * 2100)])
+def test_chunk_reports_more_rows_than_its_bound(hq, hkv, bound, lens):
+    """A chunk longer than max_query_len is reported and left alone, whatever form the call takes."""
+    lens = np.array(lens)
+    w = wl.make_workload("longer", np.full(len(lens), 5), lens, num_prefill=len(lens), seed=4, pool_slack=0.1)
+    st = State(w, hkv, hq, rows=int(lens.sum()))
+    ref, tol = attend(st.q, st.k64, st.v64, w.block_tables, w.context_lens, st.scale, w.new_lens)
+    got = st.chunk(bound)
+    assert int(st.status.item()) == pa.DEVFLAG_BAD_CONTEXT
+    over = torch.from_numpy(np.repeat(lens > bound, lens))
+    assert bool(torch.isnan(got[over.cuda()]).all())  # left as they were
+    close(got[~over.cuda()], ref[~over], tol[~over], "the others")
+    st.status.zero_()
+    close(st.chunk(), ref, tol, "all")
+    assert st.ok()
+
+
 # ---- one workspace --------------------------------------------------------------------------
 def test_one_workspace_serves_batches_of_every_size():
     """A program's one buffer, zeroed once, under batches that come and go: the counters of one call
