@@ -65,7 +65,6 @@ constexpr int kSegmentUnits = 2;
 constexpr int kOwnCtaSlack = 5;
 constexpr float kPShift = 7.f;                // log2 of the factor on p
 constexpr float kVFactor = 1.f / 32768.f;     // 2^-(kPShift + 8): on the value scales, and on l
-constexpr int kQExp = 13;                     // exponent of a row's largest f16 query element
 static_assert(kStages <= kWindow, "a window's scales are loaded a ring's length ahead");
 
 struct Q8Params {
@@ -101,8 +100,8 @@ __device__ __forceinline__ void attend_pair(const uint8_t* ta, const uint8_t* tb
                                             int valid, const float (&xs)[2], const float (&vs)[2],
                                             const uint32_t (&qa0)[4], const uint32_t (&qa2)[4],
                                             float& m, float& l, float2 (&o)[8]) {
-  const int t0 = q8_token_of(2 * q, 0);
-  const int k_off = q8_token_of(r, 0) * kQ8RowBytes + 16 * q;
+  const int t0 = q8_token_of(2 * q);
+  const int k_off = q8_token_of(r) * kQ8RowBytes + 16 * q;
   const int v_off = kQ8TileBytes + t0 * kQ8RowBytes + 8 * r;
   uint2 v[2][4];  // tokens t0, t0 + 2, t0 + 8, t0 + 10 of each tile, codes of dims 8r .. 8r + 7
   float x[2][4];
@@ -631,11 +630,9 @@ paged_decode_q8_kernel(const __grid_constant__ KParams p, const Q8Params sp8) {
         big = max(big, max((w[i] << 16) & 0x7fff0000u, w[i] & 0x7fff0000u));
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-      int shift = 0;  // q * 2^shift
-      if (big != 0u && big < 0x7f800000u)
-        shift = min(126, kQExp + 127 - static_cast<int>(max(big >> 23, 1u)));
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
-      row_scale *= __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+      const int shift = query_shift(big);
+      const float up = power_of_two(shift);
+      row_scale *= power_of_two(-shift);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 a = bf16x2_to_float2(w[2 * j]), b = bf16x2_to_float2(w[2 * j + 1]);

@@ -102,10 +102,9 @@ struct Schedule {
 
 // KEPT: the 8-bit kernel's form, from what the plan kept of the sequences, chunks bounded by
 // max_query_len (which the plan has reported by then).
-// LISTED: the batch is known to fit the list, and the code of the grid order is left out.
-template <int TOKENS, int KEYS, bool KEPT = false, bool LISTED = false>
+template <int TOKENS, int KEYS, bool KEPT = false>
 __device__ __forceinline__ bool next_unit(const PParams& p, const Schedule& sc, int& k, Unit& u) {
-  if (LISTED || sc.n_units >= 0) {
+  if (sc.n_units >= 0) {
     if (k >= sc.n_units) return false;
     u.s = sc.unit_s[k];
     const int tg = sc.unit_tg[k];

@@ -90,7 +90,6 @@ constexpr uint32_t kOCol = 384;  // + 64 per half: fp32
 // when a score passes it: weights stay below 2, so the sums of p V keep the size of the values,
 // and a row rescales only when its maximum grows by more than 2^8.
 constexpr float kHeadroom = 8.0f;
-constexpr int kQExp = 13;  // exponent of a row's largest f16 query element
 // Register split (setmaxnreg): the row warps' threads and the others' share what the CTA was
 // launched with; the launcher checks that it suffices.
 constexpr int kRowRegs = 96;
@@ -161,10 +160,6 @@ __device__ __forceinline__ int half_tiles(const Unit& u, int half) {
   return (u.L - u.q_len + u.tok0 + half * HALF_TOKENS + n + kTileN - 1) / kTileN;
 }
 
-__device__ __forceinline__ uint32_t pack_half2(float x, float y) {
-  const __half2 h = __floats2half2_rn(x, y);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 __device__ __forceinline__ uint32_t pack_bf2(float x, float y) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -361,11 +356,9 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q,
         for (int i = 0; i < 4; ++i)
           big = max(big, max((y[i] << 16) & 0x7fff0000u, y[i] & 0x7fff0000u));
       }
-      int shift = 0;
-      if (big != 0u && big < 0x7f800000u)
-        shift = min(126, kQExp + 127 - static_cast<int>(max(big >> 23, 1u)));
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
-      q_factor_next = p.qk_scale * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+      const int shift = query_shift(big);
+      const float up = power_of_two(shift);
+      q_factor_next = p.qk_scale * power_of_two(-shift);
       named_barrier_sync(pair_bar, 64);  // both have read
       if (!__all_sync(0xffffffffu, abort_flag == 0)) return false;
 #pragma unroll
@@ -375,7 +368,7 @@ paged_chunk_q8_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 f = bf16x2_to_float2(x[i]);
-          y[i] = pack_half2(f.x * up, f.y * up);
+          y[i] = pack_half2_rn(f.x * up, f.y * up);
         }
         *reinterpret_cast<uint4*>(q + swz(r, c ^ (4 * part))) = make_uint4(y[0], y[1], y[2], y[3]);
       }

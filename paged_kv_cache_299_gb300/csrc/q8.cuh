@@ -14,13 +14,8 @@ constexpr int kQ8TileBytes = kHeadDim * kBlockSize;  // one (block, kv head) til
 constexpr float kCodeMax = 448.f;                    // largest e4m3 magnitude
 constexpr int kMinScaleExp = -126;                   // scales stay normal floats
 
-// Two codes (low byte first) -> two halves, exact (every e4m3 value is an f16 value).
-__device__ __forceinline__ uint32_t codes2_to_half2(uint16_t c) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
-  return h;
-}
-// The four codes of a word -> two half2 (bytes 0, 1 and bytes 2, 3).
+// The four codes of a word -> two half2 (bytes 0, 1 and bytes 2, 3), exact (every e4m3 value is an
+// f16 value).
 __device__ __forceinline__ void codes4_to_half2x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 l, h;\n\t"
       "mov.b32 {l, h}, %2;\n\t"
@@ -65,12 +60,25 @@ __device__ __forceinline__ uint32_t pack_half2_rn(float x, float y) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Token of column n (0..7) of score n-tile i.  Lane q of a quad owns columns 2q and 2q + 1, so
-// its tokens are t, t + 2, t + 8 and t + 10 with t = (q & 1) + 4 (q >> 1): their 64-byte rows
-// fall on both halves of the shared-memory banks, which leaves two wavefronts per 128 bytes
-// for the 8-byte V reads and the 16-byte K reads alike (the natural order leaves four and one).
-__device__ __forceinline__ int q8_token_of(int n, int i) {
-  return ((n >> 1) & 1) + 2 * (n & 1) + 4 * (n >> 2) + 8 * i;
+// A query row enters the products as f16 under a power of two, q 2^shift, that brings its largest
+// element to [2^13, 2^14): a bf16 significand fits, and elements down to 2^-27 of the largest keep
+// all their bits.  big: the largest magnitude's float bits (a row of zeros, or one with an infinity or
+// a NaN, stays as it is).
+__device__ __forceinline__ int query_shift(uint32_t big) {
+  return big != 0u && big < 0x7f800000u ? min(126, 13 + 127 - static_cast<int>(max(big >> 23, 1u))) : 0;
+}
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float power_of_two(int e) {
+  return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+}
+
+// Token of column n (0..7) of the first score n-tile; the second's are eight further.  Lane q of a
+// quad owns columns 2q and 2q + 1, so its tokens are t, t + 2, t + 8 and t + 10 with t = (q & 1) +
+// 4 (q >> 1): their 64-byte rows fall on both halves of the shared-memory banks, which leaves two
+// wavefronts per 128 bytes for the 8-byte V reads and the 16-byte K reads alike (the natural order
+// leaves four and one).
+__device__ __forceinline__ int q8_token_of(int n) {
+  return ((n >> 1) & 1) + 2 * (n & 1) + 4 * (n >> 2);
 }
 
 __device__ __forceinline__ bool scale_ok(float s) { return s > 0.f && s < INFINITY; }

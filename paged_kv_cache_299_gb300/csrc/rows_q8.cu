@@ -43,7 +43,6 @@ constexpr int kRecordFloats = kHeadDim + 4;  // o, maximum (log2 units), sum, pa
 constexpr float kRescaleThreshold = 8.f;     // as in the decode, like the factors below
 constexpr float kPShift = 7.f;
 constexpr float kVFactor = 1.f / 32768.f;
-constexpr int kQExp = 13;
 
 struct RowsParams {
   __nv_bfloat16* out;
@@ -129,12 +128,12 @@ __device__ __forceinline__ void attend_tiles(const uint8_t* const (&tiles)[T], i
                                              const float (&ks)[T], const float (&vs)[T],
                                              const int (&first)[T], int end, Rows<NT>& w) {
   constexpr int MT = (NT + 1) / 2;
-  const int t0 = q8_token_of(2 * q, 0);
+  const int t0 = q8_token_of(2 * q);
   uint2 v[T][4];  // tokens t0, t0 + 2, t0 + 8, t0 + 10
   float x[T][NT][4];
 #pragma unroll
   for (int t = 0; t < T; ++t) {
-    const uint8_t* kp = tiles[t] + q8_token_of(r, 0) * kQ8RowBytes + 16 * q;
+    const uint8_t* kp = tiles[t] + q8_token_of(r) * kQ8RowBytes + 16 * q;
     const uint8_t* vp = tiles[t] + kQ8TileBytes + t0 * kQ8RowBytes + 8 * r;
     const uint4 k0 = lds128(kp), k1 = lds128(kp + 8 * kQ8RowBytes);
 #pragma unroll
@@ -367,10 +366,8 @@ paged_rows_q8_kernel(const __grid_constant__ RowsParams p) {
     for (int i = 0; i < 8; ++i) big = max(big, max((x[i] << 16) & 0x7fff0000u, x[i] & 0x7fff0000u));
     big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
     big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-    int shift = 0;
-    if (big != 0u && big < 0x7f800000u)
-      shift = min(126, kQExp + 127 - static_cast<int>(max(big >> 23, 1u)));
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+    const int shift = query_shift(big);
+    const float up = power_of_two(shift);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 c = bf16x2_to_float2(x[2 * j]), d = bf16x2_to_float2(x[2 * j + 1]);
@@ -378,7 +375,7 @@ paged_rows_q8_kernel(const __grid_constant__ RowsParams p) {
       w.q[mt][j][2 + y] = nt < NT ? pack_half2_rn(d.x * up, d.y * up) : 0u;
     }
     if (nt < NT) {
-      w.factor[nt] = p.q_scale * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+      w.factor[nt] = p.q_scale * power_of_two(-shift);
       w.pos[nt] = L - q_len + row / p.group;
       w.m[nt] = -INFINITY;
       w.l[nt] = 0.f;
