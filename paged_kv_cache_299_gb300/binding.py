@@ -507,7 +507,7 @@ def _need_rows(t, name, dev, heads=None):
     heads = shape[1]
     if one != 1 or (row != 64 and heads > 1):
         raise ValueError(f"{name}: the head rows of a token must be contiguous")
-    return max(stride, heads * 64) if shape[0] <= 1 else stride
+    return heads * 64 if shape[0] <= 1 else stride
 
 
 def _need_q8(key_cache, value_cache, key_scale, value_scale, dev):

@@ -139,3 +139,13 @@ def test_binding_refuses_host_tensors():
     codes = torch.zeros(2, 8, 16, 64, dtype=torch.uint8).view(torch.float8_e4m3fn)
     with pytest.raises(ValueError):
         pa._need_q8(codes, codes, torch.ones(2, 8), torch.ones(2, 8), 0)
+
+
+@pytest.mark.parametrize("stride", [1, 1001, 512, 4096, 20000])
+def test_one_token_may_have_any_stride(stride):
+    """The stride of a single token is never stepped over, and torch leaves it at anything; host
+    tensors have device -1, so this much of the check runs without a GPU."""
+    one = torch.empty(30000, dtype=torch.bfloat16).as_strided((1, 8, 64), (stride, 64, 1))
+    assert pa._need_rows(one, "key", -1, 8) == 512
+    two = torch.empty(30000, dtype=torch.bfloat16).as_strided((2, 8, 64), (stride, 64, 1))
+    assert pa._need_rows(two, "key", -1, 8) == stride  # (the library refuses the bad ones)
