@@ -392,14 +392,15 @@ pa_status pa_rope_append(const void* q, int64_t q_stride, void* q_out, int64_t q
  * and 2^e the smallest power of two, e >= -126, with A <= 448 * 2^e, the scale becomes 2^e
  * where the call writes the block's first token, and max(old scale, 2^e) elsewhere.  Codes of
  * the block's earlier tokens are rescaled when the scale grows (exactly, but for codes that
- * turn subnormal); new ones are value / scale, rounded to nearest even once from fp32.  So a
- * chunked append and a token-by-token one of the same tokens may round small values
- * differently.  A NaN is stored as 0 and an infinity as the largest code of its sign; both set
- * PA_DEVFLAG_NONFINITE.  A block with earlier tokens whose scale in a pool is not a positive
- * finite number sets PA_DEVFLAG_BAD_SCALE and is left as it is in that pool.  Blocks that two sequences of the
- * call append to must differ (pa_copy_blocks_q8 before writing to shared blocks).  The other
- * arguments, checks and no-ops are pa_rope_append's; a sequence with any position out of range
- * stores nothing. */
+ * turn subnormal); new ones are value / scale, rounded to nearest even once from fp32 (where an old
+ * scale that is no power of two stays, value times its fp32 reciprocal).  So a chunked append and a
+ * token-by-token one of the same tokens may round small values differently.  A NaN is stored as
+ * 0 and an infinity as the largest code of its sign; both set PA_DEVFLAG_NONFINITE.  A block with
+ * earlier tokens whose scale in a pool is not a positive finite number sets PA_DEVFLAG_BAD_SCALE
+ * and is left as it is in that pool.  Blocks that two sequences of the call append to must differ
+ * (pa_copy_blocks_q8 before writing to shared blocks).  The other arguments, checks and no-ops are
+ * pa_rope_append's; a sequence with any position out of range stores nothing (queries are rotated
+ * by their own positions alone, whatever becomes of the keys). */
 pa_status pa_rope_append_q8(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
                             int32_t num_q_heads, const void* key, int64_t key_stride,
                             const void* value, int64_t value_stride, const float* cos_sin,
@@ -442,9 +443,10 @@ pa_status pa_decode_q8(void* out, const void* q, const void* key_cache, const vo
 /* pa_prefill_chunk over the 8-bit pools: causal chunks of query rows, with that call's
  * arguments and errors, for num_q_heads / num_kv_heads in {1, 2, 4}.  Rows of q and out at or
  * past query_start_loc[num_seqs] are left alone, and so are those of a chunk longer than
- * max_query_len, which is reported (PA_DEVFLAG_BAD_CONTEXT).  Calls whose max_query_len makes at
- * most 32 rows per K/V head (verify steps) run on a kernel of their own.  num_seqs x Hkv x
- * ceil(max_query_len x group / 256) must be below 2^31 (group = num_q_heads / num_kv_heads). */
+ * max_query_len, which is reported (PA_DEVFLAG_BAD_CONTEXT); max_query_len == 0 is a no-op.  Calls
+ * whose max_query_len makes at most 32 rows per K/V head (verify steps) run on a kernel of their
+ * own.  num_seqs x Hkv x ceil(max_query_len x group / 256) must be below 2^31 (group = num_q_heads /
+ * num_kv_heads). */
 pa_status pa_prefill_chunk_q8(void* out, const void* q, const int32_t* query_start_loc,
                               int32_t num_query_tokens, int32_t max_query_len,
                               const void* key_cache, const void* value_cache,

@@ -36,6 +36,7 @@ struct KParams {
   float* partials;      // [runs][2][GROUP][kPartialFloats]
   int32_t* seg_count;   // [num_seqs * Hkv] pieces published per split segment (fused merge);
                         // zero between calls: the merging warp resets its counter
+                        // (8-bit decode: one per CTA, by a split segment's first)
   int32_t fused_merge;  // 1: the last warp to finish a split segment merges it in place
   int32_t prefetch_ok;  // 1: a warp may ask L2 for tiles past its ring before its wait
   const uint8_t* k_new;  // optional [num_seqs][Hkv][64] bf16: token at position L-1 to store

@@ -99,7 +99,7 @@ struct DecodePlan {
   bool fused_merge;          // split segments merged inside the attention kernel
   bool merge_split_heads;    // otherwise: the merge kernel takes one CTA per query head
   bool prefetch_ok;          // warps may ask L2 for tiles past their ring before the wait
-  size_t ws_count_offset;    // offset of the per-segment piece counters (must start zeroed)
+  size_t ws_count_offset;    // offset of the piece counters (must start zeroed)
   size_t ws_meta_bytes;      // offset of the partials inside the workspace
   size_t workspace_bytes;    // total workspace
 };

@@ -16,7 +16,7 @@
 // contexts 487-1022, 16.6 us against 22.4; 32 x 5 rows at 800 tokens 12.8 against 24.9, 256 x 5 at
 // 1000 92 against 152, 4 x 5 at 131072 160 (3.4 TB/s) against 946; 128 x 8 at 4000 181 against
 // 242.  Bound: by the latency of the chain score, exponential, product per tile, of which an SM
-// holds twelve (38 % of the issue slots and 33 % of DRAM busy at 4 x 131072 tokens); small batches
+// holds twelve (44 % of the issue slots and 41 % of DRAM busy at 4 x 131072 tokens); small batches
 // by start-up.  12 warps on one CTA, or 15 on three (the registers spill), were slower: 256 x 5 at
 // 1000 124 and 107 us.
 #include <math.h>
