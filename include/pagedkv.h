@@ -411,6 +411,36 @@ pa_status pa_rope_append_q8(const void* q, int64_t q_stride, void* q_out, int64_
                             void* value_cache, float* key_scale, float* value_scale,
                             pa_cache_desc cd, int32_t* device_status, pa_stream_t stream);
 
+/* The same two appends for tokens whose angles do not follow their slots: the nodes of a drafted tree
+ * (several at one depth), image and video patches with a time, a height and a width.  Slots are as
+ * above; the pair i of a token t turns by row positions[axis(i)][t] of cos_sin,
+ *   cos = cos_sin[positions[axis(i)][t]][i],  sin = cos_sin[positions[axis(i)][t]][32 + i].
+ *   positions  int32 [num_axes][num_tokens], 1 <= num_axes <= 4
+ *   pair_axes  two bits per pair: axis(i) = (pair_axes >> 2 i) & 3, below num_axes
+ * A position outside [0, max_positions), on any axis, sets PA_DEVFLAG_BAD_CONTEXT; its token is
+ * skipped, and pa_rope_append_at_q8 leaves every block such a token goes to as it is (the other tokens'
+ * queries are rotated all the same).  Slots are bounded by the block-table row alone.  cos_sin is
+ * required by both.  The pages describe no counterpart (their rotation is by the token's place). */
+pa_status pa_rope_append_at(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                            int32_t num_q_heads, const void* key, int64_t key_stride,
+                            const void* value, int64_t value_stride, const float* cos_sin,
+                            int32_t max_positions, int32_t interleaved, const int32_t* positions,
+                            int32_t num_axes, uint64_t pair_axes, const int32_t* block_tables,
+                            int32_t max_blocks_per_seq, const int32_t* context_lens,
+                            const int32_t* query_start_loc, int32_t num_seqs, int32_t num_tokens,
+                            void* key_cache, void* value_cache, pa_cache_desc cd,
+                            int32_t* device_status, pa_stream_t stream);
+pa_status pa_rope_append_at_q8(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                               int32_t num_q_heads, const void* key, int64_t key_stride,
+                               const void* value, int64_t value_stride, const float* cos_sin,
+                               int32_t max_positions, int32_t interleaved, const int32_t* positions,
+                               int32_t num_axes, uint64_t pair_axes, const int32_t* block_tables,
+                               int32_t max_blocks_per_seq, const int32_t* context_lens,
+                               const int32_t* query_start_loc, int32_t num_seqs, int32_t num_tokens,
+                               void* key_cache, void* value_cache, float* key_scale,
+                               float* value_scale, pa_cache_desc cd, int32_t* device_status,
+                               pa_stream_t stream);
+
 /* Bytes of device workspace pa_decode_q8 needs for these sizes on the current device (0 when
  * the sizes are invalid).  They depend on num_q_heads / num_kv_heads alone, and the buffer holds its
  * counters in the same place for every call: zero-fill it once, before its first use, and calls of
@@ -460,6 +490,87 @@ pa_status pa_prefill_chunk_q8(void* out, const void* q, const int32_t* query_sta
 pa_status pa_copy_blocks_q8(void* key_cache, void* value_cache, float* key_scale,
                             float* value_scale, pa_cache_desc cd, const int64_t* block_mapping,
                             int32_t num_pairs, int32_t* device_status, pa_stream_t stream);
+
+/* Bytes of device workspace the tree calls need on the current device (0 without one), the same
+ * for calls of any sizes.  Zero-fill the buffer once, before its first use; then calls of any sizes,
+ * over both kinds of pools, may follow one another on it.  Calls that can overlap on the GPU
+ * (captured graphs that share it included) need buffers of their own. */
+size_t pa_tree_workspace_size(void);
+
+/* Attention of drafted trees (the verification of speculative decoding, "vLLM"
+ * (blog.rlaisqls.com), section Speculative Decoding, for several continuations at once).  The last
+ * q_len tokens of a sequence, q_len = query_start_loc[s+1] - query_start_loc[s], are drafted nodes
+ * whose keys and values are stored already (pa_rope_append_at); the prefix is the P = context_lens[s] -
+ * q_len tokens before them.  Row i sees every key of the prefix, and drafted key j where bit j of its
+ * mask row is set:
+ *   out[i][h][:] = sum_j softmax_j(scale * q[i][h] . K_j) V_j  over the keys that row i sees,
+ * a row that sees none is 0.  What a row does not see (a drafted key or value that is no number, a slot
+ * past the context) never reaches it.
+ *   q, out           bf16 [num_query_tokens][num_q_heads][64], num_q_heads / num_kv_heads in {1, 2, 4}
+ *   tree_mask        int32 [num_query_tokens][mask_words]: bit j of a row is bit j % 32 of its word
+ *                    j / 32; bits from q_len on are not looked at.  A tree's row has the bits of the
+ *                    node itself and of its ancestors
+ *   mask_words       at least ceil(max_query_len / 32)
+ *   max_query_len    host bound of q_len, at most 1024; a longer sequence of rows sets
+ *                    PA_DEVFLAG_BAD_CONTEXT and is left alone, as is one with rows outside q or a context
+ *                    shorter than them or longer than its block-table row
+ *   workspace        pa_tree_workspace_size() bytes, 16-byte aligned
+ * A block id outside [0, num_blocks) sets PA_DEVFLAG_BAD_BLOCK; rows of that sequence are undefined.
+ * Rows of q and out outside query_start_loc[0] .. query_start_loc[num_seqs] - 1 are left alone.
+ * Results do not depend on the order in which CTAs run.  num_seqs == 0, num_query_tokens == 0 and
+ * max_query_len == 0 are no-ops. */
+pa_status pa_tree_attention(void* out, const void* q, const int32_t* tree_mask, int32_t mask_words,
+                            const int32_t* query_start_loc, int32_t num_query_tokens,
+                            int32_t max_query_len, const void* key_cache, const void* value_cache,
+                            pa_cache_desc cd, const int32_t* block_tables,
+                            int32_t max_blocks_per_seq, const int32_t* context_lens,
+                            int32_t num_seqs, int32_t num_q_heads, float scale, void* workspace,
+                            size_t workspace_bytes, int32_t* device_status, pa_stream_t stream);
+
+/* The same over the 8-bit pools, with pa_decode_q8's limits on scales, values and codes. */
+pa_status pa_tree_attention_q8(void* out, const void* q, const int32_t* tree_mask,
+                               int32_t mask_words, const int32_t* query_start_loc,
+                               int32_t num_query_tokens, int32_t max_query_len,
+                               const void* key_cache, const void* value_cache,
+                               const float* key_scale, const float* value_scale,
+                               pa_cache_desc cd, const int32_t* block_tables,
+                               int32_t max_blocks_per_seq, const int32_t* context_lens,
+                               int32_t num_seqs, int32_t num_q_heads, float scale,
+                               void* workspace, size_t workspace_bytes, int32_t* device_status,
+                               pa_stream_t stream);
+
+/* Compaction of kept tokens, in place (the accepted nodes of a drafted tree move behind their prefix
+ * and the rest is given up; a history is thinned out).  Of sequence s, with kept_s its entries
+ * kept[kept_start_loc[s]] .. kept[kept_start_loc[s+1] - 1], the token at position first[s] + kept_s[i]
+ * moves to position first[s] + i, keys and values of all heads; its context is first[s] + the number
+ * of entries from then on (the caller's to set).  Other slots keep what they hold.
+ *   kept            int32 [num_kept], rising within a sequence from 0 or more
+ *   kept_start_loc  int32 [num_seqs + 1]
+ *   first           int32 [num_seqs]: the prefix length, for a tree
+ *   max_kept        host bound of a sequence's number of entries
+ * A sequence with more than max_kept entries, entries outside kept or a negative first sets
+ * PA_DEVFLAG_BAD_CONTEXT and is left alone; an entry that does not rise, or lies past the block-table
+ * row, sets it and does not move (what the others' order was meant to protect may be lost); a bad
+ * block id sets PA_DEVFLAG_BAD_BLOCK and its tokens do not move.  Blocks in which a sequence's tokens
+ * move must be its own (pa_copy_blocks before writing to shared blocks); sequences that keep all they have
+ * move nothing.  num_seqs == 0, num_kept == 0 and max_kept == 0 are no-ops. */
+pa_status pa_compact_tokens(const int32_t* kept, const int32_t* kept_start_loc,
+                            const int32_t* first, int32_t num_kept, int32_t max_kept,
+                            void* key_cache, void* value_cache, pa_cache_desc cd,
+                            const int32_t* block_tables, int32_t max_blocks_per_seq,
+                            int32_t num_seqs, int32_t* device_status, pa_stream_t stream);
+
+/* The same in the 8-bit pools: the values code * scale go to their new blocks as pa_rope_append_q8
+ * would store them (also those whose slot stays the same).  A block whose first slot receives a token starts with the smallest scale that
+ * fits what moves into it; one with tokens before first[s] keeps its scale or grows it (and their codes
+ * are rescaled).  A block that a bad entry, block id or scale (negative, not finite; zero too where
+ * earlier tokens stay) takes part in is reported and left as it is. */
+pa_status pa_compact_tokens_q8(const int32_t* kept, const int32_t* kept_start_loc,
+                               const int32_t* first, int32_t num_kept, int32_t max_kept,
+                               void* key_cache, void* value_cache, float* key_scale,
+                               float* value_scale, pa_cache_desc cd, const int32_t* block_tables,
+                               int32_t max_blocks_per_seq, int32_t num_seqs,
+                               int32_t* device_status, pa_stream_t stream);
 
 /* Host-side block manager ("vLLM", PagedAttention and Continuous Batching): a pool of
  * num_blocks physical blocks of block_size tokens; each sequence owns a table of blocks,

@@ -63,7 +63,9 @@ EXPORTED = ("pa_compute_slot_mapping", "pa_reshape_and_cache", "pa_decode_worksp
             "pa_varlen_workspace_size", "pa_attention_varlen", "pa_stream_read",
             "pa_prefill_chunk_ex", "pa_attention_varlen_ex", "pa_rope_append",
             "pa_rope_append_q8", "pa_decode_q8_workspace_size", "pa_decode_q8",
-            "pa_prefill_chunk_q8", "pa_copy_blocks_q8")
+            "pa_prefill_chunk_q8", "pa_copy_blocks_q8", "pa_rope_append_at",
+            "pa_rope_append_at_q8", "pa_tree_workspace_size", "pa_tree_attention",
+            "pa_tree_attention_q8", "pa_compact_tokens", "pa_compact_tokens_q8")
 
 
 def library_path() -> str:
@@ -151,6 +153,25 @@ def load(path: str | None = None):
     lib.pa_prefill_chunk_q8.restype = st
     lib.pa_copy_blocks_q8.argtypes = [P, P, P, P, CacheDesc, P, i32, P, P]
     lib.pa_copy_blocks_q8.restype = st
+    u64 = ctypes.c_uint64
+    at = [P, i64, P, i64, i32, P, i64, P, i64, P, i32, i32, P, i32, u64, P, i32, P, P, i32, i32]
+    lib.pa_rope_append_at.argtypes = [*at, P, P, CacheDesc, P, P]
+    lib.pa_rope_append_at.restype = st
+    lib.pa_rope_append_at_q8.argtypes = [*at, P, P, P, P, CacheDesc, P, P]
+    lib.pa_rope_append_at_q8.restype = st
+    lib.pa_tree_workspace_size.argtypes = []
+    lib.pa_tree_workspace_size.restype = sz
+    lib.pa_tree_attention.argtypes = [P, P, P, i32, P, i32, i32, P, P, CacheDesc, P, i32, P, i32,
+                                      i32, f32, P, sz, P, P]
+    lib.pa_tree_attention.restype = st
+    lib.pa_tree_attention_q8.argtypes = [P, P, P, i32, P, i32, i32, P, P, P, P, CacheDesc, P, i32,
+                                         P, i32, i32, f32, P, sz, P, P]
+    lib.pa_tree_attention_q8.restype = st
+    lib.pa_compact_tokens.argtypes = [P, P, P, i32, i32, P, P, CacheDesc, P, i32, i32, P, P]
+    lib.pa_compact_tokens.restype = st
+    lib.pa_compact_tokens_q8.argtypes = [P, P, P, i32, i32, P, P, P, P, CacheDesc, P, i32, i32, P,
+                                         P]
+    lib.pa_compact_tokens_q8.restype = st
     lib.pa_selftest_wait_timeout.argtypes = [P, i32, P]
     lib.pa_selftest_wait_timeout.restype = st
     lib.pa_stream_read.argtypes = [P, sz, P, P]
@@ -685,6 +706,193 @@ def pa_copy_blocks_q8(key_cache, value_cache, key_scale, value_scale, block_mapp
                                             _status_ptr(device_status, dev), _current_stream(stream))
     if st:
         _check(st, "pa_copy_blocks_q8")
+
+
+_packed_axes = {}  # pair_axes as the call takes them, by the tuple
+
+
+def _pair_axes(pair_axes, num_axes):
+    """32 axis numbers (None: all pairs on axis 0) as two bits each."""
+    if pair_axes is None:
+        return 0
+    key = tuple(pair_axes)
+    packed = _packed_axes.get(key)
+    if packed is None:
+        if len(key) != 32 or not all(isinstance(a, int) and 0 <= a < 4 for a in key):
+            raise ValueError("pair_axes must be 32 axis numbers, one per rotation pair")
+        packed = _packed_axes[key] = sum(a << (2 * i) for i, a in enumerate(key))
+    if max(key) >= num_axes:
+        raise ValueError(f"pair_axes names axis {max(key)}, positions has {num_axes}")
+    return packed
+
+
+def _rope_append_at_args(args, cos_sin, positions, pair_axes, dev):
+    """_rope_append_args' tuple with the positions in their place."""
+    if cos_sin is None:
+        raise ValueError("cos_sin is required")
+    pos = _check_tensor(positions, "positions", torch.int32, 2, dev)
+    axes, tokens = positions.shape
+    if not 1 <= axes <= 4 or tokens != args[-1]:
+        raise ValueError(f"positions must be [1 to 4 axes, {args[-1]} tokens], got {axes, tokens}")
+    return (*args[:12], pos, axes, _pair_axes(pair_axes, axes), *args[12:])
+
+
+def pa_rope_append_at(q, key, value, cos_sin, positions, key_cache, value_cache, block_tables,
+                      context_lens, query_start_loc=None, pair_axes=None, q_out=None,
+                      interleaved=False, device_status=None, stream=None):
+    """pa_rope_append with the tokens' own positions, int32 [axes, T] with one to four axes; the slots
+    follow the contexts as before.  pair_axes: the axis of each of the 32 rotation pairs (None:
+    axis 0); see include/pagedkv.h."""
+    dev = _current_device()
+    kc = _check_tensor(key_cache, "key_cache", torch.bfloat16, 4, dev)
+    vc = _check_tensor(value_cache, "value_cache", torch.bfloat16, 4, dev)
+    shape = key_cache.shape
+    if value_cache.shape != shape:
+        raise ValueError("cache shapes differ")
+    q_out, args = _rope_append_args(q, key, value, cos_sin, shape[1], block_tables, context_lens,
+                                    query_start_loc, q_out, interleaved, stream, dev)
+    args = _rope_append_at_args(args, cos_sin, positions, pair_axes, dev)
+    st = (_lib or load()).pa_rope_append_at(*args, kc, vc, _kept_desc(shape),
+                                            _status_ptr(device_status, dev), _current_stream(stream))
+    if st:
+        _check(st, "pa_rope_append_at")
+    return q_out
+
+
+def pa_rope_append_at_q8(q, key, value, cos_sin, positions, key_cache, value_cache, key_scale,
+                         value_scale, block_tables, context_lens, query_start_loc=None,
+                         pair_axes=None, q_out=None, interleaved=False, device_status=None,
+                         stream=None):
+    """pa_rope_append_at into the 8-bit pools."""
+    dev = _current_device()
+    kc, vc, ks, vs, shape = _need_q8(key_cache, value_cache, key_scale, value_scale, dev)
+    q_out, args = _rope_append_args(q, key, value, cos_sin, shape[1], block_tables, context_lens,
+                                    query_start_loc, q_out, interleaved, stream, dev)
+    args = _rope_append_at_args(args, cos_sin, positions, pair_axes, dev)
+    st = (_lib or load()).pa_rope_append_at_q8(*args, kc, vc, ks, vs, _kept_desc(shape),
+                                               _status_ptr(device_status, dev),
+                                               _current_stream(stream))
+    if st:
+        _check(st, "pa_rope_append_at_q8")
+    return q_out
+
+
+def pa_tree_workspace_size() -> int:
+    return int(load().pa_tree_workspace_size())
+
+
+def pack_tree_mask(seen):
+    """bool [T, n] (row t sees drafted token j of its sequence) as pa_tree_attention's int32
+    [T, ceil(n / 32)] mask."""
+    if seen.dtype is not torch.bool or seen.dim() != 2:
+        raise ValueError("seen must be bool [rows, drafted tokens]")
+    words = (seen.shape[1] + 31) // 32
+    bits = torch.nn.functional.pad(seen, (0, 32 * words - seen.shape[1])).view(-1, words, 32)
+    place = torch.arange(32, dtype=torch.int64, device=seen.device)
+    return (bits.to(torch.int64) << place).sum(dim=2).to(torch.int32)
+
+
+def _tree_args(out, q, tree_mask, query_start_loc, block_tables, context_lens, workspace, stream, dev):
+    op = _check_tensor(out, "out", torch.bfloat16, 3, dev)
+    qp = _check_tensor(q, "q", torch.bfloat16, 3, dev)
+    mask = _check_tensor(tree_mask, "tree_mask", torch.int32, 2, dev)
+    starts = _check_tensor(query_start_loc, "query_start_loc", torch.int32, 1, dev)
+    bt = _check_tensor(block_tables, "block_tables", torch.int32, 2, dev)
+    ctx = _check_tensor(context_lens, "context_lens", torch.int32, 1, dev)
+    q_shape = q.shape
+    num_seqs = context_lens.shape[0]
+    if out.shape != q_shape or q_shape[2] != 64 or tree_mask.shape[0] != q_shape[0] or \
+            query_start_loc.shape[0] != num_seqs + 1 or block_tables.shape[0] != num_seqs:
+        raise ValueError("tree argument shapes disagree")
+    if workspace is None:
+        workspace = _on_stream(stream, lambda: torch.zeros(pa_tree_workspace_size(),
+                                                           dtype=torch.uint8, device=q.device))
+    ws = _check_tensor(workspace, "workspace", torch.uint8, 1, dev)
+    return op, qp, mask, starts, bt, ctx, ws, workspace
+
+
+def pa_tree_attention(out, q, tree_mask, query_start_loc, max_query_len, key_cache, value_cache,
+                      block_tables, context_lens, scale, workspace=None, device_status=None,
+                      stream=None):
+    """Attention of drafted trees over the bf16 pools: the last rows of every sequence see the keys
+    before them, and one another as tree_mask says (pack_tree_mask); writes out [Tq, Hq, D]."""
+    dev = _current_device()
+    op, qp, mask, starts, bt, ctx, ws, workspace = _tree_args(
+        out, q, tree_mask, query_start_loc, block_tables, context_lens, workspace, stream, dev)
+    kc = _check_tensor(key_cache, "key_cache", torch.bfloat16, 4, dev)
+    vc = _check_tensor(value_cache, "value_cache", torch.bfloat16, 4, dev)
+    shape = key_cache.shape
+    if value_cache.shape != shape:
+        raise ValueError("cache shapes differ")
+    tokens, hq, _ = q.shape
+    seqs, width = block_tables.shape
+    st = (_lib or load()).pa_tree_attention(
+        op, qp, mask, tree_mask.shape[1], starts, tokens, int(max_query_len), kc, vc,
+        _kept_desc(shape), bt, width, ctx, seqs, hq, float(scale), ws, workspace.shape[0],
+        _status_ptr(device_status, dev), _current_stream(stream))
+    if st:
+        _check(st, "pa_tree_attention")
+    return out
+
+
+def pa_tree_attention_q8(out, q, tree_mask, query_start_loc, max_query_len, key_cache, value_cache,
+                         key_scale, value_scale, block_tables, context_lens, scale, workspace=None,
+                         device_status=None, stream=None):
+    """pa_tree_attention over the 8-bit pools."""
+    dev = _current_device()
+    op, qp, mask, starts, bt, ctx, ws, workspace = _tree_args(
+        out, q, tree_mask, query_start_loc, block_tables, context_lens, workspace, stream, dev)
+    kc, vc, ks, vs, shape = _need_q8(key_cache, value_cache, key_scale, value_scale, dev)
+    tokens, hq, _ = q.shape
+    seqs, width = block_tables.shape
+    st = (_lib or load()).pa_tree_attention_q8(
+        op, qp, mask, tree_mask.shape[1], starts, tokens, int(max_query_len), kc, vc, ks, vs,
+        _kept_desc(shape), bt, width, ctx, seqs, hq, float(scale), ws, workspace.shape[0],
+        _status_ptr(device_status, dev), _current_stream(stream))
+    if st:
+        _check(st, "pa_tree_attention_q8")
+    return out
+
+
+def _compact_args(kept, kept_start_loc, first, max_kept, block_tables, dev):
+    kp = _check_tensor(kept, "kept", torch.int32, 1, dev)
+    starts = _check_tensor(kept_start_loc, "kept_start_loc", torch.int32, 1, dev)
+    fp = _check_tensor(first, "first", torch.int32, 1, dev)
+    bt = _check_tensor(block_tables, "block_tables", torch.int32, 2, dev)
+    seqs, width = block_tables.shape
+    if first.shape[0] != seqs or kept_start_loc.shape[0] != seqs + 1:
+        raise ValueError("kept_start_loc, first and block_tables disagree on the sequence count")
+    return (kp, starts, fp, kept.shape[0], int(max_kept)), (bt, width, seqs)
+
+
+def pa_compact_tokens(kept, kept_start_loc, first, max_kept, key_cache, value_cache, block_tables,
+                      device_status=None, stream=None):
+    """Move the kept tokens of every sequence together, in place: the one at position first[s] +
+    kept[i] to first[s] + i (kept rising within a sequence); see include/pagedkv.h."""
+    dev = _current_device()
+    kc = _check_tensor(key_cache, "key_cache", torch.bfloat16, 4, dev)
+    vc = _check_tensor(value_cache, "value_cache", torch.bfloat16, 4, dev)
+    shape = key_cache.shape
+    if value_cache.shape != shape:
+        raise ValueError("cache shapes differ")
+    lists, tables = _compact_args(kept, kept_start_loc, first, max_kept, block_tables, dev)
+    st = (_lib or load()).pa_compact_tokens(*lists, kc, vc, _kept_desc(shape), *tables,
+                                            _status_ptr(device_status, dev), _current_stream(stream))
+    if st:
+        _check(st, "pa_compact_tokens")
+
+
+def pa_compact_tokens_q8(kept, kept_start_loc, first, max_kept, key_cache, value_cache, key_scale,
+                         value_scale, block_tables, device_status=None, stream=None):
+    """pa_compact_tokens in the 8-bit pools: the moved values are stored as an append stores them."""
+    dev = _current_device()
+    kc, vc, ks, vs, shape = _need_q8(key_cache, value_cache, key_scale, value_scale, dev)
+    lists, tables = _compact_args(kept, kept_start_loc, first, max_kept, block_tables, dev)
+    st = (_lib or load()).pa_compact_tokens_q8(*lists, kc, vc, ks, vs, _kept_desc(shape), *tables,
+                                               _status_ptr(device_status, dev),
+                                               _current_stream(stream))
+    if st:
+        _check(st, "pa_compact_tokens_q8")
 
 
 class BlockManager:

@@ -40,6 +40,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 constexpr int32_t kMaxQHeads = 1024;  // query heads the rotating appends take
+constexpr int32_t kMaxTreeRows = 1024;  // drafted tokens of a sequence
 
 pa_status check_desc(const pa_cache_desc& cd) {
   if (cd.num_blocks <= 0 || cd.num_kv_heads <= 0 || cd.num_kv_heads > 64)
@@ -481,6 +482,9 @@ pa_status append_args(const void* q, int64_t q_stride, void* q_out, int64_t q_ou
   a->cos_sin = cos_sin;
   a->max_positions = max_positions;
   a->interleaved = interleaved != 0;
+  a->positions = nullptr;
+  a->num_axes = 0;
+  a->pair_axes = 0;
   a->block_tables = block_tables;
   a->max_blocks_per_seq = max_blocks_per_seq;
   a->context_lens = context_lens;
@@ -545,6 +549,73 @@ pa_status pa_rope_append_q8(const void* q, int64_t q_stride, void* q_out, int64_
   a.value_scale = value_scale;
   return from_cuda(pkv::launch_rope_append_q8(a, reinterpret_cast<cudaStream_t>(stream)),
                    "rope_append_q8 launch");
+}
+
+namespace {
+
+// The positions of the appends that have their own; after the other arguments' checks.
+pa_status append_positions(const int32_t* positions, int32_t num_axes, uint64_t pair_axes, pkv::AppendArgs* a) {
+  if (num_axes < 1 || num_axes > 4) return fail(PA_ERR_INVALID_ARG, "num_axes %d (1..4)", num_axes);
+  for (int i = 0; i < pkv::kHeadDim / 2; ++i)
+    if (static_cast<int32_t>((pair_axes >> (2 * i)) & 3u) >= num_axes)
+      return fail(PA_ERR_INVALID_ARG, "pair %d turns by axis %d of %d", i,
+                  static_cast<int>((pair_axes >> (2 * i)) & 3u), num_axes);
+  if (!positions || !aligned4(positions)) return fail(PA_ERR_INVALID_ARG, "null or misaligned positions");
+  a->positions = positions;
+  a->num_axes = num_axes;
+  a->pair_axes = pair_axes;
+  return PA_OK;
+}
+
+}  // namespace
+
+pa_status pa_rope_append_at(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                            int32_t num_q_heads, const void* key, int64_t key_stride,
+                            const void* value, int64_t value_stride, const float* cos_sin,
+                            int32_t max_positions, int32_t interleaved, const int32_t* positions,
+                            int32_t num_axes, uint64_t pair_axes, const int32_t* block_tables,
+                            int32_t max_blocks_per_seq, const int32_t* context_lens,
+                            const int32_t* query_start_loc, int32_t num_seqs, int32_t num_tokens,
+                            void* key_cache, void* value_cache, pa_cache_desc cd,
+                            int32_t* device_status, pa_stream_t stream) {
+  pkv::AppendArgs a;
+  bool skip;
+  pa_status st = append_args(q, q_stride, q_out, q_out_stride, num_q_heads, key, key_stride, value,
+                             value_stride, cos_sin, max_positions, interleaved, block_tables,
+                             max_blocks_per_seq, context_lens, query_start_loc, num_seqs,
+                             num_tokens, key_cache, value_cache, cd, device_status, true, &a, &skip);
+  if (st != PA_OK) return st;
+  if (skip) return ok();
+  if ((st = append_positions(positions, num_axes, pair_axes, &a)) != PA_OK) return st;
+  return from_cuda(pkv::launch_rope_append(a, reinterpret_cast<cudaStream_t>(stream)),
+                   "rope_append_at launch");
+}
+
+pa_status pa_rope_append_at_q8(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                               int32_t num_q_heads, const void* key, int64_t key_stride,
+                               const void* value, int64_t value_stride, const float* cos_sin,
+                               int32_t max_positions, int32_t interleaved, const int32_t* positions,
+                               int32_t num_axes, uint64_t pair_axes, const int32_t* block_tables,
+                               int32_t max_blocks_per_seq, const int32_t* context_lens,
+                               const int32_t* query_start_loc, int32_t num_seqs, int32_t num_tokens,
+                               void* key_cache, void* value_cache, float* key_scale,
+                               float* value_scale, pa_cache_desc cd, int32_t* device_status,
+                               pa_stream_t stream) {
+  pkv::AppendArgs a;
+  bool skip;
+  pa_status st = append_args(q, q_stride, q_out, q_out_stride, num_q_heads, key, key_stride, value,
+                             value_stride, cos_sin, max_positions, interleaved, block_tables,
+                             max_blocks_per_seq, context_lens, query_start_loc, num_seqs,
+                             num_tokens, key_cache, value_cache, cd, device_status, true, &a, &skip);
+  if (st != PA_OK) return st;
+  if (skip) return ok();
+  if ((st = append_positions(positions, num_axes, pair_axes, &a)) != PA_OK) return st;
+  if (!key_scale || !value_scale || !aligned4(key_scale) || !aligned4(value_scale))
+    return fail(PA_ERR_INVALID_ARG, "null or misaligned scales");
+  a.key_scale = key_scale;
+  a.value_scale = value_scale;
+  return from_cuda(pkv::launch_rope_append_q8(a, reinterpret_cast<cudaStream_t>(stream)),
+                   "rope_append_at_q8 launch");
 }
 
 size_t pa_decode_q8_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t num_q_heads,
@@ -674,6 +745,196 @@ pa_status pa_prefill_chunk_q8(void* out, const void* q, const int32_t* query_sta
   a.status = device_status;
   return from_cuda(pkv::launch_prefill_q8(a, reinterpret_cast<cudaStream_t>(stream)),
                    "prefill_chunk_q8 launch");
+}
+
+size_t pa_tree_workspace_size(void) { return pkv::tree_workspace_size(); }
+
+namespace {
+
+// Shared checks of the tree calls; *skip: a checked no-op.
+pa_status tree_args(void* out, const void* q, const int32_t* tree_mask, int32_t mask_words,
+                    const int32_t* query_start_loc, int32_t num_query_tokens, int32_t max_query_len,
+                    const void* key_cache, const void* value_cache, const float* key_scale,
+                    const float* value_scale, bool q8, const pa_cache_desc& cd, const int32_t* block_tables,
+                    int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t num_seqs,
+                    int32_t num_q_heads, float scale, void* workspace, size_t workspace_bytes,
+                    int32_t* device_status, pkv::TreeArgs* a, bool* skip) {
+  *skip = false;
+  pa_status st = check_attention_pools(cd);
+  if (st != PA_OK) return st;
+  if (num_seqs < 0 || max_query_len < 0 || num_query_tokens < 0 || max_blocks_per_seq <= 0)
+    return fail(PA_ERR_INVALID_ARG,
+                "num_seqs %d, num_query_tokens %d, max_query_len %d, max_blocks_per_seq %d",
+                num_seqs, num_query_tokens, max_query_len, max_blocks_per_seq);
+  if (num_q_heads <= 0 || num_q_heads % cd.num_kv_heads != 0)
+    return fail(PA_ERR_INVALID_ARG, "num_q_heads %d not a multiple of num_kv_heads %d", num_q_heads,
+                cd.num_kv_heads);
+  const int group = num_q_heads / cd.num_kv_heads;
+  if (group != 1 && group != 2 && group != 4)
+    return fail(PA_ERR_UNSUPPORTED, "query heads per kv head %d (1, 2, 4 implemented)", group);
+  if (num_seqs == 0 || max_query_len == 0 || num_query_tokens == 0) {
+    *skip = true;
+    return PA_OK;
+  }
+  if (max_query_len > kMaxTreeRows)
+    return fail(PA_ERR_UNSUPPORTED, "max_query_len %d (at most %d drafted tokens)", max_query_len, kMaxTreeRows);
+  if (max_query_len > num_query_tokens)
+    return fail(PA_ERR_INVALID_ARG, "max_query_len %d > num_query_tokens %d", max_query_len,
+                num_query_tokens);
+  if (mask_words < (max_query_len + 31) / 32)
+    return fail(PA_ERR_INVALID_ARG, "mask_words %d for %d drafted tokens", mask_words, max_query_len);
+  if (!out || !q || !tree_mask || !query_start_loc || !key_cache || !value_cache || !block_tables ||
+      !context_lens || (q8 && (!key_scale || !value_scale)))
+    return fail(PA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(out) || !aligned16(q) || !aligned16(key_cache) || !aligned16(value_cache) ||
+      !aligned4(tree_mask) || !aligned4(key_scale) || !aligned4(value_scale))
+    return fail(PA_ERR_INVALID_ARG,
+                "out/q/cache pointers must be 16-byte aligned, mask and scale pointers 4-byte aligned");
+  if (!(scale > 0.f) || !isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "scale %g", scale);
+  const size_t need = pkv::tree_workspace_size();
+  if (!workspace || workspace_bytes < need || need == 0 || !aligned16(workspace))
+    return fail(PA_ERR_WORKSPACE, "workspace %zu bytes at %p, need %zu (16-byte aligned)",
+                workspace_bytes, workspace, need);
+  a->out = out;
+  a->q = q;
+  a->tree_mask = tree_mask;
+  a->mask_words = mask_words;
+  a->query_start_loc = query_start_loc;
+  a->num_query_tokens = num_query_tokens;
+  a->max_query_len = max_query_len;
+  a->key_cache = key_cache;
+  a->value_cache = value_cache;
+  a->key_scale = key_scale;
+  a->value_scale = value_scale;
+  a->num_blocks = cd.num_blocks;
+  a->num_kv_heads = cd.num_kv_heads;
+  a->num_q_heads = num_q_heads;
+  a->block_tables = block_tables;
+  a->max_blocks_per_seq = max_blocks_per_seq;
+  a->context_lens = context_lens;
+  a->num_seqs = num_seqs;
+  a->scale = scale;
+  a->workspace = workspace;
+  a->status = device_status;
+  return PA_OK;
+}
+
+// Shared checks of the compactions.
+pa_status compact_args(const int32_t* kept, const int32_t* kept_start_loc, const int32_t* first,
+                       int32_t num_kept, int32_t max_kept, void* key_cache, void* value_cache,
+                       const pa_cache_desc& cd, const int32_t* block_tables,
+                       int32_t max_blocks_per_seq, int32_t num_seqs, int32_t* device_status,
+                       pkv::CompactArgs* a, bool* skip) {
+  *skip = false;
+  pa_status st = check_desc(cd);
+  if (st != PA_OK) return st;
+  if (num_kept < 0 || max_kept < 0 || num_seqs < 0 || max_blocks_per_seq <= 0)
+    return fail(PA_ERR_INVALID_ARG, "num_kept %d, max_kept %d, num_seqs %d, max_blocks_per_seq %d", num_kept,
+                max_kept, num_seqs, max_blocks_per_seq);
+  if (num_kept == 0 || max_kept == 0 || num_seqs == 0) {
+    *skip = true;
+    return PA_OK;
+  }
+  const int64_t items = 2ll * num_seqs * cd.num_kv_heads;
+  if (items >= (int64_t{1} << 31))
+    return fail(PA_ERR_UNSUPPORTED, "%d sequences x %d kv heads (fewer than 2^30 supported)", num_seqs,
+                cd.num_kv_heads);
+  if (!kept || !kept_start_loc || !first || !key_cache || !value_cache || !block_tables)
+    return fail(PA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(key_cache) || !aligned16(value_cache) || !aligned4(kept))
+    return fail(PA_ERR_INVALID_ARG, "cache pointers must be 16-byte aligned, kept 4-byte aligned");
+  a->kept = kept;
+  a->kept_start_loc = kept_start_loc;
+  a->first = first;
+  a->num_kept = num_kept;
+  a->max_kept = max_kept;
+  a->num_seqs = num_seqs;
+  a->block_tables = block_tables;
+  a->max_blocks_per_seq = max_blocks_per_seq;
+  a->num_blocks = cd.num_blocks;
+  a->num_kv_heads = cd.num_kv_heads;
+  a->key_cache = key_cache;
+  a->value_cache = value_cache;
+  a->key_scale = nullptr;
+  a->value_scale = nullptr;
+  a->status = device_status;
+  return PA_OK;
+}
+
+}  // namespace
+
+pa_status pa_tree_attention(void* out, const void* q, const int32_t* tree_mask, int32_t mask_words,
+                            const int32_t* query_start_loc, int32_t num_query_tokens,
+                            int32_t max_query_len, const void* key_cache, const void* value_cache,
+                            pa_cache_desc cd, const int32_t* block_tables,
+                            int32_t max_blocks_per_seq, const int32_t* context_lens,
+                            int32_t num_seqs, int32_t num_q_heads, float scale, void* workspace,
+                            size_t workspace_bytes, int32_t* device_status, pa_stream_t stream) {
+  pkv::TreeArgs a;
+  bool skip;
+  pa_status st = tree_args(out, q, tree_mask, mask_words, query_start_loc, num_query_tokens, max_query_len,
+                           key_cache, value_cache, nullptr, nullptr, false, cd, block_tables,
+                           max_blocks_per_seq, context_lens, num_seqs, num_q_heads, scale, workspace,
+                           workspace_bytes, device_status, &a, &skip);
+  if (st != PA_OK) return st;
+  if (skip) return ok();
+  return from_cuda(pkv::launch_tree(a, reinterpret_cast<cudaStream_t>(stream)), "tree_attention launch");
+}
+
+pa_status pa_tree_attention_q8(void* out, const void* q, const int32_t* tree_mask,
+                               int32_t mask_words, const int32_t* query_start_loc,
+                               int32_t num_query_tokens, int32_t max_query_len,
+                               const void* key_cache, const void* value_cache,
+                               const float* key_scale, const float* value_scale,
+                               pa_cache_desc cd, const int32_t* block_tables,
+                               int32_t max_blocks_per_seq, const int32_t* context_lens,
+                               int32_t num_seqs, int32_t num_q_heads, float scale,
+                               void* workspace, size_t workspace_bytes, int32_t* device_status,
+                               pa_stream_t stream) {
+  pkv::TreeArgs a;
+  bool skip;
+  pa_status st = tree_args(out, q, tree_mask, mask_words, query_start_loc, num_query_tokens, max_query_len,
+                           key_cache, value_cache, key_scale, value_scale, true, cd, block_tables,
+                           max_blocks_per_seq, context_lens, num_seqs, num_q_heads, scale, workspace,
+                           workspace_bytes, device_status, &a, &skip);
+  if (st != PA_OK) return st;
+  if (skip) return ok();
+  return from_cuda(pkv::launch_tree_q8(a, reinterpret_cast<cudaStream_t>(stream)),
+                   "tree_attention_q8 launch");
+}
+
+pa_status pa_compact_tokens(const int32_t* kept, const int32_t* kept_start_loc,
+                            const int32_t* first, int32_t num_kept, int32_t max_kept,
+                            void* key_cache, void* value_cache, pa_cache_desc cd,
+                            const int32_t* block_tables, int32_t max_blocks_per_seq,
+                            int32_t num_seqs, int32_t* device_status, pa_stream_t stream) {
+  pkv::CompactArgs a;
+  bool skip;
+  pa_status st = compact_args(kept, kept_start_loc, first, num_kept, max_kept, key_cache, value_cache, cd,
+                              block_tables, max_blocks_per_seq, num_seqs, device_status, &a, &skip);
+  if (st != PA_OK) return st;
+  if (skip) return ok();
+  return from_cuda(pkv::launch_compact(a, reinterpret_cast<cudaStream_t>(stream)), "compact_tokens launch");
+}
+
+pa_status pa_compact_tokens_q8(const int32_t* kept, const int32_t* kept_start_loc,
+                               const int32_t* first, int32_t num_kept, int32_t max_kept,
+                               void* key_cache, void* value_cache, float* key_scale,
+                               float* value_scale, pa_cache_desc cd, const int32_t* block_tables,
+                               int32_t max_blocks_per_seq, int32_t num_seqs,
+                               int32_t* device_status, pa_stream_t stream) {
+  pkv::CompactArgs a;
+  bool skip;
+  pa_status st = compact_args(kept, kept_start_loc, first, num_kept, max_kept, key_cache, value_cache, cd,
+                              block_tables, max_blocks_per_seq, num_seqs, device_status, &a, &skip);
+  if (st != PA_OK) return st;
+  if (skip) return ok();
+  if (!key_scale || !value_scale || !aligned4(key_scale) || !aligned4(value_scale))
+    return fail(PA_ERR_INVALID_ARG, "null or misaligned scales");
+  a.key_scale = key_scale;
+  a.value_scale = value_scale;
+  return from_cuda(pkv::launch_compact_q8(a, reinterpret_cast<cudaStream_t>(stream)),
+                   "compact_tokens_q8 launch");
 }
 
 pa_status pa_selftest_wait_timeout(int32_t* device_status, int32_t limit_ms,

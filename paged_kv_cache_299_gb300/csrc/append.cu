@@ -7,6 +7,10 @@
 //   (a cos - b sin, b cos + a sin),   cos = table[p][i], sin = table[p][32 + i],
 // evaluated in fp32 and rounded once to what is stored (bf16, or a code of the 8-bit pools).
 //
+// With positions of their own (pa_rope_append_at: nodes of a drafted tree, image patches) tokens
+// go to the same slots, but pair i turns by row positions[axis(i)][t] of the table; axis(i) is two
+// bits of pair_axes.
+//
 // Memory-bound: every row is read once and written once.  Four lanes carry one head row, each
 // both members of eight pairs, so a row's rotation needs no exchange and a lane's cosines and
 // sines serve all the heads of its token.  Measured (32 query and 8 K/V heads): 16,000 prompt
@@ -30,6 +34,7 @@ constexpr int kPairs = kHeadDim / 2;
 constexpr int kLanePairs = 8;                     // rotation pairs per lane: 16 dims, 32 bytes
 constexpr int kLanesPerRow = kPairs / kLanePairs;  // 4
 constexpr int kRowsPerWarp = 32 / kLanesPerRow;   // 8 head rows side by side
+static_assert(kLanesPerRow == kQ8RowLanes && kRowsPerWarp == kQ8WarpRows, "rows of codes as rows of values");
 constexpr int kUnroll = 3;  // rows a lane has in flight: 48 rows (32 + 2 x 8 heads) in two rounds
 
 // The last i in [0, n) with value(i) <= key, for value rising and value(0) <= key (0 otherwise).  A
@@ -51,7 +56,9 @@ __device__ __forceinline__ int32_t last_at_most(int32_t n, int64_t key, int lane
 // Sequence of token t (the last s with query_start_loc[s] <= t; without query_start_loc,
 // sequence t) and its logical position.  false: the token is padding (at or past
 // query_start_loc[num_seqs], or a context of 0 in the one-token form) or was flagged.  (Rows past
-// num_tokens are flagged through token 0, as their own have no warp.)
+// num_tokens are flagged through token 0, as their own have no warp.)  kAt: the position names the
+// slot alone, not a row of the angles.
+template <bool kAt>
 __device__ __forceinline__ bool locate(const AppendArgs& a, int32_t t, int lane, bool report, int32_t* seq,
                                        int64_t* pos) {
   int32_t s, first, q_len;
@@ -71,7 +78,7 @@ __device__ __forceinline__ bool locate(const AppendArgs& a, int32_t t, int lane,
   const int64_t p = static_cast<int64_t>(a.context_lens[s]) - q_len + (t - first);
   if (p < 0 || t < first || t - first >= q_len || q_len > a.num_tokens - first ||
       p >= static_cast<int64_t>(a.max_blocks_per_seq) * kBlockSize ||
-      (a.cos_sin != nullptr && p >= a.max_positions) || a.context_lens[s] < q_len) {
+      (!kAt && a.cos_sin != nullptr && p >= a.max_positions) || a.context_lens[s] < q_len) {
     if (report) flag_error(a.status, PA_DEVFLAG_BAD_CONTEXT);
     return false;
   }
@@ -99,6 +106,44 @@ __device__ __forceinline__ void load_angles(const float* __restrict__ row, int l
     const float4 s = __ldg(reinterpret_cast<const float4*>(row + kPairs + kLanePairs * l + 4 * h));
     g.c[4 * h] = c.x; g.c[4 * h + 1] = c.y; g.c[4 * h + 2] = c.z; g.c[4 * h + 3] = c.w;
     g.s[4 * h] = s.x; g.s[4 * h + 1] = s.y; g.s[4 * h + 2] = s.z; g.s[4 * h + 3] = s.w;
+  }
+}
+
+// The four lanes of a row hold token t's positions, lane l that of axis l (axes there are none of:
+// 0).  *ok: this lane's lies inside the table.
+__device__ __forceinline__ int32_t load_position(const AppendArgs& a, int64_t t, int l, bool* ok) {
+  const int32_t p = l < a.num_axes ? __ldg(a.positions + l * static_cast<int64_t>(a.num_tokens) + t) : 0;
+  *ok = p >= 0 && p < a.max_positions;
+  return p;
+}
+
+// The lane's angles from the rows that its pairs' axes stand at; `mine` as above (inside the table).
+// By a whole warp.  Four pairs of one axis come by one load each.
+__device__ __forceinline__ void load_angles_at(const AppendArgs& a, int32_t mine, int lane, Angles& g) {
+  const int l = lane % kLanesPerRow;
+  const uint32_t axes = static_cast<uint32_t>(a.pair_axes >> (2 * kLanePairs * l)) & 0xffffu;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t quad = (axes >> (8 * h)) & 0xffu;
+    const int first = kLanePairs * l + 4 * h;
+    int32_t p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      p[i] = __shfl_sync(0xffffffffu, mine, (lane & ~(kLanesPerRow - 1)) + ((quad >> (2 * i)) & 3u));
+    if (quad == (quad & 3u) * 0x55u) {
+      const float* row = a.cos_sin + static_cast<int64_t>(p[0]) * kHeadDim + first;
+      const float4 c = __ldg(reinterpret_cast<const float4*>(row));
+      const float4 s = __ldg(reinterpret_cast<const float4*>(row + kPairs));
+      g.c[4 * h] = c.x; g.c[4 * h + 1] = c.y; g.c[4 * h + 2] = c.z; g.c[4 * h + 3] = c.w;
+      g.s[4 * h] = s.x; g.s[4 * h + 1] = s.y; g.s[4 * h + 2] = s.z; g.s[4 * h + 3] = s.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float* row = a.cos_sin + static_cast<int64_t>(p[i]) * kHeadDim + first + i;
+        g.c[4 * h + i] = __ldg(row);
+        g.s[4 * h + i] = __ldg(row + kPairs);
+      }
+    }
   }
 }
 
@@ -136,15 +181,26 @@ __device__ __forceinline__ uint4 pack8(const float* y) {
 // One warp serves rows part, part + parts, ... (eight at a time) of token t: its query rows,
 // then, with kStore, its key and its value rows.  kUnroll rows a lane are loaded before the
 // first is written.
-template <bool kInterleaved, bool kStore>
+template <bool kInterleaved, bool kStore, bool kAt>
 __device__ void token_rows(const AppendArgs& a, int32_t t, int part, int parts, int lane) {
   int32_t seq;
   int64_t pos;
-  if (!locate(a, t, lane, part == 0 && lane == 0, &seq, &pos)) return;
   const int l = lane % kLanesPerRow;
+  bool in_table = true;
+  int32_t mine = 0;
+  if (kAt) mine = load_position(a, t, l, &in_table);
+  if (!locate<kAt>(a, t, lane, part == 0 && lane == 0, &seq, &pos)) return;
   const int c0 = first_chunk<kInterleaved>(l), c1 = second_chunk<kInterleaved>(l);
   Angles g;
-  load_angles(a.cos_sin + pos * kHeadDim, l, g);
+  if (kAt) {
+    if (!__all_sync(0xffffffffu, in_table)) {
+      if (part == 0 && lane == 0) flag_error(a.status, PA_DEVFLAG_BAD_CONTEXT);
+      return;
+    }
+    load_angles_at(a, mine, lane, g);
+  } else {
+    load_angles(a.cos_sin + pos * kHeadDim, l, g);
+  }
   int64_t tile0 = 0;  // first (block, head) tile of the token's block
   if (kStore) {
     const int32_t phys =
@@ -199,12 +255,12 @@ __device__ void token_rows(const AppendArgs& a, int32_t t, int part, int parts, 
   }
 }
 
-template <bool kInterleaved>
+template <bool kInterleaved, bool kAt>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(const AppendArgs a, int parts) {
   const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarpsPerCta + (threadIdx.x >> 5);
   const int64_t t = w / parts;
   if (t >= a.num_tokens) return;
-  token_rows<kInterleaved, true>(a, static_cast<int32_t>(t), static_cast<int>(w % parts), parts,
+  token_rows<kInterleaved, true, kAt>(a, static_cast<int32_t>(t), static_cast<int>(w % parts), parts,
                                  threadIdx.x & 31);
 }
 
@@ -243,30 +299,7 @@ __device__ __forceinline__ uint2 codes8(const float* y, float inv) {
   return make_uint2(w[0], w[1]);
 }
 
-constexpr int kRowSteps = kBlockSize / kRowsPerWarp;  // 2 rows of the block per lane
-
-// Multiplies the codes of a tile's rows 0 .. o0-1 by `ratio` (below 1), rounding once.  Powers
-// of two keep them exact down to the subnormal codes.  By a whole warp.
-__device__ __forceinline__ void rescale_rows(uint8_t* tile, float ratio, int o0, int lane) {
-#pragma unroll
-  for (int k = 0; k < kRowSteps; ++k) {
-    const int row = k * kRowsPerWarp + lane / kLanesPerRow;
-    if (row >= o0) continue;
-    uint4* p = reinterpret_cast<uint4*>(tile + row * kQ8RowBytes) + lane % kLanesPerRow;
-    const uint4 c = *p;
-    const uint32_t in[4] = {c.x, c.y, c.z, c.w};
-    uint32_t out[4];
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      uint32_t lo, hi;
-      codes4_to_half2x2(in[h], lo, hi);
-      const float2 a = half2_to_float2(lo), b = half2_to_float2(hi);
-      out[h] = floats_to_codes2(a.x * ratio, a.y * ratio) |
-               (static_cast<uint32_t>(floats_to_codes2(b.x * ratio, b.y * ratio)) << 16);
-    }
-    *p = make_uint4(out[0], out[1], out[2], out[3]);
-  }
-}
+constexpr int kRowSteps = kQ8RowSteps;  // 2 rows of the block per lane
 
 // A lane's sixteen values as codes, into its places of a row of a tile.
 template <bool kInterleaved>
@@ -284,7 +317,7 @@ __device__ __forceinline__ void store_codes(uint8_t* row, const float* y, float 
 // pool, four lanes each.  A block with earlier tokens whose scale has to grow is rescaled by
 // the whole warp.  (A warp per head and pool, as chunks have it, took 4.5 us for 256
 // sequences and 12.1 for 1024, this 2.5 and 3.2.)
-template <bool kRotate, bool kInterleaved>
+template <bool kRotate, bool kInterleaved, bool kAt>
 __device__ void step_rows(const AppendArgs& a, int64_t item, int lane) {
   const bool is_k = (item & 1) == 0;
   item >>= 1;
@@ -295,7 +328,7 @@ __device__ void step_rows(const AppendArgs& a, int64_t item, int lane) {
   const int32_t ctx = a.context_lens[t];
   if (ctx == 0) return;  // padding
   if (ctx < 0 || static_cast<int64_t>(ctx) > static_cast<int64_t>(a.max_blocks_per_seq) * kBlockSize ||
-      (kRotate && ctx > a.max_positions)) {
+      (kRotate && !kAt && ctx > a.max_positions)) {
     if (tell) flag_error(a.status, PA_DEVFLAG_BAD_CONTEXT);
     return;
   }
@@ -310,7 +343,17 @@ __device__ void step_rows(const AppendArgs& a, int64_t item, int lane) {
   const uint4 x1 = ldg_nc128(reinterpret_cast<const uint4*>(src) + second_chunk<kInterleaved>(l));
   const bool turn = kRotate && is_k;
   Angles g = {};
-  if (turn) load_angles(a.cos_sin + static_cast<int64_t>(pos) * kHeadDim, l, g);
+  if (kAt) {
+    bool in_table;
+    const int32_t mine = load_position(a, t, l, &in_table);
+    if (!__all_sync(0xffffffffu, in_table)) {
+      if (tell) flag_error(a.status, PA_DEVFLAG_BAD_CONTEXT);
+      return;
+    }
+    if (turn) load_angles_at(a, mine, lane, g);
+  } else if (turn) {
+    load_angles(a.cos_sin + static_cast<int64_t>(pos) * kHeadDim, l, g);
+  }
   const int32_t phys = a.block_tables[t * a.max_blocks_per_seq + pos / kBlockSize];
   if (phys < 0 || phys >= a.num_blocks) {
     if (tell) flag_error(a.status, PA_DEVFLAG_BAD_BLOCK);
@@ -351,7 +394,7 @@ __device__ void step_rows(const AppendArgs& a, int64_t item, int lane) {
 // new rows (at most 16) in registers, finds their largest magnitude, settles the scale and
 // writes codes.  The tokens of a block are all this warp's, so nothing is shared between warps
 // and results do not depend on any order.
-template <bool kRotate, bool kInterleaved>
+template <bool kRotate, bool kInterleaved, bool kAt>
 __device__ void block_rows(const AppendArgs& a, int64_t item, int lane) {
   const bool is_k = (item & 1) == 0;
   item >>= 1;
@@ -376,7 +419,7 @@ __device__ void block_rows(const AppendArgs& a, int64_t item, int lane) {
   const bool tell = lane == 0 && head == 0 && index == 0 && is_k;
   if (first < 0 || static_cast<int64_t>(first) + q_len > a.num_tokens || p0 < 0 ||
       ctx > static_cast<int64_t>(a.max_blocks_per_seq) * kBlockSize ||
-      (kRotate && ctx > a.max_positions)) {
+      (kRotate && !kAt && ctx > a.max_positions)) {
     if (tell) flag_error(a.status, PA_DEVFLAG_BAD_CONTEXT);
     return;
   }
@@ -409,6 +452,21 @@ __device__ void block_rows(const AppendArgs& a, int64_t item, int lane) {
       x[k][1] = ldg_nc128(p + c1);
     }
   }
+  int32_t mine[kRowSteps] = {};  // positions of the rows, as load_position has them
+  if (kAt) {  // a block stores all of its new rows or none: the scale is theirs together
+    bool in_table = true;
+#pragma unroll
+    for (int k = 0; k < kRowSteps; ++k) {
+      const int row = k * kRowsPerWarp + lane / kLanesPerRow;
+      bool ok = true;
+      if (row >= o0 && row < o1) mine[k] = load_position(a, t0 + row, l, &ok);
+      in_table &= ok;
+    }
+    if (!__all_sync(0xffffffffu, in_table)) {
+      if (lane == 0 && head == 0 && is_k) flag_error(a.status, PA_DEVFLAG_BAD_CONTEXT);
+      return;
+    }
+  }
   float y[kRowSteps][16];
   float amax = 0.f;
   bool bad = false;
@@ -417,7 +475,11 @@ __device__ void block_rows(const AppendArgs& a, int64_t item, int lane) {
     const int row = k * kRowsPerWarp + lane / kLanesPerRow;
     Angles g = {};
     const bool turn = kRotate && is_k && row >= o0 && row < o1;
-    if (turn) load_angles(a.cos_sin + (b * kBlockSize + row) * kHeadDim, l, g);
+    if (kAt) {
+      if (is_k) load_angles_at(a, mine[k], lane, g);  // (rows there are none of: position 0)
+    } else if (turn) {
+      load_angles(a.cos_sin + (b * kBlockSize + row) * kHeadDim, l, g);
+    }
     unpack16(x[k][0], x[k][1], y[k]);
     if (turn) rotate16<kInterleaved>(g, y[k]);
     amax = fmaxf(amax, amax16(y[k], &bad));
@@ -448,7 +510,7 @@ __device__ void block_rows(const AppendArgs& a, int64_t item, int lane) {
 
 // Item CTAs serve the blocks (or a step's tokens), the rest the query rows: the item CTAs first,
 // or, with share > 0, both kinds alternating in proportion (share: item CTAs per CTA, times 2^31).
-template <bool kRotate, bool kInterleaved>
+template <bool kRotate, bool kInterleaved, bool kAt>
 __global__ void __launch_bounds__(kThreads)
 rope_append_q8_kernel(const AppendArgs a, int64_t items, uint32_t item_ctas, uint32_t share, int parts) {
   const int lane = threadIdx.x & 31;
@@ -463,17 +525,17 @@ rope_append_q8_kernel(const AppendArgs a, int64_t items, uint32_t item_ctas, uin
     const int64_t w = static_cast<int64_t>(before) * kWarpsPerCta + (threadIdx.x >> 5);
     if (w >= items) return;
     if (a.query_start_loc == nullptr)
-      step_rows<kRotate, kInterleaved>(a, w, lane);
+      step_rows<kRotate, kInterleaved, kAt>(a, w, lane);
     else
-      block_rows<kRotate, kInterleaved>(a, w, lane);
+      block_rows<kRotate, kInterleaved, kAt>(a, w, lane);
     return;
   }
   if (kRotate) {
     const int64_t w = static_cast<int64_t>(blockIdx.x - before) * kWarpsPerCta + (threadIdx.x >> 5);
     const int64_t t = w / parts;
     if (t < a.num_tokens)
-      token_rows<kInterleaved, false>(a, static_cast<int32_t>(t), static_cast<int>(w % parts),
-                                      parts, lane);
+      token_rows<kInterleaved, false, kAt>(a, static_cast<int32_t>(t), static_cast<int>(w % parts),
+                                           parts, lane);
   }
 }
 
@@ -491,10 +553,17 @@ int parts_for(int64_t tokens, int rows) {
 cudaError_t launch_rope_append(const AppendArgs& a, cudaStream_t stream) {
   const int parts = parts_for(a.num_tokens, a.num_q_heads + 2 * a.num_kv_heads);
   const int64_t ctas = (static_cast<int64_t>(a.num_tokens) * parts + kWarpsPerCta - 1) / kWarpsPerCta;
-  if (a.interleaved)
-    rope_append_kernel<true><<<static_cast<unsigned>(ctas), kThreads, 0, stream>>>(a, parts);
-  else
-    rope_append_kernel<false><<<static_cast<unsigned>(ctas), kThreads, 0, stream>>>(a, parts);
+  const unsigned grid = static_cast<unsigned>(ctas);
+  if (a.positions != nullptr) {
+    if (a.interleaved)
+      rope_append_kernel<true, true><<<grid, kThreads, 0, stream>>>(a, parts);
+    else
+      rope_append_kernel<false, true><<<grid, kThreads, 0, stream>>>(a, parts);
+  } else if (a.interleaved) {
+    rope_append_kernel<true, false><<<grid, kThreads, 0, stream>>>(a, parts);
+  } else {
+    rope_append_kernel<false, false><<<grid, kThreads, 0, stream>>>(a, parts);
+  }
   return cudaGetLastError();
 }
 
@@ -520,12 +589,18 @@ cudaError_t launch_rope_append_q8(const AppendArgs& a, cudaStream_t stream) {
       ctas > kAlternateCtas && q_ctas > 0 ? static_cast<uint32_t>(((item_ctas << 31) + ctas - 1) / ctas) : 0;
   const unsigned grid = static_cast<unsigned>(ctas);
   const uint32_t first = static_cast<uint32_t>(item_ctas);
-  if (a.cos_sin == nullptr)
-    rope_append_q8_kernel<false, false><<<grid, kThreads, 0, stream>>>(a, items, first, share, parts);
-  else if (a.interleaved)
-    rope_append_q8_kernel<true, true><<<grid, kThreads, 0, stream>>>(a, items, first, share, parts);
-  else
-    rope_append_q8_kernel<true, false><<<grid, kThreads, 0, stream>>>(a, items, first, share, parts);
+  if (a.positions != nullptr) {
+    if (a.interleaved)
+      rope_append_q8_kernel<true, true, true><<<grid, kThreads, 0, stream>>>(a, items, first, share, parts);
+    else
+      rope_append_q8_kernel<true, false, true><<<grid, kThreads, 0, stream>>>(a, items, first, share, parts);
+  } else if (a.cos_sin == nullptr) {
+    rope_append_q8_kernel<false, false, false><<<grid, kThreads, 0, stream>>>(a, items, first, share, parts);
+  } else if (a.interleaved) {
+    rope_append_q8_kernel<true, true, false><<<grid, kThreads, 0, stream>>>(a, items, first, share, parts);
+  } else {
+    rope_append_q8_kernel<true, false, false><<<grid, kThreads, 0, stream>>>(a, items, first, share, parts);
+  }
   return cudaGetLastError();
 }
 

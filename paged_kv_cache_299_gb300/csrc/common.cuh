@@ -75,6 +75,22 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   return true;
 }
 
+// mbar_wait that also gives up (false) once a warp of the CTA has, and tells the others.
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity,
+                                              volatile int* abort_flag, int32_t* status) {
+  if (*abort_flag) return false;
+  if (mbar_wait(bar, parity)) return true;
+  flag_error(status, PA_DEVFLAG_TIMEOUT);
+  *abort_flag = 1;
+  return false;
+}
+
+// wait_or_abort whose usual case, a phase that has completed, is one try_wait.
+__device__ __forceinline__ bool wait_ready(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                           int32_t* status) {
+  return mbar_try_wait(bar, parity) || wait_or_abort(bar, parity, abort_flag, status);
+}
+
 // ---- bulk asynchronous copies (TMA, non-tensor form) ------------------------------------
 // L2 policy for data read exactly once (KV tiles): evict first.
 __device__ __forceinline__ uint64_t l2_evict_first_policy() {
@@ -114,6 +130,27 @@ __device__ __forceinline__ float2 bf16x2_to_float2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
+// Two floats as a bf16 pair (x in the low half), and the product of two pairs.
+__device__ __forceinline__ uint32_t pack_bf2(float x, float y) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t mul_bf2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Lanes whose numbers differ in bit `d` exchange: the lower's b for the upper's a.
+__device__ __forceinline__ void swap_chunks(uint4& a, uint4& b, bool upper, int d) {
+  uint4 give = upper ? a : b;
+  give.x = __shfl_xor_sync(0xffffffffu, give.x, d);
+  give.y = __shfl_xor_sync(0xffffffffu, give.y, d);
+  give.z = __shfl_xor_sync(0xffffffffu, give.z, d);
+  give.w = __shfl_xor_sync(0xffffffffu, give.w, d);
+  if (upper) a = give; else b = give;
+}
+
 // Hint: bring the 128-byte line holding `p` into L2 (no register result, never faults on a
 // valid address).
 __device__ __forceinline__ void prefetch_l2(const void* p) {
@@ -131,6 +168,29 @@ __device__ __forceinline__ void bulk_prefetch_l2(const void* p, uint32_t bytes, 
 
 __device__ __forceinline__ uint4 lds128(const void* p) {
   return *reinterpret_cast<const uint4*>(p);
+}
+
+// A shared-memory float, read where it is used (not held in a register from before).
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+
+__device__ __forceinline__ void lds_f32x4(uint32_t addr, float (&v)[4]) {
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(addr));
+}
+
+// ---- four-byte asynchronous copies
+__device__ __forceinline__ void async_copy4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+// One arrival on `bar` (counted in its initial count) when this thread's asynchronous copies
+// so far have landed.
+__device__ __forceinline__ void async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
 __device__ __forceinline__ uint4 ldg_nc128(const void* p) {

@@ -46,6 +46,9 @@ struct AppendArgs {
   const float* cos_sin;  // [max_positions][64]: 32 cosines, then 32 sines; null: no rotation
   int32_t max_positions;
   bool interleaved;
+  const int32_t* positions;  // [num_axes][num_tokens] rows of cos_sin; null: the slots' positions
+  int32_t num_axes;          // 1 .. 4
+  uint64_t pair_axes;        // two bits per pair: its axis
   const int32_t* block_tables;
   int32_t max_blocks_per_seq;
   const int32_t* context_lens;
@@ -60,6 +63,52 @@ struct AppendArgs {
 
 cudaError_t launch_rope_append(const AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_rope_append_q8(const AppendArgs& a, cudaStream_t stream);
+
+// Compaction of kept tokens (pa_compact_tokens, pa_compact_tokens_q8).
+struct CompactArgs {
+  const int32_t* kept;  // rising offsets from first[s]
+  const int32_t* kept_start_loc;
+  const int32_t* first;
+  int32_t num_kept, max_kept, num_seqs;
+  const int32_t* block_tables;
+  int32_t max_blocks_per_seq;
+  int32_t num_blocks, num_kv_heads;
+  void* key_cache;
+  void* value_cache;
+  float* key_scale;  // 8-bit pools only
+  float* value_scale;
+  int32_t* status;
+};
+
+cudaError_t launch_compact(const CompactArgs& a, cudaStream_t stream);
+cudaError_t launch_compact_q8(const CompactArgs& a, cudaStream_t stream);
+
+// Attention of drafted trees (pa_tree_attention, pa_tree_attention_q8).
+struct TreeArgs {
+  void* out;
+  const void* q;
+  const int32_t* tree_mask;  // [num_query_tokens][mask_words] bits
+  int32_t mask_words;
+  const int32_t* query_start_loc;
+  int32_t num_query_tokens;
+  int32_t max_query_len;
+  const void* key_cache;
+  const void* value_cache;
+  const float* key_scale;  // 8-bit pools only
+  const float* value_scale;
+  int32_t num_blocks, num_kv_heads, num_q_heads;
+  const int32_t* block_tables;
+  int32_t max_blocks_per_seq;
+  const int32_t* context_lens;
+  int32_t num_seqs;
+  float scale;
+  void* workspace;
+  int32_t* status;
+};
+
+size_t tree_workspace_size();  // on the current device; 0 without one
+cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream);
+cudaError_t launch_tree_q8(const TreeArgs& a, cudaStream_t stream);
 
 // Attention over the 8-bit pools: rows of q are either one per sequence (query_start_loc
 // null) or causal chunks.

@@ -36,15 +36,6 @@ struct PParams {
   int32_t skip_single;  // 1: sequences with exactly one query row are served elsewhere
 };
 
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity,
-                                              volatile int* abort_flag, int32_t* status) {
-  if (*abort_flag) return false;
-  if (mbar_wait(bar, parity)) return true;
-  flag_error(status, PA_DEVFLAG_TIMEOUT);
-  *abort_flag = 1;
-  return false;
-}
-
 // One work unit: query tile `tile` (TOKENS tokens) of sequence s against K/V head g, with everything the roles derive from it.
 struct Unit {
   int s, g, tile;

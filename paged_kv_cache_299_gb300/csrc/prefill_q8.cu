@@ -100,53 +100,6 @@ struct Pools {
   const float* value_scale;
 };
 
-// wait_or_abort whose usual case, a phase that has completed, is one try_wait.
-__device__ __forceinline__ bool wait_ready(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                           int32_t* status) {
-  return mbar_try_wait(bar, parity) || wait_or_abort(bar, parity, abort_flag, status);
-}
-
-// Four 1 KiB tiles of a pool, rows[0..3] of its [tiles][1 KiB] view, by one copy.
-__device__ __forceinline__ void gather4(void* dst, const CUtensorMap* map, const int32_t* rows,
-                                        uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(rows[0]), "r"(rows[1]), "r"(rows[2]),
-      "r"(rows[3]), "r"(smem_addr(bar))
-      : "memory");
-}
-__device__ __forceinline__ void async_copy4(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-}
-// One arrival on `bar` (counted in its initial count) when this thread's asynchronous copies
-// so far have landed.
-__device__ __forceinline__ void async_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-
-// True in one lane of a converged warp (the same one on every call of the kernel).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t e;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(e));
-  return e != 0;
-}
-
-// A shared-memory float, read where it is used (not held in a register from before).
-__device__ __forceinline__ float lds_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-  return v;
-}
-
-__device__ __forceinline__ void lds_f32x4(uint32_t addr, float (&v)[4]) {
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
-               : "r"(addr));
-}
-
 // Instruction descriptor, kind::f16 with f16 A/B (both K-major) and fp32 accumulation.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n) {
   return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
@@ -158,51 +111,6 @@ __device__ __forceinline__ int half_tiles(const Unit& u, int half) {
   const int n = min(HALF_TOKENS, u.ntok - half * HALF_TOKENS);
   if (n <= 0) return 0;
   return (u.L - u.q_len + u.tok0 + half * HALF_TOKENS + n + kTileN - 1) / kTileN;
-}
-
-__device__ __forceinline__ uint32_t pack_bf2(float x, float y) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t mul_bf2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
-// Four codes of a word as bf16 pairs times 2^-120 (exact): the code's exponent and
-// significand bits, three places down from the bf16's, under its sign.
-__device__ __forceinline__ void codes4_to_bf2x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);
-  lo = (a & 0x80008000u) | ((a >> 4) & 0x07f007f0u);
-  hi = (b & 0x80008000u) | ((b >> 4) & 0x07f007f0u);
-}
-
-// f of a scale 2^e f, 1 <= f < 2, below the normal floats too; 1 for a scale of 0.
-__device__ __forceinline__ float significand(float s) {
-  const uint32_t b = __float_as_uint(s);
-  const int down = max(__clz(b) - 8, 0);  // places that a subnormal's first bit lies below the others'
-  return __uint_as_float(((b << down) & 0x7fffffu) | 0x3f800000u);
-}
-
-// 2^e as a bf16 pair, -126 <= e <= 127.
-__device__ __forceinline__ uint32_t bf2_power(int e) {
-  return static_cast<uint32_t>(e + 127) * 0x00800080u;
-}
-
-// Chunk c (16 bytes) of row r in the 128-byte-swizzled layout of 128-byte rows.
-__device__ __forceinline__ uint32_t swz(int r, int c) {
-  return static_cast<uint32_t>(r * kRowBytes + ((c ^ (r & 7)) << 4));
-}
-
-// Lanes whose numbers differ in bit `d` exchange: the lower's b for the upper's a.
-__device__ __forceinline__ void swap_chunks(uint4& a, uint4& b, bool upper, int d) {
-  uint4 give = upper ? a : b;
-  give.x = __shfl_xor_sync(0xffffffffu, give.x, d);
-  give.y = __shfl_xor_sync(0xffffffffu, give.y, d);
-  give.z = __shfl_xor_sync(0xffffffffu, give.z, d);
-  give.w = __shfl_xor_sync(0xffffffffu, give.w, d);
-  if (upper) a = give; else b = give;
 }
 
 template <int GROUP>

@@ -45,6 +45,54 @@ __device__ __forceinline__ float scale_for(float amax) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+// Four codes of a word as bf16 pairs times 2^-120 (exact): the code's exponent and
+// significand bits, three places down from the bf16's, under its sign.
+__device__ __forceinline__ void codes4_to_bf2x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);
+  lo = (a & 0x80008000u) | ((a >> 4) & 0x07f007f0u);
+  hi = (b & 0x80008000u) | ((b >> 4) & 0x07f007f0u);
+}
+
+// f of a scale 2^e f, 1 <= f < 2, below the normal floats too; 1 for a scale of 0.
+__device__ __forceinline__ float significand(float s) {
+  const uint32_t b = __float_as_uint(s);
+  const int down = max(__clz(b) - 8, 0);  // places that a subnormal's first bit lies below the others'
+  return __uint_as_float(((b << down) & 0x7fffffu) | 0x3f800000u);
+}
+
+// 2^e as a bf16 pair, -126 <= e <= 127.
+__device__ __forceinline__ uint32_t bf2_power(int e) {
+  return static_cast<uint32_t>(e + 127) * 0x00800080u;
+}
+
+// A warp over a tile's rows: four lanes a row, 16 codes each.
+constexpr int kQ8RowLanes = 4;
+constexpr int kQ8WarpRows = 32 / kQ8RowLanes;            // rows side by side
+constexpr int kQ8RowSteps = kBlockSize / kQ8WarpRows;  // rows of a tile per lane
+
+// Multiplies the codes of a tile's rows 0 .. o0-1 by `ratio` (below 1), rounding once.  Powers
+// of two keep them exact down to the subnormal codes.  By a whole warp.
+__device__ __forceinline__ void rescale_rows(uint8_t* tile, float ratio, int o0, int lane) {
+#pragma unroll
+  for (int k = 0; k < kQ8RowSteps; ++k) {
+    const int row = k * kQ8WarpRows + lane / kQ8RowLanes;
+    if (row >= o0) continue;
+    uint4* p = reinterpret_cast<uint4*>(tile + row * kQ8RowBytes) + lane % kQ8RowLanes;
+    const uint4 c = *p;
+    const uint32_t in[4] = {c.x, c.y, c.z, c.w};
+    uint32_t out[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      uint32_t lo, hi;
+      codes4_to_half2x2(in[h], lo, hi);
+      const float2 a = half2_to_float2(lo), b = half2_to_float2(hi);
+      out[h] = floats_to_codes2(a.x * ratio, a.y * ratio) |
+               (static_cast<uint32_t>(floats_to_codes2(b.x * ratio, b.y * ratio)) << 16);
+    }
+    *p = make_uint4(out[0], out[1], out[2], out[3]);
+  }
+}
+
 // One tile of a pool into shared memory, by one asynchronous copy.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar,
                                           uint64_t policy) {

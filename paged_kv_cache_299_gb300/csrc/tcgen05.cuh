@@ -1,5 +1,5 @@
 // Inline-PTX wrappers for the 5th-generation tensor cores (tcgen05 + tensor memory) and
-// tiled TMA loads, sm_103a.  Used by the chunked-prefill kernel only.
+// tiled TMA loads, sm_103a.  Used by the chunk and the tree kernels.
 #pragma once
 
 #include <cuda.h>
@@ -88,6 +88,20 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// True in one lane of a converged warp (the same one on every call of the kernel).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
+
+// Chunk c (16 bytes) of row r in the 128-byte-swizzled layout of 128-byte rows.
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+  return static_cast<uint32_t>(r * kRowBytes + ((c ^ (r & 7)) << 4));
+}
+
 // ---- UMMA descriptors -------------------------------------------------------------------
 // Shared-memory matrix descriptor for a 128-byte-swizzled canonical layout: start address,
 // leading / stride byte offsets (16-byte units), descriptor version 1, swizzle mode 2
@@ -162,6 +176,16 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
       "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
+      : "memory");
+}
+// Four 1 KiB tiles of a pool, rows[0..3] of its [tiles][1 KiB] view, by one copy.
+__device__ __forceinline__ void gather4(void* dst, const CUtensorMap* map, const int32_t* rows,
+                                        uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(rows[0]), "r"(rows[1]), "r"(rows[2]),
+      "r"(rows[3]), "r"(smem_addr(bar))
       : "memory");
 }
 __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {
