@@ -1,130 +1,1119 @@
-// Attention of drafted trees over a paged cache, bf16 and 8-bit pools.
+// Attention of drafted trees over a paged cache, bf16 and 8-bit pools, on tcgen05 tensor cores.
 //
 // A sequence's last q_len tokens are the nodes of a tree (their keys and values stored already) behind
 // a prefix of P = L - q_len tokens.  Row i sees every key of the prefix and drafted key j where bit j of
 // its mask row is set:
 //   out_i = sum_j softmax_j(scale q_i . K_j) V_j over the keys it sees, 0 where it sees none.
 //
-// One warp per (row, query head), a key per lane.
+// GB300 design.  The rows are few and the keys many: what counts is to stream K and V past 128 MMA rows
+// (128 / GROUP tokens x GROUP heads that share a K/V head) on every SM, whatever the batch looks like.
+//   * The work is a row of 128-key tiles: all tiles of all (sequence, K/V head, query tile) segments, one
+//     after the other.  It is cut into equal runs, one per CTA of a persistent grid of two CTAs per SM;
+//     a CTA serves its run's pieces of segments back to back.  A segment that one CTA serves whole goes
+//     straight to the output; pieces of a split one are kept in fp32 (sum, maximum, weight) in the
+//     workspace, and the CTA that finishes last weighs them together, in the pieces' order.
+//   * Two CTAs per SM, because a tile's chain (scores, softmax, product) is latency: 128 keys a tile
+//     amortise it, two chains fill in for each other.
+//   * Tensor memory (256 columns): scores S 128, P 64 (bf16 pairs), O 64.  P has columns of its own, so
+//     the next tile's scores are issued as soon as the row warps have read this tile's.
+//   * Warps 0-7, the row warps: two threads per row, 64 keys each.  Each also reads its partner's scores,
+//     for their maximum alone (a reduction that comes with the load), so both follow the same running
+//     maximum without meeting.  Exponentials, P as bf16, row sums in fp32; O is rescaled in place when a
+//     row's maximum grows past the headroom left above it.
+//   * One warp issues the MMAs: S = Q K^T (M128 N128 K64) and O += P V (M128 N64 K128); one the copies.
+//   * Masks are looked at only in tiles that hold drafted keys.  There the row warps also clear V rows
+//     past the context, and elements of drafted values that are no numbers (0 x NaN would reach rows
+//     that do not see them); the rows that do see them get them back in the epilogue.
+//   * 8-bit pools: two more warps turn codes into bf16 (exact) in shared memory.  With the value scale of
+//     a block written as 2^e f, 1 <= f < 2: V becomes 2^e code, f rides in the exponent of the weights and
+//     leaves the row sum again by 1 / f; the key scale multiplies the block's scores.
+// Every mbarrier wait is bounded; on timeout the CTA records PA_DEVFLAG_TIMEOUT, drains its own copies
+// and MMAs, frees its tensor memory, counts its pieces as delivered and returns.
 #include <math.h>
 
 #include "common.cuh"
 #include "internal.h"
 #include "q8.cuh"
+#include "tcgen05.cuh"
 
 namespace pkv {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kTileM = 128;
+constexpr int kTileN = 128;  // keys per tile
+constexpr int kBlocksPerTile = kTileN / kBlockSize;
+constexpr int kRowWarps = 8;
+constexpr int kRowThreads = kRowWarps * 32;
+constexpr int kMmaWarp = 8, kProducerWarp = 9, kConvWarp0 = 10, kConvWarps = 2;
+constexpr int kQBytes = kTileM * kRowBytes;   // 16 KiB
+constexpr int kOpBytes = kTileN * kRowBytes;  // one K or V tile of bf16: 16 KiB
+constexpr int kRawBytes = 2 * kTileN * kQ8RowBytes;  // codes of K, then of V
+constexpr int kConstRing = 4;                 // tiles whose score constants are kept
+constexpr int kConsts = 3 * kBlocksPerTile;   // key scale, log2 f, 1 / f of every block
+constexpr int kMaxMaskWords = 32;
+constexpr uint32_t kTmemCols = 256;
+constexpr uint32_t kSCol = 0, kPCol = 128, kOCol = 192;
+constexpr float kHeadroom = 8.0f;  // the reference of the exponents lies this far (log2) above the maximum
+constexpr float kLargeScore = 131072.f;  // 2^17: a rounding of the score (log2 units) is then 2^-7
+constexpr int kRecordChunks = kHeadDim / 4 + 1;  // float4s of a row: its sum, then maximum and weight
+constexpr int kRecordFloat4s = kRecordChunks * kTileM;
+constexpr int kMinRun = 2;  // tiles of a run, at least
+// Register split of the 8-bit kernel (setmaxnreg): what the CTA was launched with, 80 for each of 384 threads.
+constexpr int kRowRegs = 96, kOtherRegs = 48;
+
+constexpr int kPieceRing = 4;
+constexpr int kPieceBytes = 48, kWalkBytes = 48;
 
 template <bool Q8>
-__global__ void __launch_bounds__(kWarps * 32) tree_kernel(const TreeArgs a) {
-  __shared__ float sq[kWarps][kHeadDim];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-  const int32_t row = static_cast<int32_t>(w / a.num_q_heads);
-  const int head = static_cast<int>(w % a.num_q_heads);
-  if (row >= a.num_query_tokens) return;
-  int32_t s = 0;
-  while (s < a.num_seqs && a.query_start_loc[s + 1] <= row) ++s;
-  if (s >= a.num_seqs) return;
-  const int32_t q0 = a.query_start_loc[s], q_len = a.query_start_loc[s + 1] - q0, L = a.context_lens[s];
-  if (q0 < 0 || row < q0 || q_len > a.num_query_tokens - q0 || q_len > a.max_query_len || L < q_len ||
-      static_cast<int64_t>(L) > static_cast<int64_t>(a.max_blocks_per_seq) * kBlockSize) {
-    if (lane == 0) flag_error(a.status, PA_DEVFLAG_BAD_CONTEXT);
+struct Layout {
+  static constexpr int kThreads = Q8 ? 384 : 320;
+  static constexpr int kRing = Q8 ? 2 : 3;   // stages of K and V operands
+  static constexpr int kRawRing = 2;         // stages of codes
+  static constexpr int kKOff = kQBytes;
+  static constexpr int kVOff = kKOff + kRing * kOpBytes;
+  static constexpr int kRawOff = kVOff + kRing * kOpBytes;
+  static constexpr int kConstOff = kRawOff + (Q8 ? kRawRing * kRawBytes : 0);
+  static constexpr int kRawScaleOff = kConstOff + (Q8 ? kConstRing * kConsts * 4 : 0);
+  static constexpr int kBarOff = kRawScaleOff + (Q8 ? kRawRing * 2 * kBlocksPerTile * 4 : 0);
+  static constexpr int kNumBars = 9 + 2 * kRing + (Q8 ? 2 * kRawRing + 2 * kRing : 0);
+  static constexpr int kMiscOff = kBarOff + (kNumBars + 1) / 2 * 16;
+  static constexpr int kPieceOff = kMiscOff + 64;  // the row warps' pieces and the walk they come from
+  static constexpr int kOddOff = kPieceOff + kPieceRing * kPieceBytes + kWalkBytes;  // drafted tokens whose values are no numbers: [2][1 + 32] words
+  static constexpr int kBytes = kOddOff + (Q8 ? 0 : 2 * (1 + kMaxMaskWords) * 4);
+  static_assert(2 * (kBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+};
+
+struct TreeParams {
+  __nv_bfloat16* out;
+  const int32_t* tree_mask;
+  const int32_t* query_start_loc;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const __nv_bfloat16* value_cache;  // bf16 pools
+  const float* key_scale;            // 8-bit pools
+  const float* value_scale;
+  int32_t* counters;  // [grid] pieces delivered of the segment that starts in a CTA and goes on past it
+  float4* records;    // [grid][2][kRecordChunks][128]
+  int32_t* status;
+  int32_t mask_words, max_blocks_per_seq, num_blocks, num_kv_heads, num_q_heads;
+  int32_t num_query_tokens, max_query_len, num_seqs;
+  float qk_scale;  // scale * log2(e)
+};
+
+// The sequence whose tiles a run is in.
+struct Seq {
+  int s, q0, q_len, L;
+  int tiles;     // of a segment
+  int segments;  // K/V heads x query tiles; 0: none to serve
+};
+
+// Sequences without rows have no work; ones that cannot be served are reported (when `report`).
+template <int GROUP>
+__device__ __forceinline__ void load_seq(const TreeParams& p, int s, bool report, Seq& q) {
+  q.s = s;
+  q.q0 = __ldg(p.query_start_loc + s);
+  q.q_len = __ldg(p.query_start_loc + s + 1) - q.q0;
+  q.L = __ldg(p.context_lens + s);
+  q.segments = 0;
+  q.tiles = 1;
+  if (q.q_len <= 0) return;
+  if (q.q0 < 0 || q.q_len > p.num_query_tokens - q.q0 || q.q_len > p.max_query_len || q.L < q.q_len ||
+      q.L > static_cast<int64_t>(p.max_blocks_per_seq) * kBlockSize ||
+      q.L > static_cast<int64_t>(p.num_blocks) * kBlockSize) {
+    if (report) flag_error(p.status, PA_DEVFLAG_BAD_CONTEXT);
     return;
   }
-  const int g = head / (a.num_q_heads / a.num_kv_heads);
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + w * kHeadDim;
-  sq[warp][lane] = __bfloat162float(q[lane]);
-  sq[warp][lane + 32] = __bfloat162float(q[lane + 32]);
-  __syncwarp();
-  const int P = L - q_len;
-  const int32_t* table = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
-  const int32_t* bits = a.tree_mask + static_cast<int64_t>(row) * a.mask_words;
-  float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
-  for (int k0 = 0; k0 < L; k0 += 32) {
-    const int k = k0 + lane;
-    bool seen = k < L && (k < P || ((bits[(k - P) >> 5] >> ((k - P) & 31)) & 1) != 0);
-    int64_t at = 0;  // row of the pool
-    if (seen) {
-      const int32_t b = table[k / kBlockSize];
-      if (b < 0 || b >= a.num_blocks) {
-        flag_error(a.status, PA_DEVFLAG_BAD_BLOCK);
-        seen = false;
-      } else {
-        at = (static_cast<int64_t>(b) * a.num_kv_heads + g) * kBlockSize + k % kBlockSize;
-      }
-    }
-    float x = -INFINITY;
-    if (seen) {
-      x = 0.f;
-      for (int d = 0; d < kHeadDim; d += 4) {
-        float4 f;
-        if (Q8) {
-          uint32_t lo, hi;
-          codes4_to_half2x2(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.key_cache) + at * kHeadDim + d), lo, hi);
-          const float2 y = half2_to_float2(lo), z = half2_to_float2(hi);
-          f = make_float4(y.x, y.y, z.x, z.y);
-        } else {
-          const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.key_cache) + at * kHeadDim + d);
-          const float2 y = bf16x2_to_float2(u.x), z = bf16x2_to_float2(u.y);
-          f = make_float4(y.x, y.y, z.x, z.y);
-        }
-        x += sq[warp][d] * f.x + sq[warp][d + 1] * f.y + sq[warp][d + 2] * f.z + sq[warp][d + 3] * f.w;
-      }
-      x *= a.scale * 1.4426950408889634f;
-      if (Q8) x *= a.key_scale[at / kBlockSize];
-    }
-    float top = x;
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const float m_new = fmaxf(m, top);
-    const float ref = m_new == -INFINITY ? 0.f : m_new;
-    const float alpha = fast_exp2(m - ref);
-    m = m_new;
-    const float p = seen ? fast_exp2(x - ref) : 0.f;
-    l = l * alpha + p;
-    o0 *= alpha;
-    o1 *= alpha;
-    for (int j = 0; j < 32; ++j) {
-      if (!__shfl_sync(0xffffffffu, seen, j)) continue;
-      const float pj = __shfl_sync(0xffffffffu, p, j);
-      const int64_t aj = __shfl_sync(0xffffffffu, at, j);
+  constexpr int kTokens = kTileM / GROUP;
+  q.tiles = (q.L + kTileN - 1) / kTileN;
+  q.segments = p.num_kv_heads * ((q.q_len + kTokens - 1) / kTokens);
+}
+
+// A piece of a segment: key tiles j0 .. j0 + n - 1 of query tile tok0 / TOKENS against K/V head g.
+struct Piece {
+  int64_t first;  // the segment's first tile in the row of all tiles
+  int s, g, q0, q_len, L, tok0;
+  int j0, n, tiles;  // n == 0: none
+};
+
+// Walks a run.  A sequence's tiles stay below 2^31: its context fits a pool of fewer than 2^31 rows, which
+// K/V heads multiply, so tiles x heads < 2^24, and it has at most 32 query tiles.
+struct Walk {
+  int64_t at, end;  // the next tile and the run's end among all
+  Seq q;
+  int off;         // of the next tile among the sequence's
+};
+
+template <int GROUP>
+__device__ __forceinline__ bool next_piece(const TreeParams& p, Walk& w, Piece& u) {
+  if (w.at >= w.end) return false;
+  while (w.off >= w.q.tiles * w.q.segments) {
+    w.off -= w.q.tiles * w.q.segments;
+    load_seq<GROUP>(p, w.q.s + 1, false, w.q);
+  }
+  constexpr int kTokens = kTileM / GROUP;
+  const int seg = w.off / w.q.tiles;
+  const int q_tiles = (w.q.q_len + kTokens - 1) / kTokens;
+  u.s = w.q.s;
+  u.q0 = w.q.q0;
+  u.q_len = w.q.q_len;
+  u.L = w.q.L;
+  u.tiles = w.q.tiles;
+  u.g = seg / q_tiles;
+  u.tok0 = (seg - u.g * q_tiles) * kTokens;
+  u.j0 = w.off - seg * w.q.tiles;
+  u.n = static_cast<int>(min(static_cast<int64_t>(u.tiles - u.j0), w.end - w.at));
+  u.first = w.at - u.j0;
+  w.off += u.n;
+  w.at += u.n;
+  return true;
+}
+
+static_assert(sizeof(Piece) <= kPieceBytes && sizeof(Walk) <= kWalkBytes, "room for pieces");
+
+// Where all CTAs' runs lie: run r holds tiles total r / runs .. total (r + 1) / runs - 1.
+struct Runs {
+  int64_t total;
+  int runs;
+};
+__device__ __forceinline__ int64_t run_start(const Runs& x, int64_t r) { return x.total * r / x.runs; }
+// The run that holds a tile (none is empty).
+__device__ __forceinline__ int run_of(const Runs& x, int64_t tile) {
+  return static_cast<int>(((tile + 1) * x.runs + x.total - 1) / x.total - 1);
+}
+
+// Bits o .. o + 31 of what a row sees, counted from the first drafted key: below 0 the prefix, from q_len
+// on nothing.
+__device__ __forceinline__ uint32_t mask_word(const int32_t* bits, int q_len, int i) {
+  if (i < 0) return 0xffffffffu;
+  const int left = q_len - 32 * i;
+  if (left <= 0) return 0u;
+  const uint32_t w = static_cast<uint32_t>(__ldg(bits + i));
+  return left >= 32 ? w : w & ((1u << left) - 1u);
+}
+__device__ __forceinline__ uint32_t seen_bits(const int32_t* bits, int q_len, int o) {
+  return __funnelshift_r(mask_word(bits, q_len, o >> 5), mask_word(bits, q_len, (o >> 5) + 1), o & 31);
+}
+
+// A bf16 pair's elements that are no numbers (infinities and NaNs): ones in their halves.
+__device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
+  return ((w & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
+}
+
+template <int GROUP, bool Q8>
+__global__ void __launch_bounds__(Layout<Q8>::kThreads, 2)
+tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+            const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ TreeParams p) {
+  using Lay = Layout<Q8>;
+  constexpr int kThreads = Lay::kThreads, kRing = Lay::kRing, kRawRing = Lay::kRawRing;
+  const int tid = threadIdx.x;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (so that what depends on it stays uniform)
+  const int lane = tid & 31;
+  extern __shared__ __align__(1024) uint8_t smem[];  // 128-byte swizzle atoms need 1 KiB
+  if ((smem_addr(smem) & 1023u) != 0) {
+    if (tid == 0) flag_error(p.status, PA_DEVFLAG_LAYOUT);
+    return;
+  }
+  uint8_t* sq = smem;
+  uint8_t* sk = smem + Lay::kKOff;
+  uint8_t* sv = smem + Lay::kVOff;
+  uint8_t* sraw = smem + Lay::kRawOff;
+  float* consts = reinterpret_cast<float*>(smem + Lay::kConstOff);
+  float* raw_scale = reinterpret_cast<float*>(smem + Lay::kRawScaleOff);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::kBarOff);
+  uint64_t* q_full = bars;            // a piece's Q landed
+  uint64_t* s_full = bars + 1;        // scores in tensor memory
+  uint64_t* s_free = bars + 2;        // and read into registers
+  uint64_t* p_full = bars + 3;        // P in tensor memory
+  uint64_t* o_free = bars + 4;        // O of a finished piece read out
+  uint64_t* l_bar = bars + 5;         // the row warps' sums exchanged
+  uint64_t* piece_bar = bars + 6;     // a piece's record written
+  uint64_t* last_bar = bars + 7;      // whether it was the segment's last
+  uint64_t* drain = bars + 8;
+  uint64_t* kv_full = bars + 9;       // [kRing] K (and V, from bf16 pools) of a tile there
+  uint64_t* pv_done = kv_full + kRing;  // [kRing] P V of a tile done: its stage and P free, O up to date
+  uint64_t* v_full = pv_done + kRing;   // 8-bit pools: [kRing] V converted
+  uint64_t* k_empty = v_full + kRing;   // [kRing] scores that read K done
+  uint64_t* raw_full = k_empty + kRing;  // [kRawRing] codes and scales landed
+  uint64_t* raw_empty = raw_full + kRawRing;
+  int* misc = reinterpret_cast<int*>(smem + Lay::kMiscOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
+  volatile int& abort_flag = *reinterpret_cast<volatile int*>(misc + 1);
+  volatile int& is_last = *reinterpret_cast<volatile int*>(misc + 2);
+  volatile int& delivered = *reinterpret_cast<volatile int*>(misc + 3);
+  int* start_seq = misc + 4;
+  int* start_off = misc + 5;
+  uint32_t* odd = reinterpret_cast<uint32_t*>(smem + Lay::kOddOff);
+  auto piece_slot = [&](int u) -> Piece* {
+    return reinterpret_cast<Piece*>(smem + Lay::kPieceOff + (u & (kPieceRing - 1)) * kPieceBytes);
+  };
+  Walk* const row_walk = reinterpret_cast<Walk*>(smem + Lay::kPieceOff + kPieceRing * kPieceBytes);
+
+  if (tid == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(s_full, Q8 ? 2 : 1);
+    mbar_init(s_free, kRowWarps);
+    mbar_init(p_full, kRowWarps);
+    mbar_init(o_free, kRowWarps);
+    mbar_init(l_bar, kRowWarps);
+    mbar_init(piece_bar, kRowWarps);
+    mbar_init(last_bar, 1);
+    mbar_init(drain, 1);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&kv_full[i], Q8 ? kConvWarps : 1);
+      mbar_init(&pv_done[i], 1);
       if (Q8) {
-        uint32_t lo, hi;
-        codes4_to_half2x2(*reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(a.value_cache) + aj * kHeadDim + 2 * lane), lo, hi);
-        const float2 v = half2_to_float2(lo);
-        const float sc = a.value_scale[aj / kBlockSize];
-        o0 += pj * (v.x * sc);
-        o1 += pj * (v.y * sc);
-      } else {
-        const float2 v = bf16x2_to_float2(reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.value_cache) + aj * kHeadDim)[lane]);
-        o0 += pj * v.x;
-        o1 += pj * v.y;
+        mbar_init(&v_full[i], kConvWarps);
+        mbar_init(&k_empty[i], 1);
+      }
+    }
+    if (Q8) {
+      for (int i = 0; i < kRawRing; ++i) {
+        mbar_init(&raw_full[i], 1 + kBlocksPerTile);
+        mbar_init(&raw_empty[i], kConvWarps);
+      }
+    }
+    fence_barrier_init();
+    abort_flag = 0;
+    delivered = 0;
+    *start_seq = -1;
+    piece_slot(0)->n = 0;
+  }
+  if (!Q8 && tid < 2 * (1 + kMaxMaskWords)) odd[tid] = 0u;
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == kProducerWarp && lane == 0) {
+    prefetch_tensormap(&tmap_q);
+    prefetch_tensormap(&tmap_k);
+    prefetch_tensormap(&tmap_v);
+  }
+  // ---- the plan: how many tiles there are, and where this CTA's run begins ----
+  Runs runs;
+  int64_t lo, hi;
+  {
+    int64_t* warp_sum = reinterpret_cast<int64_t*>(smem);  // (before any copy lands there)
+    const int per = (p.num_seqs + kThreads - 1) / kThreads;
+    const int s0 = min(tid * per, p.num_seqs), s1 = min(s0 + per, p.num_seqs);
+    int64_t mine = 0;
+    Seq q;
+    for (int s = s0; s < s1; ++s) {
+      load_seq<GROUP>(p, s, blockIdx.x == 0, q);
+      mine += static_cast<int64_t>(q.tiles) * q.segments;
+    }
+    int64_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += x;
+    }
+    if (lane == 31) warp_sum[warp] = upto;
+    __syncthreads();
+    runs.total = 0;
+    int64_t before = upto - mine;
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) before += warp_sum[i];
+      runs.total += warp_sum[i];
+    }
+    runs.runs = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max((runs.total + kMinRun - 1) / kMinRun, int64_t{1})));
+    const bool any = static_cast<int>(blockIdx.x) < runs.runs;
+    lo = any ? run_start(runs, blockIdx.x) : 0;
+    hi = any ? run_start(runs, blockIdx.x + 1) : 0;
+    if (lo < hi && lo >= before && lo < before + mine) {
+      int64_t off = lo - before;
+      for (int s = s0; s < s1; ++s) {
+        load_seq<GROUP>(p, s, false, q);
+        const int64_t n = static_cast<int64_t>(q.tiles) * q.segments;
+        if (off < n) {
+          *start_seq = s;
+          *start_off = static_cast<int>(off);
+          // the row warps' first two pieces
+          Walk w;
+          w.at = lo;
+          w.end = hi;
+          w.q = q;
+          w.off = static_cast<int>(off);
+          for (int u = 0; u < 2; ++u) {
+            Piece x;
+            if (!next_piece<GROUP>(p, w, x)) x.n = 0;
+            *piece_slot(u) = x;
+          }
+          *row_walk = w;
+          break;
+        }
+        off -= n;
       }
     }
   }
-  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-  const float inv = m == -INFINITY ? 0.f : 1.f / l;
-  reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.out) + w * kHeadDim)[lane] =
-      __floats2bfloat162_rn(o0 * inv, o1 * inv);
+  fence_proxy_async_smem();  // the plan's scratch before copies touch the buffers
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  if (warp < kRowWarps) {
+    // ============================ row warps ============================
+    if (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
+    const int part = warp >> 2;            // keys 64 part .. 64 part + 63 of every tile
+    const int r = (warp & 3) * 32 + lane;  // MMA row == TMEM lane; also a key of the tile, for V
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t s_mine = lane_addr + kSCol + part * (kTileN / 2);
+    const uint32_t s_theirs = lane_addr + kSCol + (part ^ 1) * (kTileN / 2);
+    const uint32_t p_addr = lane_addr + kPCol + part * (kTileN / 4);
+    const uint32_t o_addr = lane_addr + kOCol + part * (kHeadDim / 2);
+    const uint32_t o_theirs = lane_addr + kOCol + (part ^ 1) * (kHeadDim / 2);
+    auto wait_row = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, wait_ready(bar, parity, &abort_flag, p.status));
+    };
+    // this row's mask, and how far into its tile the first drafted key lies
+    auto mask_row = [&](const Piece* u) -> const int32_t* {
+      return p.tree_mask + static_cast<int64_t>(u->q0 + min(u->tok0 + r / GROUP, u->q_len - 1)) * p.mask_words;
+    };
+    auto cur_lead = [&](const Piece* u) -> int { return (u->L - u->q_len) % kTileN; };
+    // Pieces come through shared memory, two ahead, so that the tiles' loop keeps its registers: a warp
+    // looks piece u + 1 up after the row warps met in piece u's epilogue, and its slot was last read in
+    // piece u - 2, which all of them have left by then.
+    auto load_q = [&](int u) {  // by warp 0's lane 0
+      const Piece& x = *piece_slot(u);
+      if (x.n == 0) return;
+      mbar_arrive_expect_tx(q_full, kQBytes);
+      tma_load_3d(sq, &tmap_q, 0, x.g * GROUP, x.q0 + x.tok0, q_full);
+    };
+    if (warp == 0 && lane == 0) load_q(0);
+    bool ok = true;
+    int c = 0;       // tiles so far
+    int units = 0;   // pieces so far
+    int split = 0;   // of them, pieces of split segments
+    int ring = 0, ring_prev = 0;  // stage of this tile and the one before
+    uint32_t ph = 0, ph_prev = 0;
+    for (; ok && piece_slot(units)->n > 0; ++units) {
+      const Piece* const cur = piece_slot(units);
+      const int n = cur->n;
+      const int tail_j = (cur->L - cur->q_len) / kTileN - cur->j0;  // from here on tiles hold drafted keys
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j, ++c) {
+        if (!(ok = wait_row(s_full, static_cast<uint32_t>(c & 1)))) break;
+        tc_fence_after_sync();
+        // the piece's last scores are done with Q: the next piece's may land there
+        if (j == n - 1 && warp == 0 && lane == 0) load_q(units + 1);
+        uint32_t v[2][32];
+        float top[kBlocksPerTile];  // largest raw score of each block, the partner's first
+#pragma unroll
+        for (int b = 0; b < kBlocksPerTile / 2; ++b)
+          tmem_ld16_max(s_theirs + 16 * b, &v[b >> 1][16 * (b & 1)], top[b]);
+        tmem_wait_ld();
+        const bool tail = j >= tail_j;  // (uniform)
+        if (tail) {
+          const int32_t* bits = mask_row(cur);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t seen =
+                seen_bits(bits, cur->q_len, (j - tail_j) * kTileN + (part ^ 1) * (kTileN / 2) + 32 * h - cur_lead(cur));
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              float x = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if ((seen >> (16 * b + i)) & 1u) x = fmaxf(x, __uint_as_float(v[h][16 * b + i]));
+              top[2 * h + b] = x;
+            }
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < kBlocksPerTile / 2; ++b)
+          tmem_ld16_max(s_mine + 16 * b, &v[b >> 1][16 * (b & 1)], top[kBlocksPerTile / 2 + b]);
+        tmem_wait_ld();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_free);
+        if (tail) {
+          const int32_t* bits = mask_row(cur);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t seen =
+                seen_bits(bits, cur->q_len, (j - tail_j) * kTileN + part * (kTileN / 2) + 32 * h - cur_lead(cur));
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              float x = -INFINITY;
+#pragma unroll
+              for (int i = 16 * b; i < 16 * b + 16; ++i) {
+                if (!((seen >> i) & 1u)) v[h][i] = __float_as_uint(-INFINITY);
+                x = fmaxf(x, __uint_as_float(v[h][i]));
+              }
+              top[kBlocksPerTile / 2 + 2 * h + b] = x;
+            }
+          }
+          if (!Q8) {
+            // V rows past the context weigh nothing but may hold anything, and so may drafted values
+            // that some row does not see: this thread looks at half of row r of the tile
+            if (!(ok = wait_row(&kv_full[ring], ph))) break;
+            const int key = (j - tail_j) * kTileN + r - cur_lead(cur);  // of the drafted ones
+            if (key >= 0) {
+              uint32_t* const my_odd = odd + (units & 1) * (1 + kMaxMaskWords);
+              uint32_t any = 0u;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint4* x = reinterpret_cast<uint4*>(sv + ring * kOpBytes + swz(r, 4 * part + i));
+                if (key >= cur->q_len) {
+                  *x = make_uint4(0u, 0u, 0u, 0u);
+                } else {
+                  uint4 y = *x;
+                  const uint4 z = make_uint4(odd_halves(y.x), odd_halves(y.y), odd_halves(y.z), odd_halves(y.w));
+                  if ((z.x | z.y | z.z | z.w) != 0u) {
+                    any = 1u;
+                    *x = make_uint4(y.x & ~z.x, y.y & ~z.y, y.z & ~z.z, y.w & ~z.w);
+                  }
+                }
+              }
+              if (any != 0u) {
+                atomicOr(my_odd + 1 + (key >> 5), 1u << (key & 31));
+                atomicOr(my_odd, 1u);
+              }
+            }
+            fence_proxy_async_smem();
+          }
+        }
+        float f[kBlocksPerTile / 2] = {};  // score factors of this thread's blocks (8-bit pools)
+        float mt;
+        const uint32_t cs = smem_addr(consts + c % kConstRing * kConsts);
+        if (Q8) {
+          float g[kBlocksPerTile / 2];  // the partner's
+          lds_f32x4(cs + 4 * part * (kBlocksPerTile / 2), f);
+          lds_f32x4(cs + 4 * (part ^ 1) * (kBlocksPerTile / 2), g);
+          mt = -INFINITY;
+#pragma unroll
+          for (int b = 0; b < kBlocksPerTile / 2; ++b) {
+            f[b] = fmaxf(f[b] * p.qk_scale, 1.17549435e-38f);  // (a hidden key's -inf * 0 is a NaN)
+            g[b] = fmaxf(g[b] * p.qk_scale, 1.17549435e-38f);
+            mt = max3f(mt, top[kBlocksPerTile / 2 + b] * f[b], top[b] * g[b]);
+          }
+        } else {
+          mt = max3f(max3f(top[0], top[1], top[2]), max3f(top[3], top[4], top[5]), fmaxf(top[6], top[7])) * p.qk_scale;
+        }
+        const bool grow = mt > m;  // true on the first tile in which the row sees a key
+        float alpha = 1.f;
+        if (grow) {
+          alpha = fast_exp2(m - (mt + kHeadroom));
+          m = mt + kHeadroom;
+        }
+        l *= alpha;
+        const float ref = m == -INFINITY ? 0.f : m;  // a row that has seen no key yet: weights of 0
+        float factor = p.qk_scale;
+        if (__any_sync(0xffffffffu, fabsf(ref) > kLargeScore)) {
+          // score x factor has to be rounded as it was for the maximum, or the fused form below would leave
+          // the rounding of a large product, whole powers of two, in the exponent
+#pragma unroll
+          for (int i = 0; i < kTileN / 2; ++i) {
+            float& x = reinterpret_cast<float&>(v[i >> 5][i & 31]);
+            x = __fmul_rn(x, Q8 ? f[i / kBlockSize] : factor);
+          }
+          factor = 1.f;
+#pragma unroll
+          for (int b = 0; b < kBlocksPerTile / 2; ++b) f[b] = 1.f;
+        }
+        if (Q8) {
+          float lf[kBlocksPerTile / 2];
+          lds_f32x4(cs + 4 * (kBlocksPerTile + part * (kBlocksPerTile / 2)), lf);
+#pragma unroll
+          for (int b = 0; b < kBlocksPerTile / 2; ++b) {
+            const float nb = lf[b] - ref;
+            const float2 fb = make_float2(f[b], f[b]), nb2 = make_float2(nb, nb);
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kBlockSize / 2; ++i) {
+              const int e = b * kBlockSize + 2 * i;
+              const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[e >> 5][e & 31]),
+                                                      __uint_as_float(v[e >> 5][(e & 31) + 1])), fb, nb2);
+              const float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+              sum = __fadd2_rn(sum, y);
+              v[0][e >> 1] = pack_bf2(y.x, y.y);
+            }
+            l += (sum.x + sum.y) * lds_f32(cs + 4 * (2 * kBlocksPerTile + part * (kBlocksPerTile / 2) + b));
+          }
+        } else {
+          const float2 fb = make_float2(factor, factor), nb2 = make_float2(-ref, -ref);
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < kTileN / 4; ++i) {
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[i >> 4][(2 * i) & 31]),
+                                                    __uint_as_float(v[i >> 4][(2 * i + 1) & 31])), fb, nb2);
+            const float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            sum = __fadd2_rn(sum, y);
+            v[0][i] = pack_bf2(y.x, y.y);
+          }
+          l += sum.x + sum.y;
+        }
+        if (c > 0) {  // the previous P V: P's columns are free and O is up to date
+          if (!(ok = wait_row(&pv_done[ring_prev], ph_prev))) break;
+          tc_fence_after_sync();
+        }
+        tmem_st32(p_addr, v[0]);
+        if (j > 0 && __any_sync(0xffffffffu, grow)) {
+          const float2 a2 = make_float2(alpha, alpha);
+          uint32_t(&o)[32] = v[1];  // this thread's 32 columns of O
+          tmem_ld32(o_addr, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 x = __fmul2_rn(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), a2);
+            o[2 * i] = __float_as_uint(x.x);
+            o[2 * i + 1] = __float_as_uint(x.y);
+          }
+          tmem_st32(o_addr, o);
+        }
+        tmem_wait_st();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+        if (j == 0 && warp == 0 && lane == 0) {
+          Walk w = *row_walk;
+          Piece x;
+          if (!next_piece<GROUP>(p, w, x)) x.n = 0;
+          *piece_slot(units + 2) = x;
+          *row_walk = w;
+        }
+        ring_prev = ring;
+        ph_prev = ph;
+        if (++ring == kRing) {
+          ring = 0;
+          ph ^= 1u;
+        }
+      }
+      if (!ok) break;
+      // ---- epilogue: this thread's 32 dims ----
+      if (!(ok = wait_row(&pv_done[ring_prev], ph_prev))) break;
+      tc_fence_after_sync();
+      uint32_t o[32];
+      tmem_ld32(o_addr, o);
+      tmem_wait_ld();
+      // the two sums of a row meet over O's columns, which nothing writes before o_free
+      tmem_st1(o_addr, __float_as_uint(l));
+      tmem_wait_st();
+      tc_fence_before_sync();
+      // (the other buffer of odd tokens was last read before every warp's last P: clear it for the next)
+      if (!Q8 && tid == 0) {
+        uint32_t* other = odd + ((units & 1) ^ 1) * (1 + kMaxMaskWords);
+        if (other[0] != 0u)
+          for (int i = 0; i <= kMaxMaskWords; ++i) other[i] = 0u;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(l_bar);
+      if (!(ok = wait_row(l_bar, static_cast<uint32_t>(units & 1)))) break;
+      tc_fence_after_sync();
+      const float l_theirs = __uint_as_float(tmem_ld1(o_theirs));
+      tmem_wait_ld();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free);
+      l = part ? l_theirs + l : l + l_theirs;
+      const uint32_t* const my_odd = odd + (units & 1) * (1 + kMaxMaskWords);
+      if (!Q8 && *const_cast<const volatile uint32_t*>(my_odd) != 0u) {
+        // drafted values that are no numbers go to the rows that see them, and to no other
+        const int32_t* table = p.block_tables + static_cast<int64_t>(cur->s) * p.max_blocks_per_seq;
+        const int32_t* bits = mask_row(cur);
+        for (int i = 0; 32 * i < cur->q_len; ++i) {
+          uint32_t w = my_odd[1 + i] & mask_word(bits, cur->q_len, i);
+          while (w != 0u) {
+            const int pos = cur->L - cur->q_len + 32 * i + __ffs(w) - 1;
+            w &= w - 1u;
+            const int32_t b = __ldg(table + pos / kBlockSize);
+            if (b < 0 || b >= p.num_blocks) continue;
+            const uint4* x = reinterpret_cast<const uint4*>(
+                p.value_cache + ((static_cast<int64_t>(b) * p.num_kv_heads + cur->g) * kBlockSize + pos % kBlockSize) *
+                                    kHeadDim + part * (kHeadDim / 2));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint4 y = __ldg(x + k);
+              const uint32_t z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 g = bf16x2_to_float2(z[e] & odd_halves(z[e]));
+                o[8 * k + 2 * e] = __float_as_uint(__uint_as_float(o[8 * k + 2 * e]) + g.x);
+                o[8 * k + 2 * e + 1] = __float_as_uint(__uint_as_float(o[8 * k + 2 * e + 1]) + g.y);
+              }
+            }
+          }
+        }
+      }
+      const bool row_ok = cur->tok0 + r / GROUP < cur->q_len;
+      bool write = n == cur->tiles;
+      if (!write) {
+        // ---- a piece of a split segment: its record, and whoever comes last weighs them all ----
+        const int from = run_of(runs, cur->first), to = run_of(runs, cur->first + cur->tiles - 1);
+        if (row_ok) {
+          float4* rec = p.records + (2ll * blockIdx.x + (cur->j0 == 0 ? 1 : 0)) * kRecordFloat4s + r;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            rec[(8 * part + i) * kTileM] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                       __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+          if (part == 0) rec[(kRecordChunks - 1) * kTileM] = make_float4(m, l, 0.f, 0.f);
+        }
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(piece_bar);
+        if (warp == 0 && lane == 0) {
+          if (wait_ready(piece_bar, static_cast<uint32_t>(split & 1), &abort_flag, p.status)) {
+            __threadfence();
+            const int before = atomicAdd(p.counters + from, 1);
+            is_last = before == to - from;
+            delivered = split + 1;
+            if (before == to - from) p.counters[from] = 0;
+            __threadfence();
+            mbar_arrive(last_bar);
+          }
+        }
+        __syncwarp();
+        if (!(ok = wait_row(last_bar, static_cast<uint32_t>(split & 1)))) break;
+        ++split;
+        write = is_last != 0;
+        if (write) {
+          __threadfence();
+          float top_m = -INFINITY;
+          auto record = [&](int k) {
+            return p.records + (2ll * (from + k) + (k == 0 ? 1 : 0)) * kRecordFloat4s + r;
+          };
+          const int pieces = row_ok ? to - from + 1 : 0;
+          for (int k = 0; k < pieces; ++k) top_m = fmaxf(top_m, __ldcg(record(k) + (kRecordChunks - 1) * kTileM).x);
+          const float at = top_m == -INFINITY ? 0.f : top_m;
+          float acc[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+          l = 0.f;
+          for (int k = 0; k < pieces; ++k) {
+            const float4* rec = record(k);
+            const float4 ml = __ldcg(rec + (kRecordChunks - 1) * kTileM);
+            float4 x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __ldcg(rec + (8 * part + i) * kTileM);
+            const float w = fast_exp2(ml.x - at);
+            l += w * ml.y;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              acc[4 * i] += w * x[i].x;
+              acc[4 * i + 1] += w * x[i].y;
+              acc[4 * i + 2] += w * x[i].z;
+              acc[4 * i + 3] += w * x[i].w;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(acc[i]);
+        }
+      }
+      if (write) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        // Four lanes exchange what they hold (four rows by four 16-byte chunks), so that each store covers
+        // 64 bytes of eight rows.
+        uint4 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = make_uint4(pack_bf2(__uint_as_float(o[8 * i]) * inv, __uint_as_float(o[8 * i + 1]) * inv),
+                            pack_bf2(__uint_as_float(o[8 * i + 2]) * inv, __uint_as_float(o[8 * i + 3]) * inv),
+                            pack_bf2(__uint_as_float(o[8 * i + 4]) * inv, __uint_as_float(o[8 * i + 5]) * inv),
+                            pack_bf2(__uint_as_float(o[8 * i + 6]) * inv, __uint_as_float(o[8 * i + 7]) * inv));
+        swap_chunks(w[0], w[1], lane & 1, 1);
+        swap_chunks(w[2], w[3], lane & 1, 1);
+        swap_chunks(w[0], w[2], lane & 2, 2);
+        swap_chunks(w[1], w[3], lane & 2, 2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = (r & ~3) + i;
+          if (cur->tok0 + rr / GROUP < cur->q_len)
+            *reinterpret_cast<uint4*>(
+                p.out + (static_cast<int64_t>(cur->q0 + cur->tok0 + rr / GROUP) * p.num_q_heads + cur->g * GROUP +
+                         rr % GROUP) * kHeadDim + part * (kHeadDim / 2) + 8 * (lane & 3)) = w[i];
+        }
+      }
+    }
+    // leave no copy in flight: the next piece's Q, if one was given up on
+    if (warp == 0 && lane == 0 && !ok) {
+      for (int u = 0; u < 2; ++u) {  // (piece `units` was asked for at the latest, and perhaps the one after)
+        if (piece_slot(units + u)->n > 0) mbar_wait(q_full, static_cast<uint32_t>((units + u) & 1));
+      }
+      flag_error(p.status, PA_DEVFLAG_TIMEOUT);
+    }
+  } else {
+    if (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    Walk walk;
+    walk.at = lo;
+    walk.end = *start_seq >= 0 ? hi : lo;
+    walk.off = *start_off;
+    if (walk.at < walk.end) load_seq<GROUP>(p, *start_seq, false, walk.q);
+    if (warp == kMmaWarp) {
+      // ============================ MMA issuer ============================
+      // The whole warp walks the tiles, so that barriers, counters and descriptors stay uniform; one
+      // elected lane issues.  Order: S(0), S(1), PV(0), S(2), PV(1), ... over the tiles of all pieces.
+      constexpr uint32_t kIdescS = idesc_bf16_f32(kTileM, kTileN, false);
+      constexpr uint32_t kIdescO = idesc_bf16_f32(kTileM, kHeadDim, true);
+      const bool leader = elect_one();
+      const uint64_t q_desc = sw128_desc(smem_addr(sq), 16, 1024);
+      const uint64_t k_desc0 = sw128_desc(smem_addr(sk), 16, 1024);
+      const uint64_t v_desc0 = sw128_desc(smem_addr(sv), 16, 1024);
+      constexpr uint64_t kStageStep = kOpBytes >> 4;  // of a descriptor's start address
+      int s_issued = 0, pv_issued = 0, units_s = 0, units_o = 0;
+      int ks = 0, vs = 0;
+      uint32_t kph = 0, vph = 0;
+      auto issue_s = [&](bool first) -> bool {
+        if (!wait_ready(&kv_full[ks], kph, &abort_flag, p.status)) return false;
+        if (first) {
+          if (!wait_ready(q_full, static_cast<uint32_t>(units_s & 1), &abort_flag, p.status)) return false;
+          ++units_s;
+        }
+        if (s_issued > 0 &&
+            !wait_ready(s_free, static_cast<uint32_t>((s_issued - 1) & 1), &abort_flag, p.status))
+          return false;
+        tc_fence_after_sync();
+        const uint64_t k_desc = k_desc0 + kStageStep * ks;
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < kHeadDim / 16; ++kk)
+            umma_bf16(tmem + kSCol, q_desc + 2 * kk, k_desc + 2 * kk, kIdescS, kk > 0 ? 1u : 0u);
+          umma_commit(s_full);
+          if (Q8) {
+            mbar_arrive(s_full);  // passes on what the converters wrote before their arrivals (the constants)
+            umma_commit(&k_empty[ks]);
+          }
+        }
+        ++s_issued;
+        if (++ks == kRing) {
+          ks = 0;
+          kph ^= 1u;
+        }
+        return true;
+      };
+      auto issue_pv = [&](bool first) -> bool {
+        if (Q8 && !wait_ready(&v_full[vs], vph, &abort_flag, p.status)) return false;
+        if (!wait_ready(p_full, static_cast<uint32_t>(pv_issued & 1), &abort_flag, p.status)) return false;
+        if (first) {  // O starts anew: the previous piece's has been read out
+          if (units_o > 0 && !wait_ready(o_free, static_cast<uint32_t>((units_o - 1) & 1), &abort_flag, p.status))
+            return false;
+          ++units_o;
+        }
+        tc_fence_after_sync();
+        const uint64_t v_desc = v_desc0 + kStageStep * vs;
+        if (leader) {
+          umma_bf16_ts(tmem + kOCol, tmem + kPCol, v_desc, kIdescO, first ? 0u : 1u);
+#pragma unroll
+          for (int kk = 1; kk < kTileN / 16; ++kk)  // 16 keys: 2 KiB of V, 8 columns of P
+            umma_bf16_ts(tmem + kOCol, tmem + kPCol + kk * 8, v_desc + 128 * kk, kIdescO, 1u);
+          umma_commit(&pv_done[vs]);
+        }
+        ++pv_issued;
+        if (++vs == kRing) {
+          vs = 0;
+          vph ^= 1u;
+        }
+        return true;
+      };
+      Piece cur, nxt;
+      bool have = next_piece<GROUP>(p, walk, cur);
+      bool have_next = have && next_piece<GROUP>(p, walk, nxt);
+      bool ok = have && issue_s(true);
+      while (ok && have) {
+        const int n = cur.n;
+        for (int j = 0; ok && j < n; ++j) {
+          const bool last = j + 1 == n;
+          if (!last || have_next) ok = issue_s(last);
+          if (ok) ok = issue_pv(j == 0);
+        }
+        cur = nxt;
+        have = have_next;
+        if (have) have_next = next_piece<GROUP>(p, walk, nxt);
+      }
+      // wait (bounded) until every MMA issued above has completed
+      if (leader) {
+        umma_commit(drain);
+        if (!mbar_wait(drain, 0)) flag_error(p.status, PA_DEVFLAG_TIMEOUT);
+      }
+      __syncwarp();
+    } else if (warp == kProducerWarp) {
+      // ============================ producer ============================
+      const bool leader = elect_one();
+      Piece cur;
+      bool ok = true;
+      int jt = 0;
+      constexpr int kStages = Q8 ? kRawRing : kRing;
+      uint64_t* const full = Q8 ? raw_full : kv_full;
+      uint64_t* const empty = Q8 ? raw_empty : pv_done;
+      while (ok && next_piece<GROUP>(p, walk, cur)) {
+        const int32_t* row = p.block_tables + static_cast<int64_t>(cur.s) * p.max_blocks_per_seq;
+        const int blocks = (cur.L + kBlockSize - 1) / kBlockSize;
+        // 32 table entries (four tiles) at a time, one per lane, the next window in flight
+        int win_base = cur.j0 * kBlocksPerTile;
+        auto fetch = [&](int base) -> int32_t { return base + lane < blocks ? __ldg(row + base + lane) : 0; };
+        int32_t win = fetch(win_base);
+        int32_t win_next = fetch(win_base + 32);
+        for (int j = 0; j < cur.n; ++j, ++jt) {
+          const int st = jt % kStages;
+          const int lb0 = (cur.j0 + j) * kBlocksPerTile;
+          if (lb0 >= win_base + 32) {
+            win_base += 32;
+            win = win_next;
+            win_next = fetch(win_base + 32);
+          }
+          const bool need = lane < kBlocksPerTile && lb0 + lane < blocks;
+          const int32_t entry = __shfl_sync(0xffffffffu, win, (lb0 - win_base) + (lane & (kBlocksPerTile - 1)));
+          const bool bad = need && (entry < 0 || entry >= p.num_blocks);
+          if (__any_sync(0xffffffffu, bad) && lane == 0) flag_error(p.status, PA_DEVFLAG_BAD_BLOCK);
+          ok = wait_ready(&empty[st], static_cast<uint32_t>((jt / kStages) & 1) ^ 1u, &abort_flag, p.status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (Q8) {
+            // tile (row) of each block; one that is not needed, or bad, brings the pool's first
+            const int32_t tile = need && !bad ? entry * p.num_kv_heads + cur.g : 0;
+            int32_t rows[kBlocksPerTile];
+#pragma unroll
+            for (int b = 0; b < kBlocksPerTile; ++b) rows[b] = __shfl_sync(0xffffffffu, tile, b);
+            if (leader) {
+              mbar_arrive_expect_tx(&full[st], kRawBytes);
+              uint8_t* dst = sraw + st * kRawBytes;
+#pragma unroll
+              for (int b = 0; b < kBlocksPerTile; b += 4) {
+                gather4(dst + b * kQ8TileBytes, &tmap_k, &rows[b], &full[st]);
+                gather4(dst + (kBlocksPerTile + b) * kQ8TileBytes, &tmap_v, &rows[b], &full[st]);
+              }
+            }
+            if (lane < kBlocksPerTile) {
+              float* s = raw_scale + st * 2 * kBlocksPerTile + lane;
+              async_copy4(s, p.key_scale + tile);
+              async_copy4(s + kBlocksPerTile, p.value_scale + tile);
+              async_arrive(&full[st]);
+            }
+          } else {
+            const bool load = need && !bad;
+            const unsigned mask = __ballot_sync(0xffffffffu, load);
+            if (lane == 0) mbar_arrive_expect_tx(&full[st], __popc(mask) * 2u * kTileBytes);
+            __syncwarp();
+            if (load) {
+              const int y = (entry * p.num_kv_heads + cur.g) * kBlockSize;
+              tma_load_2d(sk + st * kOpBytes + lane * kTileBytes, &tmap_k, 0, y, &full[st]);
+              tma_load_2d(sv + st * kOpBytes + lane * kTileBytes, &tmap_v, 0, y, &full[st]);
+            }
+          }
+        }
+      }
+      // leave no copy in flight: wait (bounded) for the last fill of each stage
+      if (Q8) asm volatile("cp.async.wait_all;" ::: "memory");
+      if (lane == 0) {
+        for (int st = 0; st < kStages && st < jt; ++st) {
+          const int last = st + ((jt - 1 - st) / kStages) * kStages;
+          if (!mbar_wait(&full[st], static_cast<uint32_t>((last / kStages) & 1)))
+            flag_error(p.status, PA_DEVFLAG_TIMEOUT);
+        }
+      }
+      __syncwarp();
+    } else {
+      // ============================ converters (8-bit pools) ============================
+      constexpr int kMyBlocks = kBlocksPerTile / kConvWarps;  // blocks kMyBlocks cw .. of every tile
+      const int cw = warp - kConvWarp0;
+      const int row0 = cw * kMyBlocks * kBlockSize + (lane >> 2);
+      const int c0 = 2 * (lane & 3);  // 16 codes of a row: two 16-byte chunks
+      int st = 0, rs = 0, slot = 0;   // operand stage, stage of codes
+      uint32_t ph = 0, rph = 0;
+      Piece cur;
+      bool ok = true;
+      while (ok && next_piece<GROUP>(p, walk, cur)) {
+        const int blocks = (cur.L + kBlockSize - 1) / kBlockSize;
+        for (int j = 0; j < cur.n; ++j) {
+          ok = wait_ready(&raw_full[rs], rph, &abort_flag, p.status) &&
+               wait_ready(&k_empty[st], ph ^ 1u, &abort_flag, p.status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          const float* scales = raw_scale + rs * 2 * kBlocksPerTile + kMyBlocks * cw;
+          uint32_t my_m = 0u;  // lane b: 2^(120 + e) of block b's value scale, a bf16 pair
+          int my_high = 0;     // e where 120 + e is beyond bf16: then my_m is 2^120
+          if (lane < kMyBlocks) {
+            const bool needed = (cur.j0 + j) * kBlocksPerTile + kMyBlocks * cw + lane < blocks;
+            const float value = needed ? scales[kBlocksPerTile + lane] : 1.f;
+            const uint32_t bits = __float_as_uint(value) & 0x7fffffffu;
+            const int e = static_cast<int>(bits >> 23) - 127;
+            if (e > -127) {
+              my_high = e > 7 ? min(e, 127) : 0;
+              my_m = bf2_power(e > 7 ? 120 : 120 + e);
+            } else if (bits != 0u) {  // below the normal floats: e = -118 - clz
+              my_m = bf2_power(2 - __clz(bits));
+            }
+            // the row warps' constants of this warp's blocks
+            const float f = significand(value);
+            float lf = 0.f, fi = 1.f;
+            if (f != 1.f) {
+              lf = __log2f(f);
+              fi = 1.f / f;
+            }
+            float* cs = consts + slot * kConsts + kMyBlocks * cw + lane;
+            cs[0] = needed ? scales[lane] : 1.f;
+            cs[kBlocksPerTile] = lf;
+            cs[2 * kBlocksPerTile] = fi;
+          }
+          const bool any_high = __any_sync(0xffffffffu, my_high != 0);
+          const uint8_t* raw = sraw + rs * kRawBytes + cw * kMyBlocks * kQ8TileBytes + 16 * lane;
+          const uint32_t up = bf2_power(120);
+          uint8_t* dst = sk + st * kOpBytes;
+#pragma unroll
+          for (int i = 0; i < 2 * kMyBlocks; ++i) {
+            const uint4 w = lds128(raw + i * 512);
+            uint4 a, b;
+            codes4_to_bf2x2(w.x, a.x, a.y);
+            codes4_to_bf2x2(w.y, a.z, a.w);
+            codes4_to_bf2x2(w.z, b.x, b.y);
+            codes4_to_bf2x2(w.w, b.z, b.w);
+            a.x = mul_bf2(a.x, up); a.y = mul_bf2(a.y, up); a.z = mul_bf2(a.z, up); a.w = mul_bf2(a.w, up);
+            b.x = mul_bf2(b.x, up); b.y = mul_bf2(b.y, up); b.z = mul_bf2(b.z, up); b.w = mul_bf2(b.w, up);
+            *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * i, c0)) = a;
+            *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * i, c0 + 1)) = b;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&kv_full[st]);
+          ok = wait_ready(&pv_done[st], ph ^ 1u, &abort_flag, p.status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          dst = sv + st * kOpBytes;
+          const int keys_left = cur.L - (cur.j0 + j) * kTileN - row0;
+          raw += kTileN * kQ8RowBytes;
+#pragma unroll
+          for (int i = 0; i < 2 * kMyBlocks; ++i) {
+            uint4 w = lds128(raw + i * 512);
+            // keys past the context weigh nothing, but may hold anything
+            if (8 * i >= keys_left) w = make_uint4(0u, 0u, 0u, 0u);
+            uint4 a, b;
+            codes4_to_bf2x2(w.x, a.x, a.y);
+            codes4_to_bf2x2(w.y, a.z, a.w);
+            codes4_to_bf2x2(w.z, b.x, b.y);
+            codes4_to_bf2x2(w.w, b.z, b.w);
+            const uint32_t m0 = __shfl_sync(0xffffffffu, my_m, i >> 1);
+            a.x = mul_bf2(a.x, m0); a.y = mul_bf2(a.y, m0); a.z = mul_bf2(a.z, m0); a.w = mul_bf2(a.w, m0);
+            b.x = mul_bf2(b.x, m0); b.y = mul_bf2(b.y, m0); b.z = mul_bf2(b.z, m0); b.w = mul_bf2(b.w, m0);
+            if (any_high) {  // a scale above 2^7: the rest of it
+              const uint32_t m1 = bf2_power(__shfl_sync(0xffffffffu, my_high, i >> 1));
+              a.x = mul_bf2(a.x, m1); a.y = mul_bf2(a.y, m1); a.z = mul_bf2(a.z, m1); a.w = mul_bf2(a.w, m1);
+              b.x = mul_bf2(b.x, m1); b.y = mul_bf2(b.y, m1); b.z = mul_bf2(b.z, m1); b.w = mul_bf2(b.w, m1);
+            }
+            *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * i, c0)) = a;
+            *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * i, c0 + 1)) = b;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&v_full[st]);
+            mbar_arrive(&raw_empty[rs]);
+          }
+          if (++st == kRing) {
+            st = 0;
+            ph ^= 1u;
+          }
+          if (++rs == kRawRing) {
+            rs = 0;
+            rph ^= 1u;
+          }
+          slot = (slot + 1) % kConstRing;
+        }
+      }
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+  if (abort_flag != 0 && tid == 0 && *start_seq >= 0) {
+    // the counters come back to zero all the same: pieces that were not delivered count as if
+    Walk w;
+    w.at = lo;
+    w.end = hi;
+    w.off = *start_off;
+    load_seq<GROUP>(p, *start_seq, false, w.q);
+    Piece u;
+    int n = 0;
+    while (next_piece<GROUP>(p, w, u)) {
+      if (u.n == u.tiles || n++ < delivered) continue;
+      const int from = run_of(runs, u.first), to = run_of(runs, u.first + u.tiles - 1);
+      if (atomicAdd(p.counters + from, 1) == to - from) p.counters[from] = 0;
+    }
+  }
+}
+
+constexpr size_t record_bytes(int ctas) { return static_cast<size_t>(ctas) * 2 * kRecordFloat4s * 16; }
+constexpr size_t counter_bytes(int ctas) { return (static_cast<size_t>(ctas) * 4 + 255) / 256 * 256; }
+
+cudaError_t device_sms(int* dev, int* sms) {
+  cudaError_t e = cudaGetDevice(dev);
+  return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
+}
+
+template <int GROUP, bool Q8>
+cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
+  using Lay = Layout<Q8>;
+  static bool ready[kMaxDevices] = {};  // benign race: the calls are idempotent
+  int dev = 0, sms = 0;
+  cudaError_t e = device_sms(&dev, &sms);
+  if (e != cudaSuccess) return e;
+  auto kernel = tree_kernel<GROUP, Q8>;
+  if (dev >= kMaxDevices || !ready[dev]) {
+    if (Q8) {
+      cudaFuncAttributes attr;
+      if ((e = cudaFuncGetAttributes(&attr, kernel)) != cudaSuccess) return e;
+      // setmaxnreg waits for registers the launch never had: refuse instead
+      if (attr.numRegs * Lay::kThreads < kRowThreads * kRowRegs + (Lay::kThreads - kRowThreads) * kOtherRegs)
+        return cudaErrorInvalidConfiguration;
+    }
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kBytes);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDevices) ready[dev] = true;
+  }
+  CUtensorMap tq, tk, tv;
+  if (!encode_query_tiles(&tq, a.q, static_cast<uint64_t>(a.num_query_tokens), a.num_q_heads, GROUP, kTileM / GROUP))
+    return cudaErrorInvalidValue;
+  const uint64_t tiles = static_cast<uint64_t>(a.num_blocks) * a.num_kv_heads;
+  const bool maps = Q8 ? encode_tile_rows(&tk, a.key_cache, tiles) && encode_tile_rows(&tv, a.value_cache, tiles)
+                       : encode_pool_rows(&tk, a.key_cache, tiles * kBlockSize, kBlockSize) &&
+                             encode_pool_rows(&tv, a.value_cache, tiles * kBlockSize, kBlockSize);
+  if (!maps) return cudaErrorInvalidValue;
+  TreeParams p;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.tree_mask = a.tree_mask;
+  p.query_start_loc = a.query_start_loc;
+  p.block_tables = a.block_tables;
+  p.context_lens = a.context_lens;
+  p.value_cache = static_cast<const __nv_bfloat16*>(a.value_cache);
+  p.key_scale = a.key_scale;
+  p.value_scale = a.value_scale;
+  p.counters = static_cast<int32_t*>(a.workspace);
+  p.records = reinterpret_cast<float4*>(static_cast<uint8_t*>(a.workspace) + counter_bytes(2 * sms));
+  p.status = a.status;
+  p.mask_words = a.mask_words;
+  p.max_blocks_per_seq = a.max_blocks_per_seq;
+  p.num_blocks = a.num_blocks;
+  p.num_kv_heads = a.num_kv_heads;
+  p.num_q_heads = a.num_q_heads;
+  p.num_query_tokens = a.num_query_tokens;
+  p.max_query_len = a.max_query_len;
+  p.num_seqs = a.num_seqs;
+  p.qk_scale = a.scale * 1.4426950408889634f;
+  tree_kernel<GROUP, Q8><<<2 * sms, Lay::kThreads, Lay::kBytes, stream>>>(tq, tk, tv, p);
+  return cudaGetLastError();
+}
+
+template <bool Q8>
+cudaError_t launch_group(const TreeArgs& a, cudaStream_t stream) {
+  switch (a.num_q_heads / a.num_kv_heads) {
+    case 1: return launch<1, Q8>(a, stream);
+    case 2: return launch<2, Q8>(a, stream);
+    case 4: return launch<4, Q8>(a, stream);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace
 
-size_t tree_workspace_size() { return 16; }
-
-cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream) {
-  const int64_t warps = static_cast<int64_t>(a.num_query_tokens) * a.num_q_heads;
-  tree_kernel<false><<<static_cast<unsigned>((warps + kWarps - 1) / kWarps), kWarps * 32, 0, stream>>>(a);
-  return cudaGetLastError();
+size_t tree_workspace_size() {
+  int dev = 0, sms = 0;
+  if (device_sms(&dev, &sms) != cudaSuccess) return 0;
+  return counter_bytes(2 * sms) + record_bytes(2 * sms);
 }
 
-cudaError_t launch_tree_q8(const TreeArgs& a, cudaStream_t stream) {
-  const int64_t warps = static_cast<int64_t>(a.num_query_tokens) * a.num_q_heads;
-  tree_kernel<true><<<static_cast<unsigned>((warps + kWarps - 1) / kWarps), kWarps * 32, 0, stream>>>(a);
-  return cudaGetLastError();
-}
+cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream) { return launch_group<false>(a, stream); }
+cudaError_t launch_tree_q8(const TreeArgs& a, cudaStream_t stream) { return launch_group<true>(a, stream); }
 
 }  // namespace pkv
