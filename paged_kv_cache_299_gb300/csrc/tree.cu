@@ -8,10 +8,12 @@
 // GB300 design.  The rows are few and the keys many: what counts is to stream K and V past 128 MMA rows
 // (128 / GROUP tokens x GROUP heads that share a K/V head) on every SM, whatever the batch looks like.
 //   * The work is a row of 128-key tiles: all tiles of all (sequence, K/V head, query tile) segments, one
-//     after the other.  It is cut into equal runs, one per CTA of a persistent grid of two CTAs per SM;
-//     a CTA serves its run's pieces of segments back to back.  A segment that one CTA serves whole goes
-//     straight to the output; pieces of a split one are kept in fp32 (sum, maximum, weight) in the
-//     workspace, and the CTA that finishes last weighs them together, in the pieces' order.
+//     after the other, for a persistent grid of two CTAs per SM.  Where there are CTAs enough, every
+//     segment gets CTAs of its own, as many as bring the longest piece down; otherwise, or where lengths are
+//     so uneven that equal shares win, the row is cut into equal runs, one per CTA, that begin and end
+//     inside segments.  A segment that one CTA serves whole goes straight to the output; pieces of a split
+//     one are kept in fp32 (sum, maximum, weight) in the workspace, and the warp that finishes last for its
+//     rows weighs them together, in the pieces' order.
 //   * Two CTAs per SM, because a tile's chain (scores, softmax, product) is latency: 128 keys a tile
 //     amortise it, two chains fill in for each other.
 //   * Tensor memory (256 columns): scores S 128, P 64 (bf16 pairs), O 64.  P has columns of its own, so
@@ -56,9 +58,11 @@ constexpr uint32_t kTmemCols = 256;
 constexpr uint32_t kSCol = 0, kPCol = 128, kOCol = 192;
 constexpr float kHeadroom = 8.0f;  // the reference of the exponents lies this far (log2) above the maximum
 constexpr float kLargeScore = 131072.f;  // 2^17: a rounding of the score (log2 units) is then 2^-7
-constexpr int kRecordChunks = kHeadDim / 4 + 1;  // float4s of a row: its sum, then maximum and weight
-constexpr int kRecordFloat4s = kRecordChunks * kTileM;
-constexpr int kMinRun = 2;  // tiles of a run, at least
+constexpr int kPartChunks = kHeadDim / 8 + 1;  // float4s of a row for each half of the dims: sum; maximum, weight
+constexpr int kRecordFloat4s = 2 * kPartChunks * kTileM;
+constexpr int kMinPiece = 4;      // tiles of a piece of a split segment, at least
+constexpr int kSplitTiles = 5;    // what meeting costs, in tiles: equal runs begin to pay beyond it
+constexpr int kMaxDealtSeqs = 1024;  // sequences whose segments may get CTAs of their own
 // Register split of the 8-bit kernel (setmaxnreg): what the CTA was launched with, 80 for each of 384 threads.
 constexpr int kRowRegs = 96, kOtherRegs = 48;
 
@@ -76,10 +80,10 @@ struct Layout {
   static constexpr int kConstOff = kRawOff + (Q8 ? kRawRing * kRawBytes : 0);
   static constexpr int kRawScaleOff = kConstOff + (Q8 ? kConstRing * kConsts * 4 : 0);
   static constexpr int kBarOff = kRawScaleOff + (Q8 ? kRawRing * 2 * kBlocksPerTile * 4 : 0);
-  static constexpr int kNumBars = 9 + 2 * kRing + (Q8 ? 2 * kRawRing + 2 * kRing : 0);
+  static constexpr int kNumBars = 7 + 2 * kRing + (Q8 ? 2 * kRawRing + 2 * kRing : 0);
   static constexpr int kMiscOff = kBarOff + (kNumBars + 1) / 2 * 16;
   static constexpr int kPieceOff = kMiscOff + 64;  // the row warps' pieces and the walk they come from
-  static constexpr int kOddOff = kPieceOff + kPieceRing * kPieceBytes + kWalkBytes;  // drafted tokens whose values are no numbers: [2][1 + 32] words
+  static constexpr int kOddOff = kPieceOff + kPieceRing * kPieceBytes + 2 * kWalkBytes;  // drafted tokens whose values are no numbers: [2][1 + 32] words
   static constexpr int kBytes = kOddOff + (Q8 ? 0 : 2 * (1 + kMaxMaskWords) * 4);
   static_assert(2 * (kBytes + 1024) <= 228 * 1024, "two CTAs per SM");
 };
@@ -93,8 +97,8 @@ struct TreeParams {
   const __nv_bfloat16* value_cache;  // bf16 pools
   const float* key_scale;            // 8-bit pools
   const float* value_scale;
-  int32_t* counters;  // [grid] pieces delivered of the segment that starts in a CTA and goes on past it
-  float4* records;    // [grid][2][kRecordChunks][128]
+  int32_t* counters;  // [grid][8] pieces delivered by each row warp of the segment that starts in a CTA and goes on
+  float4* records;    // [grid][2][half of the dims][kPartChunks][128]
   int32_t* status;
   int32_t mask_words, max_blocks_per_seq, num_blocks, num_kv_heads, num_q_heads;
   int32_t num_query_tokens, max_query_len, num_seqs;
@@ -169,7 +173,7 @@ __device__ __forceinline__ bool next_piece(const TreeParams& p, Walk& w, Piece& 
   return true;
 }
 
-static_assert(sizeof(Piece) <= kPieceBytes && sizeof(Walk) <= kWalkBytes, "room for pieces");
+static_assert(sizeof(Piece) <= kPieceBytes && sizeof(Walk) == kWalkBytes, "room for pieces");
 
 // Where all CTAs' runs lie: run r holds tiles total r / runs .. total (r + 1) / runs - 1.
 struct Runs {
@@ -227,10 +231,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
   uint64_t* p_full = bars + 3;        // P in tensor memory
   uint64_t* o_free = bars + 4;        // O of a finished piece read out
   uint64_t* l_bar = bars + 5;         // the row warps' sums exchanged
-  uint64_t* piece_bar = bars + 6;     // a piece's record written
-  uint64_t* last_bar = bars + 7;      // whether it was the segment's last
-  uint64_t* drain = bars + 8;
-  uint64_t* kv_full = bars + 9;       // [kRing] K (and V, from bf16 pools) of a tile there
+  uint64_t* drain = bars + 6;
+  uint64_t* kv_full = bars + 7;       // [kRing] K (and V, from bf16 pools) of a tile there
   uint64_t* pv_done = kv_full + kRing;  // [kRing] P V of a tile done: its stage and P free, O up to date
   uint64_t* v_full = pv_done + kRing;   // 8-bit pools: [kRing] V converted
   uint64_t* k_empty = v_full + kRing;   // [kRing] scores that read K done
@@ -239,15 +241,15 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
   int* misc = reinterpret_cast<int*>(smem + Lay::kMiscOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
   volatile int& abort_flag = *reinterpret_cast<volatile int*>(misc + 1);
-  volatile int& is_last = *reinterpret_cast<volatile int*>(misc + 2);
-  volatile int& delivered = *reinterpret_cast<volatile int*>(misc + 3);
-  int* start_seq = misc + 4;
-  int* start_off = misc + 5;
+  int* own_first = misc + 2;  // CTAs of the one segment this CTA has a piece of; -1: a run of the row of tiles
+  int* own_last = misc + 3;
   uint32_t* odd = reinterpret_cast<uint32_t*>(smem + Lay::kOddOff);
   auto piece_slot = [&](int u) -> Piece* {
     return reinterpret_cast<Piece*>(smem + Lay::kPieceOff + (u & (kPieceRing - 1)) * kPieceBytes);
   };
   Walk* const row_walk = reinterpret_cast<Walk*>(smem + Lay::kPieceOff + kPieceRing * kPieceBytes);
+  Walk* const start_walk = row_walk + 1;
+  int* delivered = misc + 4;  // [8] pieces of split segments that each row warp has delivered
 
   if (tid == 0) {
     mbar_init(q_full, 1);
@@ -256,8 +258,6 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
     mbar_init(p_full, kRowWarps);
     mbar_init(o_free, kRowWarps);
     mbar_init(l_bar, kRowWarps);
-    mbar_init(piece_bar, kRowWarps);
-    mbar_init(last_bar, 1);
     mbar_init(drain, 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&kv_full[i], Q8 ? kConvWarps : 1);
@@ -275,9 +275,9 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
     }
     fence_barrier_init();
     abort_flag = 0;
-    delivered = 0;
-    *start_seq = -1;
     piece_slot(0)->n = 0;
+    start_walk->at = start_walk->end = 0;
+    for (int i = 0; i < kRowWarps; ++i) delivered[i] = 0;
   }
   if (!Q8 && tid < 2 * (1 + kMaxMaskWords)) odd[tid] = 0u;
   if (warp == kMmaWarp) {
@@ -289,60 +289,118 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
     prefetch_tensormap(&tmap_k);
     prefetch_tensormap(&tmap_v);
   }
-  // ---- the plan: how many tiles there are, and where this CTA's run begins ----
+  // ---- the plan: what this CTA serves ----
   Runs runs;
-  int64_t lo, hi;
   {
     int64_t* warp_sum = reinterpret_cast<int64_t*>(smem);  // (before any copy lands there)
+    int* seq_tiles = reinterpret_cast<int*>(smem + 1024);  // of every sequence, and its segments
+    int* seq_segments = seq_tiles + kMaxDealtSeqs;
+    int* tried = seq_segments + kMaxDealtSeqs;  // CTAs wanted by each warp's piece length
+    const int ctas = static_cast<int>(gridDim.x);
     const int per = (p.num_seqs + kThreads - 1) / kThreads;
     const int s0 = min(tid * per, p.num_seqs), s1 = min(s0 + per, p.num_seqs);
-    int64_t mine = 0;
+    int64_t tiles = 0, segments = 0;
     Seq q;
     for (int s = s0; s < s1; ++s) {
       load_seq<GROUP>(p, s, blockIdx.x == 0, q);
-      mine += static_cast<int64_t>(q.tiles) * q.segments;
+      tiles += static_cast<int64_t>(q.tiles) * q.segments;
+      segments += q.segments;
+      if (p.num_seqs <= kMaxDealtSeqs) {
+        seq_tiles[s] = q.tiles;
+        seq_segments[s] = q.segments;
+      }
     }
-    int64_t upto = mine;
+    // the sum of what the threads before this one have, and of all
+    auto scan = [&](int64_t mine, int64_t* sums, int64_t* total) -> int64_t {
+      int64_t upto = mine;
 #pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += x;
+      for (int d = 1; d < 32; d *= 2) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += x;
+      }
+      if (lane == 31) sums[warp] = upto;
+      __syncthreads();
+      int64_t before = upto - mine;
+      *total = 0;
+      for (int i = 0; i < kThreads / 32; ++i) {
+        if (i < warp) before += sums[i];
+        *total += sums[i];
+      }
+      return before;
+    };
+    // (a number of segments beyond the CTAs' matters no further)
+    const int most = __reduce_max_sync(0xffffffffu, static_cast<int>(min(segments, int64_t{ctas} + 1)));
+    const int some = __reduce_add_sync(0xffffffffu, static_cast<int>(min(segments, int64_t{ctas} + 1)));
+    if (lane == 0) tried[warp] = most > ctas ? most : some;
+    int64_t total;
+    const int64_t before_tiles = scan(tiles, warp_sum, &runs.total);
+    int64_t all_segments = 0;
+    for (int i = 0; i < kThreads / 32; ++i) all_segments += tried[i];
+    runs.runs = static_cast<int>(min(static_cast<int64_t>(ctas), max(runs.total, int64_t{1})));
+    // CTAs of their own: the shortest piece length under which the pieces are no more than the CTAs; every
+    // warp tries one.  No shorter one fits, and a longer one is no better than equal runs.
+    int length = 0;
+    if (p.num_seqs <= kMaxDealtSeqs && all_segments <= ctas && runs.total > 0) {
+      __syncthreads();  // (`tried` has been read)
+      const int mine = max(static_cast<int>((runs.total + ctas - 1) / ctas), kMinPiece) + min(warp, kSplitTiles);
+      int wanted = 0;
+      for (int s = lane; s < p.num_seqs; s += 32) wanted += seq_segments[s] * ((seq_tiles[s] + mine - 1) / mine);
+      wanted = __reduce_add_sync(0xffffffffu, wanted);
+      if (lane == 0) tried[warp] = wanted <= ctas ? mine : 0;
+      __syncthreads();
+      for (int i = kSplitTiles; i >= 0; --i)
+        if (tried[i] > 0) length = tried[i];
     }
-    if (lane == 31) warp_sum[warp] = upto;
-    __syncthreads();
-    runs.total = 0;
-    int64_t before = upto - mine;
-    for (int i = 0; i < kThreads / 32; ++i) {
-      if (i < warp) before += warp_sum[i];
-      runs.total += warp_sum[i];
+    int64_t before, mine;  // this thread's sequences: CTAs, or tiles
+    int64_t want;          // which one of them this CTA looks for
+    if (length > 0) {
+      mine = 0;
+      for (int s = s0; s < s1; ++s) mine += seq_segments[s] * ((seq_tiles[s] + length - 1) / length);
+      before = scan(mine, warp_sum + kThreads / 32, &total);
+      want = blockIdx.x;
+      if (want >= total) want = -1;
+    } else {
+      before = before_tiles;
+      mine = tiles;
+      want = static_cast<int>(blockIdx.x) < runs.runs && runs.total > 0 ? run_start(runs, blockIdx.x) : -1;
     }
-    runs.runs = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max((runs.total + kMinRun - 1) / kMinRun, int64_t{1})));
-    const bool any = static_cast<int>(blockIdx.x) < runs.runs;
-    lo = any ? run_start(runs, blockIdx.x) : 0;
-    hi = any ? run_start(runs, blockIdx.x + 1) : 0;
-    if (lo < hi && lo >= before && lo < before + mine) {
-      int64_t off = lo - before;
+    if (want >= before && want < before + mine) {
+      int64_t off = want - before;
       for (int s = s0; s < s1; ++s) {
         load_seq<GROUP>(p, s, false, q);
-        const int64_t n = static_cast<int64_t>(q.tiles) * q.segments;
-        if (off < n) {
-          *start_seq = s;
-          *start_off = static_cast<int>(off);
-          // the row warps' first two pieces
-          Walk w;
-          w.at = lo;
-          w.end = hi;
-          w.q = q;
-          w.off = static_cast<int>(off);
-          for (int u = 0; u < 2; ++u) {
-            Piece x;
-            if (!next_piece<GROUP>(p, w, x)) x.n = 0;
-            *piece_slot(u) = x;
-          }
-          *row_walk = w;
-          break;
+        const int pieces = length > 0 ? (q.tiles + length - 1) / length : q.tiles;
+        const int64_t n = static_cast<int64_t>(pieces) * q.segments;
+        if (off >= n) {
+          off -= n;
+          continue;
         }
-        off -= n;
+        // the walk begins here; with CTAs of their own, it ends with the piece
+        Walk w;
+        w.q = q;
+        if (length > 0) {
+          const int seg = static_cast<int>(off) / pieces, k = static_cast<int>(off) - seg * pieces;
+          const int j0 = static_cast<int>(static_cast<int64_t>(q.tiles) * k / pieces);
+          const int j1 = static_cast<int>(static_cast<int64_t>(q.tiles) * (k + 1) / pieces);
+          w.off = seg * q.tiles + j0;
+          w.at = 0;
+          w.end = j1 - j0;
+          *own_first = static_cast<int>(blockIdx.x) - k;
+          *own_last = *own_first + pieces - 1;
+        } else {
+          w.off = static_cast<int>(off);
+          w.at = want;
+          w.end = run_start(runs, blockIdx.x + 1);
+          *own_first = -1;
+        }
+        *start_walk = w;
+        // the row warps' first two pieces
+        for (int u = 0; u < 2; ++u) {
+          Piece x;
+          if (!next_piece<GROUP>(p, w, x)) x.n = 0;
+          *piece_slot(u) = x;
+        }
+        *row_walk = w;
+        break;
       }
     }
   }
@@ -351,6 +409,19 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  // The CTAs that a piece's segment is split over.
+  auto piece_ctas = [&](const Piece& u, int* from, int* to) {
+    if (*own_first >= 0) {
+      *from = *own_first;
+      *to = *own_last;
+    } else {
+      *from = run_of(runs, u.first);
+      *to = run_of(runs, u.first + u.tiles - 1);
+    }
+  };
+  // Whether any of the 32 MMA rows of row warp w holds a token.
+  auto warp_active = [&](const Piece& u, int w) { return u.tok0 + (w & 3) * 32 / GROUP < u.q_len; };
+
   if (warp < kRowWarps) {
     // ============================ row warps ============================
     if (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
@@ -383,13 +454,69 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
     bool ok = true;
     int c = 0;       // tiles so far
     int units = 0;   // pieces so far
-    int split = 0;   // of them, pieces of split segments
     int ring = 0, ring_prev = 0;  // stage of this tile and the one before
     uint32_t ph = 0, ph_prev = 0;
+    auto advance = [&] {
+      ring_prev = ring;
+      ph_prev = ph;
+      if (++ring == kRing) {
+        ring = 0;
+        ph ^= 1u;
+      }
+    };
+    // V rows past the context weigh nothing but may hold anything, and so may drafted values that some row
+    // does not see: in a tile that starts at drafted key `base`, this thread clears half of row r of what
+    // lies past the last one, and elements that are no numbers, whose tokens it notes down.
+    auto clear_values = [&](const Piece* cur, int base) -> bool {
+      if (!wait_row(&kv_full[ring], ph)) return false;
+      const int key = base + r;
+      if (key >= 0) {
+        uint32_t any = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint4* x = reinterpret_cast<uint4*>(sv + ring * kOpBytes + swz(r, 4 * part + i));
+          if (key >= cur->q_len) {
+            *x = make_uint4(0u, 0u, 0u, 0u);
+          } else {
+            const uint4 y = *x;
+            const uint4 z = make_uint4(odd_halves(y.x), odd_halves(y.y), odd_halves(y.z), odd_halves(y.w));
+            if ((z.x | z.y | z.z | z.w) != 0u) {
+              any = 1u;
+              *x = make_uint4(y.x & ~z.x, y.y & ~z.y, y.z & ~z.z, y.w & ~z.w);
+            }
+          }
+        }
+        if (any != 0u) {
+          uint32_t* const my_odd = odd + (units & 1) * (1 + kMaxMaskWords);
+          atomicOr(my_odd + 1 + (key >> 5), 1u << (key & 31));
+          atomicOr(my_odd, 1u);
+        }
+      }
+      fence_proxy_async_smem();
+      return true;
+    };
     for (; ok && piece_slot(units)->n > 0; ++units) {
       const Piece* const cur = piece_slot(units);
       const int n = cur->n;
       const int tail_j = (cur->L - cur->q_len) / kTileN - cur->j0;  // from here on tiles hold drafted keys
+      if (!warp_active(*cur, warp)) {
+        // a warp without rows keeps the others' pace (its rows of P and O may hold anything)
+        for (int j = 0; ok && j < n; ++j, ++c) {
+          if (!(ok = wait_row(s_full, static_cast<uint32_t>(c & 1)))) break;
+          if (lane == 0) mbar_arrive(s_free);
+          if (!Q8 && j >= tail_j && !(ok = clear_values(cur, (j - tail_j) * kTileN - cur_lead(cur)))) break;
+          // (the next scores may be there before the others' P: an arrival now would count for theirs)
+          if (c > 0 && !(ok = wait_row(&pv_done[ring_prev], ph_prev))) break;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full);
+          advance();
+        }
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(l_bar);
+        if (!(ok = wait_row(l_bar, static_cast<uint32_t>(units & 1)))) break;
+        if (lane == 0) mbar_arrive(o_free);
+        continue;
+      }
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++c) {
         if (!(ok = wait_row(s_full, static_cast<uint32_t>(c & 1)))) break;
@@ -443,35 +570,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
               top[kBlocksPerTile / 2 + 2 * h + b] = x;
             }
           }
-          if (!Q8) {
-            // V rows past the context weigh nothing but may hold anything, and so may drafted values
-            // that some row does not see: this thread looks at half of row r of the tile
-            if (!(ok = wait_row(&kv_full[ring], ph))) break;
-            const int key = (j - tail_j) * kTileN + r - cur_lead(cur);  // of the drafted ones
-            if (key >= 0) {
-              uint32_t* const my_odd = odd + (units & 1) * (1 + kMaxMaskWords);
-              uint32_t any = 0u;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint4* x = reinterpret_cast<uint4*>(sv + ring * kOpBytes + swz(r, 4 * part + i));
-                if (key >= cur->q_len) {
-                  *x = make_uint4(0u, 0u, 0u, 0u);
-                } else {
-                  uint4 y = *x;
-                  const uint4 z = make_uint4(odd_halves(y.x), odd_halves(y.y), odd_halves(y.z), odd_halves(y.w));
-                  if ((z.x | z.y | z.z | z.w) != 0u) {
-                    any = 1u;
-                    *x = make_uint4(y.x & ~z.x, y.y & ~z.y, y.z & ~z.z, y.w & ~z.w);
-                  }
-                }
-              }
-              if (any != 0u) {
-                atomicOr(my_odd + 1 + (key >> 5), 1u << (key & 31));
-                atomicOr(my_odd, 1u);
-              }
-            }
-            fence_proxy_async_smem();
-          }
+          if (!Q8 && !(ok = clear_values(cur, (j - tail_j) * kTileN - cur_lead(cur)))) break;
         }
         float f[kBlocksPerTile / 2] = {};  // score factors of this thread's blocks (8-bit pools)
         float mt;
@@ -572,12 +671,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
           *piece_slot(units + 2) = x;
           *row_walk = w;
         }
-        ring_prev = ring;
-        ph_prev = ph;
-        if (++ring == kRing) {
-          ring = 0;
-          ph ^= 1u;
-        }
+        advance();
       }
       if (!ok) break;
       // ---- epilogue: this thread's 32 dims ----
@@ -638,42 +732,36 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       const bool row_ok = cur->tok0 + r / GROUP < cur->q_len;
       bool write = n == cur->tiles;
       if (!write) {
-        // ---- a piece of a split segment: its record, and whoever comes last weighs them all ----
-        const int from = run_of(runs, cur->first), to = run_of(runs, cur->first + cur->tiles - 1);
+        // ---- a piece of a split segment: its record, and the warp that comes last weighs them all ----
+        int from, to;
+        piece_ctas(*cur, &from, &to);
         if (row_ok) {
-          float4* rec = p.records + (2ll * blockIdx.x + (cur->j0 == 0 ? 1 : 0)) * kRecordFloat4s + r;
+          float4* rec = p.records + (2ll * blockIdx.x + (cur->j0 == 0 ? 1 : 0)) * kRecordFloat4s +
+                        part * kPartChunks * kTileM + r;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            rec[(8 * part + i) * kTileM] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                                       __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
-          if (part == 0) rec[(kRecordChunks - 1) * kTileM] = make_float4(m, l, 0.f, 0.f);
+            rec[i * kTileM] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                          __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+          rec[8 * kTileM] = make_float4(m, l, 0.f, 0.f);
         }
         __threadfence();
         __syncwarp();
-        if (lane == 0) mbar_arrive(piece_bar);
-        if (warp == 0 && lane == 0) {
-          if (wait_ready(piece_bar, static_cast<uint32_t>(split & 1), &abort_flag, p.status)) {
-            __threadfence();
-            const int before = atomicAdd(p.counters + from, 1);
-            is_last = before == to - from;
-            delivered = split + 1;
-            if (before == to - from) p.counters[from] = 0;
-            __threadfence();
-            mbar_arrive(last_bar);
-          }
+        int last = 0;
+        if (lane == 0) {
+          int32_t* counter = p.counters + from * kRowWarps + warp;
+          last = atomicAdd(counter, 1) == to - from;
+          if (last) *counter = 0;
+          ++delivered[warp];
         }
-        __syncwarp();
-        if (!(ok = wait_row(last_bar, static_cast<uint32_t>(split & 1)))) break;
-        ++split;
-        write = is_last != 0;
+        write = __shfl_sync(0xffffffffu, last, 0) != 0;
         if (write) {
           __threadfence();
           float top_m = -INFINITY;
           auto record = [&](int k) {
-            return p.records + (2ll * (from + k) + (k == 0 ? 1 : 0)) * kRecordFloat4s + r;
+            return p.records + (2ll * (from + k) + (k == 0 ? 1 : 0)) * kRecordFloat4s + part * kPartChunks * kTileM + r;
           };
           const int pieces = row_ok ? to - from + 1 : 0;
-          for (int k = 0; k < pieces; ++k) top_m = fmaxf(top_m, __ldcg(record(k) + (kRecordChunks - 1) * kTileM).x);
+          for (int k = 0; k < pieces; ++k) top_m = fmaxf(top_m, __ldcg(record(k) + 8 * kTileM).x);
           const float at = top_m == -INFINITY ? 0.f : top_m;
           float acc[32];
 #pragma unroll
@@ -681,10 +769,10 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
           l = 0.f;
           for (int k = 0; k < pieces; ++k) {
             const float4* rec = record(k);
-            const float4 ml = __ldcg(rec + (kRecordChunks - 1) * kTileM);
+            const float4 ml = __ldcg(rec + 8 * kTileM);
             float4 x[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = __ldcg(rec + (8 * part + i) * kTileM);
+            for (int i = 0; i < 8; ++i) x[i] = __ldcg(rec + i * kTileM);
             const float w = fast_exp2(ml.x - at);
             l += w * ml.y;
 #pragma unroll
@@ -733,11 +821,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
     }
   } else {
     if (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    Walk walk;
-    walk.at = lo;
-    walk.end = *start_seq >= 0 ? hi : lo;
-    walk.off = *start_off;
-    if (walk.at < walk.end) load_seq<GROUP>(p, *start_seq, false, walk.q);
+    Walk walk = *start_walk;
     if (warp == kMmaWarp) {
       // ============================ MMA issuer ============================
       // The whole warp walks the tiles, so that barriers, counters and descriptors stay uniform; one
@@ -1015,25 +1099,23 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
     tc_fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
   }
-  if (abort_flag != 0 && tid == 0 && *start_seq >= 0) {
+  if (abort_flag != 0 && tid < kRowWarps) {
     // the counters come back to zero all the same: pieces that were not delivered count as if
-    Walk w;
-    w.at = lo;
-    w.end = hi;
-    w.off = *start_off;
-    load_seq<GROUP>(p, *start_seq, false, w.q);
+    Walk w = *start_walk;
     Piece u;
     int n = 0;
     while (next_piece<GROUP>(p, w, u)) {
-      if (u.n == u.tiles || n++ < delivered) continue;
-      const int from = run_of(runs, u.first), to = run_of(runs, u.first + u.tiles - 1);
-      if (atomicAdd(p.counters + from, 1) == to - from) p.counters[from] = 0;
+      if (u.n == u.tiles || !warp_active(u, tid) || n++ < delivered[tid]) continue;
+      int from, to;
+      piece_ctas(u, &from, &to);
+      int32_t* counter = p.counters + from * kRowWarps + tid;
+      if (atomicAdd(counter, 1) == to - from) *counter = 0;
     }
   }
 }
 
 constexpr size_t record_bytes(int ctas) { return static_cast<size_t>(ctas) * 2 * kRecordFloat4s * 16; }
-constexpr size_t counter_bytes(int ctas) { return (static_cast<size_t>(ctas) * 4 + 255) / 256 * 256; }
+constexpr size_t counter_bytes(int ctas) { return (static_cast<size_t>(ctas) * kRowWarps * 4 + 255) / 256 * 256; }
 
 cudaError_t device_sms(int* dev, int* sms) {
   cudaError_t e = cudaGetDevice(dev);
