@@ -157,6 +157,11 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
+// The same into L1.
+__device__ __forceinline__ void prefetch_l1(const void* p) {
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
+}
+
 // Hint: bring `bytes` (a multiple of 16) from a 16-byte-aligned global address into L2 with
 // one bulk request under an L2 cache policy; nothing lands in shared memory and nothing
 // signals completion.

@@ -42,50 +42,54 @@ namespace pkv {
 
 namespace {
 
-constexpr int kTileM = 128;
+constexpr int kTileM = 128;  // MMA rows of one half
 constexpr int kTileN = 128;  // keys per tile
 constexpr int kBlocksPerTile = kTileN / kBlockSize;
-constexpr int kRowWarps = 8;
-constexpr int kRowThreads = kRowWarps * 32;
-constexpr int kMmaWarp = 8, kProducerWarp = 9, kConvWarp0 = 10, kConvWarps = 2;
+constexpr int kHalfWarps = 8;                 // row warps of one half
 constexpr int kQBytes = kTileM * kRowBytes;   // 16 KiB
 constexpr int kOpBytes = kTileN * kRowBytes;  // one K or V tile of bf16: 16 KiB
 constexpr int kRawBytes = 2 * kTileN * kQ8RowBytes;  // codes of K, then of V
-constexpr int kConstRing = 4;                 // tiles whose score constants are kept
 constexpr int kConsts = 3 * kBlocksPerTile;   // key scale, log2 f, 1 / f of every block
 constexpr int kMaxMaskWords = 32;
-constexpr uint32_t kTmemCols = 256;
-constexpr uint32_t kSCol = 0, kPCol = 128, kOCol = 192;
 constexpr float kHeadroom = 8.0f;  // the reference of the exponents lies this far (log2) above the maximum
 constexpr float kLargeScore = 131072.f;  // 2^17: a rounding of the score (log2 units) is then 2^-7
 constexpr int kPartChunks = kHeadDim / 8 + 1;  // float4s of a row for each half of the dims: sum; maximum, weight
-constexpr int kRecordFloat4s = 2 * kPartChunks * kTileM;
+constexpr int kRecordFloat4s = 2 * kPartChunks * kTileM;  // of one half
 constexpr int kMinPiece = 4;      // tiles of a piece of a split segment, at least
 constexpr int kSplitTiles = 5;    // what meeting costs, in tiles: equal runs begin to pay beyond it
+constexpr int kPieceTiles = 1;    // what a piece costs beside its tiles, in tiles
 constexpr int kMaxDealtSeqs = 1024;  // sequences whose segments may get CTAs of their own
-// Register split of the 8-bit kernel (setmaxnreg): what the CTA was launched with, 80 for each of 384 threads.
-constexpr int kRowRegs = 96, kOtherRegs = 48;
-
 constexpr int kPieceRing = 4;
 constexpr int kPieceBytes = 48, kWalkBytes = 48;
 
-template <bool Q8>
+// HALVES 1: 128 rows a CTA, two CTAs per SM; 2: 256 rows that share every K and V tile, one CTA per SM.
+template <bool Q8, int HALVES>
 struct Layout {
-  static constexpr int kThreads = Q8 ? 384 : 320;
-  static constexpr int kRing = Q8 ? 2 : 3;   // stages of K and V operands
-  static constexpr int kRawRing = 2;         // stages of codes
-  static constexpr int kKOff = kQBytes;
+  static constexpr int kRowWarps = HALVES * kHalfWarps;
+  static constexpr int kMmaWarp = kRowWarps, kProducerWarp = kRowWarps + 1, kConvWarp0 = kRowWarps + 2;
+  static constexpr int kConvWarps = Q8 ? 4 : 0;
+  static constexpr int kThreads = Q8 ? (HALVES == 1 ? 512 : 768) : (kRowWarps + 2) * 32;
+  static constexpr int kCtasPerSm = HALVES == 1 ? 2 : 1;
+  // Register split of the 8-bit kernels (setmaxnreg): what the CTA was launched with.
+  static constexpr int kRowRegs = HALVES == 1 ? 88 : 96, kOtherRegs = HALVES == 1 ? 40 : 48;
+  static constexpr uint32_t kTmemCols = 256 * HALVES;
+  static constexpr uint32_t kSCol = 0, kPCol = 128 * HALVES, kOCol = 192 * HALVES;  // + 128, 64, 64 per half
+  static constexpr int kRing = Q8 ? (HALVES == 1 ? 2 : 3) : (HALVES == 1 ? 3 : 6);  // stages of K and V operands
+  static constexpr int kRawRing = HALVES == 1 ? 2 : 4;                               // stages of codes
+  static constexpr int kConstRing = HALVES == 1 ? 4 : 8;  // tiles whose score constants are kept (kRing + 2, at least)
+  static constexpr int kKOff = HALVES * kQBytes;
   static constexpr int kVOff = kKOff + kRing * kOpBytes;
   static constexpr int kRawOff = kVOff + kRing * kOpBytes;
   static constexpr int kConstOff = kRawOff + (Q8 ? kRawRing * kRawBytes : 0);
   static constexpr int kRawScaleOff = kConstOff + (Q8 ? kConstRing * kConsts * 4 : 0);
   static constexpr int kBarOff = kRawScaleOff + (Q8 ? kRawRing * 2 * kBlocksPerTile * 4 : 0);
-  static constexpr int kNumBars = 7 + 2 * kRing + (Q8 ? 2 * kRawRing + 2 * kRing : 0);
+  static constexpr int kNumBars = 6 * HALVES + 2 + 2 * kRing + (Q8 ? 2 * kRawRing + 2 * kRing : 0);
   static constexpr int kMiscOff = kBarOff + (kNumBars + 1) / 2 * 16;
-  static constexpr int kPieceOff = kMiscOff + 64;  // the row warps' pieces and the walk they come from
-  static constexpr int kOddOff = kPieceOff + kPieceRing * kPieceBytes + 2 * kWalkBytes;  // drafted tokens whose values are no numbers: [2][1 + 32] words
-  static constexpr int kBytes = kOddOff + (Q8 ? 0 : 2 * (1 + kMaxMaskWords) * 4);
-  static_assert(2 * (kBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+  static constexpr int kPieceOff = kMiscOff + 16 + 4 * kRowWarps;  // the row warps' pieces and the walks
+  static constexpr int kOddOff = kPieceOff + kPieceRing * kPieceBytes + 2 * kWalkBytes;
+  // drafted tokens whose values are no numbers: [3][any; 32 words of bits]
+  static constexpr int kBytes = kOddOff + (Q8 ? 0 : 3 * (1 + kMaxMaskWords) * 4);
+  static_assert(kCtasPerSm * (kBytes + 1024) <= 228 * 1024, "CTAs of an SM fit in its shared memory");
 };
 
 struct TreeParams {
@@ -97,8 +101,8 @@ struct TreeParams {
   const __nv_bfloat16* value_cache;  // bf16 pools
   const float* key_scale;            // 8-bit pools
   const float* value_scale;
-  int32_t* counters;  // [grid][8] pieces delivered by each row warp of the segment that starts in a CTA and goes on
-  float4* records;    // [grid][2][half of the dims][kPartChunks][128]
+  int32_t* counters;  // [grid][row warps] pieces delivered by each of the segment that starts in a CTA and goes on
+  float4* records;    // [grid][2][halves][half of the dims][kPartChunks][128]
   int32_t* status;
   int32_t mask_words, max_blocks_per_seq, num_blocks, num_kv_heads, num_q_heads;
   int32_t num_query_tokens, max_query_len, num_seqs;
@@ -113,7 +117,7 @@ struct Seq {
 };
 
 // Sequences without rows have no work; ones that cannot be served are reported (when `report`).
-template <int GROUP>
+template <int TOKENS>
 __device__ __forceinline__ void load_seq(const TreeParams& p, int s, bool report, Seq& q) {
   q.s = s;
   q.q0 = __ldg(p.query_start_loc + s);
@@ -128,14 +132,16 @@ __device__ __forceinline__ void load_seq(const TreeParams& p, int s, bool report
     if (report) flag_error(p.status, PA_DEVFLAG_BAD_CONTEXT);
     return;
   }
-  constexpr int kTokens = kTileM / GROUP;
   q.tiles = (q.L + kTileN - 1) / kTileN;
-  q.segments = p.num_kv_heads * ((q.q_len + kTokens - 1) / kTokens);
+  q.segments = p.num_kv_heads * ((q.q_len + TOKENS - 1) / TOKENS);
 }
 
-// A piece of a segment: key tiles j0 .. j0 + n - 1 of query tile tok0 / TOKENS against K/V head g.
+// A segment's length in the row of all tiles: what it costs beside its tiles comes first.
+__device__ __forceinline__ int span(const Seq& q) { return q.tiles + kPieceTiles; }
+
+// A piece of a segment: key tiles j0 .. j0 + n - 1 of the query tile that begins at tok0, against K/V head g.
 struct Piece {
-  int64_t first;  // the segment's first tile in the row of all tiles
+  int64_t first;  // the segment's beginning in the row of all tiles
   int s, g, q0, q_len, L, tok0;
   int j0, n, tiles;  // n == 0: none
 };
@@ -145,35 +151,39 @@ struct Piece {
 struct Walk {
   int64_t at, end;  // the next tile and the run's end among all
   Seq q;
-  int off;         // of the next tile among the sequence's
+  int off;          // of the next tile among the sequence's
 };
 
-template <int GROUP>
+template <int TOKENS>
 __device__ __forceinline__ bool next_piece(const TreeParams& p, Walk& w, Piece& u) {
-  if (w.at >= w.end) return false;
-  while (w.off >= w.q.tiles * w.q.segments) {
-    w.off -= w.q.tiles * w.q.segments;
-    load_seq<GROUP>(p, w.q.s + 1, false, w.q);
+  while (w.at < w.end) {
+    while (w.off >= span(w.q) * w.q.segments) {
+      w.off -= span(w.q) * w.q.segments;
+      load_seq<TOKENS>(p, w.q.s + 1, false, w.q);
+    }
+    const int seg = w.off / span(w.q);
+    const int v0 = w.off - seg * span(w.q);
+    const int n = static_cast<int>(min(static_cast<int64_t>(span(w.q) - v0), w.end - w.at));
+    u.first = w.at - v0;
+    w.off += n;
+    w.at += n;
+    u.j0 = max(v0 - kPieceTiles, 0);
+    u.n = v0 + n - kPieceTiles - u.j0;
+    if (u.n <= 0) continue;  // (nothing but what comes before the tiles)
+    const int q_tiles = (w.q.q_len + TOKENS - 1) / TOKENS;
+    u.s = w.q.s;
+    u.q0 = w.q.q0;
+    u.q_len = w.q.q_len;
+    u.L = w.q.L;
+    u.tiles = w.q.tiles;
+    u.g = seg / q_tiles;
+    u.tok0 = (seg - u.g * q_tiles) * TOKENS;
+    return true;
   }
-  constexpr int kTokens = kTileM / GROUP;
-  const int seg = w.off / w.q.tiles;
-  const int q_tiles = (w.q.q_len + kTokens - 1) / kTokens;
-  u.s = w.q.s;
-  u.q0 = w.q.q0;
-  u.q_len = w.q.q_len;
-  u.L = w.q.L;
-  u.tiles = w.q.tiles;
-  u.g = seg / q_tiles;
-  u.tok0 = (seg - u.g * q_tiles) * kTokens;
-  u.j0 = w.off - seg * w.q.tiles;
-  u.n = static_cast<int>(min(static_cast<int64_t>(u.tiles - u.j0), w.end - w.at));
-  u.first = w.at - u.j0;
-  w.off += u.n;
-  w.at += u.n;
-  return true;
+  return false;
 }
 
-static_assert(sizeof(Piece) <= kPieceBytes && sizeof(Walk) == kWalkBytes, "room for pieces");
+static_assert(sizeof(Piece) <= kPieceBytes && sizeof(Walk) <= kWalkBytes && sizeof(Walk) % 8 == 0, "room for pieces");
 
 // Where all CTAs' runs lie: run r holds tiles total r / runs .. total (r + 1) / runs - 1.
 struct Runs {
@@ -204,12 +214,17 @@ __device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
   return ((w & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
 }
 
-template <int GROUP, bool Q8>
-__global__ void __launch_bounds__(Layout<Q8>::kThreads, 2)
+template <int GROUP, bool Q8, int HALVES>
+__global__ void __launch_bounds__(Layout<Q8, HALVES>::kThreads, Layout<Q8, HALVES>::kCtasPerSm)
 tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
             const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ TreeParams p) {
-  using Lay = Layout<Q8>;
+  using Lay = Layout<Q8, HALVES>;
   constexpr int kThreads = Lay::kThreads, kRing = Lay::kRing, kRawRing = Lay::kRawRing;
+  constexpr int kConstRing = Lay::kConstRing;
+  constexpr int kRowWarps = Lay::kRowWarps, kConvWarps = Lay::kConvWarps, kConvWarp0 = Lay::kConvWarp0;
+  constexpr int kMmaWarp = Lay::kMmaWarp, kProducerWarp = Lay::kProducerWarp;
+  constexpr int kHalfTokens = kTileM / GROUP;      // query tokens of a half
+  constexpr int kTokens = HALVES * kHalfTokens;    // and of a segment
   const int tid = threadIdx.x;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (so that what depends on it stays uniform)
   const int lane = tid & 31;
@@ -225,18 +240,20 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
   float* consts = reinterpret_cast<float*>(smem + Lay::kConstOff);
   float* raw_scale = reinterpret_cast<float*>(smem + Lay::kRawScaleOff);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::kBarOff);
-  uint64_t* q_full = bars;            // a piece's Q landed
-  uint64_t* s_full = bars + 1;        // scores in tensor memory
-  uint64_t* s_free = bars + 2;        // and read into registers
-  uint64_t* p_full = bars + 3;        // P in tensor memory
-  uint64_t* o_free = bars + 4;        // O of a finished piece read out
-  uint64_t* l_bar = bars + 5;         // the row warps' sums exchanged
-  uint64_t* drain = bars + 6;
-  uint64_t* kv_full = bars + 7;       // [kRing] K (and V, from bf16 pools) of a tile there
-  uint64_t* pv_done = kv_full + kRing;  // [kRing] P V of a tile done: its stage and P free, O up to date
-  uint64_t* v_full = pv_done + kRing;   // 8-bit pools: [kRing] V converted
-  uint64_t* k_empty = v_full + kRing;   // [kRing] scores that read K done
-  uint64_t* raw_full = k_empty + kRing;  // [kRawRing] codes and scales landed
+  // [HALVES] each.  A half without rows in a piece takes no part in it; phases count what it took part in.
+  uint64_t* q_full = bars;             // a piece's Q landed
+  uint64_t* s_full = q_full + HALVES;  // scores in tensor memory
+  uint64_t* s_free = s_full + HALVES;  // and read into registers
+  uint64_t* p_full = s_free + HALVES;  // P in tensor memory
+  uint64_t* o_free = p_full + HALVES;  // O of a finished piece read out
+  uint64_t* half_done = o_free + HALVES;  // P V of a tile done: P free, O up to date (HALVES 1: tile_done says it)
+  uint64_t* l_bar = half_done + HALVES;   // all row warps: the sums of a row exchanged
+  uint64_t* drain = l_bar + 1;
+  uint64_t* kv_full = drain + 1;          // [kRing] K (and V, from bf16 pools) of a tile there
+  uint64_t* tile_done = kv_full + kRing;  // [kRing] P V of a tile done: its stage is free
+  uint64_t* v_full = tile_done + kRing;   // 8-bit pools: [kRing] V converted
+  uint64_t* k_empty = v_full + kRing;     // [kRing] scores that read K done
+  uint64_t* raw_full = k_empty + kRing;   // [kRawRing] codes and scales landed
   uint64_t* raw_empty = raw_full + kRawRing;
   int* misc = reinterpret_cast<int*>(smem + Lay::kMiscOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
@@ -249,19 +266,22 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
   };
   Walk* const row_walk = reinterpret_cast<Walk*>(smem + Lay::kPieceOff + kPieceRing * kPieceBytes);
   Walk* const start_walk = row_walk + 1;
-  int* delivered = misc + 4;  // [8] pieces of split segments that each row warp has delivered
+  int* delivered = misc + 4;  // [row warps] pieces of split segments that each row warp has delivered
 
   if (tid == 0) {
-    mbar_init(q_full, 1);
-    mbar_init(s_full, Q8 ? 2 : 1);
-    mbar_init(s_free, kRowWarps);
-    mbar_init(p_full, kRowWarps);
-    mbar_init(o_free, kRowWarps);
+    for (int h = 0; h < HALVES; ++h) {
+      mbar_init(&q_full[h], 1);
+      mbar_init(&s_full[h], Q8 ? 2 : 1);
+      mbar_init(&s_free[h], kHalfWarps);
+      mbar_init(&p_full[h], kHalfWarps);
+      mbar_init(&o_free[h], kHalfWarps);
+      mbar_init(&half_done[h], 1);
+    }
     mbar_init(l_bar, kRowWarps);
     mbar_init(drain, 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&kv_full[i], Q8 ? kConvWarps : 1);
-      mbar_init(&pv_done[i], 1);
+      mbar_init(&tile_done[i], 1);
       if (Q8) {
         mbar_init(&v_full[i], kConvWarps);
         mbar_init(&k_empty[i], 1);
@@ -279,9 +299,9 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
     start_walk->at = start_walk->end = 0;
     for (int i = 0; i < kRowWarps; ++i) delivered[i] = 0;
   }
-  if (!Q8 && tid < 2 * (1 + kMaxMaskWords)) odd[tid] = 0u;
+  if (!Q8 && tid < 3 * (1 + kMaxMaskWords)) odd[tid] = 0u;
   if (warp == kMmaWarp) {
-    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_alloc(tmem_slot, Lay::kTmemCols);
     tmem_relinquish();
   }
   if (warp == kProducerWarp && lane == 0) {
@@ -302,8 +322,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
     int64_t tiles = 0, segments = 0;
     Seq q;
     for (int s = s0; s < s1; ++s) {
-      load_seq<GROUP>(p, s, blockIdx.x == 0, q);
-      tiles += static_cast<int64_t>(q.tiles) * q.segments;
+      load_seq<kTokens>(p, s, blockIdx.x == 0, q);
+      tiles += static_cast<int64_t>(span(q)) * q.segments;
       segments += q.segments;
       if (p.num_seqs <= kMaxDealtSeqs) {
         seq_tiles[s] = q.tiles;
@@ -342,7 +362,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
     int length = 0;
     if (p.num_seqs <= kMaxDealtSeqs && all_segments <= ctas && runs.total > 0) {
       __syncthreads();  // (`tried` has been read)
-      const int mine = max(static_cast<int>((runs.total + ctas - 1) / ctas), kMinPiece) + min(warp, kSplitTiles);
+      const int mine = max(static_cast<int>((runs.total - kPieceTiles * all_segments + ctas - 1) / ctas), kMinPiece) +
+                       min(warp, kSplitTiles);
       int wanted = 0;
       for (int s = lane; s < p.num_seqs; s += 32) wanted += seq_segments[s] * ((seq_tiles[s] + mine - 1) / mine);
       wanted = __reduce_add_sync(0xffffffffu, wanted);
@@ -367,8 +388,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
     if (want >= before && want < before + mine) {
       int64_t off = want - before;
       for (int s = s0; s < s1; ++s) {
-        load_seq<GROUP>(p, s, false, q);
-        const int pieces = length > 0 ? (q.tiles + length - 1) / length : q.tiles;
+        load_seq<kTokens>(p, s, false, q);
+        const int pieces = length > 0 ? (q.tiles + length - 1) / length : span(q);
         const int64_t n = static_cast<int64_t>(pieces) * q.segments;
         if (off >= n) {
           off -= n;
@@ -381,7 +402,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
           const int seg = static_cast<int>(off) / pieces, k = static_cast<int>(off) - seg * pieces;
           const int j0 = static_cast<int>(static_cast<int64_t>(q.tiles) * k / pieces);
           const int j1 = static_cast<int>(static_cast<int64_t>(q.tiles) * (k + 1) / pieces);
-          w.off = seg * q.tiles + j0;
+          w.off = seg * span(q) + kPieceTiles + j0;
           w.at = 0;
           w.end = j1 - j0;
           *own_first = static_cast<int>(blockIdx.x) - k;
@@ -396,7 +417,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
         // the row warps' first two pieces
         for (int u = 0; u < 2; ++u) {
           Piece x;
-          if (!next_piece<GROUP>(p, w, x)) x.n = 0;
+          if (!next_piece<kTokens>(p, w, x)) x.n = 0;
           *piece_slot(u) = x;
         }
         *row_walk = w;
@@ -415,45 +436,56 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       *from = *own_first;
       *to = *own_last;
     } else {
-      *from = run_of(runs, u.first);
-      *to = run_of(runs, u.first + u.tiles - 1);
+      *from = run_of(runs, u.first + kPieceTiles);
+      *to = run_of(runs, u.first + kPieceTiles + u.tiles - 1);
     }
   };
-  // Whether any of the 32 MMA rows of row warp w holds a token.
-  auto warp_active = [&](const Piece& u, int w) { return u.tok0 + (w & 3) * 32 / GROUP < u.q_len; };
+  // Whether a half holds any token of a piece, and any of the 32 MMA rows of row warp w.
+  auto half_active = [&](const Piece& u, int h) { return u.tok0 + h * kHalfTokens < u.q_len; };
+  auto warp_active = [&](const Piece& u, int w) {
+    return u.tok0 + (w / kHalfWarps) * kHalfTokens + (w & 3) * 32 / GROUP < u.q_len;
+  };
 
   if (warp < kRowWarps) {
     // ============================ row warps ============================
-    if (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
-    const int part = warp >> 2;            // keys 64 part .. 64 part + 63 of every tile
+    if (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Lay::kRowRegs));
+    const int half = warp / kHalfWarps;
+    const int part = (warp >> 2) & 1;      // keys 64 part .. 64 part + 63 of every tile
     const int r = (warp & 3) * 32 + lane;  // MMA row == TMEM lane; also a key of the tile, for V
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t s_mine = lane_addr + kSCol + part * (kTileN / 2);
-    const uint32_t s_theirs = lane_addr + kSCol + (part ^ 1) * (kTileN / 2);
-    const uint32_t p_addr = lane_addr + kPCol + part * (kTileN / 4);
-    const uint32_t o_addr = lane_addr + kOCol + part * (kHeadDim / 2);
-    const uint32_t o_theirs = lane_addr + kOCol + (part ^ 1) * (kHeadDim / 2);
+    const uint32_t s_mine = lane_addr + Lay::kSCol + half * kTileN + part * (kTileN / 2);
+    const uint32_t s_theirs = lane_addr + Lay::kSCol + half * kTileN + (part ^ 1) * (kTileN / 2);
+    const uint32_t p_addr = lane_addr + Lay::kPCol + half * (kTileN / 2) + part * (kTileN / 4);
+    const uint32_t o_addr = lane_addr + Lay::kOCol + half * kHeadDim + part * (kHeadDim / 2);
+    const uint32_t o_theirs = lane_addr + Lay::kOCol + half * kHeadDim + (part ^ 1) * (kHeadDim / 2);
     auto wait_row = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, wait_ready(bar, parity, &abort_flag, p.status));
     };
     // this row's mask, and how far into its tile the first drafted key lies
     auto mask_row = [&](const Piece* u) -> const int32_t* {
-      return p.tree_mask + static_cast<int64_t>(u->q0 + min(u->tok0 + r / GROUP, u->q_len - 1)) * p.mask_words;
+      return p.tree_mask + static_cast<int64_t>(u->q0 + min(u->tok0 + half * kHalfTokens + r / GROUP, u->q_len - 1)) * p.mask_words;
     };
     auto cur_lead = [&](const Piece* u) -> int { return (u->L - u->q_len) % kTileN; };
     // Pieces come through shared memory, two ahead, so that the tiles' loop keeps its registers: a warp
     // looks piece u + 1 up after the row warps met in piece u's epilogue, and its slot was last read in
     // piece u - 2, which all of them have left by then.
-    auto load_q = [&](int u) {  // by warp 0's lane 0
-      const Piece& x = *piece_slot(u);
-      if (x.n == 0) return;
-      mbar_arrive_expect_tx(q_full, kQBytes);
-      tma_load_3d(sq, &tmap_q, 0, x.g * GROUP, x.q0 + x.tok0, q_full);
+    // This thread's share of a CTA's record: of its piece of the segment that begins there, or else.
+    auto record_of = [&](int cta, bool begins) -> float4* {
+      return p.records + ((2ll * cta + (begins ? 1 : 0)) * HALVES + half) * kRecordFloat4s + part * kPartChunks * kTileM + r;
     };
-    if (warp == 0 && lane == 0) load_q(0);
+    const bool q_loader = (warp & (kHalfWarps - 1)) == 0 && lane == 0;
+    int q_asked = 0;  // the half's Qs asked for, by its loader
+    auto load_q = [&](const Piece& x) {
+      mbar_arrive_expect_tx(&q_full[half], kQBytes);
+      tma_load_3d(sq + half * kQBytes, &tmap_q, 0, x.g * GROUP, x.q0 + x.tok0 + half * kHalfTokens, &q_full[half]);
+      ++q_asked;
+    };
+    auto wanted = [&](int u) { return piece_slot(u)->n > 0 && half_active(*piece_slot(u), half); };
     bool ok = true;
-    int c = 0;       // tiles so far
+    int c = 0;       // tiles that this half took part in
+    int jt = 0;      // tiles of the CTA before this piece
     int units = 0;   // pieces so far
+    int q_used = 0;  // and those this half took part in
     int ring = 0, ring_prev = 0;  // stage of this tile and the one before
     uint32_t ph = 0, ph_prev = 0;
     auto advance = [&] {
@@ -463,6 +495,11 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
         ring = 0;
         ph ^= 1u;
       }
+    };
+    // until the half's last P V is done
+    auto wait_pv = [&]() -> bool {
+      return HALVES == 1 ? wait_row(&tile_done[ring_prev], ph_prev)
+                         : wait_row(&half_done[half], static_cast<uint32_t>((c - 1) & 1));
     };
     // V rows past the context weigh nothing but may hold anything, and so may drafted values that some row
     // does not see: in a tile that starts at drafted key `base`, this thread clears half of row r of what
@@ -487,7 +524,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
           }
         }
         if (any != 0u) {
-          uint32_t* const my_odd = odd + (units & 1) * (1 + kMaxMaskWords);
+          uint32_t* const my_odd = odd + units % 3 * (1 + kMaxMaskWords);
           atomicOr(my_odd + 1 + (key >> 5), 1u << (key & 31));
           atomicOr(my_odd, 1u);
         }
@@ -499,30 +536,42 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       const Piece* const cur = piece_slot(units);
       const int n = cur->n;
       const int tail_j = (cur->L - cur->q_len) / kTileN - cur->j0;  // from here on tiles hold drafted keys
+      if (HALVES > 1 && !half_active(*cur, half)) {  // (half 1)
+        // (the next piece's Q is wanted before half 0 can finish this one)
+        if (q_loader && q_asked == q_used && wanted(units + 1)) load_q(*piece_slot(units + 1));
+        if (lane == 0) mbar_arrive(l_bar);
+        ok = wait_row(l_bar, static_cast<uint32_t>(units & 1));
+        jt += n;
+        continue;
+      }
+      if (q_loader && q_asked == q_used) load_q(*cur);
+      ++q_used;
       if (!warp_active(*cur, warp)) {
         // a warp without rows keeps the others' pace (its rows of P and O may hold anything)
         for (int j = 0; ok && j < n; ++j, ++c) {
-          if (!(ok = wait_row(s_full, static_cast<uint32_t>(c & 1)))) break;
-          if (lane == 0) mbar_arrive(s_free);
-          if (!Q8 && j >= tail_j && !(ok = clear_values(cur, (j - tail_j) * kTileN - cur_lead(cur)))) break;
+          if (!(ok = wait_row(&s_full[half], static_cast<uint32_t>(c & 1)))) break;
+          if (lane == 0) mbar_arrive(&s_free[half]);
+          if (!Q8 && half == 0 && j >= tail_j && !(ok = clear_values(cur, (j - tail_j) * kTileN - cur_lead(cur)))) break;
           // (the next scores may be there before the others' P: an arrival now would count for theirs)
-          if (c > 0 && !(ok = wait_row(&pv_done[ring_prev], ph_prev))) break;
+          if (c > 0 && !(ok = wait_pv())) break;
           __syncwarp();
-          if (lane == 0) mbar_arrive(p_full);
+          if (lane == 0) mbar_arrive(&p_full[half]);
           advance();
         }
         if (!ok) break;
         if (lane == 0) mbar_arrive(l_bar);
         if (!(ok = wait_row(l_bar, static_cast<uint32_t>(units & 1)))) break;
-        if (lane == 0) mbar_arrive(o_free);
+        if (lane == 0) mbar_arrive(&o_free[half]);
+        jt += n;
         continue;
       }
+      prefetch_l1(mask_row(cur));
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++c) {
-        if (!(ok = wait_row(s_full, static_cast<uint32_t>(c & 1)))) break;
+        if (!(ok = wait_row(&s_full[half], static_cast<uint32_t>(c & 1)))) break;
         tc_fence_after_sync();
         // the piece's last scores are done with Q: the next piece's may land there
-        if (j == n - 1 && warp == 0 && lane == 0) load_q(units + 1);
+        if (j == n - 1 && q_loader && wanted(units + 1)) load_q(*piece_slot(units + 1));
         uint32_t v[2][32];
         float top[kBlocksPerTile];  // largest raw score of each block, the partner's first
 #pragma unroll
@@ -552,7 +601,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
         tmem_wait_ld();
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(s_free);
+        if (lane == 0) mbar_arrive(&s_free[half]);
         if (tail) {
           const int32_t* bits = mask_row(cur);
 #pragma unroll
@@ -570,11 +619,11 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
               top[kBlocksPerTile / 2 + 2 * h + b] = x;
             }
           }
-          if (!Q8 && !(ok = clear_values(cur, (j - tail_j) * kTileN - cur_lead(cur)))) break;
+          if (!Q8 && half == 0 && !(ok = clear_values(cur, (j - tail_j) * kTileN - cur_lead(cur)))) break;
         }
         float f[kBlocksPerTile / 2] = {};  // score factors of this thread's blocks (8-bit pools)
         float mt;
-        const uint32_t cs = smem_addr(consts + c % kConstRing * kConsts);
+        const uint32_t cs = smem_addr(consts + (jt + j) % kConstRing * kConsts);
         if (Q8) {
           float g[kBlocksPerTile / 2];  // the partner's
           lds_f32x4(cs + 4 * part * (kBlocksPerTile / 2), f);
@@ -643,7 +692,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
           l += sum.x + sum.y;
         }
         if (c > 0) {  // the previous P V: P's columns are free and O is up to date
-          if (!(ok = wait_row(&pv_done[ring_prev], ph_prev))) break;
+          if (!(ok = wait_pv())) break;
           tc_fence_after_sync();
         }
         tmem_st32(p_addr, v[0]);
@@ -663,11 +712,11 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
         tmem_wait_st();
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full);
+        if (lane == 0) mbar_arrive(&p_full[half]);
         if (j == 0 && warp == 0 && lane == 0) {
           Walk w = *row_walk;
           Piece x;
-          if (!next_piece<GROUP>(p, w, x)) x.n = 0;
+          if (!next_piece<kTokens>(p, w, x)) x.n = 0;
           *piece_slot(units + 2) = x;
           *row_walk = w;
         }
@@ -675,7 +724,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       }
       if (!ok) break;
       // ---- epilogue: this thread's 32 dims ----
-      if (!(ok = wait_row(&pv_done[ring_prev], ph_prev))) break;
+      jt += n;
+      if (!(ok = wait_pv())) break;
       tc_fence_after_sync();
       uint32_t o[32];
       tmem_ld32(o_addr, o);
@@ -684,11 +734,11 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       tmem_st1(o_addr, __float_as_uint(l));
       tmem_wait_st();
       tc_fence_before_sync();
-      // (the other buffer of odd tokens was last read before every warp's last P: clear it for the next)
+      // (the next piece's odd tokens: the buffer was last read two pieces ago, before the row warps last met)
       if (!Q8 && tid == 0) {
-        uint32_t* other = odd + ((units & 1) ^ 1) * (1 + kMaxMaskWords);
-        if (other[0] != 0u)
-          for (int i = 0; i <= kMaxMaskWords; ++i) other[i] = 0u;
+        uint32_t* next_odd = odd + (units + 1) % 3 * (1 + kMaxMaskWords);
+        if (next_odd[0] != 0u)
+          for (int i = 0; i <= kMaxMaskWords; ++i) next_odd[i] = 0u;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(l_bar);
@@ -698,9 +748,9 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       tmem_wait_ld();
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(o_free);
+      if (lane == 0) mbar_arrive(&o_free[half]);
       l = part ? l_theirs + l : l + l_theirs;
-      const uint32_t* const my_odd = odd + (units & 1) * (1 + kMaxMaskWords);
+      const uint32_t* const my_odd = odd + units % 3 * (1 + kMaxMaskWords);
       if (!Q8 && *const_cast<const volatile uint32_t*>(my_odd) != 0u) {
         // drafted values that are no numbers go to the rows that see them, and to no other
         const int32_t* table = p.block_tables + static_cast<int64_t>(cur->s) * p.max_blocks_per_seq;
@@ -729,15 +779,15 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
           }
         }
       }
-      const bool row_ok = cur->tok0 + r / GROUP < cur->q_len;
+      const int tok0 = cur->tok0 + half * kHalfTokens;
+      const bool row_ok = tok0 + r / GROUP < cur->q_len;
       bool write = n == cur->tiles;
       if (!write) {
         // ---- a piece of a split segment: its record, and the warp that comes last weighs them all ----
         int from, to;
         piece_ctas(*cur, &from, &to);
         if (row_ok) {
-          float4* rec = p.records + (2ll * blockIdx.x + (cur->j0 == 0 ? 1 : 0)) * kRecordFloat4s +
-                        part * kPartChunks * kTileM + r;
+          float4* rec = record_of(blockIdx.x, cur->j0 == 0);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             rec[i * kTileM] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
@@ -757,18 +807,15 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
         if (write) {
           __threadfence();
           float top_m = -INFINITY;
-          auto record = [&](int k) {
-            return p.records + (2ll * (from + k) + (k == 0 ? 1 : 0)) * kRecordFloat4s + part * kPartChunks * kTileM + r;
-          };
           const int pieces = row_ok ? to - from + 1 : 0;
-          for (int k = 0; k < pieces; ++k) top_m = fmaxf(top_m, __ldcg(record(k) + 8 * kTileM).x);
+          for (int k = 0; k < pieces; ++k) top_m = fmaxf(top_m, __ldcg(record_of(from + k, k == 0) + 8 * kTileM).x);
           const float at = top_m == -INFINITY ? 0.f : top_m;
           float acc[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) acc[i] = 0.f;
           l = 0.f;
           for (int k = 0; k < pieces; ++k) {
-            const float4* rec = record(k);
+            const float4* rec = record_of(from + k, k == 0);
             const float4 ml = __ldcg(rec + 8 * kTileM);
             float4 x[8];
 #pragma unroll
@@ -805,22 +852,19 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int rr = (r & ~3) + i;
-          if (cur->tok0 + rr / GROUP < cur->q_len)
+          if (tok0 + rr / GROUP < cur->q_len)
             *reinterpret_cast<uint4*>(
-                p.out + (static_cast<int64_t>(cur->q0 + cur->tok0 + rr / GROUP) * p.num_q_heads + cur->g * GROUP +
+                p.out + (static_cast<int64_t>(cur->q0 + tok0 + rr / GROUP) * p.num_q_heads + cur->g * GROUP +
                          rr % GROUP) * kHeadDim + part * (kHeadDim / 2) + 8 * (lane & 3)) = w[i];
         }
       }
     }
-    // leave no copy in flight: the next piece's Q, if one was given up on
-    if (warp == 0 && lane == 0 && !ok) {
-      for (int u = 0; u < 2; ++u) {  // (piece `units` was asked for at the latest, and perhaps the one after)
-        if (piece_slot(units + u)->n > 0) mbar_wait(q_full, static_cast<uint32_t>((units + u) & 1));
-      }
+    if (!ok && q_loader) {  // leave no copy in flight (bounded waits)
       flag_error(p.status, PA_DEVFLAG_TIMEOUT);
+      if (q_asked > 0) mbar_wait(&q_full[half], static_cast<uint32_t>((q_asked - 1) & 1));
     }
   } else {
-    if (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Lay::kOtherRegs));
     Walk walk = *start_walk;
     if (warp == kMmaWarp) {
       // ============================ MMA issuer ============================
@@ -833,55 +877,66 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       const uint64_t k_desc0 = sw128_desc(smem_addr(sk), 16, 1024);
       const uint64_t v_desc0 = sw128_desc(smem_addr(sv), 16, 1024);
       constexpr uint64_t kStageStep = kOpBytes >> 4;  // of a descriptor's start address
-      int s_issued = 0, pv_issued = 0, units_s = 0, units_o = 0;
+      constexpr uint64_t kQStep = kQBytes >> 4;
+      int s_issued[HALVES] = {}, pv_issued[HALVES] = {}, q_used[HALVES] = {}, o_used[HALVES] = {};
       int ks = 0, vs = 0;
       uint32_t kph = 0, vph = 0;
-      auto issue_s = [&](bool first) -> bool {
+      // a tile's scores, for the first `halves` of them
+      auto issue_s = [&](bool first, int halves) -> bool {
         if (!wait_ready(&kv_full[ks], kph, &abort_flag, p.status)) return false;
-        if (first) {
-          if (!wait_ready(q_full, static_cast<uint32_t>(units_s & 1), &abort_flag, p.status)) return false;
-          ++units_s;
-        }
-        if (s_issued > 0 &&
-            !wait_ready(s_free, static_cast<uint32_t>((s_issued - 1) & 1), &abort_flag, p.status))
-          return false;
-        tc_fence_after_sync();
         const uint64_t k_desc = k_desc0 + kStageStep * ks;
-        if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < kHeadDim / 16; ++kk)
-            umma_bf16(tmem + kSCol, q_desc + 2 * kk, k_desc + 2 * kk, kIdescS, kk > 0 ? 1u : 0u);
-          umma_commit(s_full);
-          if (Q8) {
-            mbar_arrive(s_full);  // passes on what the converters wrote before their arrivals (the constants)
-            umma_commit(&k_empty[ks]);
+        for (int h = 0; h < HALVES; ++h) {
+          if (h >= halves) continue;
+          if (first && !wait_ready(&q_full[h], static_cast<uint32_t>(q_used[h]++ & 1), &abort_flag, p.status))
+            return false;
+          if (s_issued[h] > 0 &&
+              !wait_ready(&s_free[h], static_cast<uint32_t>((s_issued[h] - 1) & 1), &abort_flag, p.status))
+            return false;
+          tc_fence_after_sync();
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < kHeadDim / 16; ++kk)
+              umma_bf16(tmem + Lay::kSCol + h * kTileN, q_desc + kQStep * h + 2 * kk, k_desc + 2 * kk, kIdescS,
+                        kk > 0 ? 1u : 0u);
+            umma_commit(&s_full[h]);
+            if (Q8) mbar_arrive(&s_full[h]);  // passes on what the converters wrote before their arrivals (the constants)
           }
+          ++s_issued[h];
         }
-        ++s_issued;
+        if (Q8 && leader) umma_commit(&k_empty[ks]);
         if (++ks == kRing) {
           ks = 0;
           kph ^= 1u;
         }
         return true;
       };
-      auto issue_pv = [&](bool first) -> bool {
+      // and its P V: half 0 first, whose row warps clear V for both
+      auto issue_pv = [&](bool first, int halves) -> bool {
         if (Q8 && !wait_ready(&v_full[vs], vph, &abort_flag, p.status)) return false;
-        if (!wait_ready(p_full, static_cast<uint32_t>(pv_issued & 1), &abort_flag, p.status)) return false;
-        if (first) {  // O starts anew: the previous piece's has been read out
-          if (units_o > 0 && !wait_ready(o_free, static_cast<uint32_t>((units_o - 1) & 1), &abort_flag, p.status))
-            return false;
-          ++units_o;
-        }
-        tc_fence_after_sync();
         const uint64_t v_desc = v_desc0 + kStageStep * vs;
-        if (leader) {
-          umma_bf16_ts(tmem + kOCol, tmem + kPCol, v_desc, kIdescO, first ? 0u : 1u);
 #pragma unroll
-          for (int kk = 1; kk < kTileN / 16; ++kk)  // 16 keys: 2 KiB of V, 8 columns of P
-            umma_bf16_ts(tmem + kOCol, tmem + kPCol + kk * 8, v_desc + 128 * kk, kIdescO, 1u);
-          umma_commit(&pv_done[vs]);
+        for (int h = 0; h < HALVES; ++h) {
+          if (h >= halves) continue;
+          if (!wait_ready(&p_full[h], static_cast<uint32_t>(pv_issued[h] & 1), &abort_flag, p.status)) return false;
+          if (first) {  // O starts anew: the half's previous piece has been read out
+            if (o_used[h] > 0 &&
+                !wait_ready(&o_free[h], static_cast<uint32_t>((o_used[h] - 1) & 1), &abort_flag, p.status))
+              return false;
+            ++o_used[h];
+          }
+          tc_fence_after_sync();
+          if (leader) {
+            const uint32_t o_tmem = tmem + Lay::kOCol + h * kHeadDim, p_tmem = tmem + Lay::kPCol + h * (kTileN / 2);
+            umma_bf16_ts(o_tmem, p_tmem, v_desc, kIdescO, first ? 0u : 1u);
+#pragma unroll
+            for (int kk = 1; kk < kTileN / 16; ++kk)  // 16 keys: 2 KiB of V, 8 columns of P
+              umma_bf16_ts(o_tmem, p_tmem + kk * 8, v_desc + 128 * kk, kIdescO, 1u);
+            if (HALVES > 1) umma_commit(&half_done[h]);
+          }
+          ++pv_issued[h];
         }
-        ++pv_issued;
+        if (leader) umma_commit(&tile_done[vs]);
         if (++vs == kRing) {
           vs = 0;
           vph ^= 1u;
@@ -889,19 +944,22 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
         return true;
       };
       Piece cur, nxt;
-      bool have = next_piece<GROUP>(p, walk, cur);
-      bool have_next = have && next_piece<GROUP>(p, walk, nxt);
-      bool ok = have && issue_s(true);
+      bool have = next_piece<kTokens>(p, walk, cur);
+      bool have_next = have && next_piece<kTokens>(p, walk, nxt);
+      auto halves_of = [&](const Piece& u) { return HALVES > 1 && half_active(u, 1) ? 2 : 1; };
+      int halves = have ? halves_of(cur) : 0;
+      bool ok = have && issue_s(true, halves);
       while (ok && have) {
-        const int n = cur.n;
+        const int n = cur.n, after = have_next ? halves_of(nxt) : 0;
         for (int j = 0; ok && j < n; ++j) {
           const bool last = j + 1 == n;
-          if (!last || have_next) ok = issue_s(last);
-          if (ok) ok = issue_pv(j == 0);
+          if (!last || have_next) ok = issue_s(last, last ? after : halves);
+          if (ok) ok = issue_pv(j == 0, halves);
         }
         cur = nxt;
+        halves = after;
         have = have_next;
-        if (have) have_next = next_piece<GROUP>(p, walk, nxt);
+        if (have) have_next = next_piece<kTokens>(p, walk, nxt);
       }
       // wait (bounded) until every MMA issued above has completed
       if (leader) {
@@ -917,8 +975,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       int jt = 0;
       constexpr int kStages = Q8 ? kRawRing : kRing;
       uint64_t* const full = Q8 ? raw_full : kv_full;
-      uint64_t* const empty = Q8 ? raw_empty : pv_done;
-      while (ok && next_piece<GROUP>(p, walk, cur)) {
+      uint64_t* const empty = Q8 ? raw_empty : tile_done;
+      while (ok && next_piece<kTokens>(p, walk, cur)) {
         const int32_t* row = p.block_tables + static_cast<int64_t>(cur.s) * p.max_blocks_per_seq;
         const int blocks = (cur.L + kBlockSize - 1) / kBlockSize;
         // 32 table entries (four tiles) at a time, one per lane, the next window in flight
@@ -984,17 +1042,18 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
         }
       }
       __syncwarp();
-    } else {
+    } else if (warp < kConvWarp0 + kConvWarps) {
       // ============================ converters (8-bit pools) ============================
-      constexpr int kMyBlocks = kBlocksPerTile / kConvWarps;  // blocks kMyBlocks cw .. of every tile
+      constexpr int kMyBlocks = Q8 ? kBlocksPerTile / (Q8 ? kConvWarps : 1) : 1;  // blocks kMyBlocks cw .. of every tile
       const int cw = warp - kConvWarp0;
       const int row0 = cw * kMyBlocks * kBlockSize + (lane >> 2);
       const int c0 = 2 * (lane & 3);  // 16 codes of a row: two 16-byte chunks
+      constexpr int kBatch = 4;       // rows a lane holds at once
       int st = 0, rs = 0, slot = 0;   // operand stage, stage of codes
       uint32_t ph = 0, rph = 0;
       Piece cur;
       bool ok = true;
-      while (ok && next_piece<GROUP>(p, walk, cur)) {
+      while (ok && next_piece<kTokens>(p, walk, cur)) {
         const int blocks = (cur.L + kBlockSize - 1) / kBlockSize;
         for (int j = 0; j < cur.n; ++j) {
           ok = wait_ready(&raw_full[rs], rph, &abort_flag, p.status) &&
@@ -1031,46 +1090,58 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
           const uint32_t up = bf2_power(120);
           uint8_t* dst = sk + st * kOpBytes;
 #pragma unroll
-          for (int i = 0; i < 2 * kMyBlocks; ++i) {
-            const uint4 w = lds128(raw + i * 512);
-            uint4 a, b;
-            codes4_to_bf2x2(w.x, a.x, a.y);
-            codes4_to_bf2x2(w.y, a.z, a.w);
-            codes4_to_bf2x2(w.z, b.x, b.y);
-            codes4_to_bf2x2(w.w, b.z, b.w);
-            a.x = mul_bf2(a.x, up); a.y = mul_bf2(a.y, up); a.z = mul_bf2(a.z, up); a.w = mul_bf2(a.w, up);
-            b.x = mul_bf2(b.x, up); b.y = mul_bf2(b.y, up); b.z = mul_bf2(b.z, up); b.w = mul_bf2(b.w, up);
-            *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * i, c0)) = a;
-            *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * i, c0 + 1)) = b;
+          for (int i0 = 0; i0 < 2 * kMyBlocks; i0 += kBatch) {
+            uint4 in[kBatch];  // (the stores may alias the loads, so these come first)
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) in[i] = lds128(raw + (i0 + i) * 512);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const uint4 w = in[i];
+              uint4 a, b;
+              codes4_to_bf2x2(w.x, a.x, a.y);
+              codes4_to_bf2x2(w.y, a.z, a.w);
+              codes4_to_bf2x2(w.z, b.x, b.y);
+              codes4_to_bf2x2(w.w, b.z, b.w);
+              a.x = mul_bf2(a.x, up); a.y = mul_bf2(a.y, up); a.z = mul_bf2(a.z, up); a.w = mul_bf2(a.w, up);
+              b.x = mul_bf2(b.x, up); b.y = mul_bf2(b.y, up); b.z = mul_bf2(b.z, up); b.w = mul_bf2(b.w, up);
+              *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * (i0 + i), c0)) = a;
+              *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * (i0 + i), c0 + 1)) = b;
+            }
           }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&kv_full[st]);
-          ok = wait_ready(&pv_done[st], ph ^ 1u, &abort_flag, p.status);
+          ok = wait_ready(&tile_done[st], ph ^ 1u, &abort_flag, p.status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           dst = sv + st * kOpBytes;
           const int keys_left = cur.L - (cur.j0 + j) * kTileN - row0;
           raw += kTileN * kQ8RowBytes;
 #pragma unroll
-          for (int i = 0; i < 2 * kMyBlocks; ++i) {
-            uint4 w = lds128(raw + i * 512);
-            // keys past the context weigh nothing, but may hold anything
-            if (8 * i >= keys_left) w = make_uint4(0u, 0u, 0u, 0u);
-            uint4 a, b;
-            codes4_to_bf2x2(w.x, a.x, a.y);
-            codes4_to_bf2x2(w.y, a.z, a.w);
-            codes4_to_bf2x2(w.z, b.x, b.y);
-            codes4_to_bf2x2(w.w, b.z, b.w);
-            const uint32_t m0 = __shfl_sync(0xffffffffu, my_m, i >> 1);
-            a.x = mul_bf2(a.x, m0); a.y = mul_bf2(a.y, m0); a.z = mul_bf2(a.z, m0); a.w = mul_bf2(a.w, m0);
-            b.x = mul_bf2(b.x, m0); b.y = mul_bf2(b.y, m0); b.z = mul_bf2(b.z, m0); b.w = mul_bf2(b.w, m0);
-            if (any_high) {  // a scale above 2^7: the rest of it
-              const uint32_t m1 = bf2_power(__shfl_sync(0xffffffffu, my_high, i >> 1));
-              a.x = mul_bf2(a.x, m1); a.y = mul_bf2(a.y, m1); a.z = mul_bf2(a.z, m1); a.w = mul_bf2(a.w, m1);
-              b.x = mul_bf2(b.x, m1); b.y = mul_bf2(b.y, m1); b.z = mul_bf2(b.z, m1); b.w = mul_bf2(b.w, m1);
+          for (int i0 = 0; i0 < 2 * kMyBlocks; i0 += kBatch) {
+            uint4 in[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) in[i] = lds128(raw + (i0 + i) * 512);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              uint4 w = in[i];
+              // keys past the context weigh nothing, but may hold anything
+              if (8 * (i0 + i) >= keys_left) w = make_uint4(0u, 0u, 0u, 0u);
+              uint4 a, b;
+              codes4_to_bf2x2(w.x, a.x, a.y);
+              codes4_to_bf2x2(w.y, a.z, a.w);
+              codes4_to_bf2x2(w.z, b.x, b.y);
+              codes4_to_bf2x2(w.w, b.z, b.w);
+              const uint32_t m0 = __shfl_sync(0xffffffffu, my_m, (i0 + i) >> 1);
+              a.x = mul_bf2(a.x, m0); a.y = mul_bf2(a.y, m0); a.z = mul_bf2(a.z, m0); a.w = mul_bf2(a.w, m0);
+              b.x = mul_bf2(b.x, m0); b.y = mul_bf2(b.y, m0); b.z = mul_bf2(b.z, m0); b.w = mul_bf2(b.w, m0);
+              if (any_high) {  // a scale above 2^7: the rest of it
+                const uint32_t m1 = bf2_power(__shfl_sync(0xffffffffu, my_high, (i0 + i) >> 1));
+                a.x = mul_bf2(a.x, m1); a.y = mul_bf2(a.y, m1); a.z = mul_bf2(a.z, m1); a.w = mul_bf2(a.w, m1);
+                b.x = mul_bf2(b.x, m1); b.y = mul_bf2(b.y, m1); b.z = mul_bf2(b.z, m1); b.w = mul_bf2(b.w, m1);
+              }
+              *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * (i0 + i), c0)) = a;
+              *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * (i0 + i), c0 + 1)) = b;
             }
-            *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * i, c0)) = a;
-            *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * i, c0 + 1)) = b;
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -1097,14 +1168,14 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
   if (warp == kMmaWarp) {
     __syncwarp();
     tc_fence_after_sync();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(tmem, Lay::kTmemCols);
   }
   if (abort_flag != 0 && tid < kRowWarps) {
     // the counters come back to zero all the same: pieces that were not delivered count as if
     Walk w = *start_walk;
     Piece u;
     int n = 0;
-    while (next_piece<GROUP>(p, w, u)) {
+    while (next_piece<kTokens>(p, w, u)) {
       if (u.n == u.tiles || !warp_active(u, tid) || n++ < delivered[tid]) continue;
       int from, to;
       piece_ctas(u, &from, &to);
@@ -1114,28 +1185,30 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
   }
 }
 
-constexpr size_t record_bytes(int ctas) { return static_cast<size_t>(ctas) * 2 * kRecordFloat4s * 16; }
-constexpr size_t counter_bytes(int ctas) { return (static_cast<size_t>(ctas) * kRowWarps * 4 + 255) / 256 * 256; }
+// Both forms have 16 row warps and 256 rows per SM, so their counters and records take the same room, and
+// the counters the same place.
+constexpr size_t counter_bytes(int sms) { return (static_cast<size_t>(sms) * 2 * kHalfWarps * 4 + 255) / 256 * 256; }
+constexpr size_t record_bytes(int sms) { return static_cast<size_t>(sms) * 2 * 2 * kRecordFloat4s * 16; }
 
 cudaError_t device_sms(int* dev, int* sms) {
   cudaError_t e = cudaGetDevice(dev);
   return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
 }
 
-template <int GROUP, bool Q8>
+template <int GROUP, bool Q8, int HALVES>
 cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
-  using Lay = Layout<Q8>;
+  using Lay = Layout<Q8, HALVES>;
   static bool ready[kMaxDevices] = {};  // benign race: the calls are idempotent
   int dev = 0, sms = 0;
   cudaError_t e = device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
-  auto kernel = tree_kernel<GROUP, Q8>;
+  auto kernel = tree_kernel<GROUP, Q8, HALVES>;
   if (dev >= kMaxDevices || !ready[dev]) {
     if (Q8) {
       cudaFuncAttributes attr;
       if ((e = cudaFuncGetAttributes(&attr, kernel)) != cudaSuccess) return e;
       // setmaxnreg waits for registers the launch never had: refuse instead
-      if (attr.numRegs * Lay::kThreads < kRowThreads * kRowRegs + (Lay::kThreads - kRowThreads) * kOtherRegs)
+      if (attr.numRegs * Lay::kThreads < Lay::kRowWarps * 32 * Lay::kRowRegs + (Lay::kThreads - Lay::kRowWarps * 32) * Lay::kOtherRegs)
         return cudaErrorInvalidConfiguration;
     }
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kBytes);
@@ -1162,7 +1235,7 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
   p.key_scale = a.key_scale;
   p.value_scale = a.value_scale;
   p.counters = static_cast<int32_t*>(a.workspace);
-  p.records = reinterpret_cast<float4*>(static_cast<uint8_t*>(a.workspace) + counter_bytes(2 * sms));
+  p.records = reinterpret_cast<float4*>(static_cast<uint8_t*>(a.workspace) + counter_bytes(sms));
   p.status = a.status;
   p.mask_words = a.mask_words;
   p.max_blocks_per_seq = a.max_blocks_per_seq;
@@ -1173,16 +1246,22 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
   p.max_query_len = a.max_query_len;
   p.num_seqs = a.num_seqs;
   p.qk_scale = a.scale * 1.4426950408889634f;
-  tree_kernel<GROUP, Q8><<<2 * sms, Lay::kThreads, Lay::kBytes, stream>>>(tq, tk, tv, p);
+  kernel<<<Lay::kCtasPerSm * sms, Lay::kThreads, Lay::kBytes, stream>>>(tq, tk, tv, p);
   return cudaGetLastError();
+}
+
+// More rows than one half holds: both halves, so that a tile is fetched (and converted) once for them.
+template <int GROUP, bool Q8>
+cudaError_t launch_halves(const TreeArgs& a, cudaStream_t stream) {
+  return a.max_query_len * GROUP > kTileM ? launch<GROUP, Q8, 2>(a, stream) : launch<GROUP, Q8, 1>(a, stream);
 }
 
 template <bool Q8>
 cudaError_t launch_group(const TreeArgs& a, cudaStream_t stream) {
   switch (a.num_q_heads / a.num_kv_heads) {
-    case 1: return launch<1, Q8>(a, stream);
-    case 2: return launch<2, Q8>(a, stream);
-    case 4: return launch<4, Q8>(a, stream);
+    case 1: return launch_halves<1, Q8>(a, stream);
+    case 2: return launch_halves<2, Q8>(a, stream);
+    case 4: return launch_halves<4, Q8>(a, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -1192,7 +1271,7 @@ cudaError_t launch_group(const TreeArgs& a, cudaStream_t stream) {
 size_t tree_workspace_size() {
   int dev = 0, sms = 0;
   if (device_sms(&dev, &sms) != cudaSuccess) return 0;
-  return counter_bytes(2 * sms) + record_bytes(2 * sms);
+  return counter_bytes(sms) + record_bytes(sms);
 }
 
 cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream) { return launch_group<false>(a, stream); }

@@ -118,6 +118,14 @@ def test_serving_batch(pool):
 
 
 @pytest.mark.parametrize("pool", POOLS)
+@pytest.mark.parametrize("hist,seqs", [(100, 70), (1500, 40), (1500, 70), (4000, 30)])
+def test_large_and_small_trees_together(pool, hist, seqs):
+    """More segments than CTAs, and of the two halves of a CTA's rows now one, now both in use."""
+    r = np.random.default_rng(seqs)
+    Trees(pool, r.integers(0, hist, seqs), r.integers(1, 70, seqs), 32, 8, "tree", seed=seqs).check()
+
+
+@pytest.mark.parametrize("pool", POOLS)
 def test_many_short_sequences(pool):
     r = np.random.default_rng(5)
     Trees(pool, r.integers(0, 40, 3000), r.integers(0, 3, 3000), 4, 1, "tree", seed=5).check()
