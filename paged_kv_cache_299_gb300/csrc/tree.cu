@@ -60,7 +60,129 @@ constexpr int kSplitTiles = 5;    // what meeting costs, in tiles: equal runs be
 constexpr int kPieceTiles = 1;    // what a piece costs beside its tiles, in tiles
 constexpr int kMaxDealtSeqs = 1024;  // sequences whose segments may get CTAs of their own
 constexpr int kPieceRing = 4;
-constexpr int kPieceBytes = 48, kWalkBytes = 48;
+constexpr int kWalkBytes = 56;
+
+struct TreeParams {
+  __nv_bfloat16* out;
+  const int32_t* tree_mask;
+  const int32_t* query_start_loc;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const __nv_bfloat16* value_cache;  // bf16 pools
+  const float* key_scale;            // 8-bit pools
+  const float* value_scale;
+  int32_t* counters;  // [grid][row warps] pieces delivered by each of the segment that starts in a CTA and goes on
+  float4* records;    // [grid][2][halves][half of the dims][kPartChunks][128]
+  int32_t* status;
+  int32_t mask_words, max_blocks_per_seq, num_blocks, num_kv_heads, num_q_heads;
+  int32_t num_query_tokens, max_query_len, num_seqs;
+  float qk_scale;  // scale * log2(e)
+};
+
+// The sequence whose tiles a run is in.
+struct Seq {
+  int s, q0, q_len, L;
+  int tiles;    // of a segment
+  int q_tiles;  // segments of a K/V head; 0: none to serve
+};
+
+// Sequences without rows have no work; ones that cannot be served are reported (when `report`).
+template <int TOKENS>
+__device__ __forceinline__ void load_seq(const TreeParams& p, int s, bool report, Seq& q) {
+  q.s = s;
+  q.q0 = __ldg(p.query_start_loc + s);
+  q.q_len = __ldg(p.query_start_loc + s + 1) - q.q0;
+  q.L = __ldg(p.context_lens + s);
+  q.q_tiles = 0;
+  q.tiles = 1;
+  if (q.q_len <= 0) return;
+  if (q.q0 < 0 || q.q_len > p.num_query_tokens - q.q0 || q.q_len > p.max_query_len || q.L < q.q_len ||
+      q.L > static_cast<int64_t>(p.max_blocks_per_seq) * kBlockSize ||
+      q.L > static_cast<int64_t>(p.num_blocks) * kBlockSize) {
+    if (report) flag_error(p.status, PA_DEVFLAG_BAD_CONTEXT);
+    return;
+  }
+  q.tiles = (q.L + kTileN - 1) / kTileN;
+  q.q_tiles = (q.q_len + TOKENS - 1) / TOKENS;
+}
+
+// A segment's length in the row of all tiles: what it costs beside its tiles comes first.
+__device__ __forceinline__ int span(const Seq& q) { return q.tiles + kPieceTiles; }
+
+// A piece of a segment: key tiles j0 .. j0 + n - 1 of the query tile that begins at tok0, against K/V head g.
+struct Piece {
+  int s, g, q0, q_len, L, tok0;
+  int j0, n;     // n == 0: none
+  int from, to;  // the CTAs that the segment is split over: one, if the piece is all of it
+};
+
+// Walks a run: the query tiles of a K/V head, then the next head's, then the next sequence's.
+struct Walk {
+  int64_t at, end;  // the next tile and the run's end among all
+  Seq q;
+  int g, q_tile, v;  // the segment, and its tile
+};
+
+// w.q is set; the walk begins at place `off` of its sequence's `length`-long segments.
+__device__ __forceinline__ int enter_seq(Walk& w, int64_t off, int length) {
+  const int64_t seg = off / length;
+  w.g = static_cast<int>(seg / w.q.q_tiles);
+  w.q_tile = static_cast<int>(seg - static_cast<int64_t>(w.g) * w.q.q_tiles);
+  return static_cast<int>(off - seg * length);
+}
+
+static_assert(sizeof(Walk) == kWalkBytes, "room for pieces");
+
+// Where all CTAs' runs lie: run r holds tiles total r / runs .. total (r + 1) / runs - 1.
+struct Runs {
+  int64_t total;
+  int runs;
+  int own_first, own_last;  // the CTAs of the one segment this CTA has a piece of; -1: it has a run of all tiles
+};
+__device__ __forceinline__ int64_t run_start(const Runs& x, int64_t r) { return x.total * r / x.runs; }
+// The run that holds a tile (none is empty).
+__device__ __forceinline__ int run_of(const Runs& x, int64_t tile) {
+  return static_cast<int>(((tile + 1) * x.runs + x.total - 1) / x.total - 1);
+}
+
+template <int TOKENS>
+__device__ __forceinline__ bool next_piece(const TreeParams& p, const Runs& runs, Walk& w, Piece& u) {
+  while (w.at < w.end) {
+    while (w.q.q_tiles == 0 || w.g == p.num_kv_heads) {
+      load_seq<TOKENS>(p, w.q.s + 1, false, w.q);
+      w.g = w.q_tile = w.v = 0;
+    }
+    const int n = static_cast<int>(min(static_cast<int64_t>(span(w.q) - w.v), w.end - w.at));
+    const int64_t first = w.at - w.v;  // where the segment begins
+    u.s = w.q.s;
+    u.q0 = w.q.q0;
+    u.q_len = w.q.q_len;
+    u.L = w.q.L;
+    u.g = w.g;
+    u.tok0 = w.q_tile * TOKENS;
+    u.j0 = max(w.v - kPieceTiles, 0);
+    u.n = w.v + n - kPieceTiles - u.j0;
+    w.at += n;
+    w.v += n;
+    if (w.v == span(w.q)) {
+      w.v = 0;
+      if (++w.q_tile == w.q.q_tiles) {
+        w.q_tile = 0;
+        ++w.g;
+      }
+    }
+    if (u.n <= 0) continue;  // (nothing but what comes before the tiles)
+    u.from = runs.own_first;
+    u.to = runs.own_last;
+    if (runs.own_first < 0) {
+      u.from = u.to = static_cast<int>(blockIdx.x);
+      if (u.j0 > 0) u.from = run_of(runs, first + kPieceTiles);
+      if (u.j0 + u.n < w.q.tiles) u.to = run_of(runs, first + span(w.q) - 1);
+    }
+    return true;
+  }
+  return false;
+}
 
 // HALVES 1: 128 rows a CTA, two CTAs per SM; 2: 256 rows that share every K and V tile, one CTA per SM.
 template <bool Q8, int HALVES>
@@ -86,115 +208,12 @@ struct Layout {
   static constexpr int kNumBars = 6 * HALVES + 2 + 2 * kRing + (Q8 ? 2 * kRawRing + 2 * kRing : 0);
   static constexpr int kMiscOff = kBarOff + (kNumBars + 1) / 2 * 16;
   static constexpr int kPieceOff = kMiscOff + 16 + 4 * kRowWarps;  // the row warps' pieces and the walks
-  static constexpr int kOddOff = kPieceOff + kPieceRing * kPieceBytes + 2 * kWalkBytes;
+  static constexpr int kOddOff = kPieceOff + kPieceRing * static_cast<int>(sizeof(Piece)) + 2 * kWalkBytes;
+  static constexpr int kKeysOff = kOddOff;  // 8-bit pools: [kRawRing]
   // drafted tokens whose values are no numbers: [3][any; 32 words of bits]
-  static constexpr int kBytes = kOddOff + (Q8 ? 0 : 3 * (1 + kMaxMaskWords) * 4);
+  static constexpr int kBytes = kOddOff + (Q8 ? 4 * kRawRing : 3 * (1 + kMaxMaskWords) * 4);
   static_assert(kCtasPerSm * (kBytes + 1024) <= 228 * 1024, "CTAs of an SM fit in its shared memory");
 };
-
-struct TreeParams {
-  __nv_bfloat16* out;
-  const int32_t* tree_mask;
-  const int32_t* query_start_loc;
-  const int32_t* block_tables;
-  const int32_t* context_lens;
-  const __nv_bfloat16* value_cache;  // bf16 pools
-  const float* key_scale;            // 8-bit pools
-  const float* value_scale;
-  int32_t* counters;  // [grid][row warps] pieces delivered by each of the segment that starts in a CTA and goes on
-  float4* records;    // [grid][2][halves][half of the dims][kPartChunks][128]
-  int32_t* status;
-  int32_t mask_words, max_blocks_per_seq, num_blocks, num_kv_heads, num_q_heads;
-  int32_t num_query_tokens, max_query_len, num_seqs;
-  float qk_scale;  // scale * log2(e)
-};
-
-// The sequence whose tiles a run is in.
-struct Seq {
-  int s, q0, q_len, L;
-  int tiles;     // of a segment
-  int segments;  // K/V heads x query tiles; 0: none to serve
-};
-
-// Sequences without rows have no work; ones that cannot be served are reported (when `report`).
-template <int TOKENS>
-__device__ __forceinline__ void load_seq(const TreeParams& p, int s, bool report, Seq& q) {
-  q.s = s;
-  q.q0 = __ldg(p.query_start_loc + s);
-  q.q_len = __ldg(p.query_start_loc + s + 1) - q.q0;
-  q.L = __ldg(p.context_lens + s);
-  q.segments = 0;
-  q.tiles = 1;
-  if (q.q_len <= 0) return;
-  if (q.q0 < 0 || q.q_len > p.num_query_tokens - q.q0 || q.q_len > p.max_query_len || q.L < q.q_len ||
-      q.L > static_cast<int64_t>(p.max_blocks_per_seq) * kBlockSize ||
-      q.L > static_cast<int64_t>(p.num_blocks) * kBlockSize) {
-    if (report) flag_error(p.status, PA_DEVFLAG_BAD_CONTEXT);
-    return;
-  }
-  q.tiles = (q.L + kTileN - 1) / kTileN;
-  q.segments = p.num_kv_heads * ((q.q_len + TOKENS - 1) / TOKENS);
-}
-
-// A segment's length in the row of all tiles: what it costs beside its tiles comes first.
-__device__ __forceinline__ int span(const Seq& q) { return q.tiles + kPieceTiles; }
-
-// A piece of a segment: key tiles j0 .. j0 + n - 1 of the query tile that begins at tok0, against K/V head g.
-struct Piece {
-  int64_t first;  // the segment's beginning in the row of all tiles
-  int s, g, q0, q_len, L, tok0;
-  int j0, n, tiles;  // n == 0: none
-};
-
-// Walks a run.  A sequence's tiles stay below 2^31: its context fits a pool of fewer than 2^31 rows, which
-// K/V heads multiply, so tiles x heads < 2^24, and it has at most 32 query tiles.
-struct Walk {
-  int64_t at, end;  // the next tile and the run's end among all
-  Seq q;
-  int off;          // of the next tile among the sequence's
-};
-
-template <int TOKENS>
-__device__ __forceinline__ bool next_piece(const TreeParams& p, Walk& w, Piece& u) {
-  while (w.at < w.end) {
-    while (w.off >= span(w.q) * w.q.segments) {
-      w.off -= span(w.q) * w.q.segments;
-      load_seq<TOKENS>(p, w.q.s + 1, false, w.q);
-    }
-    const int seg = w.off / span(w.q);
-    const int v0 = w.off - seg * span(w.q);
-    const int n = static_cast<int>(min(static_cast<int64_t>(span(w.q) - v0), w.end - w.at));
-    u.first = w.at - v0;
-    w.off += n;
-    w.at += n;
-    u.j0 = max(v0 - kPieceTiles, 0);
-    u.n = v0 + n - kPieceTiles - u.j0;
-    if (u.n <= 0) continue;  // (nothing but what comes before the tiles)
-    const int q_tiles = (w.q.q_len + TOKENS - 1) / TOKENS;
-    u.s = w.q.s;
-    u.q0 = w.q.q0;
-    u.q_len = w.q.q_len;
-    u.L = w.q.L;
-    u.tiles = w.q.tiles;
-    u.g = seg / q_tiles;
-    u.tok0 = (seg - u.g * q_tiles) * TOKENS;
-    return true;
-  }
-  return false;
-}
-
-static_assert(sizeof(Piece) <= kPieceBytes && sizeof(Walk) <= kWalkBytes && sizeof(Walk) % 8 == 0, "room for pieces");
-
-// Where all CTAs' runs lie: run r holds tiles total r / runs .. total (r + 1) / runs - 1.
-struct Runs {
-  int64_t total;
-  int runs;
-};
-__device__ __forceinline__ int64_t run_start(const Runs& x, int64_t r) { return x.total * r / x.runs; }
-// The run that holds a tile (none is empty).
-__device__ __forceinline__ int run_of(const Runs& x, int64_t tile) {
-  return static_cast<int>(((tile + 1) * x.runs + x.total - 1) / x.total - 1);
-}
 
 // Bits o .. o + 31 of what a row sees, counted from the first drafted key: below 0 the prefix, from q_len
 // on nothing.
@@ -246,8 +265,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
   uint64_t* s_free = s_full + HALVES;  // and read into registers
   uint64_t* p_full = s_free + HALVES;  // P in tensor memory
   uint64_t* o_free = p_full + HALVES;  // O of a finished piece read out
-  uint64_t* half_done = o_free + HALVES;  // P V of a tile done: P free, O up to date (HALVES 1: tile_done says it)
-  uint64_t* l_bar = half_done + HALVES;   // all row warps: the sums of a row exchanged
+  uint64_t* pv_done = o_free + HALVES;  // P V of a tile done: P free, O up to date
+  uint64_t* l_bar = pv_done + HALVES;   // all row warps: the sums of a row exchanged
   uint64_t* drain = l_bar + 1;
   uint64_t* kv_full = drain + 1;          // [kRing] K (and V, from bf16 pools) of a tile there
   uint64_t* tile_done = kv_full + kRing;  // [kRing] P V of a tile done: its stage is free
@@ -260,11 +279,12 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
   volatile int& abort_flag = *reinterpret_cast<volatile int*>(misc + 1);
   int* own_first = misc + 2;  // CTAs of the one segment this CTA has a piece of; -1: a run of the row of tiles
   int* own_last = misc + 3;
+  int* raw_keys = reinterpret_cast<int*>(smem + Lay::kKeysOff);  // keys of the context from a stage's first on; 0: the end
   uint32_t* odd = reinterpret_cast<uint32_t*>(smem + Lay::kOddOff);
   auto piece_slot = [&](int u) -> Piece* {
-    return reinterpret_cast<Piece*>(smem + Lay::kPieceOff + (u & (kPieceRing - 1)) * kPieceBytes);
+    return reinterpret_cast<Piece*>(smem + Lay::kPieceOff + (u & (kPieceRing - 1)) * sizeof(Piece));
   };
-  Walk* const row_walk = reinterpret_cast<Walk*>(smem + Lay::kPieceOff + kPieceRing * kPieceBytes);
+  Walk* const row_walk = reinterpret_cast<Walk*>(smem + Lay::kPieceOff + kPieceRing * static_cast<int>(sizeof(Piece)));
   Walk* const start_walk = row_walk + 1;
   int* delivered = misc + 4;  // [row warps] pieces of split segments that each row warp has delivered
 
@@ -275,7 +295,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       mbar_init(&s_free[h], kHalfWarps);
       mbar_init(&p_full[h], kHalfWarps);
       mbar_init(&o_free[h], kHalfWarps);
-      mbar_init(&half_done[h], 1);
+      mbar_init(&pv_done[h], 1);
     }
     mbar_init(l_bar, kRowWarps);
     mbar_init(drain, 1);
@@ -297,6 +317,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
     abort_flag = 0;
     piece_slot(0)->n = 0;
     start_walk->at = start_walk->end = 0;
+    *own_first = *own_last = -1;
     for (int i = 0; i < kRowWarps; ++i) delivered[i] = 0;
   }
   if (!Q8 && tid < 3 * (1 + kMaxMaskWords)) odd[tid] = 0u;
@@ -311,6 +332,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
   }
   // ---- the plan: what this CTA serves ----
   Runs runs;
+  runs.own_first = runs.own_last = -1;
   {
     int64_t* warp_sum = reinterpret_cast<int64_t*>(smem);  // (before any copy lands there)
     int* seq_tiles = reinterpret_cast<int*>(smem + 1024);  // of every sequence, and its segments
@@ -323,11 +345,12 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
     Seq q;
     for (int s = s0; s < s1; ++s) {
       load_seq<kTokens>(p, s, blockIdx.x == 0, q);
-      tiles += static_cast<int64_t>(span(q)) * q.segments;
-      segments += q.segments;
+      const int n = q.q_tiles * p.num_kv_heads;
+      tiles += static_cast<int64_t>(span(q)) * n;
+      segments += n;
       if (p.num_seqs <= kMaxDealtSeqs) {
         seq_tiles[s] = q.tiles;
-        seq_segments[s] = q.segments;
+        seq_segments[s] = n;
       }
     }
     // the sum of what the threads before this one have, and of all
@@ -390,7 +413,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       for (int s = s0; s < s1; ++s) {
         load_seq<kTokens>(p, s, false, q);
         const int pieces = length > 0 ? (q.tiles + length - 1) / length : span(q);
-        const int64_t n = static_cast<int64_t>(pieces) * q.segments;
+        const int64_t n = static_cast<int64_t>(pieces) * (q.q_tiles * p.num_kv_heads);
         if (off >= n) {
           off -= n;
           continue;
@@ -399,25 +422,26 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
         Walk w;
         w.q = q;
         if (length > 0) {
-          const int seg = static_cast<int>(off) / pieces, k = static_cast<int>(off) - seg * pieces;
+          const int k = enter_seq(w, off, pieces);
           const int j0 = static_cast<int>(static_cast<int64_t>(q.tiles) * k / pieces);
           const int j1 = static_cast<int>(static_cast<int64_t>(q.tiles) * (k + 1) / pieces);
-          w.off = seg * span(q) + kPieceTiles + j0;
+          w.v = kPieceTiles + j0;
           w.at = 0;
           w.end = j1 - j0;
-          *own_first = static_cast<int>(blockIdx.x) - k;
-          *own_last = *own_first + pieces - 1;
+          runs.own_first = static_cast<int>(blockIdx.x) - k;
+          runs.own_last = runs.own_first + pieces - 1;
         } else {
-          w.off = static_cast<int>(off);
+          w.v = enter_seq(w, off, pieces);
           w.at = want;
           w.end = run_start(runs, blockIdx.x + 1);
-          *own_first = -1;
         }
         *start_walk = w;
+        *own_first = runs.own_first;
+        *own_last = runs.own_last;
         // the row warps' first two pieces
         for (int u = 0; u < 2; ++u) {
           Piece x;
-          if (!next_piece<kTokens>(p, w, x)) x.n = 0;
+          if (!next_piece<kTokens>(p, runs, w, x)) x.n = 0;
           *piece_slot(u) = x;
         }
         *row_walk = w;
@@ -430,16 +454,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  // The CTAs that a piece's segment is split over.
-  auto piece_ctas = [&](const Piece& u, int* from, int* to) {
-    if (*own_first >= 0) {
-      *from = *own_first;
-      *to = *own_last;
-    } else {
-      *from = run_of(runs, u.first + kPieceTiles);
-      *to = run_of(runs, u.first + kPieceTiles + u.tiles - 1);
-    }
-  };
+  runs.own_first = *own_first;
+  runs.own_last = *own_last;
   // Whether a half holds any token of a piece, and any of the 32 MMA rows of row warp w.
   auto half_active = [&](const Piece& u, int h) { return u.tok0 + h * kHalfTokens < u.q_len; };
   auto warp_active = [&](const Piece& u, int w) {
@@ -454,10 +470,10 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
     const int r = (warp & 3) * 32 + lane;  // MMA row == TMEM lane; also a key of the tile, for V
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t s_mine = lane_addr + Lay::kSCol + half * kTileN + part * (kTileN / 2);
-    const uint32_t s_theirs = lane_addr + Lay::kSCol + half * kTileN + (part ^ 1) * (kTileN / 2);
+    const uint32_t s_theirs = s_mine ^ (kTileN / 2);
     const uint32_t p_addr = lane_addr + Lay::kPCol + half * (kTileN / 2) + part * (kTileN / 4);
-    const uint32_t o_addr = lane_addr + Lay::kOCol + half * kHeadDim + part * (kHeadDim / 2);
-    const uint32_t o_theirs = lane_addr + Lay::kOCol + half * kHeadDim + (part ^ 1) * (kHeadDim / 2);
+    const uint32_t o_addr = p_addr + (Lay::kOCol - Lay::kPCol);
+    const uint32_t o_theirs = o_addr ^ (kHeadDim / 2);
     auto wait_row = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, wait_ready(bar, parity, &abort_flag, p.status));
     };
@@ -474,38 +490,25 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       return p.records + ((2ll * cta + (begins ? 1 : 0)) * HALVES + half) * kRecordFloat4s + part * kPartChunks * kTileM + r;
     };
     const bool q_loader = (warp & (kHalfWarps - 1)) == 0 && lane == 0;
-    int q_asked = 0;  // the half's Qs asked for, by its loader
     auto load_q = [&](const Piece& x) {
       mbar_arrive_expect_tx(&q_full[half], kQBytes);
       tma_load_3d(sq + half * kQBytes, &tmap_q, 0, x.g * GROUP, x.q0 + x.tok0 + half * kHalfTokens, &q_full[half]);
-      ++q_asked;
     };
     auto wanted = [&](int u) { return piece_slot(u)->n > 0 && half_active(*piece_slot(u), half); };
+    if (q_loader && wanted(0)) load_q(*piece_slot(0));
     bool ok = true;
     int c = 0;       // tiles that this half took part in
-    int jt = 0;      // tiles of the CTA before this piece
+    int skipped = 0;  // and ones of pieces without rows for it (half 1)
     int units = 0;   // pieces so far
-    int q_used = 0;  // and those this half took part in
-    int ring = 0, ring_prev = 0;  // stage of this tile and the one before
-    uint32_t ph = 0, ph_prev = 0;
-    auto advance = [&] {
-      ring_prev = ring;
-      ph_prev = ph;
-      if (++ring == kRing) {
-        ring = 0;
-        ph ^= 1u;
-      }
-    };
+    int took = 0;    // and those this half took part in
     // until the half's last P V is done
-    auto wait_pv = [&]() -> bool {
-      return HALVES == 1 ? wait_row(&tile_done[ring_prev], ph_prev)
-                         : wait_row(&half_done[half], static_cast<uint32_t>((c - 1) & 1));
-    };
+    auto wait_pv = [&]() -> bool { return wait_row(&pv_done[half], static_cast<uint32_t>((c - 1) & 1)); };
     // V rows past the context weigh nothing but may hold anything, and so may drafted values that some row
     // does not see: in a tile that starts at drafted key `base`, this thread clears half of row r of what
     // lies past the last one, and elements that are no numbers, whose tokens it notes down.
     auto clear_values = [&](const Piece* cur, int base) -> bool {
-      if (!wait_row(&kv_full[ring], ph)) return false;
+      const int ring = c % kRing;  // (half 0 takes part in every tile)
+      if (!wait_row(&kv_full[ring], static_cast<uint32_t>(c / kRing & 1))) return false;
       const int key = base + r;
       if (key >= 0) {
         uint32_t any = 0u;
@@ -538,14 +541,13 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       const int tail_j = (cur->L - cur->q_len) / kTileN - cur->j0;  // from here on tiles hold drafted keys
       if (HALVES > 1 && !half_active(*cur, half)) {  // (half 1)
         // (the next piece's Q is wanted before half 0 can finish this one)
-        if (q_loader && q_asked == q_used && wanted(units + 1)) load_q(*piece_slot(units + 1));
+        if (q_loader && wanted(units + 1)) load_q(*piece_slot(units + 1));
         if (lane == 0) mbar_arrive(l_bar);
         ok = wait_row(l_bar, static_cast<uint32_t>(units & 1));
-        jt += n;
+        skipped += n;
         continue;
       }
-      if (q_loader && q_asked == q_used) load_q(*cur);
-      ++q_used;
+      ++took;
       if (!warp_active(*cur, warp)) {
         // a warp without rows keeps the others' pace (its rows of P and O may hold anything)
         for (int j = 0; ok && j < n; ++j, ++c) {
@@ -556,13 +558,11 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
           if (c > 0 && !(ok = wait_pv())) break;
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_full[half]);
-          advance();
         }
         if (!ok) break;
         if (lane == 0) mbar_arrive(l_bar);
         if (!(ok = wait_row(l_bar, static_cast<uint32_t>(units & 1)))) break;
         if (lane == 0) mbar_arrive(&o_free[half]);
-        jt += n;
         continue;
       }
       prefetch_l1(mask_row(cur));
@@ -573,18 +573,18 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
         // the piece's last scores are done with Q: the next piece's may land there
         if (j == n - 1 && q_loader && wanted(units + 1)) load_q(*piece_slot(units + 1));
         uint32_t v[2][32];
-        float top[kBlocksPerTile];  // largest raw score of each block, the partner's first
+        float top[kBlocksPerTile / 2];  // largest raw score of each block
 #pragma unroll
         for (int b = 0; b < kBlocksPerTile / 2; ++b)
           tmem_ld16_max(s_theirs + 16 * b, &v[b >> 1][16 * (b & 1)], top[b]);
         tmem_wait_ld();
         const bool tail = j >= tail_j;  // (uniform)
         if (tail) {
-          const int32_t* bits = mask_row(cur);
+          const int base = (j - tail_j) * kTileN - cur_lead(cur) + (part ^ 1) * (kTileN / 2);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t seen =
-                seen_bits(bits, cur->q_len, (j - tail_j) * kTileN + (part ^ 1) * (kTileN / 2) + 32 * h - cur_lead(cur));
+            if (base + 32 * h + 32 <= 0) continue;  // keys of the prefix (uniform)
+            const uint32_t seen = seen_bits(mask_row(cur), cur->q_len, base + 32 * h);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
               float x = -INFINITY;
@@ -595,19 +595,31 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
             }
           }
         }
+        const uint32_t cs = smem_addr(consts + (c + skipped) % kConstRing * kConsts);
+        // score factor of a part's block (8-bit pools: a hidden key's -inf * 0 is a NaN); read where it is used
+        auto factor = [&](int of_part, int b) -> float {
+          return Q8 ? fmaxf(lds_f32(cs + 4 * (of_part * (kBlocksPerTile / 2) + b)) * p.qk_scale, 1.17549435e-38f)
+                    : p.qk_scale;
+        };
+        auto largest = [&](int of_part) -> float {
+          if (!Q8) return fmaxf(max3f(top[0], top[1], top[2]), top[3]) * p.qk_scale;
+          return fmaxf(max3f(top[0] * factor(of_part, 0), top[1] * factor(of_part, 1), top[2] * factor(of_part, 2)),
+                       top[3] * factor(of_part, 3));
+        };
+        float mt = largest(part ^ 1);
 #pragma unroll
         for (int b = 0; b < kBlocksPerTile / 2; ++b)
-          tmem_ld16_max(s_mine + 16 * b, &v[b >> 1][16 * (b & 1)], top[kBlocksPerTile / 2 + b]);
+          tmem_ld16_max(s_mine + 16 * b, &v[b >> 1][16 * (b & 1)], top[b]);
         tmem_wait_ld();
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_free[half]);
         if (tail) {
-          const int32_t* bits = mask_row(cur);
+          const int base = (j - tail_j) * kTileN - cur_lead(cur) + part * (kTileN / 2);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t seen =
-                seen_bits(bits, cur->q_len, (j - tail_j) * kTileN + part * (kTileN / 2) + 32 * h - cur_lead(cur));
+            if (base + 32 * h + 32 <= 0) continue;
+            const uint32_t seen = seen_bits(mask_row(cur), cur->q_len, base + 32 * h);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
               float x = -INFINITY;
@@ -616,28 +628,12 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
                 if (!((seen >> i) & 1u)) v[h][i] = __float_as_uint(-INFINITY);
                 x = fmaxf(x, __uint_as_float(v[h][i]));
               }
-              top[kBlocksPerTile / 2 + 2 * h + b] = x;
+              top[2 * h + b] = x;
             }
           }
           if (!Q8 && half == 0 && !(ok = clear_values(cur, (j - tail_j) * kTileN - cur_lead(cur)))) break;
         }
-        float f[kBlocksPerTile / 2] = {};  // score factors of this thread's blocks (8-bit pools)
-        float mt;
-        const uint32_t cs = smem_addr(consts + (jt + j) % kConstRing * kConsts);
-        if (Q8) {
-          float g[kBlocksPerTile / 2];  // the partner's
-          lds_f32x4(cs + 4 * part * (kBlocksPerTile / 2), f);
-          lds_f32x4(cs + 4 * (part ^ 1) * (kBlocksPerTile / 2), g);
-          mt = -INFINITY;
-#pragma unroll
-          for (int b = 0; b < kBlocksPerTile / 2; ++b) {
-            f[b] = fmaxf(f[b] * p.qk_scale, 1.17549435e-38f);  // (a hidden key's -inf * 0 is a NaN)
-            g[b] = fmaxf(g[b] * p.qk_scale, 1.17549435e-38f);
-            mt = max3f(mt, top[kBlocksPerTile / 2 + b] * f[b], top[b] * g[b]);
-          }
-        } else {
-          mt = max3f(max3f(top[0], top[1], top[2]), max3f(top[3], top[4], top[5]), fmaxf(top[6], top[7])) * p.qk_scale;
-        }
+        mt = fmaxf(mt, largest(part));
         const bool grow = mt > m;  // true on the first tile in which the row sees a key
         float alpha = 1.f;
         if (grow) {
@@ -646,51 +642,42 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
         }
         l *= alpha;
         const float ref = m == -INFINITY ? 0.f : m;  // a row that has seen no key yet: weights of 0
-        float factor = p.qk_scale;
-        if (__any_sync(0xffffffffu, fabsf(ref) > kLargeScore)) {
+        const bool large = __any_sync(0xffffffffu, fabsf(ref) > kLargeScore);
+        if (large) {
           // score x factor has to be rounded as it was for the maximum, or the fused form below would leave
           // the rounding of a large product, whole powers of two, in the exponent
 #pragma unroll
-          for (int i = 0; i < kTileN / 2; ++i) {
-            float& x = reinterpret_cast<float&>(v[i >> 5][i & 31]);
-            x = __fmul_rn(x, Q8 ? f[i / kBlockSize] : factor);
-          }
-          factor = 1.f;
-#pragma unroll
-          for (int b = 0; b < kBlocksPerTile / 2; ++b) f[b] = 1.f;
-        }
-        if (Q8) {
-          float lf[kBlocksPerTile / 2];
-          lds_f32x4(cs + 4 * (kBlocksPerTile + part * (kBlocksPerTile / 2)), lf);
-#pragma unroll
           for (int b = 0; b < kBlocksPerTile / 2; ++b) {
-            const float nb = lf[b] - ref;
-            const float2 fb = make_float2(f[b], f[b]), nb2 = make_float2(nb, nb);
-            float2 sum = make_float2(0.f, 0.f);
+            const float fb = factor(part, b);
 #pragma unroll
-            for (int i = 0; i < kBlockSize / 2; ++i) {
-              const int e = b * kBlockSize + 2 * i;
-              const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[e >> 5][e & 31]),
-                                                      __uint_as_float(v[e >> 5][(e & 31) + 1])), fb, nb2);
-              const float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-              sum = __fadd2_rn(sum, y);
-              v[0][e >> 1] = pack_bf2(y.x, y.y);
-            }
-            l += (sum.x + sum.y) * lds_f32(cs + 4 * (2 * kBlocksPerTile + part * (kBlocksPerTile / 2) + b));
+            for (int i = kBlockSize * b; i < kBlockSize * (b + 1); ++i)
+              v[i >> 5][i & 31] = __float_as_uint(__fmul_rn(__uint_as_float(v[i >> 5][i & 31]), fb));
           }
-        } else {
-          const float2 fb = make_float2(factor, factor), nb2 = make_float2(-ref, -ref);
-          float2 sum = make_float2(0.f, 0.f);
+        }
+        const float2 ref2 = make_float2(-ref, -ref);
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int i = 0; i < kTileN / 4; ++i) {
-            const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[i >> 4][(2 * i) & 31]),
-                                                    __uint_as_float(v[i >> 4][(2 * i + 1) & 31])), fb, nb2);
+        for (int b = 0; b < kBlocksPerTile / 2; ++b) {
+          const float fb = large ? 1.f : factor(part, b);
+          const float2 fb2 = make_float2(fb, fb);
+          float2 nb2 = ref2;
+          if (Q8) {
+            const float nb = lds_f32(cs + 4 * (kBlocksPerTile + part * (kBlocksPerTile / 2) + b)) - ref;
+            nb2 = make_float2(nb, nb);
+            sum = make_float2(0.f, 0.f);
+          }
+#pragma unroll
+          for (int i = 0; i < kBlockSize / 2; ++i) {
+            const int e = b * kBlockSize + 2 * i;
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[e >> 5][e & 31]),
+                                                    __uint_as_float(v[e >> 5][(e & 31) + 1])), fb2, nb2);
             const float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
             sum = __fadd2_rn(sum, y);
-            v[0][i] = pack_bf2(y.x, y.y);
+            v[0][e >> 1] = pack_bf2(y.x, y.y);
           }
-          l += sum.x + sum.y;
+          if (Q8) l += (sum.x + sum.y) * lds_f32(cs + 4 * (2 * kBlocksPerTile + part * (kBlocksPerTile / 2) + b));
         }
+        if (!Q8) l += sum.x + sum.y;
         if (c > 0) {  // the previous P V: P's columns are free and O is up to date
           if (!(ok = wait_pv())) break;
           tc_fence_after_sync();
@@ -716,15 +703,13 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
         if (j == 0 && warp == 0 && lane == 0) {
           Walk w = *row_walk;
           Piece x;
-          if (!next_piece<kTokens>(p, w, x)) x.n = 0;
+          if (!next_piece<kTokens>(p, runs, w, x)) x.n = 0;
           *piece_slot(units + 2) = x;
           *row_walk = w;
         }
-        advance();
       }
       if (!ok) break;
       // ---- epilogue: this thread's 32 dims ----
-      jt += n;
       if (!(ok = wait_pv())) break;
       tc_fence_after_sync();
       uint32_t o[32];
@@ -781,11 +766,10 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       }
       const int tok0 = cur->tok0 + half * kHalfTokens;
       const bool row_ok = tok0 + r / GROUP < cur->q_len;
-      bool write = n == cur->tiles;
+      const int from = cur->from, to = cur->to;
+      bool write = from == to;
       if (!write) {
         // ---- a piece of a split segment: its record, and the warp that comes last weighs them all ----
-        int from, to;
-        piece_ctas(*cur, &from, &to);
         if (row_ok) {
           float4* rec = record_of(blockIdx.x, cur->j0 == 0);
 #pragma unroll
@@ -861,11 +845,12 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
     }
     if (!ok && q_loader) {  // leave no copy in flight (bounded waits)
       flag_error(p.status, PA_DEVFLAG_TIMEOUT);
-      if (q_asked > 0) mbar_wait(&q_full[half], static_cast<uint32_t>((q_asked - 1) & 1));
+      // (the Q of the piece given up on, or the next one's too)
+      if (took > 0) mbar_wait(&q_full[half], static_cast<uint32_t>((took - 1) & 1));
+      mbar_wait(&q_full[half], static_cast<uint32_t>(took & 1));
     }
   } else {
     if (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Lay::kOtherRegs));
-    Walk walk = *start_walk;
     if (warp == kMmaWarp) {
       // ============================ MMA issuer ============================
       // The whole warp walks the tiles, so that barriers, counters and descriptors stay uniform; one
@@ -932,7 +917,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
 #pragma unroll
             for (int kk = 1; kk < kTileN / 16; ++kk)  // 16 keys: 2 KiB of V, 8 columns of P
               umma_bf16_ts(o_tmem, p_tmem + kk * 8, v_desc + 128 * kk, kIdescO, 1u);
-            if (HALVES > 1) umma_commit(&half_done[h]);
+            umma_commit(&pv_done[h]);
           }
           ++pv_issued[h];
         }
@@ -943,23 +928,27 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
         }
         return true;
       };
-      Piece cur, nxt;
-      bool have = next_piece<kTokens>(p, walk, cur);
-      bool have_next = have && next_piece<kTokens>(p, walk, nxt);
+      // Pieces as the row warps have them: piece u + 1 was written before warp 0 read piece u's last scores.
       auto halves_of = [&](const Piece& u) { return HALVES > 1 && half_active(u, 1) ? 2 : 1; };
-      int halves = have ? halves_of(cur) : 0;
-      bool ok = have && issue_s(true, halves);
-      while (ok && have) {
-        const int n = cur.n, after = have_next ? halves_of(nxt) : 0;
+      int units = 0;
+      int n = piece_slot(0)->n, halves = n > 0 ? halves_of(*piece_slot(0)) : 0;
+      bool ok = n > 0 && issue_s(true, halves);
+      while (ok && n > 0) {
+        int after = 0, halves_after = 0;
         for (int j = 0; ok && j < n; ++j) {
           const bool last = j + 1 == n;
-          if (!last || have_next) ok = issue_s(last, last ? after : halves);
+          if (last) {
+            if (!(ok = wait_ready(s_free, static_cast<uint32_t>((s_issued[0] - 1) & 1), &abort_flag, p.status))) break;
+            const Piece& next = *piece_slot(units + 1);
+            after = next.n;
+            halves_after = halves_of(next);
+          }
+          if (!last || after > 0) ok = issue_s(last, last ? halves_after : halves);
           if (ok) ok = issue_pv(j == 0, halves);
         }
-        cur = nxt;
-        halves = after;
-        have = have_next;
-        if (have) have_next = next_piece<kTokens>(p, walk, nxt);
+        n = after;
+        halves = halves_after;
+        ++units;
       }
       // wait (bounded) until every MMA issued above has completed
       if (leader) {
@@ -970,13 +959,14 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
     } else if (warp == kProducerWarp) {
       // ============================ producer ============================
       const bool leader = elect_one();
+      Walk walk = *start_walk;
       Piece cur;
       bool ok = true;
       int jt = 0;
       constexpr int kStages = Q8 ? kRawRing : kRing;
       uint64_t* const full = Q8 ? raw_full : kv_full;
       uint64_t* const empty = Q8 ? raw_empty : tile_done;
-      while (ok && next_piece<kTokens>(p, walk, cur)) {
+      while (ok && next_piece<kTokens>(p, runs, walk, cur)) {
         const int32_t* row = p.block_tables + static_cast<int64_t>(cur.s) * p.max_blocks_per_seq;
         const int blocks = (cur.L + kBlockSize - 1) / kBlockSize;
         // 32 table entries (four tiles) at a time, one per lane, the next window in flight
@@ -1005,6 +995,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
 #pragma unroll
             for (int b = 0; b < kBlocksPerTile; ++b) rows[b] = __shfl_sync(0xffffffffu, tile, b);
             if (leader) {
+              raw_keys[st] = cur.L - (cur.j0 + j) * kTileN;
               mbar_arrive_expect_tx(&full[st], kRawBytes);
               uint8_t* dst = sraw + st * kRawBytes;
 #pragma unroll
@@ -1032,10 +1023,23 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
           }
         }
       }
+      int ended = -1;
+      if (Q8 && ok) {  // the converters' end: a stage without keys
+        const int st = jt % kStages;
+        ok = wait_ready(&empty[st], static_cast<uint32_t>((jt / kStages) & 1) ^ 1u, &abort_flag, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok && leader) {
+          raw_keys[st] = 0;
+          mbar_arrive(&full[st]);
+        }
+        if (ok && lane < kBlocksPerTile) mbar_arrive(&full[st]);
+        if (ok) ended = st;  // (its last fill has been read)
+      }
       // leave no copy in flight: wait (bounded) for the last fill of each stage
       if (Q8) asm volatile("cp.async.wait_all;" ::: "memory");
       if (lane == 0) {
         for (int st = 0; st < kStages && st < jt; ++st) {
+          if (st == ended) continue;
           const int last = st + ((jt - 1 - st) / kStages) * kStages;
           if (!mbar_wait(&full[st], static_cast<uint32_t>((last / kStages) & 1)))
             flag_error(p.status, PA_DEVFLAG_TIMEOUT);
@@ -1051,19 +1055,18 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       constexpr int kBatch = 4;       // rows a lane holds at once
       int st = 0, rs = 0, slot = 0;   // operand stage, stage of codes
       uint32_t ph = 0, rph = 0;
-      Piece cur;
-      bool ok = true;
-      while (ok && next_piece<kTokens>(p, walk, cur)) {
-        const int blocks = (cur.L + kBlockSize - 1) / kBlockSize;
-        for (int j = 0; j < cur.n; ++j) {
-          ok = wait_ready(&raw_full[rs], rph, &abort_flag, p.status) &&
-               wait_ready(&k_empty[st], ph ^ 1u, &abort_flag, p.status);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      for (;;) {
+          bool ok = wait_ready(&raw_full[rs], rph, &abort_flag, p.status);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          const int keys = raw_keys[rs];
+          if (keys == 0) break;
+          ok = wait_ready(&k_empty[st], ph ^ 1u, &abort_flag, p.status);
+          if (!__all_sync(0xffffffffu, ok)) break;
           const float* scales = raw_scale + rs * 2 * kBlocksPerTile + kMyBlocks * cw;
           uint32_t my_m = 0u;  // lane b: 2^(120 + e) of block b's value scale, a bf16 pair
           int my_high = 0;     // e where 120 + e is beyond bf16: then my_m is 2^120
           if (lane < kMyBlocks) {
-            const bool needed = (cur.j0 + j) * kBlocksPerTile + kMyBlocks * cw + lane < blocks;
+            const bool needed = (kMyBlocks * cw + lane) * kBlockSize < keys;
             const float value = needed ? scales[kBlocksPerTile + lane] : 1.f;
             const uint32_t bits = __float_as_uint(value) & 0x7fffffffu;
             const int e = static_cast<int>(bits >> 23) - 127;
@@ -1112,9 +1115,9 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
           __syncwarp();
           if (lane == 0) mbar_arrive(&kv_full[st]);
           ok = wait_ready(&tile_done[st], ph ^ 1u, &abort_flag, p.status);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (!__all_sync(0xffffffffu, ok)) break;
           dst = sv + st * kOpBytes;
-          const int keys_left = cur.L - (cur.j0 + j) * kTileN - row0;
+          const int keys_left = keys - row0;
           raw += kTileN * kQ8RowBytes;
 #pragma unroll
           for (int i0 = 0; i0 < 2 * kMyBlocks; i0 += kBatch) {
@@ -1158,7 +1161,6 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
             rph ^= 1u;
           }
           slot = (slot + 1) % kConstRing;
-        }
       }
     }
   }
@@ -1175,12 +1177,10 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
     Walk w = *start_walk;
     Piece u;
     int n = 0;
-    while (next_piece<kTokens>(p, w, u)) {
-      if (u.n == u.tiles || !warp_active(u, tid) || n++ < delivered[tid]) continue;
-      int from, to;
-      piece_ctas(u, &from, &to);
-      int32_t* counter = p.counters + from * kRowWarps + tid;
-      if (atomicAdd(counter, 1) == to - from) *counter = 0;
+    while (next_piece<kTokens>(p, runs, w, u)) {
+      if (u.from == u.to || !warp_active(u, tid) || n++ < delivered[tid]) continue;
+      int32_t* counter = p.counters + u.from * kRowWarps + tid;
+      if (atomicAdd(counter, 1) == u.to - u.from) *counter = 0;
     }
   }
 }
