@@ -26,7 +26,7 @@
 //   * Masks are looked at only in tiles that hold drafted keys.  There the row warps also clear V rows
 //     past the context, and elements of drafted values that are no numbers (0 x NaN would reach rows
 //     that do not see them); the rows that do see them get them back in the epilogue.
-//   * 8-bit pools: two more warps turn codes into bf16 (exact) in shared memory.  With the value scale of
+//   * 8-bit pools: six more warps turn codes into bf16 (exact) in shared memory.  With the value scale of
 //     a block written as 2^e f, 1 <= f < 2: V becomes 2^e code, f rides in the exponent of the weights and
 //     leaves the row sum again by 1 / f; the key scale multiplies the block's scores.
 // Every mbarrier wait is bounded; on timeout the CTA records PA_DEVFLAG_TIMEOUT, drains its own copies
@@ -189,7 +189,7 @@ template <bool Q8, int HALVES>
 struct Layout {
   static constexpr int kRowWarps = HALVES * kHalfWarps;
   static constexpr int kMmaWarp = kRowWarps, kProducerWarp = kRowWarps + 1, kConvWarp0 = kRowWarps + 2;
-  static constexpr int kConvWarps = Q8 ? 4 : 0;
+  static constexpr int kKWarps = Q8 ? 2 : 0, kVWarps = Q8 ? 4 : 0;
   static constexpr int kThreads = Q8 ? (HALVES == 1 ? 512 : 768) : (kRowWarps + 2) * 32;
   static constexpr int kCtasPerSm = HALVES == 1 ? 2 : 1;
   // Register split of the 8-bit kernels (setmaxnreg): what the CTA was launched with.
@@ -240,7 +240,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
   using Lay = Layout<Q8, HALVES>;
   constexpr int kThreads = Lay::kThreads, kRing = Lay::kRing, kRawRing = Lay::kRawRing;
   constexpr int kConstRing = Lay::kConstRing;
-  constexpr int kRowWarps = Lay::kRowWarps, kConvWarps = Lay::kConvWarps, kConvWarp0 = Lay::kConvWarp0;
+  constexpr int kRowWarps = Lay::kRowWarps, kConvWarp0 = Lay::kConvWarp0;
+  constexpr int kKWarps = Lay::kKWarps, kVWarps = Lay::kVWarps;
   constexpr int kMmaWarp = Lay::kMmaWarp, kProducerWarp = Lay::kProducerWarp;
   constexpr int kHalfTokens = kTileM / GROUP;      // query tokens of a half
   constexpr int kTokens = HALVES * kHalfTokens;    // and of a segment
@@ -300,17 +301,17 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
     mbar_init(l_bar, kRowWarps);
     mbar_init(drain, 1);
     for (int i = 0; i < kRing; ++i) {
-      mbar_init(&kv_full[i], Q8 ? kConvWarps : 1);
+      mbar_init(&kv_full[i], Q8 ? kKWarps : 1);
       mbar_init(&tile_done[i], 1);
       if (Q8) {
-        mbar_init(&v_full[i], kConvWarps);
+        mbar_init(&v_full[i], kVWarps);
         mbar_init(&k_empty[i], 1);
       }
     }
     if (Q8) {
       for (int i = 0; i < kRawRing; ++i) {
         mbar_init(&raw_full[i], 1 + kBlocksPerTile);
-        mbar_init(&raw_empty[i], kConvWarps);
+        mbar_init(&raw_empty[i], kKWarps + kVWarps);
       }
     }
     fence_barrier_init();
@@ -1046,121 +1047,103 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
         }
       }
       __syncwarp();
-    } else if (warp < kConvWarp0 + kConvWarps) {
+    } else if (warp < kConvWarp0 + kKWarps + kVWarps) {
       // ============================ converters (8-bit pools) ============================
-      constexpr int kMyBlocks = Q8 ? kBlocksPerTile / (Q8 ? kConvWarps : 1) : 1;  // blocks kMyBlocks cw .. of every tile
-      const int cw = warp - kConvWarp0;
-      const int row0 = cw * kMyBlocks * kBlockSize + (lane >> 2);
+      // kKWarps warps for K and kVWarps for V, each with its share of a tile's blocks, so that K runs ahead of
+      // the products that V waits for.
+      constexpr int kBatch = 2;  // rows a lane holds at once (the stores may alias the loads, so those come first)
+      const bool is_k = warp < kConvWarp0 + kKWarps;
+      const int cw = warp - kConvWarp0 - (is_k ? 0 : kKWarps);
+      const int blocks = kBlocksPerTile / (is_k ? kKWarps : kVWarps);  // blocks cw * blocks .. of every tile
+      const int row0 = cw * blocks * kBlockSize + (lane >> 2);
       const int c0 = 2 * (lane & 3);  // 16 codes of a row: two 16-byte chunks
-      constexpr int kBatch = 4;       // rows a lane holds at once
+      uint64_t* const full = is_k ? kv_full : v_full;
+      uint64_t* const empty = is_k ? k_empty : tile_done;
       int st = 0, rs = 0, slot = 0;   // operand stage, stage of codes
       uint32_t ph = 0, rph = 0;
       for (;;) {
-          bool ok = wait_ready(&raw_full[rs], rph, &abort_flag, p.status);
-          if (!__all_sync(0xffffffffu, ok)) break;
-          const int keys = raw_keys[rs];
-          if (keys == 0) break;
-          ok = wait_ready(&k_empty[st], ph ^ 1u, &abort_flag, p.status);
-          if (!__all_sync(0xffffffffu, ok)) break;
-          const float* scales = raw_scale + rs * 2 * kBlocksPerTile + kMyBlocks * cw;
-          uint32_t my_m = 0u;  // lane b: 2^(120 + e) of block b's value scale, a bf16 pair
-          int my_high = 0;     // e where 120 + e is beyond bf16: then my_m is 2^120
-          if (lane < kMyBlocks) {
-            const bool needed = (kMyBlocks * cw + lane) * kBlockSize < keys;
-            const float value = needed ? scales[kBlocksPerTile + lane] : 1.f;
-            const uint32_t bits = __float_as_uint(value) & 0x7fffffffu;
-            const int e = static_cast<int>(bits >> 23) - 127;
-            if (e > -127) {
-              my_high = e > 7 ? min(e, 127) : 0;
-              my_m = bf2_power(e > 7 ? 120 : 120 + e);
-            } else if (bits != 0u) {  // below the normal floats: e = -118 - clz
-              my_m = bf2_power(2 - __clz(bits));
-            }
-            // the row warps' constants of this warp's blocks
+        bool ok = wait_ready(&raw_full[rs], rph, &abort_flag, p.status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const int keys = raw_keys[rs];
+        if (keys == 0) break;
+        ok = wait_ready(&empty[st], ph ^ 1u, &abort_flag, p.status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        // lane b: what block b's codes, as bf16 pairs times 2^-120, are multiplied by: 2^120 for K, and
+        // 2^(120 + e) for V, e where 120 + e is beyond bf16 apart
+        uint32_t up = bf2_power(120);
+        int high = 0;
+        if (lane < blocks) {
+          const int blk = cw * blocks + lane;
+          const bool needed = blk * kBlockSize < keys;
+          const float* scales = raw_scale + rs * 2 * kBlocksPerTile + blk;
+          const float value = needed ? scales[kBlocksPerTile] : 1.f;
+          if (is_k) {  // the row warps' constants
             const float f = significand(value);
             float lf = 0.f, fi = 1.f;
             if (f != 1.f) {
               lf = __log2f(f);
               fi = 1.f / f;
             }
-            float* cs = consts + slot * kConsts + kMyBlocks * cw + lane;
-            cs[0] = needed ? scales[lane] : 1.f;
+            float* cs = consts + slot * kConsts + blk;
+            cs[0] = needed ? scales[0] : 1.f;
             cs[kBlocksPerTile] = lf;
             cs[2 * kBlocksPerTile] = fi;
-          }
-          const bool any_high = __any_sync(0xffffffffu, my_high != 0);
-          const uint8_t* raw = sraw + rs * kRawBytes + cw * kMyBlocks * kQ8TileBytes + 16 * lane;
-          const uint32_t up = bf2_power(120);
-          uint8_t* dst = sk + st * kOpBytes;
-#pragma unroll
-          for (int i0 = 0; i0 < 2 * kMyBlocks; i0 += kBatch) {
-            uint4 in[kBatch];  // (the stores may alias the loads, so these come first)
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) in[i] = lds128(raw + (i0 + i) * 512);
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              const uint4 w = in[i];
-              uint4 a, b;
-              codes4_to_bf2x2(w.x, a.x, a.y);
-              codes4_to_bf2x2(w.y, a.z, a.w);
-              codes4_to_bf2x2(w.z, b.x, b.y);
-              codes4_to_bf2x2(w.w, b.z, b.w);
-              a.x = mul_bf2(a.x, up); a.y = mul_bf2(a.y, up); a.z = mul_bf2(a.z, up); a.w = mul_bf2(a.w, up);
-              b.x = mul_bf2(b.x, up); b.y = mul_bf2(b.y, up); b.z = mul_bf2(b.z, up); b.w = mul_bf2(b.w, up);
-              *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * (i0 + i), c0)) = a;
-              *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * (i0 + i), c0 + 1)) = b;
+          } else {
+            const uint32_t bits = __float_as_uint(value) & 0x7fffffffu;
+            const int e = static_cast<int>(bits >> 23) - 127;
+            if (e > -127) {
+              high = e > 7 ? min(e, 127) : 0;
+              up = bf2_power(e > 7 ? 120 : 120 + e);
+            } else {  // below the normal floats: e = -118 - clz; zero
+              up = bits != 0u ? bf2_power(2 - __clz(bits)) : 0u;
             }
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&kv_full[st]);
-          ok = wait_ready(&tile_done[st], ph ^ 1u, &abort_flag, p.status);
-          if (!__all_sync(0xffffffffu, ok)) break;
-          dst = sv + st * kOpBytes;
-          const int keys_left = keys - row0;
-          raw += kTileN * kQ8RowBytes;
+        }
+        const bool any_high = __any_sync(0xffffffffu, high != 0);
+        const uint8_t* raw = sraw + rs * kRawBytes + (is_k ? 0 : kTileN * kQ8RowBytes) + cw * blocks * kQ8TileBytes + 16 * lane;
+        uint8_t* dst = (is_k ? sk : sv) + st * kOpBytes;
+        const int keys_left = keys - row0;
+        for (int i0 = 0; i0 < 2 * blocks; i0 += kBatch) {
+          uint4 in[kBatch];
 #pragma unroll
-          for (int i0 = 0; i0 < 2 * kMyBlocks; i0 += kBatch) {
-            uint4 in[kBatch];
+          for (int i = 0; i < kBatch; ++i) in[i] = lds128(raw + (i0 + i) * 512);
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) in[i] = lds128(raw + (i0 + i) * 512);
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              uint4 w = in[i];
-              // keys past the context weigh nothing, but may hold anything
-              if (8 * (i0 + i) >= keys_left) w = make_uint4(0u, 0u, 0u, 0u);
-              uint4 a, b;
-              codes4_to_bf2x2(w.x, a.x, a.y);
-              codes4_to_bf2x2(w.y, a.z, a.w);
-              codes4_to_bf2x2(w.z, b.x, b.y);
-              codes4_to_bf2x2(w.w, b.z, b.w);
-              const uint32_t m0 = __shfl_sync(0xffffffffu, my_m, (i0 + i) >> 1);
-              a.x = mul_bf2(a.x, m0); a.y = mul_bf2(a.y, m0); a.z = mul_bf2(a.z, m0); a.w = mul_bf2(a.w, m0);
-              b.x = mul_bf2(b.x, m0); b.y = mul_bf2(b.y, m0); b.z = mul_bf2(b.z, m0); b.w = mul_bf2(b.w, m0);
-              if (any_high) {  // a scale above 2^7: the rest of it
-                const uint32_t m1 = bf2_power(__shfl_sync(0xffffffffu, my_high, (i0 + i) >> 1));
-                a.x = mul_bf2(a.x, m1); a.y = mul_bf2(a.y, m1); a.z = mul_bf2(a.z, m1); a.w = mul_bf2(a.w, m1);
-                b.x = mul_bf2(b.x, m1); b.y = mul_bf2(b.y, m1); b.z = mul_bf2(b.z, m1); b.w = mul_bf2(b.w, m1);
-              }
-              *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * (i0 + i), c0)) = a;
-              *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * (i0 + i), c0 + 1)) = b;
+          for (int i = 0; i < kBatch; ++i) {
+            uint4 w = in[i];
+            // V past the context weighs nothing, but may hold anything
+            if (!is_k && 8 * (i0 + i) >= keys_left) w = make_uint4(0u, 0u, 0u, 0u);
+            uint4 a, b;
+            codes4_to_bf2x2(w.x, a.x, a.y);
+            codes4_to_bf2x2(w.y, a.z, a.w);
+            codes4_to_bf2x2(w.z, b.x, b.y);
+            codes4_to_bf2x2(w.w, b.z, b.w);
+            const uint32_t m0 = __shfl_sync(0xffffffffu, up, (i0 + i) >> 1);
+            a.x = mul_bf2(a.x, m0); a.y = mul_bf2(a.y, m0); a.z = mul_bf2(a.z, m0); a.w = mul_bf2(a.w, m0);
+            b.x = mul_bf2(b.x, m0); b.y = mul_bf2(b.y, m0); b.z = mul_bf2(b.z, m0); b.w = mul_bf2(b.w, m0);
+            if (any_high) {  // a scale above 2^7: the rest of it
+              const uint32_t m1 = bf2_power(__shfl_sync(0xffffffffu, high, (i0 + i) >> 1));
+              a.x = mul_bf2(a.x, m1); a.y = mul_bf2(a.y, m1); a.z = mul_bf2(a.z, m1); a.w = mul_bf2(a.w, m1);
+              b.x = mul_bf2(b.x, m1); b.y = mul_bf2(b.y, m1); b.z = mul_bf2(b.z, m1); b.w = mul_bf2(b.w, m1);
             }
+            *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * (i0 + i), c0)) = a;
+            *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * (i0 + i), c0 + 1)) = b;
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&v_full[st]);
-            mbar_arrive(&raw_empty[rs]);
-          }
-          if (++st == kRing) {
-            st = 0;
-            ph ^= 1u;
-          }
-          if (++rs == kRawRing) {
-            rs = 0;
-            rph ^= 1u;
-          }
-          slot = (slot + 1) % kConstRing;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&full[st]);
+          mbar_arrive(&raw_empty[rs]);
+        }
+        if (++st == kRing) {
+          st = 0;
+          ph ^= 1u;
+        }
+        if (++rs == kRawRing) {
+          rs = 0;
+          rph ^= 1u;
+        }
+        slot = (slot + 1) % kConstRing;
       }
     }
   }
