@@ -79,6 +79,12 @@ struct TreeParams {
   float qk_scale;  // scale * log2(e)
 };
 
+// a / b, a >= 0 and b > 0: a division of 64 bits takes several hundred cycles, one of 32 a quarter of that.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // The sequence whose tiles a run is in.
 struct Seq {
   int s, q0, q_len, L;
@@ -125,8 +131,8 @@ struct Walk {
 
 // w.q is set; the walk begins at place `off` of its sequence's `length`-long segments.
 __device__ __forceinline__ int enter_seq(Walk& w, int64_t off, int length) {
-  const int64_t seg = off / length;
-  w.g = static_cast<int>(seg / w.q.q_tiles);
+  const int64_t seg = quotient(off, length);
+  w.g = static_cast<int>(quotient(seg, w.q.q_tiles));
   w.q_tile = static_cast<int>(seg - static_cast<int64_t>(w.g) * w.q.q_tiles);
   return static_cast<int>(off - seg * length);
 }
@@ -139,10 +145,10 @@ struct Runs {
   int runs;
   int own_first, own_last;  // the CTAs of the one segment this CTA has a piece of; -1: it has a run of all tiles
 };
-__device__ __forceinline__ int64_t run_start(const Runs& x, int64_t r) { return x.total * r / x.runs; }
+__device__ __forceinline__ int64_t run_start(const Runs& x, int64_t r) { return quotient(x.total * r, x.runs); }
 // The run that holds a tile (none is empty).
 __device__ __forceinline__ int run_of(const Runs& x, int64_t tile) {
-  return static_cast<int>(((tile + 1) * x.runs + x.total - 1) / x.total - 1);
+  return static_cast<int>(quotient((tile + 1) * x.runs + x.total - 1, x.total) - 1);
 }
 
 template <int TOKENS>
@@ -208,7 +214,7 @@ struct Layout {
   static constexpr int kNumBars = 6 * HALVES + 2 + 2 * kRing + (Q8 ? 2 * kRawRing + 2 * kRing : 0);
   static constexpr int kMiscOff = kBarOff + (kNumBars + 1) / 2 * 16;
   static constexpr int kPieceOff = kMiscOff + 16 + 4 * kRowWarps;  // the row warps' pieces and the walks
-  static constexpr int kOddOff = kPieceOff + kPieceRing * static_cast<int>(sizeof(Piece)) + 2 * kWalkBytes;
+  static constexpr int kOddOff = kPieceOff + kPieceRing * static_cast<int>(sizeof(Piece)) + 2 * kWalkBytes + static_cast<int>(sizeof(Runs));
   static constexpr int kKeysOff = kOddOff;  // 8-bit pools: [kRawRing]
   // drafted tokens whose values are no numbers: [3][any; 32 words of bits]
   static constexpr int kBytes = kOddOff + (Q8 ? 4 * kRawRing : 3 * (1 + kMaxMaskWords) * 4);
@@ -287,6 +293,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
   };
   Walk* const row_walk = reinterpret_cast<Walk*>(smem + Lay::kPieceOff + kPieceRing * static_cast<int>(sizeof(Piece)));
   Walk* const start_walk = row_walk + 1;
+  Runs* const shared_runs = reinterpret_cast<Runs*>(start_walk + 1);
   int* delivered = misc + 4;  // [row warps] pieces of split segments that each row warp has delivered
 
   if (tid == 0) {
@@ -335,118 +342,151 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
   Runs runs;
   runs.own_first = runs.own_last = -1;
   {
-    int64_t* warp_sum = reinterpret_cast<int64_t*>(smem);  // (before any copy lands there)
-    int* seq_tiles = reinterpret_cast<int*>(smem + 1024);  // of every sequence, and its segments
-    int* seq_segments = seq_tiles + kMaxDealtSeqs;
-    int* tried = seq_segments + kMaxDealtSeqs;  // CTAs wanted by each warp's piece length
     const int ctas = static_cast<int>(gridDim.x);
-    const int per = (p.num_seqs + kThreads - 1) / kThreads;
-    const int s0 = min(tid * per, p.num_seqs), s1 = min(s0 + per, p.num_seqs);
-    int64_t tiles = 0, segments = 0;
-    Seq q;
-    for (int s = s0; s < s1; ++s) {
-      load_seq<kTokens>(p, s, blockIdx.x == 0, q);
-      const int n = q.q_tiles * p.num_kv_heads;
-      tiles += static_cast<int64_t>(span(q)) * n;
-      segments += n;
-      if (p.num_seqs <= kMaxDealtSeqs) {
-        seq_tiles[s] = q.tiles;
-        seq_segments[s] = n;
-      }
-    }
-    // the sum of what the threads before this one have, and of all
-    auto scan = [&](int64_t mine, int64_t* sums, int64_t* total) -> int64_t {
-      int64_t upto = mine;
+    // CTAs of their own are dealt under the shortest piece length for which the pieces are no more than the
+    // CTAs; no shorter one fits, and one longer by kSplitTiles is no better than equal runs.
+    auto shortest = [&](int segments) {
+      return max(static_cast<int>(quotient(runs.total - kPieceTiles * segments + ctas - 1, ctas)), kMinPiece);
+    };
+    auto inclusive = [&](auto x) {
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
-        if (lane >= d) upto += x;
+        const auto y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
       }
-      if (lane == 31) sums[warp] = upto;
-      __syncthreads();
-      int64_t before = upto - mine;
-      *total = 0;
-      for (int i = 0; i < kThreads / 32; ++i) {
-        if (i < warp) before += sums[i];
-        *total += sums[i];
-      }
-      return before;
+      return x;
     };
-    // (a number of segments beyond the CTAs' matters no further)
-    const int most = __reduce_max_sync(0xffffffffu, static_cast<int>(min(segments, int64_t{ctas} + 1)));
-    const int some = __reduce_add_sync(0xffffffffu, static_cast<int>(min(segments, int64_t{ctas} + 1)));
-    if (lane == 0) tried[warp] = most > ctas ? most : some;
-    int64_t total;
-    const int64_t before_tiles = scan(tiles, warp_sum, &runs.total);
-    int64_t all_segments = 0;
-    for (int i = 0; i < kThreads / 32; ++i) all_segments += tried[i];
-    runs.runs = static_cast<int>(min(static_cast<int64_t>(ctas), max(runs.total, int64_t{1})));
-    // CTAs of their own: the shortest piece length under which the pieces are no more than the CTAs; every
-    // warp tries one.  No shorter one fits, and a longer one is no better than equal runs.
-    int length = 0;
-    if (p.num_seqs <= kMaxDealtSeqs && all_segments <= ctas && runs.total > 0) {
-      __syncthreads();  // (`tried` has been read)
-      const int mine = max(static_cast<int>((runs.total - kPieceTiles * all_segments + ctas - 1) / ctas), kMinPiece) +
-                       min(warp, kSplitTiles);
-      int wanted = 0;
-      for (int s = lane; s < p.num_seqs; s += 32) wanted += seq_segments[s] * ((seq_tiles[s] + mine - 1) / mine);
-      wanted = __reduce_add_sync(0xffffffffu, wanted);
-      if (lane == 0) tried[warp] = wanted <= ctas ? mine : 0;
-      __syncthreads();
-      for (int i = kSplitTiles; i >= 0; --i)
-        if (tried[i] > 0) length = tried[i];
-    }
-    int64_t before, mine;  // this thread's sequences: CTAs, or tiles
-    int64_t want;          // which one of them this CTA looks for
-    if (length > 0) {
-      mine = 0;
-      for (int s = s0; s < s1; ++s) mine += seq_segments[s] * ((seq_tiles[s] + length - 1) / length);
-      before = scan(mine, warp_sum + kThreads / 32, &total);
-      want = blockIdx.x;
-      if (want >= total) want = -1;
+    // This CTA's run begins at place `off` of sequence q, or its piece is number `off` of q's: by one thread.
+    auto settle = [&](const Seq& q, int64_t off, int length) {
+      Walk w;
+      w.q = q;
+      if (length > 0) {
+        const int pieces = (q.tiles + length - 1) / length;
+        const int k = enter_seq(w, off, pieces);
+        const int j0 = static_cast<int>(quotient(static_cast<int64_t>(q.tiles) * k, pieces));
+        const int j1 = static_cast<int>(quotient(static_cast<int64_t>(q.tiles) * (k + 1), pieces));
+        w.v = kPieceTiles + j0;
+        w.at = 0;  // the walk ends with the piece
+        w.end = j1 - j0;
+        runs.own_first = static_cast<int>(blockIdx.x) - k;
+        runs.own_last = runs.own_first + pieces - 1;
+      } else {
+        w.v = enter_seq(w, off, span(q));
+        w.at = run_start(runs, blockIdx.x);
+        w.end = run_start(runs, blockIdx.x + 1);
+      }
+      *start_walk = w;
+      *own_first = runs.own_first;
+      *own_last = runs.own_last;
+      // the row warps' first two pieces
+      for (int u = 0; u < 2; ++u) {
+        Piece x;
+        if (!next_piece<kTokens>(p, runs, w, x)) x.n = 0;
+        *piece_slot(u) = x;
+      }
+      *row_walk = w;
+    };
+    if (p.num_seqs <= 32) {
+      // one warp, a sequence per lane: the CTA need not meet
+      if (warp == 0) {
+        Seq q;
+        q.q_tiles = 0;
+        q.tiles = 1;
+        if (lane < p.num_seqs) load_seq<kTokens>(p, lane, blockIdx.x == 0, q);
+        const int segments = q.q_tiles * p.num_kv_heads;
+        const int64_t tiles = static_cast<int64_t>(span(q)) * segments;
+        int64_t upto = inclusive(tiles);
+        runs.total = __shfl_sync(0xffffffffu, upto, 31);
+        runs.runs = static_cast<int>(min(static_cast<int64_t>(ctas), max(runs.total, int64_t{1})));
+        const int all = __reduce_add_sync(0xffffffffu, segments);
+        int length = 0, pieces = 0;
+        if (all <= ctas && runs.total > 0) {
+          const int low = shortest(all);
+          for (int t = 0; t <= kSplitTiles && length == 0; ++t) {
+            pieces = segments * ((q.tiles + low + t - 1) / (low + t));
+            if (__reduce_add_sync(0xffffffffu, pieces) <= ctas) length = low + t;
+          }
+        }
+        const int64_t mine = length > 0 ? pieces : tiles;
+        if (length > 0) upto = inclusive(pieces);
+        const int64_t want = length > 0 ? blockIdx.x
+                             : static_cast<int>(blockIdx.x) < runs.runs ? run_start(runs, blockIdx.x) : -1;
+        if (lane == 0) *shared_runs = runs;
+        if (want >= upto - mine && want < upto) settle(q, want - (upto - mine), length);
+      }
     } else {
-      before = before_tiles;
-      mine = tiles;
-      want = static_cast<int>(blockIdx.x) < runs.runs && runs.total > 0 ? run_start(runs, blockIdx.x) : -1;
-    }
-    if (want >= before && want < before + mine) {
-      int64_t off = want - before;
+      int64_t* warp_sum = reinterpret_cast<int64_t*>(smem);  // (before any copy lands there)
+      int* seq_tiles = reinterpret_cast<int*>(smem + 1024);  // of every sequence, and its segments
+      int* seq_segments = seq_tiles + kMaxDealtSeqs;
+      int* tried = seq_segments + kMaxDealtSeqs;  // CTAs wanted by each warp's piece length
+      const int per = (p.num_seqs + kThreads - 1) / kThreads;
+      const int s0 = min(tid * per, p.num_seqs), s1 = min(s0 + per, p.num_seqs);
+      int64_t mine = 0, segments = 0;  // tiles, then CTAs wanted
+      Seq q;
       for (int s = s0; s < s1; ++s) {
-        load_seq<kTokens>(p, s, false, q);
-        const int pieces = length > 0 ? (q.tiles + length - 1) / length : span(q);
-        const int64_t n = static_cast<int64_t>(pieces) * (q.q_tiles * p.num_kv_heads);
-        if (off >= n) {
+        load_seq<kTokens>(p, s, blockIdx.x == 0, q);
+        const int n = q.q_tiles * p.num_kv_heads;
+        mine += static_cast<int64_t>(span(q)) * n;
+        segments += n;
+        if (p.num_seqs <= kMaxDealtSeqs) {
+          seq_tiles[s] = q.tiles;
+          seq_segments[s] = n;
+        }
+      }
+      // the sum of what the threads before this one have, and of all
+      auto scan = [&](int64_t x, int64_t* sums, int64_t* total) -> int64_t {
+        const int64_t upto = inclusive(x);
+        if (lane == 31) sums[warp] = upto;
+        __syncthreads();
+        int64_t first = upto - x;
+        *total = 0;
+        for (int i = 0; i < kThreads / 32; ++i) {
+          if (i < warp) first += sums[i];
+          *total += sums[i];
+        }
+        return first;
+      };
+      // (a number of segments beyond the CTAs' matters no further)
+      const int some = static_cast<int>(min(segments, int64_t{ctas} + 1));
+      const int most = __reduce_max_sync(0xffffffffu, some), sum = __reduce_add_sync(0xffffffffu, some);
+      if (lane == 0) tried[warp] = most > ctas ? most : sum;
+      int64_t before = scan(mine, warp_sum, &runs.total);
+      int64_t all = 0;
+      for (int i = 0; i < kThreads / 32; ++i) all += tried[i];
+      runs.runs = static_cast<int>(min(static_cast<int64_t>(ctas), max(runs.total, int64_t{1})));
+      int length = 0;
+      if (p.num_seqs <= kMaxDealtSeqs && all <= ctas && runs.total > 0) {
+        __syncthreads();  // (`tried` has been read)
+        const int t = shortest(static_cast<int>(all)) + min(warp, kSplitTiles);  // every warp tries a length
+        int wanted = 0;
+        for (int s = lane; s < p.num_seqs; s += 32) wanted += seq_segments[s] * ((seq_tiles[s] + t - 1) / t);
+        wanted = __reduce_add_sync(0xffffffffu, wanted);
+        if (lane == 0) tried[warp] = wanted <= ctas ? t : 0;
+        __syncthreads();
+        for (int i = kSplitTiles; i >= 0; --i)
+          if (tried[i] > 0) length = tried[i];
+      }
+      int64_t want = static_cast<int>(blockIdx.x) < runs.runs ? run_start(runs, blockIdx.x) : -1;
+      if (length > 0) {
+        mine = 0;
+        for (int s = s0; s < s1; ++s) mine += seq_segments[s] * ((seq_tiles[s] + length - 1) / length);
+        int64_t total;
+        before = scan(mine, warp_sum + kThreads / 32, &total);
+        want = blockIdx.x;
+      }
+      if (tid == 0) *shared_runs = runs;
+      if (want >= before && want < before + mine) {
+        int64_t off = want - before;
+        for (int s = s0; s < s1; ++s) {
+          load_seq<kTokens>(p, s, false, q);
+          const int64_t n = static_cast<int64_t>(length > 0 ? (q.tiles + length - 1) / length : span(q)) *
+                            (q.q_tiles * p.num_kv_heads);
+          if (off < n) {
+            settle(q, off, length);
+            break;
+          }
           off -= n;
-          continue;
         }
-        // the walk begins here; with CTAs of their own, it ends with the piece
-        Walk w;
-        w.q = q;
-        if (length > 0) {
-          const int k = enter_seq(w, off, pieces);
-          const int j0 = static_cast<int>(static_cast<int64_t>(q.tiles) * k / pieces);
-          const int j1 = static_cast<int>(static_cast<int64_t>(q.tiles) * (k + 1) / pieces);
-          w.v = kPieceTiles + j0;
-          w.at = 0;
-          w.end = j1 - j0;
-          runs.own_first = static_cast<int>(blockIdx.x) - k;
-          runs.own_last = runs.own_first + pieces - 1;
-        } else {
-          w.v = enter_seq(w, off, pieces);
-          w.at = want;
-          w.end = run_start(runs, blockIdx.x + 1);
-        }
-        *start_walk = w;
-        *own_first = runs.own_first;
-        *own_last = runs.own_last;
-        // the row warps' first two pieces
-        for (int u = 0; u < 2; ++u) {
-          Piece x;
-          if (!next_piece<kTokens>(p, runs, w, x)) x.n = 0;
-          *piece_slot(u) = x;
-        }
-        *row_walk = w;
-        break;
       }
     }
   }
@@ -455,6 +495,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  runs = *shared_runs;
   runs.own_first = *own_first;
   runs.own_last = *own_last;
   // Whether a half holds any token of a piece, and any of the 32 MMA rows of row warp w.
@@ -1229,7 +1270,13 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
   p.max_query_len = a.max_query_len;
   p.num_seqs = a.num_seqs;
   p.qk_scale = a.scale * 1.4426950408889634f;
-  kernel<<<Lay::kCtasPerSm * sms, Lay::kThreads, Lay::kBytes, stream>>>(tq, tk, tv, p);
+  // no more CTAs than there can be tiles
+  constexpr int kTokens = HALVES * kTileM / GROUP;
+  const int64_t segments = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * ((a.max_query_len + kTokens - 1) / kTokens);
+  const int64_t longest = (static_cast<int64_t>(a.max_blocks_per_seq) * kBlockSize + kTileN - 1) / kTileN;
+  const int64_t most = Lay::kCtasPerSm * sms;
+  const int64_t grid = segments >= most || longest >= most || segments * longest >= most ? most : segments * longest;
+  kernel<<<static_cast<unsigned>(grid), Lay::kThreads, Lay::kBytes, stream>>>(tq, tk, tv, p);
   return cudaGetLastError();
 }
 
