@@ -708,7 +708,7 @@ def pa_copy_blocks_q8(key_cache, value_cache, key_scale, value_scale, block_mapp
         _check(st, "pa_copy_blocks_q8")
 
 
-_packed_axes = {}  # pair_axes as the call takes them, by the tuple
+_packed_axes = {}  # of the pair_axes seen: their packed form and their last axis
 
 
 def _pair_axes(pair_axes, num_axes):
@@ -720,10 +720,12 @@ def _pair_axes(pair_axes, num_axes):
     if packed is None:
         if len(key) != 32 or not all(isinstance(a, int) and 0 <= a < 4 for a in key):
             raise ValueError("pair_axes must be 32 axis numbers, one per rotation pair")
-        packed = _packed_axes[key] = sum(a << (2 * i) for i, a in enumerate(key))
-    if max(key) >= num_axes:
-        raise ValueError(f"pair_axes names axis {max(key)}, positions has {num_axes}")
-    return packed
+        if len(_packed_axes) >= 64:
+            _packed_axes.clear()
+        packed = _packed_axes[key] = sum(a << (2 * i) for i, a in enumerate(key)), max(key)
+    if packed[1] >= num_axes:
+        raise ValueError(f"pair_axes names axis {packed[1]}, positions has {num_axes}")
+    return packed[0]
 
 
 def _rope_append_at_args(args, cos_sin, positions, pair_axes, dev):

@@ -29,6 +29,9 @@ constexpr int kRowsAtOnce = 32 / kRowLanes;  // 4
 constexpr int kUnroll = 4;                   // rows a lane has in flight
 constexpr int kWarpRows = kRowsAtOnce * kUnroll;  // 16: a warp's share of a round
 constexpr int kCtaWarps = 4;  // of a CTA whose warps serve an item each
+constexpr int64_t kManyItems = 2 * 152;   // more items than CTAs of 16 warps run side by side
+constexpr int64_t kManyShort = 8 * 152;  // (8 bits, up to 8 tokens: 512 items 3.2 us with two warps each, 3.9 with one;
+                                         // 4096 items 7.4 and 6.2)
 
 // The list of sequence s; false where there is nothing to do, or it was reported.
 __device__ __forceinline__ bool kept_list(const CompactArgs& a, int32_t s, bool report, int32_t* start, int32_t* n,
@@ -44,26 +47,44 @@ __device__ __forceinline__ bool kept_list(const CompactArgs& a, int32_t s, bool 
   return true;
 }
 
-// Source position of the list's entry i, or -1 (reported) where it does not rise or lies past the
-// block-table row.
-__device__ __forceinline__ int64_t source_of(const CompactArgs& a, const int32_t* kept, int32_t i, int32_t first,
-                                             bool report) {
-  const int32_t k = __ldg(kept + i);
-  const int32_t before = i > 0 ? __ldg(kept + i - 1) : -1;
-  const int64_t p = static_cast<int64_t>(first) + k;
-  if (k <= before || k < i || p >= static_cast<int64_t>(a.max_blocks_per_seq) * kBlockSize) {
-    if (report) flag_error(a.status, PA_DEVFLAG_BAD_CONTEXT);
-    return -1;
+// Source positions of N entries i[u] of a list (below 0: none wanted), or -1; an entry that does not rise
+// or lies past the block-table row is reported.  Loads of one kind come side by side, here and below: a
+// round is a chain of list, tables and rows.
+template <int N>
+__device__ __forceinline__ bool sources_of(const CompactArgs& a, const int32_t* kept, const int32_t (&i)[N],
+                                           int32_t first, int32_t (&src)[N]) {
+  int32_t k[N], before[N];
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    k[u] = i[u] >= 0 ? __ldg(kept + i[u]) : 0;
+    before[u] = i[u] > 0 ? __ldg(kept + i[u] - 1) : -1;
   }
-  return p;
+  bool fine = true;
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const int64_t p = static_cast<int64_t>(first) + k[u];
+    const bool bad = k[u] <= before[u] || k[u] < i[u] || p > INT32_MAX ||
+                     p >= static_cast<int64_t>(a.max_blocks_per_seq) * kBlockSize;
+    if (i[u] >= 0 && bad) fine = false;
+    src[u] = i[u] < 0 || bad ? -1 : static_cast<int32_t>(p);
+  }
+  return fine;
 }
 
-// Physical block of position p of a sequence, or -1 (reported).
-__device__ __forceinline__ int32_t block_of(const CompactArgs& a, const int32_t* table, int64_t p, bool report) {
-  const int32_t b = __ldg(table + p / kBlockSize);
-  if (b >= 0 && b < a.num_blocks) return b;
-  if (report) flag_error(a.status, PA_DEVFLAG_BAD_BLOCK);
-  return -1;
+// Physical blocks of N positions (below 0: none wanted), or -1; false where one is bad.
+template <int N>
+__device__ __forceinline__ bool blocks_of(const CompactArgs& a, const int32_t* table, const int32_t (&p)[N],
+                                          int32_t (&block)[N]) {
+#pragma unroll
+  for (int u = 0; u < N; ++u) block[u] = p[u] >= 0 ? __ldg(table + p[u] / kBlockSize) : 0;
+  bool fine = true;
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const bool bad = block[u] < 0 || block[u] >= a.num_blocks;
+    if (bad) fine = false;
+    if (bad || p[u] < 0) block[u] = -1;
+  }
+  return fine;
 }
 
 // WARPS warps (of one CTA, if more than one) serve one (sequence, K/V head, pool).
@@ -77,38 +98,41 @@ __global__ void __launch_bounds__((WARPS > 1 ? WARPS : kCtaWarps) * 32) compact_
   const bool is_k = (item & 1) == 0;
   const int h = static_cast<int>((item >> 1) % a.num_kv_heads);
   const int32_t s = static_cast<int32_t>((item >> 1) / a.num_kv_heads);
-  const bool report = is_k && h == 0 && lane % kRowLanes == 0;
+  const bool report = is_k && h == 0;
   int32_t start, n, first;
-  if (!kept_list(a, s, report, &start, &n, &first)) return;
+  if (!kept_list(a, s, report && lane == 0, &start, &n, &first)) return;
   const int32_t* const kept = a.kept + start;
   const int32_t* const table = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
   uint4* const pool = static_cast<uint4*>(is_k ? a.key_cache : a.value_cache);
-  // 16-byte chunk of this lane in the row of position p
-  auto place = [&](int32_t block, int64_t p) -> int64_t {
-    return ((static_cast<int64_t>(block) * a.num_kv_heads + h) * kBlockSize + p % kBlockSize) * kRowLanes +
+  const int mine = (WARPS > 1 ? warp : 0) * kWarpRows + lane / kRowLanes;
+  auto place = [&](int32_t block, int32_t p) -> uint4* {  // 16-byte chunk of this lane in the row of position p
+    return pool + ((static_cast<int64_t>(block) * a.num_kv_heads + h) * kBlockSize + p % kBlockSize) * kRowLanes +
            lane % kRowLanes;
   };
-  const int mine = (WARPS > 1 ? warp : 0) * kWarpRows + lane / kRowLanes;
   for (int32_t i0 = 0; i0 < n; i0 += WARPS * kWarpRows) {
-    uint4 x[kUnroll];
-    int64_t to[kUnroll];
+    int32_t i[kUnroll], src[kUnroll], dst[kUnroll], from[kUnroll], at[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int32_t i = i0 + mine + u * kRowsAtOnce;
-      to[u] = -1;
-      if (i >= n) continue;
-      const int64_t src = source_of(a, kept, i, first, report);
-      const int64_t dst = static_cast<int64_t>(first) + i;
-      if (src < 0 || src == dst) continue;
-      const int32_t from = block_of(a, table, src, report), at = block_of(a, table, dst, report);
-      if (from < 0 || at < 0) continue;
-      x[u] = pool[place(from, src)];
-      to[u] = place(at, dst);
+      const int32_t x = i0 + mine + u * kRowsAtOnce;
+      i[u] = x < n ? x : -1;
     }
+    const bool fine = sources_of(a, kept, i, first, src);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      dst[u] = src[u] >= 0 ? first + i[u] : -1;
+      if (src[u] == dst[u]) src[u] = dst[u] = -1;  // it stays
+    }
+    const bool blocks = blocks_of(a, table, src, from) & blocks_of(a, table, dst, at);
+    if (report && !fine) flag_error(a.status, PA_DEVFLAG_BAD_CONTEXT);
+    if (report && !blocks) flag_error(a.status, PA_DEVFLAG_BAD_BLOCK);
+    uint4 x[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (from[u] >= 0 && at[u] >= 0) x[u] = *place(from[u], src[u]);
     if (WARPS > 1) __syncthreads(); else __syncwarp();  // a round is read before it is written
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
-      if (to[u] >= 0) pool[to[u]] = x[u];
+      if (from[u] >= 0 && at[u] >= 0) *place(at[u], dst[u]) = x[u];
   }
 }
 
@@ -139,10 +163,9 @@ __device__ __forceinline__ uint4 floats16_to_codes(const float (&y)[16], float i
 template <int WARPS>
 __global__ void __launch_bounds__((WARPS > 1 ? WARPS : kCtaWarps) * 32) compact_q8_kernel(const CompactArgs a) {
   const int lane = threadIdx.x & 31;
-  const int warp = threadIdx.x >> 5;
-  const int64_t item = WARPS > 1 ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kCtaWarps + warp;
-  const int64_t items = 2ll * a.num_seqs * a.num_kv_heads;
-  if (item >= items) return;
+  const int warp = WARPS > 1 ? threadIdx.x >> 5 : 0;
+  const int64_t item = WARPS > 1 ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kCtaWarps + (threadIdx.x >> 5);
+  if (item >= 2ll * a.num_seqs * a.num_kv_heads) return;
   const bool is_k = (item & 1) == 0;
   const int h = static_cast<int>((item >> 1) % a.num_kv_heads);
   const int32_t s = static_cast<int32_t>((item >> 1) / a.num_kv_heads);
@@ -155,63 +178,73 @@ __global__ void __launch_bounds__((WARPS > 1 ? WARPS : kCtaWarps) * 32) compact_
   float* const scales = is_k ? a.key_scale : a.value_scale;
   const int row0 = lane / kQ8RowLanes, l = lane % kQ8RowLanes;
   const int64_t b_lo = first / kBlockSize, b_hi = (static_cast<int64_t>(first) + n - 1) / kBlockSize;
-  for (int64_t b0 = b_lo; b0 <= b_hi; b0 += WARPS) {
-    const int64_t b = b0 + (WARPS > 1 ? warp : 0);
-    bool live = b <= b_hi;
-    // rows o0 .. o1 - 1 of the block are written; row o is the list's entry b * 16 + o - first
-    const int o0 = b == b_lo ? first % kBlockSize : 0;
-    const int o1 = live ? static_cast<int>(min(static_cast<int64_t>(kBlockSize), first + n - b * kBlockSize)) : 0;
-    const int32_t at = live ? block_of(a, table, b * kBlockSize, report && lane == 0) : -1;
-    live = at >= 0;
-    const int64_t tile = (static_cast<int64_t>(at < 0 ? 0 : at) * a.num_kv_heads + h);
-    float y[kQ8RowSteps][16];
-    float amax = 0.f, old = 0.f;
-    if (live) {
-      bool bad_index = false, bad_scale = false;
-      uint4 c[kQ8RowSteps];
-      float from_scale[kQ8RowSteps];
-      old = scales[tile];
+  // A round: a destination block per warp.
+  struct Round {
+    uint4 c[kQ8RowSteps];
+    float scale[kQ8RowSteps], old;  // of the rows' blocks, and the destination's
+    int32_t block;                  // or -1: nothing to write
+  };
+  // rows o0 .. o1 - 1 of block b are written; row o is the list's entry b * 16 + o - first
+  auto first_row = [&](int64_t b) { return b == b_lo ? first % kBlockSize : 0; };
+  auto last_row = [&](int64_t b) {
+    return b <= b_hi ? static_cast<int>(min(static_cast<int64_t>(kBlockSize), first + n - b * kBlockSize)) : 0;
+  };
+  auto read = [&](int64_t b, Round& r) {
+    const int o0 = first_row(b), o1 = last_row(b);
+    int32_t i[kQ8RowSteps], from[kQ8RowSteps], at[1];
+    int32_t src[kQ8RowSteps];
+    const int32_t dst[1] = {b <= b_hi ? static_cast<int32_t>(b) * kBlockSize : -1};
 #pragma unroll
-      for (int k = 0; k < kQ8RowSteps; ++k) {
-        const int o = row0 + k * kQ8WarpRows;
-        c[k] = make_uint4(0u, 0u, 0u, 0u);
-        from_scale[k] = 1.f;
-        if (o < o0 || o >= o1) continue;
-        const int64_t src = source_of(a, kept, static_cast<int32_t>(b * kBlockSize + o - first), first, report && l == 0);
-        const int32_t from = src < 0 ? -1 : block_of(a, table, src, report && l == 0);
-        if (from < 0) {
-          bad_index = true;
-          continue;
-        }
-        const int64_t t = static_cast<int64_t>(from) * a.num_kv_heads + h;
-        from_scale[k] = scales[t];
-        c[k] = reinterpret_cast<const uint4*>(pool + t * kQ8TileBytes + src % kBlockSize * kQ8RowBytes)[l];
-      }
-#pragma unroll
-      for (int k = 0; k < kQ8RowSteps; ++k) {
-        bad_scale |= !(from_scale[k] >= 0.f && from_scale[k] < INFINITY);
-        codes16_to_floats(c[k], from_scale[k], y[k]);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(y[k][i]));
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-      bad_scale |= o0 > 0 && !scale_ok(old);
-      if (__any_sync(0xffffffffu, bad_index)) live = false;
-      if (__any_sync(0xffffffffu, bad_scale) || !(amax < INFINITY)) {
-        if (lane == 0) flag_error(a.status, PA_DEVFLAG_BAD_SCALE);
-        live = false;
-      }
+    for (int k = 0; k < kQ8RowSteps; ++k) {
+      const int o = row0 + k * kQ8WarpRows;
+      i[k] = o >= o0 && o < o1 ? static_cast<int32_t>(b * kBlockSize + o - first) : -1;
     }
+    const bool fine = sources_of(a, kept, i, first, src);
+    const bool blocks = blocks_of(a, table, src, from) & blocks_of(a, table, dst, at);
+    const bool all_fine = __all_sync(0xffffffffu, fine), all_blocks = __all_sync(0xffffffffu, blocks);
+    if (report && lane == 0 && !all_fine) flag_error(a.status, PA_DEVFLAG_BAD_CONTEXT);
+    if (report && lane == 0 && !all_blocks) flag_error(a.status, PA_DEVFLAG_BAD_BLOCK);
+    r.block = all_fine && all_blocks ? at[0] : -1;
+    r.old = r.block >= 0 ? scales[static_cast<int64_t>(r.block) * a.num_kv_heads + h] : 1.f;
+#pragma unroll
+    for (int k = 0; k < kQ8RowSteps; ++k) {
+      r.c[k] = make_uint4(0u, 0u, 0u, 0u);
+      r.scale[k] = 1.f;
+      if (from[k] < 0) continue;
+      const int64_t t = static_cast<int64_t>(from[k]) * a.num_kv_heads + h;
+      r.scale[k] = scales[t];
+      r.c[k] = reinterpret_cast<const uint4*>(pool + t * kQ8TileBytes + src[k] % kBlockSize * kQ8RowBytes)[l];
+    }
+  };
+  auto write = [&](int64_t b, const Round& r) {
+    const int o0 = first_row(b), o1 = last_row(b);
+    float y[kQ8RowSteps][16];
+    float amax = 0.f;
+    bool bad = o0 > 0 && !scale_ok(r.old);
+#pragma unroll
+    for (int k = 0; k < kQ8RowSteps; ++k) {
+      bad |= !(r.scale[k] >= 0.f && r.scale[k] < INFINITY);
+      codes16_to_floats(r.c[k], r.scale[k], y[k]);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(y[k][i]));
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+    bad = __any_sync(0xffffffffu, bad) || !(amax < INFINITY);
     if (WARPS > 1) __syncthreads(); else __syncwarp();  // a round is read before it is written
-    if (!live) continue;
+    if (r.block < 0) return;
+    if (bad) {
+      if (lane == 0) flag_error(a.status, PA_DEVFLAG_BAD_SCALE);
+      return;
+    }
+    const int64_t tile = static_cast<int64_t>(r.block) * a.num_kv_heads + h;
     uint8_t* const codes = pool + tile * kQ8TileBytes;
     float now = scale_for(amax);
     if (o0 > 0) {
-      if (now > old)
-        rescale_rows(codes, old / now, o0, lane);
+      if (now > r.old)
+        rescale_rows(codes, r.old / now, o0, lane);
       else
-        now = old;
+        now = r.old;
     }
     const float inv = 1.f / now;
 #pragma unroll
@@ -220,29 +253,48 @@ __global__ void __launch_bounds__((WARPS > 1 ? WARPS : kCtaWarps) * 32) compact_
       if (o >= o0 && o < o1) reinterpret_cast<uint4*>(codes + o * kQ8RowBytes)[l] = floats16_to_codes(y[k], inv);
     }
     if (lane == 0) scales[tile] = now;
+  };
+  for (int64_t b0 = b_lo; b0 <= b_hi; b0 += WARPS) {
+    Round r;
+    read(b0 + warp, r);
+    write(b0 + warp, r);
   }
-}
-
-template <typename One, typename Four, typename Sixteen>
-cudaError_t launch(const CompactArgs& a, cudaStream_t stream, One one, Four four, Sixteen sixteen) {
-  const int64_t items = 2ll * a.num_seqs * a.num_kv_heads;
-  if (a.max_kept <= 2 * kWarpRows)
-    one<<<static_cast<unsigned>((items + kCtaWarps - 1) / kCtaWarps), kCtaWarps * 32, 0, stream>>>(a);
-  else if (a.max_kept <= 8 * kWarpRows)
-    four<<<static_cast<unsigned>(items), 4 * 32, 0, stream>>>(a);
-  else
-    sixteen<<<static_cast<unsigned>(items), 16 * 32, 0, stream>>>(a);
-  return cudaGetLastError();
 }
 
 }  // namespace
 
+// Warps of an item (sequence, head, pool), by the longest list: of a few tokens a warp, four items a CTA;
+// otherwise a CTA, of so many warps that a round or two takes the list, as long as the CTAs run side by side
+// (bf16, 300 to 500 tokens of 8 sequences with 8 heads: 5.5 us with 16 warps, 6.4 with 8, 9.5 with 4; of 64
+// sequences: 23.5, 20.4, 19.6).
 cudaError_t launch_compact(const CompactArgs& a, cudaStream_t stream) {
-  return launch(a, stream, compact_kernel<1>, compact_kernel<4>, compact_kernel<16>);
+  const int64_t items = 2ll * a.num_seqs * a.num_kv_heads;
+  const unsigned grid = static_cast<unsigned>(items);
+  if (a.max_kept <= 2 * kWarpRows)
+    compact_kernel<1><<<static_cast<unsigned>((items + kCtaWarps - 1) / kCtaWarps), kCtaWarps * 32, 0, stream>>>(a);
+  else if (a.max_kept <= 8 * kWarpRows)
+    compact_kernel<4><<<grid, 4 * 32, 0, stream>>>(a);
+  else if (items > kManyItems)
+    compact_kernel<8><<<grid, 8 * 32, 0, stream>>>(a);
+  else
+    compact_kernel<16><<<grid, 16 * 32, 0, stream>>>(a);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_compact_q8(const CompactArgs& a, cudaStream_t stream) {
-  return launch(a, stream, compact_q8_kernel<1>, compact_q8_kernel<4>, compact_q8_kernel<16>);
+  const int64_t items = 2ll * a.num_seqs * a.num_kv_heads;
+  const unsigned grid = static_cast<unsigned>(items);
+  if (a.max_kept <= 2 * kBlockSize + 1 && items > kManyShort)
+    compact_q8_kernel<1><<<static_cast<unsigned>((items + kCtaWarps - 1) / kCtaWarps), kCtaWarps * 32, 0, stream>>>(a);
+  else if (a.max_kept <= kBlockSize + 1)  // two blocks at most
+    compact_q8_kernel<2><<<grid, 2 * 32, 0, stream>>>(a);
+  else if (a.max_kept <= 8 * kBlockSize)
+    compact_q8_kernel<4><<<grid, 4 * 32, 0, stream>>>(a);
+  else if (items > kManyItems)
+    compact_q8_kernel<8><<<grid, 8 * 32, 0, stream>>>(a);
+  else
+    compact_q8_kernel<16><<<grid, 16 * 32, 0, stream>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace pkv
