@@ -130,6 +130,8 @@ struct AttendQ8Args {
   int32_t num_seqs;
   float scale;
   int32_t* status;
+  const int32_t* tree_mask = nullptr;  // few rows: those of drafted trees, [num_query_tokens][mask_words]
+  int32_t mask_words = 0;
 };
 
 cudaError_t launch_prefill_q8(const AttendQ8Args& a, cudaStream_t stream);

@@ -1,7 +1,9 @@
-// Causal attention of short chunks over the 8-bit pools: a few query rows per sequence (a
-// verify step's K + 1 tokens), up to 32 rows per K/V head.
+// Attention of short chunks and small drafted trees over the 8-bit pools: a few query rows per sequence
+// (a verify step's K + 1 tokens), up to 32 rows per K/V head.
 //
-// Chunk row i of a sequence sits at position L - q_len + i and attends keys 0 .. L - q_len + i.
+// Chunk row i of a sequence sits at position L - q_len + i and attends keys 0 .. L - q_len + i; a tree's
+// row i sees the keys before the q_len drafted ones, and of those the ones its mask row has bits for (at
+// most 32: one word).
 // The mathematics of a tile is the 8-bit decode's: one scale per tile for the scores, one for
 // its share of the output; codes, queries and weights enter the tensor cores as f16.
 //
@@ -59,6 +61,8 @@ struct RowsParams {
   int32_t num_query_tokens, max_query_len;
   float q_scale;  // scale * log2(e)
   int32_t* status;
+  const int32_t* tree_mask;  // trees: [num_query_tokens][mask_words]
+  int32_t mask_words;
 };
 
 __device__ __forceinline__ void mma_rows(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -113,7 +117,7 @@ template <int NT>
 struct Rows {
   uint32_t q[(NT + 1) / 2][4][4];  // f16 query fragments, 16 rows each
   float factor[NT];                // score factor of row 8 nt + r
-  int pos[NT];                     // last key that row sees
+  int pos[NT];                     // last key that row sees; of a tree's, the bits of its mask row
   float m[NT], l[NT];
   float2 o[NT][4][2];
 };
@@ -121,12 +125,13 @@ struct Rows {
 // T tiles (16 tokens each) at a time.  Scores are Q K^T with 16 rows a fragment, so P arrives
 // with a row's neighbouring tokens in one register, which is what the second factor of O^T = V^T
 // P^T wants: 16 dims by 8 rows, no padding beyond the eighth row.  Fragments and the order of
-// dims and tokens as in the 8-bit decode.  MASK: row x sees tokens up to pos[x], tile t holds
-// tokens from first[t] on, and tokens past `end` may hold anything.
-template <int NT, int T, bool MASK>
+// dims and tokens as in the 8-bit decode.  MASK: row x sees tokens up to pos[x], or, of a tree, those before
+// `drafted` and the ones its bits name; tile t holds tokens from first[t] on, and tokens past `end` may hold
+// anything.
+template <int NT, int T, bool MASK, bool TREE>
 __device__ __forceinline__ void attend_tiles(const uint8_t* const (&tiles)[T], int r, int q,
                                              const float (&ks)[T], const float (&vs)[T],
-                                             const int (&first)[T], int end, Rows<NT>& w) {
+                                             const int (&first)[T], int end, int drafted, Rows<NT>& w) {
   constexpr int MT = (NT + 1) / 2;
   const int t0 = q8_token_of(2 * q);
   uint2 v[T][4];  // tokens t0, t0 + 2, t0 + 8, t0 + 10
@@ -172,7 +177,9 @@ __device__ __forceinline__ void attend_tiles(const uint8_t* const (&tiles)[T], i
         if (token > end) v[t][i] = make_uint2(0u, 0u);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          if (token > w.pos[nt]) x[t][nt][i] = -INFINITY;
+          if (TREE ? token >= drafted + 32 || (token >= drafted && ((w.pos[nt] >> (token - drafted)) & 1) == 0)
+                   : token > w.pos[nt])
+            x[t][nt][i] = -INFINITY;
       }
     }
   }
@@ -273,7 +280,7 @@ constexpr int smem_bytes() {
   return kWarps * kStages * (kStageBytes + 8) + (kWarps + 1) * 8 * NT * kRecordFloats * 4;
 }
 
-template <int NT>
+template <int NT, bool TREE>
 __global__ void __launch_bounds__(kThreads, 2)
 paged_rows_q8_kernel(const __grid_constant__ RowsParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -376,7 +383,12 @@ paged_rows_q8_kernel(const __grid_constant__ RowsParams p) {
     }
     if (nt < NT) {
       w.factor[nt] = p.q_scale * power_of_two(-shift);
-      w.pos[nt] = L - q_len + row / p.group;
+      if (TREE) {  // (a row of padding takes the last row's)
+        const uint32_t bits = static_cast<uint32_t>(__ldg(p.tree_mask + static_cast<int64_t>(q0 + row / p.group) * p.mask_words));
+        w.pos[nt] = static_cast<int>(bits & (0xffffffffu >> (32 - q_len)));
+      } else {
+        w.pos[nt] = L - q_len + row / p.group;
+      }
       w.m[nt] = -INFINITY;
       w.l[nt] = 0.f;
 #pragma unroll
@@ -385,7 +397,7 @@ paged_rows_q8_kernel(const __grid_constant__ RowsParams p) {
   }
 
   // blocks below this one are seen whole by every row
-  const int whole = (L - q_len + 1) / kBlockSize - b_lo;
+  const int whole = (L - q_len + (TREE ? 0 : 1)) / kBlockSize - b_lo;
   bool ok = true;
   int k = 0;
 #pragma unroll 1
@@ -412,12 +424,12 @@ paged_rows_q8_kernel(const __grid_constant__ RowsParams p) {
     }
     if (!(ok = __all_sync(0xffffffffu, here))) break;
     if (k + T <= min(whole, n)) {
-      attend_tiles<NT, T, false>(tiles, r, q, ks, vs, first, 0, w);
+      attend_tiles<NT, T, false, TREE>(tiles, r, q, ks, vs, first, 0, 0, w);
     } else {
 #pragma unroll
       for (int t = 1; t < T; ++t)
         if (t >= left) vs[t] = 0.f;
-      attend_tiles<NT, T, true>(tiles, r, q, ks, vs, first, L - 1, w);
+      attend_tiles<NT, T, true, TREE>(tiles, r, q, ks, vs, first, L - 1, L - q_len, w);
     }
     __syncwarp();  // every lane has read the stages
     k += T;
@@ -454,7 +466,7 @@ paged_rows_q8_kernel(const __grid_constant__ RowsParams p) {
   }
   __syncthreads();
   auto finish = [&](int row, int c, float Lsum, const float4& acc) {
-    const float inv = 1.f / Lsum;
+    const float inv = TREE && Lsum == 0.f ? 0.f : 1.f / Lsum;  // a tree's row may see nothing
     __nv_bfloat16* out = p.out + (static_cast<int64_t>(q0 + row / p.group) * p.num_q_heads + g * p.group +
                                   row % p.group) * kHeadDim;
     const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
@@ -491,16 +503,16 @@ paged_rows_q8_kernel(const __grid_constant__ RowsParams p) {
   cluster_sync();  // this CTA's shared memory outlives the others' reads
 }
 
-template <int NT>
+template <int NT, bool TREE>
 cudaError_t launch(const RowsParams& p, int64_t segments, int cluster, cudaStream_t stream) {
   static bool done[kMaxDevices] = {};  // benign race: the attribute calls are idempotent
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= kMaxDevices || !done[dev]) {
-    e = cudaFuncSetAttribute(paged_rows_q8_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NT>());
+    e = cudaFuncSetAttribute(paged_rows_q8_kernel<NT, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NT>());
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(paged_rows_q8_kernel<NT>, cudaFuncAttributePreferredSharedMemoryCarveout,
+      e = cudaFuncSetAttribute(paged_rows_q8_kernel<NT, TREE>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
     if (dev < kMaxDevices) done[dev] = true;
@@ -517,7 +529,7 @@ cudaError_t launch(const RowsParams& p, int64_t segments, int cluster, cudaStrea
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, paged_rows_q8_kernel<NT>, p);
+  e = cudaLaunchKernelEx(&cfg, paged_rows_q8_kernel<NT, TREE>, p);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
@@ -560,11 +572,14 @@ cudaError_t launch_rows_q8(const AttendQ8Args& a, cudaStream_t stream) {
   while (cluster < kMaxCluster && segments * cluster * 2 <= 2 * sms &&
          a.max_blocks_per_seq >= 2 * cluster * kWarps)
     cluster *= 2;
+  p.tree_mask = a.tree_mask;
+  p.mask_words = a.mask_words;
+  const bool tree = a.tree_mask != nullptr;
   switch ((p.max_query_len * p.group + 7) / 8) {  // groups of eight rows
-    case 1: return launch<1>(p, segments, cluster, stream);
-    case 2: return launch<2>(p, segments, cluster, stream);
-    case 3: return launch<3>(p, segments, cluster, stream);
-    default: return launch<4>(p, segments, cluster, stream);
+    case 1: return tree ? launch<1, true>(p, segments, cluster, stream) : launch<1, false>(p, segments, cluster, stream);
+    case 2: return tree ? launch<2, true>(p, segments, cluster, stream) : launch<2, false>(p, segments, cluster, stream);
+    case 3: return tree ? launch<3, true>(p, segments, cluster, stream) : launch<3, false>(p, segments, cluster, stream);
+    default: return tree ? launch<4, true>(p, segments, cluster, stream) : launch<4, false>(p, segments, cluster, stream);
   }
 }
 

@@ -1305,6 +1305,31 @@ size_t tree_workspace_size() {
 }
 
 cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream) { return launch_group<false>(a, stream); }
-cudaError_t launch_tree_q8(const TreeArgs& a, cudaStream_t stream) { return launch_group<true>(a, stream); }
+cudaError_t launch_tree_q8(const TreeArgs& a, cudaStream_t stream) {
+  AttendQ8Args r;
+  r.out = a.out;
+  r.q = a.q;
+  r.query_start_loc = a.query_start_loc;
+  r.num_query_tokens = a.num_query_tokens;
+  r.max_query_len = a.max_query_len;
+  r.max_context_len = 0;
+  r.key_cache = a.key_cache;
+  r.value_cache = a.value_cache;
+  r.key_scale = a.key_scale;
+  r.value_scale = a.value_scale;
+  r.num_blocks = a.num_blocks;
+  r.num_kv_heads = a.num_kv_heads;
+  r.num_q_heads = a.num_q_heads;
+  r.block_tables = a.block_tables;
+  r.max_blocks_per_seq = a.max_blocks_per_seq;
+  r.context_lens = a.context_lens;
+  r.num_seqs = a.num_seqs;
+  r.scale = a.scale;
+  r.status = a.status;
+  r.tree_mask = a.tree_mask;
+  r.mask_words = a.mask_words;
+  if (rows_q8_takes(r)) return launch_rows_q8(r, stream);
+  return launch_group<true>(a, stream);
+}
 
 }  // namespace pkv
