@@ -137,6 +137,7 @@ struct AttendQ8Args {
 cudaError_t launch_prefill_q8(const AttendQ8Args& a, cudaStream_t stream);
 // Its form for chunks of a few rows (at most 32 per K/V head), and whether a call is one.
 bool rows_q8_takes(const AttendQ8Args& a);
+int rows_q8_cluster(const AttendQ8Args& a, int sms);  // CTAs that share a (sequence, K/V head)
 cudaError_t launch_rows_q8(const AttendQ8Args& a, cudaStream_t stream);
 
 // Work decomposition of one pa_decode call (identical in the size query and the call).

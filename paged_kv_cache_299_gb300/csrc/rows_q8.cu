@@ -541,6 +541,17 @@ bool rows_q8_takes(const AttendQ8Args& a) {
          static_cast<int64_t>(a.num_seqs) * a.num_kv_heads < (1 << 27);
 }
 
+// CTAs per segment: as many as run side by side, two per SM, and may have a tile per warp each
+// (5 rows at 1000 tokens 6.7 us with clusters up to that, 9.0 where it takes four tiles).
+int rows_q8_cluster(const AttendQ8Args& a, int sms) {
+  const int64_t segments = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
+  int cluster = 1;
+  while (cluster < kMaxCluster && segments * cluster * 2 <= 2 * sms &&
+         a.max_blocks_per_seq >= 2 * cluster * kWarps)
+    cluster *= 2;
+  return cluster;
+}
+
 cudaError_t launch_rows_q8(const AttendQ8Args& a, cudaStream_t stream) {
   RowsParams p;
   p.out = static_cast<__nv_bfloat16*>(a.out);
@@ -565,13 +576,8 @@ cudaError_t launch_rows_q8(const AttendQ8Args& a, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  // CTAs per segment: as many as run side by side, two per SM, and may have a tile per warp each
-  // (5 rows at 1000 tokens 6.7 us with clusters up to that, 9.0 where it takes four tiles).
   const int64_t segments = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
-  int cluster = 1;
-  while (cluster < kMaxCluster && segments * cluster * 2 <= 2 * sms &&
-         a.max_blocks_per_seq >= 2 * cluster * kWarps)
-    cluster *= 2;
+  const int cluster = rows_q8_cluster(a, sms);
   p.tree_mask = a.tree_mask;
   p.mask_words = a.mask_words;
   const bool tree = a.tree_mask != nullptr;

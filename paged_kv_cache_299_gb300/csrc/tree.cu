@@ -55,9 +55,13 @@ constexpr float kHeadroom = 8.0f;  // the reference of the exponents lies this f
 constexpr float kLargeScore = 131072.f;  // 2^17: a rounding of the score (log2 units) is then 2^-7
 constexpr int kPartChunks = kHeadDim / 8 + 1;  // float4s of a row for each half of the dims: sum; maximum, weight
 constexpr int kRecordFloat4s = 2 * kPartChunks * kTileM;  // of one half
-constexpr int kMinPiece = 4;      // tiles of a piece of a split segment, at least
+constexpr int kMinPiece = 6;      // tiles of a piece of a split segment, at least
 constexpr int kSplitTiles = 5;    // what meeting costs, in tiles: equal runs begin to pay beyond it
+constexpr int kFlatPieces = 10;   // so many pieces are weighed at once, more by groups first: one warp's loads
+constexpr int kGroupPieces = 8;   // of a record take 0.4 us, a meeting of a group 2
+constexpr int kTogether = 3;      // records whose loads are in flight at a time
 constexpr int kPieceTiles = 1;    // what a piece costs beside its tiles, in tiles
+constexpr int kRowsBlocks = 240;     // 8-bit blocks per CTA that the few-rows kernel walks gladly: some 40 us
 constexpr int kMaxDealtSeqs = 1024;  // sequences whose segments may get CTAs of their own
 constexpr int kPieceRing = 4;
 constexpr int kWalkBytes = 56;
@@ -72,6 +76,7 @@ struct TreeParams {
   const float* key_scale;            // 8-bit pools
   const float* value_scale;
   int32_t* counters;  // [grid][row warps] pieces delivered by each of the segment that starts in a CTA and goes on
+  int32_t* group_counters;  // the same of groups of pieces, by the CTA of their first
   float4* records;    // [grid][2][halves][half of the dims][kPartChunks][128]
   int32_t* status;
   int32_t mask_words, max_blocks_per_seq, num_blocks, num_kv_heads, num_q_heads;
@@ -812,53 +817,90 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       bool write = from == to;
       if (!write) {
         // ---- a piece of a split segment: its record, and the warp that comes last weighs them all ----
-        if (row_ok) {
-          float4* rec = record_of(blockIdx.x, cur->j0 == 0);
+        // whether this warp is the last of `count` to arrive at a counter; then it sees what the others wrote
+        auto arrive = [&](int32_t* counter, int count) -> bool {
+          __threadfence();
+          __syncwarp();
+          int last = 0;
+          if (lane == 0) {
+            last = atomicAdd(counter, 1) == count - 1;
+            if (last) *counter = 0;
+          }
+          last = __shfl_sync(0xffffffffu, last, 0);
+          if (last) __threadfence();
+          return last != 0;
+        };
+        // weighs the records of `count` CTAs, every `step`-th from `cta` on, into m, l and o
+        auto weigh = [&](int cta, int step, int count) {
+#pragma unroll
+          for (int d = 0; d < 2; ++d) {  // 16 of the thread's dims at a time, kTogether records' loads in flight
+            float acc[16] = {};
+            l = 0.f;
+            m = -INFINITY;
+            for (int k0 = 0; k0 < count; k0 += kTogether) {
+              float4 x[kTogether][4], ml[kTogether];
+#pragma unroll
+              for (int u = 0; u < kTogether; ++u) {
+                const int c = cta + min(k0 + u, count - 1) * step;
+                const float4* rec = record_of(c, c == from);
+                ml[u] = __ldcg(rec + 8 * kTileM);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[u][i] = __ldcg(rec + (4 * d + i) * kTileM);
+              }
+              float top = m;
+#pragma unroll
+              for (int u = 0; u < kTogether; ++u) top = fmaxf(top, ml[u].x);
+              const float at = top == -INFINITY ? 0.f : top;  // a row that has seen no key yet
+              const float alpha = fast_exp2(m - at);
+              m = top;
+              l *= alpha;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) acc[i] *= alpha;
+#pragma unroll
+              for (int u = 0; u < kTogether; ++u) {
+                if (k0 + u >= count) continue;
+                const float w = fast_exp2(ml[u].x - at);
+                l += w * ml[u].y;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  acc[4 * i] += w * x[u][i].x;
+                  acc[4 * i + 1] += w * x[u][i].y;
+                  acc[4 * i + 2] += w * x[u][i].z;
+                  acc[4 * i + 3] += w * x[u][i].w;
+                }
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[16 * d + i] = __float_as_uint(acc[i]);
+          }
+        };
+        auto keep = [&](float4* rec) {
+          if (!row_ok) return;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             rec[i * kTileM] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
                                           __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
           rec[8 * kTileM] = make_float4(m, l, 0.f, 0.f);
-        }
-        __threadfence();
-        __syncwarp();
-        int last = 0;
-        if (lane == 0) {
-          int32_t* counter = p.counters + from * kRowWarps + warp;
-          last = atomicAdd(counter, 1) == to - from;
-          if (last) *counter = 0;
-          ++delivered[warp];
-        }
-        write = __shfl_sync(0xffffffffu, last, 0) != 0;
-        if (write) {
-          __threadfence();
-          float top_m = -INFINITY;
-          const int pieces = row_ok ? to - from + 1 : 0;
-          for (int k = 0; k < pieces; ++k) top_m = fmaxf(top_m, __ldcg(record_of(from + k, k == 0) + 8 * kTileM).x);
-          const float at = top_m == -INFINITY ? 0.f : top_m;
-          float acc[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-          l = 0.f;
-          for (int k = 0; k < pieces; ++k) {
-            const float4* rec = record_of(from + k, k == 0);
-            const float4 ml = __ldcg(rec + 8 * kTileM);
-            float4 x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = __ldcg(rec + i * kTileM);
-            const float w = fast_exp2(ml.x - at);
-            l += w * ml.y;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              acc[4 * i] += w * x[i].x;
-              acc[4 * i + 1] += w * x[i].y;
-              acc[4 * i + 2] += w * x[i].z;
-              acc[4 * i + 3] += w * x[i].w;
-            }
+        };
+        const int pieces = to - from + 1;
+        keep(record_of(blockIdx.x, cur->j0 == 0));
+        int32_t* const counter = p.counters + from * kRowWarps + warp;
+        if (pieces <= kFlatPieces) {
+          write = arrive(counter, pieces);
+          if (write && row_ok) weigh(from, 1, pieces);
+        } else {
+          // groups first, whose sums take the place of their first records; then the groups
+          const int first = from + (static_cast<int>(blockIdx.x) - from) / kGroupPieces * kGroupPieces;
+          const int count = min(kGroupPieces, to + 1 - first);
+          if (arrive(p.group_counters + first * kRowWarps + warp, count)) {
+            if (row_ok) weigh(first, 1, count);
+            keep(record_of(first, first == from));
+            const int groups = (pieces + kGroupPieces - 1) / kGroupPieces;
+            write = arrive(counter, groups);
+            if (write && row_ok) weigh(from, kGroupPieces, groups);
           }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(acc[i]);
         }
+        if (lane == 0) ++delivered[warp];
       }
       if (write) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -1203,8 +1245,17 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
     int n = 0;
     while (next_piece<kTokens>(p, runs, w, u)) {
       if (u.from == u.to || !warp_active(u, tid) || n++ < delivered[tid]) continue;
+      const int pieces = u.to - u.from + 1;
       int32_t* counter = p.counters + u.from * kRowWarps + tid;
-      if (atomicAdd(counter, 1) == u.to - u.from) *counter = 0;
+      int count = pieces;
+      if (pieces > kFlatPieces) {
+        const int first = u.from + (static_cast<int>(blockIdx.x) - u.from) / kGroupPieces * kGroupPieces;
+        int32_t* group = p.group_counters + first * kRowWarps + tid;
+        if (atomicAdd(group, 1) != min(kGroupPieces, u.to + 1 - first) - 1) continue;
+        *group = 0;
+        count = (pieces + kGroupPieces - 1) / kGroupPieces;
+      }
+      if (atomicAdd(counter, 1) == count - 1) *counter = 0;
     }
   }
 }
@@ -1259,7 +1310,8 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
   p.key_scale = a.key_scale;
   p.value_scale = a.value_scale;
   p.counters = static_cast<int32_t*>(a.workspace);
-  p.records = reinterpret_cast<float4*>(static_cast<uint8_t*>(a.workspace) + counter_bytes(sms));
+  p.group_counters = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(a.workspace) + counter_bytes(sms));
+  p.records = reinterpret_cast<float4*>(static_cast<uint8_t*>(a.workspace) + 2 * counter_bytes(sms));
   p.status = a.status;
   p.mask_words = a.mask_words;
   p.max_blocks_per_seq = a.max_blocks_per_seq;
@@ -1301,7 +1353,7 @@ cudaError_t launch_group(const TreeArgs& a, cudaStream_t stream) {
 size_t tree_workspace_size() {
   int dev = 0, sms = 0;
   if (device_sms(&dev, &sms) != cudaSuccess) return 0;
-  return counter_bytes(sms) + record_bytes(sms);
+  return 2 * counter_bytes(sms) + record_bytes(sms);
 }
 
 cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream) { return launch_group<false>(a, stream); }
@@ -1328,7 +1380,18 @@ cudaError_t launch_tree_q8(const TreeArgs& a, cudaStream_t stream) {
   r.status = a.status;
   r.tree_mask = a.tree_mask;
   r.mask_words = a.mask_words;
-  if (rows_q8_takes(r)) return launch_rows_q8(r, stream);
+  int dev = 0, sms = 0;
+  const cudaError_t e = device_sms(&dev, &sms);
+  if (e != cudaSuccess) return e;
+  if (rows_q8_takes(r)) {
+    // Few rows run best on the few-rows kernel (8 nodes, 8 heads: one context of 700 9.2 us against 14.5, 32
+    // of 1000 19.1 against 23.7, 256 of 1000 117 and 160, 4 of 131072 191 and 219), but its clusters take
+    // equal parts of a segment: long contexts that leave its CTAs few keep it waiting (one of 131072 161 us
+    // against 67, 20 of 16000 185 and 143).
+    const int cluster = rows_q8_cluster(r, sms);
+    const int64_t ctas = static_cast<int64_t>(r.num_seqs) * r.num_kv_heads * cluster;
+    if (3 * ctas >= 4 * sms || r.max_blocks_per_seq <= kRowsBlocks * cluster) return launch_rows_q8(r, stream);
+  }
   return launch_group<true>(a, stream);
 }
 

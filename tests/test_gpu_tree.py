@@ -100,6 +100,13 @@ def test_one_sequence(pool, L, n):
     Trees(pool, [L], [n], 8, 2, "tree", seed=L + n, slack=0.5).check()
 
 
+@pytest.mark.parametrize("L", [300, 4000, 32000, 60000])
+@pytest.mark.parametrize("seqs,hq,hkv,n", [(1, 8, 2, 8), (3, 4, 1, 3), (1, 2, 1, 16), (1, 1, 1, 32)])
+def test_few_rows_over_8_bits(L, seqs, hq, hkv, n):
+    """At most 32 rows per K/V head: contexts on both sides of where another kernel takes over."""
+    Trees("q8", [L - 7 * i for i in range(seqs)], [n] + [max(1, n - 2)] * (seqs - 1), hq, hkv, "mask", seed=L + n).check()
+
+
 @pytest.mark.parametrize("pool", POOLS)
 @pytest.mark.parametrize("hist,nodes", [
     ([20000] + [30] * 40, [20] + [5] * 40),
