@@ -512,6 +512,14 @@ def _status_ptr(device_status, dev):
 
 def _need_rows(t, name, dev, heads=None):
     """bf16 [T, heads, 64] whose rows are contiguous per token; returns the token stride."""
+    try:  # a quick way through for rows that are as they should be
+        if t.dtype is torch.bfloat16 and t.get_device() == dev:
+            tokens, h, dims = t.shape
+            stride, row, one = t.stride()
+            if dims == 64 and one == 1 and (row == 64 or h <= 1) and (heads is None or h == heads):
+                return h * 64 if tokens <= 1 else stride
+    except (AttributeError, ValueError):
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.get_device() != dev:

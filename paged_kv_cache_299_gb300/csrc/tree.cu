@@ -49,7 +49,7 @@ constexpr int kHalfWarps = 8;                 // row warps of one half
 constexpr int kQBytes = kTileM * kRowBytes;   // 16 KiB
 constexpr int kOpBytes = kTileN * kRowBytes;  // one K or V tile of bf16: 16 KiB
 constexpr int kRawBytes = 2 * kTileN * kQ8RowBytes;  // codes of K, then of V
-constexpr int kConsts = 3 * kBlocksPerTile;   // key scale, log2 f, 1 / f of every block
+constexpr int kConsts = 3 * kBlocksPerTile;   // score factor, log2 f, 1 / f of every block
 constexpr int kMaxMaskWords = 32;
 constexpr float kHeadroom = 8.0f;  // the reference of the exponents lies this far (log2) above the maximum
 constexpr float kLargeScore = 131072.f;  // 2^17: a rounding of the score (log2 units) is then 2^-7
@@ -384,11 +384,11 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       *own_first = runs.own_first;
       *own_last = runs.own_last;
       // the row warps' first two pieces
-      for (int u = 0; u < 2; ++u) {
-        Piece x;
-        if (!next_piece<kTokens>(p, runs, w, x)) x.n = 0;
-        *piece_slot(u) = x;
-      }
+      Piece x;
+      if (!next_piece<kTokens>(p, runs, w, x)) x.n = 0;
+      *piece_slot(0) = x;
+      if (length > 0 || !next_piece<kTokens>(p, runs, w, x)) x.n = 0;
+      *piece_slot(1) = x;
       *row_walk = w;
     };
     if (p.num_seqs <= 32) {
@@ -643,15 +643,15 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
           }
         }
         const uint32_t cs = smem_addr(consts + (c + skipped) % kConstRing * kConsts);
-        // score factor of a part's block (8-bit pools: a hidden key's -inf * 0 is a NaN); read where it is used
+        // score factor of a part's block; read where it is used
         auto factor = [&](int of_part, int b) -> float {
-          return Q8 ? fmaxf(lds_f32(cs + 4 * (of_part * (kBlocksPerTile / 2) + b)) * p.qk_scale, 1.17549435e-38f)
-                    : p.qk_scale;
+          return Q8 ? lds_f32(cs + 4 * (of_part * (kBlocksPerTile / 2) + b)) : p.qk_scale;
         };
         auto largest = [&](int of_part) -> float {
           if (!Q8) return fmaxf(max3f(top[0], top[1], top[2]), top[3]) * p.qk_scale;
-          return fmaxf(max3f(top[0] * factor(of_part, 0), top[1] * factor(of_part, 1), top[2] * factor(of_part, 2)),
-                       top[3] * factor(of_part, 3));
+          float f[kBlocksPerTile / 2];
+          lds_f32x4(cs + 4 * of_part * (kBlocksPerTile / 2), f);
+          return fmaxf(max3f(top[0] * f[0], top[1] * f[1], top[2] * f[2]), top[3] * f[3]);
         };
         float mt = largest(part ^ 1);
 #pragma unroll
@@ -1168,7 +1168,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
               fi = 1.f / f;
             }
             float* cs = consts + slot * kConsts + blk;
-            cs[0] = needed ? scales[0] : 1.f;
+            // (a hidden key's score is minus infinity: times 0 it would be a NaN)
+            cs[0] = fmaxf((needed ? scales[0] : 1.f) * p.qk_scale, 1.17549435e-38f);
             cs[kBlocksPerTile] = lf;
             cs[2 * kBlocksPerTile] = fi;
           } else {
