@@ -193,15 +193,16 @@ __global__ void __launch_bounds__((WARPS > 1 ? WARPS : kCtaWarps) * 32) compact_
     const int o0 = first_row(b), o1 = last_row(b);
     int32_t i[kQ8RowSteps], from[kQ8RowSteps], at[1];
     int32_t src[kQ8RowSteps];
-    const int32_t dst[1] = {b <= b_hi ? static_cast<int32_t>(b) * kBlockSize : -1};
 #pragma unroll
     for (int k = 0; k < kQ8RowSteps; ++k) {
       const int o = row0 + k * kQ8WarpRows;
       i[k] = o >= o0 && o < o1 ? static_cast<int32_t>(b * kBlockSize + o - first) : -1;
     }
-    const bool fine = sources_of(a, kept, i, first, src);
+    const bool all_fine = __all_sync(0xffffffffu, sources_of(a, kept, i, first, src));
+    // (a destination is known to lie in the table by its sources, at or behind it)
+    const int32_t dst[1] = {all_fine && b <= b_hi ? static_cast<int32_t>(b * kBlockSize) : -1};
     const bool blocks = blocks_of(a, table, src, from) & blocks_of(a, table, dst, at);
-    const bool all_fine = __all_sync(0xffffffffu, fine), all_blocks = __all_sync(0xffffffffu, blocks);
+    const bool all_blocks = __all_sync(0xffffffffu, blocks);
     if (report && lane == 0 && !all_fine) flag_error(a.status, PA_DEVFLAG_BAD_CONTEXT);
     if (report && lane == 0 && !all_blocks) flag_error(a.status, PA_DEVFLAG_BAD_BLOCK);
     r.block = all_fine && all_blocks ? at[0] : -1;

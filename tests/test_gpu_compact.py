@@ -208,6 +208,11 @@ def test_bad_entries_are_reported(pool):
     c.run(bt=bt)
     assert word(c) == pa.DEVFLAG_BAD_BLOCK
     c.check(skip=[1])
+    for far in (16 * c.bt.shape[1], 1 << 28, (1 << 31) - 20):  # destinations past the block-table row
+        c = fresh()
+        c.run(first=i32([20, far, 0]))
+        assert word(c) == pa.DEVFLAG_BAD_CONTEXT
+        c.check(skip=[1])
     for entries in ([1, 3, 9, 7, 7, 7, 7, 4, 5], [1, 3, 9, 0, 1 << 30, (1 << 30) + 1, (1 << 31) - 1, 4, 5],
                     [1, 3, 9, -1, -5, -(1 << 31), 0, 4, 5]):
         c = fresh()
