@@ -529,9 +529,6 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       return p.tree_mask + static_cast<int64_t>(u->q0 + min(u->tok0 + half * kHalfTokens + r / GROUP, u->q_len - 1)) * p.mask_words;
     };
     auto cur_lead = [&](const Piece* u) -> int { return (u->L - u->q_len) % kTileN; };
-    // Pieces come through shared memory, two ahead, so that the tiles' loop keeps its registers: a warp
-    // looks piece u + 1 up after the row warps met in piece u's epilogue, and its slot was last read in
-    // piece u - 2, which all of them have left by then.
     // This thread's share of a CTA's record: of its piece of the segment that begins there, or else.
     auto record_of = [&](int cta, bool begins) -> float4* {
       return p.records + ((2ll * cta + (begins ? 1 : 0)) * HALVES + half) * kRecordFloat4s + part * kPartChunks * kTileM + r;
@@ -582,6 +579,9 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       fence_proxy_async_smem();
       return true;
     };
+    // Pieces come through shared memory, written two ahead by one thread, so that the tiles' loop keeps its
+    // registers (and the MMA warp has them too).  Piece u + 2 is written in piece u, when all row warps have left
+    // piece u - 2, whose slot it takes; they look it up after they met in the epilogue of u or u + 1.
     for (; ok && piece_slot(units)->n > 0; ++units) {
       const Piece* const cur = piece_slot(units);
       const int n = cur->n;

@@ -285,19 +285,30 @@ def test_replays_and_streams(pool):
     t.check(out)
 
 
+@pytest.mark.parametrize("n", [4, 40])
 @pytest.mark.parametrize("pool", POOLS)
-def test_bad_entries_are_reported(pool):
+def test_contexts_longer_than_the_pool_are_reported(pool, n):
+    t = Trees(pool, [100, 20], [n, 3], 4, 1, seed=33)
+    wide = t.bt.repeat(1, 40).contiguous().clamp(min=0)
+    got = t.run(bt=wide, ctx=i32([16 * t.w.num_blocks + 1, 23]))
+    assert int(t.status.item()) == pa.DEVFLAG_BAD_CONTEXT and (got[:n] == 7.0).all()
+
+
+@pytest.mark.parametrize("n", [6, 70])
+@pytest.mark.parametrize("pool", POOLS)
+def test_bad_entries_are_reported(pool, n):
     def flag(t, **kw):
         t.status.zero_()
         got = t.run(**kw)
         return int(t.status.item()), got.cpu().double()
 
     def fresh():
-        return Trees(pool, [100, 40, 7], [9, 6, 3], 8, 2, seed=31)
+        return Trees(pool, [100, 40, 7], [9, n, 3], 8, 2, seed=31)
 
     t = fresh()
     ref, tol = t.expected()
-    others = list(range(9)) + [15, 16, 17]
+    others = list(range(9)) + [9 + n, 10 + n, 11 + n]
+    past = 40 + n
     bt = t.bt.clone()
     bt[1, 1] = t.w.num_blocks
     word, got = flag(t, bt=bt)
@@ -308,15 +319,18 @@ def test_bad_entries_are_reported(pool):
     for ctx in ([109, 5, 10], [109, -3, 10], [109, 1 << 30, 10]):  # shorter than its rows; past its table row
         word, got = flag(t, ctx=i32(ctx))
         assert word == pa.DEVFLAG_BAD_CONTEXT
-        assert (got[9:15] == 7.0).all()
+        assert (got[9:9 + n] == 7.0).all()
         close(got[others], ref[others], tol[others])
-    word, got = flag(t, most=8)  # a tree larger than max_query_len
-    assert word == pa.DEVFLAG_BAD_CONTEXT and (got[:9] == 7.0).all()
-    close(got[9:], ref[9:], tol[9:])
-    word, got = flag(t, starts=i32([0, 9, 15, 19]), ctx=i32([109, 46, 11]))  # rows past the buffer
-    assert word == pa.DEVFLAG_BAD_CONTEXT and (got[15:] == 7.0).all()
-    close(got[:15], ref[:15], tol[:15])
-    word, got = flag(t, starts=i32([0, 9, 4, 7]), ctx=i32([109, 46, 10]))  # fewer than no rows: none
+    most = max(9, n) - 1  # a tree larger than max_query_len
+    word, got = flag(t, most=most)
+    lost = list(range(9)) if n < 9 else list(range(9, 9 + n))
+    kept = [i for i in range(t.rows) if i not in lost]
+    assert word == pa.DEVFLAG_BAD_CONTEXT and (got[lost] == 7.0).all()
+    close(got[kept], ref[kept], tol[kept])
+    word, got = flag(t, starts=i32([0, 9, 9 + n, 13 + n]), ctx=i32([109, past, 11]))  # rows past the buffer
+    assert word == pa.DEVFLAG_BAD_CONTEXT and (got[9 + n:] == 7.0).all()
+    close(got[:9 + n], ref[:9 + n], tol[:9 + n])
+    word, got = flag(t, starts=i32([0, 9, 4, 7]), ctx=i32([109, past, 10]))  # fewer than no rows: none
     assert word in (0, pa.DEVFLAG_BAD_CONTEXT)
     t = fresh()
     t.check()  # and the call after is as ever
