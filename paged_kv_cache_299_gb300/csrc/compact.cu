@@ -13,7 +13,10 @@
 // put them: a scale of their own where the block's first slot is among them, and one that only grows
 // where earlier tokens stay.
 //
-// Memory-bound: every row is read and written once.
+// Memory-bound: every row is read and written once.  Measured (8 K/V heads): 64 histories of 300 to 500
+// kept tokens 20.2 us (106.7 MB, 5.3 TB/s, 0.78 of the copy rate: a list, a table entry and a row one after
+// the other, then the writes, in one or two rounds a CTA); 32 paths of up to 5 tokens 2.7 us, into the
+// 8-bit pools 3.2, 256 of up to 8 there 5.9: the launch and the chain of dependent loads.
 #include <math.h>
 
 #include "common.cuh"

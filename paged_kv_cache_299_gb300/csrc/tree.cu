@@ -8,27 +8,39 @@
 // GB300 design.  The rows are few and the keys many: what counts is to stream K and V past 128 MMA rows
 // (128 / GROUP tokens x GROUP heads that share a K/V head) on every SM, whatever the batch looks like.
 //   * The work is a row of 128-key tiles: all tiles of all (sequence, K/V head, query tile) segments, one
-//     after the other, for a persistent grid of two CTAs per SM.  Where there are CTAs enough, every
+//     after the other, for a persistent grid that fills every SM.  Where there are CTAs enough, every
 //     segment gets CTAs of its own, as many as bring the longest piece down; otherwise, or where lengths are
 //     so uneven that equal shares win, the row is cut into equal runs, one per CTA, that begin and end
 //     inside segments.  A segment that one CTA serves whole goes straight to the output; pieces of a split
 //     one are kept in fp32 (sum, maximum, weight) in the workspace, and the warp that finishes last for its
-//     rows weighs them together, in the pieces' order.
-//   * Two CTAs per SM, because a tile's chain (scores, softmax, product) is latency: 128 keys a tile
-//     amortise it, two chains fill in for each other.
-//   * Tensor memory (256 columns): scores S 128, P 64 (bf16 pairs), O 64.  P has columns of its own, so
-//     the next tile's scores are issued as soon as the row warps have read this tile's.
-//   * Warps 0-7, the row warps: two threads per row, 64 keys each.  Each also reads its partner's scores,
+//     rows weighs them together, in the pieces' order (many pieces in groups, then the groups): the result
+//     does not depend on who that is.
+//   * Trees of at most 128 rows (64 over 8 bits): two CTAs per SM of one half (128 MMA rows) each, because a tile's chain
+//     (scores, softmax, product) is latency: 128 keys a tile amortise it, two chains fill in for each other.
+//     Larger ones: one CTA per SM with two halves that share every K and V tile, which is fetched, and
+//     converted, once for 256 rows (8-bit 2 x 131072 x 60: 324 us with 128 rows a CTA, 197 with halves;
+//     bf16 4 x 131072 x 26, 104 rows: 180 us with 128, 205 with halves; 32 ragged trees, of up to 128: 19.6 and 29.0).
+//   * Tensor memory (256 columns a half): scores S 128, P 64 (bf16 pairs), O 64.  P has columns of its own,
+//     so the next tile's scores are issued as soon as the row warps have read this tile's.
+//   * Row warps, eight a half: two threads per row, 64 keys each.  Each also reads its partner's scores,
 //     for their maximum alone (a reduction that comes with the load), so both follow the same running
-//     maximum without meeting.  Exponentials, P as bf16, row sums in fp32; O is rescaled in place when a
-//     row's maximum grows past the headroom left above it.
+//     maximum without meeting.  Exponentials and row sums in fp32, P as bf16 (what the
+//     product takes; up to 2^-8 of each weight, of both signs, so that sums lose far less); O is rescaled
+//     in place when a row's maximum grows past the headroom left above it.
 //   * One warp issues the MMAs: S = Q K^T (M128 N128 K64) and O += P V (M128 N64 K128); one the copies.
 //   * Masks are looked at only in tiles that hold drafted keys.  There the row warps also clear V rows
 //     past the context, and elements of drafted values that are no numbers (0 x NaN would reach rows
 //     that do not see them); the rows that do see them get them back in the epilogue.
-//   * 8-bit pools: six more warps turn codes into bf16 (exact) in shared memory.  With the value scale of
+//   * 8-bit pools: six more warps (two for K, four for V) turn codes into bf16 (exact) in shared memory.  With the value scale of
 //     a block written as 2^e f, 1 <= f < 2: V becomes 2^e code, f rides in the exponent of the weights and
 //     leaves the row sum again by 1 / f; the key scale multiplies the block's scores.
+// Measured (GB300, 32 query and 8 K/V heads, us in a graph; floor: K and V read once at the copy rate):
+// 26 nodes over four contexts of 131,072 180 (floor 159: 5.9 TB/s, 0.88 of the copy rate; DRAM), over one of
+// 131,072 67, of 16,000 26; 12 over one of 300 10.5 and 32 ragged trees over 100-1500 19.6 (the start: plan,
+// table, first tile, some 5 us; the masked last tile; the meeting of pieces, some 2.5 us); 60 nodes over
+// four of 131,072 264 (256 rows: a tile's chain, 2,350 cycles).  8-bit: 60 over two of 131,072 185 (floor 68)
+// and 48 mixed trees 53 (floor 7.4): instructions (7,800 a tile of 256 rows, 2,100 of them the converters', at 61 %
+// of the issue slots: 3,150 cycles) and 3 to 5 us from one piece to the next.
 // Every mbarrier wait is bounded; on timeout the CTA records PA_DEVFLAG_TIMEOUT, drains its own copies
 // and MMAs, frees its tensor memory, counts its pieces as delivered and returns.
 #include <math.h>
@@ -55,12 +67,15 @@ constexpr float kHeadroom = 8.0f;  // the reference of the exponents lies this f
 constexpr float kLargeScore = 131072.f;  // 2^17: a rounding of the score (log2 units) is then 2^-7
 constexpr int kPartChunks = kHeadDim / 8 + 1;  // float4s of a row for each half of the dims: sum; maximum, weight
 constexpr int kRecordFloat4s = 2 * kPartChunks * kTileM;  // of one half
-constexpr int kMinPiece = 6;      // tiles of a piece of a split segment, at least
-constexpr int kSplitTiles = 5;    // what meeting costs, in tiles: equal runs begin to pay beyond it
+constexpr int kMinPiece = 6;      // tiles of a piece of a split segment, at least (4, 6 and 8: 32 ragged trees 20.1, 19.6, 19.8 us)
+// What meeting costs, in tiles: equal runs begin to pay beyond it (bf16, 3, 5 and 8: 16 x 8000 x 32 61.5, 60.1,
+// 59.8 us, 20 x 2000 x 32 31.3, 31.3, 28.3; 8 bits, 3 and 5: 16 x 8000 x 32 83.3 and 91.8, 4 x 16000 x 26 48.0, 54.0).
+constexpr int kSplitTilesBf16 = 8, kSplitTilesQ8 = 3;
 constexpr int kFlatPieces = 10;   // so many pieces are weighed at once, more by groups first: one warp's loads
 constexpr int kGroupPieces = 8;   // of a record take 0.4 us, a meeting of a group 2
 constexpr int kTogether = 3;      // records whose loads are in flight at a time
-constexpr int kPieceTiles = 1;    // what a piece costs beside its tiles, in tiles
+constexpr int kPieceTiles = 1;    // what a piece costs beside its tiles, in tiles (8-bit, 48 mixed trees: 70.6 us
+                                  // with 0, 60.6 with 1, 59.5 with 2; other batches lost as much with 2)
 constexpr int kRowsBlocks = 240;     // 8-bit blocks per CTA that the few-rows kernel walks gladly: some 40 us
 constexpr int kMaxDealtSeqs = 1024;  // sequences whose segments may get CTAs of their own
 constexpr int kPieceRing = 4;
@@ -142,7 +157,7 @@ __device__ __forceinline__ int enter_seq(Walk& w, int64_t off, int length) {
   return static_cast<int>(off - seg * length);
 }
 
-static_assert(sizeof(Walk) == kWalkBytes, "room for pieces");
+static_assert(sizeof(Walk) == kWalkBytes, "room for a walk");
 
 // Where all CTAs' runs lie: run r holds tiles total r / runs .. total (r + 1) / runs - 1.
 struct Runs {
@@ -256,6 +271,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
   constexpr int kMmaWarp = Lay::kMmaWarp, kProducerWarp = Lay::kProducerWarp;
   constexpr int kHalfTokens = kTileM / GROUP;      // query tokens of a half
   constexpr int kTokens = HALVES * kHalfTokens;    // and of a segment
+  constexpr int kSplitTiles = Q8 ? kSplitTilesQ8 : kSplitTilesBf16;
+  static_assert(kSplitTiles < kThreads / 32, "a warp for every length tried");
   const int tid = threadIdx.x;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (so that what depends on it stays uniform)
   const int lane = tid & 31;
@@ -1134,7 +1151,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       // ============================ converters (8-bit pools) ============================
       // kKWarps warps for K and kVWarps for V, each with its share of a tile's blocks, so that K runs ahead of
       // the products that V waits for.
-      constexpr int kBatch = 2;  // rows a lane holds at once (the stores may alias the loads, so those come first)
+      constexpr int kBatch = kQ8RowSteps;  // a block's rows of a lane, loaded first (the stores may alias the loads)
       const bool is_k = warp < kConvWarp0 + kKWarps;
       const int cw = warp - kConvWarp0 - (is_k ? 0 : kKWarps);
       const int blocks = kBlocksPerTile / (is_k ? kKWarps : kVWarps);  // blocks cw * blocks .. of every tile
@@ -1191,21 +1208,24 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
           uint4 in[kBatch];
 #pragma unroll
           for (int i = 0; i < kBatch; ++i) in[i] = lds128(raw + (i0 + i) * 512);
+          if (!is_k && keys < kTileN) {  // V past the context weighs nothing, but may hold anything
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+              if (8 * (i0 + i) >= keys_left) in[i] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          const uint32_t m0 = __shfl_sync(0xffffffffu, up, i0 / kBatch);
 #pragma unroll
           for (int i = 0; i < kBatch; ++i) {
-            uint4 w = in[i];
-            // V past the context weighs nothing, but may hold anything
-            if (!is_k && 8 * (i0 + i) >= keys_left) w = make_uint4(0u, 0u, 0u, 0u);
+            const uint4 w = in[i];
             uint4 a, b;
             codes4_to_bf2x2(w.x, a.x, a.y);
             codes4_to_bf2x2(w.y, a.z, a.w);
             codes4_to_bf2x2(w.z, b.x, b.y);
             codes4_to_bf2x2(w.w, b.z, b.w);
-            const uint32_t m0 = __shfl_sync(0xffffffffu, up, (i0 + i) >> 1);
             a.x = mul_bf2(a.x, m0); a.y = mul_bf2(a.y, m0); a.z = mul_bf2(a.z, m0); a.w = mul_bf2(a.w, m0);
             b.x = mul_bf2(b.x, m0); b.y = mul_bf2(b.y, m0); b.z = mul_bf2(b.z, m0); b.w = mul_bf2(b.w, m0);
             if (any_high) {  // a scale above 2^7: the rest of it
-              const uint32_t m1 = bf2_power(__shfl_sync(0xffffffffu, high, (i0 + i) >> 1));
+              const uint32_t m1 = bf2_power(__shfl_sync(0xffffffffu, high, i0 / kBatch));
               a.x = mul_bf2(a.x, m1); a.y = mul_bf2(a.y, m1); a.z = mul_bf2(a.z, m1); a.w = mul_bf2(a.w, m1);
               b.x = mul_bf2(b.x, m1); b.y = mul_bf2(b.y, m1); b.z = mul_bf2(b.z, m1); b.w = mul_bf2(b.w, m1);
             }
@@ -1333,10 +1353,13 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-// More rows than one half holds: both halves, so that a tile is fetched (and converted) once for them.
+// More rows than one half holds: both halves, so that a tile is fetched (and converted) once for them.  Over 8
+// bits from half of that on, although the second half idles: the converters serve one CTA an SM instead of two
+// (one and two CTAs: 1 x 16000 x 26 26.8 and 35.7 us, 1 x 131072 x 26 87.8, 90.5, 20 x 2000 x 32 36.1, 37.8, but
+// 64 x 2000 x 16, 64 rows, 90.7 and 73.6).  bf16 figures in this file's header.
 template <int GROUP, bool Q8>
 cudaError_t launch_halves(const TreeArgs& a, cudaStream_t stream) {
-  return a.max_query_len * GROUP > kTileM ? launch<GROUP, Q8, 2>(a, stream) : launch<GROUP, Q8, 1>(a, stream);
+  return a.max_query_len * GROUP > (Q8 ? kTileM / 2 : kTileM) ? launch<GROUP, Q8, 2>(a, stream) : launch<GROUP, Q8, 1>(a, stream);
 }
 
 template <bool Q8>
