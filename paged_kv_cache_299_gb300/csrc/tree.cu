@@ -18,7 +18,7 @@
 //   * Trees of at most 128 rows (64 over 8 bits): two CTAs per SM of one half (128 MMA rows) each, because a tile's chain
 //     (scores, softmax, product) is latency: 128 keys a tile amortise it, two chains fill in for each other.
 //     Larger ones: one CTA per SM with two halves that share every K and V tile, which is fetched, and
-//     converted, once for 256 rows (8-bit 2 x 131072 x 60: 324 us with 128 rows a CTA, 197 with halves;
+//     converted, once for 256 rows (8-bit 2 x 131072 x 60: 324 us with 128 rows a CTA, 197 with halves, when they came;
 //     bf16 4 x 131072 x 26, 104 rows: 180 us with 128, 205 with halves; 32 ragged trees, of up to 128: 19.6 and 29.0).
 //   * Tensor memory (256 columns a half): scores S 128, P 64 (bf16 pairs), O 64.  P has columns of its own,
 //     so the next tile's scores are issued as soon as the row warps have read this tile's.
@@ -31,16 +31,16 @@
 //   * Masks are looked at only in tiles that hold drafted keys.  There the row warps also clear V rows
 //     past the context, and elements of drafted values that are no numbers (0 x NaN would reach rows
 //     that do not see them); the rows that do see them get them back in the epilogue.
-//   * 8-bit pools: six more warps (two for K, four for V) turn codes into bf16 (exact) in shared memory.  With the value scale of
+//   * 8-bit pools: six more warps (two for K, four for V; four and four beside two halves) turn codes into bf16 (exact) in shared memory.  With the value scale of
 //     a block written as 2^e f, 1 <= f < 2: V becomes 2^e code, f rides in the exponent of the weights and
 //     leaves the row sum again by 1 / f; the key scale multiplies the block's scores.
 // Measured (GB300, 32 query and 8 K/V heads, us in a graph; floor: K and V read once at the copy rate):
 // 26 nodes over four contexts of 131,072 180 (floor 159: 5.9 TB/s, 0.88 of the copy rate; DRAM), over one of
 // 131,072 67, of 16,000 26; 12 over one of 300 10.5 and 32 ragged trees over 100-1500 19.6 (the start: plan,
 // table, first tile, some 5 us; the masked last tile; the meeting of pieces, some 2.5 us); 60 nodes over
-// four of 131,072 264 (256 rows: a tile's chain, 2,350 cycles).  8-bit: 60 over two of 131,072 185 (floor 68)
-// and 48 mixed trees 53 (floor 7.4): instructions (7,800 a tile of 256 rows, 2,100 of them the converters', at 61 %
-// of the issue slots: 3,150 cycles) and 3 to 5 us from one piece to the next.
+// four of 131,072 264 (256 rows: a tile's chain, 2,350 cycles).  8-bit: 60 over two of 131,072 181 (floor 68)
+// and 48 mixed trees 53 (floor 7.4): instructions (some 7,800 a tile of 256 rows, 2,100 of them the converters', at 61 %
+// of the issue slots: 3,100 cycles) and 3 to 5 us from one piece to the next.
 // Every mbarrier wait is bounded; on timeout the CTA records PA_DEVFLAG_TIMEOUT, drains its own copies
 // and MMAs, frees its tensor memory, counts its pieces as delivered and returns.
 #include <math.h>
@@ -215,11 +215,11 @@ template <bool Q8, int HALVES>
 struct Layout {
   static constexpr int kRowWarps = HALVES * kHalfWarps;
   static constexpr int kMmaWarp = kRowWarps, kProducerWarp = kRowWarps + 1, kConvWarp0 = kRowWarps + 2;
-  static constexpr int kKWarps = Q8 ? 2 : 0, kVWarps = Q8 ? 4 : 0;
-  static constexpr int kThreads = Q8 ? (HALVES == 1 ? 512 : 768) : (kRowWarps + 2) * 32;
+  static constexpr int kKWarps = Q8 ? (HALVES == 1 ? 2 : 4) : 0, kVWarps = Q8 ? 4 : 0;
+  static constexpr int kThreads = Q8 ? (HALVES == 1 ? 512 : 896) : (kRowWarps + 2) * 32;
   static constexpr int kCtasPerSm = HALVES == 1 ? 2 : 1;
   // Register split of the 8-bit kernels (setmaxnreg): what the CTA was launched with.
-  static constexpr int kRowRegs = HALVES == 1 ? 88 : 96, kOtherRegs = HALVES == 1 ? 40 : 48;
+  static constexpr int kRowRegs = HALVES == 1 ? 88 : 96, kOtherRegs = 40;
   static constexpr uint32_t kTmemCols = 256 * HALVES;
   static constexpr uint32_t kSCol = 0, kPCol = 128 * HALVES, kOCol = 192 * HALVES;  // + 128, 64, 64 per half
   static constexpr int kRing = Q8 ? (HALVES == 1 ? 2 : 3) : (HALVES == 1 ? 3 : 6);  // stages of K and V operands
@@ -257,6 +257,18 @@ __device__ __forceinline__ uint32_t seen_bits(const int32_t* bits, int q_len, in
 // A bf16 pair's elements that are no numbers (infinities and NaNs): ones in their halves.
 __device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
   return ((w & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
+}
+
+// wait_ready, its unusual case out of line where OUT: the loops of the roles share the instruction caches.  The
+// issuing and loading warps over bf16 pools: 100 trees of 5-16 nodes over 50-3000 tokens 62.9 us against 65.6; over 8
+// bits a call costs them registers (2 x 131072 x 60 195 us against 183).  The converters: 180.5 us against 183.
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
+  return wait_or_abort(bar, parity, abort_flag, status);
+}
+template <bool OUT>
+__device__ __forceinline__ bool wait_role(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
+  if (!OUT) return wait_ready(bar, parity, abort_flag, status);
+  return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag, status);
 }
 
 template <int GROUP, bool Q8, int HALVES>
@@ -969,15 +981,15 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       uint32_t kph = 0, vph = 0;
       // a tile's scores, for the first `halves` of them
       auto issue_s = [&](bool first, int halves) -> bool {
-        if (!wait_ready(&kv_full[ks], kph, &abort_flag, p.status)) return false;
+        if (!wait_role<!Q8>(&kv_full[ks], kph, &abort_flag, p.status)) return false;
         const uint64_t k_desc = k_desc0 + kStageStep * ks;
 #pragma unroll
         for (int h = 0; h < HALVES; ++h) {
           if (h >= halves) continue;
-          if (first && !wait_ready(&q_full[h], static_cast<uint32_t>(q_used[h]++ & 1), &abort_flag, p.status))
+          if (first && !wait_role<!Q8>(&q_full[h], static_cast<uint32_t>(q_used[h]++ & 1), &abort_flag, p.status))
             return false;
           if (s_issued[h] > 0 &&
-              !wait_ready(&s_free[h], static_cast<uint32_t>((s_issued[h] - 1) & 1), &abort_flag, p.status))
+              !wait_role<!Q8>(&s_free[h], static_cast<uint32_t>((s_issued[h] - 1) & 1), &abort_flag, p.status))
             return false;
           tc_fence_after_sync();
           if (leader) {
@@ -999,15 +1011,15 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       };
       // and its P V: half 0 first, whose row warps clear V for both
       auto issue_pv = [&](bool first, int halves) -> bool {
-        if (Q8 && !wait_ready(&v_full[vs], vph, &abort_flag, p.status)) return false;
+        if (Q8 && !wait_role<!Q8>(&v_full[vs], vph, &abort_flag, p.status)) return false;
         const uint64_t v_desc = v_desc0 + kStageStep * vs;
 #pragma unroll
         for (int h = 0; h < HALVES; ++h) {
           if (h >= halves) continue;
-          if (!wait_ready(&p_full[h], static_cast<uint32_t>(pv_issued[h] & 1), &abort_flag, p.status)) return false;
+          if (!wait_role<!Q8>(&p_full[h], static_cast<uint32_t>(pv_issued[h] & 1), &abort_flag, p.status)) return false;
           if (first) {  // O starts anew: the half's previous piece has been read out
             if (o_used[h] > 0 &&
-                !wait_ready(&o_free[h], static_cast<uint32_t>((o_used[h] - 1) & 1), &abort_flag, p.status))
+                !wait_role<!Q8>(&o_free[h], static_cast<uint32_t>((o_used[h] - 1) & 1), &abort_flag, p.status))
               return false;
             ++o_used[h];
           }
@@ -1039,7 +1051,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
         for (int j = 0; ok && j < n; ++j) {
           const bool last = j + 1 == n;
           if (last) {
-            if (!(ok = wait_ready(s_free, static_cast<uint32_t>((s_issued[0] - 1) & 1), &abort_flag, p.status))) break;
+            if (!(ok = wait_role<!Q8>(s_free, static_cast<uint32_t>((s_issued[0] - 1) & 1), &abort_flag, p.status))) break;
             const Piece& next = *piece_slot(units + 1);
             after = next.n;
             halves_after = halves_of(next);
@@ -1087,7 +1099,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
           const int32_t entry = __shfl_sync(0xffffffffu, win, (lb0 - win_base) + (lane & (kBlocksPerTile - 1)));
           const bool bad = need && (entry < 0 || entry >= p.num_blocks);
           if (__any_sync(0xffffffffu, bad) && lane == 0) flag_error(p.status, PA_DEVFLAG_BAD_BLOCK);
-          ok = wait_ready(&empty[st], static_cast<uint32_t>((jt / kStages) & 1) ^ 1u, &abort_flag, p.status);
+          ok = wait_role<!Q8>(&empty[st], static_cast<uint32_t>((jt / kStages) & 1) ^ 1u, &abort_flag, p.status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           if (Q8) {
             // tile (row) of each block; one that is not needed, or bad, brings the pool's first
@@ -1127,7 +1139,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       int ended = -1;
       if (Q8 && ok) {  // the converters' end: a stage without keys
         const int st = jt % kStages;
-        ok = wait_ready(&empty[st], static_cast<uint32_t>((jt / kStages) & 1) ^ 1u, &abort_flag, p.status);
+        ok = wait_role<!Q8>(&empty[st], static_cast<uint32_t>((jt / kStages) & 1) ^ 1u, &abort_flag, p.status);
         ok = __all_sync(0xffffffffu, ok);
         if (ok && leader) {
           raw_keys[st] = 0;
@@ -1162,11 +1174,11 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       int st = 0, rs = 0, slot = 0;   // operand stage, stage of codes
       uint32_t ph = 0, rph = 0;
       for (;;) {
-        bool ok = wait_ready(&raw_full[rs], rph, &abort_flag, p.status);
+        bool ok = wait_role<true>(&raw_full[rs], rph, &abort_flag, p.status);
         if (!__all_sync(0xffffffffu, ok)) break;
         const int keys = raw_keys[rs];
         if (keys == 0) break;
-        ok = wait_ready(&empty[st], ph ^ 1u, &abort_flag, p.status);
+        ok = wait_role<true>(&empty[st], ph ^ 1u, &abort_flag, p.status);
         if (!__all_sync(0xffffffffu, ok)) break;
         // lane b: what block b's codes, as bf16 pairs times 2^-120, are multiplied by: 2^120 for K, and
         // 2^(120 + e) for V, e where 120 + e is beyond bf16 apart
@@ -1182,7 +1194,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
             float lf = 0.f, fi = 1.f;
             if (f != 1.f) {
               lf = __log2f(f);
-              fi = 1.f / f;
+              fi = __fdividef(1.f, f);
             }
             float* cs = consts + slot * kConsts + blk;
             // (a hidden key's score is minus infinity: times 0 it would be a NaN)
@@ -1204,6 +1216,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
         const uint8_t* raw = sraw + rs * kRawBytes + (is_k ? 0 : kTileN * kQ8RowBytes) + cw * blocks * kQ8TileBytes + 16 * lane;
         uint8_t* dst = (is_k ? sk : sv) + st * kOpBytes;
         const int keys_left = keys - row0;
+#pragma unroll 1  // (and the rest of a large scale beside the loop: 185 us against 183, 16 x 8000 x 32 83 against 78)
         for (int i0 = 0; i0 < 2 * blocks; i0 += kBatch) {
           uint4 in[kBatch];
 #pragma unroll
@@ -1224,13 +1237,20 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
             codes4_to_bf2x2(w.w, b.z, b.w);
             a.x = mul_bf2(a.x, m0); a.y = mul_bf2(a.y, m0); a.z = mul_bf2(a.z, m0); a.w = mul_bf2(a.w, m0);
             b.x = mul_bf2(b.x, m0); b.y = mul_bf2(b.y, m0); b.z = mul_bf2(b.z, m0); b.w = mul_bf2(b.w, m0);
-            if (any_high) {  // a scale above 2^7: the rest of it
-              const uint32_t m1 = bf2_power(__shfl_sync(0xffffffffu, high, i0 / kBatch));
-              a.x = mul_bf2(a.x, m1); a.y = mul_bf2(a.y, m1); a.z = mul_bf2(a.z, m1); a.w = mul_bf2(a.w, m1);
-              b.x = mul_bf2(b.x, m1); b.y = mul_bf2(b.y, m1); b.z = mul_bf2(b.z, m1); b.w = mul_bf2(b.w, m1);
-            }
             *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * (i0 + i), c0)) = a;
             *reinterpret_cast<uint4*>(dst + swz(row0 + 8 * (i0 + i), c0 + 1)) = b;
+          }
+        }
+        if (any_high) {  // a scale above 2^7: the rest of it (each lane what it wrote)
+#pragma unroll 1
+          for (int i = 0; i < 2 * blocks; ++i) {
+            const uint32_t m1 = bf2_power(__shfl_sync(0xffffffffu, high, i / kBatch));
+#pragma unroll 1
+            for (int c = c0; c < c0 + 2; ++c) {
+              uint4* const at = reinterpret_cast<uint4*>(dst + swz(row0 + 8 * i, c));
+              const uint4 a = *at;
+              *at = make_uint4(mul_bf2(a.x, m1), mul_bf2(a.y, m1), mul_bf2(a.z, m1), mul_bf2(a.w, m1));
+            }
           }
         }
         fence_proxy_async_smem();
@@ -1355,8 +1375,9 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
 
 // More rows than one half holds: both halves, so that a tile is fetched (and converted) once for them.  Over 8
 // bits from half of that on, although the second half idles: the converters serve one CTA an SM instead of two
-// (one and two CTAs: 1 x 16000 x 26 26.8 and 35.7 us, 1 x 131072 x 26 87.8, 90.5, 20 x 2000 x 32 36.1, 37.8, but
-// 64 x 2000 x 16, 64 rows, 90.7 and 73.6).  bf16 figures in this file's header.
+// (one and two CTAs: 1 x 16000 x 26 26.1 and 35.7 us, 1 x 131072 x 26 78.1, 90.5, 20 x 2000 x 32 33.9, 37.8, but
+// 64 x 2000 x 16, 64 rows, 90.7 and 73.6).  Eight converter warps beside two halves, four for K (six: 16 x 8000 x 32
+// 78.3 us against 75.0, 1 x 131072 x 26 83.0 and 78.9, 2 x 131072 x 60 183.2 and 180.7, 48 mixed 52.7 and 53.5).  bf16 figures in this file's header.
 template <int GROUP, bool Q8>
 cudaError_t launch_halves(const TreeArgs& a, cudaStream_t stream) {
   return a.max_query_len * GROUP > (Q8 ? kTileM / 2 : kTileM) ? launch<GROUP, Q8, 2>(a, stream) : launch<GROUP, Q8, 1>(a, stream);
