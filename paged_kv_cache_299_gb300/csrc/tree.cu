@@ -74,8 +74,10 @@ constexpr int kSplitTilesBf16 = 8, kSplitTilesQ8 = 3;
 constexpr int kFlatPieces = 10;   // so many pieces are weighed at once, more by groups first: one warp's loads
 constexpr int kGroupPieces = 8;   // of a record take 0.4 us, a meeting of a group 2
 constexpr int kTogether = 3;      // records whose loads are in flight at a time
-constexpr int kPieceTiles = 1;    // what a piece costs beside its tiles, in tiles (8-bit, 48 mixed trees: 70.6 us
-                                  // with 0, 60.6 with 1, 59.5 with 2; other batches lost as much with 2)
+// What a piece costs beside its tiles, in tiles (bf16, 1, 3, 4 and 5: 64 x 1-8192 x 4-64 87.2, 77.9, 75.5, 77.0 us,
+// 40 x 1-32000 x 8-60 131.9, 121.9, 116.2, 117.3; 8 bits: 48 x 1-8192 x 4-64 53.2, 50.5, 51.8, 53.3, 40 x 1-32000 x 8-60
+// 149.5, 135.5, 137.9, 140.6).
+constexpr int kPieceTilesBf16 = 4, kPieceTilesQ8 = 3;
 constexpr int kRowsBlocks = 240;     // 8-bit blocks per CTA that the few-rows kernel walks gladly: some 40 us
 constexpr int kMaxDealtSeqs = 1024;  // sequences whose segments may get CTAs of their own
 constexpr int kPieceRing = 4;
@@ -133,7 +135,8 @@ __device__ __forceinline__ void load_seq(const TreeParams& p, int s, bool report
 }
 
 // A segment's length in the row of all tiles: what it costs beside its tiles comes first.
-__device__ __forceinline__ int span(const Seq& q) { return q.tiles + kPieceTiles; }
+template <int COST>
+__device__ __forceinline__ int span(const Seq& q) { return q.tiles + COST; }
 
 // A piece of a segment: key tiles j0 .. j0 + n - 1 of the query tile that begins at tok0, against K/V head g.
 struct Piece {
@@ -171,14 +174,14 @@ __device__ __forceinline__ int run_of(const Runs& x, int64_t tile) {
   return static_cast<int>(quotient((tile + 1) * x.runs + x.total - 1, x.total) - 1);
 }
 
-template <int TOKENS>
+template <int TOKENS, int COST>
 __device__ __forceinline__ bool next_piece(const TreeParams& p, const Runs& runs, Walk& w, Piece& u) {
   while (w.at < w.end) {
     while (w.q.q_tiles == 0 || w.g == p.num_kv_heads) {
       load_seq<TOKENS>(p, w.q.s + 1, false, w.q);
       w.g = w.q_tile = w.v = 0;
     }
-    const int n = static_cast<int>(min(static_cast<int64_t>(span(w.q) - w.v), w.end - w.at));
+    const int n = static_cast<int>(min(static_cast<int64_t>(span<COST>(w.q) - w.v), w.end - w.at));
     const int64_t first = w.at - w.v;  // where the segment begins
     u.s = w.q.s;
     u.q0 = w.q.q0;
@@ -186,11 +189,11 @@ __device__ __forceinline__ bool next_piece(const TreeParams& p, const Runs& runs
     u.L = w.q.L;
     u.g = w.g;
     u.tok0 = w.q_tile * TOKENS;
-    u.j0 = max(w.v - kPieceTiles, 0);
-    u.n = w.v + n - kPieceTiles - u.j0;
+    u.j0 = max(w.v - COST, 0);
+    u.n = w.v + n - COST - u.j0;
     w.at += n;
     w.v += n;
-    if (w.v == span(w.q)) {
+    if (w.v == span<COST>(w.q)) {
       w.v = 0;
       if (++w.q_tile == w.q.q_tiles) {
         w.q_tile = 0;
@@ -202,8 +205,8 @@ __device__ __forceinline__ bool next_piece(const TreeParams& p, const Runs& runs
     u.to = runs.own_last;
     if (runs.own_first < 0) {
       u.from = u.to = static_cast<int>(blockIdx.x);
-      if (u.j0 > 0) u.from = run_of(runs, first + kPieceTiles);
-      if (u.j0 + u.n < w.q.tiles) u.to = run_of(runs, first + span(w.q) - 1);
+      if (u.j0 > 0) u.from = run_of(runs, first + COST);
+      if (u.j0 + u.n < w.q.tiles) u.to = run_of(runs, first + span<COST>(w.q) - 1);
     }
     return true;
   }
@@ -284,6 +287,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
   constexpr int kHalfTokens = kTileM / GROUP;      // query tokens of a half
   constexpr int kTokens = HALVES * kHalfTokens;    // and of a segment
   constexpr int kSplitTiles = Q8 ? kSplitTilesQ8 : kSplitTilesBf16;
+  constexpr int kPieceTiles = Q8 ? kPieceTilesQ8 : kPieceTilesBf16;
   static_assert(kSplitTiles < kThreads / 32, "a warp for every length tried");
   const int tid = threadIdx.x;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (so that what depends on it stays uniform)
@@ -405,7 +409,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
         runs.own_first = static_cast<int>(blockIdx.x) - k;
         runs.own_last = runs.own_first + pieces - 1;
       } else {
-        w.v = enter_seq(w, off, span(q));
+        w.v = enter_seq(w, off, span<kPieceTiles>(q));
         w.at = run_start(runs, blockIdx.x);
         w.end = run_start(runs, blockIdx.x + 1);
       }
@@ -414,9 +418,9 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       *own_last = runs.own_last;
       // the row warps' first two pieces
       Piece x;
-      if (!next_piece<kTokens>(p, runs, w, x)) x.n = 0;
+      if (!next_piece<kTokens, kPieceTiles>(p, runs, w, x)) x.n = 0;
       *piece_slot(0) = x;
-      if (length > 0 || !next_piece<kTokens>(p, runs, w, x)) x.n = 0;
+      if (length > 0 || !next_piece<kTokens, kPieceTiles>(p, runs, w, x)) x.n = 0;
       *piece_slot(1) = x;
       *row_walk = w;
     };
@@ -428,7 +432,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
         q.tiles = 1;
         if (lane < p.num_seqs) load_seq<kTokens>(p, lane, blockIdx.x == 0, q);
         const int segments = q.q_tiles * p.num_kv_heads;
-        const int64_t tiles = static_cast<int64_t>(span(q)) * segments;
+        const int64_t tiles = static_cast<int64_t>(span<kPieceTiles>(q)) * segments;
         int64_t upto = inclusive(tiles);
         runs.total = __shfl_sync(0xffffffffu, upto, 31);
         runs.runs = static_cast<int>(min(static_cast<int64_t>(ctas), max(runs.total, int64_t{1})));
@@ -460,7 +464,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       for (int s = s0; s < s1; ++s) {
         load_seq<kTokens>(p, s, blockIdx.x == 0, q);
         const int n = q.q_tiles * p.num_kv_heads;
-        mine += static_cast<int64_t>(span(q)) * n;
+        mine += static_cast<int64_t>(span<kPieceTiles>(q)) * n;
         segments += n;
         if (p.num_seqs <= kMaxDealtSeqs) {
           seq_tiles[s] = q.tiles;
@@ -513,7 +517,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
         int64_t off = want - before;
         for (int s = s0; s < s1; ++s) {
           load_seq<kTokens>(p, s, false, q);
-          const int64_t n = static_cast<int64_t>(length > 0 ? (q.tiles + length - 1) / length : span(q)) *
+          const int64_t n = static_cast<int64_t>(length > 0 ? (q.tiles + length - 1) / length : span<kPieceTiles>(q)) *
                             (q.q_tiles * p.num_kv_heads);
           if (off < n) {
             settle(q, off, length);
@@ -779,7 +783,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
         if (j == 0 && warp == 0 && lane == 0) {
           Walk w = *row_walk;
           Piece x;
-          if (!next_piece<kTokens>(p, runs, w, x)) x.n = 0;
+          if (!next_piece<kTokens, kPieceTiles>(p, runs, w, x)) x.n = 0;
           *piece_slot(units + 2) = x;
           *row_walk = w;
         }
@@ -1079,7 +1083,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       constexpr int kStages = Q8 ? kRawRing : kRing;
       uint64_t* const full = Q8 ? raw_full : kv_full;
       uint64_t* const empty = Q8 ? raw_empty : tile_done;
-      while (ok && next_piece<kTokens>(p, runs, walk, cur)) {
+      while (ok && next_piece<kTokens, kPieceTiles>(p, runs, walk, cur)) {
         const int32_t* row = p.block_tables + static_cast<int64_t>(cur.s) * p.max_blocks_per_seq;
         const int blocks = (cur.L + kBlockSize - 1) / kBlockSize;
         // 32 table entries (four tiles) at a time, one per lane, the next window in flight
@@ -1284,7 +1288,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
     Walk w = *start_walk;
     Piece u;
     int n = 0;
-    while (next_piece<kTokens>(p, runs, w, u)) {
+    while (next_piece<kTokens, kPieceTiles>(p, runs, w, u)) {
       if (u.from == u.to || !warp_active(u, tid) || n++ < delivered[tid]) continue;
       const int pieces = u.to - u.from + 1;
       int32_t* counter = p.counters + u.from * kRowWarps + tid;
