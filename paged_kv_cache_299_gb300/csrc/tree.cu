@@ -35,12 +35,12 @@
 //     a block written as 2^e f, 1 <= f < 2: V becomes 2^e code, f rides in the exponent of the weights and
 //     leaves the row sum again by 1 / f; the key scale multiplies the block's scores.
 // Measured (GB300, 32 query and 8 K/V heads, us in a graph; floor: K and V read once at the copy rate):
-// 26 nodes over four contexts of 131,072 180 (floor 159: 5.9 TB/s, 0.88 of the copy rate; DRAM), over one of
-// 131,072 67, of 16,000 26; 12 over one of 300 10.5 and 32 ragged trees over 100-1500 19.6 (the start: plan,
+// 26 nodes over four contexts of 131,072 179 (floor 159: 6.0 TB/s, 0.89 of the copy rate; DRAM), over one of
+// 131,072 67, of 16,000 26; 12 over one of 300 10.3 and 32 ragged trees over 100-1500 18.7 (the start: plan,
 // table, first tile, some 5 us; the masked last tile; the meeting of pieces, some 2.5 us); 60 nodes over
-// four of 131,072 264 (256 rows: a tile's chain, 2,350 cycles).  8-bit: 60 over two of 131,072 181 (floor 68)
-// and 48 mixed trees 53 (floor 7.4): instructions (some 7,800 a tile of 256 rows, 2,100 of them the converters', at 61 %
-// of the issue slots: 3,100 cycles) and 3 to 5 us from one piece to the next.
+// four of 131,072 266 (256 rows: a tile's chain, 2,350 cycles).  8-bit: 60 over two of 131,072 181 (floor 68)
+// and 48 mixed trees 50 (floor 7.4): instructions (7,900 a tile of 256 rows, 2,200 of them the converters', at 66 %
+// of the issue slots: 3,000 cycles) and 3 to 5 us from one piece to the next.
 // Every mbarrier wait is bounded; on timeout the CTA records PA_DEVFLAG_TIMEOUT, drains its own copies
 // and MMAs, frees its tensor memory, counts its pieces as delivered and returns.
 #include <math.h>
@@ -78,7 +78,7 @@ constexpr int kTogether = 3;      // records whose loads are in flight at a time
 // 40 x 1-32000 x 8-60 131.9, 121.9, 116.2, 117.3; 8 bits: 48 x 1-8192 x 4-64 53.2, 50.5, 51.8, 53.3, 40 x 1-32000 x 8-60
 // 149.5, 135.5, 137.9, 140.6).
 constexpr int kPieceTilesBf16 = 4, kPieceTilesQ8 = 3;
-constexpr int kRowsBlocks = 240;     // 8-bit blocks per CTA that the few-rows kernel walks gladly: some 40 us
+constexpr int kRowsBlocks = 128;  // 8-bit blocks per CTA of the few-rows kernel, at most: some 20 us
 constexpr int kMaxDealtSeqs = 1024;  // sequences whose segments may get CTAs of their own
 constexpr int kPieceRing = 4;
 constexpr int kWalkBytes = 56;
@@ -1433,13 +1433,12 @@ cudaError_t launch_tree_q8(const TreeArgs& a, cudaStream_t stream) {
   const cudaError_t e = device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
   if (rows_q8_takes(r)) {
-    // Few rows run best on the few-rows kernel (8 nodes, 8 heads: one context of 700 9.2 us against 14.5, 32
-    // of 1000 19.1 against 23.7, 256 of 1000 117 and 160, 4 of 131072 191 and 219), but its clusters take
-    // equal parts of a segment: long contexts that leave its CTAs few keep it waiting (one of 131072 161 us
-    // against 67, 20 of 16000 185 and 143).
-    const int cluster = rows_q8_cluster(r, sms);
-    const int64_t ctas = static_cast<int64_t>(r.num_seqs) * r.num_kv_heads * cluster;
-    if (3 * ctas >= 4 * sms || r.max_blocks_per_seq <= kRowsBlocks * cluster) return launch_rows_q8(r, stream);
+    // Few rows run best on the few-rows kernel (8 nodes, 8 K/V heads: one context of 700 9.1 us against 14.0, of
+    // 4000 11.9 and 19.5, 32 of 1000 18.9 and 21.6, 100 of 2000 82 and 94), but its clusters take equal parts of a
+    // segment, so the longest context there may be is what it waits for (64 of 1-8192 90 us against 47, 64 of 1-32000
+    // 321 and 100, one of 131072 160 and 65, 20 of 16000 182 and 124): where that is long, even batches do
+    // without it as well (64 of 4000 101 and 110, 40 of 4000 75.5 and 74.8).
+    if (r.max_blocks_per_seq <= kRowsBlocks * rows_q8_cluster(r, sms)) return launch_rows_q8(r, stream);
   }
   return launch_group<true>(a, stream);
 }
