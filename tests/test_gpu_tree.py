@@ -107,6 +107,16 @@ def test_few_rows_over_8_bits(L, seqs, hq, hkv, n):
     Trees("q8", [L - 7 * i for i in range(seqs)], [n] + [max(1, n - 2)] * (seqs - 1), hq, hkv, "mask", seed=L + n).check()
 
 
+@pytest.mark.parametrize("seqs,hq,hkv", [(40, 32, 8), (14, 16, 8), (9, 32, 8), (24, 3, 3)])
+def test_small_trees_of_uneven_batches(seqs, hq, hkv):
+    """Under block tables as wide as the contexts, and as wide as a cache for much longer ones (entries that are not
+    in use name no block): what serves the call depends on it."""
+    r = np.random.default_rng(seqs)
+    t = Trees("q8", r.integers(0, 1900, seqs), r.integers(1, 9, seqs), hq, hkv, "tree", seed=seqs)
+    t.check()
+    t.check(t.run(bt=torch.nn.functional.pad(t.bt, (0, 1100), value=-1)))
+
+
 @pytest.mark.parametrize("pool", POOLS)
 @pytest.mark.parametrize("hist,nodes", [
     ([20000] + [30] * 40, [20] + [5] * 40),
