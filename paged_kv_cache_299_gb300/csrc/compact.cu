@@ -90,6 +90,23 @@ __device__ __forceinline__ bool blocks_of(const CompactArgs& a, const int32_t* t
   return fine;
 }
 
+// Where N entries of a list (below 0: none wanted) move: positions and blocks; one block of a move is below 0
+// where nothing is to do, or something was reported.
+template <int N>
+__device__ __forceinline__ void moves_of(const CompactArgs& a, const int32_t* kept, const int32_t* table,
+                                         const int32_t (&i)[N], int32_t first, bool report, int32_t (&src)[N],
+                                         int32_t (&dst)[N], int32_t (&from)[N], int32_t (&at)[N]) {
+  const bool fine = sources_of(a, kept, i, first, src);
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    dst[u] = src[u] >= 0 ? first + i[u] : -1;
+    if (src[u] == dst[u]) src[u] = dst[u] = -1;  // it stays
+  }
+  const bool blocks = blocks_of(a, table, src, from) & blocks_of(a, table, dst, at);
+  if (report && !fine) flag_error(a.status, PA_DEVFLAG_BAD_CONTEXT);
+  if (report && !blocks) flag_error(a.status, PA_DEVFLAG_BAD_BLOCK);
+}
+
 // WARPS warps (of one CTA, if more than one) serve one (sequence, K/V head, pool).
 template <int WARPS>
 __global__ void __launch_bounds__((WARPS > 1 ? WARPS : kCtaWarps) * 32) compact_kernel(const CompactArgs a) {
@@ -112,30 +129,61 @@ __global__ void __launch_bounds__((WARPS > 1 ? WARPS : kCtaWarps) * 32) compact_
     return pool + ((static_cast<int64_t>(block) * a.num_kv_heads + h) * kBlockSize + p % kBlockSize) * kRowLanes +
            lane % kRowLanes;
   };
-  for (int32_t i0 = 0; i0 < n; i0 += WARPS * kWarpRows) {
-    int32_t i[kUnroll], src[kUnroll], dst[kUnroll], from[kUnroll], at[kUnroll];
+  if (WARPS == 1) {
+    for (int32_t i0 = 0; i0 < n; i0 += kWarpRows) {
+      int32_t i[kUnroll], src[kUnroll], dst[kUnroll], from[kUnroll], at[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int32_t x = i0 + mine + u * kRowsAtOnce;
+      for (int u = 0; u < kUnroll; ++u) {
+        const int32_t x = i0 + mine + u * kRowsAtOnce;
+        i[u] = x < n ? x : -1;
+      }
+      moves_of(a, kept, table, i, first, report, src, dst, from, at);
+      uint4 x[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (from[u] >= 0 && at[u] >= 0) x[u] = *place(from[u], src[u]);
+      __syncwarp();  // a round is read before it is written
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (from[u] >= 0 && at[u] >= 0) *place(at[u], dst[u]) = x[u];
+    }
+    return;
+  }
+  // A CTA looks kRounds rounds' moves up at once, a thread kMoves of them, and keeps them in shared memory, so that
+  // the list and the tables are waited for once.
+  constexpr int kRounds = 4, kRoundRows = WARPS * kWarpRows, kMoves = kRounds * kRoundRows / (WARPS * 32);
+  __shared__ int2 blocks[kRounds * kRoundRows];      // of source and destination; below 0: nothing moves
+  __shared__ uint8_t offset[kRounds * kRoundRows];   // the source's in its block
+  for (int32_t i0 = 0; i0 < n; i0 += kRounds * kRoundRows) {
+    int32_t i[kMoves], src[kMoves], dst[kMoves], from[kMoves], at[kMoves];
+#pragma unroll
+    for (int u = 0; u < kMoves; ++u) {
+      const int32_t x = i0 + static_cast<int>(threadIdx.x) + u * WARPS * 32;
       i[u] = x < n ? x : -1;
     }
-    const bool fine = sources_of(a, kept, i, first, src);
+    moves_of(a, kept, table, i, first, report, src, dst, from, at);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      dst[u] = src[u] >= 0 ? first + i[u] : -1;
-      if (src[u] == dst[u]) src[u] = dst[u] = -1;  // it stays
+    for (int u = 0; u < kMoves; ++u) {
+      const int e = threadIdx.x + u * WARPS * 32;
+      blocks[e] = at[u] >= 0 ? make_int2(from[u], at[u]) : make_int2(-1, -1);
+      offset[e] = static_cast<uint8_t>(src[u] & (kBlockSize - 1));
     }
-    const bool blocks = blocks_of(a, table, src, from) & blocks_of(a, table, dst, at);
-    if (report && !fine) flag_error(a.status, PA_DEVFLAG_BAD_CONTEXT);
-    if (report && !blocks) flag_error(a.status, PA_DEVFLAG_BAD_BLOCK);
-    uint4 x[kUnroll];
+    __syncthreads();
+#pragma unroll 1
+    for (int e0 = 0; e0 < kRounds * kRoundRows && i0 + e0 < n; e0 += kRoundRows) {
+      uint4 x[kUnroll];
+      int2 b[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (from[u] >= 0 && at[u] >= 0) x[u] = *place(from[u], src[u]);
-    if (WARPS > 1) __syncthreads(); else __syncwarp();  // a round is read before it is written
+      for (int u = 0; u < kUnroll; ++u) {
+        const int e = e0 + mine + u * kRowsAtOnce;
+        b[u] = blocks[e];
+        if (b[u].x >= 0) x[u] = *place(b[u].x, offset[e]);
+      }
+      __syncthreads();  // a round is read before it is written
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (from[u] >= 0 && at[u] >= 0) *place(at[u], dst[u]) = x[u];
+      for (int u = 0; u < kUnroll; ++u)
+        if (b[u].x >= 0) *place(b[u].y, first + i0 + e0 + mine + u * kRowsAtOnce) = x[u];
+    }
   }
 }
 
