@@ -14,9 +14,9 @@
 // where earlier tokens stay.
 //
 // Memory-bound: every row is read and written once.  Measured (8 K/V heads): 64 histories of 300 to 500
-// kept tokens 20.2 us (106.7 MB, 5.3 TB/s, 0.78 of the copy rate: a list, a table entry and a row one after
-// the other, then the writes, in one or two rounds a CTA); 32 paths of up to 5 tokens 2.7 us, into the
-// 8-bit pools 3.2, 256 of up to 8 there 5.9: the launch and the chain of dependent loads.
+// kept tokens (106.9 MB) 13.3 us where a replay finds what the last one wrote in L2, 17.8 from DRAM (6.0 TB/s, 0.89
+// of the copy rate; 23.2 with the list and the tables waited for in every round); 32 paths of up to 5 tokens 2.6 us,
+// 256 of up to 8 in the 8-bit pools 5.7: the launch and the chain of dependent loads.
 #include <math.h>
 
 #include "common.cuh"
@@ -316,18 +316,16 @@ __global__ void __launch_bounds__((WARPS > 1 ? WARPS : kCtaWarps) * 32) compact_
 }  // namespace
 
 // Warps of an item (sequence, head, pool), by the longest list: of a few tokens a warp, four items a CTA;
-// otherwise a CTA, of so many warps that a round or two takes the list, as long as the CTAs run side by side
-// (bf16, 300 to 500 tokens of 8 sequences with 8 heads: 5.5 us with 16 warps, 6.4 with 8, 9.5 with 4; of 64
-// sequences: 23.5, 20.4, 19.6).
+// otherwise a CTA, of sixteen warps as long as the CTAs run side by side, of four beyond (bf16, 4, 8 and 16
+// warps: 8 sequences of 300 to 500 tokens, 8 heads 6.3, 4.3, 4.2 us, 64 of them 13.5, 14.5, 17.1, 256 of 100 to 250
+// 33.0, 39.3, 50.5, 2 of 4000 to 6000 40.2, 23.1, 18.5).
 cudaError_t launch_compact(const CompactArgs& a, cudaStream_t stream) {
   const int64_t items = 2ll * a.num_seqs * a.num_kv_heads;
   const unsigned grid = static_cast<unsigned>(items);
   if (a.max_kept <= 2 * kWarpRows)
     compact_kernel<1><<<static_cast<unsigned>((items + kCtaWarps - 1) / kCtaWarps), kCtaWarps * 32, 0, stream>>>(a);
-  else if (a.max_kept <= 8 * kWarpRows)
+  else if (a.max_kept <= 8 * kWarpRows || items > kManyItems)
     compact_kernel<4><<<grid, 4 * 32, 0, stream>>>(a);
-  else if (items > kManyItems)
-    compact_kernel<8><<<grid, 8 * 32, 0, stream>>>(a);
   else
     compact_kernel<16><<<grid, 16 * 32, 0, stream>>>(a);
   return cudaGetLastError();
