@@ -131,6 +131,15 @@ def test_shift_by_one_over_many_rounds(pool):
 
 
 @pytest.mark.parametrize("pool", POOLS)
+def test_many_long_lists(pool):
+    rng = np.random.default_rng(6)
+    kept = lists(rng, 20, 900, 1, 600) + [list(range(1, n)) for n in (2, 256, 257, 258, 513, 700)]
+    c = Cache(pool, rng.integers(0, 40, len(kept)), kept, 8, seed=6)
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("pool", POOLS)
 def test_a_large_bound_changes_nothing(pool):
     rng = np.random.default_rng(5)
     first, kept = rng.integers(0, 100, 12), lists(rng, 12, 50, 0, 30)
