@@ -517,6 +517,7 @@ size_t pa_tree_workspace_size(void);
  *   workspace        pa_tree_workspace_size() bytes, 16-byte aligned
  * A block id outside [0, num_blocks) sets PA_DEVFLAG_BAD_BLOCK; rows of that sequence are undefined.
  * Rows of q and out outside query_start_loc[0] .. query_start_loc[num_seqs] - 1 are left alone.
+ * Tight bounds pay: max_query_len and the width of the block tables choose how the work is split.
  * Results do not depend on the order in which CTAs run.  num_seqs == 0, num_query_tokens == 0 and
  * max_query_len == 0 are no-ops. */
 pa_status pa_tree_attention(void* out, const void* q, const int32_t* tree_mask, int32_t mask_words,
@@ -561,9 +562,9 @@ pa_status pa_compact_tokens(const int32_t* kept, const int32_t* kept_start_loc,
                             int32_t num_seqs, int32_t* device_status, pa_stream_t stream);
 
 /* The same in the 8-bit pools: the values code * scale go to their new blocks as pa_rope_append_q8
- * would store them (also those whose slot stays the same).  A block whose first slot receives a token starts with the smallest scale that
- * fits what moves into it; one with tokens before first[s] keeps its scale or grows it (and their codes
- * are rescaled).  A block that a bad entry, block id or scale (negative, not finite; zero too where
+ * would store them (also those whose slot stays the same).  A block whose first slot receives a token
+ * starts with the smallest scale that fits what moves into it; one with tokens before first[s] keeps
+ * its scale or grows it (and their codes are rescaled).  A block that a bad entry, block id or scale (negative, not finite; zero too where
  * earlier tokens stay) takes part in is reported and left as it is. */
 pa_status pa_compact_tokens_q8(const int32_t* kept, const int32_t* kept_start_loc,
                                const int32_t* first, int32_t num_kept, int32_t max_kept,
