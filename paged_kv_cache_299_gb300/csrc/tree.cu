@@ -93,7 +93,9 @@ struct TreeParams {
   const float* key_scale;            // 8-bit pools
   const float* value_scale;
   int32_t* counters;  // [grid][row warps] pieces delivered by each of the segment that starts in a CTA and goes on
-  int32_t* group_counters;  // the same of groups of pieces, by the CTA of their first
+  // [grid][2][row warps] the same of groups of pieces, by the CTA of their first piece: the first group of the segment
+  // that starts there (as in a record's place), or a group of one that began before.  A CTA can hold both.
+  int32_t* group_counters;
   float4* records;    // [grid][2][halves][half of the dims][kPartChunks][128]
   int32_t* status;
   int32_t mask_words, max_blocks_per_seq, num_blocks, num_kv_heads, num_q_heads;
@@ -541,6 +543,10 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
   auto warp_active = [&](const Piece& u, int w) {
     return u.tok0 + (w / kHalfWarps) * kHalfTokens + (w & 3) * 32 / GROUP < u.q_len;
   };
+  // Where row warps w deliver the group of a segment's pieces (from CTA `from` on) whose first is CTA `first`'s.
+  auto group_counter = [&](int first, int from, int w) -> int32_t* {
+    return p.group_counters + (2 * first + (first == from ? 1 : 0)) * kRowWarps + w;
+  };
 
   if (warp < kRowWarps) {
     // ============================ row warps ============================
@@ -925,7 +931,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
           // groups first, whose sums take the place of their first records; then the groups
           const int first = from + (static_cast<int>(blockIdx.x) - from) / kGroupPieces * kGroupPieces;
           const int count = min(kGroupPieces, to + 1 - first);
-          if (arrive(p.group_counters + first * kRowWarps + warp, count)) {
+          if (arrive(group_counter(first, from, warp), count)) {
             if (row_ok) weigh(first, 1, count);
             keep(record_of(first, first == from));
             const int groups = (pieces + kGroupPieces - 1) / kGroupPieces;
@@ -1295,7 +1301,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ 
       int count = pieces;
       if (pieces > kFlatPieces) {
         const int first = u.from + (static_cast<int>(blockIdx.x) - u.from) / kGroupPieces * kGroupPieces;
-        int32_t* group = p.group_counters + first * kRowWarps + tid;
+        int32_t* group = group_counter(first, u.from, tid);
         if (atomicAdd(group, 1) != min(kGroupPieces, u.to + 1 - first) - 1) continue;
         *group = 0;
         count = (pieces + kGroupPieces - 1) / kGroupPieces;
@@ -1356,7 +1362,7 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
   p.value_scale = a.value_scale;
   p.counters = static_cast<int32_t*>(a.workspace);
   p.group_counters = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(a.workspace) + counter_bytes(sms));
-  p.records = reinterpret_cast<float4*>(static_cast<uint8_t*>(a.workspace) + 2 * counter_bytes(sms));
+  p.records = reinterpret_cast<float4*>(static_cast<uint8_t*>(a.workspace) + 3 * counter_bytes(sms));
   p.status = a.status;
   p.mask_words = a.mask_words;
   p.max_blocks_per_seq = a.max_blocks_per_seq;
@@ -1402,7 +1408,7 @@ cudaError_t launch_group(const TreeArgs& a, cudaStream_t stream) {
 size_t tree_workspace_size() {
   int dev = 0, sms = 0;
   if (device_sms(&dev, &sms) != cudaSuccess) return 0;
-  return 2 * counter_bytes(sms) + record_bytes(sms);
+  return 3 * counter_bytes(sms) + record_bytes(sms);
 }
 
 cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream) { return launch_group<false>(a, stream); }

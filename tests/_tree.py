@@ -115,3 +115,14 @@ def live_slots(num_blocks, tables, context_lens):
         for b in range(-(-n // 16)):
             live[int(tables[s, b]), :min(16, n - 16 * b)] = True
     return live
+
+
+# Uneven batches, 4 query heads per K/V head: (pool, K/V heads, prefixes, nodes).  On 152 SMs neighbouring
+# segments of more than ten pieces meet in one CTA, the first with its last piece (17, 25, ... in all) alone.
+MEETING_BATCHES = {
+    "bf16 one half": ("bf16", 8, [45519] * 2 + [326] * 18, [12] * 20),
+    "bf16 two halves": ("bf16", 4, [45493] * 2 + [623] * 13, [40] * 15),
+    "q8 short ones behind": ("q8", 4, [29294] * 2 + [363] * 14, [20] * 16),
+    "q8 even": ("q8", 3, [131072] * 3, [40] * 3),
+    "q8 more rows than a segment takes": ("q8", 4, [16217, 105684, 426], [101, 91, 107]),
+}
