@@ -238,7 +238,8 @@ __global__ void __launch_bounds__((WARPS > 1 ? WARPS : kCtaWarps) * 32) compact_
   // rows o0 .. o1 - 1 of block b are written; row o is the list's entry b * 16 + o - first
   auto first_row = [&](int64_t b) { return b == b_lo ? first % kBlockSize : 0; };
   auto last_row = [&](int64_t b) {
-    return b <= b_hi ? static_cast<int>(min(static_cast<int64_t>(kBlockSize), first + n - b * kBlockSize)) : 0;
+    // (in 64 bits: a wrong `first` may lie near the end of the ints)
+    return b <= b_hi ? static_cast<int>(min(static_cast<int64_t>(kBlockSize), static_cast<int64_t>(first) + n - b * kBlockSize)) : 0;
   };
   auto read = [&](int64_t b, Round& r) {
     const int o0 = first_row(b), o1 = last_row(b);
