@@ -45,6 +45,11 @@ __device__ __forceinline__ float scale_for(float amax) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+// A word's codes with the largest of its sign in place of one that is no number (0x7f, 0xff).
+__device__ __forceinline__ uint32_t number_codes(uint32_t w) {
+  return w & ~((((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7);
+}
+
 // Four codes of a word as bf16 pairs times 2^-120 (exact): the code's exponent and
 // significand bits, three places down from the bf16's, under its sign.
 __device__ __forceinline__ void codes4_to_bf2x2(uint32_t w, uint32_t& lo, uint32_t& hi) {

@@ -174,7 +174,8 @@ __device__ __forceinline__ void attend_tiles(const uint8_t* const (&tiles)[T], i
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int token = first[t] + t0 + 2 * (i & 1) + 8 * (i >> 1);
-        if (token > end) v[t][i] = make_uint2(0u, 0u);
+        // (a weight of 0 times a code that is no number would reach rows that do not see it)
+        v[t][i] = token > end ? make_uint2(0u, 0u) : make_uint2(number_codes(v[t][i].x), number_codes(v[t][i].y));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
           if (TREE ? token >= drafted + 32 || (token >= drafted && ((w.pos[nt] >> (token - drafted)) & 1) == 0)

@@ -1,0 +1,44 @@
+"""pa_tree_attention where rows, masks and codes are at the ends of what its documentation allows."""
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_cache_299_gb300 import binding as pa
+from _gpu import i32
+from test_gpu_tree import POOLS, Trees, close
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("code", [0x7f, 0xff])
+@pytest.mark.parametrize("hist,n,hq,hkv", [(0, 7, 4, 1), (50, 8, 8, 2), (61, 30, 3, 3), (1000, 6, 4, 1), (0, 20, 4, 1),
+                                           (60, 70, 2, 2)])
+def test_codes_that_are_no_numbers_reach_no_row_that_does_not_see_them(code, hist, n, hq, hkv):
+    """A drafted token's key or value codes, on the few-rows kernel (up to 32 rows per K/V head) and the other."""
+    for which in (0, 1):
+        t = Trees("q8", [hist, 10], [n, 5], hq, hkv, "tree", seed=11)
+        pos = hist + n // 2
+        clean = t.check().to(torch.bfloat16)
+        t.dev[which].view(torch.uint8)[int(t.w.block_tables[0, pos // 16]), :, pos % 16, 5:40] = code
+        got = t.run().cpu()
+        assert t.ok()
+        blind = [i for i in range(t.rows) if i >= n or not t.bits[0][i] >> (n // 2) & 1]
+        assert 5 < len(blind) < t.rows
+        assert torch.equal(got[blind], clean[blind])
+
+
+@pytest.mark.parametrize("code", [0x7f, 0xff])
+def test_codes_that_are_no_numbers_reach_no_earlier_row_of_a_chunk(code):
+    t = Trees("q8", [100, 3], [8, 5], 4, 1, "chain", seed=12)
+
+    def chunk():
+        out = torch.zeros_like(t.q, device="cuda")
+        pa.pa_prefill_chunk_q8(out, t.q.cuda(), t.starts, t.most, *t.dev, t.bt, t.ctx, 0.125)
+        return out.cpu()
+
+    clean = chunk()
+    assert torch.isfinite(clean).all()
+    t.dev[1].view(torch.uint8)[int(t.w.block_tables[0, 105 // 16]), :, 105 % 16, :] = code
+    got = chunk()
+    blind = [i for i in range(t.rows) if i < 5 or i >= 8]
+    assert torch.equal(got[blind], clean[blind])
