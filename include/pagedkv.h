@@ -512,8 +512,9 @@ size_t pa_tree_workspace_size(void);
  *                    node itself and of its ancestors
  *   mask_words       at least ceil(max_query_len / 32)
  *   max_query_len    host bound of q_len, at most 1024; a longer sequence of rows sets
- *                    PA_DEVFLAG_BAD_CONTEXT and is left alone, as is one with rows outside q or a context
- *                    shorter than them, longer than its block-table row or longer than the pool
+ *                    PA_DEVFLAG_BAD_CONTEXT and is left alone, as is one with fewer than no rows
+ *                    (query_start_loc falls), with rows outside q or with a context shorter than
+ *                    them, longer than its block-table row or longer than the pool
  *   workspace        pa_tree_workspace_size() bytes, 16-byte aligned
  * A block id outside [0, num_blocks) sets PA_DEVFLAG_BAD_BLOCK; rows of that sequence are undefined.
  * Rows of q and out outside query_start_loc[0] .. query_start_loc[num_seqs] - 1 are left alone.

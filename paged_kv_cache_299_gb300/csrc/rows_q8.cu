@@ -302,8 +302,8 @@ paged_rows_q8_kernel(const __grid_constant__ RowsParams p) {
   const int q0 = p.query_start_loc[s];
   const int q_len = p.query_start_loc[s + 1] - q0;
   const int L = p.context_lens[s];
-  if (q_len <= 0) return;
-  if (q0 < 0 || q_len > p.num_query_tokens - q0 || q_len > p.max_query_len || L < q_len ||
+  if (TREE ? q_len == 0 : q_len <= 0) return;
+  if (q_len < 0 || q0 < 0 || q_len > p.num_query_tokens - q0 || q_len > p.max_query_len || L < q_len ||
       static_cast<int64_t>(L) > static_cast<int64_t>(p.max_blocks_per_seq) * kBlockSize ||
       (TREE && static_cast<int64_t>(L) > static_cast<int64_t>(p.num_blocks) * kBlockSize)) {
     if (g == 0 && rank == 0 && tid == 0) flag_error(p.status, PA_DEVFLAG_BAD_CONTEXT);

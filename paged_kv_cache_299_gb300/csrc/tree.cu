@@ -125,8 +125,8 @@ __device__ __forceinline__ void load_seq(const TreeParams& p, int s, bool report
   q.L = __ldg(p.context_lens + s);
   q.q_tiles = 0;
   q.tiles = 1;
-  if (q.q_len <= 0) return;
-  if (q.q0 < 0 || q.q_len > p.num_query_tokens - q.q0 || q.q_len > p.max_query_len || q.L < q.q_len ||
+  if (q.q_len == 0) return;
+  if (q.q_len < 0 || q.q0 < 0 || q.q_len > p.num_query_tokens - q.q0 || q.q_len > p.max_query_len || q.L < q.q_len ||
       q.L > static_cast<int64_t>(p.max_blocks_per_seq) * kBlockSize ||
       q.L > static_cast<int64_t>(p.num_blocks) * kBlockSize) {
     if (report) flag_error(p.status, PA_DEVFLAG_BAD_CONTEXT);

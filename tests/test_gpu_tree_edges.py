@@ -1,5 +1,4 @@
 """pa_tree_attention where rows, masks and codes are at the ends of what its documentation allows."""
-import numpy as np
 import pytest
 import torch
 
@@ -42,3 +41,28 @@ def test_codes_that_are_no_numbers_reach_no_earlier_row_of_a_chunk(code):
     got = chunk()
     blind = [i for i in range(t.rows) if i < 5 or i >= 8]
     assert torch.equal(got[blind], clean[blind])
+
+
+@pytest.mark.parametrize("pool", POOLS)
+@pytest.mark.parametrize("most", [4, 9])  # over 8 bits the few-rows kernel and the other
+def test_starts_that_fall_are_reported(pool, most):
+    """A sequence of fewer than no rows has none; the others' rows are right, and no other row is written."""
+    t = Trees(pool, [30, 40, 50], [4, 2, 3], 4, 1, seed=13)
+    ref, tol = t.expected()
+    at = {0: 6, 1: 7, 2: 8, 5: 0, 6: 1, 7: 2, 8: 3}  # rows of the call: the third sequence's, then the first's
+    q, mask = t.q.clone(), t.mask.clone()
+    for row, old in at.items():
+        q[row], mask[row] = t.q[old], t.mask[old]
+    got = t.run(q=q.cuda(), mask=mask, starts=i32([5, 9, 0, 3]), most=most).cpu().double()
+    assert int(t.status.item()) == pa.DEVFLAG_BAD_CONTEXT
+    close(got[list(at)], ref[list(at.values())], tol[list(at.values())])
+    assert (got[[3, 4]] == 7.0).all()
+
+
+@pytest.mark.parametrize("pool", POOLS)
+@pytest.mark.parametrize("count", [1, 33])
+def test_empty_sequences_are_not_reported(pool, count):
+    """Also with a context of 0, as padding has it; among up to 32 sequences and among more."""
+    t = Trees(pool, [30] + [0] * count, [4] + [0] * count, 4, 1, seed=14)
+    t.check()
+    t.check(t.run(ctx=i32([34] + [-1] * count)))
