@@ -716,17 +716,21 @@ def pa_copy_blocks_q8(key_cache, value_cache, key_scale, value_scale, block_mapp
         _check(st, "pa_copy_blocks_q8")
 
 
-_packed_axes = {}  # of the pair_axes seen: their packed form and their last axis
+_packed_axes = {}  # of the pair_axes seen, as bytes: their packed form and their last axis
 
 
 def _pair_axes(pair_axes, num_axes):
     """32 axis numbers (None: all pairs on axis 0) as two bits each."""
     if pair_axes is None:
         return 0
-    key = tuple(pair_axes)
+    try:
+        # (whole numbers alone, whatever their type; bytes of a number or an array would be something else)
+        key = bytes(pair_axes if type(pair_axes) is list else tuple(pair_axes))
+    except (TypeError, ValueError):
+        key = b""
     packed = _packed_axes.get(key)
     if packed is None:
-        if len(key) != 32 or not all(isinstance(a, int) and 0 <= a < 4 for a in key):
+        if len(key) != 32 or max(key) > 3:
             raise ValueError("pair_axes must be 32 axis numbers, one per rotation pair")
         if len(_packed_axes) >= 64:
             _packed_axes.clear()
