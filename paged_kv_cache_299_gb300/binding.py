@@ -801,7 +801,7 @@ def pack_tree_mask(seen):
     if seen.dtype is not torch.bool or seen.dim() != 2:
         raise ValueError("seen must be bool [rows, drafted tokens]")
     words = (seen.shape[1] + 31) // 32
-    bits = torch.nn.functional.pad(seen, (0, 32 * words - seen.shape[1])).view(-1, words, 32)
+    bits = torch.nn.functional.pad(seen, (0, 32 * words - seen.shape[1])).view(seen.shape[0], words, 32)
     place = torch.arange(32, dtype=torch.int64, device=seen.device)
     return (bits.to(torch.int64) << place).sum(dim=2).to(torch.int32)
 

@@ -27,3 +27,15 @@ def test_pair_axes_that_are_none_are_refused(axes):
         with pytest.raises(ValueError):
             pa._pair_axes(axes, 4)
         pa._pair_axes([1] * 32, 4)
+
+
+@pytest.mark.parametrize("rows", [0, 1, 5])
+def test_masks_of_no_drafted_tokens(rows):
+    packed = pa.pack_tree_mask(torch.zeros(rows, 0, dtype=torch.bool))
+    assert packed.dtype is torch.int32 and packed.shape == (rows, 0)
+
+
+def test_masks_that_are_not_contiguous():
+    seen = torch.rand(40, 70, generator=torch.Generator().manual_seed(1)) < 0.5
+    assert torch.equal(pa.pack_tree_mask(seen.t().contiguous().t()), pa.pack_tree_mask(seen))
+    assert torch.equal(pa.pack_tree_mask(seen[:, :64]), pa.pack_tree_mask(seen)[:, :2])
