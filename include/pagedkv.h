@@ -554,19 +554,23 @@ pa_status pa_tree_attention_q8(void* out, const void* q, const int32_t* tree_mas
  * PA_DEVFLAG_BAD_CONTEXT and is left alone; an entry that does not rise, or lies past the block-table
  * row, sets it and does not move (what the others' order was meant to protect may be lost); a bad
  * block id sets PA_DEVFLAG_BAD_BLOCK and its tokens do not move.  Blocks in which a sequence's tokens
- * move must be its own (pa_copy_blocks before writing to shared blocks); sequences that keep all they have
- * move nothing.  num_seqs == 0, num_kept == 0 and max_kept == 0 are no-ops. */
+ * move must be its own (pa_copy_blocks before writing to shared blocks); tokens whose slot stays the same
+ * are not written.  num_seqs == 0, num_kept == 0 and max_kept == 0 are no-ops. */
 pa_status pa_compact_tokens(const int32_t* kept, const int32_t* kept_start_loc,
                             const int32_t* first, int32_t num_kept, int32_t max_kept,
                             void* key_cache, void* value_cache, pa_cache_desc cd,
                             const int32_t* block_tables, int32_t max_blocks_per_seq,
                             int32_t num_seqs, int32_t* device_status, pa_stream_t stream);
 
-/* The same in the 8-bit pools: the values code * scale go to their new blocks as pa_rope_append_q8
- * would store them (also those whose slot stays the same).  A block whose first slot receives a token
- * starts with the smallest scale that fits what moves into it; one with tokens before first[s] keeps
- * its scale or grows it (and their codes are rescaled).  A block that a bad entry, block id or scale (negative, not finite; zero too where
- * earlier tokens stay) takes part in is reported and left as it is. */
+/* The same in the 8-bit pools.  Every block that a sequence's list covers, those of the positions
+ * first[s] .. first[s] + its number of entries - 1, is stored anew, also where its tokens stay where they
+ * are: the values code * scale go into it as pa_rope_append_q8 would store them (a code that is no
+ * number stays one).  A block whose first slot receives a token starts with the smallest scale that
+ * fits what it receives; one with tokens before first[s] keeps its scale or grows it (and their codes are
+ * rescaled).  So all of these blocks must be the sequence's own, also where it keeps all it has
+ * (pa_copy_blocks_q8 before), and what their slots past the list stood for is lost: their codes stay, their
+ * scale may not.  A block that a bad entry, block id or scale (negative, not finite, or so large that a
+ * value is not; zero too where earlier tokens stay) takes part in is reported and left as it is. */
 pa_status pa_compact_tokens_q8(const int32_t* kept, const int32_t* kept_start_loc,
                                const int32_t* first, int32_t num_kept, int32_t max_kept,
                                void* key_cache, void* value_cache, float* key_scale,
