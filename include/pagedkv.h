@@ -519,7 +519,8 @@ size_t pa_tree_workspace_size(void);
  * A block id outside [0, num_blocks) sets PA_DEVFLAG_BAD_BLOCK; rows of that sequence are undefined.
  * Rows of q and out outside query_start_loc[0] .. query_start_loc[num_seqs] - 1 are left alone.
  * Tight bounds pay: max_query_len and the width of the block tables choose how the work is split.
- * Results do not depend on the order in which CTAs run.  num_seqs == 0, num_query_tokens == 0 and
+ * Scores, maxima and sums are fp32; the softmax weights are rounded to bf16 (by up to 2^-8 of each) before
+ * they meet the values.  Results do not depend on the order in which CTAs run.  num_seqs == 0, num_query_tokens == 0 and
  * max_query_len == 0 are no-ops. */
 pa_status pa_tree_attention(void* out, const void* q, const int32_t* tree_mask, int32_t mask_words,
                             const int32_t* query_start_loc, int32_t num_query_tokens,
@@ -529,7 +530,10 @@ pa_status pa_tree_attention(void* out, const void* q, const int32_t* tree_mask, 
                             int32_t num_seqs, int32_t num_q_heads, float scale, void* workspace,
                             size_t workspace_bytes, int32_t* device_status, pa_stream_t stream);
 
-/* The same over the 8-bit pools, with pa_decode_q8's limits on scales, values and codes. */
+/* The same over the 8-bit pools, with pa_decode_q8's limits on scales, values and codes.  Calls whose
+ * max_query_len makes at most 32 rows per K/V head, under block tables that are not too wide for it, run on
+ * a kernel that rounds the weights to f16 (by up to 2^-11): the last bits of one and the same tree's rows
+ * depend on these two. */
 pa_status pa_tree_attention_q8(void* out, const void* q, const int32_t* tree_mask,
                                int32_t mask_words, const int32_t* query_start_loc,
                                int32_t num_query_tokens, int32_t max_query_len,

@@ -19,7 +19,9 @@
 // decode step of 64 tokens 2.0 us and of 256 into the 8-bit pools 2.3, three dependent loads
 // (context, block table, scale) and the launch.  At positions of their own: the nodes of 16 trees of 12 3.1
 // us (the position stands before the angles in the chain), prompts with images, three axes, of 15,000 tokens into the bf16 pools
-// 32.5 us (5.9 TB/s, 0.88), of 12,000 into the 8-bit ones 29.6 (4.9 TB/s, 0.72).
+// 32.5 us (5.9 TB/s, 0.88), of 12,000 into the 8-bit ones 29.8 (4.9 TB/s, 0.72); over four such batches in turn 31.4,
+// 30.9 with the axes in sections of the pairs (four pairs by one load) and 27.8 to 28.2 for the same rows by slot: the positions are
+// one more load in a block's chain, ahead of its angles, and angles from three rows of the table instead of one.
 #include <math.h>
 
 #include "common.cuh"

@@ -13,10 +13,13 @@
 // put them: a scale of their own where the block's first slot is among them, and one that only grows
 // where earlier tokens stay.
 //
-// Memory-bound: every row is read and written once.  Measured (8 K/V heads): 64 histories of 300 to 500
-// kept tokens (106.9 MB) 13.3 us where a replay finds what the last one wrote in L2, 17.8 from DRAM (6.0 TB/s, 0.89
-// of the copy rate; 23.2 with the list and the tables waited for in every round); 32 paths of up to 5 tokens 2.6 us,
-// 256 of up to 8 in the 8-bit pools 5.7: the launch and the chain of dependent loads.
+// Every row is read and written once.  Measured (8 K/V heads): 64 histories of 300 to 500 kept tokens (106.9 MB) 13.2
+// us where a replay finds what the last one wrote in L2; 21.4 where eleven such batches take turns, so that every row
+// comes from DRAM and goes back there within the time (5.0 TB/s, 0.74 of the copy rate: a CTA either reads a
+// round or writes one, and between the two nothing is in flight); 256 of 100 to 250 34.2 (5.2 TB/s).  In the 8-bit
+// pools the same 64 (53.7 MB) 20.2 and 28.4 us (1.9 TB/s): list, tables and scales are waited for block by
+// block.  32 paths of up to 5 tokens 2.6 us, 256 of up to 8 in the 8-bit pools 5.8: the launch and the chain of
+// dependent loads.
 #include <math.h>
 
 #include "common.cuh"
