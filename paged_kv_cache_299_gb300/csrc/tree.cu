@@ -93,8 +93,8 @@ struct TreeParams {
   const float* key_scale;            // 8-bit pools
   const float* value_scale;
   int32_t* counters;  // [grid][row warps] pieces delivered by each of the segment that starts in a CTA and goes on
-  // [grid][2][row warps] the same of groups of pieces, by the CTA of their first piece: the first group of the segment
-  // that starts there (as in a record's place), or a group of one that began before.  A CTA can hold both.
+  // [grid][2][row warps] the same of groups of pieces, by the CTA of a group's first piece: a later group of the
+  // segment that comes from the CTAs before, or the first of the one that starts there (a CTA can hold both).
   int32_t* group_counters;
   float4* records;    // [grid][2][halves][half of the dims][kPartChunks][128]
   int32_t* status;

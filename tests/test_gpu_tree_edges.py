@@ -66,3 +66,25 @@ def test_empty_sequences_are_not_reported(pool, count):
     t = Trees(pool, [30] + [0] * count, [4] + [0] * count, 4, 1, seed=14)
     t.check()
     t.check(t.run(ctx=i32([34] + [-1] * count)))
+
+
+@pytest.mark.parametrize("pool", POOLS)
+def test_two_calls_at_once(pool):
+    """On two streams, each with a workspace of its own."""
+    batches = [Trees(pool, [9000] * 3 + [200] * 9, [70] * 12, 8, 2, seed=15), Trees(pool, [20000, 30], [12, 9], 8, 2, seed=16)]
+    spaces = [torch.zeros(pa.pa_tree_workspace_size(), dtype=torch.uint8, device="cuda") for _ in batches]
+    want = [t.run(workspace=ws) for t, ws in zip(batches, spaces)]
+    for t, got in zip(batches, want):
+        t.check(got)
+    f = pa.pa_tree_attention_q8 if pool == "q8" else pa.pa_tree_attention
+    queries = [t.q.cuda() for t in batches]
+    outs = [[torch.zeros_like(q) for _ in range(20)] for q in queries]
+    streams = [torch.cuda.Stream() for _ in batches]
+    torch.cuda.synchronize()
+    for turn in range(20):
+        for t, ws, q, out, stream in zip(batches, spaces, queries, outs, streams):
+            f(out[turn], q, t.mask, t.starts, t.most, *t.dev, t.bt, t.ctx, 0.125, workspace=ws, device_status=t.status,
+              stream=stream)
+    torch.cuda.synchronize()
+    for t, first, out in zip(batches, want, outs):
+        assert t.ok() and all(torch.equal(x, first) for x in out)
